@@ -94,6 +94,7 @@ typedef enum dg_status {
                                     /* normal power of two                       */
 #define DG_DEVERR_BAD_K_OFFSET 16u  /* K-grouped: k_offsets not increasing       */
                                     /* multiples of 128 within [0, K]            */
+#define DG_DEVERR_BAD_EXPERT 32u    /* layout: a chosen expert not in [-1,E)     */
 
 /*
  * Dense GEMM: D[M,N] = scaled A[M,K] . B[N,K]^T (section "常规密集型 GEMM（非分组）",
@@ -265,6 +266,193 @@ DG_API dg_status dg_grouped_contiguous_nt(uint16_t* D, const uint8_t* A, const f
 DG_API dg_status dg_grouped_masked_nt(uint16_t* D, const uint8_t* A, const float* sa, int sa_stride,
                                const uint8_t* B, const float* sb, const int32_t* masked_m,
                                int G, int M_max, int N, int K, int expected_m, void* stream);
+
+/*
+ * Around the grouped GEMMs: routing, dispatch, combine and 8-bit activation
+ * checkpoints (no counterpart on the pages, which start from m_indices or
+ * masked_m and from cast operands).  One training step of a MoE layer is
+ *   dg_route_topk, dg_route_layout, dg_dispatch_fp8_1x128,
+ *   dg_grouped_contiguous_nt, dg_swiglu_fp8, dg_grouped_contiguous_nt,
+ *   dg_combine
+ * and backwards, from the e4m3 operands kept as checkpoints,
+ *   dg_combine_bwd, dg_grouped_contiguous_nt (transposed weights),
+ *   dg_swiglu_fp8_bwd, dg_grouped_contiguous_nt, dg_combine (w null),
+ *   dg_k_grouped_fp8_gemm_tn for both weight gradients, with
+ *   dg_fp8_1x128_to_128x128 for the dispatched input, and dg_route_topk_bwd.
+ * Decoding uses dg_route_layout's masked form with dg_grouped_masked_nt.
+ *
+ * Words: a token t < T has k slots, slot t*k + j; `rows` is the number of rows
+ * of the grouped layout (M_total, or G*M_max).  Sums, softmax statistics and
+ * products are FP32; e4m3 casts are dg_to_fp8_1x128's steps (amax floored at
+ * 1e-4, s = amax/448, x * (448/amax) rounded to nearest even, NaN stays NaN).
+ * The general conventions at the top hold: nothing is allocated, synchronised
+ * or read by the host, every call may be captured, results are deterministic.
+ */
+
+/* Element type of logits. */
+#define DG_DTYPE_BF16 0
+#define DG_DTYPE_FP32 1
+/* Scores of logits. */
+#define DG_SCORE_SOFTMAX 0
+#define DG_SCORE_SIGMOID 1
+
+/*
+ * The k experts of each token, and their weights.
+ *   s = softmax(l) over the token's E logits, or sigmoid(l)
+ *   c = s + bias                     (bias null: 0; it moves the choice only)
+ *   n_groups > 1: the experts form n_groups runs of E/n_groups; a group's score
+ *     is the sum of its group_top (1 or 2) largest c; the topk_groups groups of
+ *     the largest score stay, experts of the others are out
+ *   idx[t][j], j < k: the experts of the k largest c, largest first
+ *   w[t][j] = s[idx[t][j]], renorm != 0: divided by (their sum + 1e-20); times
+ *     scale
+ * Ties go to the lower index, among groups too.  The order is that of exact
+ * arithmetic (FP64 where FP32 cannot tell), and without a bias that of the
+ * logits.  A logit or bias of -inf takes the expert out; if fewer than k are
+ * left the remaining slots get idx -1 and w 0.  A NaN ranks first, and its
+ * weight is NaN.
+ *   topk_idx  int32 [T][k], topk_w float32 [T][k]
+ *   logits    [T][E], bf16 or float32 (logits_dtype)
+ *   bias      float32 [E] or null
+ * E <= 1024, k <= 16 and k <= E, n_groups <= 32 dividing E, 1 <= topk_groups
+ * <= n_groups.  T == 0 is valid and launches nothing.
+ */
+DG_API dg_status dg_route_topk(int32_t* topk_idx, float* topk_w, const void* logits, int logits_dtype,
+                               const float* bias, int T, int E, int k, int n_groups, int topk_groups, int group_top,
+                               int score, int renorm, float scale, void* stream);
+
+/*
+ * Gradient of dg_route_topk's weights with respect to the logits (the choice
+ * itself and the bias have none).  Every dlogits element is written.  A slot
+ * with topk_idx outside [0,E) counts as absent; an expert in two slots gets
+ * both gradients.
+ *   dlogits   [T][E], the logits' type; dw float32 [T][k]; topk_idx int32 [T][k]
+ * score, renorm and scale as in the forward call; E <= 1024, k <= 16.
+ */
+DG_API dg_status dg_route_topk_bwd(void* dlogits, const float* dw, const void* logits, int logits_dtype,
+                                   const int32_t* topk_idx, int T, int E, int k, int score, int renorm, float scale,
+                                   void* stream);
+
+/*
+ * Rows that dg_route_layout's contiguous form needs for any choice of experts:
+ * T*k slots in at most min(E, T*k) segments, each rounded up to whole 128
+ * rows.  -1 for sizes it does not take.
+ */
+DG_API int dg_get_layout_rows(int T, int k, int E);
+
+/*
+ * The grouped layout of a choice of experts: group e's rows hold the slots
+ * with topk_idx == e in slot order.
+ *   max_rows == 0  contiguous: each group's segment starts on a multiple of 128;
+ *                  rows >= dg_get_layout_rows(T, k, E), a multiple of 128
+ *   max_rows > 0   masked: group e owns rows [e*max_rows, (e+1)*max_rows), rows
+ *                  == E*max_rows; slots past max_rows are dropped
+ *   topk_idx       int32 [T][k], -1: no expert (other values outside [0,E) set
+ *                  DG_DEVERR_BAD_EXPERT and count as -1)
+ *   row_of         int32 [T][k]: the slot's row, -1 without one
+ *   m_indices      int32 [rows]: the row's expert, -1 without a slot (as
+ *                  dg_grouped_contiguous_nt reads it)
+ *   slot_of        int32 [rows]: the row's slot, -1 without one
+ *   group_offsets  int32 [E+1]: each group's first row, then the end of the
+ *                  last (contiguous: dg_k_grouped_fp8_gemm_tn's k_offsets)
+ *   counts         int32 [E]: rows of each group that hold a slot (masked:
+ *                  dg_grouped_masked_nt's masked_m)
+ * All outputs are written whole.  E <= 1024, k <= 32, T*k < 2^31.
+ */
+DG_API dg_status dg_route_layout(int32_t* row_of, int32_t* m_indices, int32_t* slot_of, int32_t* group_offsets,
+                                 int32_t* counts, const int32_t* topk_idx, int T, int k, int E, int rows,
+                                 int max_rows, void* stream);
+
+/*
+ * The FP8 cast of each token (dg_to_fp8_1x128's steps), written to all rows of
+ * its slots; rows without a slot are left untouched.
+ *   Q          uint8 e4m3 [rows][K]
+ *   sa         group_rows == 0: sa[kb*sa_stride + row], sa_stride >= rows;
+ *              else (masked) group g's block starts at g*(K/128)*sa_stride,
+ *              rows a multiple of group_rows, sa_stride >= group_rows
+ *   X          bf16 [T][K], row_of int32 [T][k] (values outside [0,rows): none)
+ * K % 128 == 0, k <= 32; X and Q 16-byte aligned.
+ */
+DG_API dg_status dg_dispatch_fp8_1x128(uint8_t* Q, float* sa, int sa_stride, const uint16_t* X,
+                                       const int32_t* row_of, int T, int k, int K, int rows, int group_rows,
+                                       void* stream);
+
+/*
+ * Weighted sum of each token's rows: out[t] = sum_j w[t][j] * Y[row_of[t][j]],
+ * in FP32 over j, rounded once to bf16.  Slots without a row add nothing; a
+ * token without any row gets zeros.  w null: every weight 1, which is the
+ * backward pass of the dispatch.
+ *   out bf16 [T][N], Y bf16 [rows][N], row_of int32 [T][k], w float32 [T][k]
+ * N % 8 == 0, k <= 32; out and Y 16-byte aligned.
+ */
+DG_API dg_status dg_combine(uint16_t* out, const uint16_t* Y, const int32_t* row_of, const float* w, int T, int k,
+                            int N, int rows, void* stream);
+
+/*
+ * Gradient of dg_combine in the contiguous layout: dY[row] = w[slot] * dout[t]
+ * for the row's slot, in both casts that the backward GEMMs read, and
+ *   dw[t][j] = sum_n dout[t][n] * Y[row_of[t][j]][n]   (0 without a row).
+ *   Qr, sr     dY cast per 1x128 along N: e4m3 [rows][N], sr[kb*sr_stride + row]
+ *              (A of dg_grouped_contiguous_nt)
+ *   Qc, sc     dY cast per 128x1 along the rows: e4m3 [rows][N],
+ *              sc[(row/128)*sc_stride + n], sc_stride >= N (A of
+ *              dg_k_grouped_fp8_gemm_tn, whose K is the rows)
+ *   dout bf16 [T][N], Y bf16 [rows][N], row_of int32 [T][k], slot_of int32
+ *   [rows], w float32 [T][k]
+ * Rows without a slot are zeros; a block of 128 rows without any slot is left
+ * untouched.  N % 128 == 0, rows % 128 == 0, k <= 32.
+ */
+DG_API dg_status dg_combine_bwd(float* dw, uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, float* sc,
+                                int sc_stride, const uint16_t* dout, const uint16_t* Y, const int32_t* row_of,
+                                const int32_t* slot_of, const float* w, int T, int k, int N, int rows, void* stream);
+
+/*
+ * Gated activation between a MoE layer's two GEMMs, a = silu(gate) * up with
+ * silu(x) = x / (1 + exp(-x)), cast for the second GEMM, and gate and up cast
+ * as the 8-bit checkpoint of the backward pass.
+ *   Q, sa      a per 1x128: e4m3 [rows][F], sa as dg_dispatch_fp8_1x128's
+ *   C, cs      gate and up per 1x128: e4m3 [rows][2F], cs[kb*cs_stride + row]
+ *              over 2F/128 blocks (masked: per group, like sa); C null: no
+ *              checkpoint, cs is not used
+ *   H          bf16 [rows][2F]: gate, then up
+ *   m_indices  int32 [rows] or null; a row with a negative value is neither
+ *              read nor written
+ * F % 128 == 0; Q, C and H 16-byte aligned.  rows == 0 launches nothing.
+ */
+DG_API dg_status dg_swiglu_fp8(uint8_t* Q, float* sa, int sa_stride, uint8_t* C, float* cs, int cs_stride,
+                               const uint16_t* H, const int32_t* m_indices, int rows, int F, int group_rows,
+                               void* stream);
+
+/*
+ * Backward pass of dg_swiglu_fp8 from its checkpoint (gate and up are what C
+ * and cs stand for), in the contiguous layout:
+ *   d gate = dA * up * s * (1 + gate * (1 - s)), s = 1 / (1 + exp(-gate))
+ *   d up   = dA * silu(gate)
+ *   Qr, sr     dH = [d gate, d up] per 1x128: e4m3 [rows][2F], sr[kb*sr_stride + row]
+ *   Qc, sc     dH per 128x1: e4m3 [rows][2F], sc[(row/128)*sc_stride + n],
+ *              sc_stride >= 2F
+ *   Qa, sb     a again, per 128x128: e4m3 [rows][F], sb[(n/128)*(rows/128) +
+ *              row/128] (B of dg_k_grouped_fp8_gemm_tn)
+ *   dA bf16 [rows][F]; C, cs as written by dg_swiglu_fp8 (cs_stride >= rows)
+ * Rows with a negative m_indices are not read and are zeros in the outputs; a
+ * block of 128 rows with only such rows is left untouched.  F % 128 == 0,
+ * rows % 128 == 0.
+ */
+DG_API dg_status dg_swiglu_fp8_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, float* sc, int sc_stride,
+                                   uint8_t* Qa, float* sb, const uint16_t* dA, const uint8_t* C, const float* cs,
+                                   int cs_stride, const int32_t* m_indices, int rows, int F, void* stream);
+
+/*
+ * A checkpoint's second use: e4m3 with a scale per 1x128 (dg_to_fp8_1x128's or
+ * dg_dispatch_fp8_1x128's output) cast again per 128x128, as B of the weight
+ * gradient's dg_k_grouped_fp8_gemm_tn.
+ *   Qb         uint8 e4m3 [rows][K], sb float32 [K/128][rows/128]
+ *   Q          uint8 e4m3 [rows][K], sa[kb*sa_stride + row]
+ *   m_indices  as in dg_swiglu_fp8_bwd
+ * K % 128 == 0, rows % 128 == 0.
+ */
+DG_API dg_status dg_fp8_1x128_to_128x128(uint8_t* Qb, float* sb, const uint8_t* Q, const float* sa, int sa_stride,
+                                         const int32_t* m_indices, int rows, int K, void* stream);
 
 /* Utility functions (section "工具函数" (utility functions) of the same page). */
 

@@ -26,6 +26,9 @@ LIB_PATH = os.path.join(_HERE, "libdg.so")
 DG_OK, DG_ERR_INVALID_ARG, DG_ERR_UNSUPPORTED, DG_ERR_MISALIGNED, DG_ERR_CUDA = range(5)
 DG_DEVERR_TIMEOUT, DG_DEVERR_BAD_M_INDEX, DG_DEVERR_BAD_MASKED_M, DG_DEVERR_NOT_POW2 = 1, 2, 4, 8
 DG_DEVERR_BAD_K_OFFSET = 16
+DG_DEVERR_BAD_EXPERT = 32
+DG_DTYPE_BF16, DG_DTYPE_FP32 = 0, 1
+DG_SCORE_SOFTMAX, DG_SCORE_SIGMOID = 0, 1
 
 _lock = threading.Lock()
 _lib = None
@@ -74,6 +77,20 @@ def lib() -> ctypes.CDLL:
             L.dg_grouped_contiguous_nt.argtypes = [P, P, P, I, P, P, P, I, I, I, I, P]
             L.dg_grouped_masked_nt.restype = I
             L.dg_grouped_masked_nt.argtypes = [P, P, P, I, P, P, P, I, I, I, I, I, P]
+            F = ctypes.c_float
+            for nm, at in (
+                    ("dg_route_topk", [P, P, P, I, P, I, I, I, I, I, I, I, I, F, P]),
+                    ("dg_route_topk_bwd", [P, P, P, I, P, I, I, I, I, I, F, P]),
+                    ("dg_get_layout_rows", [I, I, I]),
+                    ("dg_route_layout", [P, P, P, P, P, P, I, I, I, I, I, P]),
+                    ("dg_dispatch_fp8_1x128", [P, P, I, P, P, I, I, I, I, I, P]),
+                    ("dg_combine", [P, P, P, P, I, I, I, I, P]),
+                    ("dg_combine_bwd", [P, P, P, I, P, P, I, P, P, P, P, P, I, I, I, I, P]),
+                    ("dg_swiglu_fp8", [P, P, I, P, P, I, P, P, I, I, I, P]),
+                    ("dg_swiglu_fp8_bwd", [P, P, I, P, P, I, P, P, P, P, P, I, P, I, I, P]),
+                    ("dg_fp8_1x128_to_128x128", [P, P, P, P, I, P, I, I, P])):
+                getattr(L, nm).restype = I
+                getattr(L, nm).argtypes = at
             L.dg_set_pdl.restype = None
             L.dg_set_pdl.argtypes = [I]
             L.dg_get_pdl.restype = I
@@ -297,6 +314,197 @@ def dg_grouped_masked_nt(D, A, sa, sa_stride: int, B, sb, masked_m, expected_m: 
     _check("dg_grouped_masked_nt",
            lib().dg_grouped_masked_nt(_ptr(D), _ptr(A), _ptr(sa), int(sa_stride), _ptr(B), _ptr(sb),
                                       _ptr(masked_m), G, Mmax, N, K, int(expected_m), _stream(stream)))
+
+
+def _shape2(func: str, name: str, t):
+    if t is None or t.dim() != 2:
+        raise DGError(func, DG_ERR_INVALID_ARG, f"{name} must be a tensor of rank 2")
+    return t.shape
+
+
+def _shape1(func: str, name: str, t) -> int:
+    if t is None or t.dim() != 1:
+        raise DGError(func, DG_ERR_INVALID_ARG, f"{name} must be a tensor of rank 1")
+    return t.shape[0]
+
+
+def _check_kinds(func: str, **kinds) -> None:
+    """Element types that the size alone does not tell apart: name=(tensor, "int32", "float32" or "bfloat16")."""
+    for name, (t, kind) in kinds.items():
+        if t is not None and str(t.dtype) != "torch." + kind:
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call takes {kind}")
+
+
+def _logits_dtype(func: str, logits) -> int:
+    import torch
+    if logits.dtype == torch.bfloat16:
+        return DG_DTYPE_BF16
+    if logits.dtype == torch.float32:
+        return DG_DTYPE_FP32
+    raise DGError(func, DG_ERR_INVALID_ARG, f"logits are {logits.dtype}, the call takes bfloat16 or float32")
+
+
+def _scales_need(nkb: int, stride: int, rows: int, group_rows: int) -> int:
+    """Elements of a transposed scale array over rows, in one block (group_rows 0) or one per group."""
+    if group_rows > 0 and rows >= group_rows:
+        return _sa_need(rows // group_rows * nkb, stride, group_rows)
+    return _sa_need(nkb, stride, rows)
+
+
+def dg_route_topk(topk_idx, topk_w, logits, bias=None, n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+                  score: int = DG_SCORE_SOFTMAX, renorm: bool = False, scale: float = 1.0, stream=None) -> None:
+    """The k experts of each token: logits [T,E] (bfloat16 or float32), optional
+    float32 bias [E] -> int32 topk_idx [T,k] and float32 topk_w [T,k]."""
+    func = "dg_route_topk"
+    T, E = _shape2(func, "logits", logits)
+    Ti, k = _shape2(func, "topk_idx", topk_idx)
+    _check_dim(func, "token count of topk_idx", Ti, T)
+    dt = _logits_dtype(func, logits)
+    _check_kinds(func, topk_idx=(topk_idx, "int32"), topk_w=(topk_w, "float32"), bias=(bias, "float32"))
+    _check_args(func, ("topk_idx", topk_idx, 4, T * k), ("topk_w", topk_w, 4, T * k),
+                ("logits", logits, logits.element_size(), T * E), ("bias", bias, 4, E))
+    _check(func, lib().dg_route_topk(_ptr(topk_idx), _ptr(topk_w), _ptr(logits), dt, _ptr(bias), T, E, k,
+                                     int(n_groups), int(topk_groups), int(group_top), int(score), int(bool(renorm)),
+                                     float(scale), _stream(stream)))
+
+
+def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTMAX, renorm: bool = False,
+                      scale: float = 1.0, stream=None) -> None:
+    """Gradient of dg_route_topk: float32 dw [T,k] -> dlogits [T,E] (the logits' type)."""
+    func = "dg_route_topk_bwd"
+    T, E = _shape2(func, "logits", logits)
+    Ti, k = _shape2(func, "topk_idx", topk_idx)
+    _check_dim(func, "token count of topk_idx", Ti, T)
+    dt = _logits_dtype(func, logits)
+    if dlogits is not None and dlogits.dtype != logits.dtype:
+        raise DGError(func, DG_ERR_INVALID_ARG, f"dlogits are {dlogits.dtype}, logits {logits.dtype}")
+    _check_kinds(func, topk_idx=(topk_idx, "int32"), dw=(dw, "float32"))
+    _check_args(func, ("dlogits", dlogits, logits.element_size(), T * E), ("dw", dw, 4, T * k),
+                ("logits", logits, logits.element_size(), T * E), ("topk_idx", topk_idx, 4, T * k))
+    _check(func, lib().dg_route_topk_bwd(_ptr(dlogits), _ptr(dw), _ptr(logits), dt, _ptr(topk_idx), T, E, k,
+                                         int(score), int(bool(renorm)), float(scale), _stream(stream)))
+
+
+def dg_get_layout_rows(T: int, k: int, E: int) -> int:
+    """Rows that dg_route_layout's contiguous form needs for any choice of experts."""
+    return int(lib().dg_get_layout_rows(int(T), int(k), int(E)))
+
+
+def dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx, max_rows: int = 0,
+                    stream=None) -> None:
+    """The grouped layout of topk_idx [T,k] (all int32): row_of [T,k],
+    m_indices and slot_of [rows], group_offsets [E+1], counts [E]; contiguous,
+    or masked with max_rows rows per group."""
+    func = "dg_route_layout"
+    T, k = _shape2(func, "topk_idx", topk_idx)
+    rows, E = _shape1(func, "m_indices", m_indices), _shape1(func, "counts", counts)
+    _check_kinds(func, row_of=(row_of, "int32"), m_indices=(m_indices, "int32"), slot_of=(slot_of, "int32"),
+                 group_offsets=(group_offsets, "int32"), counts=(counts, "int32"), topk_idx=(topk_idx, "int32"))
+    _check_args(func, ("row_of", row_of, 4, T * k), ("m_indices", m_indices, 4, rows), ("slot_of", slot_of, 4, rows),
+                ("group_offsets", group_offsets, 4, E + 1), ("counts", counts, 4, E), ("topk_idx", topk_idx, 4, T * k))
+    _check(func, lib().dg_route_layout(_ptr(row_of), _ptr(m_indices), _ptr(slot_of), _ptr(group_offsets),
+                                       _ptr(counts), _ptr(topk_idx), T, k, E, rows, int(max_rows), _stream(stream)))
+
+
+def dg_dispatch_fp8_1x128(Q, sa, sa_stride: int, X, row_of, group_rows: int = 0, stream=None) -> None:
+    """Cast bf16 X [T,K] into the rows of the layout: e4m3 Q [rows,K] (or
+    [G,M_max,K]) and its transposed scales; group_rows = M_max when masked."""
+    func = "dg_dispatch_fp8_1x128"
+    T, K = _shape2(func, "X", X)
+    Ti, k = _shape2(func, "row_of", row_of)
+    _check_dim(func, "token count of row_of", Ti, T)
+    _check_dim(func, "K of Q", Q.shape[-1], K)
+    rows = Q.numel() // K if K else 0
+    _check_kinds(func, row_of=(row_of, "int32"), sa=(sa, "float32"), X=(X, "bfloat16"))
+    _check_args(func, ("Q", Q, 1, rows * K), ("sa", sa, 4, _scales_need(_cdiv(K, 128), sa_stride, rows, group_rows)),
+                ("X", X, 2, T * K), ("row_of", row_of, 4, T * k))
+    _check(func, lib().dg_dispatch_fp8_1x128(_ptr(Q), _ptr(sa), int(sa_stride), _ptr(X), _ptr(row_of), T, k, K, rows,
+                                             int(group_rows), _stream(stream)))
+
+
+def dg_combine(out, Y, row_of, w=None, stream=None) -> None:
+    """out [T,N] = sum over slots of w [T,k] (None: ones) times the rows of Y
+    ([rows,N] or [G,M_max,N]), bf16; without w the backward pass of the dispatch."""
+    func = "dg_combine"
+    T, N = _shape2(func, "out", out)
+    Ti, k = _shape2(func, "row_of", row_of)
+    _check_dim(func, "token count of row_of", Ti, T)
+    _check_dim(func, "N of Y", Y.shape[-1], N)
+    rows = Y.numel() // N if N else 0
+    _check_kinds(func, out=(out, "bfloat16"), Y=(Y, "bfloat16"), row_of=(row_of, "int32"), w=(w, "float32"))
+    _check_args(func, ("out", out, 2, T * N), ("Y", Y, 2, rows * N), ("row_of", row_of, 4, T * k), ("w", w, 4, T * k))
+    _check(func, lib().dg_combine(_ptr(out), _ptr(Y), _ptr(row_of), _ptr(w), T, k, N, rows, _stream(stream)))
+
+
+def dg_combine_bwd(dw, Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, dout, Y, row_of, slot_of, w,
+                   stream=None) -> None:
+    """Gradient of dg_combine (contiguous layout): dout [T,N] -> dY [rows,N]
+    cast per 1x128 (Qr, sr) and per 128x1 (Qc, sc), and float32 dw [T,k]."""
+    func = "dg_combine_bwd"
+    T, N = _shape2(func, "dout", dout)
+    Ti, k = _shape2(func, "row_of", row_of)
+    rows, Ny = _shape2(func, "Y", Y)
+    _check_dim(func, "token count of row_of", Ti, T)
+    _check_dim(func, "N of Y", Ny, N)
+    _check_kinds(func, dw=(dw, "float32"), sr=(sr, "float32"), sc=(sc, "float32"), dout=(dout, "bfloat16"), Y=(Y, "bfloat16"),
+                 w=(w, "float32"), row_of=(row_of, "int32"), slot_of=(slot_of, "int32"))
+    _check_args(func, ("dw", dw, 4, T * k), ("Qr", Qr, 1, rows * N),
+                ("sr", sr, 4, _sa_need(_cdiv(N, 128), sr_stride, rows)), ("Qc", Qc, 1, rows * N),
+                ("sc", sc, 4, _sa_need(_cdiv(rows, 128), sc_stride, N)), ("dout", dout, 2, T * N),
+                ("Y", Y, 2, rows * N), ("row_of", row_of, 4, T * k), ("slot_of", slot_of, 4, rows), ("w", w, 4, T * k))
+    _check(func, lib().dg_combine_bwd(_ptr(dw), _ptr(Qr), _ptr(sr), int(sr_stride), _ptr(Qc), _ptr(sc),
+                                      int(sc_stride), _ptr(dout), _ptr(Y), _ptr(row_of), _ptr(slot_of), _ptr(w),
+                                      T, k, N, rows, _stream(stream)))
+
+
+def dg_swiglu_fp8(Q, sa, sa_stride: int, H, C=None, cs=None, cs_stride: int = 0, m_indices=None, group_rows: int = 0,
+                  stream=None) -> None:
+    """silu(gate) * up of bf16 H [rows,2F] (or [G,M_max,2F]) -> e4m3 Q [rows,F]
+    and sa; with C and cs also the e4m3 checkpoint of gate and up [rows,2F]."""
+    func = "dg_swiglu_fp8"
+    F = H.shape[-1] // 2
+    _check_dim(func, "last extent of H", H.shape[-1], 2 * F)
+    _check_dim(func, "F of Q", Q.shape[-1], F)
+    rows = H.numel() // (2 * F) if F else 0
+    _check_kinds(func, H=(H, "bfloat16"), sa=(sa, "float32"), cs=(cs, "float32"), m_indices=(m_indices, "int32"))
+    _check_args(func, ("Q", Q, 1, rows * F), ("sa", sa, 4, _scales_need(_cdiv(F, 128), sa_stride, rows, group_rows)),
+                ("H", H, 2, rows * 2 * F), ("C", C, 1, rows * 2 * F),
+                ("cs", cs if C is not None else None, 4, _scales_need(2 * _cdiv(F, 128), cs_stride, rows, group_rows)),
+                ("m_indices", m_indices, 4, rows))
+    _check(func, lib().dg_swiglu_fp8(_ptr(Q), _ptr(sa), int(sa_stride), _ptr(C), _ptr(cs), int(cs_stride), _ptr(H),
+                                     _ptr(m_indices), rows, F, int(group_rows), _stream(stream)))
+
+
+def dg_swiglu_fp8_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, Qa, sb, dA, C, cs, cs_stride: int,
+                      m_indices=None, stream=None) -> None:
+    """Backward of dg_swiglu_fp8 from its checkpoint (contiguous layout): bf16
+    dA [rows,F] -> dH [rows,2F] cast per 1x128 (Qr, sr) and per 128x1 (Qc, sc),
+    and the activation again per 128x128 (Qa [rows,F], sb [F/128, rows/128])."""
+    func = "dg_swiglu_fp8_bwd"
+    rows, F = _shape2(func, "dA", dA)
+    _check_dim(func, "last extent of C", C.shape[-1], 2 * F)
+    _check_kinds(func, sr=(sr, "float32"), sc=(sc, "float32"), sb=(sb, "float32"), dA=(dA, "bfloat16"), cs=(cs, "float32"),
+                 m_indices=(m_indices, "int32"))
+    _check_args(func, ("Qr", Qr, 1, rows * 2 * F), ("sr", sr, 4, _sa_need(2 * _cdiv(F, 128), sr_stride, rows)),
+                ("Qc", Qc, 1, rows * 2 * F), ("sc", sc, 4, _sa_need(_cdiv(rows, 128), sc_stride, 2 * F)),
+                ("Qa", Qa, 1, rows * F), ("sb", sb, 4, _cdiv(F, 128) * _cdiv(rows, 128)), ("dA", dA, 2, rows * F),
+                ("C", C, 1, rows * 2 * F), ("cs", cs, 4, _sa_need(2 * _cdiv(F, 128), cs_stride, rows)),
+                ("m_indices", m_indices, 4, rows))
+    _check(func, lib().dg_swiglu_fp8_bwd(_ptr(Qr), _ptr(sr), int(sr_stride), _ptr(Qc), _ptr(sc), int(sc_stride),
+                                         _ptr(Qa), _ptr(sb), _ptr(dA), _ptr(C), _ptr(cs), int(cs_stride),
+                                         _ptr(m_indices), rows, F, _stream(stream)))
+
+
+def dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride: int, m_indices=None, stream=None) -> None:
+    """e4m3 Q [rows,K] with scales per 1x128 -> Qb [rows,K] with scales per
+    128x128, sb [K/128, rows/128] (contiguous layout)."""
+    func = "dg_fp8_1x128_to_128x128"
+    rows, K = _shape2(func, "Q", Q)
+    _check_kinds(func, sb=(sb, "float32"), sa=(sa, "float32"), m_indices=(m_indices, "int32"))
+    _check_args(func, ("Qb", Qb, 1, rows * K), ("sb", sb, 4, _cdiv(K, 128) * _cdiv(rows, 128)), ("Q", Q, 1, rows * K),
+                ("sa", sa, 4, _sa_need(_cdiv(K, 128), sa_stride, rows)), ("m_indices", m_indices, 4, rows))
+    _check(func, lib().dg_fp8_1x128_to_128x128(_ptr(Qb), _ptr(sb), _ptr(Q), _ptr(sa), int(sa_stride),
+                                               _ptr(m_indices), rows, K, _stream(stream)))
 
 
 def dg_set_pdl(enable) -> None:

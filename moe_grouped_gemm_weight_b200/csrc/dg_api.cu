@@ -21,6 +21,9 @@
 #include "dg_kernel.cuh"
 #include "dg_kernel_small.cuh"
 #include "dg_cast.cuh"
+#include "dg_ckpt.cuh"
+#include "dg_moe.cuh"
+#include "dg_route.cuh"
 #include "dg_kernel_ue8m0.cuh"
 
 namespace dg {
@@ -57,6 +60,7 @@ dg_status ok() {
 }
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
+int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -826,6 +830,107 @@ dg_status noalloc_scratch(unsigned char** out) {
     return DG_OK;
 }
 
+// ------------------------------------------- around the grouped GEMMs ----
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Launch of a kernel without a register split: programmatic dependent launch
+// as everywhere, `cluster` CTAs per cluster, `smem` bytes of dynamic shared
+// memory (raised once per device where it is above the 48 KiB default).
+template <typename P>
+dg_status launch_plain(void (*kern)(P), const P& p, int64_t grid, int threads, int smem, int cluster, void* stream) {
+    if (grid > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED, "problem too large");
+    if (smem > 48 * 1024) {
+        // Not remembered: the attribute belongs to (kernel, device), the call costs under a microsecond.
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return fail(DG_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(cudaGetLastError()));
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    set_pdl(attr[0]);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(DG_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+// Sizes that the routing calls share.
+dg_status check_route(int T, int E, int k, int dtype, int score) {
+    if (T < 0 || E <= 0 || k <= 0) return fail(DG_ERR_INVALID_ARG, "bad sizes T=%d E=%d k=%d", T, E, k);
+    if (k > E) return fail(DG_ERR_INVALID_ARG, "k=%d is more than E=%d", k, E);
+    if (dtype != DG_DTYPE_BF16 && dtype != DG_DTYPE_FP32) return fail(DG_ERR_INVALID_ARG, "bad logits_dtype %d", dtype);
+    if (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID) return fail(DG_ERR_INVALID_ARG, "bad score %d", score);
+    if (E > dg::kRouteMaxExperts) return fail(DG_ERR_UNSUPPORTED, "E=%d is more than %d", E, dg::kRouteMaxExperts);
+    if (k > dg::kRouteMaxK) return fail(DG_ERR_UNSUPPORTED, "k=%d is more than %d", k, dg::kRouteMaxK);
+    if (static_cast<int64_t>(T) * k > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED, "T*k does not fit in 31 bits");
+    return DG_OK;
+}
+
+// Sizes that the calls on slots and rows share.
+constexpr int kMaxSlots = 32;
+dg_status check_slots(int T, int k, int64_t rows) {
+    if (T < 0 || k <= 0 || rows < 0)
+        return fail(DG_ERR_INVALID_ARG, "bad sizes T=%d k=%d rows=%lld", T, k, static_cast<long long>(rows));
+    if (k > kMaxSlots) return fail(DG_ERR_UNSUPPORTED, "k=%d is more than %d", k, kMaxSlots);
+    if (static_cast<int64_t>(T) * k > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED, "T*k does not fit in 31 bits");
+    return DG_OK;
+}
+
+dg_status check_scale_layout(const char* what, int stride, int64_t rows, int group_rows) {
+    if (group_rows < 0) return fail(DG_ERR_INVALID_ARG, "group_rows=%d is negative", group_rows);
+    if (group_rows > 0 && rows % group_rows != 0)
+        return fail(DG_ERR_INVALID_ARG, "rows=%lld is not a multiple of group_rows=%d", static_cast<long long>(rows), group_rows);
+    const int64_t need = group_rows > 0 ? group_rows : rows;
+    if (stride < need)
+        return fail(DG_ERR_INVALID_ARG, "%s=%d must be >= %lld", what, stride, static_cast<long long>(need));
+    return DG_OK;
+}
+
+dg_status check_row_blocks(int64_t rows, int N, const char* name) {
+    if (rows < 0 || N <= 0) return fail(DG_ERR_INVALID_ARG, "bad sizes rows=%lld %s=%d", static_cast<long long>(rows), name, N);
+    if (rows % 128 != 0) return fail(DG_ERR_INVALID_ARG, "rows=%lld is not a multiple of 128", static_cast<long long>(rows));
+    if (N % 128 != 0) return fail(DG_ERR_UNSUPPORTED, "%s=%d must be a multiple of 128", name, N);
+    if (N > (1 << 28)) return fail(DG_ERR_UNSUPPORTED, "%s=%d is too large", name, N);
+    return DG_OK;
+}
+
+// The routing kernels' instance: lanes hold ceil(E / 32) experts, rounded up
+// to a power of two.
+template <typename L>
+dg_status launch_route(const dg::RouteParams& p, int64_t grid, int smem, void* st) {
+    const int threads = dg::kRouteWarps * 32, per = cdiv(p.E, 32);
+    if (per <= 1) return launch_plain(dg::route_topk_kernel<1, L>, p, grid, threads, smem, 1, st);
+    if (per <= 2) return launch_plain(dg::route_topk_kernel<2, L>, p, grid, threads, smem, 1, st);
+    if (per <= 4) return launch_plain(dg::route_topk_kernel<4, L>, p, grid, threads, smem, 1, st);
+    if (per <= 8) return launch_plain(dg::route_topk_kernel<8, L>, p, grid, threads, smem, 1, st);
+    if (per <= 16) return launch_plain(dg::route_topk_kernel<16, L>, p, grid, threads, smem, 1, st);
+    return launch_plain(dg::route_topk_kernel<32, L>, p, grid, threads, smem, 1, st);
+}
+
+template <typename L>
+dg_status launch_route_bwd(const dg::RouteBwdParams& p, int64_t grid, void* st) {
+    const int threads = dg::kRouteWarps * 32, per = cdiv(p.E, 32);
+    if (per <= 1) return launch_plain(dg::route_topk_bwd_kernel<1, L>, p, grid, threads, 0, 1, st);
+    if (per <= 2) return launch_plain(dg::route_topk_bwd_kernel<2, L>, p, grid, threads, 0, 1, st);
+    if (per <= 4) return launch_plain(dg::route_topk_bwd_kernel<4, L>, p, grid, threads, 0, 1, st);
+    if (per <= 8) return launch_plain(dg::route_topk_bwd_kernel<8, L>, p, grid, threads, 0, 1, st);
+    if (per <= 16) return launch_plain(dg::route_topk_bwd_kernel<16, L>, p, grid, threads, 0, 1, st);
+    return launch_plain(dg::route_topk_bwd_kernel<32, L>, p, grid, threads, 0, 1, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1157,6 +1262,198 @@ dg_status dg_to_fp8_128x128(uint8_t* Q, float* sb, const uint16_t* W, int N, int
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(DG_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
     return ok();
+}
+
+dg_status dg_route_topk(int32_t* topk_idx, float* topk_w, const void* logits, int logits_dtype, const float* bias, int T,
+                        int E, int k, int n_groups, int topk_groups, int group_top, int score, int renorm, float scale,
+                        void* stream) {
+    dg_status s = check_route(T, E, k, logits_dtype, score);
+    if (s != DG_OK) return s;
+    if (n_groups <= 0 || topk_groups <= 0 || topk_groups > n_groups || E % n_groups != 0)
+        return fail(DG_ERR_INVALID_ARG, "bad groups: n_groups=%d topk_groups=%d E=%d", n_groups, topk_groups, E);
+    if (group_top != 1 && group_top != 2) return fail(DG_ERR_INVALID_ARG, "group_top=%d must be 1 or 2", group_top);
+    if (n_groups > dg::kRouteMaxGroups)
+        return fail(DG_ERR_UNSUPPORTED, "n_groups=%d is more than %d", n_groups, dg::kRouteMaxGroups);
+    if (T == 0) return ok();
+    if (!topk_idx || !topk_w || !logits) return fail(DG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(bias, 4) ||
+        !aligned(logits, logits_dtype == DG_DTYPE_BF16 ? 2 : 4))
+        return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements");
+    // Keeping every group is the same as having none.
+    const int groups = topk_groups == n_groups ? 1 : n_groups;
+    const int gsize = E / groups;
+    dg::RouteParams p{logits, bias, topk_idx, topk_w, T, E, k, groups, groups == 1 ? 1 : topk_groups, group_top, gsize,
+                      (1u << 20) / static_cast<uint32_t>(gsize) + 1u, score == DG_SCORE_SOFTMAX, renorm != 0, scale};
+    const int64_t grid = cdiv64(T, dg::kRouteWarps);
+    const int smem = groups > 1 ? dg::kRouteWarps * E * static_cast<int>(sizeof(float)) : 0;
+    return logits_dtype == DG_DTYPE_BF16 ? launch_route<uint16_t>(p, grid, smem, stream)
+                                         : launch_route<float>(p, grid, smem, stream);
+}
+
+dg_status dg_route_topk_bwd(void* dlogits, const float* dw, const void* logits, int logits_dtype,
+                            const int32_t* topk_idx, int T, int E, int k, int score, int renorm, float scale,
+                            void* stream) {
+    dg_status s = check_route(T, E, k, logits_dtype, score);
+    if (s != DG_OK) return s;
+    if (T == 0) return ok();
+    if (!dlogits || !dw || !logits || !topk_idx) return fail(DG_ERR_INVALID_ARG, "null pointer");
+    const unsigned el = logits_dtype == DG_DTYPE_BF16 ? 2 : 4;
+    if (!aligned(topk_idx, 4) || !aligned(dw, 4) || !aligned(logits, el) || !aligned(dlogits, el))
+        return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements");
+    dg::RouteBwdParams p{dlogits, dw, logits, topk_idx, T, E, k, score == DG_SCORE_SOFTMAX, renorm != 0, scale};
+    const int64_t grid = cdiv64(T, dg::kRouteWarps);
+    return logits_dtype == DG_DTYPE_BF16 ? launch_route_bwd<uint16_t>(p, grid, stream)
+                                         : launch_route_bwd<float>(p, grid, stream);
+}
+
+int dg_get_layout_rows(int T, int k, int E) {
+    if (T < 0 || k <= 0 || k > kMaxSlots || E <= 0 || E > dg::kRouteMaxExperts) return -1;
+    const int64_t S = static_cast<int64_t>(T) * k;
+    const int64_t rows = (S + 127 * (S < E ? S : E)) / 128 * 128;
+    return S <= 0x7FFFFFFF && rows <= 0x7FFFFFFF ? static_cast<int>(rows) : -1;
+}
+
+dg_status dg_route_layout(int32_t* row_of, int32_t* m_indices, int32_t* slot_of, int32_t* group_offsets,
+                          int32_t* counts, const int32_t* topk_idx, int T, int k, int E, int rows, int max_rows,
+                          void* stream) {
+    dg_status s = check_slots(T, k, rows);
+    if (s != DG_OK) return s;
+    if (E <= 0 || max_rows < 0) return fail(DG_ERR_INVALID_ARG, "bad sizes E=%d max_rows=%d", E, max_rows);
+    if (E > dg::kRouteMaxExperts) return fail(DG_ERR_UNSUPPORTED, "E=%d is more than %d", E, dg::kRouteMaxExperts);
+    if (max_rows > 0 ? static_cast<int64_t>(E) * max_rows != rows : rows % 128 != 0)
+        return fail(DG_ERR_INVALID_ARG, "rows=%d must be %s", rows, max_rows > 0 ? "E*max_rows" : "a multiple of 128");
+    if (max_rows == 0) {
+        const int need = dg_get_layout_rows(T, k, E);
+        if (need < 0) return fail(DG_ERR_UNSUPPORTED, "the layout's rows do not fit in 31 bits");
+        if (rows < need) return fail(DG_ERR_INVALID_ARG, "rows=%d, any choice of experts fits in %d", rows, need);
+    }
+    const int64_t S = static_cast<int64_t>(T) * k;
+    if ((S > 0 && (!row_of || !topk_idx)) || (rows > 0 && (!m_indices || !slot_of)) || !group_offsets || !counts)
+        return fail(DG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(row_of, 4) || !aligned(m_indices, 4) || !aligned(slot_of, 4) || !aligned(group_offsets, 4) ||
+        !aligned(counts, 4) || !aligned(topk_idx, 4))
+        return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements");
+    // One CTA per 4096 slots, up to a cluster of 8.
+    int ctas = 1;
+    while (ctas < dg::kLayoutMaxCluster && S > static_cast<int64_t>(ctas) * 4096) ctas *= 2;
+    const int64_t warps = static_cast<int64_t>(ctas) * dg::kLayoutWarps;
+    dg::LayoutParams p{topk_idx, row_of, m_indices, slot_of, group_offsets, counts, S, cdiv64(cdiv64(S, warps), 32) * 32,
+                       E, rows, max_rows};
+    return launch_plain(dg::route_layout_kernel, p, ctas, dg::kLayoutThreads,
+                        dg::layout_smem_ints(E) * static_cast<int>(sizeof(int)), ctas, stream);
+}
+
+dg_status dg_dispatch_fp8_1x128(uint8_t* Q, float* sa, int sa_stride, const uint16_t* X, const int32_t* row_of, int T,
+                                int k, int K, int rows, int group_rows, void* stream) {
+    dg_status s = check_slots(T, k, rows);
+    if (s != DG_OK) return s;
+    if (K <= 0) return fail(DG_ERR_INVALID_ARG, "bad size K=%d", K);
+    if (K % dg::kBK != 0) return fail(DG_ERR_UNSUPPORTED, "K=%d must be a multiple of 128", K);
+    if ((s = check_scale_layout("sa_stride", sa_stride, rows, group_rows)) != DG_OK) return s;
+    if (T == 0 || rows == 0) return ok();
+    if (!Q || !sa || !X || !row_of) return fail(DG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(Q) || !aligned16(X) || !aligned(sa, 4) || !aligned(row_of, 4))
+        return fail(DG_ERR_MISALIGNED, "X and Q must be 16-byte aligned, sa and row_of 4-byte aligned");
+    const int sms = effective_sms();
+    if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
+    dg::DispatchParams p{Q, sa, X, row_of, T, k, K, K / dg::kBK, sa_stride, group_rows, rows};
+    const int64_t groups = cdiv64(T, dg::kCastRowsPerCta), cap = static_cast<int64_t>(sms) * 8;
+    // Four K blocks at a time while that still gives every SM a CTA, else one.
+    const int64_t wide = groups * cdiv(p.nkb, 4);
+    if (wide >= sms) return launch_plain(dg::dispatch_1x128_kernel<4>, p, wide < cap ? wide : cap, dg::kCastThreads, 0, 1, stream);
+    const int64_t one = groups * p.nkb;
+    return launch_plain(dg::dispatch_1x128_kernel<1>, p, one < cap ? one : cap, dg::kCastThreads, 0, 1, stream);
+}
+
+dg_status dg_combine(uint16_t* out, const uint16_t* Y, const int32_t* row_of, const float* w, int T, int k, int N,
+                     int rows, void* stream) {
+    dg_status s = check_slots(T, k, rows);
+    if (s != DG_OK) return s;
+    if (N <= 0) return fail(DG_ERR_INVALID_ARG, "bad size N=%d", N);
+    if (N % 8 != 0) return fail(DG_ERR_UNSUPPORTED, "N=%d must be a multiple of 8", N);
+    if (T == 0) return ok();
+    if (!out || !row_of || (rows > 0 && !Y)) return fail(DG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(out) || !aligned16(Y) || !aligned(row_of, 4) || !aligned(w, 4))
+        return fail(DG_ERR_MISALIGNED, "out and Y must be 16-byte aligned, row_of and w 4-byte aligned");
+    dg::CombineParams p{out, Y, row_of, w, T, k, N, rows};
+    return launch_plain(dg::combine_kernel, p, static_cast<int64_t>(T) * cdiv(N / 8, dg::kCombineThreads),
+                        dg::kCombineThreads, 0, 1, stream);
+}
+
+dg_status dg_combine_bwd(float* dw, uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, float* sc, int sc_stride,
+                         const uint16_t* dout, const uint16_t* Y, const int32_t* row_of, const int32_t* slot_of,
+                         const float* w, int T, int k, int N, int rows, void* stream) {
+    dg_status s = check_slots(T, k, rows);
+    if (s != DG_OK) return s;
+    if ((s = check_row_blocks(rows, N, "N")) != DG_OK) return s;
+    if (sr_stride < rows) return fail(DG_ERR_INVALID_ARG, "sr_stride=%d must be >= rows=%d", sr_stride, rows);
+    if (sc_stride < N) return fail(DG_ERR_INVALID_ARG, "sc_stride=%d must be >= N=%d", sc_stride, N);
+    if (T == 0) return ok();
+    if (rows == 0) return fail(DG_ERR_INVALID_ARG, "a layout of %d slots has rows", T * k);
+    if (!dw || !Qr || !sr || !Qc || !sc || !dout || !Y || !row_of || !slot_of || !w)
+        return fail(DG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(Qr) || !aligned16(Qc) || !aligned16(dout) || !aligned16(Y) || !aligned(dw, 4) || !aligned(sr, 4) ||
+        !aligned(sc, 4) || !aligned(row_of, 4) || !aligned(slot_of, 4) || !aligned(w, 4))
+        return fail(DG_ERR_MISALIGNED, "Qr, Qc, dout and Y must be 16-byte aligned, the others 4-byte aligned");
+    dg::CombineBwdParams p{{Qr, sr, Qc, sc, sr_stride, sc_stride}, dw, dout, Y, row_of, slot_of, w,
+                           static_cast<int64_t>(T) * k, k, N, N / 128, rows};
+    int ctas = 1;
+    while (ctas < 8 && ctas * 2 <= p.nkb) ctas *= 2;
+    return launch_plain(dg::combine_bwd_kernel, p, static_cast<int64_t>(rows / 128) * ctas, dg::kTileThreads, 0, ctas,
+                        stream);
+}
+
+dg_status dg_swiglu_fp8(uint8_t* Q, float* sa, int sa_stride, uint8_t* C, float* cs, int cs_stride, const uint16_t* H,
+                        const int32_t* m_indices, int rows, int F, int group_rows, void* stream) {
+    if (rows < 0 || F <= 0) return fail(DG_ERR_INVALID_ARG, "bad sizes rows=%d F=%d", rows, F);
+    if (F % dg::kBK != 0) return fail(DG_ERR_UNSUPPORTED, "F=%d must be a multiple of 128", F);
+    if (F > (1 << 28)) return fail(DG_ERR_UNSUPPORTED, "F=%d is too large", F);
+    dg_status s = check_scale_layout("sa_stride", sa_stride, rows, group_rows);
+    if (s == DG_OK && C) s = check_scale_layout("cs_stride", cs_stride, rows, group_rows);
+    if (s != DG_OK) return s;
+    if (rows == 0) return ok();
+    if (!Q || !sa || !H || (C && !cs)) return fail(DG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(Q) || !aligned16(C) || !aligned16(H) || !aligned(sa, 4) || !aligned(cs, 4) || !aligned(m_indices, 4))
+        return fail(DG_ERR_MISALIGNED, "Q, C and H must be 16-byte aligned, the others 4-byte aligned");
+    const int sms = effective_sms();
+    if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
+    dg::SwigluParams p{Q, sa, C, cs, H, m_indices, sa_stride, cs_stride, group_rows, F, F / dg::kBK, rows};
+    const int64_t groups = cdiv64(rows, dg::kCastRowsPerCta), cap = static_cast<int64_t>(sms) * 8;
+    const int64_t items = groups * cdiv(p.nfb, 2);
+    return launch_plain(dg::swiglu_fp8_kernel<2>, p, items < cap ? items : cap, dg::kCastThreads, 0, 1, stream);
+}
+
+dg_status dg_swiglu_fp8_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, float* sc, int sc_stride, uint8_t* Qa,
+                            float* sb, const uint16_t* dA, const uint8_t* C, const float* cs, int cs_stride,
+                            const int32_t* m_indices, int rows, int F, void* stream) {
+    dg_status s = check_row_blocks(rows, F, "F");
+    if (s != DG_OK) return s;
+    if (sr_stride < rows || cs_stride < rows)
+        return fail(DG_ERR_INVALID_ARG, "sr_stride=%d and cs_stride=%d must be >= rows=%d", sr_stride, cs_stride, rows);
+    if (sc_stride < 2 * F) return fail(DG_ERR_INVALID_ARG, "sc_stride=%d must be >= 2F=%d", sc_stride, 2 * F);
+    if (rows == 0) return ok();
+    if (!Qr || !sr || !Qc || !sc || !Qa || !sb || !dA || !C || !cs) return fail(DG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(Qr) || !aligned16(Qc) || !aligned16(Qa) || !aligned16(dA) || !aligned16(C) || !aligned(sr, 4) ||
+        !aligned(sc, 4) || !aligned(sb, 4) || !aligned(cs, 4) || !aligned(m_indices, 4))
+        return fail(DG_ERR_MISALIGNED, "Qr, Qc, Qa, dA and C must be 16-byte aligned, the others 4-byte aligned");
+    dg::SwigluBwdParams p{{Qr, sr, Qc, sc, sr_stride, sc_stride}, Qa, sb, dA, C, cs, m_indices, cs_stride, F,
+                          F / dg::kBK, rows};
+    return launch_plain(dg::swiglu_fp8_bwd_kernel, p, static_cast<int64_t>(rows / 128) * p.nfb, dg::kTileThreads, 0, 1,
+                        stream);
+}
+
+dg_status dg_fp8_1x128_to_128x128(uint8_t* Qb, float* sb, const uint8_t* Q, const float* sa, int sa_stride,
+                                  const int32_t* m_indices, int rows, int K, void* stream) {
+    dg_status s = check_row_blocks(rows, K, "K");
+    if (s != DG_OK) return s;
+    if (sa_stride < rows) return fail(DG_ERR_INVALID_ARG, "sa_stride=%d must be >= rows=%d", sa_stride, rows);
+    if (rows == 0) return ok();
+    if (!Qb || !sb || !Q || !sa) return fail(DG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(Qb) || !aligned16(Q) || !aligned(sb, 4) || !aligned(sa, 4) || !aligned(m_indices, 4))
+        return fail(DG_ERR_MISALIGNED, "Qb and Q must be 16-byte aligned, the others 4-byte aligned");
+    dg::RecastParams p{Qb, sb, Q, sa, m_indices, sa_stride, K, K / dg::kBK, rows};
+    return launch_plain(dg::recast_128x128_kernel, p, static_cast<int64_t>(rows / 128) * p.nkb, dg::kRecastThreads, 0, 1,
+                        stream);
 }
 
 void dg_set_pdl(int enable) { g_pdl.store(enable < 0 ? -1 : (enable ? 1 : 0)); }
