@@ -20,6 +20,8 @@ import ctypes
 import os
 import threading
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdg.so")
 
@@ -169,7 +171,6 @@ def _check_args(func: str, *specs) -> None:
         if t.device.type != "cuda":
             raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is not on a CUDA device ({t.device})")
     if given:
-        import torch
         cur = torch.cuda.current_device()
         for name, t, _, _ in given:
             if t.device.index != cur:
@@ -188,7 +189,6 @@ def _check_dense(func: str, D, A, sa, sa_stride, B, sb, M: int, N: int, K: int, 
 
 def _stream(stream) -> int:
     if stream is None:
-        import torch
         return int(torch.cuda.current_stream().cuda_stream)
     return int(stream if isinstance(stream, int) else stream.cuda_stream)
 
@@ -328,15 +328,48 @@ def _shape1(func: str, name: str, t) -> int:
     return t.shape[0]
 
 
-def _check_kinds(func: str, **kinds) -> None:
-    """Element types that the size alone does not tell apart: name=(tensor, "int32", "float32" or "bfloat16")."""
-    for name, (t, kind) in kinds.items():
-        if t is not None and str(t.dtype) != "torch." + kind:
-            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call takes {kind}")
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+
+
+def _check_tensors(func: str, *specs) -> int:
+    """_check_args for the calls around the GEMMs, and the current device's index.
+
+    Each spec is (name, tensor, torch dtype or element bytes, elements the call
+    touches).  One pass over the tensors: a decoding step makes these calls every
+    few microseconds."""
+    dev, stray = None, None
+    for name, t, kind, need in specs:
+        if t is None:
+            continue
+        if kind is not t.dtype and kind != t.element_size():
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call takes "
+                          + (f"{kind}-byte elements" if isinstance(kind, int) else str(kind)))
+        if not t.is_contiguous():
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is not contiguous")
+        if t.numel() < need:
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} holds {t.numel()} elements, the call touches {need}")
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        if d != dev or d < 0:
+            stray = stray or (name, t)
+    if stray is not None and any(t is not None and t.device.type != "cuda" for _, t, _, _ in specs):
+        name, t = next((n, t) for n, t, _, _ in specs if t is not None and t.device.type != "cuda")
+        raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is not on a CUDA device ({t.device})")
+    cur = torch.cuda.current_device()
+    if stray is not None or dev != cur:
+        name, t = next((n, t) for n, t, _, _ in specs if t is not None and t.get_device() != cur)
+        raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is on {t.device}, the current device is cuda:{cur}")
+    return cur
+
+
+def _raw_stream(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
 
 
 def _logits_dtype(func: str, logits) -> int:
-    import torch
     if logits.dtype == torch.bfloat16:
         return DG_DTYPE_BF16
     if logits.dtype == torch.float32:
@@ -360,12 +393,11 @@ def dg_route_topk(topk_idx, topk_w, logits, bias=None, n_groups: int = 1, topk_g
     Ti, k = _shape2(func, "topk_idx", topk_idx)
     _check_dim(func, "token count of topk_idx", Ti, T)
     dt = _logits_dtype(func, logits)
-    _check_kinds(func, topk_idx=(topk_idx, "int32"), topk_w=(topk_w, "float32"), bias=(bias, "float32"))
-    _check_args(func, ("topk_idx", topk_idx, 4, T * k), ("topk_w", topk_w, 4, T * k),
-                ("logits", logits, logits.element_size(), T * E), ("bias", bias, 4, E))
+    dev = _check_tensors(func, ("topk_idx", topk_idx, _I32, T * k), ("topk_w", topk_w, _F32, T * k),
+                         ("logits", logits, logits.dtype, T * E), ("bias", bias, _F32, E))
     _check(func, lib().dg_route_topk(_ptr(topk_idx), _ptr(topk_w), _ptr(logits), dt, _ptr(bias), T, E, k,
                                      int(n_groups), int(topk_groups), int(group_top), int(score), int(bool(renorm)),
-                                     float(scale), _stream(stream)))
+                                     float(scale), _raw_stream(stream, dev)))
 
 
 def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTMAX, renorm: bool = False,
@@ -378,11 +410,10 @@ def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTM
     dt = _logits_dtype(func, logits)
     if dlogits is not None and dlogits.dtype != logits.dtype:
         raise DGError(func, DG_ERR_INVALID_ARG, f"dlogits are {dlogits.dtype}, logits {logits.dtype}")
-    _check_kinds(func, topk_idx=(topk_idx, "int32"), dw=(dw, "float32"))
-    _check_args(func, ("dlogits", dlogits, logits.element_size(), T * E), ("dw", dw, 4, T * k),
-                ("logits", logits, logits.element_size(), T * E), ("topk_idx", topk_idx, 4, T * k))
+    dev = _check_tensors(func, ("dlogits", dlogits, logits.dtype, T * E), ("dw", dw, _F32, T * k),
+                         ("logits", logits, logits.dtype, T * E), ("topk_idx", topk_idx, _I32, T * k))
     _check(func, lib().dg_route_topk_bwd(_ptr(dlogits), _ptr(dw), _ptr(logits), dt, _ptr(topk_idx), T, E, k,
-                                         int(score), int(bool(renorm)), float(scale), _stream(stream)))
+                                         int(score), int(bool(renorm)), float(scale), _raw_stream(stream, dev)))
 
 
 def dg_get_layout_rows(T: int, k: int, E: int) -> int:
@@ -398,12 +429,11 @@ def dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx,
     func = "dg_route_layout"
     T, k = _shape2(func, "topk_idx", topk_idx)
     rows, E = _shape1(func, "m_indices", m_indices), _shape1(func, "counts", counts)
-    _check_kinds(func, row_of=(row_of, "int32"), m_indices=(m_indices, "int32"), slot_of=(slot_of, "int32"),
-                 group_offsets=(group_offsets, "int32"), counts=(counts, "int32"), topk_idx=(topk_idx, "int32"))
-    _check_args(func, ("row_of", row_of, 4, T * k), ("m_indices", m_indices, 4, rows), ("slot_of", slot_of, 4, rows),
-                ("group_offsets", group_offsets, 4, E + 1), ("counts", counts, 4, E), ("topk_idx", topk_idx, 4, T * k))
+    dev = _check_tensors(func, ("row_of", row_of, _I32, T * k), ("m_indices", m_indices, _I32, rows),
+                         ("slot_of", slot_of, _I32, rows), ("group_offsets", group_offsets, _I32, E + 1),
+                         ("counts", counts, _I32, E), ("topk_idx", topk_idx, _I32, T * k))
     _check(func, lib().dg_route_layout(_ptr(row_of), _ptr(m_indices), _ptr(slot_of), _ptr(group_offsets),
-                                       _ptr(counts), _ptr(topk_idx), T, k, E, rows, int(max_rows), _stream(stream)))
+                                       _ptr(counts), _ptr(topk_idx), T, k, E, rows, int(max_rows), _raw_stream(stream, dev)))
 
 
 def dg_dispatch_fp8_1x128(Q, sa, sa_stride: int, X, row_of, group_rows: int = 0, stream=None) -> None:
@@ -415,11 +445,11 @@ def dg_dispatch_fp8_1x128(Q, sa, sa_stride: int, X, row_of, group_rows: int = 0,
     _check_dim(func, "token count of row_of", Ti, T)
     _check_dim(func, "K of Q", Q.shape[-1], K)
     rows = Q.numel() // K if K else 0
-    _check_kinds(func, row_of=(row_of, "int32"), sa=(sa, "float32"), X=(X, "bfloat16"))
-    _check_args(func, ("Q", Q, 1, rows * K), ("sa", sa, 4, _scales_need(_cdiv(K, 128), sa_stride, rows, group_rows)),
-                ("X", X, 2, T * K), ("row_of", row_of, 4, T * k))
+    dev = _check_tensors(func, ("Q", Q, 1, rows * K),
+                         ("sa", sa, _F32, _scales_need(_cdiv(K, 128), sa_stride, rows, group_rows)),
+                         ("X", X, _BF16, T * K), ("row_of", row_of, _I32, T * k))
     _check(func, lib().dg_dispatch_fp8_1x128(_ptr(Q), _ptr(sa), int(sa_stride), _ptr(X), _ptr(row_of), T, k, K, rows,
-                                             int(group_rows), _stream(stream)))
+                                             int(group_rows), _raw_stream(stream, dev)))
 
 
 def dg_combine(out, Y, row_of, w=None, stream=None) -> None:
@@ -431,9 +461,9 @@ def dg_combine(out, Y, row_of, w=None, stream=None) -> None:
     _check_dim(func, "token count of row_of", Ti, T)
     _check_dim(func, "N of Y", Y.shape[-1], N)
     rows = Y.numel() // N if N else 0
-    _check_kinds(func, out=(out, "bfloat16"), Y=(Y, "bfloat16"), row_of=(row_of, "int32"), w=(w, "float32"))
-    _check_args(func, ("out", out, 2, T * N), ("Y", Y, 2, rows * N), ("row_of", row_of, 4, T * k), ("w", w, 4, T * k))
-    _check(func, lib().dg_combine(_ptr(out), _ptr(Y), _ptr(row_of), _ptr(w), T, k, N, rows, _stream(stream)))
+    dev = _check_tensors(func, ("out", out, _BF16, T * N), ("Y", Y, _BF16, rows * N), ("row_of", row_of, _I32, T * k),
+                         ("w", w, _F32, T * k))
+    _check(func, lib().dg_combine(_ptr(out), _ptr(Y), _ptr(row_of), _ptr(w), T, k, N, rows, _raw_stream(stream, dev)))
 
 
 def dg_combine_bwd(dw, Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, dout, Y, row_of, slot_of, w,
@@ -446,15 +476,14 @@ def dg_combine_bwd(dw, Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, dout, Y, 
     rows, Ny = _shape2(func, "Y", Y)
     _check_dim(func, "token count of row_of", Ti, T)
     _check_dim(func, "N of Y", Ny, N)
-    _check_kinds(func, dw=(dw, "float32"), sr=(sr, "float32"), sc=(sc, "float32"), dout=(dout, "bfloat16"), Y=(Y, "bfloat16"),
-                 w=(w, "float32"), row_of=(row_of, "int32"), slot_of=(slot_of, "int32"))
-    _check_args(func, ("dw", dw, 4, T * k), ("Qr", Qr, 1, rows * N),
-                ("sr", sr, 4, _sa_need(_cdiv(N, 128), sr_stride, rows)), ("Qc", Qc, 1, rows * N),
-                ("sc", sc, 4, _sa_need(_cdiv(rows, 128), sc_stride, N)), ("dout", dout, 2, T * N),
-                ("Y", Y, 2, rows * N), ("row_of", row_of, 4, T * k), ("slot_of", slot_of, 4, rows), ("w", w, 4, T * k))
+    dev = _check_tensors(func, ("dw", dw, _F32, T * k), ("Qr", Qr, 1, rows * N),
+                         ("sr", sr, _F32, _sa_need(_cdiv(N, 128), sr_stride, rows)), ("Qc", Qc, 1, rows * N),
+                         ("sc", sc, _F32, _sa_need(_cdiv(rows, 128), sc_stride, N)), ("dout", dout, _BF16, T * N),
+                         ("Y", Y, _BF16, rows * N), ("row_of", row_of, _I32, T * k), ("slot_of", slot_of, _I32, rows),
+                         ("w", w, _F32, T * k))
     _check(func, lib().dg_combine_bwd(_ptr(dw), _ptr(Qr), _ptr(sr), int(sr_stride), _ptr(Qc), _ptr(sc),
                                       int(sc_stride), _ptr(dout), _ptr(Y), _ptr(row_of), _ptr(slot_of), _ptr(w),
-                                      T, k, N, rows, _stream(stream)))
+                                      T, k, N, rows, _raw_stream(stream, dev)))
 
 
 def dg_swiglu_fp8(Q, sa, sa_stride: int, H, C=None, cs=None, cs_stride: int = 0, m_indices=None, group_rows: int = 0,
@@ -466,13 +495,13 @@ def dg_swiglu_fp8(Q, sa, sa_stride: int, H, C=None, cs=None, cs_stride: int = 0,
     _check_dim(func, "last extent of H", H.shape[-1], 2 * F)
     _check_dim(func, "F of Q", Q.shape[-1], F)
     rows = H.numel() // (2 * F) if F else 0
-    _check_kinds(func, H=(H, "bfloat16"), sa=(sa, "float32"), cs=(cs, "float32"), m_indices=(m_indices, "int32"))
-    _check_args(func, ("Q", Q, 1, rows * F), ("sa", sa, 4, _scales_need(_cdiv(F, 128), sa_stride, rows, group_rows)),
-                ("H", H, 2, rows * 2 * F), ("C", C, 1, rows * 2 * F),
-                ("cs", cs if C is not None else None, 4, _scales_need(2 * _cdiv(F, 128), cs_stride, rows, group_rows)),
-                ("m_indices", m_indices, 4, rows))
+    dev = _check_tensors(func, ("Q", Q, 1, rows * F),
+                         ("sa", sa, _F32, _scales_need(_cdiv(F, 128), sa_stride, rows, group_rows)),
+                         ("H", H, _BF16, rows * 2 * F), ("C", C, 1, rows * 2 * F),
+                         ("cs", cs if C is not None else None, _F32, _scales_need(2 * _cdiv(F, 128), cs_stride, rows, group_rows)),
+                         ("m_indices", m_indices, _I32, rows))
     _check(func, lib().dg_swiglu_fp8(_ptr(Q), _ptr(sa), int(sa_stride), _ptr(C), _ptr(cs), int(cs_stride), _ptr(H),
-                                     _ptr(m_indices), rows, F, int(group_rows), _stream(stream)))
+                                     _ptr(m_indices), rows, F, int(group_rows), _raw_stream(stream, dev)))
 
 
 def dg_swiglu_fp8_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, Qa, sb, dA, C, cs, cs_stride: int,
@@ -483,16 +512,15 @@ def dg_swiglu_fp8_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, Qa, sb, dA
     func = "dg_swiglu_fp8_bwd"
     rows, F = _shape2(func, "dA", dA)
     _check_dim(func, "last extent of C", C.shape[-1], 2 * F)
-    _check_kinds(func, sr=(sr, "float32"), sc=(sc, "float32"), sb=(sb, "float32"), dA=(dA, "bfloat16"), cs=(cs, "float32"),
-                 m_indices=(m_indices, "int32"))
-    _check_args(func, ("Qr", Qr, 1, rows * 2 * F), ("sr", sr, 4, _sa_need(2 * _cdiv(F, 128), sr_stride, rows)),
-                ("Qc", Qc, 1, rows * 2 * F), ("sc", sc, 4, _sa_need(_cdiv(rows, 128), sc_stride, 2 * F)),
-                ("Qa", Qa, 1, rows * F), ("sb", sb, 4, _cdiv(F, 128) * _cdiv(rows, 128)), ("dA", dA, 2, rows * F),
-                ("C", C, 1, rows * 2 * F), ("cs", cs, 4, _sa_need(2 * _cdiv(F, 128), cs_stride, rows)),
-                ("m_indices", m_indices, 4, rows))
+    dev = _check_tensors(func, ("Qr", Qr, 1, rows * 2 * F),
+                         ("sr", sr, _F32, _sa_need(2 * _cdiv(F, 128), sr_stride, rows)), ("Qc", Qc, 1, rows * 2 * F),
+                         ("sc", sc, _F32, _sa_need(_cdiv(rows, 128), sc_stride, 2 * F)), ("Qa", Qa, 1, rows * F),
+                         ("sb", sb, _F32, _cdiv(F, 128) * _cdiv(rows, 128)), ("dA", dA, _BF16, rows * F),
+                         ("C", C, 1, rows * 2 * F), ("cs", cs, _F32, _sa_need(2 * _cdiv(F, 128), cs_stride, rows)),
+                         ("m_indices", m_indices, _I32, rows))
     _check(func, lib().dg_swiglu_fp8_bwd(_ptr(Qr), _ptr(sr), int(sr_stride), _ptr(Qc), _ptr(sc), int(sc_stride),
                                          _ptr(Qa), _ptr(sb), _ptr(dA), _ptr(C), _ptr(cs), int(cs_stride),
-                                         _ptr(m_indices), rows, F, _stream(stream)))
+                                         _ptr(m_indices), rows, F, _raw_stream(stream, dev)))
 
 
 def dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride: int, m_indices=None, stream=None) -> None:
@@ -500,11 +528,11 @@ def dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride: int, m_indices=None, strea
     128x128, sb [K/128, rows/128] (contiguous layout)."""
     func = "dg_fp8_1x128_to_128x128"
     rows, K = _shape2(func, "Q", Q)
-    _check_kinds(func, sb=(sb, "float32"), sa=(sa, "float32"), m_indices=(m_indices, "int32"))
-    _check_args(func, ("Qb", Qb, 1, rows * K), ("sb", sb, 4, _cdiv(K, 128) * _cdiv(rows, 128)), ("Q", Q, 1, rows * K),
-                ("sa", sa, 4, _sa_need(_cdiv(K, 128), sa_stride, rows)), ("m_indices", m_indices, 4, rows))
+    dev = _check_tensors(func, ("Qb", Qb, 1, rows * K), ("sb", sb, _F32, _cdiv(K, 128) * _cdiv(rows, 128)),
+                         ("Q", Q, 1, rows * K), ("sa", sa, _F32, _sa_need(_cdiv(K, 128), sa_stride, rows)),
+                         ("m_indices", m_indices, _I32, rows))
     _check(func, lib().dg_fp8_1x128_to_128x128(_ptr(Qb), _ptr(sb), _ptr(Q), _ptr(sa), int(sa_stride),
-                                               _ptr(m_indices), rows, K, _stream(stream)))
+                                               _ptr(m_indices), rows, K, _raw_stream(stream, dev)))
 
 
 def dg_set_pdl(enable) -> None:
@@ -569,7 +597,6 @@ def dg_get_col_major_tma_aligned_tensor(s):
 
     Layout helper for callers (the pages' get_col_major_tma_aligned_tensor);
     runs as torch tensor ops outside the timed path."""
-    import torch
     grouped = s.dim() == 3
     s3 = s if grouped else s.unsqueeze(0)
     G, M, nkb = s3.shape

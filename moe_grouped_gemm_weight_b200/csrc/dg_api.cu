@@ -907,6 +907,10 @@ dg_status check_row_blocks(int64_t rows, int N, const char* name) {
     return DG_OK;
 }
 
+// Every lane holds `per` experts, and that is an instance's number: wide loads
+// and stores of whole lanes.
+bool full_lanes(int E, int per) { return E == 32 * per && (per & (per - 1)) == 0; }
+
 // The routing kernels' instance: lanes hold ceil(E / 32) experts, rounded up
 // to a power of two.
 template <typename L>
@@ -1282,10 +1286,15 @@ dg_status dg_route_topk(int32_t* topk_idx, float* topk_w, const void* logits, in
     // Keeping every group is the same as having none.
     const int groups = topk_groups == n_groups ? 1 : n_groups;
     const int gsize = E / groups;
+    const int per = cdiv(E, 32), gl = gsize % per == 0 ? gsize / per : 0;
+    // Groups of whole lanes need no shared memory; every group's lanes join in a power of two.
+    const int group_lanes = groups > 1 && gl > 0 && (gl & (gl - 1)) == 0 ? gl : 0;
     dg::RouteParams p{logits, bias, topk_idx, topk_w, T, E, k, groups, groups == 1 ? 1 : topk_groups, group_top, gsize,
-                      (1u << 20) / static_cast<uint32_t>(gsize) + 1u, score == DG_SCORE_SOFTMAX, renorm != 0, scale};
+                      (1u << 20) / static_cast<uint32_t>(gsize) + 1u, per, group_lanes,
+                      full_lanes(E, per) && aligned16(logits) && aligned16(bias), score == DG_SCORE_SOFTMAX, renorm != 0,
+                      scale};
     const int64_t grid = cdiv64(T, dg::kRouteWarps);
-    const int smem = groups > 1 ? dg::kRouteWarps * E * static_cast<int>(sizeof(float)) : 0;
+    const int smem = groups > 1 && !group_lanes ? dg::kRouteWarps * E * static_cast<int>(sizeof(float)) : 0;
     return logits_dtype == DG_DTYPE_BF16 ? launch_route<uint16_t>(p, grid, smem, stream)
                                          : launch_route<float>(p, grid, smem, stream);
 }
@@ -1300,7 +1309,10 @@ dg_status dg_route_topk_bwd(void* dlogits, const float* dw, const void* logits, 
     const unsigned el = logits_dtype == DG_DTYPE_BF16 ? 2 : 4;
     if (!aligned(topk_idx, 4) || !aligned(dw, 4) || !aligned(logits, el) || !aligned(dlogits, el))
         return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements");
-    dg::RouteBwdParams p{dlogits, dw, logits, topk_idx, T, E, k, score == DG_SCORE_SOFTMAX, renorm != 0, scale};
+    const int per = cdiv(E, 32);
+    dg::RouteBwdParams p{dlogits, dw, logits, topk_idx, T, E, k, per,
+                         full_lanes(E, per) && aligned16(logits) && aligned16(dlogits), score == DG_SCORE_SOFTMAX,
+                         renorm != 0, scale};
     const int64_t grid = cdiv64(T, dg::kRouteWarps);
     return logits_dtype == DG_DTYPE_BF16 ? launch_route_bwd<uint16_t>(p, grid, stream)
                                          : launch_route_bwd<float>(p, grid, stream);
@@ -1399,8 +1411,8 @@ dg_status dg_combine_bwd(float* dw, uint8_t* Qr, float* sr, int sr_stride, uint8
                            static_cast<int64_t>(T) * k, k, N, N / 128, rows};
     int ctas = 1;
     while (ctas < 8 && ctas * 2 <= p.nkb) ctas *= 2;
-    return launch_plain(dg::combine_bwd_kernel, p, static_cast<int64_t>(rows / 128) * ctas, dg::kTileThreads, 0, ctas,
-                        stream);
+    return launch_plain(dg::combine_bwd_kernel, p, static_cast<int64_t>(rows / 128) * ctas, dg::kCombineBwdThreads,
+                        dg::kCombineBwdStage, ctas, stream);
 }
 
 dg_status dg_swiglu_fp8(uint8_t* Q, float* sa, int sa_stride, uint8_t* C, float* cs, int cs_stride, const uint16_t* H,
@@ -1438,8 +1450,11 @@ dg_status dg_swiglu_fp8_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, 
         return fail(DG_ERR_MISALIGNED, "Qr, Qc, Qa, dA and C must be 16-byte aligned, the others 4-byte aligned");
     dg::SwigluBwdParams p{{Qr, sr, Qc, sc, sr_stride, sc_stride}, Qa, sb, dA, C, cs, m_indices, cs_stride, F,
                           F / dg::kBK, rows};
-    return launch_plain(dg::swiglu_fp8_bwd_kernel, p, static_cast<int64_t>(rows / 128) * p.nfb, dg::kTileThreads, 0, 1,
-                        stream);
+    const int sms = effective_sms();
+    if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
+    const int64_t tiles = static_cast<int64_t>(rows / 128) * p.nfb;
+    return launch_plain(dg::swiglu_fp8_bwd_kernel, p, tiles < sms ? tiles : sms, dg::kSwigluBwdThreads,
+                        2 * dg::kSwigluBwdStage, 1, stream);
 }
 
 dg_status dg_fp8_1x128_to_128x128(uint8_t* Qb, float* sb, const uint8_t* Q, const float* sa, int sa_stride,

@@ -77,21 +77,22 @@ swiglu_fp8_kernel(const SwigluParams p) {
             bf16x8_to_float(vu[b], u);
 #pragma unroll
             for (int x = 0; x < 8; ++x) a[x] = __fdividef(g[x], 1.f + __expf(-g[x])) * u[x];
-            const float am = fmaxf(half_warp_max(amax8(a)), 1e-4f);
-            const float gm = fmaxf(half_warp_max(amax8(g)), 1e-4f);
-            const float um = fmaxf(half_warp_max(amax8(u)), 1e-4f);
+            // three casts: the scales of a, gate and up (the fourth place is spare)
+            float m[4] = {amax8(a), amax8(g), amax8(u), 0.f};
+            const float sc = spread_scale<4>(half_warp_max_spread<4>(m));
+            const int base = threadIdx.x & 16;
+            const float ra = __shfl_sync(0xffffffffu, sc, base), rg = __shfl_sync(0xffffffffu, sc, base + 1);
+            const float ru = __shfl_sync(0xffffffffu, sc, base + 2);
             if (!there || fb0 + b >= p.nfb) continue;
             const int fb = fb0 + b;
-            *reinterpret_cast<uint2*>(p.Q + row * p.F + fb * 128 + hl * 8) = e4m3x8(a, __fdiv_rn(448.f, am));
-            if (hl == 0) p.sa[scale_at(row, fb, p.nfb, p.sa_stride, p.group_rows)] = __fdiv_rn(am, 448.f);
+            *reinterpret_cast<uint2*>(p.Q + row * p.F + fb * 128 + hl * 8) = e4m3x8(a, ra);
+            if (hl == 4) p.sa[scale_at(row, fb, p.nfb, p.sa_stride, p.group_rows)] = sc;
             if (p.C != nullptr) {
                 uint8_t* cr = p.C + row * 2 * p.F + fb * 128 + hl * 8;
-                *reinterpret_cast<uint2*>(cr) = e4m3x8(g, __fdiv_rn(448.f, gm));
-                *reinterpret_cast<uint2*>(cr + p.F) = e4m3x8(u, __fdiv_rn(448.f, um));
-                if (hl == 0) {
-                    p.cs[scale_at(row, fb, 2 * p.nfb, p.cs_stride, p.group_rows)] = __fdiv_rn(gm, 448.f);
-                    p.cs[scale_at(row, p.nfb + fb, 2 * p.nfb, p.cs_stride, p.group_rows)] = __fdiv_rn(um, 448.f);
-                }
+                *reinterpret_cast<uint2*>(cr) = e4m3x8(g, rg);
+                *reinterpret_cast<uint2*>(cr + p.F) = e4m3x8(u, ru);
+                if (hl == 5 || hl == 6)
+                    p.cs[scale_at(row, fb + (hl == 6 ? p.nfb : 0), 2 * p.nfb, p.cs_stride, p.group_rows)] = sc;
             }
         }
     }
@@ -112,109 +113,152 @@ struct SwigluBwdParams {
     int64_t rows;
 };
 
-// A CTA takes a 128 x 128 tile of the expert width, for gate and up: thread
-// layout as in dg_moe.cuh's tiles.  dg stays in registers; du = da silu and
-// a = silu u are formed again from silu where they are used (one product),
-// which keeps the tile within the register file.
-__global__ void __launch_bounds__(kTileThreads)
+constexpr int kSwigluBwdThreads = 512;
+// A stage of shared memory: each thread's pieces of dA, gate and up, then the
+// rows' two scales.
+constexpr int kSwigluBwdScales = 128 * 128 * 4;
+constexpr int kSwigluBwdStage = kSwigluBwdScales + 128 * 2 * 4;
+
+// A persistent CTA takes 128 x 128 tiles of the expert width, for gate and up:
+// thread layout as in dg_moe.cuh's tiles.  dg and silu stay in registers;
+// du = da silu and a = silu u are formed where they are used (one product),
+// from da and u in shared memory, which keeps the tile within the register
+// file.  Two stages: the next tile's bytes arrive during this one's casts, and
+// as every thread copies what it will itself use, no barrier guards them.
+__global__ void __launch_bounds__(kSwigluBwdThreads)
 swiglu_fp8_bwd_kernel(const SwigluBwdParams p) {
-    __shared__ float cm[2][kTileThreads / 32 * 128];
+    constexpr int T = kSwigluBwdThreads, R = CastTile<T>::kRows;
+    static_assert(R == 4 && CastTile<T>::kStep == 32, "a mask of row flags per i");
+    extern __shared__ __align__(16) uint8_t stage_smem[];
+    __shared__ __align__(16) float cm[2][CastTile<T>::kWarps * CastTile<T>::kStride];
     __shared__ __align__(16) float cr[2][128];
-    __shared__ float wm[kTileThreads / 32];
+    __shared__ float wm[CastTile<T>::kWarps];
     griddep_wait();
     griddep_launch_dependents();
-    const int tid = threadIdx.x, half = tid >> 4, hl = tid & 15;
-    const int64_t rb = blockIdx.x / p.nfb;
-    const int fb = static_cast<int>(blockIdx.x % p.nfb);
-    const int64_t row0 = rb * 128;
-    const int col = fb * 128 + hl * 8;
+    const int tid = threadIdx.x, lane = tid & 31, half = tid >> 4, hl = tid & 15;
+    const int64_t tiles = p.rows / 128 * p.nfb;
+    const uint32_t stage0 = smem_u32(stage_smem);
 
-    bool there[kTileRows];
-    bool any = false;
+    // Row flags of a tile: bit r of mask i is row r + 32 i.
+    auto flags = [&](int64_t tile, uint32_t (&mask)[4]) {
+        const int64_t row0 = tile / p.nfb * 128;
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        there[i] = p.m_indices == nullptr || p.m_indices[row0 + half + 32 * i] >= 0;
-        any |= there[i];
-    }
-    if (!__syncthreads_or(any)) return;
-
-    uint4 da[kTileRows];
-    uint2 cu[kTileRows], cg[kTileRows];
-    float sg[kTileRows], su[kTileRows];
+        for (int i = 0; i < 4; ++i)
+            mask[i] = __ballot_sync(0xffffffffu, p.m_indices == nullptr || p.m_indices[row0 + lane + 32 * i] >= 0);
+    };
+    auto fetch = [&](int64_t tile, const uint32_t (&mask)[4], int st) {
+        const int64_t row0 = tile / p.nfb * 128;
+        const int fb = static_cast<int>(tile % p.nfb);
+        const int64_t col = fb * 128 + hl * 8;
+        const uint32_t at = stage0 + st * kSwigluBwdStage;
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        da[i] = make_uint4(0, 0, 0, 0);
-        cg[i] = cu[i] = make_uint2(0, 0);
-        sg[i] = su[i] = 0.f;
-        if (there[i]) {
+        for (int i = 0; i < R; ++i) {
             const int64_t row = row0 + half + 32 * i;
-            da[i] = ld_once_16(p.dA + row * p.F + col);
-            cg[i] = ld_once_8(p.C + row * 2 * p.F + col);
-            cu[i] = ld_once_8(p.C + row * 2 * p.F + p.F + col);
-            sg[i] = p.cs[static_cast<int64_t>(fb) * p.cs_stride + row];
-            su[i] = p.cs[static_cast<int64_t>(p.nfb + fb) * p.cs_stride + row];
+            const bool ok = (mask[i] >> half) & 1u;
+            cp_async_16(at + (i * T + tid) * 16, p.dA + row * p.F + col, ok ? 16 : 0);
+            cp_async_8(at + R * T * 16 + (2 * i * T + tid) * 8, p.C + row * 2 * p.F + col, ok ? 8 : 0);
+            cp_async_8(at + R * T * 16 + ((2 * i + 1) * T + tid) * 8, p.C + row * 2 * p.F + p.F + col, ok ? 8 : 0);
         }
-    }
-    float dg[kTileRows][8], silu[kTileRows][8];
-    float am = 0.f;
-#pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        float u[8], d[8];
-        e4m3x8_to_float(cg[i], silu[i]);
-        e4m3x8_to_float(cu[i], u);
-        bf16x8_to_float(da[i], d);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const float g = __fmul_rn(silu[i][x], sg[i]), v = __fmul_rn(u[x], su[i]);
-            const float s = __fdividef(1.f, 1.f + __expf(-g));
-            silu[i][x] = __fmul_rn(g, s);
-            dg[i][x] = d[x] * v * fmaf(silu[i][x], 1.f - s, s);
-            am = fmaxf(am, fabsf(__fmul_rn(silu[i][x], v)));
+        if (hl < 8) {  // lane i: gate scale of row i, lane 4 + i: up scale
+            const int64_t row = row0 + half + 32 * (hl & 3);
+            const uint32_t m = (hl & 2) ? (hl & 1 ? mask[3] : mask[2]) : (hl & 1 ? mask[1] : mask[0]);
+            cp_async_4(at + kSwigluBwdScales + (half * 8 + hl) * 4,
+                       p.cs + static_cast<int64_t>(fb + (hl & 4 ? p.nfb : 0)) * p.cs_stride + row, (m >> half) & 1u ? 4 : 0);
         }
+        cp_async_commit();
+    };
+
+    int64_t tile = blockIdx.x;
+    uint32_t mask[4];
+    if (tile < tiles) {
+        flags(tile, mask);
+        fetch(tile, mask, 0);
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-    if ((tid & 31) == 0) wm[tid >> 5] = am;
-    tile_column_max(dg, cm[0]);
-    tile_cast_rows(p.out, dg, row0, 2 * p.F, fb * 128);
-    {
-        float du[kTileRows][8];
-#pragma unroll
-        for (int i = 0; i < kTileRows; ++i) {
-            float d[8];
-            bf16x8_to_float(da[i], d);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) du[i][x] = __fmul_rn(d[x], silu[i][x]);
+    for (int st = 0; tile < tiles; tile += gridDim.x, st ^= 1) {
+        const bool live = (mask[0] | mask[1] | mask[2] | mask[3]) != 0;
+        if (tile + gridDim.x < tiles) {
+            flags(tile + gridDim.x, mask);
+            fetch(tile + gridDim.x, mask, st ^ 1);
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
         }
-        tile_column_max(du, cm[1]);
-        tile_cast_rows(p.out, du, row0, 2 * p.F, p.F + fb * 128);
-    }
-    __syncthreads();
-    if (tid < 128) tile_column_scale(p.out, cm[0], cr[0], row0, fb * 128, tid);
-    else if (tid < 256) tile_column_scale(p.out, cm[1], cr[1], row0, p.F + fb * 128, tid - 128);
-    am = wm[0];
+        if (!live) continue;  // the same answer in every warp
+        __syncwarp();         // the scales were copied by other lanes
+        const int64_t rb = tile / p.nfb, row0 = rb * 128;
+        const int fb = static_cast<int>(tile % p.nfb);
+        const uint32_t at = stage0 + st * kSwigluBwdStage;
+        auto piece_da = [&](int i, float (&f)[8]) { bf16x8_to_float(ld_shared_16(at + (i * T + tid) * 16), f); };
+        auto piece_c = [&](int i, int up, float (&f)[8]) {
+            uint2 c;
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(c.x), "=r"(c.y) : "r"(at + R * T * 16 + ((2 * i + up) * T + tid) * 8) : "memory");
+            float s;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(at + kSwigluBwdScales + (half * 8 + up * 4 + i) * 4) : "memory");
+            e4m3x8_to_float(c, f);
 #pragma unroll
-    for (int w = 1; w < kTileThreads / 32; ++w) am = fmaxf(am, wm[w]);
-    am = fmaxf(am, 1e-4f);
-    if (tid == 256) p.sb[static_cast<int64_t>(fb) * (p.rows / 128) + rb] = __fdiv_rn(am, 448.f);
-    __syncthreads();
-    tile_cast_columns(p.out, dg, cr[0], row0, 2 * p.F, fb * 128);
-    const float ra = __fdiv_rn(448.f, am);
+            for (int x = 0; x < 8; ++x) f[x] = __fmul_rn(f[x], s);
+        };
+
+        float dg[R][8], silu[R][8];
+        float am = 0.f;
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        float d[8];
-        bf16x8_to_float(da[i], d);
+        for (int i = 0; i < R; ++i) {
+            float u[8], d[8];
+            piece_c(i, 0, silu[i]);
+            piece_c(i, 1, u);
+            piece_da(i, d);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) dg[i][x] = __fmul_rn(d[x], silu[i][x]);
-    }
-    tile_cast_columns(p.out, dg, cr[1], row0, 2 * p.F, p.F + fb * 128);
+            for (int x = 0; x < 8; ++x) {
+                const float g = silu[i][x];
+                const float s = __fdividef(1.f, 1.f + __expf(-g));
+                silu[i][x] = __fmul_rn(g, s);
+                dg[i][x] = d[x] * u[x] * fmaf(silu[i][x], 1.f - s, s);
+                am = fmaxf(am, fabsf(__fmul_rn(silu[i][x], u[x])));
+            }
+        }
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        float u[8];
-        e4m3x8_to_float(cu[i], u);
+        for (int o = 16; o >= 1; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        if (lane == 0) wm[tid >> 5] = am;
+        tile_column_max<T>(dg, cm[0]);
+        tile_cast_rows<T>(p.out, dg, row0, 2 * p.F, fb * 128);
+        {
+            float du[R][8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) u[x] = __fmul_rn(silu[i][x], __fmul_rn(u[x], su[i]));
-        *reinterpret_cast<uint2*>(p.Qa + (row0 + half + 32 * i) * p.F + col) = e4m3x8(u, ra);
+            for (int i = 0; i < R; ++i) {
+                piece_da(i, du[i]);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) du[i][x] = __fmul_rn(du[i][x], silu[i][x]);
+            }
+            tile_column_max<T>(du, cm[1]);
+            tile_cast_rows<T>(p.out, du, row0, 2 * p.F, p.F + fb * 128);
+        }
+        __syncthreads();
+        tile_column_scale<T>(p.out, cm[0], cr[0], row0, fb * 128);
+        tile_column_scale<T>(p.out, cm[1], cr[1], row0, p.F + fb * 128);
+        am = wm[0];
+#pragma unroll
+        for (int w = 1; w < CastTile<T>::kWarps; ++w) am = fmaxf(am, wm[w]);
+        am = fmaxf(am, 1e-4f);
+        const float ra = __fdiv_rn(448.f, am);
+        if (tid == 0) p.sb[static_cast<int64_t>(fb) * (p.rows / 128) + rb] = __fdiv_rn(am, 448.f);
+        __syncthreads();
+        tile_cast_columns<T>(p.out, dg, cr[0], row0, 2 * p.F, fb * 128);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            piece_da(i, dg[i]);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) dg[i][x] = __fmul_rn(dg[i][x], silu[i][x]);
+        }
+        tile_cast_columns<T>(p.out, dg, cr[1], row0, 2 * p.F, p.F + fb * 128);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float u[8];
+            piece_c(i, 1, u);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) u[x] = __fmul_rn(silu[i][x], u[x]);
+            *reinterpret_cast<uint2*>(p.Qa + (row0 + half + 32 * i) * p.F + fb * 128 + hl * 8) = e4m3x8(u, ra);
+        }
     }
 }
 

@@ -29,15 +29,39 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ float half_warp_max(float v) {
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
 __device__ __forceinline__ float half_warp_sum(float v) {
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// Maxima of R values over the 16 lanes of a half-warp, spread: lane hl gets
+// that of a[hl % R].  Each step halves the values that a lane carries, so R
+// values cost R - 1 + log2(16 / R) exchanges instead of 4 R.
+template <int R>
+__device__ __forceinline__ float half_warp_max_spread(float (&a)[R]) {
+    const int hl = threadIdx.x & 15;
+#pragma unroll
+    for (int n = R, bit = 1; n > 1; n >>= 1, bit <<= 1) {
+        const bool hi = hl & bit;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float keep = hi ? a[2 * i + 1] : a[2 * i], send = hi ? a[2 * i] : a[2 * i + 1];
+            a[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+        }
+    }
+#pragma unroll
+    for (int bit = R; bit < 16; bit <<= 1) a[0] = fmaxf(a[0], __shfl_xor_sync(0xffffffffu, a[0], bit));
+    return a[0];
+}
+
+// Scales of R tiles (R <= 8) from their spread maxima, one division a lane:
+// lane i < R gets 448 / amax of tile i, lane R + i amax / 448 of tile i.
+template <int R>
+__device__ __forceinline__ float spread_scale(float amax) {
+    const bool back = threadIdx.x & R;
+    amax = fmaxf(amax, 1e-4f);
+    return __fdiv_rn(back ? amax : 448.f, back ? 448.f : amax);
 }
 
 // Place of row r's scale of K block kb: groups of group_rows rows have blocks
@@ -90,14 +114,21 @@ dispatch_1x128_kernel(const DispatchParams p) {
             row[h] = there && j < p.k ? p.row_of[t * p.k + j] : -1;
             if (row[h] >= p.rows) row[h] = -1;
         }
+        float a[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float f[8];
+            bf16x8_to_float(v[b], f);
+            a[b] = amax8(f);
+        }
+        const float sc = spread_scale<NB>(half_warp_max_spread<NB>(a));
         uint2 q[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             float f[8];
             bf16x8_to_float(v[b], f);
-            const float a = fmaxf(half_warp_max(amax8(f)), 1e-4f);
-            q[b] = e4m3x8(f, __fdiv_rn(448.f, a));
-            const float s = __fdiv_rn(a, 448.f);
+            q[b] = e4m3x8(f, __shfl_sync(0xffffffffu, sc, base + b));
+            const float s = __shfl_sync(0xffffffffu, sc, base + NB + b);
             if (kb0 + b < p.nkb) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -171,13 +202,19 @@ combine_kernel(const CombineParams p) {
 
 // ---------------------------------------------- two casts of one gradient ----
 
-// A CTA of kTileThreads holds a 128 x 128 tile of a gradient in registers:
-// half-warp h (0..31) the rows h + 32 i (i < 4), lane hl of it columns
+// A CTA of T threads holds a 128 x 128 tile of a gradient in registers:
+// half-warp h (of T / 16) the rows h + (T / 16) i, lane hl of it columns
 // 8 hl .. 8 hl + 7.  Both casts that a backward pass needs come from the same
 // values: a scale per row (1x128, the input gradient's operand) and a scale
 // per column (128x1, the weight gradient's, whose K is the rows).
-constexpr int kTileThreads = 512;
-constexpr int kTileRows = 4;  // rows per thread
+template <int T>
+struct CastTile {
+    static constexpr int kRows = 128 * 16 / T;   // rows per thread
+    static constexpr int kStep = T / 16;         // between a thread's rows
+    static constexpr int kWarps = T / 32;
+    static constexpr int kParts = T / 128;       // threads per column in the join
+    static constexpr int kStride = 128 + 32 / kParts;  // of the warps' maxima: the join's reads hit all banks
+};
 
 struct TileOut {
     uint8_t* Qr;   // [rows][N], scales sr[kb * sr_stride + row]
@@ -187,66 +224,91 @@ struct TileOut {
     int64_t sr_stride, sc_stride;
 };
 
-// 1x128: each half-warp has a whole row of the tile.
-__device__ __forceinline__ void tile_cast_rows(const TileOut& o, const float (&v)[kTileRows][8], int64_t row0, int N,
-                                               int col0) {
-    const int half = threadIdx.x >> 4, hl = threadIdx.x & 15;
+// 1x128: each half-warp has whole rows of the tile.
+template <int T>
+__device__ __forceinline__ void tile_cast_rows(const TileOut& o, const float (&v)[CastTile<T>::kRows][8], int64_t row0,
+                                               int N, int col0) {
+    constexpr int R = CastTile<T>::kRows;
+    const int half = threadIdx.x >> 4, hl = threadIdx.x & 15, base = threadIdx.x & 16;
+    float a[R];
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        const int64_t row = row0 + half + 32 * i;
-        const float a = fmaxf(half_warp_max(amax8(v[i])), 1e-4f);
-        *reinterpret_cast<uint2*>(o.Qr + row * N + col0 + hl * 8) = e4m3x8(v[i], __fdiv_rn(448.f, a));
-        if (hl == 0) o.sr[static_cast<int64_t>(col0 / 128) * o.sr_stride + row] = __fdiv_rn(a, 448.f);
-    }
+    for (int i = 0; i < R; ++i) a[i] = amax8(v[i]);
+    const float s = spread_scale<R>(half_warp_max_spread<R>(a));
+    if (hl >= R && hl < 2 * R)
+        o.sr[static_cast<int64_t>(col0 / 128) * o.sr_stride + row0 + half + CastTile<T>::kStep * (hl - R)] = s;
+    uint8_t* q = o.Qr + (row0 + half) * N + col0 + hl * 8;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        *reinterpret_cast<uint2*>(q + static_cast<int64_t>(CastTile<T>::kStep * i) * N) =
+            e4m3x8(v[i], __shfl_sync(0xffffffffu, s, base + i));
 }
 
-// 128x1, first half: the warps' column maxima into cm[warp][128].
-__device__ __forceinline__ void tile_column_max(const float (&v)[kTileRows][8], float* cm) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// 128x1, first part: the warps' column maxima into cm[warp][kStride].  The two
+// half-warps exchange four columns each.
+template <int T>
+__device__ __forceinline__ void tile_column_max(const float (&v)[CastTile<T>::kRows][8], float* cm) {
+    const int warp = threadIdx.x >> 5, hl = threadIdx.x & 15;
+    const bool hi = threadIdx.x & 16;
     float m[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
         m[x] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kTileRows; ++i) m[x] = fmaxf(m[x], fabsf(v[i][x]));
-        m[x] = fmaxf(m[x], __shfl_xor_sync(0xffffffffu, m[x], 16));
+        for (int i = 0; i < CastTile<T>::kRows; ++i) m[x] = fmaxf(m[x], fabsf(v[i][x]));
     }
-    if (lane < 16) {
-        float4* to = reinterpret_cast<float4*>(cm + warp * 128 + lane * 8);
-        to[0] = make_float4(m[0], m[1], m[2], m[3]);
-        to[1] = make_float4(m[4], m[5], m[6], m[7]);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const float keep = hi ? m[4 + x] : m[x], send = hi ? m[x] : m[4 + x];
+        m[x] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 16));
     }
+    *reinterpret_cast<float4*>(cm + warp * CastTile<T>::kStride + hl * 8 + (hi ? 4 : 0)) = make_float4(m[0], m[1], m[2], m[3]);
 }
 
-// Second half, after a barrier: threads 0..127 join the warps' maxima, write
-// the scales and leave 448 / amax in cr[128].
-__device__ __forceinline__ void tile_column_scale(const TileOut& o, const float* cm, float* cr, int64_t row0, int col0,
-                                                  int tid) {
-    float a = cm[tid];
+// Second part, after a barrier: kParts threads to a column join the warps'
+// maxima; one of them leaves 448 / amax in cr, another writes the scale.
+template <int T>
+__device__ __forceinline__ void tile_column_scale(const TileOut& o, const float* cm, float* cr, int64_t row0, int col0) {
+    const int c = threadIdx.x / CastTile<T>::kParts, part = threadIdx.x % CastTile<T>::kParts;
+    float a = 1e-4f;
 #pragma unroll
-    for (int w = 1; w < kTileThreads / 32; ++w) a = fmaxf(a, cm[w * 128 + tid]);
-    a = fmaxf(a, 1e-4f);
-    cr[tid] = __fdiv_rn(448.f, a);
-    o.sc[(row0 / 128) * o.sc_stride + col0 + tid] = __fdiv_rn(a, 448.f);
+    for (int w = part; w < CastTile<T>::kWarps; w += CastTile<T>::kParts) a = fmaxf(a, cm[w * CastTile<T>::kStride + c]);
+#pragma unroll
+    for (int b = 1; b < CastTile<T>::kParts; b <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, b));
+    const float s = __fdiv_rn(part ? a : 448.f, part ? 448.f : a);
+    if (part == 0) cr[c] = s;
+    if (part == 1) o.sc[(row0 / 128) * o.sc_stride + col0 + c] = s;
 }
 
 // Third part, after another barrier.
-__device__ __forceinline__ void tile_cast_columns(const TileOut& o, const float (&v)[kTileRows][8], const float* cr,
-                                                  int64_t row0, int N, int col0) {
+template <int T>
+__device__ __forceinline__ void tile_cast_columns(const TileOut& o, const float (&v)[CastTile<T>::kRows][8],
+                                                  const float* cr, int64_t row0, int N, int col0) {
     const int half = threadIdx.x >> 4, hl = threadIdx.x & 15;
     float r[8];
     *reinterpret_cast<float4*>(r) = *reinterpret_cast<const float4*>(cr + hl * 8);
     *reinterpret_cast<float4*>(r + 4) = *reinterpret_cast<const float4*>(cr + hl * 8 + 4);
+    uint8_t* to = o.Qc + (row0 + half) * N + col0 + hl * 8;
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
+    for (int i = 0; i < CastTile<T>::kRows; ++i) {
         uint32_t q[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
             q[x] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v[i][2 * x], r[2 * x]), __fmul_rn(v[i][2 * x + 1], r[2 * x + 1])),
                                             __NV_SATFINITE, __NV_E4M3);
-        *reinterpret_cast<uint2*>(o.Qc + (row0 + half + 32 * i) * N + col0 + hl * 8) =
+        *reinterpret_cast<uint2*>(to + static_cast<int64_t>(CastTile<T>::kStep * i) * N) =
             make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
     }
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
 // ----------------------------------------------------- combine, backward ----
@@ -264,13 +326,23 @@ struct CombineBwdParams {
     int64_t rows;
 };
 
+constexpr int kCombineBwdThreads = 256;
+constexpr int kCombineBwdStage = 2 * 128 * 128 * 2;  // bytes: a tile of dout and of Y
+
 // dY[row] = w dout[t], cast both ways, and dw = <dout[t], Y[row]>.  A cluster
 // of CTAs takes a block of 128 rows, each CTA a run of its 128-column tiles;
 // the row sums of dw are joined through distributed shared memory in CTA
 // order.  Rows without a slot count as zeros; a block without any is left.
-__global__ void __launch_bounds__(kTileThreads)
+//
+// Each thread copies the 16-byte pieces that it will use itself to shared
+// memory (cp.async), takes them into registers when they have landed and at
+// once asks for the next tile's, so HBM works during the casts and no barrier
+// guards the buffer.
+__global__ void __launch_bounds__(kCombineBwdThreads, 2)
 combine_bwd_kernel(const CombineBwdParams p) {
-    __shared__ float cm[kTileThreads / 32 * 128];
+    constexpr int T = kCombineBwdThreads, R = CastTile<T>::kRows;
+    extern __shared__ __align__(16) uint8_t stage_smem[];
+    __shared__ __align__(16) float cm[CastTile<T>::kWarps * CastTile<T>::kStride];
     __shared__ __align__(16) float cr[128];
     __shared__ float part[128];
     griddep_wait();
@@ -280,61 +352,65 @@ combine_bwd_kernel(const CombineBwdParams p) {
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / nctas) * 128;
 
     // Slots that have no row have no gradient.
-    for (int64_t s = static_cast<int64_t>(blockIdx.x) * kTileThreads + tid; s < p.S;
-         s += static_cast<int64_t>(gridDim.x) * kTileThreads) {
+    for (int64_t s = static_cast<int64_t>(blockIdx.x) * T + tid; s < p.S; s += static_cast<int64_t>(gridDim.x) * T) {
         const int r = p.row_of[s];
         if (r < 0 || r >= p.rows) p.dw[s] = 0.f;
     }
 
-    int64_t slot[kTileRows];
-    float w[kTileRows], dot[kTileRows];
+    int token[R];  // -1: no slot
+    float w[R], dot[R];
     bool any = false;
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-        const int s = p.slot_of[row0 + half + 32 * i];
-        slot[i] = s >= 0 && s < p.S ? s : -1;
-        w[i] = slot[i] >= 0 ? p.w[slot[i]] : 0.f;
+    for (int i = 0; i < R; ++i) {
+        const int s = p.slot_of[row0 + half + CastTile<T>::kStep * i];
+        const bool ok = s >= 0 && s < p.S;
+        token[i] = ok ? s / p.k : -1;
+        w[i] = ok ? p.w[s] : 0.f;
         dot[i] = 0.f;
-        any |= slot[i] >= 0;
+        any |= ok;
     }
     if (!__syncthreads_or(any)) return;  // the same answer in every CTA of the cluster
 
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / nctas);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / nctas);
-    for (int kb = kb0; kb < kb1; ++kb) {
-        const int col = kb * 128 + hl * 8;
-        uint4 g[kTileRows], y[kTileRows];
+    const uint32_t stage = smem_u32(stage_smem) + tid * 16;
+    auto fetch = [&](int kb) {
+        const int64_t col = kb * 128 + hl * 8;
 #pragma unroll
-        for (int i = 0; i < kTileRows; ++i) {
-            g[i] = y[i] = make_uint4(0, 0, 0, 0);
-            if (slot[i] >= 0) {
-                g[i] = ld_once_16(p.dout + (slot[i] / p.k) * p.N + col);
-                y[i] = ld_once_16(p.Y + (row0 + half + 32 * i) * p.N + col);
-            }
+        for (int i = 0; i < R; ++i) {
+            const uint32_t bytes = token[i] >= 0 ? 16 : 0;
+            cp_async_16(stage + 2 * i * T * 16, p.dout + static_cast<int64_t>(max(token[i], 0)) * p.N + col, bytes);
+            cp_async_16(stage + (2 * i + 1) * T * 16, p.Y + (row0 + half + CastTile<T>::kStep * i) * p.N + col, bytes);
         }
-        float v[kTileRows][8];
+        cp_async_commit();
+    };
+    fetch(kb0);
+    for (int kb = kb0; kb < kb1; ++kb) {
+        cp_async_wait<0>();
+        float v[R][8];
 #pragma unroll
-        for (int i = 0; i < kTileRows; ++i) {
+        for (int i = 0; i < R; ++i) {
             float yf[8];
-            bf16x8_to_float(g[i], v[i]);
-            bf16x8_to_float(y[i], yf);
+            bf16x8_to_float(ld_shared_16(stage + 2 * i * T * 16), v[i]);
+            bf16x8_to_float(ld_shared_16(stage + (2 * i + 1) * T * 16), yf);
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 dot[i] = fmaf(v[i][x], yf[x], dot[i]);
-                v[i][x] = slot[i] >= 0 ? __fmul_rn(v[i][x], w[i]) : 0.f;
+                v[i][x] = token[i] >= 0 ? __fmul_rn(v[i][x], w[i]) : 0.f;
             }
         }
-        tile_column_max(v, cm);
-        tile_cast_rows(p.out, v, row0, p.N, kb * 128);
+        if (kb + 1 < kb1) fetch(kb + 1);
+        tile_column_max<T>(v, cm);
+        tile_cast_rows<T>(p.out, v, row0, p.N, kb * 128);
         __syncthreads();
-        if (tid < 128) tile_column_scale(p.out, cm, cr, row0, kb * 128, tid);
+        tile_column_scale<T>(p.out, cm, cr, row0, kb * 128);
         __syncthreads();
-        tile_cast_columns(p.out, v, cr, row0, p.N, kb * 128);
+        tile_cast_columns<T>(p.out, v, cr, row0, p.N, kb * 128);
     }
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
+    for (int i = 0; i < R; ++i) {
         const float d = half_warp_sum(dot[i]);
-        if (hl == 0) part[half + 32 * i] = d;
+        if (hl == 0) part[half + CastTile<T>::kStep * i] = d;
     }
     __syncwarp();
     cluster_sync();
