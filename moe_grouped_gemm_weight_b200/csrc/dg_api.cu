@@ -911,6 +911,26 @@ dg_status check_row_blocks(int64_t rows, int N, const char* name) {
 // and stores of whole lanes.
 bool full_lanes(int E, int per) { return E == 32 * per && (per & (per - 1)) == 0; }
 
+// CTAs (a cluster) that share a block of 128 rows in combine's gradient.  A
+// wave of `slots` CTAs costs its tiles and about two more to start and join;
+// about half of the blocks that the layout keeps for uneven groups hold a
+// slot.  Measured for 287 of 319 blocks of 56 tiles on 296 slots: 212, 218,
+// 243, 260 us for 1, 2, 4, 8 CTAs a block (wide clusters also wait for a whole
+// cluster's room, and their later waves read dout again).
+int combine_bwd_split(int64_t slots_held, int64_t blocks, int nkb, int slots) {
+    const int64_t full = cdiv64(slots_held, 128), live = full < blocks ? full + (blocks - full) / 2 : blocks;
+    int best = 1;
+    int64_t best_cost = 0;
+    for (int c = 1; c <= 8 && c <= nkb; c *= 2) {
+        const int64_t cost = cdiv64(live * c, slots) * (cdiv(nkb, c) + 2);
+        if (best_cost == 0 || cost < best_cost) {
+            best = c;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
 // The routing kernels' instance: lanes hold ceil(E / 32) experts, rounded up
 // to a power of two.
 template <typename L>
@@ -924,15 +944,21 @@ dg_status launch_route(const dg::RouteParams& p, int64_t grid, int smem, void* s
     return launch_plain(dg::route_topk_kernel<32, L>, p, grid, threads, smem, 1, st);
 }
 
+template <typename L, int EPL>
+dg_status launch_route_bwd_one(const dg::RouteBwdParams& p, int64_t grid, void* st) {
+    return launch_plain(dg::route_topk_bwd_kernel<EPL, L>, p, grid, dg::kRouteWarps * 32,
+                        dg::kRouteWarps * 32 * EPL * static_cast<int>(sizeof(float)), 1, st);
+}
+
 template <typename L>
 dg_status launch_route_bwd(const dg::RouteBwdParams& p, int64_t grid, void* st) {
-    const int threads = dg::kRouteWarps * 32, per = cdiv(p.E, 32);
-    if (per <= 1) return launch_plain(dg::route_topk_bwd_kernel<1, L>, p, grid, threads, 0, 1, st);
-    if (per <= 2) return launch_plain(dg::route_topk_bwd_kernel<2, L>, p, grid, threads, 0, 1, st);
-    if (per <= 4) return launch_plain(dg::route_topk_bwd_kernel<4, L>, p, grid, threads, 0, 1, st);
-    if (per <= 8) return launch_plain(dg::route_topk_bwd_kernel<8, L>, p, grid, threads, 0, 1, st);
-    if (per <= 16) return launch_plain(dg::route_topk_bwd_kernel<16, L>, p, grid, threads, 0, 1, st);
-    return launch_plain(dg::route_topk_bwd_kernel<32, L>, p, grid, threads, 0, 1, st);
+    const int per = p.per;
+    if (per <= 1) return launch_route_bwd_one<L, 1>(p, grid, st);
+    if (per <= 2) return launch_route_bwd_one<L, 2>(p, grid, st);
+    if (per <= 4) return launch_route_bwd_one<L, 4>(p, grid, st);
+    if (per <= 8) return launch_route_bwd_one<L, 8>(p, grid, st);
+    if (per <= 16) return launch_route_bwd_one<L, 16>(p, grid, st);
+    return launch_route_bwd_one<L, 32>(p, grid, st);
 }
 
 }  // namespace
@@ -1345,9 +1371,9 @@ dg_status dg_route_layout(int32_t* row_of, int32_t* m_indices, int32_t* slot_of,
     if (!aligned(row_of, 4) || !aligned(m_indices, 4) || !aligned(slot_of, 4) || !aligned(group_offsets, 4) ||
         !aligned(counts, 4) || !aligned(topk_idx, 4))
         return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements");
-    // One CTA per 4096 slots, up to a cluster of 8.
+    // One CTA per 1024 slots, up to a cluster of 8.
     int ctas = 1;
-    while (ctas < dg::kLayoutMaxCluster && S > static_cast<int64_t>(ctas) * 4096) ctas *= 2;
+    while (ctas < dg::kLayoutMaxCluster && S > static_cast<int64_t>(ctas) * 1024) ctas *= 2;
     const int64_t warps = static_cast<int64_t>(ctas) * dg::kLayoutWarps;
     dg::LayoutParams p{topk_idx, row_of, m_indices, slot_of, group_offsets, counts, S, cdiv64(cdiv64(S, warps), 32) * 32,
                        E, rows, max_rows};
@@ -1368,13 +1394,15 @@ dg_status dg_dispatch_fp8_1x128(uint8_t* Q, float* sa, int sa_stride, const uint
         return fail(DG_ERR_MISALIGNED, "X and Q must be 16-byte aligned, sa and row_of 4-byte aligned");
     const int sms = effective_sms();
     if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
-    dg::DispatchParams p{Q, sa, X, row_of, T, k, K, K / dg::kBK, sa_stride, group_rows, rows};
+    dg::DispatchParams p{Q, sa, X, row_of, T, k, K, K / dg::kBK, sa_stride, group_rows, rows, 0};
     const int64_t groups = cdiv64(T, dg::kCastRowsPerCta), cap = static_cast<int64_t>(sms) * 8;
     // Four K blocks at a time while that still gives every SM a CTA, else one.
-    const int64_t wide = groups * cdiv(p.nkb, 4);
-    if (wide >= sms) return launch_plain(dg::dispatch_1x128_kernel<4>, p, wide < cap ? wide : cap, dg::kCastThreads, 0, 1, stream);
-    const int64_t one = groups * p.nkb;
-    return launch_plain(dg::dispatch_1x128_kernel<1>, p, one < cap ? one : cap, dg::kCastThreads, 0, 1, stream);
+    const bool wide = groups * cdiv(p.nkb, 4) >= sms;
+    const int64_t items = groups * (wide ? cdiv(p.nkb, 4) : p.nkb), grid = items < cap ? items : cap;
+    if (items > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED, "problem too large");
+    p.items = static_cast<uint32_t>(items);
+    return wide ? launch_plain(dg::dispatch_1x128_kernel<4>, p, grid, dg::kCastThreads, 0, 1, stream)
+                : launch_plain(dg::dispatch_1x128_kernel<1>, p, grid, dg::kCastThreads, 0, 1, stream);
 }
 
 dg_status dg_combine(uint16_t* out, const uint16_t* Y, const int32_t* row_of, const float* w, int T, int k, int N,
@@ -1409,8 +1437,9 @@ dg_status dg_combine_bwd(float* dw, uint8_t* Qr, float* sr, int sr_stride, uint8
         return fail(DG_ERR_MISALIGNED, "Qr, Qc, dout and Y must be 16-byte aligned, the others 4-byte aligned");
     dg::CombineBwdParams p{{Qr, sr, Qc, sc, sr_stride, sc_stride}, dw, dout, Y, row_of, slot_of, w,
                            static_cast<int64_t>(T) * k, k, N, N / 128, rows};
-    int ctas = 1;
-    while (ctas < 8 && ctas * 2 <= p.nkb) ctas *= 2;
+    const int sms = effective_sms();
+    if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
+    const int ctas = combine_bwd_split(static_cast<int64_t>(T) * k, rows / 128, p.nkb, 2 * sms);
     return launch_plain(dg::combine_bwd_kernel, p, static_cast<int64_t>(rows / 128) * ctas, dg::kCombineBwdThreads,
                         dg::kCombineBwdStage, ctas, stream);
 }
@@ -1429,10 +1458,12 @@ dg_status dg_swiglu_fp8(uint8_t* Q, float* sa, int sa_stride, uint8_t* C, float*
         return fail(DG_ERR_MISALIGNED, "Q, C and H must be 16-byte aligned, the others 4-byte aligned");
     const int sms = effective_sms();
     if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
-    dg::SwigluParams p{Q, sa, C, cs, H, m_indices, sa_stride, cs_stride, group_rows, F, F / dg::kBK, rows};
-    const int64_t groups = cdiv64(rows, dg::kCastRowsPerCta), cap = static_cast<int64_t>(sms) * 8;
-    const int64_t items = groups * cdiv(p.nfb, 2);
-    return launch_plain(dg::swiglu_fp8_kernel<2>, p, items < cap ? items : cap, dg::kCastThreads, 0, 1, stream);
+    dg::SwigluParams p{Q, sa, C, cs, H, m_indices, sa_stride, cs_stride, group_rows, F, F / dg::kBK, rows, 0};
+    const int64_t items = cdiv64(rows, dg::kCastRowsPerCta) * cdiv(p.nfb, 2);
+    const int64_t cap = static_cast<int64_t>(sms) * dg::kSwigluCtas;
+    if (items > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED, "problem too large");
+    p.items = static_cast<uint32_t>(items);
+    return launch_plain(dg::swiglu_fp8_kernel, p, items < cap ? items : cap, dg::kCastThreads, 0, 1, stream);
 }
 
 dg_status dg_swiglu_fp8_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, float* sc, int sc_stride, uint8_t* Qa,
@@ -1449,10 +1480,12 @@ dg_status dg_swiglu_fp8_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, 
         !aligned(sc, 4) || !aligned(sb, 4) || !aligned(cs, 4) || !aligned(m_indices, 4))
         return fail(DG_ERR_MISALIGNED, "Qr, Qc, Qa, dA and C must be 16-byte aligned, the others 4-byte aligned");
     dg::SwigluBwdParams p{{Qr, sr, Qc, sc, sr_stride, sc_stride}, Qa, sb, dA, C, cs, m_indices, cs_stride, F,
-                          F / dg::kBK, rows};
+                          F / dg::kBK, rows, 0};
     const int sms = effective_sms();
     if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
     const int64_t tiles = static_cast<int64_t>(rows / 128) * p.nfb;
+    if (tiles > 0x7FFFFFFF - sms) return fail(DG_ERR_UNSUPPORTED, "problem too large");
+    p.tiles = static_cast<uint32_t>(tiles);
     return launch_plain(dg::swiglu_fp8_bwd_kernel, p, tiles < sms ? tiles : sms, dg::kSwigluBwdThreads,
                         2 * dg::kSwigluBwdStage, 1, stream);
 }

@@ -16,22 +16,28 @@
 
 namespace dg {
 
-// 8 e4m3 codes -> floats (exact).
-__device__ __forceinline__ void e4m3x8_to_float(const uint2& c, float (&f)[8]) {
-    const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-        const float2 x = __half22float2(__half2(h));
-        f[2 * i] = x.x;
-        f[2 * i + 1] = x.y;
-    }
+// Eight e4m3 codes -> floats (exact).
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t two) {
+    return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3));
 }
+__device__ __forceinline__ void e4m3x8_to_f8(const uint2& c, F8& f) {
+    f[0] = __half22float2(e4m3x2_to_half2(c.x));
+    f[1] = __half22float2(e4m3x2_to_half2(c.x >> 16));
+    f[2] = __half22float2(e4m3x2_to_half2(c.y));
+    f[3] = __half22float2(e4m3x2_to_half2(c.y >> 16));
+}
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 
-__device__ __forceinline__ uint2 ld_once_8(const void* p) {
-    uint2 v;
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
-    return v;
+// s = 1 / (1 + exp(-g)) of a pair, from the special-function unit: relative
+// error 2^-21 and |g| 2^-24.
+__device__ __forceinline__ float2 sigmoid2(float2 g) {
+    float2 e = __fmul2_rn(g, pair(-1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    e = __fadd2_rn(e, pair(1.f));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    return e;
 }
 
 // -------------------------------------------------------------- forward ----
@@ -45,55 +51,72 @@ struct SwigluParams {
     const int32_t* m_indices;  // [rows] or null; negative: the row is left
     int sa_stride, cs_stride, group_rows;
     int F, nfb;                // nfb = F / 128
-    int64_t rows;
+    int rows;
+    uint32_t items;            // row groups times pairs of blocks
 };
 
-// Half-warp h of a CTA takes a row, NB pairs of gate and up blocks at a time.
-template <int NB>
-__global__ void __launch_bounds__(kCastThreads)
+constexpr int kSwigluCtas = 4;  // resident per SM
+
+// Half-warp h of a CTA takes a row, two pairs of gate and up blocks at a time:
+// six tiles whose scales are found together (places 3 and 7 of 8 are spare).
+__global__ void __launch_bounds__(kCastThreads, kSwigluCtas)
 swiglu_fp8_kernel(const SwigluParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int half = threadIdx.x >> 4, hl = threadIdx.x & 15;
-    const int64_t row_groups = (p.rows + kCastRowsPerCta - 1) / kCastRowsPerCta;
-    const int fb_groups = (p.nfb + NB - 1) / NB;
-    const int64_t items = row_groups * fb_groups;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int64_t row = (it / fb_groups) * kCastRowsPerCta + half;
-        const int fb0 = static_cast<int>(it % fb_groups) * NB;
+    const int half = threadIdx.x >> 4, hl = threadIdx.x & 15, base = threadIdx.x & 16;
+    const uint32_t fb_groups = (p.nfb + 1) / 2;
+    for (uint32_t it = blockIdx.x; it < p.items; it += gridDim.x) {
+        const uint32_t rg = it / fb_groups;
+        const int row = static_cast<int>(rg) * kCastRowsPerCta + half;
+        const int fb0 = static_cast<int>(it - rg * fb_groups) * 2;
         const bool there = row < p.rows && (p.m_indices == nullptr || p.m_indices[row] >= 0);
-        const uint16_t* hr = p.H + row * 2 * p.F + fb0 * 128 + hl * 8;
-        uint4 vg[NB], vu[NB];
+        if (!__any_sync(0xffffffffu, there)) continue;
+        const uint16_t* hr = p.H + static_cast<int64_t>(row) * 2 * p.F + fb0 * 128 + hl * 8;
+        uint4 vg[2], vu[2];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
+        for (int b = 0; b < 2; ++b) {
             const bool ok = there && fb0 + b < p.nfb;
             vg[b] = ok ? ld_once_16(hr + b * 128) : make_uint4(0, 0, 0, 0);
             vu[b] = ok ? ld_once_16(hr + p.F + b * 128) : make_uint4(0, 0, 0, 0);
         }
+        F8 a[2], g[2], u[2];
+        float m[8];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float g[8], u[8], a[8];
-            bf16x8_to_float(vg[b], g);
-            bf16x8_to_float(vu[b], u);
+        for (int b = 0; b < 2; ++b) {
+            bf16x8_to_f8(vg[b], g[b]);
+            bf16x8_to_f8(vu[b], u[b]);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) a[x] = __fdividef(g[x], 1.f + __expf(-g[x])) * u[x];
-            // three casts: the scales of a, gate and up (the fourth place is spare)
-            float m[4] = {amax8(a), amax8(g), amax8(u), 0.f};
-            const float sc = spread_scale<4>(half_warp_max_spread<4>(m));
-            const int base = threadIdx.x & 16;
-            const float ra = __shfl_sync(0xffffffffu, sc, base), rg = __shfl_sync(0xffffffffu, sc, base + 1);
-            const float ru = __shfl_sync(0xffffffffu, sc, base + 2);
-            if (!there || fb0 + b >= p.nfb) continue;
-            const int fb = fb0 + b;
-            *reinterpret_cast<uint2*>(p.Q + row * p.F + fb * 128 + hl * 8) = e4m3x8(a, ra);
-            if (hl == 4) p.sa[scale_at(row, fb, p.nfb, p.sa_stride, p.group_rows)] = sc;
-            if (p.C != nullptr) {
-                uint8_t* cr = p.C + row * 2 * p.F + fb * 128 + hl * 8;
-                *reinterpret_cast<uint2*>(cr) = e4m3x8(g, rg);
-                *reinterpret_cast<uint2*>(cr + p.F) = e4m3x8(u, ru);
-                if (hl == 5 || hl == 6)
-                    p.cs[scale_at(row, fb + (hl == 6 ? p.nfb : 0), 2 * p.nfb, p.cs_stride, p.group_rows)] = sc;
+            for (int x = 0; x < 4; ++x) a[b][x] = __fmul2_rn(__fmul2_rn(g[b][x], sigmoid2(g[b][x])), u[b][x]);
+            m[4 * b] = amax8(a[b]);
+            m[4 * b + 1] = amax8(g[b]);
+            m[4 * b + 2] = amax8(u[b]);
+            m[4 * b + 3] = 0.f;
+        }
+        const float sc = spread_scale<8>(half_warp_max_spread<8>(m));
+        // lane 8 + 4 b + i writes the scale of block b's a, gate or up
+        const int b = (hl >> 2) & 1, i = hl & 3;
+        if (hl >= 8 && there && fb0 + b < p.nfb && i < 3) {
+            if (i == 0)
+                p.sa[scale_base(row, p.nfb, p.sa_stride, p.group_rows) + static_cast<int64_t>(fb0 + b) * p.sa_stride] = sc;
+            else if (p.C != nullptr)
+                p.cs[scale_base(row, 2 * p.nfb, p.cs_stride, p.group_rows) +
+                     static_cast<int64_t>(fb0 + b + (i == 2 ? p.nfb : 0)) * p.cs_stride] = sc;
+        }
+        __syncwarp();
+        uint8_t* qr = p.Q + static_cast<int64_t>(row) * p.F + fb0 * 128 + hl * 8;
+        uint8_t* cr = p.C + static_cast<int64_t>(row) * 2 * p.F + fb0 * 128 + hl * 8;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const float ra = __shfl_sync(0xffffffffu, sc, base + 4 * b), rg = __shfl_sync(0xffffffffu, sc, base + 4 * b + 1);
+            const float ru = __shfl_sync(0xffffffffu, sc, base + 4 * b + 2);
+            if (there && fb0 + b < p.nfb) {
+                *reinterpret_cast<uint2*>(qr + b * 128) = e4m3x8(a[b], ra);
+                if (p.C != nullptr) {
+                    *reinterpret_cast<uint2*>(cr + b * 128) = e4m3x8(g[b], rg);
+                    *reinterpret_cast<uint2*>(cr + p.F + b * 128) = e4m3x8(u[b], ru);
+                }
             }
+            __syncwarp();
         }
     }
 }
@@ -110,7 +133,8 @@ struct SwigluBwdParams {
     const int32_t* m_indices;  // [rows] or null
     int64_t cs_stride;
     int F, nfb;
-    int64_t rows;
+    int rows;
+    uint32_t tiles;            // row blocks times F blocks
 };
 
 constexpr int kSwigluBwdThreads = 512;
@@ -128,56 +152,73 @@ constexpr int kSwigluBwdStage = kSwigluBwdScales + 128 * 2 * 4;
 __global__ void __launch_bounds__(kSwigluBwdThreads)
 swiglu_fp8_bwd_kernel(const SwigluBwdParams p) {
     constexpr int T = kSwigluBwdThreads, R = CastTile<T>::kRows;
-    static_assert(R == 4 && CastTile<T>::kStep == 32, "a mask of row flags per i");
+    static_assert(R == 2 || R == 4, "row flags below");
     extern __shared__ __align__(16) uint8_t stage_smem[];
     __shared__ __align__(16) float cm[2][CastTile<T>::kWarps * CastTile<T>::kStride];
     __shared__ __align__(16) float cr[2][128];
     __shared__ float wm[CastTile<T>::kWarps];
+    __shared__ uint64_t bars[2];
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) {
+        mbar_init(&bars[0], CastTile<T>::kWarps);
+        mbar_init(&bars[1], CastTile<T>::kWarps);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    SplitBarrier maxima{&bars[0], &abort_flag}, joined{&bars[1], &abort_flag};
+    __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, half = tid >> 4, hl = tid & 15;
-    const int64_t tiles = p.rows / 128 * p.nfb;
     const uint32_t stage0 = smem_u32(stage_smem);
 
-    // Row flags of a tile: bit r of mask i is row r + 32 i.
-    auto flags = [&](int64_t tile, uint32_t (&mask)[4]) {
-        const int64_t row0 = tile / p.nfb * 128;
+    // Row flags of a tile, bit half & 31 of mask i: this thread's row i; `live`: any row.
+    auto flags = [&](uint32_t tile, uint32_t (&mask)[R], bool& live) {
+        const int64_t row0 = static_cast<int64_t>(tile / p.nfb) * 128;
+        uint32_t all[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            mask[i] = __ballot_sync(0xffffffffu, p.m_indices == nullptr || p.m_indices[row0 + lane + 32 * i] >= 0);
+            all[i] = __ballot_sync(0xffffffffu, p.m_indices == nullptr || p.m_indices[row0 + lane + 32 * i] >= 0);
+        live = (all[0] | all[1] | all[2] | all[3]) != 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) mask[i] = R == 4 ? all[i] : half < 32 ? all[2 * i] : all[2 * i + 1];
     };
-    auto fetch = [&](int64_t tile, const uint32_t (&mask)[4], int st) {
-        const int64_t row0 = tile / p.nfb * 128;
+    auto fetch = [&](uint32_t tile, const uint32_t (&mask)[R], int st) {
+        const int64_t row0 = static_cast<int64_t>(tile / p.nfb) * 128;
         const int fb = static_cast<int>(tile % p.nfb);
         const int64_t col = fb * 128 + hl * 8;
         const uint32_t at = stage0 + st * kSwigluBwdStage;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int64_t row = row0 + half + 32 * i;
-            const bool ok = (mask[i] >> half) & 1u;
+            const int64_t row = row0 + half + CastTile<T>::kStep * i;
+            const bool ok = (mask[i] >> (half & 31)) & 1u;
             cp_async_16(at + (i * T + tid) * 16, p.dA + row * p.F + col, ok ? 16 : 0);
             cp_async_8(at + R * T * 16 + (2 * i * T + tid) * 8, p.C + row * 2 * p.F + col, ok ? 8 : 0);
             cp_async_8(at + R * T * 16 + ((2 * i + 1) * T + tid) * 8, p.C + row * 2 * p.F + p.F + col, ok ? 8 : 0);
         }
-        if (hl < 8) {  // lane i: gate scale of row i, lane 4 + i: up scale
-            const int64_t row = row0 + half + 32 * (hl & 3);
-            const uint32_t m = (hl & 2) ? (hl & 1 ? mask[3] : mask[2]) : (hl & 1 ? mask[1] : mask[0]);
-            cp_async_4(at + kSwigluBwdScales + (half * 8 + hl) * 4,
-                       p.cs + static_cast<int64_t>(fb + (hl & 4 ? p.nfb : 0)) * p.cs_stride + row, (m >> half) & 1u ? 4 : 0);
+        if (hl < 2 * R) {  // lane i: gate scale of row i, lane R + i: up scale
+            const int i = hl & (R - 1);
+            uint32_t m = mask[0];
+#pragma unroll
+            for (int x = 1; x < R; ++x) m = i == x ? mask[x] : m;
+            cp_async_4(at + kSwigluBwdScales + (half * 2 * R + hl) * 4,
+                       p.cs + static_cast<int64_t>(fb + (hl >= R ? p.nfb : 0)) * p.cs_stride + row0 + half + CastTile<T>::kStep * i,
+                       (m >> (half & 31)) & 1u ? 4 : 0);
         }
         cp_async_commit();
     };
 
-    int64_t tile = blockIdx.x;
-    uint32_t mask[4];
-    if (tile < tiles) {
-        flags(tile, mask);
+    uint32_t tile = blockIdx.x;
+    uint32_t mask[R];
+    bool next_live = false;
+    if (tile < p.tiles) {
+        flags(tile, mask, next_live);
         fetch(tile, mask, 0);
     }
-    for (int st = 0; tile < tiles; tile += gridDim.x, st ^= 1) {
-        const bool live = (mask[0] | mask[1] | mask[2] | mask[3]) != 0;
-        if (tile + gridDim.x < tiles) {
-            flags(tile + gridDim.x, mask);
+    for (int st = 0; tile < p.tiles; tile += gridDim.x, st ^= 1) {
+        const bool live = next_live;
+        if (tile + gridDim.x < p.tiles) {
+            flags(tile + gridDim.x, mask, next_live);
             fetch(tile + gridDim.x, mask, st ^ 1);
             cp_async_wait<1>();
         } else {
@@ -188,77 +229,59 @@ swiglu_fp8_bwd_kernel(const SwigluBwdParams p) {
         const int64_t rb = tile / p.nfb, row0 = rb * 128;
         const int fb = static_cast<int>(tile % p.nfb);
         const uint32_t at = stage0 + st * kSwigluBwdStage;
-        auto piece_da = [&](int i, float (&f)[8]) { bf16x8_to_float(ld_shared_16(at + (i * T + tid) * 16), f); };
-        auto piece_c = [&](int i, int up, float (&f)[8]) {
-            uint2 c;
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                         : "=r"(c.x), "=r"(c.y) : "r"(at + R * T * 16 + ((2 * i + up) * T + tid) * 8) : "memory");
-            float s;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(at + kSwigluBwdScales + (half * 8 + up * 4 + i) * 4) : "memory");
-            e4m3x8_to_float(c, f);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) f[x] = __fmul_rn(f[x], s);
-        };
-
-        float dg[R][8], silu[R][8];
+        F8 dg[R], du[R], act[R];
         float am = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            float u[8], d[8];
-            piece_c(i, 0, silu[i]);
-            piece_c(i, 1, u);
-            piece_da(i, d);
+            uint2 cg, cu;
+            float sg, su;
+            F8 g, u, d;
+            const uint32_t codes = at + R * T * 16 + (2 * i * T + tid) * 8, scale = at + kSwigluBwdScales + (half * 2 * R + i) * 4;
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(cg.x), "=r"(cg.y) : "r"(codes) : "memory");
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(cu.x), "=r"(cu.y) : "r"(codes + T * 8) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sg) : "r"(scale) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(su) : "r"(scale + R * 4) : "memory");
+            bf16x8_to_f8(ld_shared_16(at + (i * T + tid) * 16), d);
+            e4m3x8_to_f8(cg, g);
+            e4m3x8_to_f8(cu, u);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const float g = silu[i][x];
-                const float s = __fdividef(1.f, 1.f + __expf(-g));
-                silu[i][x] = __fmul_rn(g, s);
-                dg[i][x] = d[x] * u[x] * fmaf(silu[i][x], 1.f - s, s);
-                am = fmaxf(am, fabsf(__fmul_rn(silu[i][x], u[x])));
+            for (int x = 0; x < 4; ++x) {
+                g[x] = __fmul2_rn(g[x], pair(sg));
+                u[x] = __fmul2_rn(u[x], pair(su));
+                const float2 s = sigmoid2(g[x]);
+                const float2 silu = __fmul2_rn(g[x], s);
+                const float2 t = __ffma2_rn(silu, __ffma2_rn(s, pair(-1.f), pair(1.f)), s);
+                dg[i][x] = __fmul2_rn(__fmul2_rn(d[x], u[x]), t);
+                du[i][x] = __fmul2_rn(d[x], silu);
+                act[i][x] = __fmul2_rn(silu, u[x]);
+                am = amax3(am, act[i][x].x, act[i][x].y);
             }
         }
+        tile_column_max<T>(dg, cm[0]);
+        tile_column_max<T>(du, cm[1]);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
         if (lane == 0) wm[tid >> 5] = am;
-        tile_column_max<T>(dg, cm[0]);
+        maxima.arrive();
         tile_cast_rows<T>(p.out, dg, row0, 2 * p.F, fb * 128);
-        {
-            float du[R][8];
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                piece_da(i, du[i]);
-#pragma unroll
-                for (int x = 0; x < 8; ++x) du[i][x] = __fmul_rn(du[i][x], silu[i][x]);
-            }
-            tile_column_max<T>(du, cm[1]);
-            tile_cast_rows<T>(p.out, du, row0, 2 * p.F, p.F + fb * 128);
-        }
-        __syncthreads();
+        maxima.wait();
         tile_column_scale<T>(p.out, cm[0], cr[0], row0, fb * 128);
         tile_column_scale<T>(p.out, cm[1], cr[1], row0, p.F + fb * 128);
-        am = wm[0];
+        am = wm[lane & (CastTile<T>::kWarps - 1)];
+        joined.arrive();
 #pragma unroll
-        for (int w = 1; w < CastTile<T>::kWarps; ++w) am = fmaxf(am, wm[w]);
+        for (int o = CastTile<T>::kWarps / 2; o >= 1; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
         am = fmaxf(am, 1e-4f);
         const float ra = __fdiv_rn(448.f, am);
         if (tid == 0) p.sb[static_cast<int64_t>(fb) * (p.rows / 128) + rb] = __fdiv_rn(am, 448.f);
-        __syncthreads();
+        uint8_t* qa = p.Qa + (row0 + half) * p.F + fb * 128 + hl * 8;
+#pragma unroll
+        for (int i = 0; i < R; ++i, qa += static_cast<int64_t>(CastTile<T>::kStep) * p.F)
+            *reinterpret_cast<uint2*>(qa) = e4m3x8(act[i], ra);
+        tile_cast_rows<T>(p.out, du, row0, 2 * p.F, p.F + fb * 128);
+        joined.wait();
         tile_cast_columns<T>(p.out, dg, cr[0], row0, 2 * p.F, fb * 128);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            piece_da(i, dg[i]);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) dg[i][x] = __fmul_rn(dg[i][x], silu[i][x]);
-        }
-        tile_cast_columns<T>(p.out, dg, cr[1], row0, 2 * p.F, p.F + fb * 128);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            float u[8];
-            piece_c(i, 1, u);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) u[x] = __fmul_rn(silu[i][x], u[x]);
-            *reinterpret_cast<uint2*>(p.Qa + (row0 + half + 32 * i) * p.F + fb * 128 + hl * 8) = e4m3x8(u, ra);
-        }
+        tile_cast_columns<T>(p.out, du, cr[1], row0, 2 * p.F, p.F + fb * 128);
     }
 }
 
@@ -274,52 +297,46 @@ struct RecastParams {
     const int32_t* m_indices;  // [rows] or null
     int64_t sa_stride;
     int K, nkb;
-    int64_t rows;
+    int rows;
 };
 
-// Largest magnitude among 16 codes, NaN (0x7F) not counted: the 7 low bits of
-// an e4m3 code order its magnitudes.
-__device__ __forceinline__ uint32_t max_code(const uint4& v) {
-    uint32_t m = 0;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t x = w[i] & 0x7F7F7F7Fu;
-        x &= ~__vcmpeq4(x, 0x7F7F7F7Fu);
-        m = __vmaxu4(m, x);
-    }
-    m = max(max(m & 255u, (m >> 8) & 255u), max((m >> 16) & 255u, m >> 24));
-    return m;
-}
-
-// One CTA per 128 x 128 block, 8 threads to a row (16 codes each).  The block's
-// maximum comes from the rows' largest codes: code order is magnitude order,
-// and rounding code * scale keeps it.
+// One CTA per 128 x 128 block, 8 threads to a row (16 codes each).  The
+// block's maximum comes from the rows' largest codes: rounding code * scale
+// keeps their order.  A NaN is no maximum.
 __global__ void __launch_bounds__(kRecastThreads)
 recast_128x128_kernel(const RecastParams p) {
     __shared__ float wm[kRecastThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x;
-    const int kb = static_cast<int>(blockIdx.x % p.nkb);
-    const int64_t rb = blockIdx.x / p.nkb;
-    const int64_t at = (rb * 128 + (tid >> 3)) * p.K + kb * 128 + (tid & 7) * 16;
+    const uint32_t rb = blockIdx.x / p.nkb;
+    const int kb = static_cast<int>(blockIdx.x - rb * p.nkb);
+    const int row0 = static_cast<int>(rb) * 128 + (tid >> 3);
+    const int64_t at = static_cast<int64_t>(row0) * p.K + kb * 128 + (tid & 7) * 16, step = 32ll * p.K;
+    const float* sa = p.sa + static_cast<int64_t>(kb) * p.sa_stride + row0;
     uint4 v[4];
     float s[4];
     bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool there = p.m_indices == nullptr || p.m_indices[row0 + 32 * i] >= 0;
+        any |= there;
+        v[i] = there ? ld_once_16(p.Q + at + i * step) : make_uint4(0, 0, 0, 0);
+        s[i] = there ? sa[32 * i] : 0.f;
+    }
+    __half2 h[4][8];
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t row = rb * 128 + (tid >> 3) + 32 * i;
-        const bool there = p.m_indices == nullptr || p.m_indices[row] >= 0;
-        any |= there;
-        v[i] = there ? ld_once_16(p.Q + at + static_cast<int64_t>(32 * i) * p.K) : make_uint4(0, 0, 0, 0);
-        s[i] = there ? p.sa[static_cast<int64_t>(kb) * p.sa_stride + row] : 0.f;
-    }
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        __half2 m = __half2(__half(0.f), __half(0.f));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(max_code(v[i])), __NV_E4M3);
-        a = fmaxf(a, fabsf(__fmul_rn(__half2float(__half(h)), s[i])));
+        for (int x = 0; x < 8; ++x) {
+            h[i][x] = e4m3x2_to_half2(x & 1 ? w[x / 2] >> 16 : w[x / 2]);
+            m = __hmax2(m, __habs2(h[i][x]));
+        }
+        const float2 f = __half22float2(m);
+        a = fmaxf(a, fabsf(__fmul_rn(fmaxf(f.x, f.y), s[i])));
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -335,14 +352,13 @@ recast_128x128_kernel(const RecastParams p) {
     for (int i = 0; i < 4; ++i) {
         uint2 q[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float f[8];
-            e4m3x8_to_float(h ? make_uint2(v[i].z, v[i].w) : make_uint2(v[i].x, v[i].y), f);
+        for (int o = 0; o < 2; ++o) {
+            F8 f;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) f[x] = __fmul_rn(f[x], s[i]);
-            q[h] = e4m3x8(f, r);
+            for (int x = 0; x < 4; ++x) f[x] = __fmul2_rn(__half22float2(h[i][4 * o + x]), pair(s[i]));
+            q[o] = e4m3x8(f, r);
         }
-        *reinterpret_cast<uint4*>(p.Qb + at + static_cast<int64_t>(32 * i) * p.K) = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+        *reinterpret_cast<uint4*>(p.Qb + at + i * step) = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
     }
 }
 

@@ -29,6 +29,48 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return r;
 }
 
+// Eight values as four pairs: products of pairs are one instruction.
+using F8 = float2[4];
+
+__device__ __forceinline__ void bf16x8_to_f8(const uint4& v, F8& f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+// max(|a|, |b|, |c|), NaN not counted.
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float amax8(const F8& f) {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a = amax3(a, f[i].x, f[i].y);
+    return a;
+}
+// c + a . b over the bf16 pairs of two words: products exact, one rounding each.
+__device__ __forceinline__ float dot_bf16x2(uint32_t a, uint32_t b, float c) {
+    asm("{\n\t.reg .b16 al, ah, bl, bh;\n\t"
+        "mov.b32 {al, ah}, %1;\n\tmov.b32 {bl, bh}, %2;\n\t"
+        "fma.rn.f32.bf16 %0, al, bl, %0;\n\tfma.rn.f32.bf16 %0, ah, bh, %0;\n\t}"
+        : "+f"(c) : "r"(a), "r"(b));
+    return c;
+}
+__device__ __forceinline__ uint2 pack_e4m3x8(const F8& y) {
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = __nv_cvt_float2_to_fp8x2(y[i], __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
+}
+// e4m3x8 of dg_cast.cuh, the same roundings.
+__device__ __forceinline__ uint2 e4m3x8(const F8& f, float r) {
+    F8 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(f[i], make_float2(r, r));
+    return pack_e4m3x8(y);
+}
+
 __device__ __forceinline__ float half_warp_sum(float v) {
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -64,12 +106,13 @@ __device__ __forceinline__ float spread_scale(float amax) {
     return __fdiv_rn(back ? amax : 448.f, back ? 448.f : amax);
 }
 
-// Place of row r's scale of K block kb: groups of group_rows rows have blocks
-// of their own (masked layout); group_rows == 0: one block for all rows.
-__device__ __forceinline__ int64_t scale_at(int64_t r, int kb, int nkb, int stride, int group_rows) {
-    if (group_rows == 0) return static_cast<int64_t>(kb) * stride + r;
-    const int64_t g = r / group_rows;
-    return (g * nkb + kb) * stride + (r - g * group_rows);
+// Place of row r's scale of K block 0; block kb lies kb * stride behind it.
+// Groups of group_rows rows have scale arrays of their own (masked layout);
+// group_rows == 0: one for all rows.
+__device__ __forceinline__ int64_t scale_base(int r, int nkb, int stride, int group_rows) {
+    if (group_rows == 0) return r;
+    const int g = r / group_rows;
+    return static_cast<int64_t>(g) * nkb * stride + (r - g * group_rows);
 }
 
 // ------------------------------------------------------------- dispatch ----
@@ -81,7 +124,8 @@ struct DispatchParams {
     const int32_t* row_of; // [T][k]
     int T, k, K, nkb;
     int sa_stride, group_rows;
-    int64_t rows;
+    int rows;
+    uint32_t items;        // token groups times K block groups
 };
 
 // The cast of dg_cast.cuh's cast_1x128_kernel, a token read and cast once and
@@ -95,52 +139,53 @@ dispatch_1x128_kernel(const DispatchParams p) {
     griddep_launch_dependents();
     const int half = threadIdx.x >> 4, hl = threadIdx.x & 15;
     const int base = threadIdx.x & 16;  // first lane of this half-warp
-    const int token_groups = (p.T + kCastRowsPerCta - 1) / kCastRowsPerCta;
-    const int kb_groups = (p.nkb + NB - 1) / NB;
-    const int64_t items = static_cast<int64_t>(token_groups) * kb_groups;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int64_t t = (it / kb_groups) * kCastRowsPerCta + half;
-        const int kb0 = static_cast<int>(it % kb_groups) * NB;
+    const uint32_t kb_groups = (p.nkb + NB - 1) / NB;
+    for (uint32_t it = blockIdx.x; it < p.items; it += gridDim.x) {
+        const uint32_t tg = it / kb_groups;
+        const int t = static_cast<int>(tg) * kCastRowsPerCta + half;
+        const int kb0 = static_cast<int>(it - tg * kb_groups) * NB;
         const bool there = t < p.T;
-        const uint16_t* xr = p.X + t * p.K + kb0 * 128 + hl * 8;
+        const uint16_t* xr = p.X + static_cast<int64_t>(t) * p.K + kb0 * 128 + hl * 8;
         uint4 v[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
             v[b] = there && kb0 + b < p.nkb ? ld_once_16(xr + b * 128) : make_uint4(0, 0, 0, 0);
-        int row[2];
+        int row[2] = {-1, -1};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int j = hl + 16 * h;
-            row[h] = there && j < p.k ? p.row_of[t * p.k + j] : -1;
+            if (there && j < p.k) row[h] = p.row_of[static_cast<int64_t>(t) * p.k + j];
             if (row[h] >= p.rows) row[h] = -1;
         }
+        F8 f[NB];
         float a[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            float f[8];
-            bf16x8_to_float(v[b], f);
-            a[b] = amax8(f);
+            bf16x8_to_f8(v[b], f[b]);
+            a[b] = amax8(f[b]);
         }
         const float sc = spread_scale<NB>(half_warp_max_spread<NB>(a));
         uint2 q[NB];
+        float s[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            float f[8];
-            bf16x8_to_float(v[b], f);
-            q[b] = e4m3x8(f, __shfl_sync(0xffffffffu, sc, base + b));
-            const float s = __shfl_sync(0xffffffffu, sc, base + NB + b);
-            if (kb0 + b < p.nkb) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (row[h] >= 0) p.sa[scale_at(row[h], kb0 + b, p.nkb, p.sa_stride, p.group_rows)] = s;
-            }
+            q[b] = e4m3x8(f[b], __shfl_sync(0xffffffffu, sc, base + b));
+            s[b] = __shfl_sync(0xffffffffu, sc, base + NB + b);
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (row[h] < 0) continue;
+            float* to = p.sa + scale_base(row[h], p.nkb, p.sa_stride, p.group_rows) + static_cast<int64_t>(kb0) * p.sa_stride;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                if (kb0 + b < p.nkb) to[static_cast<int64_t>(b) * p.sa_stride] = s[b];
+        }
+        uint8_t* qc = p.Q + kb0 * 128 + hl * 8;
+        __syncwarp();
         for (int j = 0; j < p.k; ++j) {
-            const int r = __shfl_sync(0xffffffffu, row[0], base + (j & 15));
-            const int r1 = __shfl_sync(0xffffffffu, row[1], base + (j & 15));
-            const int to = j < 16 ? r : r1;
+            const int to = __shfl_sync(0xffffffffu, j < 16 ? row[0] : row[1], base + (j & 15));
             if (to < 0) continue;
-            uint8_t* qr = p.Q + static_cast<int64_t>(to) * p.K + kb0 * 128 + hl * 8;
+            uint8_t* qr = qc + static_cast<int64_t>(to) * p.K;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
                 if (kb0 + b < p.nkb) *reinterpret_cast<uint2*>(qr + b * 128) = q[b];
@@ -226,7 +271,7 @@ struct TileOut {
 
 // 1x128: each half-warp has whole rows of the tile.
 template <int T>
-__device__ __forceinline__ void tile_cast_rows(const TileOut& o, const float (&v)[CastTile<T>::kRows][8], int64_t row0,
+__device__ __forceinline__ void tile_cast_rows(const TileOut& o, const F8 (&v)[CastTile<T>::kRows], int64_t row0,
                                                int N, int col0) {
     constexpr int R = CastTile<T>::kRows;
     const int half = threadIdx.x >> 4, hl = threadIdx.x & 15, base = threadIdx.x & 16;
@@ -237,16 +282,32 @@ __device__ __forceinline__ void tile_cast_rows(const TileOut& o, const float (&v
     if (hl >= R && hl < 2 * R)
         o.sr[static_cast<int64_t>(col0 / 128) * o.sr_stride + row0 + half + CastTile<T>::kStep * (hl - R)] = s;
     uint8_t* q = o.Qr + (row0 + half) * N + col0 + hl * 8;
+    const int64_t step = static_cast<int64_t>(CastTile<T>::kStep) * N;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-        *reinterpret_cast<uint2*>(q + static_cast<int64_t>(CastTile<T>::kStep * i) * N) =
-            e4m3x8(v[i], __shfl_sync(0xffffffffu, s, base + i));
+    for (int i = 0; i < R; ++i, q += step) *reinterpret_cast<uint2*>(q) = e4m3x8(v[i], __shfl_sync(0xffffffffu, s, base + i));
 }
+
+// A CTA barrier in two halves, so that work between them hides the wait: each
+// warp arrives, later each thread waits.  Several in turn order a tile's
+// shared values as __syncthreads would.  The wait is bounded like every other.
+struct SplitBarrier {
+    uint64_t* bar;
+    int* abort_flag;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void arrive() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    }
+    __device__ __forceinline__ void wait() {
+        mbar_wait(bar, phase, abort_flag);
+        phase ^= 1;
+    }
+};
 
 // 128x1, first part: the warps' column maxima into cm[warp][kStride].  The two
 // half-warps exchange four columns each.
 template <int T>
-__device__ __forceinline__ void tile_column_max(const float (&v)[CastTile<T>::kRows][8], float* cm) {
+__device__ __forceinline__ void tile_column_max(const F8 (&v)[CastTile<T>::kRows], float* cm) {
     const int warp = threadIdx.x >> 5, hl = threadIdx.x & 15;
     const bool hi = threadIdx.x & 16;
     float m[8];
@@ -254,7 +315,8 @@ __device__ __forceinline__ void tile_column_max(const float (&v)[CastTile<T>::kR
     for (int x = 0; x < 8; ++x) {
         m[x] = 0.f;
 #pragma unroll
-        for (int i = 0; i < CastTile<T>::kRows; ++i) m[x] = fmaxf(m[x], fabsf(v[i][x]));
+        for (int i = 0; i < CastTile<T>::kRows; i += 2)
+            m[x] = x & 1 ? amax3(m[x], v[i][x / 2].y, v[i + 1][x / 2].y) : amax3(m[x], v[i][x / 2].x, v[i + 1][x / 2].x);
     }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -281,22 +343,19 @@ __device__ __forceinline__ void tile_column_scale(const TileOut& o, const float*
 
 // Third part, after another barrier.
 template <int T>
-__device__ __forceinline__ void tile_cast_columns(const TileOut& o, const float (&v)[CastTile<T>::kRows][8],
+__device__ __forceinline__ void tile_cast_columns(const TileOut& o, const F8 (&v)[CastTile<T>::kRows],
                                                   const float* cr, int64_t row0, int N, int col0) {
     const int half = threadIdx.x >> 4, hl = threadIdx.x & 15;
-    float r[8];
-    *reinterpret_cast<float4*>(r) = *reinterpret_cast<const float4*>(cr + hl * 8);
-    *reinterpret_cast<float4*>(r + 4) = *reinterpret_cast<const float4*>(cr + hl * 8 + 4);
-    uint8_t* to = o.Qc + (row0 + half) * N + col0 + hl * 8;
+    const float4 r0 = *reinterpret_cast<const float4*>(cr + hl * 8), r1 = *reinterpret_cast<const float4*>(cr + hl * 8 + 4);
+    const F8 r = {make_float2(r0.x, r0.y), make_float2(r0.z, r0.w), make_float2(r1.x, r1.y), make_float2(r1.z, r1.w)};
+    uint8_t* q = o.Qc + (row0 + half) * N + col0 + hl * 8;
+    const int64_t step = static_cast<int64_t>(CastTile<T>::kStep) * N;
 #pragma unroll
-    for (int i = 0; i < CastTile<T>::kRows; ++i) {
-        uint32_t q[4];
+    for (int i = 0; i < CastTile<T>::kRows; ++i, q += step) {
+        F8 y;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            q[x] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v[i][2 * x], r[2 * x]), __fmul_rn(v[i][2 * x + 1], r[2 * x + 1])),
-                                            __NV_SATFINITE, __NV_E4M3);
-        *reinterpret_cast<uint2*>(to + static_cast<int64_t>(CastTile<T>::kStep * i) * N) =
-            make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+        for (int x = 0; x < 4; ++x) y[x] = __fmul2_rn(v[i][x], r[x]);
+        *reinterpret_cast<uint2*>(q) = pack_e4m3x8(y);
     }
 }
 
@@ -345,9 +404,18 @@ combine_bwd_kernel(const CombineBwdParams p) {
     __shared__ __align__(16) float cm[CastTile<T>::kWarps * CastTile<T>::kStride];
     __shared__ __align__(16) float cr[128];
     __shared__ float part[128];
+    __shared__ uint64_t bars[2];
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, half = tid >> 4, hl = tid & 15;
+    if (tid == 0) {
+        mbar_init(&bars[0], CastTile<T>::kWarps);
+        mbar_init(&bars[1], CastTile<T>::kWarps);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    SplitBarrier maxima{&bars[0], &abort_flag}, joined{&bars[1], &abort_flag};
     griddep_wait();
     griddep_launch_dependents();
-    const int tid = threadIdx.x, half = tid >> 4, hl = tid & 15;
     const uint32_t rank = cluster_ctarank(), nctas = cluster_nctarank();
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / nctas) * 128;
 
@@ -374,37 +442,42 @@ combine_bwd_kernel(const CombineBwdParams p) {
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / nctas);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / nctas);
     const uint32_t stage = smem_u32(stage_smem) + tid * 16;
+    const uint16_t* y0 = p.Y + (row0 + half) * p.N + hl * 8;
+    const int64_t step = static_cast<int64_t>(CastTile<T>::kStep) * p.N;
     auto fetch = [&](int kb) {
-        const int64_t col = kb * 128 + hl * 8;
+        const uint16_t* y = y0 + kb * 128;
+        const uint16_t* d = p.dout + kb * 128 + hl * 8;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const uint32_t bytes = token[i] >= 0 ? 16 : 0;
-            cp_async_16(stage + 2 * i * T * 16, p.dout + static_cast<int64_t>(max(token[i], 0)) * p.N + col, bytes);
-            cp_async_16(stage + (2 * i + 1) * T * 16, p.Y + (row0 + half + CastTile<T>::kStep * i) * p.N + col, bytes);
+        for (int i = 0; i < R; ++i, y += step) {
+            const uint32_t bytes = token[i] >= 0 ? 16 : 0;  // missing rows are zeros
+            cp_async_16(stage + 2 * i * T * 16, d + static_cast<int64_t>(max(token[i], 0)) * p.N, bytes);
+            cp_async_16(stage + (2 * i + 1) * T * 16, y, bytes);
         }
         cp_async_commit();
     };
     fetch(kb0);
     for (int kb = kb0; kb < kb1; ++kb) {
         cp_async_wait<0>();
-        float v[R][8];
+        F8 v[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            float yf[8];
-            bf16x8_to_float(ld_shared_16(stage + 2 * i * T * 16), v[i]);
-            bf16x8_to_float(ld_shared_16(stage + (2 * i + 1) * T * 16), yf);
+            bf16x8_to_f8(ld_shared_16(stage + 2 * i * T * 16), v[i]);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                dot[i] = fmaf(v[i][x], yf[x], dot[i]);
-                v[i][x] = token[i] >= 0 ? __fmul_rn(v[i][x], w[i]) : 0.f;
-            }
+            for (int x = 0; x < 4; ++x) v[i][x] = __fmul2_rn(v[i][x], make_float2(w[i], w[i]));
+        }
+        tile_column_max<T>(v, cm);
+        maxima.arrive();
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const uint4 d = ld_shared_16(stage + 2 * i * T * 16), y = ld_shared_16(stage + (2 * i + 1) * T * 16);
+            dot[i] = dot_bf16x2(d.x, y.x, dot_bf16x2(d.y, y.y, dot_bf16x2(d.z, y.z, dot_bf16x2(d.w, y.w, dot[i]))));
         }
         if (kb + 1 < kb1) fetch(kb + 1);
-        tile_column_max<T>(v, cm);
-        tile_cast_rows<T>(p.out, v, row0, p.N, kb * 128);
-        __syncthreads();
+        maxima.wait();
         tile_column_scale<T>(p.out, cm, cr, row0, kb * 128);
-        __syncthreads();
+        joined.arrive();
+        tile_cast_rows<T>(p.out, v, row0, p.N, kb * 128);
+        joined.wait();
         tile_cast_columns<T>(p.out, v, cr, row0, p.N, kb * 128);
     }
 #pragma unroll

@@ -104,24 +104,31 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v)
     return static_cast<unsigned long long>(hi) << 32 | lo;
 }
 
-// For choosing only: absolute error below 2^-22 (exponential and reciprocal
-// good to 2 ulp, one rounding of the sum between).
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// exp and the sigmoid by the special-function unit alone, without the care for
+// subnormal numbers: relative error 2^-22 and |x| 2^-24 for the argument's
+// rounding; absolute error of the sigmoid below 2^-22.
+__device__ __forceinline__ float exp_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.f + exp_fast(-x)); }
 // For results: relative error a few 2^-24.
 __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
 
-// The two largest of a set in the order (value, lower index first).
-struct Top2 {
-    float v1 = -INFINITY, v2 = -INFINITY;
-    int i1 = 0, i2 = 0;
-    __device__ __forceinline__ void add(float x, int i) {  // indices come in rising order
-        const bool p = x > v1, q = x > v2;
-        i2 = p ? i1 : q ? i : i2;
-        i1 = p ? i : i1;
-        v2 = fmaxf(v2, fminf(v1, x));
-        v1 = fmaxf(v1, x);
-    }
-};
+// Signed integers in the order of finite or infinite floats, and back.
+__device__ __forceinline__ int ordered_int(float f) {
+    const int b = __float_as_int(f);
+    return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float ordered_float(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)); }
+constexpr int kNoKey = -0x7FFFFFFF - 1;
+constexpr int kLeastKey = static_cast<int>(0x80800000u);  // of the lowest finite float
 
 // The choice in FP64 over the whole row, for a token that FP32 cannot decide
 // even in part (a NaN, groups next to one another, a crowd at the border).
@@ -153,24 +160,22 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const L* row) {
         }
         for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     }
-    uint32_t ok = 0;  // bit i: the lane's expert i is eligible
+    unsigned long long key[EPL];  // of the choice value, 0: not eligible
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         const int e = lane * p.per + i;
+        key[i] = 0;
         if (i < p.per && e < p.E) {
             const float l = logit_at(row + e);
             const float b = p.bias ? p.bias[e] : 0.f;
             const double s = p.softmax ? c[i] / z : 1.0 / (1.0 + exp(-static_cast<double>(l)));
-            c[i] = s + static_cast<double>(b);
-            if (l != -INFINITY && b != -INFINITY) ok |= 1u << i;
-        } else {
-            c[i] = 0.0;
+            if (l != -INFINITY && b != -INFINITY) key[i] = order_key(s + static_cast<double>(b));
         }
     }
     if (p.groups > 1) {
         unsigned long long mine = 0;
         for (int g = 0; g < p.groups; ++g) {
-            // The group's best is removed for the second round, by its index.
+            // The group's best is left out of the second round, by its index.
             unsigned long long top[2] = {0, 0};
             int taken = -1;
             for (int r = 0; r < p.gtop; ++r) {
@@ -179,9 +184,8 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const L* row) {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
                     const int e = lane * p.per + i;
-                    const unsigned long long x =
-                        ((ok >> i) & 1u) && e / p.gsize == g && e != taken ? order_key(c[i]) : 0;
-                    if (x > best) { best = x; at = e; }
+                    const int grp = static_cast<int>((static_cast<uint32_t>(e) * p.gsize_magic) >> 20);
+                    if (grp == g && e != taken && key[i] > best) { best = key[i]; at = e; }
                 }
                 const unsigned long long t = warp_max_u64(best);
                 taken = __reduce_min_sync(0xffffffffu, best == t ? at : 0x7FFFFFFF);
@@ -202,31 +206,75 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const L* row) {
         }
         const uint32_t kept = __ballot_sync(0xffffffffu, lane < p.groups && mine != 0 && rank < p.keep);
 #pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const uint32_t grp = (static_cast<uint32_t>(lane * p.per + i) * p.gsize_magic) >> 20;
+            if (!((kept >> (grp & 31u)) & 1u)) key[i] = 0;
+        }
+    }
+    if (!p.bias) {  // in the order of the logits themselves
+#pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (!((kept >> (((lane * p.per + i) / p.gsize) & 31)) & 1u)) ok &= ~(1u << i);
+            if (key[i]) key[i] = order_key(static_cast<double>(logit_at(row + lane * p.per + i)));
     }
     int my = -1;
     for (int j = 0; j < p.k; ++j) {
         unsigned long long best = 0;
         int at = 0x7FFFFFFF;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = lane * p.per + i;
-            if (!((ok >> i) & 1u)) continue;
-            const unsigned long long x = order_key(p.bias ? c[i] : static_cast<double>(logit_at(row + e)));
-            if (x > best) { best = x; at = e; }
-        }
+        for (int i = 0; i < EPL; ++i)
+            if (key[i] > best) { best = key[i]; at = lane * p.per + i; }
         const unsigned long long top = warp_max_u64(best);
         if (top == 0) break;
         at = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7FFFFFFF);
         if (lane == j) my = at;
-        if (at / p.per == lane) ok &= ~(1u << (at - lane * p.per));
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (lane * p.per + i == at) key[i] = 0;
     }
     return my;
 }
 
-// The order of n <= 32 candidates in FP64: lane j < n holds expert e.  Every
-// other expert is known to lie below the k-th of them.  Returns the lane's rank.
+// The groups kept, decided in FP64 where groups are whole lanes: a lane's two
+// best experts are e1 and e2 (-1: none; no third is close to them).  Returns
+// whether this lane's group is kept.
+template <typename L>
+__device__ __noinline__ bool keep_groups_exact(const RouteParams& p, const L* row, int e1, int e2) {
+    const int lane = threadIdx.x & 31, g = lane / p.group_lanes;
+    double m = 0.0, z = 1.0;
+    if (p.softmax) {
+        m = -INFINITY;
+        z = 0.0;
+        for (int i = lane; i < p.E; i += 32) m = fmax(m, static_cast<double>(logit_at(row + i)));
+        for (int o = 16; o >= 1; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int i = lane; i < p.E; i += 32) z += exp(static_cast<double>(logit_at(row + i)) - m);
+        for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    }
+    double v[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = i ? e2 : e1;
+        if (e < 0) continue;
+        const double l = logit_at(row + e);
+        v[i] = (p.softmax ? exp(l - m) / z : 1.0 / (1.0 + exp(-l))) + (p.bias ? static_cast<double>(p.bias[e]) : 0.0);
+    }
+    double a = fmax(v[0], v[1]), b = fmin(v[0], v[1]);
+    for (int o = p.group_lanes >> 1; o >= 1; o >>= 1) {
+        const double xa = __shfl_xor_sync(0xffffffffu, a, o), xb = __shfl_xor_sync(0xffffffffu, b, o);
+        b = fmax(fmax(b, xb), fmin(a, xa));
+        a = fmax(a, xa);
+    }
+    double sum = a + (p.gtop == 2 && b != -INFINITY ? b : 0.0);
+    if (g >= p.groups) sum = -INFINITY;
+    int rank = 0;
+    for (int h = 0; h < p.groups; ++h) {
+        const double o = __shfl_sync(0xffffffffu, sum, h * p.group_lanes);
+        rank += (o > sum || (o == sum && h < g)) ? 1 : 0;
+    }
+    return sum != -INFINITY && rank < p.keep;
+}
+
+// The order of n <= 32 candidates in FP64: lane j < n holds expert e.  Returns
+// the lane's rank.
 template <int EPL, typename L>
 __device__ __noinline__ int rank_candidates(const RouteParams& p, const L* row, int n, int e) {
     const int lane = threadIdx.x & 31;
@@ -251,14 +299,23 @@ __device__ __noinline__ int rank_candidates(const RouteParams& p, const L* row, 
     return rank;
 }
 
-// One warp per token, lane i holding the experts i * per ..; the order within
-// a lane, then over the lanes, is the experts' own, so ties fall to the lowest
-// lane.  Each lane keeps the two best of its experts: their sums over a
-// group's lanes are the group scores, and the k rounds of a warp-wide maximum
-// take from them; a lane that gives both looks through its experts again.
+// One warp per token, lane i holding the experts i * per ...
+//
+// The choice works on keys: a value's leading bits in integer order, and in
+// its low bits the expert's place (lane, then place in the lane, counted down),
+// so that a maximum of keys is a value, its expert and the rule for ties at
+// once.  A key costs three instructions, keeping a lane's two largest three
+// more, and a round of the choice one warp-wide maximum.  The k experts so
+// found are the right set where the (k+1)-th key is clearly below; their order
+// is decided by their FP32 values, and by FP64 values where those are not
+// clearly apart.  bf16 logits without a bias fit a key whole.
+//
+// Bound by instructions: 16384 tokens of 256 float32 logits are 2.6 us of HBM.
 template <int EPL, typename L>
-__global__ void __launch_bounds__(kRouteWarps * 32)
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1)
 route_topk_kernel(const RouteParams p) {
+    constexpr int kMask = 32 * EPL - 1;  // a key's place bits
+    constexpr bool kShort = sizeof(L) == 2;
     extern __shared__ float route_smem[];  // groups that are not whole lanes: E values per warp
     __shared__ uint16_t cand_smem[kRouteWarps][32];
     griddep_wait();
@@ -268,6 +325,7 @@ route_topk_kernel(const RouteParams p) {
     if (t >= p.T) return;
     const L* row = static_cast<const L*>(p.logits) + t * p.E;
     const int e0 = lane * p.per;
+    const bool biased = p.bias != nullptr;
 
     float v[EPL];  // logits, then (with a bias) choice values; -inf: not eligible
     if (p.vec) {
@@ -276,10 +334,6 @@ route_topk_kernel(const RouteParams p) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) v[i] = i < p.per && e0 + i < p.E ? logit_at(row + e0 + i) : -INFINITY;
     }
-    bool odd = false;  // a NaN somewhere, or an infinite choice value
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) odd |= v[i] != v[i];
-
     float mx = 0.f, rz = 1.f;
     if (p.softmax) {
         float m = v[0];
@@ -288,72 +342,87 @@ route_topk_kernel(const RouteParams p) {
         mx = warp_max(m);
         float z = 0.f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) z += __expf(v[i] - mx);
+        for (int i = 0; i < EPL; ++i) z += exp_fast(v[i] - mx);
         rz = 1.f / warp_sum(z);
-        odd |= rz != rz && mx != -INFINITY;  // an infinite logit
     }
     // FP32 moves a choice value by less than `slack` (of the largest score:
     // exponential, sum and reciprocal of a softmax 2^-20, sigmoid_fast 2^-22),
     // and adding the bias by 2^-24 of the value.
     const float slack = p.softmax ? rz * 0x1p-20f : 0x1p-22f;
+    auto apart_by = [&](float x, float y) {  // more than FP32 can have moved x - y
+        return biased ? 2.f * slack + 0x1p-22f * (fabsf(x) + fabsf(y)) : 0.f;
+    };
+    auto score = [&](float x) { return p.softmax ? exp_fast(x - mx) * rz : sigmoid_fast(x); };
 
-    if (p.bias != nullptr) {
+    if (biased) {
         float b[EPL];
         if (p.vec) {
             load_logits<EPL>(p.bias + lane * EPL, b);
         } else {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) b[i] = i < p.per && e0 + i < p.E ? p.bias[e0 + i] : 0.f;
+            for (int i = 0; i < EPL; ++i) b[i] = i < p.per && e0 + i < p.E ? p.bias[e0 + i] : -INFINITY;
+        }
+        float low = v[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) low = fminf(low, v[i]);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) b[i] += score(v[i]);
+        if (low == -INFINITY) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) b[i] = v[i] == -INFINITY ? -INFINITY : b[i];
         }
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const float s = p.softmax ? __expf(v[i] - mx) * rz : sigmoid_fast(v[i]);
-            v[i] = v[i] == -INFINITY ? -INFINITY : s + b[i];
-            odd |= !(v[i] < INFINITY);
-        }
+        for (int i = 0; i < EPL; ++i) v[i] = b[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) v[i] += 0.f;  // one zero
     }
+    // A NaN, or an infinite choice value: to be decided without shortcuts.
+    float all = v[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) all += v[i];
+    const bool inf_ok = !biased && !p.softmax;
+    bool odd = inf_ok ? all != all : !(all < INFINITY) || (rz != rz && mx != -INFINITY);
     odd = __any_sync(0xffffffffu, odd);
 
-    Top2 best;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) best.add(v[i], i);
     bool in = true, sure = true;  // in: the lane's experts take part
     if (p.groups > 1 && !odd) {
+        float a = -INFINITY, b = -INFINITY;  // the two best choice values of the group
+        int g, lanes;                        // this lane's group, lanes per group
         // A choice value without a bias is the score of the logit.
-        auto score = [&](float x) {
-            return x == -INFINITY || p.bias != nullptr ? x : p.softmax ? __expf(x - mx) * rz : sigmoid_fast(x);
-        };
-        float a, b;
-        int g, first, stride;  // this lane's group, and the lanes that hold the groups' sums
+        auto choice = [&](float x) { return x == -INFINITY || biased ? x : score(x); };
         if (p.group_lanes) {
-            a = score(best.v1);
-            b = score(best.v2);
-            g = lane / p.group_lanes;
-            stride = p.group_lanes;
-            first = p.group_lanes;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                b = fmaxf(b, fminf(a, v[i]));
+                a = fmaxf(a, v[i]);
+            }
+            a = choice(a);
+            b = choice(b);
+            lanes = p.group_lanes;
+            g = lane / lanes;
         } else {
-            // 2^sh lanes share a group in shared memory.
+            // A power of two of lanes share a group in shared memory.
             float* cs = route_smem + warp * p.E;
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (i < p.per && e0 + i < p.E) cs[e0 + i] = score(v[i]);
+                if (i < p.per && e0 + i < p.E) cs[e0 + i] = choice(v[i]);
             __syncwarp();
             const int sh = 31 - __clz(32 / p.groups);
             g = lane >> sh;
-            stride = first = 1 << sh;
-            a = b = -INFINITY;
+            lanes = 1 << sh;
             if (g < p.groups) {
-                const int sub = lane & (stride - 1);
+                const int sub = lane & (lanes - 1);
                 // Each group starts at another place: the same places of groups of 32 share a bank.
                 const int turn = (g << sh) % p.gsize;
-                for (int n = sub; n < p.gsize; n += stride) {
+                for (int n = sub; n < p.gsize; n += lanes) {
                     const float x = cs[g * p.gsize + (n + turn < p.gsize ? n + turn : n + turn - p.gsize)];
                     b = fmaxf(b, fminf(a, x));
                     a = fmaxf(a, x);
                 }
             }
         }
-        for (int o = first >> 1; o >= 1; o >>= 1) {
+        for (int o = lanes >> 1; o >= 1; o >>= 1) {
             const float xa = __shfl_xor_sync(0xffffffffu, a, o), xb = __shfl_xor_sync(0xffffffffu, b, o);
             b = fmaxf(fmaxf(b, xb), fminf(a, xa));
             a = fmaxf(a, xa);
@@ -362,92 +431,133 @@ route_topk_kernel(const RouteParams p) {
         if (g >= p.groups) sum = -INFINITY;
         int rank = 0;
         for (int h = 0; h < p.groups; ++h) {
-            const float o = __shfl_sync(0xffffffffu, sum, h * stride);
+            const float o = __shfl_sync(0xffffffffu, sum, h * lanes);
             rank += (o > sum || (o == sum && h < g)) ? 1 : 0;
         }
-        const bool kept = sum != -INFINITY && rank < p.keep;
+        bool kept = sum != -INFINITY && rank < p.keep;
         // Certain when the worst kept group and the best other are clearly apart.
         const float lo = warp_min(kept ? sum : INFINITY), hi = warp_max(kept ? -INFINITY : sum);
-        if (hi != -INFINITY && !(lo - hi > 4.f * slack + 0x1p-21f * (fabsf(lo) + fabsf(hi)))) sure = false;
+        if (hi != -INFINITY && !(lo - hi > 4.f * slack + 0x1p-21f * (fabsf(lo) + fabsf(hi)))) {
+            // The lane's two best, if no third can take their place in FP64.
+            float b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
+            int e1 = -1, e2 = -1;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const bool first = v[i] > b1, second = v[i] > b2;
+                b3 = fmaxf(b3, fminf(b2, v[i]));
+                e2 = first ? e1 : second ? e0 + i : e2;
+                e1 = first ? e0 + i : e1;
+                b2 = fmaxf(b2, fminf(b1, v[i]));
+                b1 = fmaxf(b1, v[i]);
+            }
+            const bool two = b3 == -INFINITY || b2 - b3 > apart_by(b2, b3) || (!biased && b2 == b3);
+            if (p.group_lanes && __all_sync(0xffffffffu, two)) kept = keep_groups_exact<L>(p, row, e1, e2);
+            else sure = false;
+        }
         if (p.group_lanes) {
             in = kept;
-            if (!kept) best = Top2();
         } else {
-            const uint32_t lanes = __ballot_sync(0xffffffffu, kept);
-            best = Top2();
+            const uint32_t on = __ballot_sync(0xffffffffu, kept);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const uint32_t grp = (static_cast<uint32_t>(e0 + i) * p.gsize_magic) >> 20;
-                if (!((lanes >> ((grp * stride) & 31u)) & 1u)) v[i] = -INFINITY;
-                best.add(v[i], i);
+                if (!((on >> ((grp * lanes) & 31u)) & 1u)) v[i] = -INFINITY;
             }
         }
     }
 
-    // k rounds, with a bias one more for the runner-up.
-    int my = -1;
-    float my_v = -INFINITY;
-    bool two = true;  // v2 is the lane's second best
-    const int rounds = p.k + (p.bias != nullptr ? 1 : 0);
-    for (int j = 0; j < rounds; ++j) {
-        const float top = warp_max(best.v1);
-        if (top == -INFINITY) break;
-        const int wl = __ffs(__ballot_sync(0xffffffffu, best.v1 == top)) - 1;
-        const int wi = __shfl_sync(0xffffffffu, best.i1, wl);
-        if (lane == j) {
-            my = wl * p.per + wi;
-            my_v = top;
-        }
-        if (lane == wl) {
-            if (two) {
-                best.v1 = best.v2;
-                best.i1 = best.i2;
-                two = false;
-            } else {
-                best = Top2();
+    int my = -1, slot = lane;
+    if (sure && !odd) {
+        // Keys: without the lane's bits, which the lane's own order does not need.
+        const int lane_bits = (31 - lane) * EPL;
+        int key[EPL], k1 = kNoKey, k2 = kNoKey;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    best.add(v[i] < top || (v[i] == top && i > wi) ? v[i] : -INFINITY, i);
-                two = true;
-            }
+        for (int i = 0; i < EPL; ++i) {
+            key[i] = (ordered_int(v[i]) & ~kMask) | (EPL - 1 - i);
+            k2 = max(k2, min(k1, key[i]));
+            k1 = max(k1, key[i]);
         }
-    }
-    int slot = lane;
-    if (p.bias != nullptr && sure && !odd) {
-        // Neighbours in the order must be clearly apart, or equal because both
-        // logit and bias are (then the lower index is right).
-        const int next = __shfl_down_sync(0xffffffffu, my, 1);
-        const float next_v = __shfl_down_sync(0xffffffffu, my_v, 1);
-        bool apart = true;
-        if (lane < p.k && next >= 0)
-            apart = my_v - next_v > 2.f * slack + 0x1p-22f * (fabsf(my_v) + fabsf(next_v)) ||
-                    (logit_at(row + my) == logit_at(row + next) && p.bias[my] == p.bias[next]);
-        if (!__all_sync(0xffffffffu, apart)) {
-            // All experts that may belong to the k: those not clearly below the k-th.
-            const float last = __shfl_sync(0xffffffffu, my_v, p.k - 1);
-            const float floor_v = last - (2.f * slack + 0x1p-21f * fabsf(last));
-            int n = 0, e = -1;
+        if (in) {
+            k1 |= lane_bits;
+            k2 |= lane_bits;
+        } else {
+            k1 = k2 = kNoKey;
+        }
+        // k rounds, one more for the runner-up.
+        int my_key = kNoKey;
+        bool two = true;  // k2 is the lane's second largest
+        for (int j = 0; j <= p.k; ++j) {
+            const int top = __reduce_max_sync(0xffffffffu, k1);
+            if (top < kLeastKey) break;
+            if (lane == j) my_key = top;
+            if (k1 == top) {
+                if (two) {
+                    k1 = k2;
+                    two = false;
+                } else {
+                    // Look for the largest below it again.
+                    const int below = top ^ lane_bits;
+                    k1 = kNoKey;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const bool c = in && v[i] >= floor_v && v[i] != -INFINITY;
-                const uint32_t who = __ballot_sync(0xffffffffu, c);
-                const int at = n + __popc(who & ((1u << lane) - 1u));
-                if (c && at < 32) cand_smem[warp][at] = static_cast<uint16_t>(e0 + i);
-                n += __popc(who);
-            }
-            __syncwarp();
-            if (n <= 32) {
-                if (lane < n) e = cand_smem[warp][lane];
-                slot = rank_candidates<EPL, L>(p, row, n, e);
-                my = e;
-                if (lane >= n) slot = 32;
-                // Fewer experts than slots: lanes past them fill the rest.
-                if (lane >= n && lane < p.k) {
-                    my = -1;
-                    slot = lane;
+                    for (int i = 0; i < EPL; ++i) k1 = max(k1, key[i] < below ? key[i] : kNoKey);
+                    k1 |= lane_bits;
                 }
-            } else {
-                sure = false;
+            }
+        }
+        auto expert_of = [&](int k) { return (31 - (k & kMask) / EPL) * p.per + EPL - 1 - (k & (EPL - 1)); };
+        if (my_key >= kLeastKey) my = expert_of(my_key);
+
+        if (!kShort || biased) {
+            int n = p.k;  // candidates: lane j < n holds one, or none
+            bool ranked = true;  // the lanes may not be in order
+            const int last = __shfl_sync(0xffffffffu, my_key, p.k - 1), next = __shfl_sync(0xffffffffu, my_key, p.k);
+            const float x = ordered_float(last & ~kMask), y = ordered_float(next | kMask);
+            if (next >= kLeastKey && !(x - y > apart_by(x, y))) {
+                // All experts that may belong to the k: those not clearly below the k-th.
+                const int least = ordered_int(x - apart_by(x, x)) & ~kMask;
+                n = 0;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const bool c = in && key[i] >= least && key[i] >= kLeastKey;
+                    const uint32_t who = __ballot_sync(0xffffffffu, c);
+                    const int at = n + __popc(who & ((1u << lane) - 1u));
+                    if (c && at < 32) cand_smem[warp][at] = static_cast<uint16_t>(e0 + i);
+                    n += __popc(who);
+                }
+                __syncwarp();
+                ranked = false;
+                if (n > 32) {
+                    sure = false;
+                } else {
+                    my = lane < n ? cand_smem[warp][lane] : -1;
+                }
+            }
+            // The candidates' values: lane order holds if every one is clearly above the next.
+            const bool some = lane < n && my >= 0;
+            const float l = some ? logit_at(row + my) : 0.f, b = some && biased ? p.bias[my] : 0.f;
+            const float c = !some ? -INFINITY : biased ? score(l) + b : l;
+            if (sure) {
+                const float below = __shfl_down_sync(0xffffffffu, c, 1);
+                const int below_e = __shfl_down_sync(0xffffffffu, my, 1);
+                const bool last_one = lane + 1 >= n || below_e < 0 || !some;
+                const bool good = last_one || c - below > apart_by(c, below) || (!biased && c == below && my < below_e);
+                if (!ranked || !__all_sync(0xffffffffu, good)) {
+                    int rank = 0;
+                    bool near = false;
+                    for (int h = 0; h < n; ++h) {
+                        const float o = __shfl_sync(0xffffffffu, c, h);
+                        const int oe = __shfl_sync(0xffffffffu, my, h);
+                        const float ol = __shfl_sync(0xffffffffu, l, h), ob = __shfl_sync(0xffffffffu, b, h);
+                        rank += (o > c || (o == c && oe < my)) ? 1 : 0;
+                        // Equal because both logit and bias are: the lower index is right.
+                        near |= some && oe >= 0 && oe != my && !(fabsf(o - c) > apart_by(o, c)) && !(ol == l && ob == b);
+                    }
+                    if (biased && __any_sync(0xffffffffu, near)) {
+                        const int m = __popc(__ballot_sync(0xffffffffu, some));  // lanes 0 .. m - 1
+                        rank = rank_candidates<EPL, L>(p, row, m, my);
+                    }
+                    slot = some ? rank : lane < p.k ? lane : 32;  // lanes behind the last expert keep their place
+                }
             }
         }
     }
@@ -462,7 +572,7 @@ route_topk_kernel(const RouteParams p) {
         const float x = logit_at(row + my);
         s = p.softmax ? expf(x - mx) * rz : sigmoid_f(x);
     }
-    if (p.renorm) s = s / (warp_sum(s) + kRouteEps);
+    if (p.renorm) s = __fdividef(s, warp_sum(s) + kRouteEps);
     if (chosen) {
         p.idx[t * p.k + slot] = my;
         p.w[t * p.k + slot] = s * p.scale;
@@ -521,10 +631,12 @@ __device__ __forceinline__ void store_logits(uint16_t* p, const float (&f)[N]) {
 // w_j = scale s_j (/ S, S = sum_j s_j + eps):  ds_j = scale dw_j, or
 // scale/S (dw_j - sum_i dw_i s_i / S).  Sigmoid: dl = ds s (1 - s) at the
 // chosen experts, zero elsewhere; softmax: dl_e = s_e (ds_e - sum_j ds_j s_j).
-// One warp per token; only softmax reads the whole row.
+// One warp per token; only softmax reads the whole row.  The k gradients meet
+// their experts through a row of shared memory.
 template <int EPL, typename L>
 __global__ void __launch_bounds__(kRouteWarps * 32)
 route_topk_bwd_kernel(const RouteBwdParams p) {
+    extern __shared__ __align__(16) float route_smem[];  // 32 * EPL values per warp
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -540,7 +652,7 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         e = p.idx[t * p.k + lane];
         if (e < 0 || e >= p.E) e = -1;
         else x = logit_at(row + e);
-        g = p.dw[t * p.k + lane] * p.scale;
+        g = e < 0 ? 0.f : p.dw[t * p.k + lane] * p.scale;
     }
     float d[EPL];
     float mx = 0.f, rz = 1.f;
@@ -555,41 +667,49 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
 #pragma unroll
         for (int i = 1; i < EPL; ++i) m = fmaxf(m, d[i]);
         mx = warp_max(m);
+        if (mx == -INFINITY) mx = 0.f;  // every expert masked: no score, no gradient
         float z = 0.f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            d[i] = mx == -INFINITY ? 0.f : expf(d[i] - mx);  // every expert masked: no score, no gradient
+            d[i] = exp_fast(d[i] - mx);
             z += d[i];
         }
-        rz = mx == -INFINITY ? 0.f : 1.f / warp_sum(z);
+        z = warp_sum(z);
+        rz = z > 0.f || z != z ? 1.f / z : 0.f;
     }
     float s = 0.f;
-    if (e >= 0) s = !p.softmax ? sigmoid_f(x) : mx == -INFINITY ? 0.f : expf(x - mx) * rz;
-    else g = 0.f;
+    if (e >= 0) s = p.softmax ? expf(x - mx) * rz : sigmoid_f(x);
     if (p.renorm) {
         const float r = 1.f / (warp_sum(s) + kRouteEps);
-        const float mean = warp_sum(g * s) * r;  // all lanes take part
+        const float mean = warp_sum(g * s) * r;
         g = e < 0 ? 0.f : (g - mean) * r;
     }
     float dot = 0.f;
-    if (p.softmax) {
-        dot = warp_sum(g * s);
-    } else {
-        g *= s * (1.f - s);
-    }
+    if (p.softmax) dot = warp_sum(g * s);
+    else g *= s * (1.f - s);
+
+    float* line = route_smem + warp * 32 * EPL;
     float r[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) r[i] = -dot;
-    for (int j = 0; j < p.k; ++j) {
-        const int ej = __shfl_sync(0xffffffffu, e, j) - e0;
-        const float gj = __shfl_sync(0xffffffffu, g, j);
-        // -1 - e0 matches no i in range; another lane's expert neither
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) r[i] += i == ej && i < p.per ? gj : 0.f;
+    for (int i = 0; i < EPL; ++i) r[i] = 0.f;
+    store_logits<EPL>(line + lane * EPL, r);
+    // An expert in several slots: its first slot takes the sum, in slot order.
+    const uint32_t same = __match_any_sync(0xffffffffu, e >= 0 ? e : -1 - lane);
+    if (__any_sync(0xffffffffu, (same & (same - 1u)) != 0)) {
+        float sum = 0.f;
+        for (int j = 0; j < p.k; ++j) {
+            const float gj = __shfl_sync(0xffffffffu, g, j);
+            if ((same >> j) & 1u) sum += gj;
+        }
+        g = sum;
     }
+    __syncwarp();
+    if (e >= 0 && lane == __ffs(same) - 1) line[e / p.per * EPL + e % p.per] = g;
+    __syncwarp();
+    load_logits<EPL>(line + lane * EPL, r);
     if (p.softmax) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) r[i] *= d[i] * rz;
+        for (int i = 0; i < EPL; ++i) r[i] = (r[i] - dot) * (d[i] * rz);
     }
     if (p.vec) {
         store_logits<EPL>(out + lane * EPL, r);
