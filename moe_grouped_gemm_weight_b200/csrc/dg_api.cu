@@ -867,6 +867,9 @@ dg_status launch_plain(void (*kern)(P), const P& p, int64_t grid, int threads, i
     return ok();
 }
 
+// Slots of a call: indexes and a grid's stride past the last fit in 31 bits.
+constexpr int64_t kMaxSlotCount = 0x7FF00000;
+
 // Sizes that the routing calls share.
 dg_status check_route(int T, int E, int k, int dtype, int score) {
     if (T < 0 || E <= 0 || k <= 0) return fail(DG_ERR_INVALID_ARG, "bad sizes T=%d E=%d k=%d", T, E, k);
@@ -875,7 +878,7 @@ dg_status check_route(int T, int E, int k, int dtype, int score) {
     if (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID) return fail(DG_ERR_INVALID_ARG, "bad score %d", score);
     if (E > dg::kRouteMaxExperts) return fail(DG_ERR_UNSUPPORTED, "E=%d is more than %d", E, dg::kRouteMaxExperts);
     if (k > dg::kRouteMaxK) return fail(DG_ERR_UNSUPPORTED, "k=%d is more than %d", k, dg::kRouteMaxK);
-    if (static_cast<int64_t>(T) * k > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED, "T*k does not fit in 31 bits");
+    if (static_cast<int64_t>(T) * k > kMaxSlotCount) return fail(DG_ERR_UNSUPPORTED, "T*k=%lld is too large", static_cast<long long>(T) * k);
     return DG_OK;
 }
 
@@ -885,7 +888,7 @@ dg_status check_slots(int T, int k, int64_t rows) {
     if (T < 0 || k <= 0 || rows < 0)
         return fail(DG_ERR_INVALID_ARG, "bad sizes T=%d k=%d rows=%lld", T, k, static_cast<long long>(rows));
     if (k > kMaxSlots) return fail(DG_ERR_UNSUPPORTED, "k=%d is more than %d", k, kMaxSlots);
-    if (static_cast<int64_t>(T) * k > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED, "T*k does not fit in 31 bits");
+    if (static_cast<int64_t>(T) * k > kMaxSlotCount) return fail(DG_ERR_UNSUPPORTED, "T*k=%lld is too large", static_cast<long long>(T) * k);
     return DG_OK;
 }
 
@@ -905,6 +908,12 @@ dg_status check_row_blocks(int64_t rows, int N, const char* name) {
     if (N % 128 != 0) return fail(DG_ERR_UNSUPPORTED, "%s=%d must be a multiple of 128", name, N);
     if (N > (1 << 28)) return fail(DG_ERR_UNSUPPORTED, "%s=%d is too large", name, N);
     return DG_OK;
+}
+
+// CTAs of the routing kernels: those resident at once, or fewer.
+int64_t route_grid(int T) {
+    const int64_t all = cdiv64(T, dg::kRouteWarps), cap = static_cast<int64_t>(effective_sms()) * dg::kRouteCtas;
+    return all < cap ? all : cap;
 }
 
 // Every lane holds `per` experts, and that is an instance's number: wide loads
@@ -1314,13 +1323,14 @@ dg_status dg_route_topk(int32_t* topk_idx, float* topk_w, const void* logits, in
     const int gsize = E / groups;
     const int per = cdiv(E, 32), gl = gsize % per == 0 ? gsize / per : 0;
     // Groups of whole lanes need no shared memory; every group's lanes join in a power of two.
-    const int group_lanes = groups > 1 && gl > 0 && (gl & (gl - 1)) == 0 ? gl : 0;
+    const int group_shift = groups > 1 && gl > 0 && (gl & (gl - 1)) == 0 ? __builtin_ctz(gl) : -1;
     dg::RouteParams p{logits, bias, topk_idx, topk_w, T, E, k, groups, groups == 1 ? 1 : topk_groups, group_top, gsize,
-                      (1u << 20) / static_cast<uint32_t>(gsize) + 1u, per, group_lanes,
+                      (1u << 20) / static_cast<uint32_t>(gsize) + 1u, per, group_shift,
                       full_lanes(E, per) && aligned16(logits) && aligned16(bias), score == DG_SCORE_SOFTMAX, renorm != 0,
                       scale};
-    const int64_t grid = cdiv64(T, dg::kRouteWarps);
-    const int smem = groups > 1 && !group_lanes ? dg::kRouteWarps * E * static_cast<int>(sizeof(float)) : 0;
+    const int64_t grid = route_grid(T);
+    if (grid == 0) return fail(DG_ERR_CUDA, "no CUDA device");
+    const int smem = groups > 1 && group_shift < 0 ? dg::kRouteWarps * E * static_cast<int>(sizeof(float)) : 0;
     return logits_dtype == DG_DTYPE_BF16 ? launch_route<uint16_t>(p, grid, smem, stream)
                                          : launch_route<float>(p, grid, smem, stream);
 }
@@ -1339,7 +1349,8 @@ dg_status dg_route_topk_bwd(void* dlogits, const float* dw, const void* logits, 
     dg::RouteBwdParams p{dlogits, dw, logits, topk_idx, T, E, k, per,
                          full_lanes(E, per) && aligned16(logits) && aligned16(dlogits), score == DG_SCORE_SOFTMAX,
                          renorm != 0, scale};
-    const int64_t grid = cdiv64(T, dg::kRouteWarps);
+    const int64_t grid = route_grid(T);
+    if (grid == 0) return fail(DG_ERR_CUDA, "no CUDA device");
     return logits_dtype == DG_DTYPE_BF16 ? launch_route_bwd<uint16_t>(p, grid, stream)
                                          : launch_route_bwd<float>(p, grid, stream);
 }
@@ -1348,7 +1359,7 @@ int dg_get_layout_rows(int T, int k, int E) {
     if (T < 0 || k <= 0 || k > kMaxSlots || E <= 0 || E > dg::kRouteMaxExperts) return -1;
     const int64_t S = static_cast<int64_t>(T) * k;
     const int64_t rows = (S + 127 * (S < E ? S : E)) / 128 * 128;
-    return S <= 0x7FFFFFFF && rows <= 0x7FFFFFFF ? static_cast<int>(rows) : -1;
+    return S <= kMaxSlotCount && rows <= 0x7FFFFFFF ? static_cast<int>(rows) : -1;
 }
 
 dg_status dg_route_layout(int32_t* row_of, int32_t* m_indices, int32_t* slot_of, int32_t* group_offsets,
@@ -1371,14 +1382,25 @@ dg_status dg_route_layout(int32_t* row_of, int32_t* m_indices, int32_t* slot_of,
     if (!aligned(row_of, 4) || !aligned(m_indices, 4) || !aligned(slot_of, 4) || !aligned(group_offsets, 4) ||
         !aligned(counts, 4) || !aligned(topk_idx, 4))
         return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements");
-    // One CTA per 1024 slots, up to a cluster of 8.
+    // One CTA per 1024 slots or 8192 rows, up to a cluster of 8.
     int ctas = 1;
-    while (ctas < dg::kLayoutMaxCluster && S > static_cast<int64_t>(ctas) * 1024) ctas *= 2;
-    const int64_t warps = static_cast<int64_t>(ctas) * dg::kLayoutWarps;
-    dg::LayoutParams p{topk_idx, row_of, m_indices, slot_of, group_offsets, counts, S, cdiv64(cdiv64(S, warps), 32) * 32,
-                       E, rows, max_rows};
-    return launch_plain(dg::route_layout_kernel, p, ctas, dg::kLayoutThreads,
-                        dg::layout_smem_ints(E) * static_cast<int>(sizeof(int)), ctas, stream);
+    while (ctas < dg::kLayoutMaxCluster && (S > ctas * 1024 || rows > ctas * 8192)) ctas *= 2;
+    int bits = 0;
+    while ((1 << bits) < E) ++bits;
+    dg::LayoutParams p{topk_idx, row_of, m_indices, slot_of, group_offsets, counts, S, 0, 0, E, bits, rows, max_rows};
+    p.warp_slots = cdiv64(cdiv64(S, static_cast<int64_t>(ctas) * dg::kLayoutWarps), 32) * 32;
+    if (p.warp_slots == 0) p.warp_slots = 32;
+    const int64_t warps = cdiv64(cdiv64(S, ctas), p.warp_slots);
+    p.warps = warps < 1 ? 1 : static_cast<int>(warps);
+    const int64_t cta_slots = p.warps * p.warp_slots;
+    const int64_t staged = cta_slots <= dg::kLayoutMaxStaged ? cta_slots : 0;
+    int64_t smem = 4ll * dg::layout_smem_ints(E, p.warps, static_cast<int>(staged));
+    const bool fits = staged > 0 && smem <= 220 * 1024;
+    if (!fits) smem = 4ll * dg::layout_smem_ints(E, p.warps, 0);
+    return launch_plain(!fits                                       ? dg::route_layout_kernel<dg::kLayoutDirect>
+                        : p.warp_slots <= 32 * dg::kLayoutHeld ? dg::route_layout_kernel<dg::kLayoutHeldRun>
+                                                                    : dg::route_layout_kernel<dg::kLayoutStaged>,
+                        p, ctas, dg::kLayoutThreads, static_cast<int>(smem), ctas, stream);
 }
 
 dg_status dg_dispatch_fp8_1x128(uint8_t* Q, float* sa, int sa_stride, const uint16_t* X, const int32_t* row_of, int T,
@@ -1394,11 +1416,15 @@ dg_status dg_dispatch_fp8_1x128(uint8_t* Q, float* sa, int sa_stride, const uint
         return fail(DG_ERR_MISALIGNED, "X and Q must be 16-byte aligned, sa and row_of 4-byte aligned");
     const int sms = effective_sms();
     if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
-    dg::DispatchParams p{Q, sa, X, row_of, T, k, K, K / dg::kBK, sa_stride, group_rows, rows, 0};
-    const int64_t groups = cdiv64(T, dg::kCastRowsPerCta), cap = static_cast<int64_t>(sms) * 8;
-    // Four K blocks at a time while that still gives every SM a CTA, else one.
-    const bool wide = groups * cdiv(p.nkb, 4) >= sms;
-    const int64_t items = groups * (wide ? cdiv(p.nkb, 4) : p.nkb), grid = items < cap ? items : cap;
+    dg::DispatchParams p{Q, sa, X, row_of, T, k, K, K / dg::kBK, sa_stride, group_rows, rows, 0, 0};
+    // Four K blocks to a half-warp while that still gives every SM a CTA, else one.
+    const bool wide = static_cast<int64_t>(T) * cdiv(p.nkb, 4) >= static_cast<int64_t>(sms) * dg::kCastRowsPerCta;
+    const int nb = wide ? 4 : 1;
+    int span = 1;
+    while (span < dg::kCastRowsPerCta && span * nb < p.nkb) span *= 2;
+    p.tokens = dg::kCastRowsPerCta / span;
+    const int64_t items = cdiv64(T, p.tokens) * cdiv(p.nkb, nb * span), cap = static_cast<int64_t>(sms) * 8;
+    const int64_t grid = items < cap ? items : cap;
     if (items > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED, "problem too large");
     p.items = static_cast<uint32_t>(items);
     return wide ? launch_plain(dg::dispatch_1x128_kernel<4>, p, grid, dg::kCastThreads, 0, 1, stream)

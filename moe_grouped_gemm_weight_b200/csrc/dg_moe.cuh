@@ -125,12 +125,14 @@ struct DispatchParams {
     int T, k, K, nkb;
     int sa_stride, group_rows;
     int rows;
+    int tokens;            // tokens per CTA and step: 1, 2, 4, 8 or 16
     uint32_t items;        // token groups times K block groups
 };
 
 // The cast of dg_cast.cuh's cast_1x128_kernel, a token read and cast once and
-// written to each of its k rows: half-warp h of a CTA takes a token, NB K
-// blocks at a time.  Lane j of the half-warp keeps the token's rows j and
+// written to each of its k rows: a half-warp of a CTA takes NB K blocks of a
+// token, as many half-warps side by side as the token has blocks for, so that
+// the copies of a row are written in long runs.  Lane j of the half-warp keeps the token's rows j and
 // j + 16 and writes their scales.
 template <int NB>
 __global__ void __launch_bounds__(kCastThreads)
@@ -139,11 +141,12 @@ dispatch_1x128_kernel(const DispatchParams p) {
     griddep_launch_dependents();
     const int half = threadIdx.x >> 4, hl = threadIdx.x & 15;
     const int base = threadIdx.x & 16;  // first lane of this half-warp
-    const uint32_t kb_groups = (p.nkb + NB - 1) / NB;
+    const int span = kCastRowsPerCta / p.tokens;  // half-warps side by side on a token
+    const uint32_t kb_groups = (p.nkb + NB * span - 1) / (NB * span);
     for (uint32_t it = blockIdx.x; it < p.items; it += gridDim.x) {
         const uint32_t tg = it / kb_groups;
-        const int t = static_cast<int>(tg) * kCastRowsPerCta + half;
-        const int kb0 = static_cast<int>(it - tg * kb_groups) * NB;
+        const int t = static_cast<int>(tg) * p.tokens + half / span;
+        const int kb0 = (static_cast<int>(it - tg * kb_groups) * span + half % span) * NB;
         const bool there = t < p.T;
         const uint16_t* xr = p.X + static_cast<int64_t>(t) * p.K + kb0 * 128 + hl * 8;
         uint4 v[NB];

@@ -15,6 +15,7 @@
 namespace dg {
 
 constexpr int kRouteWarps = 8;
+constexpr int kRouteCtas = 4;        // resident per SM (up to 256 experts)
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxK = 16;       // lanes 0..k hold the k choices and the runner-up
 constexpr int kRouteMaxGroups = 32;  // one lane at least per group
@@ -30,7 +31,7 @@ struct RouteParams {
     int gsize;            // E / groups
     uint32_t gsize_magic; // e / gsize == (e * gsize_magic) >> 20 for e < 1024
     int per;              // experts per lane: lane i holds i * per .. i * per + per - 1
-    int group_lanes;      // lanes per group where groups are whole lanes (a power of two), else 0
+    int group_shift;      // log2 of the lanes per group where groups are whole lanes, else -1
     int vec;              // every lane full, rows and bias 16-byte aligned: wide loads
     int softmax, renorm;
     float scale;
@@ -239,7 +240,7 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const L* row) {
 // whether this lane's group is kept.
 template <typename L>
 __device__ __noinline__ bool keep_groups_exact(const RouteParams& p, const L* row, int e1, int e2) {
-    const int lane = threadIdx.x & 31, g = lane / p.group_lanes;
+    const int lane = threadIdx.x & 31, lanes = 1 << p.group_shift, g = lane >> p.group_shift;
     double m = 0.0, z = 1.0;
     if (p.softmax) {
         m = -INFINITY;
@@ -258,7 +259,7 @@ __device__ __noinline__ bool keep_groups_exact(const RouteParams& p, const L* ro
         v[i] = (p.softmax ? exp(l - m) / z : 1.0 / (1.0 + exp(-l))) + (p.bias ? static_cast<double>(p.bias[e]) : 0.0);
     }
     double a = fmax(v[0], v[1]), b = fmin(v[0], v[1]);
-    for (int o = p.group_lanes >> 1; o >= 1; o >>= 1) {
+    for (int o = lanes >> 1; o >= 1; o >>= 1) {
         const double xa = __shfl_xor_sync(0xffffffffu, a, o), xb = __shfl_xor_sync(0xffffffffu, b, o);
         b = fmax(fmax(b, xb), fmin(a, xa));
         a = fmax(a, xa);
@@ -267,7 +268,7 @@ __device__ __noinline__ bool keep_groups_exact(const RouteParams& p, const L* ro
     if (g >= p.groups) sum = -INFINITY;
     int rank = 0;
     for (int h = 0; h < p.groups; ++h) {
-        const double o = __shfl_sync(0xffffffffu, sum, h * p.group_lanes);
+        const double o = __shfl_sync(0xffffffffu, sum, h * lanes);
         rank += (o > sum || (o == sum && h < g)) ? 1 : 0;
     }
     return sum != -INFINITY && rank < p.keep;
@@ -299,20 +300,60 @@ __device__ __noinline__ int rank_candidates(const RouteParams& p, const L* row, 
     return rank;
 }
 
-// One warp per token, lane i holding the experts i * per ...
+// The four largest of a lane's keys in falling order.
+struct Top4 {
+    int k[4];
+    static __device__ __forceinline__ void order(int& a, int& b) {
+        const int hi = max(a, b);
+        b = min(a, b);
+        a = hi;
+    }
+    template <int N>
+    __device__ __forceinline__ void of(const int (&key)[N]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = i < N ? key[i] : kNoKey;
+        if (N > 1) order(k[0], k[1]);
+        if (N > 2) {
+            order(k[2], k[3]);
+            order(k[0], k[2]);
+            order(k[1], k[3]);
+            order(k[1], k[2]);
+        }
+#pragma unroll
+        for (int q = 4; q < N; q += 4) {
+            int o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = key[q + i];
+            order(o[0], o[1]);
+            order(o[2], o[3]);
+            order(o[0], o[2]);
+            order(o[1], o[3]);
+            order(o[1], o[2]);
+            // the four largest of both, then in order
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = max(k[i], o[3 - i]);
+            order(k[0], k[2]);
+            order(k[1], k[3]);
+            order(k[0], k[1]);
+            order(k[2], k[3]);
+        }
+    }
+};
+
+// Warps take tokens in turn, a token to a warp, lane i holding the experts
+// i * per ..; the next token's logits are on their way meanwhile.
 //
 // The choice works on keys: a value's leading bits in integer order, and in
 // its low bits the expert's place (lane, then place in the lane, counted down),
 // so that a maximum of keys is a value, its expert and the rule for ties at
-// once.  A key costs three instructions, keeping a lane's two largest three
-// more, and a round of the choice one warp-wide maximum.  The k experts so
-// found are the right set where the (k+1)-th key is clearly below; their order
-// is decided by their FP32 values, and by FP64 values where those are not
-// clearly apart.  bf16 logits without a bias fit a key whole.
-//
-// Bound by instructions: 16384 tokens of 256 float32 logits are 2.6 us of HBM.
+// once.  A key costs three instructions, a lane's four largest in order four
+// more, and a round of the choice one warp-wide maximum and a shift.  Where
+// every chosen key is clearly above the next, the (k+1)-th included, the keys'
+// order is the exact one.  Elsewhere the candidates are ordered by their FP32
+// values, and by FP64 values where those are not clearly apart.  bf16 logits
+// without a bias fit a key whole.
 template <int EPL, typename L>
-__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? 4 : 1)
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteCtas : 1)
 route_topk_kernel(const RouteParams p) {
     constexpr int kMask = 32 * EPL - 1;  // a key's place bits
     constexpr bool kShort = sizeof(L) == 2;
@@ -321,261 +362,267 @@ route_topk_kernel(const RouteParams p) {
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-    if (t >= p.T) return;
-    const L* row = static_cast<const L*>(p.logits) + t * p.E;
     const int e0 = lane * p.per;
     const bool biased = p.bias != nullptr;
+    const int lane_bits = (31 - lane) * EPL;
+    const int stride = gridDim.x * kRouteWarps;
+    int t = blockIdx.x * kRouteWarps + warp;
+    if (t >= p.T) return;
 
-    float v[EPL];  // logits, then (with a bias) choice values; -inf: not eligible
-    if (p.vec) {
-        load_logits<EPL>(row + lane * EPL, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) v[i] = i < p.per && e0 + i < p.E ? logit_at(row + e0 + i) : -INFINITY;
-    }
-    float mx = 0.f, rz = 1.f;
-    if (p.softmax) {
-        float m = v[0];
-#pragma unroll
-        for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
-        mx = warp_max(m);
-        float z = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) z += exp_fast(v[i] - mx);
-        rz = 1.f / warp_sum(z);
-    }
-    // FP32 moves a choice value by less than `slack` (of the largest score:
-    // exponential, sum and reciprocal of a softmax 2^-20, sigmoid_fast 2^-22),
-    // and adding the bias by 2^-24 of the value.
-    const float slack = p.softmax ? rz * 0x1p-20f : 0x1p-22f;
-    auto apart_by = [&](float x, float y) {  // more than FP32 can have moved x - y
-        return biased ? 2.f * slack + 0x1p-22f * (fabsf(x) + fabsf(y)) : 0.f;
-    };
-    auto score = [&](float x) { return p.softmax ? exp_fast(x - mx) * rz : sigmoid_fast(x); };
-
-    if (biased) {
-        float b[EPL];
+    auto load = [&](int token, float (&v)[EPL]) {
+        const L* row = static_cast<const L*>(p.logits) + static_cast<int64_t>(token) * p.E;
         if (p.vec) {
-            load_logits<EPL>(p.bias + lane * EPL, b);
+            load_logits<EPL>(row + lane * EPL, v);
         } else {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) b[i] = i < p.per && e0 + i < p.E ? p.bias[e0 + i] : -INFINITY;
+            for (int i = 0; i < EPL; ++i) v[i] = i < p.per && e0 + i < p.E ? logit_at(row + e0 + i) : -INFINITY;
         }
-        float low = v[0];
-#pragma unroll
-        for (int i = 1; i < EPL; ++i) low = fminf(low, v[i]);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) b[i] += score(v[i]);
-        if (low == -INFINITY) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) b[i] = v[i] == -INFINITY ? -INFINITY : b[i];
-        }
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) v[i] = b[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) v[i] += 0.f;  // one zero
-    }
-    // A NaN, or an infinite choice value: to be decided without shortcuts.
-    float all = v[0];
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) all += v[i];
-    const bool inf_ok = !biased && !p.softmax;
-    bool odd = inf_ok ? all != all : !(all < INFINITY) || (rz != rz && mx != -INFINITY);
-    odd = __any_sync(0xffffffffu, odd);
-
-    bool in = true, sure = true;  // in: the lane's experts take part
-    if (p.groups > 1 && !odd) {
-        float a = -INFINITY, b = -INFINITY;  // the two best choice values of the group
-        int g, lanes;                        // this lane's group, lanes per group
-        // A choice value without a bias is the score of the logit.
-        auto choice = [&](float x) { return x == -INFINITY || biased ? x : score(x); };
-        if (p.group_lanes) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                b = fmaxf(b, fminf(a, v[i]));
-                a = fmaxf(a, v[i]);
-            }
-            a = choice(a);
-            b = choice(b);
-            lanes = p.group_lanes;
-            g = lane / lanes;
+    };
+    float bias[EPL], fetched[EPL];
+    load(t, fetched);
+    if (biased) {
+        if (p.vec) {
+            load_logits<EPL>(p.bias + lane * EPL, bias);
         } else {
-            // A power of two of lanes share a group in shared memory.
-            float* cs = route_smem + warp * p.E;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (i < p.per && e0 + i < p.E) cs[e0 + i] = choice(v[i]);
-            __syncwarp();
-            const int sh = 31 - __clz(32 / p.groups);
-            g = lane >> sh;
-            lanes = 1 << sh;
-            if (g < p.groups) {
-                const int sub = lane & (lanes - 1);
-                // Each group starts at another place: the same places of groups of 32 share a bank.
-                const int turn = (g << sh) % p.gsize;
-                for (int n = sub; n < p.gsize; n += lanes) {
-                    const float x = cs[g * p.gsize + (n + turn < p.gsize ? n + turn : n + turn - p.gsize)];
-                    b = fmaxf(b, fminf(a, x));
-                    a = fmaxf(a, x);
-                }
-            }
-        }
-        for (int o = lanes >> 1; o >= 1; o >>= 1) {
-            const float xa = __shfl_xor_sync(0xffffffffu, a, o), xb = __shfl_xor_sync(0xffffffffu, b, o);
-            b = fmaxf(fmaxf(b, xb), fminf(a, xa));
-            a = fmaxf(a, xa);
-        }
-        float sum = a + (p.gtop == 2 && b != -INFINITY ? b : 0.f);
-        if (g >= p.groups) sum = -INFINITY;
-        int rank = 0;
-        for (int h = 0; h < p.groups; ++h) {
-            const float o = __shfl_sync(0xffffffffu, sum, h * lanes);
-            rank += (o > sum || (o == sum && h < g)) ? 1 : 0;
-        }
-        bool kept = sum != -INFINITY && rank < p.keep;
-        // Certain when the worst kept group and the best other are clearly apart.
-        const float lo = warp_min(kept ? sum : INFINITY), hi = warp_max(kept ? -INFINITY : sum);
-        if (hi != -INFINITY && !(lo - hi > 4.f * slack + 0x1p-21f * (fabsf(lo) + fabsf(hi)))) {
-            // The lane's two best, if no third can take their place in FP64.
-            float b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
-            int e1 = -1, e2 = -1;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const bool first = v[i] > b1, second = v[i] > b2;
-                b3 = fmaxf(b3, fminf(b2, v[i]));
-                e2 = first ? e1 : second ? e0 + i : e2;
-                e1 = first ? e0 + i : e1;
-                b2 = fmaxf(b2, fminf(b1, v[i]));
-                b1 = fmaxf(b1, v[i]);
-            }
-            const bool two = b3 == -INFINITY || b2 - b3 > apart_by(b2, b3) || (!biased && b2 == b3);
-            if (p.group_lanes && __all_sync(0xffffffffu, two)) kept = keep_groups_exact<L>(p, row, e1, e2);
-            else sure = false;
-        }
-        if (p.group_lanes) {
-            in = kept;
-        } else {
-            const uint32_t on = __ballot_sync(0xffffffffu, kept);
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const uint32_t grp = (static_cast<uint32_t>(e0 + i) * p.gsize_magic) >> 20;
-                if (!((on >> ((grp * lanes) & 31u)) & 1u)) v[i] = -INFINITY;
-            }
+            for (int i = 0; i < EPL; ++i) bias[i] = i < p.per && e0 + i < p.E ? p.bias[e0 + i] : -INFINITY;
         }
     }
 
-    int my = -1, slot = lane;
-    if (sure && !odd) {
-        // Keys: without the lane's bits, which the lane's own order does not need.
-        const int lane_bits = (31 - lane) * EPL;
-        int key[EPL], k1 = kNoKey, k2 = kNoKey;
+    for (; t < p.T; t += stride) {
+        const L* row = static_cast<const L*>(p.logits) + static_cast<int64_t>(t) * p.E;
+        float v[EPL];  // logits, then (with a bias) choice values; -inf: not eligible
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            key[i] = (ordered_int(v[i]) & ~kMask) | (EPL - 1 - i);
-            k2 = max(k2, min(k1, key[i]));
-            k1 = max(k1, key[i]);
-        }
-        if (in) {
-            k1 |= lane_bits;
-            k2 |= lane_bits;
-        } else {
-            k1 = k2 = kNoKey;
-        }
-        // k rounds, one more for the runner-up.
-        int my_key = kNoKey;
-        bool two = true;  // k2 is the lane's second largest
-        for (int j = 0; j <= p.k; ++j) {
-            const int top = __reduce_max_sync(0xffffffffu, k1);
-            if (top < kLeastKey) break;
-            if (lane == j) my_key = top;
-            if (k1 == top) {
-                if (two) {
-                    k1 = k2;
-                    two = false;
-                } else {
-                    // Look for the largest below it again.
-                    const int below = top ^ lane_bits;
-                    k1 = kNoKey;
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i) k1 = max(k1, key[i] < below ? key[i] : kNoKey);
-                    k1 |= lane_bits;
-                }
-            }
-        }
-        auto expert_of = [&](int k) { return (31 - (k & kMask) / EPL) * p.per + EPL - 1 - (k & (EPL - 1)); };
-        if (my_key >= kLeastKey) my = expert_of(my_key);
+        for (int i = 0; i < EPL; ++i) v[i] = fetched[i];
+        if (p.T - t > stride) load(t + stride, fetched);
 
-        if (!kShort || biased) {
-            int n = p.k;  // candidates: lane j < n holds one, or none
-            bool ranked = true;  // the lanes may not be in order
-            const int last = __shfl_sync(0xffffffffu, my_key, p.k - 1), next = __shfl_sync(0xffffffffu, my_key, p.k);
-            const float x = ordered_float(last & ~kMask), y = ordered_float(next | kMask);
-            if (next >= kLeastKey && !(x - y > apart_by(x, y))) {
-                // All experts that may belong to the k: those not clearly below the k-th.
-                const int least = ordered_int(x - apart_by(x, x)) & ~kMask;
-                n = 0;
+        float mx = 0.f, rz = 1.f;
+        if (p.softmax) {
+            float m = v[0];
+#pragma unroll
+            for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
+            mx = warp_max(m);
+            float z = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) z += exp_fast(v[i] - mx);
+            rz = 1.f / warp_sum(z);
+        }
+        // FP32 moves a choice value by less than `slack` (of the largest score:
+        // exponential, sum and reciprocal of a softmax 2^-20, sigmoid_fast 2^-22),
+        // and adding the bias by 2^-24 of the value.
+        const float slack = p.softmax ? rz * 0x1p-20f : 0x1p-22f;
+        auto apart_by = [&](float x, float y) {  // more than FP32 can have moved x - y
+            return biased ? 2.f * slack + 0x1p-22f * (fabsf(x) + fabsf(y)) : 0.f;
+        };
+        auto score = [&](float x) { return p.softmax ? exp_fast(x - mx) * rz : sigmoid_fast(x); };
+
+        if (biased) {
+            float low = v[0];
+#pragma unroll
+            for (int i = 1; i < EPL; ++i) low = fminf(low, v[i]);
+            if (low == -INFINITY) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) v[i] = v[i] == -INFINITY ? -INFINITY : score(v[i]) + bias[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) v[i] = score(v[i]) + bias[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) v[i] += 0.f;  // one zero
+        }
+        // A NaN, or an infinite choice value: to be decided without shortcuts.
+        float all = v[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) all += v[i];
+        bool odd = !biased && !p.softmax ? all != all : !(all < INFINITY) || (rz != rz && mx != -INFINITY);
+        odd = __any_sync(0xffffffffu, odd);
+
+        bool in = true, sure = !odd;  // in: the lane's experts take part
+        if (p.groups > 1 && sure) {
+            float a = -INFINITY, b = -INFINITY;  // the two best choice values of the group
+            int g, sh;                           // this lane's group, log2 of lanes per group
+            // A choice value without a bias is the score of the logit.
+            auto choice = [&](float x) { return x == -INFINITY || biased ? x : score(x); };
+            if (p.group_shift >= 0) {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
-                    const bool c = in && key[i] >= least && key[i] >= kLeastKey;
-                    const uint32_t who = __ballot_sync(0xffffffffu, c);
-                    const int at = n + __popc(who & ((1u << lane) - 1u));
-                    if (c && at < 32) cand_smem[warp][at] = static_cast<uint16_t>(e0 + i);
-                    n += __popc(who);
+                    b = fmaxf(b, fminf(a, v[i]));
+                    a = fmaxf(a, v[i]);
                 }
+                a = choice(a);
+                b = choice(b);
+                sh = p.group_shift;
+                g = lane >> sh;
+            } else {
+                // A power of two of lanes share a group in shared memory.
+                float* cs = route_smem + warp * p.E;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (i < p.per && e0 + i < p.E) cs[e0 + i] = choice(v[i]);
                 __syncwarp();
-                ranked = false;
-                if (n > 32) {
-                    sure = false;
-                } else {
-                    my = lane < n ? cand_smem[warp][lane] : -1;
+                sh = 31 - __clz(32 / p.groups);
+                g = lane >> sh;
+                if (g < p.groups) {
+                    const int lanes = 1 << sh, sub = lane & (lanes - 1);
+                    // Each group starts at another place: the same places of groups of 32 share a bank.
+                    const int turn = (g << sh) % p.gsize;
+                    for (int n = sub; n < p.gsize; n += lanes) {
+                        const float x = cs[g * p.gsize + (n + turn < p.gsize ? n + turn : n + turn - p.gsize)];
+                        b = fmaxf(b, fminf(a, x));
+                        a = fmaxf(a, x);
+                    }
                 }
             }
-            // The candidates' values: lane order holds if every one is clearly above the next.
-            const bool some = lane < n && my >= 0;
-            const float l = some ? logit_at(row + my) : 0.f, b = some && biased ? p.bias[my] : 0.f;
-            const float c = !some ? -INFINITY : biased ? score(l) + b : l;
-            if (sure) {
-                const float below = __shfl_down_sync(0xffffffffu, c, 1);
-                const int below_e = __shfl_down_sync(0xffffffffu, my, 1);
-                const bool last_one = lane + 1 >= n || below_e < 0 || !some;
-                const bool good = last_one || c - below > apart_by(c, below) || (!biased && c == below && my < below_e);
-                if (!ranked || !__all_sync(0xffffffffu, good)) {
-                    int rank = 0;
-                    bool near = false;
-                    for (int h = 0; h < n; ++h) {
-                        const float o = __shfl_sync(0xffffffffu, c, h);
-                        const int oe = __shfl_sync(0xffffffffu, my, h);
-                        const float ol = __shfl_sync(0xffffffffu, l, h), ob = __shfl_sync(0xffffffffu, b, h);
-                        rank += (o > c || (o == c && oe < my)) ? 1 : 0;
-                        // Equal because both logit and bias are: the lower index is right.
-                        near |= some && oe >= 0 && oe != my && !(fabsf(o - c) > apart_by(o, c)) && !(ol == l && ob == b);
-                    }
-                    if (biased && __any_sync(0xffffffffu, near)) {
-                        const int m = __popc(__ballot_sync(0xffffffffu, some));  // lanes 0 .. m - 1
-                        rank = rank_candidates<EPL, L>(p, row, m, my);
-                    }
-                    slot = some ? rank : lane < p.k ? lane : 32;  // lanes behind the last expert keep their place
+            for (int o = 1 << sh >> 1; o >= 1; o >>= 1) {
+                const float xa = __shfl_xor_sync(0xffffffffu, a, o), xb = __shfl_xor_sync(0xffffffffu, b, o);
+                b = fmaxf(fmaxf(b, xb), fminf(a, xa));
+                a = fmaxf(a, xa);
+            }
+            float sum = a + (p.gtop == 2 && b != -INFINITY ? b : 0.f);
+            if (g >= p.groups) sum = -INFINITY;
+            // The best groups, one value (mostly one group) a round.
+            bool kept = false;
+            float lo = -INFINITY, hi = warp_max(sum);
+            int n = 0;
+            while (n < p.keep && hi != -INFINITY) {
+                lo = hi;
+                kept |= sum == hi;
+                n = __popc(__ballot_sync(0xffffffffu, kept)) >> sh;
+                hi = warp_max(kept ? -INFINITY : sum);
+            }
+            // Certain when the worst kept group and the best other are clearly apart.
+            if (n > p.keep || (hi != -INFINITY && !(lo - hi > 4.f * slack + 0x1p-21f * (fabsf(lo) + fabsf(hi))))) {
+                // The lane's two best, if no third can take their place in FP64.
+                float b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
+                int e1 = -1, e2 = -1;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const bool first = v[i] > b1, second = v[i] > b2;
+                    b3 = fmaxf(b3, fminf(b2, v[i]));
+                    e2 = first ? e1 : second ? e0 + i : e2;
+                    e1 = first ? e0 + i : e1;
+                    b2 = fmaxf(b2, fminf(b1, v[i]));
+                    b1 = fmaxf(b1, v[i]);
+                }
+                const bool two = b3 == -INFINITY || b2 - b3 > apart_by(b2, b3) || (!biased && b2 == b3);
+                if (p.group_shift >= 0 && __all_sync(0xffffffffu, two)) kept = keep_groups_exact<L>(p, row, e1, e2);
+                else sure = false;
+            }
+            if (p.group_shift >= 0) {
+                in = kept;
+            } else {
+                const uint32_t on = __ballot_sync(0xffffffffu, kept);
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const uint32_t grp = (static_cast<uint32_t>(e0 + i) * p.gsize_magic) >> 20;
+                    if (!((on >> ((grp << sh) & 31u)) & 1u)) v[i] = -INFINITY;
                 }
             }
         }
-    }
-    if (odd || !sure) {
-        my = choose_exact<EPL, L>(p, row);
-        slot = lane;
-    }
 
-    const bool chosen = slot < p.k;
-    float s = 0.f;
-    if (chosen && my >= 0) {
-        const float x = logit_at(row + my);
-        s = p.softmax ? expf(x - mx) * rz : sigmoid_f(x);
-    }
-    if (p.renorm) s = __fdividef(s, warp_sum(s) + kRouteEps);
-    if (chosen) {
-        p.idx[t * p.k + slot] = my;
-        p.w[t * p.k + slot] = s * p.scale;
+        int my = -1, slot = lane;
+        if (sure) {
+            // Keys without the lane's bits, which the lane's own order does not need.
+            int key[EPL];
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) key[i] = (ordered_int(v[i]) & ~kMask) | (EPL - 1 - i);
+            Top4 top;
+            top.of(key);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top.k[i] = in ? top.k[i] | lane_bits : kNoKey;
+            // k rounds, one more for the runner-up.
+            int my_key = kNoKey;
+            const bool deep = EPL > 4 && top.k[3] >= kLeastKey;  // a fifth key may follow
+            for (int j = 0; j <= p.k; ++j) {
+                const int best = __reduce_max_sync(0xffffffffu, top.k[0]);
+                my_key = lane == j ? best : my_key;
+                const bool won = top.k[0] == best;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) top.k[i] = won ? top.k[i + 1] : top.k[i];
+                top.k[3] = won ? kNoKey : top.k[3];
+            }
+            if (EPL > 4 && __any_sync(0xffffffffu, deep && top.k[0] < kLeastKey)) {
+                // A lane gave all four: the rounds again, each looking through the lane's keys.
+                int below = 0x7FFFFFFF;
+                for (int j = 0; j <= p.k; ++j) {
+                    int k1 = kNoKey;
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) k1 = max(k1, key[i] < below ? key[i] : kNoKey);
+                    k1 = in ? k1 | lane_bits : kNoKey;
+                    const int best = __reduce_max_sync(0xffffffffu, k1);
+                    my_key = lane == j ? best : my_key;
+                    if (k1 == best) below = k1 ^ lane_bits;
+                }
+            }
+            if (my_key >= kLeastKey && lane <= p.k) my = (31 - (my_key & kMask) / EPL) * p.per + EPL - 1 - (my_key & (EPL - 1));
+
+            if (!kShort || biased) {
+                // Every chosen key clearly above the next, whatever its low bits hide?
+                const int next = __shfl_down_sync(0xffffffffu, my_key, 1);
+                const float x = ordered_float(my_key & ~kMask), y = ordered_float(next | kMask);
+                const bool clear = lane >= p.k || next < kLeastKey || x - y > apart_by(x, y);
+                if (!__all_sync(0xffffffffu, clear)) {
+                    int n = p.k;  // candidates: lane j < n holds one, or none
+                    if (!__shfl_sync(0xffffffffu, clear, p.k - 1)) {
+                        // All experts that may belong to the k: those not clearly below the k-th.
+                        const float last = __shfl_sync(0xffffffffu, x, p.k - 1);
+                        const int least = ordered_int(last - apart_by(last, last)) & ~kMask;
+                        n = 0;
+#pragma unroll
+                        for (int i = 0; i < EPL; ++i) {
+                            const bool c = in && key[i] >= least && key[i] >= kLeastKey;
+                            const uint32_t who = __ballot_sync(0xffffffffu, c);
+                            const int at = n + __popc(who & ((1u << lane) - 1u));
+                            if (c && at < 32) cand_smem[warp][at] = static_cast<uint16_t>(e0 + i);
+                            n += __popc(who);
+                        }
+                        __syncwarp();
+                        my = lane < n && lane < 32 ? cand_smem[warp][lane] : -1;
+                        __syncwarp();
+                    }
+                    if (n > 32) {
+                        sure = false;
+                    } else {
+                        // By FP32 value; equal ones that are so because both logit and bias are, by index.
+                        const bool some = lane < n && my >= 0;
+                        const float l = some ? logit_at(row + my) : 0.f, b = some && biased ? p.bias[my] : 0.f;
+                        const float c = !some ? -INFINITY : biased ? score(l) + b : l;
+                        int rank = 0;
+                        bool near = false;
+                        for (int h = 0; h < n; ++h) {
+                            const float o = __shfl_sync(0xffffffffu, c, h);
+                            const int oe = __shfl_sync(0xffffffffu, my, h);
+                            const float ol = __shfl_sync(0xffffffffu, l, h), ob = __shfl_sync(0xffffffffu, b, h);
+                            rank += (o > c || (o == c && oe < my)) ? 1 : 0;
+                            near |= some && oe >= 0 && oe != my && !(fabsf(o - c) > apart_by(o, c)) && !(ol == l && ob == b);
+                        }
+                        if (biased && __any_sync(0xffffffffu, near)) {
+                            const int m = __popc(__ballot_sync(0xffffffffu, some));  // lanes 0 .. m - 1
+                            rank = rank_candidates<EPL, L>(p, row, m, my);
+                        }
+                        slot = some ? rank : lane < p.k ? lane : 32;  // lanes behind the last expert keep their place
+                    }
+                }
+            }
+        }
+        if (!sure) {
+            my = choose_exact<EPL, L>(p, row);
+            slot = lane;
+        }
+
+        const bool chosen = slot < p.k;
+        float s = 0.f;
+        if (chosen && my >= 0) {
+            const float x = logit_at(row + my);
+            s = p.softmax ? expf(x - mx) * rz : sigmoid_f(x);
+        }
+        if (p.renorm) s = __fdividef(s, warp_sum(s) + kRouteEps);
+        if (chosen) {
+            const int64_t at = static_cast<int64_t>(t) * p.k + slot;
+            p.idx[at] = my;
+            p.w[at] = s * p.scale;
+        }
     }
 }
 
@@ -631,92 +678,118 @@ __device__ __forceinline__ void store_logits(uint16_t* p, const float (&f)[N]) {
 // w_j = scale s_j (/ S, S = sum_j s_j + eps):  ds_j = scale dw_j, or
 // scale/S (dw_j - sum_i dw_i s_i / S).  Sigmoid: dl = ds s (1 - s) at the
 // chosen experts, zero elsewhere; softmax: dl_e = s_e (ds_e - sum_j ds_j s_j).
-// One warp per token; only softmax reads the whole row.  The k gradients meet
-// their experts through a row of shared memory.
+// Warps take tokens in turn; only softmax reads the whole row.  The k gradients
+// meet their experts through a row of shared memory.  What the next token needs
+// is on its way meanwhile.
 template <int EPL, typename L>
-__global__ void __launch_bounds__(kRouteWarps * 32)
+__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteCtas : 1)
 route_topk_bwd_kernel(const RouteBwdParams p) {
     extern __shared__ __align__(16) float route_smem[];  // 32 * EPL values per warp
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-    if (t >= p.T) return;
-    const L* row = static_cast<const L*>(p.logits) + t * p.E;
-    L* out = static_cast<L*>(p.dlogits) + t * p.E;
     const int e0 = lane * p.per;
+    float* line = route_smem + warp * 32 * EPL;
+    const int stride = gridDim.x * kRouteWarps;
+    int t = blockIdx.x * kRouteWarps + warp;
+    if (t >= p.T) return;
 
-    int e = -1;
-    float g = 0.f, x = 0.f;
-    if (lane < p.k) {
-        e = p.idx[t * p.k + lane];
-        if (e < 0 || e >= p.E) e = -1;
-        else x = logit_at(row + e);
-        g = e < 0 ? 0.f : p.dw[t * p.k + lane] * p.scale;
-    }
-    float d[EPL];
-    float mx = 0.f, rz = 1.f;
-    if (p.softmax) {
+    int next_e = -1;
+    float next_g = 0.f, next_d[EPL];
+    auto load = [&](int token) {
+        if (lane < p.k) {
+            next_e = p.idx[static_cast<int64_t>(token) * p.k + lane];
+            next_g = p.dw[static_cast<int64_t>(token) * p.k + lane];
+        }
+        if (p.softmax) {
+            const L* row = static_cast<const L*>(p.logits) + static_cast<int64_t>(token) * p.E;
+            if (p.vec) {
+                load_logits<EPL>(row + lane * EPL, next_d);
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) next_d[i] = i < p.per && e0 + i < p.E ? logit_at(row + e0 + i) : -INFINITY;
+            }
+        }
+    };
+    load(t);
+    for (; t < p.T; t += stride) {
+        int e = next_e;
+        float g = next_g * p.scale, d[EPL];
+        if (e < 0 || e >= p.E) {
+            e = -1;
+            g = 0.f;
+        }
+        const int place = e >= 0 ? e / p.per * EPL + e % p.per : 0;  // of the expert in `line`
+        if (p.softmax) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) d[i] = next_d[i];
+        }
+        if (p.T - t > stride) load(t + stride);
+
+        float s = 0.f;
+        if (p.softmax) {
+            float m = d[0];
+#pragma unroll
+            for (int i = 1; i < EPL; ++i) m = fmaxf(m, d[i]);
+            m = warp_max(m);
+            if (m == -INFINITY) m = 0.f;  // every expert masked: no score, no gradient
+            float z = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                d[i] = exp_fast(d[i] - m);
+                z += d[i];
+            }
+            z = warp_sum(z);
+            const float rz = z > 0.f || z != z ? 1.f / z : 0.f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) d[i] *= rz;
+            store_logits<EPL>(line + lane * EPL, d);
+            __syncwarp();
+            if (e >= 0) s = line[place];
+        } else if (e >= 0) {
+            s = sigmoid_f(logit_at(static_cast<const L*>(p.logits) + static_cast<int64_t>(t) * p.E + e));
+        }
+        if (p.renorm) {
+            const float r = 1.f / (warp_sum(s) + kRouteEps);
+            const float mean = warp_sum(g * s) * r;
+            g = e < 0 ? 0.f : (g - mean) * r;
+        }
+        float dot = 0.f;
+        if (p.softmax) dot = warp_sum(g * s);
+        else g *= s * (1.f - s);
+
+        float r[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) r[i] = 0.f;
+        __syncwarp();
+        store_logits<EPL>(line + lane * EPL, r);
+        // An expert in several slots: its first slot takes the sum, in slot order.
+        const uint32_t same = __match_any_sync(0xffffffffu, e >= 0 ? e : -1 - lane);
+        if (__any_sync(0xffffffffu, (same & (same - 1u)) != 0)) {
+            float sum = 0.f;
+            for (int j = 0; j < p.k; ++j) {
+                const float gj = __shfl_sync(0xffffffffu, g, j);
+                if ((same >> j) & 1u) sum += gj;
+            }
+            g = sum;
+        }
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) line[place] = g;
+        __syncwarp();
+        load_logits<EPL>(line + lane * EPL, r);
+        __syncwarp();
+        if (p.softmax) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) r[i] = (r[i] - dot) * d[i];
+        }
+        L* out = static_cast<L*>(p.dlogits) + static_cast<int64_t>(t) * p.E;
         if (p.vec) {
-            load_logits<EPL>(row + lane * EPL, d);
+            store_logits<EPL>(out + lane * EPL, r);
         } else {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) d[i] = i < p.per && e0 + i < p.E ? logit_at(row + e0 + i) : -INFINITY;
+            for (int i = 0; i < EPL; ++i)
+                if (i < p.per && e0 + i < p.E) store_logit(out + e0 + i, r[i]);
         }
-        float m = d[0];
-#pragma unroll
-        for (int i = 1; i < EPL; ++i) m = fmaxf(m, d[i]);
-        mx = warp_max(m);
-        if (mx == -INFINITY) mx = 0.f;  // every expert masked: no score, no gradient
-        float z = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            d[i] = exp_fast(d[i] - mx);
-            z += d[i];
-        }
-        z = warp_sum(z);
-        rz = z > 0.f || z != z ? 1.f / z : 0.f;
-    }
-    float s = 0.f;
-    if (e >= 0) s = p.softmax ? expf(x - mx) * rz : sigmoid_f(x);
-    if (p.renorm) {
-        const float r = 1.f / (warp_sum(s) + kRouteEps);
-        const float mean = warp_sum(g * s) * r;
-        g = e < 0 ? 0.f : (g - mean) * r;
-    }
-    float dot = 0.f;
-    if (p.softmax) dot = warp_sum(g * s);
-    else g *= s * (1.f - s);
-
-    float* line = route_smem + warp * 32 * EPL;
-    float r[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) r[i] = 0.f;
-    store_logits<EPL>(line + lane * EPL, r);
-    // An expert in several slots: its first slot takes the sum, in slot order.
-    const uint32_t same = __match_any_sync(0xffffffffu, e >= 0 ? e : -1 - lane);
-    if (__any_sync(0xffffffffu, (same & (same - 1u)) != 0)) {
-        float sum = 0.f;
-        for (int j = 0; j < p.k; ++j) {
-            const float gj = __shfl_sync(0xffffffffu, g, j);
-            if ((same >> j) & 1u) sum += gj;
-        }
-        g = sum;
-    }
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) line[e / p.per * EPL + e % p.per] = g;
-    __syncwarp();
-    load_logits<EPL>(line + lane * EPL, r);
-    if (p.softmax) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) r[i] = (r[i] - dot) * (d[i] * rz);
-    }
-    if (p.vec) {
-        store_logits<EPL>(out + lane * EPL, r);
-    } else {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (i < p.per && e0 + i < p.E) store_logit(out + e0 + i, r[i]);
     }
 }
 
@@ -725,6 +798,7 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
 constexpr int kLayoutThreads = 1024;
 constexpr int kLayoutWarps = kLayoutThreads / 32;
 constexpr int kLayoutMaxCluster = 8;
+constexpr int kLayoutHeld = 4;  // batches of 32 slots that a warp keeps in registers
 
 struct LayoutParams {
     const int32_t* idx;  // [S] chosen experts, -1: none
@@ -735,96 +809,166 @@ struct LayoutParams {
     int32_t* counts;     // [E]
     int64_t S;
     int64_t warp_slots;  // slots per warp, a multiple of 32
-    int E;
-    int64_t rows;
+    int warps;           // warps of a CTA that have slots
+    int E, expert_bits;  // E <= 1 << expert_bits
+    int rows;
     int max_rows;        // 0: contiguous segments of whole 128 rows; else rows per group
 };
 
-// Stable counting sort of the slots by expert, in one cluster: every warp
-// counts a consecutive run of slots per expert; the counts are scanned over
-// the warps of a CTA, over the CTAs of the cluster (distributed shared memory)
-// and over the experts; then every warp walks its run again and hands out the
-// rows.  No atomics between warps, so rows follow slot order in every run.
-// Shared memory: layout_smem_ints(E) ints.
-__host__ __device__ constexpr int layout_smem_ints(int E) { return (kLayoutWarps + 3) * E + 1 + kLayoutWarps; }
+enum LayoutKind : int {
+    kLayoutHeldRun = 0,  // a warp's run of slots stays in registers
+    kLayoutStaged = 1,   // it is read and ranked again in the second pass
+    kLayoutDirect = 2,   // ... and the CTA's slots do not fit in shared memory
+};
 
+// A CTA's slots are staged as pairs of 16-bit numbers: place in its run, expert.
+constexpr int kLayoutMaxStaged = 65536;
+
+// Shared memory of the layout kernel in ints: counts [warps][E], then [E]
+// totals of this CTA, [E + 1] starts, [E] rows held, [E] first rows of this
+// CTA's slots, [E] their places among its staged slots, [32] pairs of sums, and
+// the staged slots.
+__host__ __device__ constexpr int layout_smem_ints(int E, int warps, int staged) {
+    return (warps + 5) * E + 2 + 2 * kLayoutWarps + staged;
+}
+
+// Stable counting sort of the slots by expert, in one cluster: every warp
+// walks a consecutive run of slots; its counts per expert are scanned over the
+// warps of a CTA, over the CTAs of the cluster (distributed shared memory) and
+// over the experts; a slot's rank among the run's slots of its expert, on top
+// of the scanned count, makes its row.  No atomics between warps, so rows
+// follow slot order in every launch.  The slots pass through shared memory in
+// row order, so that the two arrays by row are written in runs (a 4-byte write
+// on its own costs as much as a whole sector).  Bound by latency: a few
+// barriers and, in each warp, one dependent step per 32 slots.  In that step the
+// lanes of equal expert find one another by a vote per bit of the expert
+// (__match_any_sync took 1300 cycles a batch with 32 warps at it, the votes 300).
+template <int kKind>
 __global__ void __launch_bounds__(kLayoutThreads)
 route_layout_kernel(const LayoutParams p) {
     extern __shared__ int layout_smem[];
-    int* run = layout_smem;                       // [kLayoutWarps][E]
-    int* total = run + kLayoutWarps * p.E;        // [E], read by the other CTAs
-    int* start = total + p.E;                     // [E + 1]
-    int* held = start + p.E + 1;                  // [E] rows of each group that hold a slot
-    int* wsum = held + p.E;                       // [kLayoutWarps]
+    int* run = layout_smem;
+    int* total = run + p.warps * p.E;  // read by the other CTAs
+    int* start = total + p.E;
+    int* held = start + p.E + 1;
+    int* base = held + p.E;
+    int* local_start = base + p.E;
+    unsigned long long* wsum = reinterpret_cast<unsigned long long*>(layout_smem + (((p.warps + 5) * p.E + 2) & ~1));
+    uint32_t* staged = reinterpret_cast<uint32_t*>(wsum + kLayoutWarps);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_ctarank(), nctas = cluster_nctarank();
+    for (int i = tid; i < p.warps * p.E; i += kLayoutThreads) run[i] = 0;
     griddep_wait();
     griddep_launch_dependents();
 
-    for (int i = tid; i < kLayoutWarps * p.E; i += kLayoutThreads) run[i] = 0;
-    __syncthreads();
-    const int64_t s0 = (static_cast<int64_t>(rank) * kLayoutWarps + warp) * p.warp_slots;
-    const int64_t s1 = s0 + p.warp_slots < p.S ? s0 + p.warp_slots : p.S;
+    const int64_t cta0 = static_cast<int64_t>(rank) * p.warps * p.warp_slots;
+    const int64_t s0 = cta0 + warp * p.warp_slots;
+    const int64_t end = s0 + p.warp_slots < p.S ? s0 + p.warp_slots : p.S, s1 = warp < p.warps ? end : s0;
     int* mine = run + warp * p.E;
+    int idx[kLayoutHeld], local[kLayoutHeld];  // expert (-1: none) and rank in the run
     bool bad = false;
-    for (int64_t s = s0 + lane; s < s1; s += 32) {
-        const int e = p.idx[s];
-        if (e >= 0 && e < p.E) atomicAdd(mine + e, 1);
-        else bad |= e != -1;
+    auto fetch = [&](int64_t at) {
+        int x = at < s1 ? p.idx[at] : -1;
+        if (x < 0 || x >= p.E) {
+            bad |= x != -1;
+            x = -1;
+        }
+        return x;
+    };
+    // Rank of a batch's slots among the run's so far; the counts move on.
+    auto rank_batch = [&](int x) {
+        uint32_t same = __ballot_sync(0xffffffffu, x >= 0);
+        for (int b = 0; b < p.expert_bits; ++b) {
+            const uint32_t ones = __ballot_sync(0xffffffffu, (x >> b) & 1);
+            same &= (x >> b) & 1 ? ones : ~ones;
+        }
+        const int r = x >= 0 ? mine[x] + __popc(same & ((1u << lane) - 1u)) : 0;
+        __syncwarp();
+        if (x >= 0 && lane == 31 - __clz(same)) mine[x] = r + 1;
+        __syncwarp();
+        return r;
+    };
+    if (kKind == kLayoutHeldRun) {
+#pragma unroll
+        for (int i = 0; i < kLayoutHeld; ++i) idx[i] = fetch(s0 + 32 * i + lane);
+    }
+    __syncthreads();
+    if (kKind == kLayoutHeldRun) {
+#pragma unroll
+        for (int i = 0; i < kLayoutHeld; ++i) local[i] = s0 + 32 * i < s1 ? rank_batch(idx[i]) : 0;
+    } else {
+        for (int64_t s = s0 + lane; s < s1; s += 32) {
+            const int x = fetch(s);
+            if (x >= 0) atomicAdd(mine + x, 1);
+        }
     }
     if (bad) atomicOr(&g_dg_error, 32u);
     __syncthreads();
-    // Exclusive over this CTA's warps.
-    for (int e = tid; e < p.E; e += kLayoutThreads) {
+    // Exclusive over this CTA's warps, eight at a time.
+    if (tid < p.E) {
         int n = 0;
+        for (int w0 = 0; w0 < p.warps; w0 += 8) {
+            int x[8];
 #pragma unroll
-        for (int w = 0; w < kLayoutWarps; ++w) {
-            const int x = run[w * p.E + e];
-            run[w * p.E + e] = n;
-            n += x;
+            for (int w = 0; w < 8; ++w) x[w] = w0 + w < p.warps ? run[(w0 + w) * p.E + tid] : 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                if (w0 + w < p.warps) run[(w0 + w) * p.E + tid] = n;
+                n += x[w];
+            }
         }
-        total[e] = n;
+        total[tid] = n;
     }
-    cluster_sync();
+    __syncwarp();
+    if (nctas > 1) cluster_sync();
     // Over the CTAs, then over the experts (at most one expert per thread).
     const int e = tid;
     int before = 0, all = 0;
     if (e < p.E) {
-        for (uint32_t r = 0; r < nctas; ++r) {
-            int x;
-            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(dsmem_addr(smem_u32(total + e), r)) : "memory");
-            if (r < rank) before += x;
-            all += x;
+        if (nctas > 1) {
+#pragma unroll
+            for (uint32_t r = 0; r < kLayoutMaxCluster; ++r) {
+                if (r >= nctas) break;
+                int x;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(dsmem_addr(smem_u32(total + e), r)) : "memory");
+                if (r < rank) before += x;
+                all += x;
+            }
+        } else {
+            all = total[e];
         }
     }
     __syncwarp();
-    cluster_arrive();  // this thread has read the other CTAs' totals
+    if (nctas > 1) cluster_arrive();  // this thread has read the other CTAs' totals
     const int kept = p.max_rows > 0 ? min(all, p.max_rows) : all;
     const int len = e >= p.E ? 0 : p.max_rows > 0 ? p.max_rows : (all + 127) / 128 * 128;
-    int incl = len;
+    // Scanned together: rows of the groups (low half) and this CTA's own slots.
+    const uint32_t own = e < p.E ? total[e] : 0;
+    unsigned long long incl = static_cast<unsigned long long>(own) << 32 | static_cast<uint32_t>(len);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
     if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    if (warp == 0) {
-        int v = wsum[lane];
+    {
+        // every warp scans the warps' sums for itself
+        unsigned long long v = wsum[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, v, o);
+            const unsigned long long x = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o) v += x;
         }
-        wsum[lane] = v;
+        const unsigned long long upto = __shfl_sync(0xffffffffu, v, (warp + 31) & 31);
+        if (warp) incl += upto;
     }
-    __syncthreads();
-    const int first = incl - len + (warp ? wsum[warp - 1] : 0);
+    const int first = static_cast<int>(static_cast<uint32_t>(incl)) - len;
     if (e < p.E) {
         start[e] = first;
         if (e == p.E - 1) start[p.E] = first + len;
-#pragma unroll 8
-        for (int w = 0; w < kLayoutWarps; ++w) run[w * p.E + e] += first + before;
+        base[e] = first + before;
+        local_start[e] = static_cast<int>(incl >> 32) - static_cast<int>(own);
         held[e] = kept;
         if (rank == 0) {
             p.offsets[e] = first;
@@ -834,38 +978,61 @@ route_layout_kernel(const LayoutParams p) {
     }
     __syncthreads();
 
-    for (int64_t s = s0; s < s1; s += 32) {
-        const int64_t at = s + lane;
-        const int x = at < s1 ? p.idx[at] : -1;
-        const bool ok = x >= 0 && x < p.E;
-        const uint32_t same = __match_any_sync(0xffffffffu, ok ? x : -1);
-        int row = -1;
-        if (ok) {
-            row = mine[x] + __popc(same & ((1u << lane) - 1u));
-            if (p.max_rows > 0 && row >= start[x] + p.max_rows) row = -1;
-        }
-        __syncwarp();
-        if (ok && lane == 31 - __clz(same)) mine[x] += __popc(same);
-        __syncwarp();
+    auto row_at = [&](int x, int r) {
+        const int row = base[x] + r;
+        return p.max_rows > 0 && row >= start[x] + p.max_rows ? -1 : row;
+    };
+    auto place = [&](int64_t at, int x, int r) {  // r: rank among the CTA's slots of x
+        const int row = x >= 0 ? row_at(x, r) : -1;
         if (at < s1) p.row_of[at] = row;
-        if (row >= 0) {
+        if (kKind != kLayoutDirect) {
+            if (x >= 0) staged[local_start[x] + r] = static_cast<uint32_t>(at - cta0) << 16 | static_cast<uint32_t>(x);
+        } else if (row >= 0) {
             p.m_indices[row] = x;
             p.slot_of[row] = static_cast<int>(at);
         }
+    };
+    if (kKind == kLayoutHeldRun) {
+#pragma unroll
+        for (int i = 0; i < kLayoutHeld; ++i)
+            if (s0 + 32 * i < s1) place(s0 + 32 * i + lane, idx[i], idx[i] >= 0 ? mine[idx[i]] + local[i] : 0);
+    } else {
+        for (int64_t s = s0; s < s1; s += 32) {
+            const int x = fetch(s + lane);
+            place(s + lane, x, rank_batch(x));
+        }
     }
     // Rows without a slot: -1 behind each group's last one, and behind the last group.
-    const int64_t gw = static_cast<int64_t>(rank) * kLayoutWarps + warp, nw = static_cast<int64_t>(nctas) * kLayoutWarps;
-    for (int64_t g = gw; g < p.E; g += nw)
-        for (int64_t r = start[g] + static_cast<int64_t>(held[g]) + lane; r < start[g + 1]; r += 32) {
-            p.m_indices[r] = -1;
-            p.slot_of[r] = -1;
-        }
-    for (int64_t r = start[p.E] + gw * 32 + lane; r < p.rows; r += nw * 32) {
+    const int t0 = static_cast<int>(rank) * kLayoutThreads + tid, nt = static_cast<int>(nctas) * kLayoutThreads;
+    auto clear = [&](int r) {
         p.m_indices[r] = -1;
         p.slot_of[r] = -1;
+    };
+    if (p.max_rows > 0) {
+        for (int64_t r = t0; r < p.rows; r += nt) {
+            const int g = static_cast<int>(r) / p.max_rows;
+            if (static_cast<int>(r) - g * p.max_rows >= held[g]) clear(static_cast<int>(r));
+        }
+    } else {
+        for (int i = t0; i < p.E * 128; i += nt) {  // fewer than 128 rows behind each
+            const int g = i >> 7, r = start[g] + held[g] + (i & 127);
+            if (r < start[g + 1]) clear(r);
+        }
+        for (int64_t r = start[p.E] + t0; r < p.rows; r += nt) clear(static_cast<int>(r));
+    }
+    if (kKind != kLayoutDirect) {
+        __syncthreads();
+        const int n = local_start[p.E - 1] + total[p.E - 1];
+        for (int i = tid; i < n; i += kLayoutThreads) {
+            const int x = static_cast<int>(staged[i] & 0xFFFFu), row = row_at(x, i - local_start[x]);
+            if (row >= 0) {
+                p.m_indices[row] = x;
+                p.slot_of[row] = static_cast<int>(cta0 + (staged[i] >> 16));
+            }
+        }
     }
     __syncwarp();
-    cluster_wait();  // no CTA leaves while another may still read its totals
+    if (nctas > 1) cluster_wait();  // no CTA leaves while another may still read its totals
 }
 
 }  // namespace dg

@@ -345,7 +345,7 @@ def run_layout(dg, idx, E, rows, max_rows=0):
 @pytest.mark.parametrize("T,k,E,extra,max_rows", [
     (0, 2, 5, 0, 0), (0, 2, 5, 256, 0), (0, 1, 4, 0, 16), (1, 1, 1, 0, 0), (1, 8, 256, 0, 0), (37, 3, 7, 128, 0),
     (500, 8, 8, 0, 0), (513, 8, 64, 384, 0), (1025, 4, 60, 0, 0), (4096, 8, 64, 0, 0), (9000, 5, 1024, 0, 0),
-    (20001, 7, 33, 1280, 0), (64, 8, 32, 0, 64), (64, 8, 32, 0, 5), (300, 6, 130, 0, 300), (5000, 8, 1000, 0, 3)])
+    (20001, 7, 33, 1280, 0), (33000, 8, 40, 0, 0), (40000, 8, 1024, 0, 0), (64, 8, 32, 0, 64), (64, 8, 32, 0, 5), (300, 6, 130, 0, 300), (5000, 8, 1000, 0, 3)])
 def test_layout(dgm, T, k, E, extra, max_rows):
     g = torch.Generator().manual_seed(T + E)
     idx = torch.randint(-1, E, (T, k), generator=g).int()
