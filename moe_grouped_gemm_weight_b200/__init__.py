@@ -123,6 +123,25 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_CALLS = ("dg_route_topk", "dg_route_topk_bwd", "dg_route_layout", "dg_dispatch_fp8_1x128", "dg_combine",
+          "dg_combine_bwd", "dg_swiglu_fp8", "dg_swiglu_fp8_bwd", "dg_fp8_1x128_to_128x128")
+_calls = None
+
+
+def _marshal():
+    """The calls around the grouped GEMMs as vector calls (csrc/dg_pycall.c), bound to the loaded library."""
+    global _calls
+    L = lib()
+    try:
+        from . import _dgcall
+    except ImportError as e:
+        raise RuntimeError(f"the extension _dgcall.so is missing in {_HERE}: run __graft_entry__.build() first") from e
+    for name in _CALLS:
+        _dgcall.bind(name, ctypes.cast(getattr(L, name), ctypes.c_void_p).value)
+    _calls = _dgcall
+    return _calls
+
+
 def _check(func: str, status: int) -> None:
     if status != DG_OK:
         L = lib()
@@ -337,30 +356,40 @@ def _check_tensors(func: str, *specs) -> int:
     Each spec is (name, tensor, torch dtype or element bytes, elements the call
     touches).  One pass over the tensors: a decoding step makes these calls every
     few microseconds."""
-    dev, stray = None, None
+    dev = cur = _device()
     for name, t, kind, need in specs:
         if t is None:
             continue
-        if kind is not t.dtype and kind != t.element_size():
-            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call takes "
-                          + (f"{kind}-byte elements" if isinstance(kind, int) else str(kind)))
-        if not t.is_contiguous():
-            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is not contiguous")
-        if t.numel() < need:
-            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} holds {t.numel()} elements, the call touches {need}")
-        d = t.get_device()
-        if dev is None:
-            dev = d
-        if d != dev or d < 0:
-            stray = stray or (name, t)
-    if stray is not None and any(t is not None and t.device.type != "cuda" for _, t, _, _ in specs):
-        name, t = next((n, t) for n, t, _, _ in specs if t is not None and t.device.type != "cuda")
-        raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is not on a CUDA device ({t.device})")
-    cur = torch.cuda.current_device()
-    if stray is not None or dev != cur:
-        name, t = next((n, t) for n, t, _, _ in specs if t is not None and t.get_device() != cur)
-        raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is on {t.device}, the current device is cuda:{cur}")
+        if (t.dtype is not kind and t.element_size() != kind) or t.numel() < need or not t.is_contiguous():
+            raise _tensor_error(func, name, t, kind, need)
+        if t.get_device() != cur:
+            dev = -1  # after the other checks: say what is wrong with the tensor itself first
+    if dev != cur or cur < 0:
+        raise _device_error(func, cur, specs)
     return cur
+
+
+def _tensor_error(func: str, name: str, t, kind, need: int) -> DGError:
+    if t.dtype is not kind and t.element_size() != kind:
+        want = f"{kind}-byte elements" if isinstance(kind, int) else str(kind)
+        return DGError(func, DG_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call takes {want}")
+    if not t.is_contiguous():
+        return DGError(func, DG_ERR_INVALID_ARG, f"{name} is not contiguous")
+    return DGError(func, DG_ERR_INVALID_ARG, f"{name} holds {t.numel()} elements, the call touches {need}")
+
+
+def _device_error(func: str, cur: int, specs) -> DGError:
+    given = [(name, t) for name, t, _, _ in specs if t is not None]
+    for name, t in given:
+        if t.device.type != "cuda":
+            return DGError(func, DG_ERR_INVALID_ARG, f"{name} is not on a CUDA device ({t.device})")
+    name, t = next((n, t) for n, t in given if t.get_device() != cur)
+    return DGError(func, DG_ERR_INVALID_ARG, f"{name} is on {t.device}, the current device is cuda:{cur}")
+
+
+def _device() -> int:
+    """The current CUDA device, -1 before CUDA has been used in this process."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
 
 
 def _raw_stream(stream, device: int) -> int:
@@ -395,9 +424,11 @@ def dg_route_topk(topk_idx, topk_w, logits, bias=None, n_groups: int = 1, topk_g
     dt = _logits_dtype(func, logits)
     dev = _check_tensors(func, ("topk_idx", topk_idx, _I32, T * k), ("topk_w", topk_w, _F32, T * k),
                          ("logits", logits, logits.dtype, T * E), ("bias", bias, _F32, E))
-    _check(func, lib().dg_route_topk(_ptr(topk_idx), _ptr(topk_w), _ptr(logits), dt, _ptr(bias), T, E, k,
-                                     int(n_groups), int(topk_groups), int(group_top), int(score), int(bool(renorm)),
-                                     float(scale), _raw_stream(stream, dev)))
+    status = (_calls or _marshal()).dg_route_topk(_ptr(topk_idx), _ptr(topk_w), _ptr(logits), dt, _ptr(bias), T, E, k,
+                                                  n_groups, topk_groups, group_top, score, 1 if renorm else 0, scale,
+                                                  _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
 
 
 def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTMAX, renorm: bool = False,
@@ -412,8 +443,10 @@ def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTM
         raise DGError(func, DG_ERR_INVALID_ARG, f"dlogits are {dlogits.dtype}, logits {logits.dtype}")
     dev = _check_tensors(func, ("dlogits", dlogits, logits.dtype, T * E), ("dw", dw, _F32, T * k),
                          ("logits", logits, logits.dtype, T * E), ("topk_idx", topk_idx, _I32, T * k))
-    _check(func, lib().dg_route_topk_bwd(_ptr(dlogits), _ptr(dw), _ptr(logits), dt, _ptr(topk_idx), T, E, k,
-                                         int(score), int(bool(renorm)), float(scale), _raw_stream(stream, dev)))
+    status = (_calls or _marshal()).dg_route_topk_bwd(_ptr(dlogits), _ptr(dw), _ptr(logits), dt, _ptr(topk_idx), T, E,
+                                                      k, score, 1 if renorm else 0, scale, _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
 
 
 def dg_get_layout_rows(T: int, k: int, E: int) -> int:
@@ -432,8 +465,11 @@ def dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx,
     dev = _check_tensors(func, ("row_of", row_of, _I32, T * k), ("m_indices", m_indices, _I32, rows),
                          ("slot_of", slot_of, _I32, rows), ("group_offsets", group_offsets, _I32, E + 1),
                          ("counts", counts, _I32, E), ("topk_idx", topk_idx, _I32, T * k))
-    _check(func, lib().dg_route_layout(_ptr(row_of), _ptr(m_indices), _ptr(slot_of), _ptr(group_offsets),
-                                       _ptr(counts), _ptr(topk_idx), T, k, E, rows, int(max_rows), _raw_stream(stream, dev)))
+    status = (_calls or _marshal()).dg_route_layout(_ptr(row_of), _ptr(m_indices), _ptr(slot_of), _ptr(group_offsets),
+                                                    _ptr(counts), _ptr(topk_idx), T, k, E, rows, max_rows,
+                                                    _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
 
 
 def dg_dispatch_fp8_1x128(Q, sa, sa_stride: int, X, row_of, group_rows: int = 0, stream=None) -> None:
@@ -448,8 +484,10 @@ def dg_dispatch_fp8_1x128(Q, sa, sa_stride: int, X, row_of, group_rows: int = 0,
     dev = _check_tensors(func, ("Q", Q, 1, rows * K),
                          ("sa", sa, _F32, _scales_need(_cdiv(K, 128), sa_stride, rows, group_rows)),
                          ("X", X, _BF16, T * K), ("row_of", row_of, _I32, T * k))
-    _check(func, lib().dg_dispatch_fp8_1x128(_ptr(Q), _ptr(sa), int(sa_stride), _ptr(X), _ptr(row_of), T, k, K, rows,
-                                             int(group_rows), _raw_stream(stream, dev)))
+    status = (_calls or _marshal()).dg_dispatch_fp8_1x128(_ptr(Q), _ptr(sa), sa_stride, _ptr(X), _ptr(row_of), T, k,
+                                                          K, rows, group_rows, _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
 
 
 def dg_combine(out, Y, row_of, w=None, stream=None) -> None:
@@ -463,7 +501,10 @@ def dg_combine(out, Y, row_of, w=None, stream=None) -> None:
     rows = Y.numel() // N if N else 0
     dev = _check_tensors(func, ("out", out, _BF16, T * N), ("Y", Y, _BF16, rows * N), ("row_of", row_of, _I32, T * k),
                          ("w", w, _F32, T * k))
-    _check(func, lib().dg_combine(_ptr(out), _ptr(Y), _ptr(row_of), _ptr(w), T, k, N, rows, _raw_stream(stream, dev)))
+    status = (_calls or _marshal()).dg_combine(_ptr(out), _ptr(Y), _ptr(row_of), _ptr(w), T, k, N, rows,
+                                               _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
 
 
 def dg_combine_bwd(dw, Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, dout, Y, row_of, slot_of, w,
@@ -481,9 +522,11 @@ def dg_combine_bwd(dw, Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, dout, Y, 
                          ("sc", sc, _F32, _sa_need(_cdiv(rows, 128), sc_stride, N)), ("dout", dout, _BF16, T * N),
                          ("Y", Y, _BF16, rows * N), ("row_of", row_of, _I32, T * k), ("slot_of", slot_of, _I32, rows),
                          ("w", w, _F32, T * k))
-    _check(func, lib().dg_combine_bwd(_ptr(dw), _ptr(Qr), _ptr(sr), int(sr_stride), _ptr(Qc), _ptr(sc),
-                                      int(sc_stride), _ptr(dout), _ptr(Y), _ptr(row_of), _ptr(slot_of), _ptr(w),
-                                      T, k, N, rows, _raw_stream(stream, dev)))
+    status = (_calls or _marshal()).dg_combine_bwd(_ptr(dw), _ptr(Qr), _ptr(sr), sr_stride, _ptr(Qc), _ptr(sc),
+                                                   sc_stride, _ptr(dout), _ptr(Y), _ptr(row_of), _ptr(slot_of),
+                                                   _ptr(w), T, k, N, rows, _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
 
 
 def dg_swiglu_fp8(Q, sa, sa_stride: int, H, C=None, cs=None, cs_stride: int = 0, m_indices=None, group_rows: int = 0,
@@ -500,8 +543,10 @@ def dg_swiglu_fp8(Q, sa, sa_stride: int, H, C=None, cs=None, cs_stride: int = 0,
                          ("H", H, _BF16, rows * 2 * F), ("C", C, 1, rows * 2 * F),
                          ("cs", cs if C is not None else None, _F32, _scales_need(2 * _cdiv(F, 128), cs_stride, rows, group_rows)),
                          ("m_indices", m_indices, _I32, rows))
-    _check(func, lib().dg_swiglu_fp8(_ptr(Q), _ptr(sa), int(sa_stride), _ptr(C), _ptr(cs), int(cs_stride), _ptr(H),
-                                     _ptr(m_indices), rows, F, int(group_rows), _raw_stream(stream, dev)))
+    status = (_calls or _marshal()).dg_swiglu_fp8(_ptr(Q), _ptr(sa), sa_stride, _ptr(C), _ptr(cs), cs_stride, _ptr(H),
+                                                  _ptr(m_indices), rows, F, group_rows, _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
 
 
 def dg_swiglu_fp8_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, Qa, sb, dA, C, cs, cs_stride: int,
@@ -518,9 +563,11 @@ def dg_swiglu_fp8_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, Qa, sb, dA
                          ("sb", sb, _F32, _cdiv(F, 128) * _cdiv(rows, 128)), ("dA", dA, _BF16, rows * F),
                          ("C", C, 1, rows * 2 * F), ("cs", cs, _F32, _sa_need(2 * _cdiv(F, 128), cs_stride, rows)),
                          ("m_indices", m_indices, _I32, rows))
-    _check(func, lib().dg_swiglu_fp8_bwd(_ptr(Qr), _ptr(sr), int(sr_stride), _ptr(Qc), _ptr(sc), int(sc_stride),
-                                         _ptr(Qa), _ptr(sb), _ptr(dA), _ptr(C), _ptr(cs), int(cs_stride),
-                                         _ptr(m_indices), rows, F, _raw_stream(stream, dev)))
+    status = (_calls or _marshal()).dg_swiglu_fp8_bwd(_ptr(Qr), _ptr(sr), sr_stride, _ptr(Qc), _ptr(sc), sc_stride,
+                                                      _ptr(Qa), _ptr(sb), _ptr(dA), _ptr(C), _ptr(cs), cs_stride,
+                                                      _ptr(m_indices), rows, F, _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
 
 
 def dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride: int, m_indices=None, stream=None) -> None:
@@ -531,8 +578,10 @@ def dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride: int, m_indices=None, strea
     dev = _check_tensors(func, ("Qb", Qb, 1, rows * K), ("sb", sb, _F32, _cdiv(K, 128) * _cdiv(rows, 128)),
                          ("Q", Q, 1, rows * K), ("sa", sa, _F32, _sa_need(_cdiv(K, 128), sa_stride, rows)),
                          ("m_indices", m_indices, _I32, rows))
-    _check(func, lib().dg_fp8_1x128_to_128x128(_ptr(Qb), _ptr(sb), _ptr(Q), _ptr(sa), int(sa_stride),
-                                               _ptr(m_indices), rows, K, _raw_stream(stream, dev)))
+    status = (_calls or _marshal()).dg_fp8_1x128_to_128x128(_ptr(Qb), _ptr(sb), _ptr(Q), _ptr(sa), sa_stride,
+                                                            _ptr(m_indices), rows, K, _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
 
 
 def dg_set_pdl(enable) -> None:

@@ -1,17 +1,22 @@
-"""Build libdg.so (the sm_100a CUDA library behind include/dg.h) in-tree with nvcc."""
+"""Build libdg.so (the sm_100a CUDA library behind include/dg.h) in-tree with nvcc, and
+_dgcall.so (argument marshalling of the binding's frequent calls) with gcc."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdg.so")
 SOURCES = [os.path.join(CSRC, "dg_api.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "dg.h")]
+CALL_LIB = os.path.join(HERE, "_dgcall.so")
+CALL_SOURCE = os.path.join(CSRC, "dg_pycall.c")
+HEADER = os.path.join(ROOT, "include", "dg.h")
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".c")] + [HEADER]
 
 
 def nvcc_path() -> str:
@@ -28,16 +33,27 @@ def command(out: str = LIB, verbose_ptxas: bool = False) -> list:
     return cmd
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def call_command(out: str = CALL_LIB) -> list:
+    return ["gcc", "-O2", "-std=gnu11", "-Wall", "-Werror", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), CALL_SOURCE, "-o", out]
+
+
+def _newer(out: str, deps: list) -> bool:
+    if not os.path.exists(out):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in DEPS if os.path.exists(d))
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(d) <= t for d in deps if os.path.exists(d))
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, DEPS)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if force or not up_to_date():
         subprocess.run(command(verbose_ptxas=verbose_ptxas), check=True)
+    if force or not _newer(CALL_LIB, [CALL_SOURCE, HEADER]):
+        subprocess.run(call_command(), check=True)
     return LIB
 
 
