@@ -347,49 +347,38 @@ def _shape1(func: str, name: str, t) -> int:
     return t.shape[0]
 
 
-_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+# Kinds of elements, as the extension's check of a call's tensors numbers them.
+_U8, _BF16, _F32, _I32 = 1, 2, 4, 5
+_KINDS = {_BF16: torch.bfloat16, _F32: torch.float32, _I32: torch.int32}
 
 
-def _check_tensors(func: str, *specs) -> int:
+def _check_tensors(func: str, names: str, *triples) -> int:
     """_check_args for the calls around the GEMMs, and the current device's index.
 
-    Each spec is (name, tensor, torch dtype or element bytes, elements the call
-    touches).  One pass over the tensors: a decoding step makes these calls every
-    few microseconds."""
-    dev = cur = _device()
-    for name, t, kind, need in specs:
-        if t is None:
-            continue
-        if (t.dtype is not kind and t.element_size() != kind) or t.numel() < need or not t.is_contiguous():
-            raise _tensor_error(func, name, t, kind, need)
-        if t.get_device() != cur:
-            dev = -1  # after the other checks: say what is wrong with the tensor itself first
-    if dev != cur or cur < 0:
-        raise _device_error(func, cur, specs)
-    return cur
-
-
-def _tensor_error(func: str, name: str, t, kind, need: int) -> DGError:
-    if t.dtype is not kind and t.element_size() != kind:
-        want = f"{kind}-byte elements" if isinstance(kind, int) else str(kind)
-        return DGError(func, DG_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call takes {want}")
-    if not t.is_contiguous():
-        return DGError(func, DG_ERR_INVALID_ARG, f"{name} is not contiguous")
-    return DGError(func, DG_ERR_INVALID_ARG, f"{name} holds {t.numel()} elements, the call touches {need}")
-
-
-def _device_error(func: str, cur: int, specs) -> DGError:
-    given = [(name, t) for name, t, _, _ in specs if t is not None]
-    for name, t in given:
+    `triples` are (tensor, kind, elements the call touches) one after the other,
+    `names` their names.  The extension checks them in one go (a decoding step
+    makes these calls every few microseconds); what is wrong is looked up only
+    for the message."""
+    cur = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    if (_calls or _marshal()).fits(cur, *triples):
+        if cur >= 0:
+            return cur
+    given = [(name, *triples[3 * i:3 * i + 3]) for i, name in enumerate(names.split()) if triples[3 * i] is not None]
+    for name, t, kind, need in given:
+        if t.element_size() != 1 if kind == _U8 else t.dtype != _KINDS[kind]:
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call takes "
+                          + ("1-byte elements" if kind == _U8 else str(_KINDS[kind])))
+        if not t.is_contiguous():
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is not contiguous")
+        if t.numel() < need:
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} holds {t.numel()} elements, the call touches {need}")
+    for name, t, _, _ in given:
         if t.device.type != "cuda":
-            return DGError(func, DG_ERR_INVALID_ARG, f"{name} is not on a CUDA device ({t.device})")
-    name, t = next((n, t) for n, t in given if t.get_device() != cur)
-    return DGError(func, DG_ERR_INVALID_ARG, f"{name} is on {t.device}, the current device is cuda:{cur}")
-
-
-def _device() -> int:
-    """The current CUDA device, -1 before CUDA has been used in this process."""
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is not on a CUDA device ({t.device})")
+    for name, t, _, _ in given:
+        if t.get_device() != cur:
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is on {t.device}, the current device is cuda:{cur}")
+    raise DGError(func, DG_ERR_INVALID_ARG, f"an argument is missing or not a tensor: {names}")
 
 
 def _raw_stream(stream, device: int) -> int:
@@ -422,11 +411,11 @@ def dg_route_topk(topk_idx, topk_w, logits, bias=None, n_groups: int = 1, topk_g
     Ti, k = _shape2(func, "topk_idx", topk_idx)
     _check_dim(func, "token count of topk_idx", Ti, T)
     dt = _logits_dtype(func, logits)
-    dev = _check_tensors(func, ("topk_idx", topk_idx, _I32, T * k), ("topk_w", topk_w, _F32, T * k),
-                         ("logits", logits, logits.dtype, T * E), ("bias", bias, _F32, E))
-    status = (_calls or _marshal()).dg_route_topk(_ptr(topk_idx), _ptr(topk_w), _ptr(logits), dt, _ptr(bias), T, E, k,
-                                                  n_groups, topk_groups, group_top, score, 1 if renorm else 0, scale,
-                                                  _raw_stream(stream, dev))
+    kind = _BF16 if dt == DG_DTYPE_BF16 else _F32
+    dev = _check_tensors(func, "topk_idx topk_w logits bias",
+                         topk_idx, _I32, T * k, topk_w, _F32, T * k, logits, kind, T * E, bias, _F32, E)
+    status = _calls.dg_route_topk(topk_idx, topk_w, logits, dt, bias, T, E, k, n_groups, topk_groups, group_top,
+                                  score, 1 if renorm else 0, scale, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -439,12 +428,13 @@ def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTM
     Ti, k = _shape2(func, "topk_idx", topk_idx)
     _check_dim(func, "token count of topk_idx", Ti, T)
     dt = _logits_dtype(func, logits)
+    kind = _BF16 if dt == DG_DTYPE_BF16 else _F32
     if dlogits is not None and dlogits.dtype != logits.dtype:
         raise DGError(func, DG_ERR_INVALID_ARG, f"dlogits are {dlogits.dtype}, logits {logits.dtype}")
-    dev = _check_tensors(func, ("dlogits", dlogits, logits.dtype, T * E), ("dw", dw, _F32, T * k),
-                         ("logits", logits, logits.dtype, T * E), ("topk_idx", topk_idx, _I32, T * k))
-    status = (_calls or _marshal()).dg_route_topk_bwd(_ptr(dlogits), _ptr(dw), _ptr(logits), dt, _ptr(topk_idx), T, E,
-                                                      k, score, 1 if renorm else 0, scale, _raw_stream(stream, dev))
+    dev = _check_tensors(func, "dlogits dw logits topk_idx",
+                         dlogits, kind, T * E, dw, _F32, T * k, logits, kind, T * E, topk_idx, _I32, T * k)
+    status = _calls.dg_route_topk_bwd(dlogits, dw, logits, dt, topk_idx, T, E, k, score, 1 if renorm else 0, scale,
+                                      _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -462,12 +452,11 @@ def dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx,
     func = "dg_route_layout"
     T, k = _shape2(func, "topk_idx", topk_idx)
     rows, E = _shape1(func, "m_indices", m_indices), _shape1(func, "counts", counts)
-    dev = _check_tensors(func, ("row_of", row_of, _I32, T * k), ("m_indices", m_indices, _I32, rows),
-                         ("slot_of", slot_of, _I32, rows), ("group_offsets", group_offsets, _I32, E + 1),
-                         ("counts", counts, _I32, E), ("topk_idx", topk_idx, _I32, T * k))
-    status = (_calls or _marshal()).dg_route_layout(_ptr(row_of), _ptr(m_indices), _ptr(slot_of), _ptr(group_offsets),
-                                                    _ptr(counts), _ptr(topk_idx), T, k, E, rows, max_rows,
-                                                    _raw_stream(stream, dev))
+    dev = _check_tensors(func, "row_of m_indices slot_of group_offsets counts topk_idx",
+                         row_of, _I32, T * k, m_indices, _I32, rows, slot_of, _I32, rows, group_offsets, _I32, E + 1,
+                         counts, _I32, E, topk_idx, _I32, T * k)
+    status = _calls.dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx, T, k, E, rows,
+                                    max_rows, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -481,11 +470,11 @@ def dg_dispatch_fp8_1x128(Q, sa, sa_stride: int, X, row_of, group_rows: int = 0,
     _check_dim(func, "token count of row_of", Ti, T)
     _check_dim(func, "K of Q", Q.shape[-1], K)
     rows = Q.numel() // K if K else 0
-    dev = _check_tensors(func, ("Q", Q, 1, rows * K),
-                         ("sa", sa, _F32, _scales_need(_cdiv(K, 128), sa_stride, rows, group_rows)),
-                         ("X", X, _BF16, T * K), ("row_of", row_of, _I32, T * k))
-    status = (_calls or _marshal()).dg_dispatch_fp8_1x128(_ptr(Q), _ptr(sa), sa_stride, _ptr(X), _ptr(row_of), T, k,
-                                                          K, rows, group_rows, _raw_stream(stream, dev))
+    dev = _check_tensors(func, "Q sa X row_of",
+                         Q, _U8, rows * K, sa, _F32, _scales_need(_cdiv(K, 128), sa_stride, rows, group_rows),
+                         X, _BF16, T * K, row_of, _I32, T * k)
+    status = _calls.dg_dispatch_fp8_1x128(Q, sa, sa_stride, X, row_of, T, k, K, rows, group_rows,
+                                          _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -499,10 +488,9 @@ def dg_combine(out, Y, row_of, w=None, stream=None) -> None:
     _check_dim(func, "token count of row_of", Ti, T)
     _check_dim(func, "N of Y", Y.shape[-1], N)
     rows = Y.numel() // N if N else 0
-    dev = _check_tensors(func, ("out", out, _BF16, T * N), ("Y", Y, _BF16, rows * N), ("row_of", row_of, _I32, T * k),
-                         ("w", w, _F32, T * k))
-    status = (_calls or _marshal()).dg_combine(_ptr(out), _ptr(Y), _ptr(row_of), _ptr(w), T, k, N, rows,
-                                               _raw_stream(stream, dev))
+    dev = _check_tensors(func, "out Y row_of w",
+                         out, _BF16, T * N, Y, _BF16, rows * N, row_of, _I32, T * k, w, _F32, T * k)
+    status = _calls.dg_combine(out, Y, row_of, w, T, k, N, rows, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -517,14 +505,12 @@ def dg_combine_bwd(dw, Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, dout, Y, 
     rows, Ny = _shape2(func, "Y", Y)
     _check_dim(func, "token count of row_of", Ti, T)
     _check_dim(func, "N of Y", Ny, N)
-    dev = _check_tensors(func, ("dw", dw, _F32, T * k), ("Qr", Qr, 1, rows * N),
-                         ("sr", sr, _F32, _sa_need(_cdiv(N, 128), sr_stride, rows)), ("Qc", Qc, 1, rows * N),
-                         ("sc", sc, _F32, _sa_need(_cdiv(rows, 128), sc_stride, N)), ("dout", dout, _BF16, T * N),
-                         ("Y", Y, _BF16, rows * N), ("row_of", row_of, _I32, T * k), ("slot_of", slot_of, _I32, rows),
-                         ("w", w, _F32, T * k))
-    status = (_calls or _marshal()).dg_combine_bwd(_ptr(dw), _ptr(Qr), _ptr(sr), sr_stride, _ptr(Qc), _ptr(sc),
-                                                   sc_stride, _ptr(dout), _ptr(Y), _ptr(row_of), _ptr(slot_of),
-                                                   _ptr(w), T, k, N, rows, _raw_stream(stream, dev))
+    dev = _check_tensors(func, "dw Qr sr Qc sc dout Y row_of slot_of w",
+                         dw, _F32, T * k, Qr, _U8, rows * N, sr, _F32, _sa_need(_cdiv(N, 128), sr_stride, rows),
+                         Qc, _U8, rows * N, sc, _F32, _sa_need(_cdiv(rows, 128), sc_stride, N), dout, _BF16, T * N,
+                         Y, _BF16, rows * N, row_of, _I32, T * k, slot_of, _I32, rows, w, _F32, T * k)
+    status = _calls.dg_combine_bwd(dw, Qr, sr, sr_stride, Qc, sc, sc_stride, dout, Y, row_of, slot_of, w, T, k, N,
+                                   rows, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -538,13 +524,13 @@ def dg_swiglu_fp8(Q, sa, sa_stride: int, H, C=None, cs=None, cs_stride: int = 0,
     _check_dim(func, "last extent of H", H.shape[-1], 2 * F)
     _check_dim(func, "F of Q", Q.shape[-1], F)
     rows = H.numel() // (2 * F) if F else 0
-    dev = _check_tensors(func, ("Q", Q, 1, rows * F),
-                         ("sa", sa, _F32, _scales_need(_cdiv(F, 128), sa_stride, rows, group_rows)),
-                         ("H", H, _BF16, rows * 2 * F), ("C", C, 1, rows * 2 * F),
-                         ("cs", cs if C is not None else None, _F32, _scales_need(2 * _cdiv(F, 128), cs_stride, rows, group_rows)),
-                         ("m_indices", m_indices, _I32, rows))
-    status = (_calls or _marshal()).dg_swiglu_fp8(_ptr(Q), _ptr(sa), sa_stride, _ptr(C), _ptr(cs), cs_stride, _ptr(H),
-                                                  _ptr(m_indices), rows, F, group_rows, _raw_stream(stream, dev))
+    dev = _check_tensors(func, "Q sa H C cs m_indices",
+                         Q, _U8, rows * F, sa, _F32, _scales_need(_cdiv(F, 128), sa_stride, rows, group_rows),
+                         H, _BF16, rows * 2 * F, C, _U8, rows * 2 * F,
+                         cs if C is not None else None, _F32, _scales_need(2 * _cdiv(F, 128), cs_stride, rows, group_rows),
+                         m_indices, _I32, rows)
+    status = _calls.dg_swiglu_fp8(Q, sa, sa_stride, C, cs, cs_stride, H, m_indices, rows, F, group_rows,
+                                  _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -557,15 +543,14 @@ def dg_swiglu_fp8_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, Qa, sb, dA
     func = "dg_swiglu_fp8_bwd"
     rows, F = _shape2(func, "dA", dA)
     _check_dim(func, "last extent of C", C.shape[-1], 2 * F)
-    dev = _check_tensors(func, ("Qr", Qr, 1, rows * 2 * F),
-                         ("sr", sr, _F32, _sa_need(2 * _cdiv(F, 128), sr_stride, rows)), ("Qc", Qc, 1, rows * 2 * F),
-                         ("sc", sc, _F32, _sa_need(_cdiv(rows, 128), sc_stride, 2 * F)), ("Qa", Qa, 1, rows * F),
-                         ("sb", sb, _F32, _cdiv(F, 128) * _cdiv(rows, 128)), ("dA", dA, _BF16, rows * F),
-                         ("C", C, 1, rows * 2 * F), ("cs", cs, _F32, _sa_need(2 * _cdiv(F, 128), cs_stride, rows)),
-                         ("m_indices", m_indices, _I32, rows))
-    status = (_calls or _marshal()).dg_swiglu_fp8_bwd(_ptr(Qr), _ptr(sr), sr_stride, _ptr(Qc), _ptr(sc), sc_stride,
-                                                      _ptr(Qa), _ptr(sb), _ptr(dA), _ptr(C), _ptr(cs), cs_stride,
-                                                      _ptr(m_indices), rows, F, _raw_stream(stream, dev))
+    dev = _check_tensors(func, "Qr sr Qc sc Qa sb dA C cs m_indices",
+                         Qr, _U8, rows * 2 * F, sr, _F32, _sa_need(2 * _cdiv(F, 128), sr_stride, rows),
+                         Qc, _U8, rows * 2 * F, sc, _F32, _sa_need(_cdiv(rows, 128), sc_stride, 2 * F),
+                         Qa, _U8, rows * F, sb, _F32, _cdiv(F, 128) * _cdiv(rows, 128), dA, _BF16, rows * F,
+                         C, _U8, rows * 2 * F, cs, _F32, _sa_need(2 * _cdiv(F, 128), cs_stride, rows),
+                         m_indices, _I32, rows)
+    status = _calls.dg_swiglu_fp8_bwd(Qr, sr, sr_stride, Qc, sc, sc_stride, Qa, sb, dA, C, cs, cs_stride, m_indices,
+                                      rows, F, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -575,11 +560,10 @@ def dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride: int, m_indices=None, strea
     128x128, sb [K/128, rows/128] (contiguous layout)."""
     func = "dg_fp8_1x128_to_128x128"
     rows, K = _shape2(func, "Q", Q)
-    dev = _check_tensors(func, ("Qb", Qb, 1, rows * K), ("sb", sb, _F32, _cdiv(K, 128) * _cdiv(rows, 128)),
-                         ("Q", Q, 1, rows * K), ("sa", sa, _F32, _sa_need(_cdiv(K, 128), sa_stride, rows)),
-                         ("m_indices", m_indices, _I32, rows))
-    status = (_calls or _marshal()).dg_fp8_1x128_to_128x128(_ptr(Qb), _ptr(sb), _ptr(Q), _ptr(sa), sa_stride,
-                                                            _ptr(m_indices), rows, K, _raw_stream(stream, dev))
+    dev = _check_tensors(func, "Qb sb Q sa m_indices",
+                         Qb, _U8, rows * K, sb, _F32, _cdiv(K, 128) * _cdiv(rows, 128), Q, _U8, rows * K,
+                         sa, _F32, _sa_need(_cdiv(K, 128), sa_stride, rows), m_indices, _I32, rows)
+    status = _calls.dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride, m_indices, rows, K, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 

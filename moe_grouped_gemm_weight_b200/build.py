@@ -1,5 +1,5 @@
 """Build libdg.so (the sm_100a CUDA library behind include/dg.h) in-tree with nvcc, and
-_dgcall.so (argument marshalling of the binding's frequent calls) with gcc."""
+_dgcall.so (argument marshalling of the binding's frequent calls) with g++."""
 from __future__ import annotations
 
 import os
@@ -14,9 +14,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdg.so")
 SOURCES = [os.path.join(CSRC, "dg_api.cu")]
 CALL_LIB = os.path.join(HERE, "_dgcall.so")
-CALL_SOURCE = os.path.join(CSRC, "dg_pycall.c")
+CALL_SOURCE = os.path.join(CSRC, "dg_pycall.cpp")
 HEADER = os.path.join(ROOT, "include", "dg.h")
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".c")] + [HEADER]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if not f.endswith(".cpp")] + [HEADER]
 
 
 def nvcc_path() -> str:
@@ -34,8 +34,14 @@ def command(out: str = LIB, verbose_ptxas: bool = False) -> list:
 
 
 def call_command(out: str = CALL_LIB) -> list:
-    return ["gcc", "-O2", "-std=gnu11", "-Wall", "-Werror", "-fPIC", "-shared", "-fvisibility=hidden",
-            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), CALL_SOURCE, "-o", out]
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [a for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+           for a in ("-isystem" if d != os.path.join(ROOT, "include") else "-I", d)]
+    return ["g++", "-O2", "-std=c++17", "-Wall", "-Werror", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, CALL_SOURCE, "-o", out,
+            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", f"-Wl,-rpath,{lib}"]
 
 
 def _newer(out: str, deps: list) -> bool:
