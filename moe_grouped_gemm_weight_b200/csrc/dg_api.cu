@@ -1513,7 +1513,7 @@ dg_status dg_swiglu_fp8_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, 
     if (tiles > 0x7FFFFFFF - sms) return fail(DG_ERR_UNSUPPORTED, "problem too large");
     p.tiles = static_cast<uint32_t>(tiles);
     return launch_plain(dg::swiglu_fp8_bwd_kernel, p, tiles < sms ? tiles : sms, dg::kSwigluBwdThreads,
-                        2 * dg::kSwigluBwdStage, 1, stream);
+                        2 * dg::kSwigluBwdStage + dg::kSwigluBwdFlags, 1, stream);
 }
 
 dg_status dg_fp8_1x128_to_128x128(uint8_t* Qb, float* sb, const uint8_t* Q, const float* sa, int sa_stride,

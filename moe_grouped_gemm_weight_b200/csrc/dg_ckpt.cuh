@@ -142,6 +142,7 @@ constexpr int kSwigluBwdThreads = 512;
 // rows' two scales.
 constexpr int kSwigluBwdScales = 128 * 128 * 4;
 constexpr int kSwigluBwdStage = kSwigluBwdScales + 128 * 2 * 4;
+constexpr int kSwigluBwdFlags = kSwigluBwdThreads / 32 * 128 * 4;  // behind the stages: each warp's copy of the next tile's row flags
 
 // A persistent CTA takes 128 x 128 tiles of the expert width, for gate and up:
 // thread layout as in dg_moe.cuh's tiles.  dg and silu stay in registers;
@@ -152,7 +153,7 @@ constexpr int kSwigluBwdStage = kSwigluBwdScales + 128 * 2 * 4;
 __global__ void __launch_bounds__(kSwigluBwdThreads)
 swiglu_fp8_bwd_kernel(const SwigluBwdParams p) {
     constexpr int T = kSwigluBwdThreads, R = CastTile<T>::kRows;
-    static_assert(R == 2 || R == 4, "row flags below");
+    static_assert(R == 4 && CastTile<T>::kMatrices == 2, "row flags and joins below");
     extern __shared__ __align__(16) uint8_t stage_smem[];
     __shared__ __align__(16) float cm[2][CastTile<T>::kWarps * CastTile<T>::kStride];
     __shared__ __align__(16) float cr[2][128];
@@ -172,29 +173,54 @@ swiglu_fp8_bwd_kernel(const SwigluBwdParams p) {
     const int tid = threadIdx.x, lane = tid & 31, half = tid >> 4, hl = tid & 15;
     const uint32_t stage0 = smem_u32(stage_smem);
 
+    // Tiles in turn: row block rb, F block fb, without a division per step.
+    struct At {
+        uint32_t rb, fb;
+    };
+    const uint32_t step_rb = gridDim.x / p.nfb, step_fb = gridDim.x % p.nfb;
+    auto advance = [&](At t) {
+        t.rb += step_rb;
+        t.fb += step_fb;
+        if (t.fb >= static_cast<uint32_t>(p.nfb)) {
+            t.fb -= p.nfb;
+            ++t.rb;
+        }
+        return t;
+    };
     // Row flags of a tile, bit half & 31 of mask i: this thread's row i; `live`: any row.
-    auto flags = [&](uint32_t tile, uint32_t (&mask)[R], bool& live) {
-        const int64_t row0 = static_cast<int64_t>(tile / p.nfb) * 128;
+    const uint32_t flags_at = stage0 + 2 * kSwigluBwdStage + ((tid >> 5) * 128 + lane) * 4;
+    auto flags = [&](uint32_t (&mask)[R], bool& live) {
         uint32_t all[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            all[i] = __ballot_sync(0xffffffffu, p.m_indices == nullptr || p.m_indices[row0 + lane + 32 * i] >= 0);
+        for (int i = 0; i < 4; ++i) {
+            int m = 0;
+            if (p.m_indices != nullptr) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(m) : "r"(flags_at + i * 128) : "memory");
+            all[i] = __ballot_sync(0xffffffffu, m >= 0);
+        }
         live = (all[0] | all[1] | all[2] | all[3]) != 0;
 #pragma unroll
-        for (int i = 0; i < R; ++i) mask[i] = R == 4 ? all[i] : half < 32 ? all[2 * i] : all[2 * i + 1];
+        for (int i = 0; i < R; ++i) mask[i] = all[i];
     };
-    auto fetch = [&](uint32_t tile, const uint32_t (&mask)[R], int st) {
-        const int64_t row0 = static_cast<int64_t>(tile / p.nfb) * 128;
-        const int fb = static_cast<int>(tile % p.nfb);
-        const int64_t col = fb * 128 + hl * 8;
-        const uint32_t at = stage0 + st * kSwigluBwdStage;
+    auto fetch_flags = [&](At t) {
+        if (p.m_indices == nullptr || t.rb * 128 >= static_cast<uint32_t>(p.rows)) return;
+        const int32_t* m = p.m_indices + static_cast<int64_t>(t.rb) * 128 + lane;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int64_t row = row0 + half + CastTile<T>::kStep * i;
+        for (int i = 0; i < 4; ++i) cp_async_4(flags_at + i * 128, m + 32 * i, 4);
+    };
+    // A tile's bytes, and the flags of the tile after it, whose own bytes they decide on.
+    auto fetch = [&](At t, const uint32_t (&mask)[R], int st) {
+        const int64_t row0 = static_cast<int64_t>(t.rb) * 128;
+        const int fb = static_cast<int>(t.fb);
+        const uint32_t at = stage0 + st * kSwigluBwdStage;
+        const int64_t first = (row0 + half) * p.F + fb * 128 + hl * 8, step = static_cast<int64_t>(CastTile<T>::kStep) * p.F;
+        const uint16_t* da = p.dA + first;
+        const uint8_t* gate = p.C + first + (row0 + half) * p.F;  // rows of C are twice as long
+#pragma unroll
+        for (int i = 0; i < R; ++i, da += step, gate += 2 * step) {
             const bool ok = (mask[i] >> (half & 31)) & 1u;
-            cp_async_16(at + (i * T + tid) * 16, p.dA + row * p.F + col, ok ? 16 : 0);
-            cp_async_8(at + R * T * 16 + (2 * i * T + tid) * 8, p.C + row * 2 * p.F + col, ok ? 8 : 0);
-            cp_async_8(at + R * T * 16 + ((2 * i + 1) * T + tid) * 8, p.C + row * 2 * p.F + p.F + col, ok ? 8 : 0);
+            cp_async_16(at + (i * T + tid) * 16, da, ok ? 16 : 0);
+            cp_async_8(at + R * T * 16 + (2 * i * T + tid) * 8, gate, ok ? 8 : 0);
+            cp_async_8(at + R * T * 16 + ((2 * i + 1) * T + tid) * 8, gate + p.F, ok ? 8 : 0);
         }
         if (hl < 2 * R) {  // lane i: gate scale of row i, lane R + i: up scale
             const int i = hl & (R - 1);
@@ -205,31 +231,36 @@ swiglu_fp8_bwd_kernel(const SwigluBwdParams p) {
                        p.cs + static_cast<int64_t>(fb + (hl >= R ? p.nfb : 0)) * p.cs_stride + row0 + half + CastTile<T>::kStep * i,
                        (m >> (half & 31)) & 1u ? 4 : 0);
         }
+        fetch_flags(advance(t));
         cp_async_commit();
     };
 
     uint32_t tile = blockIdx.x;
+    if (tile >= p.tiles) return;
     uint32_t mask[R];
     bool next_live = false;
-    if (tile < p.tiles) {
-        flags(tile, mask, next_live);
-        fetch(tile, mask, 0);
-    }
+    At here{tile / p.nfb, tile % p.nfb};
+    fetch_flags(here);
+    cp_async_commit();
+    cp_async_wait<0>();
+    flags(mask, next_live);
+    fetch(here, mask, 0);
     for (int st = 0; tile < p.tiles; tile += gridDim.x, st ^= 1) {
         const bool live = next_live;
+        cp_async_wait<0>();
+        __syncwarp();  // the scales were copied by other lanes
         if (tile + gridDim.x < p.tiles) {
-            flags(tile + gridDim.x, mask, next_live);
-            fetch(tile + gridDim.x, mask, st ^ 1);
-            cp_async_wait<1>();
-        } else {
-            cp_async_wait<0>();
+            flags(mask, next_live);
+            fetch(advance(here), mask, st ^ 1);
         }
+        const int64_t rb = here.rb, row0 = rb * 128;
+        const int fb = static_cast<int>(here.fb);
+        here = advance(here);
         if (!live) continue;  // the same answer in every warp
-        __syncwarp();         // the scales were copied by other lanes
-        const int64_t rb = tile / p.nfb, row0 = rb * 128;
-        const int fb = static_cast<int>(tile % p.nfb);
         const uint32_t at = stage0 + st * kSwigluBwdStage;
-        F8 dg[R], du[R], act[R];
+        F8 dh[2][R], act[R];  // d gate and d up; a
+        F8(&dg)[R] = dh[0], (&du)[R] = dh[1];
+        const int col[2] = {fb * 128, p.F + fb * 128};
         float am = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -263,10 +294,9 @@ swiglu_fp8_bwd_kernel(const SwigluBwdParams p) {
         for (int o = 16; o >= 1; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
         if (lane == 0) wm[tid >> 5] = am;
         maxima.arrive();
-        tile_cast_rows<T>(p.out, dg, row0, 2 * p.F, fb * 128);
+        tile_cast_rows<T, 2>(p.out, dh, row0, 2 * p.F, col);
         maxima.wait();
-        tile_column_scale<T>(p.out, cm[0], cr[0], row0, fb * 128);
-        tile_column_scale<T>(p.out, cm[1], cr[1], row0, p.F + fb * 128);
+        tile_column_scale<T>(p.out, cm[0], cr[0], row0, col);
         am = wm[lane & (CastTile<T>::kWarps - 1)];
         joined.arrive();
 #pragma unroll
@@ -278,10 +308,9 @@ swiglu_fp8_bwd_kernel(const SwigluBwdParams p) {
 #pragma unroll
         for (int i = 0; i < R; ++i, qa += static_cast<int64_t>(CastTile<T>::kStep) * p.F)
             *reinterpret_cast<uint2*>(qa) = e4m3x8(act[i], ra);
-        tile_cast_rows<T>(p.out, du, row0, 2 * p.F, p.F + fb * 128);
         joined.wait();
-        tile_cast_columns<T>(p.out, dg, cr[0], row0, 2 * p.F, fb * 128);
-        tile_cast_columns<T>(p.out, du, cr[1], row0, 2 * p.F, p.F + fb * 128);
+        tile_cast_columns<T>(p.out, dg, cr[0], row0, 2 * p.F, col[0]);
+        tile_cast_columns<T>(p.out, du, cr[1], row0, 2 * p.F, col[1]);
     }
 }
 

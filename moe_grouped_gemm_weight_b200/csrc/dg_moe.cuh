@@ -260,8 +260,8 @@ struct CastTile {
     static constexpr int kRows = 128 * 16 / T;   // rows per thread
     static constexpr int kStep = T / 16;         // between a thread's rows
     static constexpr int kWarps = T / 32;
-    static constexpr int kParts = T / 128;       // threads per column in the join
-    static constexpr int kStride = 128 + 32 / kParts;  // of the warps' maxima: the join's reads hit all banks
+    static constexpr int kMatrices = T / 256;    // joined at once, two threads to a column
+    static constexpr int kStride = 144;          // of the warps' maxima: the join's reads hit all banks
 };
 
 struct TileOut {
@@ -272,40 +272,35 @@ struct TileOut {
     int64_t sr_stride, sc_stride;
 };
 
-// 1x128: each half-warp has whole rows of the tile.
-template <int T>
-__device__ __forceinline__ void tile_cast_rows(const TileOut& o, const F8 (&v)[CastTile<T>::kRows], int64_t row0,
-                                               int N, int col0) {
-    constexpr int R = CastTile<T>::kRows;
+// 1x128: each half-warp has whole rows of the tile.  M matrices at once (at
+// columns col[m] of the output), so that a lane divides once for all their
+// scales.
+template <int T, int M>
+__device__ __forceinline__ void tile_cast_rows(const TileOut& o, const F8 (&v)[M][CastTile<T>::kRows], int64_t row0, int N,
+                                               const int (&col)[M]) {
+    constexpr int R = CastTile<T>::kRows, A = M * R;
     const int half = threadIdx.x >> 4, hl = threadIdx.x & 15, base = threadIdx.x & 16;
-    float a[R];
+    float a[A];
 #pragma unroll
-    for (int i = 0; i < R; ++i) a[i] = amax8(v[i]);
-    const float s = spread_scale<R>(half_warp_max_spread<R>(a));
-    if (hl >= R && hl < 2 * R)
-        o.sr[static_cast<int64_t>(col0 / 128) * o.sr_stride + row0 + half + CastTile<T>::kStep * (hl - R)] = s;
-    uint8_t* q = o.Qr + (row0 + half) * N + col0 + hl * 8;
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int i = 0; i < R; ++i) a[m * R + i] = amax8(v[m][i]);
+    const float s = spread_scale<A>(half_warp_max_spread<A>(a));
+    if (hl >= A && hl < 2 * A) {
+        const int m = (hl - A) / R, i = (hl - A) % R;
+        int c = col[0];
+#pragma unroll
+        for (int x = 1; x < M; ++x) c = m == x ? col[x] : c;
+        o.sr[static_cast<int64_t>(c >> 7) * o.sr_stride + row0 + half + CastTile<T>::kStep * i] = s;
+    }
     const int64_t step = static_cast<int64_t>(CastTile<T>::kStep) * N;
+    uint8_t* row = o.Qr + (row0 + half) * N + hl * 8;
 #pragma unroll
-    for (int i = 0; i < R; ++i, q += step) *reinterpret_cast<uint2*>(q) = e4m3x8(v[i], __shfl_sync(0xffffffffu, s, base + i));
+    for (int i = 0; i < R; ++i, row += step)
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            *reinterpret_cast<uint2*>(row + col[m]) = e4m3x8(v[m][i], __shfl_sync(0xffffffffu, s, base + m * R + i));
 }
-
-// A CTA barrier in two halves, so that work between them hides the wait: each
-// warp arrives, later each thread waits.  Several in turn order a tile's
-// shared values as __syncthreads would.  The wait is bounded like every other.
-struct SplitBarrier {
-    uint64_t* bar;
-    int* abort_flag;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void arrive() {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-    }
-    __device__ __forceinline__ void wait() {
-        mbar_wait(bar, phase, abort_flag);
-        phase ^= 1;
-    }
-};
 
 // 128x1, first part: the warps' column maxima into cm[warp][kStride].  The two
 // half-warps exchange four columns each.
@@ -329,19 +324,24 @@ __device__ __forceinline__ void tile_column_max(const F8 (&v)[CastTile<T>::kRows
     *reinterpret_cast<float4*>(cm + warp * CastTile<T>::kStride + hl * 8 + (hi ? 4 : 0)) = make_float4(m[0], m[1], m[2], m[3]);
 }
 
-// Second part, after a barrier: kParts threads to a column join the warps'
-// maxima; one of them leaves 448 / amax in cr, another writes the scale.
+// Second part, after a barrier: two threads to a column of the T / 256 matrices
+// (cm and cr one behind the other) join the warps' maxima; one leaves 448 /
+// amax in cr, the other writes the scale.
 template <int T>
-__device__ __forceinline__ void tile_column_scale(const TileOut& o, const float* cm, float* cr, int64_t row0, int col0) {
-    const int c = threadIdx.x / CastTile<T>::kParts, part = threadIdx.x % CastTile<T>::kParts;
+__device__ __forceinline__ void tile_column_scale(const TileOut& o, const float* cm, float* cr, int64_t row0,
+                                                  const int (&col)[CastTile<T>::kMatrices]) {
+    const int c = (threadIdx.x >> 1) & 127, m = threadIdx.x >> 8, part = threadIdx.x & 1;
+    const float* mine = cm + m * CastTile<T>::kWarps * CastTile<T>::kStride + c;
     float a = 1e-4f;
 #pragma unroll
-    for (int w = part; w < CastTile<T>::kWarps; w += CastTile<T>::kParts) a = fmaxf(a, cm[w * CastTile<T>::kStride + c]);
-#pragma unroll
-    for (int b = 1; b < CastTile<T>::kParts; b <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, b));
+    for (int w = 0; w < CastTile<T>::kWarps; w += 2) a = fmaxf(a, mine[(w + part) * CastTile<T>::kStride]);
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
     const float s = __fdiv_rn(part ? a : 448.f, part ? 448.f : a);
-    if (part == 0) cr[c] = s;
-    if (part == 1) o.sc[(row0 / 128) * o.sc_stride + col0 + c] = s;
+    if (part) {
+        o.sc[(row0 / 128) * o.sc_stride + (CastTile<T>::kMatrices > 1 && m ? col[CastTile<T>::kMatrices - 1] : col[0]) + c] = s;
+    } else {
+        cr[m * 128 + c] = s;
+    }
 }
 
 // Third part, after another barrier.
@@ -372,6 +372,23 @@ __device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
+
+// A CTA barrier in two halves, so that work between them hides the wait: each
+// warp arrives, later each thread waits.  Several in turn order a tile's
+// shared values as __syncthreads would.  The wait is bounded like every other.
+struct SplitBarrier {
+    uint64_t* bar;
+    int* abort_flag;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void arrive() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    }
+    __device__ __forceinline__ void wait() {
+        mbar_wait(bar, phase, abort_flag);
+        phase ^= 1;
+    }
+};
 
 // ----------------------------------------------------- combine, backward ----
 
@@ -461,7 +478,9 @@ combine_bwd_kernel(const CombineBwdParams p) {
     fetch(kb0);
     for (int kb = kb0; kb < kb1; ++kb) {
         cp_async_wait<0>();
-        F8 v[R];
+        F8 tile[1][R];
+        F8(&v)[R] = tile[0];
+        const int col[1] = {kb * 128};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             bf16x8_to_f8(ld_shared_16(stage + 2 * i * T * 16), v[i]);
@@ -477,9 +496,9 @@ combine_bwd_kernel(const CombineBwdParams p) {
         }
         if (kb + 1 < kb1) fetch(kb + 1);
         maxima.wait();
-        tile_column_scale<T>(p.out, cm, cr, row0, kb * 128);
+        tile_column_scale<T>(p.out, cm, cr, row0, col);
         joined.arrive();
-        tile_cast_rows<T>(p.out, v, row0, p.N, kb * 128);
+        tile_cast_rows<T, 1>(p.out, tile, row0, p.N, col);
         joined.wait();
         tile_cast_columns<T>(p.out, v, cr, row0, p.N, kb * 128);
     }

@@ -749,14 +749,22 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         } else if (e >= 0) {
             s = sigmoid_f(logit_at(static_cast<const L*>(p.logits) + static_cast<int64_t>(t) * p.E + e));
         }
-        if (p.renorm) {
-            const float r = 1.f / (warp_sum(s) + kRouteEps);
-            const float mean = warp_sum(g * s) * r;
-            g = e < 0 ? 0.f : (g - mean) * r;
+        // Two sums over the k slots (lanes past them hold zeros), side by side.
+        float dot = g * s, total = s;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            total += __shfl_xor_sync(0xffffffffu, total, o);
         }
-        float dot = 0.f;
-        if (p.softmax) dot = warp_sum(g * s);
-        else g *= s * (1.f - s);
+        if (p.renorm) {
+            const float rs = 1.f / (total + kRouteEps), mean = dot * rs;
+            g = e < 0 ? 0.f : (g - mean) * rs;
+            dot = mean * (kRouteEps * rs);  // sum of the new g s: (dot - mean total) rs, and total rs = 1 - eps rs
+        }
+        if (!p.softmax) {
+            g *= s * (1.f - s);
+            dot = 0.f;
+        }
 
         float r[EPL];
 #pragma unroll
@@ -764,17 +772,16 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         __syncwarp();
         store_logits<EPL>(line + lane * EPL, r);
         // An expert in several slots: its first slot takes the sum, in slot order.
-        const uint32_t same = __match_any_sync(0xffffffffu, e >= 0 ? e : -1 - lane);
-        if (__any_sync(0xffffffffu, (same & (same - 1u)) != 0)) {
-            float sum = 0.f;
-            for (int j = 0; j < p.k; ++j) {
-                const float gj = __shfl_sync(0xffffffffu, g, j);
-                if ((same >> j) & 1u) sum += gj;
-            }
-            g = sum;
+        bool first = e >= 0;
+        float sum = 0.f;
+        for (int j = 0; j < p.k; ++j) {
+            const int ej = __shfl_sync(0xffffffffu, e, j);
+            const float gj = __shfl_sync(0xffffffffu, g, j);
+            sum += ej == e ? gj : 0.f;
+            if (j < lane && ej == e) first = false;
         }
         __syncwarp();
-        if (e >= 0 && lane == __ffs(same) - 1) line[place] = g;
+        if (first) line[place] = sum;
         __syncwarp();
         load_logits<EPL>(line + lane * EPL, r);
         __syncwarp();
