@@ -407,10 +407,12 @@ route_topk_kernel(const RouteParams p) {
             for (int i = 0; i < EPL; ++i) z += exp_fast(v[i] - mx);
             rz = 1.f / warp_sum(z);
         }
-        // FP32 moves a choice value by less than `slack` (of the largest score:
-        // exponential, sum and reciprocal of a softmax 2^-20, sigmoid_fast 2^-22),
-        // and adding the bias by 2^-24 of the value.
-        const float slack = p.softmax ? rz * 0x1p-20f : 0x1p-22f;
+        // FP32 moves a choice value by less than `slack`: a sigmoid by 2^-22 (see
+        // sigmoid_fast); a softmax score by 2^-21 of the largest (exponential,
+        // product) and, all of a token alike, by the sum's error (at most 37
+        // roundings) and the reciprocal's, together below 2^-19.  Adding the bias
+        // adds 2^-24 of the value.
+        const float slack = p.softmax ? rz * 0x1p-19f : 0x1p-22f;
         auto apart_by = [&](float x, float y) {  // more than FP32 can have moved x - y
             return biased ? 2.f * slack + 0x1p-22f * (fabsf(x) + fabsf(y)) : 0.f;
         };

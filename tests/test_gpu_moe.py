@@ -194,6 +194,42 @@ def test_combine_gradient(dgm, T, k, E, N):
     assert bool((Qc.cpu()[~inside] == 0x5A).all() and (sc.cpu()[~L.blocks] == -7).all())
 
 
+@pytest.mark.parametrize("sms", [1, 4, 0])
+def test_results_do_not_depend_on_the_sm_cap(dgm, sms):
+    # Fewer SMs: longer runs of the persistent kernels, other splits of combine's gradient (the sums of dw are
+    # joined in another order: 2^-24 of their terms' magnitudes a join).
+    L = Layer(dgm, 300, 4, 9, 1152, 384, seed=3)
+    for t in (L.Hid, L.Y, L.dA, L.dXr):
+        t.zero_()
+    L.forward()
+    L.backward()
+    keep = ("idx", "wt", "row_of", "mi", "slot_of", "off", "cnt", "Q", "sa", "Q2", "sa2", "C", "cs", "dYr", "sr", "dYc",
+            "sc", "dHr", "shr", "dHc", "shc", "Qa", "sb", "Xb", "sx", "dX", "dlogits")
+    ops = {n: getattr(L, n).clone() for n in keep}
+    dw = L.dw.clone()
+    dgm.dg_set_num_sms(sms)
+    try:
+        dgm.dg_route_topk(L.idx, L.wt, L.logits, L.bias, score=dgm.DG_SCORE_SIGMOID, renorm=True, scale=2.0)
+        dgm.dg_route_layout(L.row_of, L.mi, L.slot_of, L.off, L.cnt, L.idx)
+        dgm.dg_dispatch_fp8_1x128(L.Q, L.sa, L.R, L.X, L.row_of)
+        dgm.dg_swiglu_fp8(L.Q2, L.sa2, L.R, L.Hid, L.C, L.cs, L.R, m_indices=L.mi)
+        dgm.dg_combine_bwd(L.dw, L.dYr, L.sr, L.R, L.dYc, L.sc, L.H, L.dout, L.Y, L.row_of, L.slot_of, L.wt)
+        dgm.dg_swiglu_fp8_bwd(L.dHr, L.shr, L.R, L.dHc, L.shc, 2 * L.F, L.Qa, L.sb, L.dA, L.C, L.cs, L.R, m_indices=L.mi)
+        dgm.dg_fp8_1x128_to_128x128(L.Xb, L.sx, L.Q, L.sa, L.R, m_indices=L.mi)
+        dgm.dg_combine(L.dX, L.dXr, L.row_of)
+        dgm.dg_route_topk_bwd(L.dlogits, dw, L.logits, L.idx, score=dgm.DG_SCORE_SIGMOID, renorm=True, scale=2.0)
+        torch.cuda.synchronize()
+    finally:
+        dgm.dg_set_num_sms(0)
+    for n in keep:
+        assert torch.equal(getattr(L, n).view(torch.uint8), ops[n].view(torch.uint8)), n
+    mag = torch.zeros_like(dw)
+    for t in range(L.T):
+        for j in range(L.k):
+            mag[t, j] = (L.dout[t].float() * L.Y[int(L.row_of[t, j])].float()).abs().sum()
+    assert bool(((L.dw - dw).abs() <= 2 * (1152 / 16 + 32) * 2.0 ** -24 * mag).all())
+
+
 def test_combine_gradient_against_differences(dgm):
     # dw is the derivative of <dout, combine(Y, w)>, which is linear in w.
     T, k, E, N = 6, 3, 5, 256
