@@ -956,7 +956,7 @@ dg_status launch_route(const dg::RouteParams& p, int64_t grid, int smem, void* s
 template <typename L, int EPL>
 dg_status launch_route_bwd_one(const dg::RouteBwdParams& p, int64_t grid, void* st) {
     return launch_plain(dg::route_topk_bwd_kernel<EPL, L>, p, grid, dg::kRouteWarps * 32,
-                        dg::kRouteWarps * 32 * EPL * static_cast<int>(sizeof(float)), 1, st);
+                        dg::kRouteWarps * (32 * EPL + 4 * dg::kRouteMaxK) * static_cast<int>(sizeof(float)), 1, st);
 }
 
 template <typename L>

@@ -49,14 +49,6 @@ __device__ __forceinline__ float amax8(const F8& f) {
     for (int i = 0; i < 4; ++i) a = amax3(a, f[i].x, f[i].y);
     return a;
 }
-// c + a . b over the bf16 pairs of two words: products exact, one rounding each.
-__device__ __forceinline__ float dot_bf16x2(uint32_t a, uint32_t b, float c) {
-    asm("{\n\t.reg .b16 al, ah, bl, bh;\n\t"
-        "mov.b32 {al, ah}, %1;\n\tmov.b32 {bl, bh}, %2;\n\t"
-        "fma.rn.f32.bf16 %0, al, bl, %0;\n\tfma.rn.f32.bf16 %0, ah, bh, %0;\n\t}"
-        : "+f"(c) : "r"(a), "r"(b));
-    return c;
-}
 __device__ __forceinline__ uint2 pack_e4m3x8(const F8& y) {
     uint32_t q[4];
 #pragma unroll
@@ -483,17 +475,19 @@ combine_bwd_kernel(const CombineBwdParams p) {
         const int col[1] = {kb * 128};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
+            F8 y;
             bf16x8_to_f8(ld_shared_16(stage + 2 * i * T * 16), v[i]);
+            bf16x8_to_f8(ld_shared_16(stage + (2 * i + 1) * T * 16), y);
+            float2 d = make_float2(dot[i], 0.f);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) v[i][x] = __fmul2_rn(v[i][x], make_float2(w[i], w[i]));
+            for (int x = 0; x < 4; ++x) {
+                d = __ffma2_rn(v[i][x], y[x], d);
+                v[i][x] = __fmul2_rn(v[i][x], make_float2(w[i], w[i]));
+            }
+            dot[i] = d.x + d.y;
         }
         tile_column_max<T>(v, cm);
         maxima.arrive();
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const uint4 d = ld_shared_16(stage + 2 * i * T * 16), y = ld_shared_16(stage + (2 * i + 1) * T * 16);
-            dot[i] = dot_bf16x2(d.x, y.x, dot_bf16x2(d.y, y.y, dot_bf16x2(d.z, y.z, dot_bf16x2(d.w, y.w, dot[i]))));
-        }
         if (kb + 1 < kb1) fetch(kb + 1);
         maxima.wait();
         tile_column_scale<T>(p.out, cm, cr, row0, col);

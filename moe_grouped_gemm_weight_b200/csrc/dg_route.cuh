@@ -686,12 +686,13 @@ __device__ __forceinline__ void store_logits(uint16_t* p, const float (&f)[N]) {
 template <int EPL, typename L>
 __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteCtas : 1)
 route_topk_bwd_kernel(const RouteBwdParams p) {
-    extern __shared__ __align__(16) float route_smem[];  // 32 * EPL values per warp
+    extern __shared__ __align__(16) float route_smem[];  // per warp 32 * EPL values, then 16 slots
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int e0 = lane * p.per;
     float* line = route_smem + warp * 32 * EPL;
+    float4* slots = reinterpret_cast<float4*>(route_smem + kRouteWarps * 32 * EPL) + warp * kRouteMaxK;
     const int stride = gridDim.x * kRouteWarps;
     int t = blockIdx.x * kRouteWarps + warp;
     if (t >= p.T) return;
@@ -758,10 +759,29 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             dot += __shfl_xor_sync(0xffffffffu, dot, o);
             total += __shfl_xor_sync(0xffffffffu, total, o);
         }
+        // The slots among themselves, through shared memory.
+        if (lane < kRouteMaxK) slots[lane] = make_float4(g, s, __int_as_float(e), 0.f);  // past k: zeros, expert -1
+        __syncwarp();
+        // g_j - sum_i g_i s_i / S = (sum_i (g_j - g_i) s_i + g_j eps) / S: nothing cancels
+        // where one expert has nearly all the weight, or is the only one.
+        float diff = g * kRouteEps;
+        bool first = e >= 0, twice = false;  // an expert in several slots: its first one takes the sum
+        for (int j0 = 0; j0 < p.k; j0 += 4) {
+            float4 o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = slots[j0 + j];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                diff = fmaf(g - o[j].x, o[j].y, diff);
+                const bool same = __float_as_int(o[j].z) == e;
+                first = first && !(same && j0 + j < lane);
+                twice = twice || (same && j0 + j != lane && e >= 0);
+            }
+        }
         if (p.renorm) {
-            const float rs = 1.f / (total + kRouteEps), mean = dot * rs;
-            g = e < 0 ? 0.f : (g - mean) * rs;
-            dot = mean * (kRouteEps * rs);  // sum of the new g s: (dot - mean total) rs, and total rs = 1 - eps rs
+            const float rs = 1.f / (total + kRouteEps);
+            g = e < 0 ? 0.f : diff * rs * rs;
+            dot = dot * rs * (kRouteEps * rs);  // sum of the new g s: the differences cancel in pairs
         }
         if (!p.softmax) {
             g *= s * (1.f - s);
@@ -773,14 +793,14 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         for (int i = 0; i < EPL; ++i) r[i] = 0.f;
         __syncwarp();
         store_logits<EPL>(line + lane * EPL, r);
-        // An expert in several slots: its first slot takes the sum, in slot order.
-        bool first = e >= 0;
-        float sum = 0.f;
-        for (int j = 0; j < p.k; ++j) {
-            const int ej = __shfl_sync(0xffffffffu, e, j);
-            const float gj = __shfl_sync(0xffffffffu, g, j);
-            sum += ej == e ? gj : 0.f;
-            if (j < lane && ej == e) first = false;
+        float sum = g;
+        if (__any_sync(0xffffffffu, twice)) {  // in slot order
+            sum = 0.f;
+            for (int j = 0; j < p.k; ++j) {
+                const int ej = __shfl_sync(0xffffffffu, e, j);
+                const float gj = __shfl_sync(0xffffffffu, g, j);
+                sum += ej == e ? gj : 0.f;
+            }
         }
         __syncwarp();
         if (first) line[place] = sum;

@@ -279,6 +279,40 @@ def test_route_gradient_of_absent_and_repeated_slots(dgm, sigmoid, renorm):
 
 
 @pytest.mark.parametrize("sigmoid", [False, True])
+def test_renormalised_gradient_does_not_cancel(dgm, sigmoid):
+    # One expert with nearly all the weight, and one expert alone (its weight is a constant up to 1e-20):
+    # dw_j - sum_i dw_i s_i / S is a small difference of large terms, but every element is good to
+    # (span + 40) 2^-24 of the sum of the magnitudes |dw_j - dw_i| s_i, which is what is left of it.
+    g = torch.Generator().manual_seed(6)
+    for k in (1, 2, 4):
+        logits = torch.randn(20, 12, generator=g)
+        logits[:, 0] += 9.0
+        idx = torch.stack([torch.cat([torch.zeros(1, dtype=torch.int64), 1 + torch.randperm(11, generator=g)[:k - 1]])
+                           for _ in range(20)]).int()
+        dw = torch.randn(20, k, generator=g)
+        d = torch.empty(20, 12, device="cuda")
+        dgm.dg_route_topk_bwd(d, dw.cuda(), logits.cuda(), idx.cuda(), score=int(sigmoid), renorm=True)
+        s = scores64(logits, sigmoid)
+        sj, w = s.gather(1, idx.long()), dw.double()
+        tot = sj.sum(1, keepdim=True) + 1e-20
+        terms = (w[:, :, None] - w[:, None, :]) * sj[:, None, :]
+        ds = (terms.sum(2) + 1e-20 * w) / tot ** 2
+        mag = (terms.abs().sum(2) + 1e-20 * w.abs()) / tot ** 2
+        full = torch.zeros_like(s).scatter_add(1, idx.long(), ds)
+        most = torch.zeros_like(s).scatter_add(1, idx.long(), mag)
+        if sigmoid:
+            factor, rest = s * (1 - s), 0.0
+        else:
+            # sum_j ds_j s_j: the differences cancel in pairs, (w_j - w_i) s_i s_j + (w_i - w_j) s_j s_i = 0, which
+            # leaves 1e-20 sum_j w_j s_j / S^2 (summed as it stands, 64 bits keep only its rounding, 1e-17)
+            factor, rest = s, 1e-20 * (w * sj).sum(1, keepdim=True) / tot ** 2
+        want = factor * (full - rest)
+        span = (logits.amax(1) - logits.amin(1)).double()[:, None]
+        tol = 2.0 ** -24 * 2 * (span + 40) * (s * (most + (abs(rest) if not sigmoid else 0.0))) + 1e-37
+        assert bool(((d.cpu().double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_gradient_against_differences(dgm, sigmoid, renorm):
     # Central differences of the 64-bit weights, the choice held.  h = 1e-4: the
