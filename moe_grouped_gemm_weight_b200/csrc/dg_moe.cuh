@@ -1,6 +1,7 @@
 // dg_moe.cuh -- sm_100a kernels between the routing and the grouped GEMMs:
 // the cast of the tokens into the rows of the grouped layout, the weighted sum
-// of the experts' rows per token, and its gradient.  All are bound by HBM.
+// of the experts' rows per token, and its gradient.  Times are of one B200 in
+// graph replays over inputs larger than L2.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -124,8 +125,12 @@ struct DispatchParams {
 // The cast of dg_cast.cuh's cast_1x128_kernel, a token read and cast once and
 // written to each of its k rows: a half-warp of a CTA takes NB K blocks of a
 // token, as many half-warps side by side as the token has blocks for, so that
-// the copies of a row are written in long runs.  Lane j of the half-warp keeps the token's rows j and
-// j + 16 and writes their scales.
+// the copies of a row are written in long runs.  Lane j of the half-warp keeps
+// the token's rows j and j + 16 and writes their scales.
+//
+// 4096 tokens of 7168 to 32768 rows: 60 us, 5.0 TB/s.  Bound by the sectors
+// written to L2: 7.3 M full ones of codes, and 1.8 M for one 4-byte scale each,
+// since a token's rows lie in k segments (49 us without the scales).
 template <int NB>
 __global__ void __launch_bounds__(kCastThreads)
 dispatch_1x128_kernel(const DispatchParams p) {
@@ -203,7 +208,8 @@ struct CombineParams {
 };
 
 // out[t] = sum_j w_j Y[row_j]: one thread per 8 columns of a token, its rows'
-// loads in flight together, FP32 sums in slot order.
+// loads in flight together, FP32 sums in slot order.  Bound by HBM: 4096 tokens
+// with 29500 rows of 7168 in 77 us, 6.2 TB/s.
 __global__ void __launch_bounds__(kCombineThreads)
 combine_kernel(const CombineParams p) {
     griddep_wait();
@@ -408,7 +414,12 @@ constexpr int kCombineBwdStage = 2 * 128 * 128 * 2;  // bytes: a tile of dout an
 // Each thread copies the 16-byte pieces that it will use itself to shared
 // memory (cp.async), takes them into registers when they have landed and at
 // once asks for the next tile's, so HBM works during the casts and no barrier
-// guards the buffer.
+// guards the buffer.  Two CTAs of 256 threads an SM: with 512 threads each the
+// issue slots fill better (56 against 47 %), but a tile takes a quarter more
+// instructions; both 219 us before the last steps.
+//
+// 32768 rows of 7168: 207 us, 4.9 TB/s (the casts alone 170 us, without loads
+// and stores).
 __global__ void __launch_bounds__(kCombineBwdThreads, 2)
 combine_bwd_kernel(const CombineBwdParams p) {
     constexpr int T = kCombineBwdThreads, R = CastTile<T>::kRows;
