@@ -357,7 +357,8 @@ DG_API int dg_get_layout_rows(int T, int k, int E);
  *                  last (contiguous: dg_k_grouped_fp8_gemm_tn's k_offsets)
  *   counts         int32 [E]: rows of each group that hold a slot (masked:
  *                  dg_grouped_masked_nt's masked_m)
- * All outputs are written whole.  E <= 1024, k <= 32, T*k < 2^31 - 2^20 (in every call here).
+ * All outputs are written whole.  E <= 1024, k <= 32, and in every call here T*k and
+ * rows < 2^31 - 2^20 and rows of at most 2^28 values.
  */
 DG_API dg_status dg_route_layout(int32_t* row_of, int32_t* m_indices, int32_t* slot_of, int32_t* group_offsets,
                                  int32_t* counts, const int32_t* topk_idx, int T, int k, int E, int rows,

@@ -867,8 +867,10 @@ dg_status launch_plain(void (*kern)(P), const P& p, int64_t grid, int threads, i
     return ok();
 }
 
-// Slots of a call: indexes and a grid's stride past the last fit in 31 bits.
+// Slots or rows of a call: an index a grid's stride past the last fits in 31
+// bits.  Columns: so does any position in a row, in bytes.
 constexpr int64_t kMaxSlotCount = 0x7FF00000;
+constexpr int kMaxColumns = 1 << 28;
 
 // Sizes that the routing calls share.
 dg_status check_route(int T, int E, int k, int dtype, int score) {
@@ -888,6 +890,7 @@ dg_status check_slots(int T, int k, int64_t rows) {
     if (T < 0 || k <= 0 || rows < 0)
         return fail(DG_ERR_INVALID_ARG, "bad sizes T=%d k=%d rows=%lld", T, k, static_cast<long long>(rows));
     if (k > kMaxSlots) return fail(DG_ERR_UNSUPPORTED, "k=%d is more than %d", k, kMaxSlots);
+    if (rows > kMaxSlotCount) return fail(DG_ERR_UNSUPPORTED, "rows=%lld is too large", static_cast<long long>(rows));
     if (static_cast<int64_t>(T) * k > kMaxSlotCount) return fail(DG_ERR_UNSUPPORTED, "T*k=%lld is too large", static_cast<long long>(T) * k);
     return DG_OK;
 }
@@ -906,7 +909,8 @@ dg_status check_row_blocks(int64_t rows, int N, const char* name) {
     if (rows < 0 || N <= 0) return fail(DG_ERR_INVALID_ARG, "bad sizes rows=%lld %s=%d", static_cast<long long>(rows), name, N);
     if (rows % 128 != 0) return fail(DG_ERR_INVALID_ARG, "rows=%lld is not a multiple of 128", static_cast<long long>(rows));
     if (N % 128 != 0) return fail(DG_ERR_UNSUPPORTED, "%s=%d must be a multiple of 128", name, N);
-    if (N > (1 << 28)) return fail(DG_ERR_UNSUPPORTED, "%s=%d is too large", name, N);
+    if (N > kMaxColumns) return fail(DG_ERR_UNSUPPORTED, "%s=%d is too large", name, N);
+    if (rows > kMaxSlotCount) return fail(DG_ERR_UNSUPPORTED, "rows=%lld is too large", static_cast<long long>(rows));
     return DG_OK;
 }
 
@@ -1359,7 +1363,7 @@ int dg_get_layout_rows(int T, int k, int E) {
     if (T < 0 || k <= 0 || k > kMaxSlots || E <= 0 || E > dg::kRouteMaxExperts) return -1;
     const int64_t S = static_cast<int64_t>(T) * k;
     const int64_t rows = (S + 127 * (S < E ? S : E)) / 128 * 128;
-    return S <= kMaxSlotCount && rows <= 0x7FFFFFFF ? static_cast<int>(rows) : -1;
+    return S <= kMaxSlotCount && rows <= kMaxSlotCount ? static_cast<int>(rows) : -1;
 }
 
 dg_status dg_route_layout(int32_t* row_of, int32_t* m_indices, int32_t* slot_of, int32_t* group_offsets,
@@ -1373,7 +1377,7 @@ dg_status dg_route_layout(int32_t* row_of, int32_t* m_indices, int32_t* slot_of,
         return fail(DG_ERR_INVALID_ARG, "rows=%d must be %s", rows, max_rows > 0 ? "E*max_rows" : "a multiple of 128");
     if (max_rows == 0) {
         const int need = dg_get_layout_rows(T, k, E);
-        if (need < 0) return fail(DG_ERR_UNSUPPORTED, "the layout's rows do not fit in 31 bits");
+        if (need < 0) return fail(DG_ERR_UNSUPPORTED, "the layout would have too many rows");
         if (rows < need) return fail(DG_ERR_INVALID_ARG, "rows=%d, any choice of experts fits in %d", rows, need);
     }
     const int64_t S = static_cast<int64_t>(T) * k;
@@ -1409,6 +1413,7 @@ dg_status dg_dispatch_fp8_1x128(uint8_t* Q, float* sa, int sa_stride, const uint
     if (s != DG_OK) return s;
     if (K <= 0) return fail(DG_ERR_INVALID_ARG, "bad size K=%d", K);
     if (K % dg::kBK != 0) return fail(DG_ERR_UNSUPPORTED, "K=%d must be a multiple of 128", K);
+    if (K > kMaxColumns) return fail(DG_ERR_UNSUPPORTED, "K=%d is too large", K);
     if ((s = check_scale_layout("sa_stride", sa_stride, rows, group_rows)) != DG_OK) return s;
     if (T == 0 || rows == 0) return ok();
     if (!Q || !sa || !X || !row_of) return fail(DG_ERR_INVALID_ARG, "null pointer");
@@ -1437,6 +1442,7 @@ dg_status dg_combine(uint16_t* out, const uint16_t* Y, const int32_t* row_of, co
     if (s != DG_OK) return s;
     if (N <= 0) return fail(DG_ERR_INVALID_ARG, "bad size N=%d", N);
     if (N % 8 != 0) return fail(DG_ERR_UNSUPPORTED, "N=%d must be a multiple of 8", N);
+    if (N > kMaxColumns) return fail(DG_ERR_UNSUPPORTED, "N=%d is too large", N);
     if (T == 0) return ok();
     if (!out || !row_of || (rows > 0 && !Y)) return fail(DG_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(out) || !aligned16(Y) || !aligned(row_of, 4) || !aligned(w, 4))
@@ -1474,7 +1480,8 @@ dg_status dg_swiglu_fp8(uint8_t* Q, float* sa, int sa_stride, uint8_t* C, float*
                         const int32_t* m_indices, int rows, int F, int group_rows, void* stream) {
     if (rows < 0 || F <= 0) return fail(DG_ERR_INVALID_ARG, "bad sizes rows=%d F=%d", rows, F);
     if (F % dg::kBK != 0) return fail(DG_ERR_UNSUPPORTED, "F=%d must be a multiple of 128", F);
-    if (F > (1 << 28)) return fail(DG_ERR_UNSUPPORTED, "F=%d is too large", F);
+    if (F > kMaxColumns) return fail(DG_ERR_UNSUPPORTED, "F=%d is too large", F);
+    if (rows > kMaxSlotCount) return fail(DG_ERR_UNSUPPORTED, "rows=%d is too large", rows);
     dg_status s = check_scale_layout("sa_stride", sa_stride, rows, group_rows);
     if (s == DG_OK && C) s = check_scale_layout("cs_stride", cs_stride, rows, group_rows);
     if (s != DG_OK) return s;

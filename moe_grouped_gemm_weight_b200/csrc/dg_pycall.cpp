@@ -9,6 +9,7 @@
  * during the call, as ctypes does.
  */
 #define PY_SSIZE_T_CLEAN
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
@@ -19,14 +20,21 @@ static void *g_entry[9];
 
 enum { ROUTE, ROUTE_BWD, LAYOUT, DISPATCH, COMBINE, COMBINE_BWD, SWIGLU, SWIGLU_BWD, RECAST };
 
-/* Argument i as a pointer (a tensor's data, None as null, or a number) or an int; *bad is set where it is none. */
+/*
+ * Argument i as a pointer (a tensor's data, None as null, or a number) or an
+ * int; *bad is set where it is none.  Nothing is looked at once an error is
+ * pending: the tensor test itself throws then.
+ */
 static void *ptr_at(PyObject *const *a, int i) {
+    if (a[i] == Py_None || PyErr_Occurred()) return nullptr;
+    if (PyLong_Check(a[i])) return PyLong_AsVoidPtr(a[i]);
     if (THPVariable_Check(a[i])) return THPVariable_Unpack(a[i]).data_ptr();
-    if (a[i] == Py_None) return nullptr;
-    return PyLong_AsVoidPtr(a[i]);
+    PyErr_Format(PyExc_TypeError, "argument %d is neither a tensor nor an address", i);
+    return nullptr;
 }
 static int int_at(PyObject *const *a, int i, int *bad) {
     int over = 0;
+    if (PyErr_Occurred()) return 0;
     const long v = PyLong_AsLongAndOverflow(a[i], &over);
     if (over || v > 0x7FFFFFFFL || v < -0x7FFFFFFFL - 1) {
         *bad = 1;
@@ -47,6 +55,19 @@ struct Ptr {
 #define P(i) ptr_at(a, i)
 #define I(i) int_at(a, i, &bad)
 
+/* What torch throws becomes a Python error: no exception leaves an entry. */
+#define NO_THROW_BEGIN try {
+#define NO_THROW_END                                                                              \
+    }                                                                                             \
+    catch (python_error & e) {                                                                    \
+        e.restore();                                                                              \
+        return NULL;                                                                              \
+    }                                                                                             \
+    catch (const std::exception &e) {                                                             \
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());                     \
+        return NULL;                                                                              \
+    }
+
 /* Defines a vector call of `count` arguments; `call` uses P(i), I(i) and `fn`. */
 #define ENTRY(name, slot, count, call)                                                            \
     static PyObject *py_##name(PyObject *self, PyObject *const *a, Py_ssize_t n) {                     \
@@ -55,8 +76,10 @@ struct Ptr {
         (void)self;                                                                               \
         if (n != (count)) return PyErr_Format(PyExc_TypeError, #name " takes %d arguments", count); \
         if (!g_entry[slot]) return PyErr_Format(PyExc_RuntimeError, #name " is not bound");       \
+        NO_THROW_BEGIN                                                                            \
         call;                                                                                     \
         return PyLong_FromLong((long)s);                                                          \
+        NO_THROW_END                                                                              \
     }
 #define CHECKED                                                                                   \
     if (PyErr_Occurred()) return NULL;                                                            \
@@ -74,13 +97,13 @@ ENTRY(dg_route_topk, ROUTE, 15, {
     Ptr p0{P(0)}; Ptr p1{P(1)}; Ptr p2{P(2)}; Ptr p4{P(4)}; Ptr st{P(14)};
     int dt = I(3); int T = I(5); int E = I(6); int k = I(7); int ng = I(8); int tg = I(9); int gt = I(10);
     int sc = I(11); int rn = I(12);
-    float f = (float)PyFloat_AsDouble(a[13]);
+    float f = PyErr_Occurred() ? 0.f : (float)PyFloat_AsDouble(a[13]);
     RUN(dg_route_topk, ROUTE, p0, p1, p2, dt, p4, T, E, k, ng, tg, gt, sc, rn, f, st);
 })
 ENTRY(dg_route_topk_bwd, ROUTE_BWD, 12, {
     Ptr p0{P(0)}; Ptr p1{P(1)}; Ptr p2{P(2)}; Ptr p4{P(4)}; Ptr st{P(11)};
     int dt = I(3); int T = I(5); int E = I(6); int k = I(7); int sc = I(8); int rn = I(9);
-    float f = (float)PyFloat_AsDouble(a[10]);
+    float f = PyErr_Occurred() ? 0.f : (float)PyFloat_AsDouble(a[10]);
     RUN(dg_route_topk_bwd, ROUTE_BWD, p0, p1, p2, dt, p4, T, E, k, sc, rn, f, st);
 })
 ENTRY(dg_route_layout, LAYOUT, 12, {
@@ -135,7 +158,9 @@ static const char *const kNames[9] = {"dg_route_topk", "dg_route_topk_bwd", "dg_
 static PyObject *fits(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
     if (n < 1 || n % 3 != 1) return PyErr_Format(PyExc_TypeError, "fits takes a device and triples");
+    NO_THROW_BEGIN
     const long device = PyLong_AsLong(a[0]);
+    if (PyErr_Occurred()) return NULL;
     for (Py_ssize_t i = 1; i < n; i += 3) {
         if (a[i] == Py_None) continue;
         if (!THPVariable_Check(a[i])) Py_RETURN_FALSE;
@@ -151,6 +176,7 @@ static PyObject *fits(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         if (!right || t.numel() < need || !t.is_contiguous() || !t.is_cuda() || t.get_device() != device) Py_RETURN_FALSE;
     }
     Py_RETURN_TRUE;
+    NO_THROW_END
 }
 
 /* bind(name, address): the C ABI function behind a call. */

@@ -54,16 +54,18 @@ REFUSALS = [
     ("dg_route_layout", LAYOUT, [
         (dict(T=-1), INV), (dict(k=0), INV), (dict(k=33), UNS), (dict(E=0), INV), (dict(E=1025), UNS),
         (dict(rows=-128), INV), (dict(rows=385), INV), (dict(rows=256), INV), (dict(max_rows=-1), INV),
-        (dict(max_rows=100), INV), (dict(T=1 << 30), UNS), (dict(T=(1 << 30) - 1, rows=2147483520), UNS),
+        (dict(max_rows=100), INV), (dict(T=1 << 30), UNS), (dict(T=(1 << 30) - 1, rows=2147483520), UNS), (dict(rows=0x7FF00080), UNS),
+        (dict(T=0x3FF80000, k=2, E=1000), UNS),
         (dict(row_of=0), INV), (dict(m_indices=0), INV), (dict(slot_of=0), INV), (dict(offsets=0), INV),
         (dict(counts=0), INV), (dict(idx=0), INV), (dict(idx=FAKE + 2), MIS), (dict(counts=FAKE + 1), MIS)]),
     ("dg_dispatch_fp8_1x128", DISPATCH, [
-        (dict(T=-1), INV), (dict(k=33), UNS), (dict(K=0), INV), (dict(K=192), UNS), (dict(stride=383), INV),
+        (dict(T=-1), INV), (dict(k=33), UNS), (dict(K=0), INV), (dict(K=192), UNS), (dict(K=(1 << 28) + 128), UNS),
+        (dict(rows=0x7FF00080, stride=0x7FF00080), UNS), (dict(stride=383), INV),
         (dict(group_rows=-1), INV), (dict(group_rows=100), INV), (dict(group_rows=128, stride=127), INV),
         (dict(Q=0), INV), (dict(sa=0), INV), (dict(X=0), INV), (dict(row_of=0), INV), (dict(Q=FAKE + 8), MIS),
         (dict(X=FAKE + 8), MIS), (dict(sa=FAKE + 2), MIS), (dict(T=0, X=0), OK), (dict(rows=0, stride=0, Q=0), OK)]),
     ("dg_combine", COMBINE, [
-        (dict(T=-1), INV), (dict(k=0), INV), (dict(k=40), UNS), (dict(N=0), INV), (dict(N=12), UNS),
+        (dict(T=-1), INV), (dict(k=0), INV), (dict(k=40), UNS), (dict(N=0), INV), (dict(N=12), UNS), (dict(N=2147483640), UNS),
         (dict(rows=-1), INV), (dict(out=0), INV), (dict(Y=0), INV), (dict(row_of=0), INV), (dict(out=FAKE + 8), MIS),
         (dict(Y=FAKE + 2), MIS), (dict(w=FAKE + 2), MIS), (dict(T=0, out=0), OK)]),
     ("dg_combine_bwd", COMBINE_BWD, [
@@ -73,7 +75,7 @@ REFUSALS = [
         (dict(dout=0), INV), (dict(Y=0), INV), (dict(row_of=0), INV), (dict(slot_of=0), INV), (dict(w=0), INV),
         (dict(Qc=FAKE + 8), MIS), (dict(dout=FAKE + 2), MIS), (dict(sc=FAKE + 2), MIS), (dict(T=0, dw=0), OK)]),
     ("dg_swiglu_fp8", SWIGLU, [
-        (dict(rows=-1), INV), (dict(F=0), INV), (dict(F=64), UNS), (dict(sa_stride=383), INV),
+        (dict(rows=-1), INV), (dict(F=0), INV), (dict(F=64), UNS), (dict(F=(1 << 28) + 128), UNS), (dict(sa_stride=383), INV),
         (dict(cs_stride=383), INV), (dict(group_rows=-2), INV), (dict(group_rows=100), INV),
         (dict(group_rows=128, sa_stride=128, cs_stride=100), INV), (dict(Q=0), INV), (dict(sa=0), INV),
         (dict(H=0), INV), (dict(cs=0), INV), (dict(H=FAKE + 8), MIS), (dict(C=FAKE + 8), MIS),
@@ -96,6 +98,43 @@ def test_bad_arguments_are_refused_before_any_launch(name, good, changes, want):
     assert getattr(L, name)(*swapped(good, **changes)) == want, L.dg_last_error_message()
     if want != OK:
         assert L.dg_last_error_message()
+
+
+def test_calls_fail_loudly_without_the_extension(monkeypatch):
+    import sys
+    monkeypatch.setattr(dg, "_calls", None)
+    monkeypatch.setitem(sys.modules, dg.__name__ + "._dgcall", None)
+    monkeypatch.delattr(dg, "_dgcall", raising=False)
+    with pytest.raises(RuntimeError, match="_dgcall"):
+        dg.dg_route_topk(**BINDING["dg_route_topk"])
+
+
+def test_marshalling_refuses_numbers_that_do_not_fit():
+    c = dg._marshal()
+    args = swapped(COMBINE, T=0)
+    assert c.dg_combine(*args) == OK
+    for bad in (1 << 31, -(1 << 31) - 1, 1 << 70):
+        with pytest.raises(OverflowError):
+            c.dg_combine(*swapped(COMBINE, T=0, N=bad))
+    with pytest.raises(TypeError):
+        c.dg_combine(*swapped(COMBINE, T=1.5))
+    for bad in ("x", 1.5, [1], object()):
+        with pytest.raises(TypeError):
+            c.dg_combine(*swapped(COMBINE, out=bad))
+        with pytest.raises(TypeError):
+            c.dg_combine(*swapped(COMBINE, T=0, out=bad, k="y"))
+    with pytest.raises(Exception):  # a tensor without memory behind it
+        c.dg_combine(*swapped(COMBINE, T=0, out=torch.zeros(2, 2).to_sparse()))
+    assert not c.fits(0, "x", 4, 1) and not c.fits(0, torch.zeros(3), 4, 3)
+    with pytest.raises(TypeError):
+        c.fits(0, torch.zeros(3), 4)
+    with pytest.raises(TypeError):
+        c.fits(0, torch.zeros(3), "a", 3)
+    with pytest.raises(TypeError):
+        c.dg_route_topk(*swapped(ROUTE, T=0, scale="z"))
+    with pytest.raises(TypeError):
+        c.dg_combine(*args[:-1])
+    assert c.dg_combine(*swapped(COMBINE, T=0, w=None, stream=None)) == OK
 
 
 def test_layout_rows():
