@@ -335,10 +335,9 @@ def dg_grouped_masked_nt(D, A, sa, sa_stride: int, B, sb, masked_m, expected_m: 
                                       _ptr(masked_m), G, Mmax, N, K, int(expected_m), _stream(stream)))
 
 
-def _shape2(func: str, name: str, t):
-    if t is None or t.dim() != 2:
-        raise DGError(func, DG_ERR_INVALID_ARG, f"{name} must be a tensor of rank 2")
-    return t.shape
+def _rank_error(func: str, **tensors) -> DGError:
+    names = [n for n, t in tensors.items() if not hasattr(t, "dim") or t.dim() != 2]
+    return DGError(func, DG_ERR_INVALID_ARG, f"{names[0]} must be a tensor of rank 2")
 
 
 def _shape1(func: str, name: str, t) -> int:
@@ -359,10 +358,9 @@ def _check_tensors(func: str, names: str, *triples) -> int:
     `names` their names.  The extension checks them in one go (a decoding step
     makes these calls every few microseconds); what is wrong is looked up only
     for the message."""
-    cur = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
-    if (_calls or _marshal()).fits(cur, *triples):
-        if cur >= 0:
-            return cur
+    cur = (_calls or _marshal()).fits(*triples)
+    if cur >= 0:
+        return cur
     given = [(name, *triples[3 * i:3 * i + 3]) for i, name in enumerate(names.split()) if triples[3 * i] is not None]
     for name, t, kind, need in given:
         if t.element_size() != 1 if kind == _U8 else t.dtype != _KINDS[kind]:
@@ -375,6 +373,7 @@ def _check_tensors(func: str, names: str, *triples) -> int:
     for name, t, _, _ in given:
         if t.device.type != "cuda":
             raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is not on a CUDA device ({t.device})")
+    cur = torch.cuda.current_device()
     for name, t, _, _ in given:
         if t.get_device() != cur:
             raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is on {t.device}, the current device is cuda:{cur}")
@@ -407,8 +406,11 @@ def dg_route_topk(topk_idx, topk_w, logits, bias=None, n_groups: int = 1, topk_g
     """The k experts of each token: logits [T,E] (bfloat16 or float32), optional
     float32 bias [E] -> int32 topk_idx [T,k] and float32 topk_w [T,k]."""
     func = "dg_route_topk"
-    T, E = _shape2(func, "logits", logits)
-    Ti, k = _shape2(func, "topk_idx", topk_idx)
+    try:
+        T, E = logits.shape
+        Ti, k = topk_idx.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, logits=logits, topk_idx=topk_idx) from None
     _check_dim(func, "token count of topk_idx", Ti, T)
     dt = _logits_dtype(func, logits)
     kind = _BF16 if dt == DG_DTYPE_BF16 else _F32
@@ -424,8 +426,11 @@ def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTM
                       scale: float = 1.0, stream=None) -> None:
     """Gradient of dg_route_topk: float32 dw [T,k] -> dlogits [T,E] (the logits' type)."""
     func = "dg_route_topk_bwd"
-    T, E = _shape2(func, "logits", logits)
-    Ti, k = _shape2(func, "topk_idx", topk_idx)
+    try:
+        T, E = logits.shape
+        Ti, k = topk_idx.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, logits=logits, topk_idx=topk_idx) from None
     _check_dim(func, "token count of topk_idx", Ti, T)
     dt = _logits_dtype(func, logits)
     kind = _BF16 if dt == DG_DTYPE_BF16 else _F32
@@ -450,7 +455,10 @@ def dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx,
     m_indices and slot_of [rows], group_offsets [E+1], counts [E]; contiguous,
     or masked with max_rows rows per group."""
     func = "dg_route_layout"
-    T, k = _shape2(func, "topk_idx", topk_idx)
+    try:
+        T, k = topk_idx.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, topk_idx=topk_idx) from None
     rows, E = _shape1(func, "m_indices", m_indices), _shape1(func, "counts", counts)
     dev = _check_tensors(func, "row_of m_indices slot_of group_offsets counts topk_idx",
                          row_of, _I32, T * k, m_indices, _I32, rows, slot_of, _I32, rows, group_offsets, _I32, E + 1,
@@ -465,8 +473,11 @@ def dg_dispatch_fp8_1x128(Q, sa, sa_stride: int, X, row_of, group_rows: int = 0,
     """Cast bf16 X [T,K] into the rows of the layout: e4m3 Q [rows,K] (or
     [G,M_max,K]) and its transposed scales; group_rows = M_max when masked."""
     func = "dg_dispatch_fp8_1x128"
-    T, K = _shape2(func, "X", X)
-    Ti, k = _shape2(func, "row_of", row_of)
+    try:
+        T, K = X.shape
+        Ti, k = row_of.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, X=X, row_of=row_of) from None
     _check_dim(func, "token count of row_of", Ti, T)
     _check_dim(func, "K of Q", Q.shape[-1], K)
     rows = Q.numel() // K if K else 0
@@ -483,8 +494,11 @@ def dg_combine(out, Y, row_of, w=None, stream=None) -> None:
     """out [T,N] = sum over slots of w [T,k] (None: ones) times the rows of Y
     ([rows,N] or [G,M_max,N]), bf16; without w the backward pass of the dispatch."""
     func = "dg_combine"
-    T, N = _shape2(func, "out", out)
-    Ti, k = _shape2(func, "row_of", row_of)
+    try:
+        T, N = out.shape
+        Ti, k = row_of.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, out=out, row_of=row_of) from None
     _check_dim(func, "token count of row_of", Ti, T)
     _check_dim(func, "N of Y", Y.shape[-1], N)
     rows = Y.numel() // N if N else 0
@@ -500,9 +514,12 @@ def dg_combine_bwd(dw, Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, dout, Y, 
     """Gradient of dg_combine (contiguous layout): dout [T,N] -> dY [rows,N]
     cast per 1x128 (Qr, sr) and per 128x1 (Qc, sc), and float32 dw [T,k]."""
     func = "dg_combine_bwd"
-    T, N = _shape2(func, "dout", dout)
-    Ti, k = _shape2(func, "row_of", row_of)
-    rows, Ny = _shape2(func, "Y", Y)
+    try:
+        T, N = dout.shape
+        Ti, k = row_of.shape
+        rows, Ny = Y.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, dout=dout, row_of=row_of, Y=Y) from None
     _check_dim(func, "token count of row_of", Ti, T)
     _check_dim(func, "N of Y", Ny, N)
     dev = _check_tensors(func, "dw Qr sr Qc sc dout Y row_of slot_of w",
@@ -541,7 +558,10 @@ def dg_swiglu_fp8_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, Qa, sb, dA
     dA [rows,F] -> dH [rows,2F] cast per 1x128 (Qr, sr) and per 128x1 (Qc, sc),
     and the activation again per 128x128 (Qa [rows,F], sb [F/128, rows/128])."""
     func = "dg_swiglu_fp8_bwd"
-    rows, F = _shape2(func, "dA", dA)
+    try:
+        rows, F = dA.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, dA=dA) from None
     _check_dim(func, "last extent of C", C.shape[-1], 2 * F)
     dev = _check_tensors(func, "Qr sr Qc sc Qa sb dA C cs m_indices",
                          Qr, _U8, rows * 2 * F, sr, _F32, _sa_need(2 * _cdiv(F, 128), sr_stride, rows),
@@ -559,7 +579,10 @@ def dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride: int, m_indices=None, strea
     """e4m3 Q [rows,K] with scales per 1x128 -> Qb [rows,K] with scales per
     128x128, sb [K/128, rows/128] (contiguous layout)."""
     func = "dg_fp8_1x128_to_128x128"
-    rows, K = _shape2(func, "Q", Q)
+    try:
+        rows, K = Q.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, Q=Q) from None
     dev = _check_tensors(func, "Qb sb Q sa m_indices",
                          Qb, _U8, rows * K, sb, _F32, _cdiv(K, 128) * _cdiv(rows, 128), Q, _U8, rows * K,
                          sa, _F32, _sa_need(_cdiv(K, 128), sa_stride, rows), m_indices, _I32, rows)

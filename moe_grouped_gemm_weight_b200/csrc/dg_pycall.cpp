@@ -9,6 +9,7 @@
  * during the call, as ctypes does.
  */
 #define PY_SSIZE_T_CLEAN
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -151,31 +152,33 @@ static const char *const kNames[9] = {"dg_route_topk", "dg_route_topk_bwd", "dg_
                                       "dg_fp8_1x128_to_128x128"};
 
 /*
- * fits(device, tensor, kind, need, ...): whether every tensor (None: absent)
- * has the kind's elements, is contiguous, holds `need` of them and lies on that
- * CUDA device.  Kinds: 1 any one-byte elements, 2 bfloat16, 4 float32, 5 int32.
+ * fits(tensor, kind, need, ...): the current CUDA device's index if every
+ * tensor (None: absent) has the kind's elements, is contiguous, holds `need` of
+ * them and lies on that device, else -1.  Kinds: 1 any one-byte elements, 2
+ * bfloat16, 4 float32, 5 int32.
  */
 static PyObject *fits(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
-    if (n < 1 || n % 3 != 1) return PyErr_Format(PyExc_TypeError, "fits takes a device and triples");
+    if (n < 3 || n % 3 != 0) return PyErr_Format(PyExc_TypeError, "fits takes triples");
     NO_THROW_BEGIN
-    const long device = PyLong_AsLong(a[0]);
-    if (PyErr_Occurred()) return NULL;
-    for (Py_ssize_t i = 1; i < n; i += 3) {
+    long device = -1;
+    for (Py_ssize_t i = 0; i < n; i += 3) {
         if (a[i] == Py_None) continue;
-        if (!THPVariable_Check(a[i])) Py_RETURN_FALSE;
+        if (!THPVariable_Check(a[i])) return PyLong_FromLong(-1);
         const at::Tensor &t = THPVariable_Unpack(a[i]);
         const long kind = PyLong_AsLong(a[i + 1]);
-        const long long need = PyLong_AsLongLong(a[i + 2]);
+        const long long need = PyErr_Occurred() ? 0 : PyLong_AsLongLong(a[i + 2]);
         if (PyErr_Occurred()) return NULL;
         const at::ScalarType type = t.scalar_type();
         const bool right = kind == 1   ? t.element_size() == 1
                            : kind == 2 ? type == at::kBFloat16
                            : kind == 4 ? type == at::kFloat
                                        : type == at::kInt;
-        if (!right || t.numel() < need || !t.is_contiguous() || !t.is_cuda() || t.get_device() != device) Py_RETURN_FALSE;
+        if (!right || t.numel() < need || !t.is_contiguous() || !t.is_cuda()) return PyLong_FromLong(-1);
+        if (device < 0) device = c10::impl::VirtualGuardImpl(at::kCUDA).getDevice().index();
+        if (t.get_device() != device) return PyLong_FromLong(-1);
     }
-    Py_RETURN_TRUE;
+    return PyLong_FromLong(device);
     NO_THROW_END
 }
 

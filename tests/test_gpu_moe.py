@@ -547,6 +547,15 @@ def test_layer_under_graph_replay_and_on_other_streams(dgm):
     torch.cuda.synchronize()
     ra, rb = ({n: t.clone() for n, t in L.results().items()} for L in (A, B))
 
+    dgm.dg_set_pdl(False)  # launches that do not overlap their predecessors: the same
+    try:
+        A.forward()
+        A.backward()
+        torch.cuda.synchronize()
+    finally:
+        dgm.dg_set_pdl(None)
+    assert all(torch.equal(t, ra[n]) for n, t in A.results().items())
+
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     for L in (A, B):
         for t in L.results().values():

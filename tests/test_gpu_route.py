@@ -181,6 +181,32 @@ def test_nan_and_infinity_show(dgm):
             assert np.array_equal(idx, route64(logits, bias, 4, 4, 2, 2, sigmoid, False, 1.0)[0])
 
 
+def off_by_one(t, value=0):
+    """The same tensor one element into a buffer: contiguous, aligned to its elements only."""
+    buf = torch.full((t.numel() + 1,), value, dtype=t.dtype, device="cuda")
+    v = buf[1:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("E", [64, 256, 1024])
+def test_tensors_aligned_to_their_elements_only(dgm, E):
+    # Whole lanes at aligned addresses take wide loads; elsewhere the same values must come out.
+    g = torch.Generator().manual_seed(E)
+    for dt in (torch.float32, torch.bfloat16):
+        logits, bias = torch.randn(33, E, generator=g).to(dt).cuda(), (0.1 * torch.randn(E, generator=g)).cuda()
+        dw = torch.randn(33, 6, generator=g).cuda()
+        out = []
+        for shift in (lambda t: t, off_by_one):
+            l, b = shift(logits), shift(bias)
+            idx, w = shift(torch.zeros(33, 6, dtype=torch.int32, device="cuda")), shift(torch.zeros(33, 6, device="cuda"))
+            dgm.dg_route_topk(idx, w, l, b, n_groups=8, topk_groups=3, group_top=2, score=1, renorm=True)
+            d = shift(torch.zeros_like(logits))
+            dgm.dg_route_topk_bwd(d, shift(dw), l, idx, score=0, renorm=True)
+            out.append((idx.clone(), w.clone(), d.clone()))
+        assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
 def test_many_tokens(dgm):
     # Every choice of 20000 tokens, against a sort in 64 bits on the device.
     g = torch.Generator(device="cuda").manual_seed(9)

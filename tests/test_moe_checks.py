@@ -125,11 +125,10 @@ def test_marshalling_refuses_numbers_that_do_not_fit():
             c.dg_combine(*swapped(COMBINE, T=0, out=bad, k="y"))
     with pytest.raises(Exception):  # a tensor without memory behind it
         c.dg_combine(*swapped(COMBINE, T=0, out=torch.zeros(2, 2).to_sparse()))
-    assert not c.fits(0, "x", 4, 1) and not c.fits(0, torch.zeros(3), 4, 3)
-    with pytest.raises(TypeError):
-        c.fits(0, torch.zeros(3), 4)
-    with pytest.raises(TypeError):
-        c.fits(0, torch.zeros(3), "a", 3)
+    assert c.fits("x", 4, 1) == -1 and c.fits(torch.zeros(3), 4, 3) == -1 and c.fits(None, 4, 3) == -1
+    for bad in ((), (torch.zeros(3), 4), (torch.zeros(3), "a", 3), (torch.zeros(3), 4, "a")):
+        with pytest.raises(TypeError):
+            c.fits(*bad)
     with pytest.raises(TypeError):
         c.dg_route_topk(*swapped(ROUTE, T=0, scale="z"))
     with pytest.raises(TypeError):
@@ -222,6 +221,16 @@ def test_binding_refuses_short_strided_and_mistyped_tensors(name, arg):
     if t.dim() == 2:
         wide = torch.zeros(t.shape[0], 2 * t.shape[1], dtype=t.dtype)[:, ::2]
         refused(name, {**kw, arg: wide}, "contiguous")
+
+
+@pytest.mark.parametrize("name,arg", [(n, a) for n, a in TENSORS if a in ("logits", "topk_idx", "X", "row_of", "dout", "Y", "dA", "Q")
+                                      and BINDING[n][a].dim() == 2 and (n, a) not in (("dg_dispatch_fp8_1x128", "Q"), ("dg_swiglu_fp8", "Q"))
+                                      and not (n == "dg_combine" and a == "Y")
+                                      and not (n == "dg_route_layout" and a == "row_of")])
+def test_tensors_whose_sizes_count_have_rank_two(name, arg):
+    kw = BINDING[name]
+    refused(name, {**kw, arg: kw[arg].reshape(-1)}, "rank 2")
+    refused(name, {**kw, arg: None}, "rank 2")
 
 
 def test_masked_scale_extents():
