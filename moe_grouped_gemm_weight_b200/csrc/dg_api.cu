@@ -925,13 +925,17 @@ int64_t route_grid(int T) {
 bool full_lanes(int E, int per) { return E == 32 * per && (per & (per - 1)) == 0; }
 
 // CTAs (a cluster) that share a block of 128 rows in combine's gradient.  A
-// wave of `slots` CTAs costs its tiles and about two more to start and join;
-// about half of the blocks that the layout keeps for uneven groups hold a
-// slot.  Measured for 287 of 319 blocks of 56 tiles on 296 slots: 212, 218,
-// 243, 260 us for 1, 2, 4, 8 CTAs a block (wide clusters also wait for a whole
-// cluster's room, and their later waves read dout again).
+// wave of `slots` CTAs costs its tiles and about two more to start and join.
+// Of the blocks that the layout keeps for uneven groups (about one a group)
+// half hold a slot, or nearly all where groups are shorter than a block.
+// Measured for 287 of 319 blocks of 56 tiles on 296 slots: 212, 218, 243, 260
+// us for 1, 2, 4, 8 CTAs a block (wide clusters also wait for a whole cluster's
+// room, and their later waves read dout again).
 int combine_bwd_split(int64_t slots_held, int64_t blocks, int nkb, int slots) {
-    const int64_t full = cdiv64(slots_held, 128), live = full < blocks ? full + (blocks - full) / 2 : blocks;
+    const int64_t full = cdiv64(slots_held, 128), spare = full < blocks ? blocks - full : 0;
+    const int64_t uneven = full + spare / 2, sparse = slots_held < spare ? slots_held : spare;
+    int64_t live = uneven > sparse ? uneven : sparse;
+    live = live < blocks ? live : blocks;
     int best = 1;
     int64_t best_cost = 0;
     for (int c = 1; c <= 8 && c <= nkb; c *= 2) {
