@@ -684,10 +684,12 @@ __device__ __forceinline__ void store_logits(uint16_t* p, const float (&f)[N]) {
 // w_j = scale s_j (/ S, S = sum_j s_j + eps):  ds_j = scale dw_j, or
 // scale/S (dw_j - sum_i dw_i s_i / S).  Sigmoid: dl = ds s (1 - s) at the
 // chosen experts, zero elsewhere; softmax: dl_e = s_e (ds_e - sum_j ds_j s_j).
-// Warps take tokens in turn; only softmax reads the whole row.  The k gradients
-// meet their experts through a row of shared memory.  What the next token needs
-// is on its way meanwhile.  16384 tokens of 256 float32 logits, softmax: 11.9 us,
-// 2.9 TB/s, bound by instructions and the shuffles' latency (HBM alone 5.4 us).
+// Warps take tokens in turn; only softmax reads the whole row.  The chosen
+// experts' scores come from the row's in shared memory; the row is stored as it
+// is without a choice, then the k elements (a row put together in shared memory
+// first took 11.9 us below).  What the next token needs is on its way meanwhile.
+// 16384 tokens of 256 float32 logits, softmax: 9.6 us, 3.6 TB/s, bound by
+// instructions (issue slots 70% used; HBM alone 5.4 us).
 template <int EPL, typename L>
 __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteCtas : 1)
 route_topk_bwd_kernel(const RouteBwdParams p) {
@@ -727,7 +729,6 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             e = -1;
             g = 0.f;
         }
-        const int place = e >= 0 ? e / p.per * EPL + e % p.per : 0;  // of the expert in `line`
         if (p.softmax) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) d[i] = next_d[i];
@@ -753,23 +754,16 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             for (int i = 0; i < EPL; ++i) d[i] *= rz;
             store_logits<EPL>(line + lane * EPL, d);
             __syncwarp();
-            if (e >= 0) s = line[place];
+            if (e >= 0) s = line[e / p.per * EPL + e % p.per];
         } else if (e >= 0) {
             s = sigmoid_f(logit_at(static_cast<const L*>(p.logits) + static_cast<int64_t>(t) * p.E + e));
         }
-        // Two sums over the k slots (lanes past them hold zeros), side by side.
-        float dot = g * s, total = s;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            total += __shfl_xor_sync(0xffffffffu, total, o);
-        }
-        // The slots among themselves, through shared memory.
-        if (lane < kRouteMaxK) slots[lane] = make_float4(g, s, __int_as_float(e), 0.f);  // past k: zeros, expert -1
+        // The slots among themselves, through shared memory; past k: zeros, expert -1.
+        if (lane < kRouteMaxK) slots[lane] = make_float4(g, s, __int_as_float(e), 0.f);
         __syncwarp();
         // g_j - sum_i g_i s_i / S = (sum_i (g_j - g_i) s_i + g_j eps) / S: nothing cancels
         // where one expert has nearly all the weight, or is the only one.
-        float diff = g * kRouteEps;
+        float diff = g * kRouteEps, total = kRouteEps, dot = 0.f;
         bool first = e >= 0, twice = false;  // an expert in several slots: its first one takes the sum
         for (int j0 = 0; j0 < p.k; j0 += 4) {
             float4 o[4];
@@ -777,6 +771,8 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             for (int j = 0; j < 4; ++j) o[j] = slots[j0 + j];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                total += o[j].y;
+                dot = fmaf(o[j].x, o[j].y, dot);
                 diff = fmaf(g - o[j].x, o[j].y, diff);
                 const bool same = __float_as_int(o[j].z) == e;
                 first = first && !(same && j0 + j < lane);
@@ -784,39 +780,24 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             }
         }
         if (p.renorm) {
-            const float rs = 1.f / (total + kRouteEps);
+            const float rs = 1.f / total;
             g = e < 0 ? 0.f : diff * rs * rs;
             dot = dot * rs * (kRouteEps * rs);  // sum of the new g s: the differences cancel in pairs
         }
-        if (!p.softmax) {
-            g *= s * (1.f - s);
-            dot = 0.f;
-        }
-
-        float r[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) r[i] = 0.f;
-        __syncwarp();
-        store_logits<EPL>(line + lane * EPL, r);
-        float sum = g;
         if (__any_sync(0xffffffffu, twice)) {  // in slot order
-            sum = 0.f;
+            float sum = 0.f;
             for (int j = 0; j < p.k; ++j) {
                 const int ej = __shfl_sync(0xffffffffu, e, j);
                 const float gj = __shfl_sync(0xffffffffu, g, j);
                 sum += ej == e ? gj : 0.f;
             }
+            g = sum;
         }
-        __syncwarp();
-        if (first) line[place] = sum;
-        __syncwarp();
-        load_logits<EPL>(line + lane * EPL, r);
-        __syncwarp();
-        if (p.softmax) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) r[i] = (r[i] - dot) * d[i];
-        }
+        // The row as it is without a choice, then the chosen experts' values over it.
         L* out = static_cast<L*>(p.dlogits) + static_cast<int64_t>(t) * p.E;
+        float r[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) r[i] = p.softmax ? -dot * d[i] : 0.f;
         if (p.vec) {
             store_logits<EPL>(out + lane * EPL, r);
         } else {
@@ -824,6 +805,8 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             for (int i = 0; i < EPL; ++i)
                 if (i < p.per && e0 + i < p.E) store_logit(out + e0 + i, r[i]);
         }
+        __syncwarp();  // orders the two stores of an element; `line` and `slots` have been read
+        if (first) store_logit(out + e, p.softmax ? s * (g - dot) : g * (s * (1.f - s)));
     }
 }
 
