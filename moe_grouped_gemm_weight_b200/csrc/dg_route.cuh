@@ -735,7 +735,7 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         }
         if (p.T - t > stride) load(t + stride);
 
-        float s = 0.f;
+        float s = 0.f, rz = 1.f;
         if (p.softmax) {
             float m = d[0];
 #pragma unroll
@@ -748,13 +748,17 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
                 d[i] = exp_fast(d[i] - m);
                 z += d[i];
             }
-            z = warp_sum(z);
-            const float rz = z > 0.f || z != z ? 1.f / z : 0.f;
+            if (p.per == EPL) {
+                store_logits<EPL>(line + e0, d);
+            } else {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) d[i] *= rz;
-            store_logits<EPL>(line + lane * EPL, d);
+                for (int i = 0; i < EPL; ++i)
+                    if (i < p.per) line[e0 + i] = d[i];
+            }
+            z = warp_sum(z);
             __syncwarp();
-            if (e >= 0) s = line[e / p.per * EPL + e % p.per];
+            rz = z > 0.f || z != z ? 1.f / z : 0.f;
+            if (e >= 0) s = line[e] * rz;
         } else if (e >= 0) {
             s = sigmoid_f(logit_at(static_cast<const L*>(p.logits) + static_cast<int64_t>(t) * p.E + e));
         }
@@ -764,7 +768,8 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         // g_j - sum_i g_i s_i / S = (sum_i (g_j - g_i) s_i + g_j eps) / S: nothing cancels
         // where one expert has nearly all the weight, or is the only one.
         float diff = g * kRouteEps, total = kRouteEps, dot = 0.f;
-        bool first = e >= 0, twice = false;  // an expert in several slots: its first one takes the sum
+        int alike = 0;  // slots with this one's expert
+#pragma unroll 1  // unrolled, its loads spill
         for (int j0 = 0; j0 < p.k; j0 += 4) {
             float4 o[4];
 #pragma unroll
@@ -774,9 +779,7 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
                 total += o[j].y;
                 dot = fmaf(o[j].x, o[j].y, dot);
                 diff = fmaf(g - o[j].x, o[j].y, diff);
-                const bool same = __float_as_int(o[j].z) == e;
-                first = first && !(same && j0 + j < lane);
-                twice = twice || (same && j0 + j != lane && e >= 0);
+                alike += __float_as_int(o[j].z) == e ? 1 : 0;
             }
         }
         if (p.renorm) {
@@ -784,20 +787,23 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             g = e < 0 ? 0.f : diff * rs * rs;
             dot = dot * rs * (kRouteEps * rs);  // sum of the new g s: the differences cancel in pairs
         }
-        if (__any_sync(0xffffffffu, twice)) {  // in slot order
+        bool first = e >= 0;
+        if (__any_sync(0xffffffffu, first && alike > 1)) {  // an expert's first slot takes the sum, in slot order
             float sum = 0.f;
             for (int j = 0; j < p.k; ++j) {
                 const int ej = __shfl_sync(0xffffffffu, e, j);
                 const float gj = __shfl_sync(0xffffffffu, g, j);
                 sum += ej == e ? gj : 0.f;
+                first = first && !(ej == e && j < lane);
             }
             g = sum;
         }
         // The row as it is without a choice, then the chosen experts' values over it.
         L* out = static_cast<L*>(p.dlogits) + static_cast<int64_t>(t) * p.E;
+        const float rest = -dot * rz;
         float r[EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) r[i] = p.softmax ? -dot * d[i] : 0.f;
+        for (int i = 0; i < EPL; ++i) r[i] = p.softmax ? rest * d[i] : 0.f;
         if (p.vec) {
             store_logits<EPL>(out + lane * EPL, r);
         } else {
