@@ -687,13 +687,13 @@ __device__ __forceinline__ void store_logits(uint16_t* p, const float (&f)[N]) {
 // Warps take tokens in turn; only softmax reads the whole row.  The chosen
 // experts' scores come from the row's in shared memory; the row is stored as it
 // is without a choice, then the k elements (a row put together in shared memory
-// first took 11.9 us below).  What the next token needs is on its way meanwhile.
-// 16384 tokens of 256 float32 logits, softmax: 9.6 us, 3.6 TB/s, bound by
-// instructions (issue slots 70% used; HBM alone 5.4 us).
+// first took 11.7 us below).  What the next token needs is on its way meanwhile.
+// 16384 tokens of 256 float32 logits, softmax: 9.5 us, 3.7 TB/s, bound by
+// instructions (328 a token, 67 % of the issue slots; HBM alone 5.4 us).
 template <int EPL, typename L>
 __global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteCtas : 1)
 route_topk_bwd_kernel(const RouteBwdParams p) {
-    extern __shared__ __align__(16) float route_smem[];  // per warp 32 * EPL values, then 16 slots
+    extern __shared__ __align__(16) float route_smem[];  // per warp a row of 32 * EPL; then per warp 16 slots
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
