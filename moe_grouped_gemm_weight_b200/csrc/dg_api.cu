@@ -915,8 +915,8 @@ dg_status check_row_blocks(int64_t rows, int N, const char* name) {
 }
 
 // CTAs of the routing kernels: those resident at once, or fewer.
-int64_t route_grid(int T) {
-    const int64_t all = cdiv64(T, dg::kRouteWarps), cap = static_cast<int64_t>(effective_sms()) * dg::kRouteCtas;
+int64_t route_grid(int T, int per) {
+    const int64_t all = cdiv64(T, dg::kRouteWarps), cap = static_cast<int64_t>(effective_sms()) * dg::route_ctas(per);
     return all < cap ? all : cap;
 }
 
@@ -948,17 +948,16 @@ int combine_bwd_split(int64_t slots_held, int64_t blocks, int nkb, int slots) {
     return best;
 }
 
-// The routing kernels' instance: lanes hold ceil(E / 32) experts, rounded up
-// to a power of two.
-template <typename L>
+// The routing kernels' instance: a lane's experts, rounded up to a power of two.
+template <typename L, bool kSpans>
 dg_status launch_route(const dg::RouteParams& p, int64_t grid, int smem, void* st) {
-    const int threads = dg::kRouteWarps * 32, per = cdiv(p.E, 32);
-    if (per <= 1) return launch_plain(dg::route_topk_kernel<1, L>, p, grid, threads, smem, 1, st);
-    if (per <= 2) return launch_plain(dg::route_topk_kernel<2, L>, p, grid, threads, smem, 1, st);
-    if (per <= 4) return launch_plain(dg::route_topk_kernel<4, L>, p, grid, threads, smem, 1, st);
-    if (per <= 8) return launch_plain(dg::route_topk_kernel<8, L>, p, grid, threads, smem, 1, st);
-    if (per <= 16) return launch_plain(dg::route_topk_kernel<16, L>, p, grid, threads, smem, 1, st);
-    return launch_plain(dg::route_topk_kernel<32, L>, p, grid, threads, smem, 1, st);
+    const int threads = dg::kRouteWarps * 32, per = p.per;
+    if (per <= 1) return launch_plain(dg::route_topk_kernel<1, kSpans, L>, p, grid, threads, smem, 1, st);
+    if (per <= 2) return launch_plain(dg::route_topk_kernel<2, kSpans, L>, p, grid, threads, smem, 1, st);
+    if (per <= 4) return launch_plain(dg::route_topk_kernel<4, kSpans, L>, p, grid, threads, smem, 1, st);
+    if (per <= 8) return launch_plain(dg::route_topk_kernel<8, kSpans, L>, p, grid, threads, smem, 1, st);
+    if (per <= 16) return launch_plain(dg::route_topk_kernel<16, kSpans, L>, p, grid, threads, smem, 1, st);
+    return launch_plain(dg::route_topk_kernel<32, kSpans, L>, p, grid, threads, smem, 1, st);
 }
 
 template <typename L, int EPL>
@@ -1329,18 +1328,31 @@ dg_status dg_route_topk(int32_t* topk_idx, float* topk_w, const void* logits, in
     // Keeping every group is the same as having none.
     const int groups = topk_groups == n_groups ? 1 : n_groups;
     const int gsize = E / groups;
-    const int per = cdiv(E, 32), gl = gsize % per == 0 ? gsize / per : 0;
-    // Groups of whole lanes need no shared memory; every group's lanes join in a power of two.
-    const int group_shift = groups > 1 && gl > 0 && (gl & (gl - 1)) == 0 ? __builtin_ctz(gl) : -1;
+    // Lanes of its own for every group, a power of two, unless one would hold more than 32 experts.
+    const int flat = cdiv(E, 32);
+    int per = flat, span = E, span_shift = 5;
+    if (groups > 1) {
+        int sh = 0;
+        while ((2 << sh) * groups <= 32) ++sh;
+        if (cdiv(gsize, 1 << sh) <= 32) {
+            per = cdiv(gsize, 1 << sh);
+            span = gsize;
+            span_shift = sh;
+        }
+    }
+    const bool group_lanes = span < E;
     dg::RouteParams p{logits, bias, topk_idx, topk_w, T, E, k, groups, groups == 1 ? 1 : topk_groups, group_top, gsize,
-                      (1u << 20) / static_cast<uint32_t>(gsize) + 1u, per, group_shift,
+                      (1u << 20) / static_cast<uint32_t>(gsize) + 1u, flat, per, span, span_shift, group_lanes,
                       full_lanes(E, per) && aligned16(logits) && aligned16(bias), score == DG_SCORE_SOFTMAX, renorm != 0,
                       scale};
-    const int64_t grid = route_grid(T);
+    const int64_t grid = route_grid(T, per);
     if (grid == 0) return fail(DG_ERR_CUDA, "no CUDA device");
-    const int smem = groups > 1 && group_shift < 0 ? dg::kRouteWarps * E * static_cast<int>(sizeof(float)) : 0;
-    return logits_dtype == DG_DTYPE_BF16 ? launch_route<uint16_t>(p, grid, smem, stream)
-                                         : launch_route<float>(p, grid, smem, stream);
+    const int smem = groups > 1 && !group_lanes ? dg::kRouteWarps * E * static_cast<int>(sizeof(float)) : 0;
+    if (group_lanes && span != per << span_shift)
+        return logits_dtype == DG_DTYPE_BF16 ? launch_route<uint16_t, true>(p, grid, smem, stream)
+                                             : launch_route<float, true>(p, grid, smem, stream);
+    return logits_dtype == DG_DTYPE_BF16 ? launch_route<uint16_t, false>(p, grid, smem, stream)
+                                         : launch_route<float, false>(p, grid, smem, stream);
 }
 
 dg_status dg_route_topk_bwd(void* dlogits, const float* dw, const void* logits, int logits_dtype,
@@ -1357,7 +1369,7 @@ dg_status dg_route_topk_bwd(void* dlogits, const float* dw, const void* logits, 
     dg::RouteBwdParams p{dlogits, dw, logits, topk_idx, T, E, k, per,
                          full_lanes(E, per) && aligned16(logits) && aligned16(dlogits), score == DG_SCORE_SOFTMAX,
                          renorm != 0, scale};
-    const int64_t grid = route_grid(T);
+    const int64_t grid = route_grid(T, per);
     if (grid == 0) return fail(DG_ERR_CUDA, "no CUDA device");
     return logits_dtype == DG_DTYPE_BF16 ? launch_route_bwd<uint16_t>(p, grid, stream)
                                          : launch_route_bwd<float>(p, grid, stream);

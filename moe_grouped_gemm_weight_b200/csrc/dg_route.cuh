@@ -15,7 +15,8 @@
 namespace dg {
 
 constexpr int kRouteWarps = 8;
-constexpr int kRouteCtas = 4;        // resident per SM (up to 256 experts)
+// CTAs resident per SM where a lane holds up to `epl` experts.
+constexpr int route_ctas(int epl) { return epl <= 8 ? 4 : epl <= 16 ? 2 : 1; }
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxK = 16;       // lanes 0..k hold the k choices and the runner-up
 constexpr int kRouteMaxGroups = 32;  // one lane at least per group
@@ -30,11 +31,24 @@ struct RouteParams {
     int groups, keep, gtop;
     int gsize;            // E / groups
     uint32_t gsize_magic; // e / gsize == (e * gsize_magic) >> 20 for e < 1024
-    int per;              // experts per lane: lane i holds i * per .. i * per + per - 1
-    int group_shift;      // log2 of the lanes per group where groups are whole lanes, else -1
+    int flat;             // ceil(E / 32)
+    int per;              // experts per lane, at most
+    int span, span_shift; // groups with lanes of their own: 1 << span_shift lanes hold the `span` experts of one
+    int group_lanes;      // ... there are such
     int vec;              // every lane full, rows and bias 16-byte aligned: wide loads
     int softmax, renorm;
     float scale;
+
+    // The first expert of a lane, and how many it has (none: <= 0).
+    template <bool kSpans>
+    __device__ __forceinline__ int first_of(int lane) const {
+        return kSpans ? (lane >> span_shift) * span + (lane & ((1 << span_shift) - 1)) * per : lane * per;
+    }
+    template <bool kSpans>
+    __device__ __forceinline__ int count_of(int lane) const {
+        if (!kSpans) return min(per, E - lane * per);
+        return (lane >> span_shift) * span < E ? min(per, span - (lane & ((1 << span_shift) - 1)) * per) : 0;
+    }
 };
 
 __device__ __forceinline__ float logit_at(const float* p) { return *p; }
@@ -142,8 +156,8 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const L* row) {
     if (p.softmax) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int e = lane * p.per + i;
-            if (i < p.per && e < p.E) {
+            const int e = lane * p.flat + i;
+            if (i < p.flat && e < p.E) {
                 const double l = logit_at(row + e);
                 m = l > m ? l : m;
             }
@@ -155,8 +169,8 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const L* row) {
         z = 0.0;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int e = lane * p.per + i;
-            c[i] = i < p.per && e < p.E ? exp(static_cast<double>(logit_at(row + e)) - m) : 0.0;
+            const int e = lane * p.flat + i;
+            c[i] = i < p.flat && e < p.E ? exp(static_cast<double>(logit_at(row + e)) - m) : 0.0;
             z += c[i];
         }
         for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
@@ -164,9 +178,9 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const L* row) {
     unsigned long long key[EPL];  // of the choice value, 0: not eligible
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        const int e = lane * p.per + i;
+        const int e = lane * p.flat + i;
         key[i] = 0;
-        if (i < p.per && e < p.E) {
+        if (i < p.flat && e < p.E) {
             const float l = logit_at(row + e);
             const float b = p.bias ? p.bias[e] : 0.f;
             const double s = p.softmax ? c[i] / z : 1.0 / (1.0 + exp(-static_cast<double>(l)));
@@ -184,7 +198,7 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const L* row) {
                 int at = 0x7FFFFFFF;
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
-                    const int e = lane * p.per + i;
+                    const int e = lane * p.flat + i;
                     const int grp = static_cast<int>((static_cast<uint32_t>(e) * p.gsize_magic) >> 20);
                     if (grp == g && e != taken && key[i] > best) { best = key[i]; at = e; }
                 }
@@ -208,14 +222,14 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const L* row) {
         const uint32_t kept = __ballot_sync(0xffffffffu, lane < p.groups && mine != 0 && rank < p.keep);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const uint32_t grp = (static_cast<uint32_t>(lane * p.per + i) * p.gsize_magic) >> 20;
+            const uint32_t grp = (static_cast<uint32_t>(lane * p.flat + i) * p.gsize_magic) >> 20;
             if (!((kept >> (grp & 31u)) & 1u)) key[i] = 0;
         }
     }
     if (!p.bias) {  // in the order of the logits themselves
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (key[i]) key[i] = order_key(static_cast<double>(logit_at(row + lane * p.per + i)));
+            if (key[i]) key[i] = order_key(static_cast<double>(logit_at(row + lane * p.flat + i)));
     }
     int my = -1;
     for (int j = 0; j < p.k; ++j) {
@@ -223,24 +237,24 @@ __device__ __noinline__ int choose_exact(const RouteParams& p, const L* row) {
         int at = 0x7FFFFFFF;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (key[i] > best) { best = key[i]; at = lane * p.per + i; }
+            if (key[i] > best) { best = key[i]; at = lane * p.flat + i; }
         const unsigned long long top = warp_max_u64(best);
         if (top == 0) break;
         at = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7FFFFFFF);
         if (lane == j) my = at;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (lane * p.per + i == at) key[i] = 0;
+            if (lane * p.flat + i == at) key[i] = 0;
     }
     return my;
 }
 
-// The groups kept, decided in FP64 where groups are whole lanes: a lane's two
-// best experts are e1 and e2 (-1: none; no third is close to them).  Returns
+// The groups kept, decided in FP64 where groups have their own lanes: a lane's
+// two best experts are e1 and e2 (-1: none; no third is close to them).  Returns
 // whether this lane's group is kept.
 template <typename L>
 __device__ __noinline__ bool keep_groups_exact(const RouteParams& p, const L* row, int e1, int e2) {
-    const int lane = threadIdx.x & 31, lanes = 1 << p.group_shift, g = lane >> p.group_shift;
+    const int lane = threadIdx.x & 31, lanes = 1 << p.span_shift, g = lane >> p.span_shift;
     double m = 0.0, z = 1.0;
     if (p.softmax) {
         m = -INFINITY;
@@ -340,8 +354,12 @@ struct Top4 {
     }
 };
 
-// Warps take tokens in turn, a token to a warp, lane i holding the experts
-// i * per ..; the next token's logits are on their way meanwhile.
+// Warps take tokens in turn, a token to a warp; the next token's logits are on
+// their way meanwhile.  Lane after lane holds consecutive experts, lane i from
+// i * per on; kSpans: groups do not end with a lane so, and each starts a lane of
+// its own (65536 tokens of 408 experts in 8 groups: 100 us, against 160 with the
+// groups read from shared memory, which is left for rows of over 512 experts
+// whose lanes would hold more than 32).
 //
 // The choice works on keys: a value's leading bits in integer order, and in
 // its low bits the expert's place (lane, then place in the lane, counted down),
@@ -356,17 +374,18 @@ struct Top4 {
 // 16384 tokens of 256 float32 logits, 8 groups, bias: 18.5 us on one B200 in
 // graph replays (HBM alone 2.6 us), 686 instructions a token at 59 % of the
 // issue slots; 17.0 us without any FP64.
-template <int EPL, typename L>
-__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteCtas : 1)
+template <int EPL, bool kSpans, typename L>
+__global__ void __launch_bounds__(kRouteWarps * 32, route_ctas(EPL))
 route_topk_kernel(const RouteParams p) {
     constexpr int kMask = 32 * EPL - 1;  // a key's place bits
     constexpr bool kShort = sizeof(L) == 2;
-    extern __shared__ float route_smem[];  // groups that are not whole lanes: E values per warp
+    // Lanes that would hold more than 32 experts of a group: only rows of over 512 have such.
+    const bool group_lanes = kSpans || EPL < 32 || p.group_lanes;
+    extern __shared__ float route_smem[];  // groups without lanes of their own: E values per warp
     __shared__ uint16_t cand_smem[kRouteWarps][32];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e0 = lane * p.per;
     const bool biased = p.bias != nullptr;
     const int lane_bits = (31 - lane) * EPL;
     const int stride = gridDim.x * kRouteWarps;
@@ -378,8 +397,9 @@ route_topk_kernel(const RouteParams p) {
         if (p.vec) {
             load_logits<EPL>(row + lane * EPL, v);
         } else {
+            const int e0 = p.first_of<kSpans>(lane), held = p.count_of<kSpans>(lane);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) v[i] = i < p.per && e0 + i < p.E ? logit_at(row + e0 + i) : -INFINITY;
+            for (int i = 0; i < EPL; ++i) v[i] = i < held ? logit_at(row + e0 + i) : -INFINITY;
         }
     };
     float bias[EPL], fetched[EPL];
@@ -388,8 +408,9 @@ route_topk_kernel(const RouteParams p) {
         if (p.vec) {
             load_logits<EPL>(p.bias + lane * EPL, bias);
         } else {
+            const int e0 = p.first_of<kSpans>(lane), held = p.count_of<kSpans>(lane);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) bias[i] = i < p.per && e0 + i < p.E ? p.bias[e0 + i] : -INFINITY;
+            for (int i = 0; i < EPL; ++i) bias[i] = i < held ? p.bias[e0 + i] : -INFINITY;
         }
     }
 
@@ -450,7 +471,7 @@ route_topk_kernel(const RouteParams p) {
             int g, sh;                           // this lane's group, log2 of lanes per group
             // A choice value without a bias is the score of the logit.
             auto choice = [&](float x) { return x == -INFINITY || biased ? x : score(x); };
-            if (p.group_shift >= 0) {
+            if (group_lanes) {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
                     b = fmaxf(b, fminf(a, v[i]));
@@ -458,22 +479,23 @@ route_topk_kernel(const RouteParams p) {
                 }
                 a = choice(a);
                 b = choice(b);
-                sh = p.group_shift;
+                sh = p.span_shift;
                 g = lane >> sh;
             } else {
                 // A power of two of lanes share a group in shared memory.
                 float* cs = route_smem + warp * p.E;
+                const int e0 = p.first_of<kSpans>(lane), held = p.count_of<kSpans>(lane);
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if (i < p.per && e0 + i < p.E) cs[e0 + i] = choice(v[i]);
+                    if (i < held) cs[e0 + i] = choice(v[i]);
                 __syncwarp();
                 sh = 31 - __clz(32 / p.groups);
                 g = lane >> sh;
                 if (g < p.groups) {
-                    const int lanes = 1 << sh, sub = lane & (lanes - 1);
+                    const int lanes = 1 << sh;
                     // Each group starts at another place: the same places of groups of 32 share a bank.
                     const int turn = (g << sh) % p.gsize;
-                    for (int n = sub; n < p.gsize; n += lanes) {
+                    for (int n = lane & (lanes - 1); n < p.gsize; n += lanes) {
                         const float x = cs[g * p.gsize + (n + turn < p.gsize ? n + turn : n + turn - p.gsize)];
                         b = fmaxf(b, fminf(a, x));
                         a = fmaxf(a, x);
@@ -506,22 +528,22 @@ route_topk_kernel(const RouteParams p) {
                 for (int i = 0; i < EPL; ++i) {
                     const bool first = v[i] > b1, second = v[i] > b2;
                     b3 = fmaxf(b3, fminf(b2, v[i]));
-                    e2 = first ? e1 : second ? e0 + i : e2;
-                    e1 = first ? e0 + i : e1;
+                    e2 = first ? e1 : second ? p.first_of<kSpans>(lane) + i : e2;
+                    e1 = first ? p.first_of<kSpans>(lane) + i : e1;
                     b2 = fmaxf(b2, fminf(b1, v[i]));
                     b1 = fmaxf(b1, v[i]);
                 }
                 const bool two = b3 == -INFINITY || b2 - b3 > apart_by(b2, b3) || (!biased && b2 == b3);
-                if (p.group_shift >= 0 && __all_sync(0xffffffffu, two)) kept = keep_groups_exact<L>(p, row, e1, e2);
+                if (group_lanes && __all_sync(0xffffffffu, two)) kept = keep_groups_exact<L>(p, row, e1, e2);
                 else sure = false;
             }
-            if (p.group_shift >= 0) {
+            if (group_lanes) {
                 in = kept;
             } else {
                 const uint32_t on = __ballot_sync(0xffffffffu, kept);
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
-                    const uint32_t grp = (static_cast<uint32_t>(e0 + i) * p.gsize_magic) >> 20;
+                    const uint32_t grp = (static_cast<uint32_t>(p.first_of<kSpans>(lane) + i) * p.gsize_magic) >> 20;
                     if (!((on >> ((grp << sh) & 31u)) & 1u)) v[i] = -INFINITY;
                 }
             }
@@ -561,7 +583,9 @@ route_topk_kernel(const RouteParams p) {
                     if (k1 == best) below = k1 ^ lane_bits;
                 }
             }
-            if (my_key >= kLeastKey && lane <= p.k) my = (31 - (my_key & kMask) / EPL) * p.per + EPL - 1 - (my_key & (EPL - 1));
+            if (my_key >= kLeastKey && lane <= p.k) {
+                my = p.first_of<kSpans>(31 - (my_key & kMask) / EPL) + EPL - 1 - (my_key & (EPL - 1));
+            }
 
             if (!kShort || biased) {
                 // Every chosen key clearly above the next, whatever its low bits hide?
@@ -580,7 +604,7 @@ route_topk_kernel(const RouteParams p) {
                             const bool c = in && key[i] >= least && key[i] >= kLeastKey;
                             const uint32_t who = __ballot_sync(0xffffffffu, c);
                             const int at = n + __popc(who & ((1u << lane) - 1u));
-                            if (c && at < 32) cand_smem[warp][at] = static_cast<uint16_t>(e0 + i);
+                            if (c && at < 32) cand_smem[warp][at] = static_cast<uint16_t>(p.first_of<kSpans>(lane) + i);
                             n += __popc(who);
                         }
                         __syncwarp();
@@ -691,7 +715,7 @@ __device__ __forceinline__ void store_logits(uint16_t* p, const float (&f)[N]) {
 // 16384 tokens of 256 float32 logits, softmax: 9.5 us, 3.7 TB/s, bound by
 // instructions (328 a token, 67 % of the issue slots; HBM alone 5.4 us).
 template <int EPL, typename L>
-__global__ void __launch_bounds__(kRouteWarps * 32, EPL <= 8 ? kRouteCtas : 1)
+__global__ void __launch_bounds__(kRouteWarps * 32, route_ctas(EPL))
 route_topk_bwd_kernel(const RouteBwdParams p) {
     extern __shared__ __align__(16) float route_smem[];  // per warp a row of 32 * EPL; then per warp 16 slots
     griddep_wait();

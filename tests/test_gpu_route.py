@@ -131,6 +131,44 @@ def test_choices_next_to_one_another(dgm, E, groups, gtop, sigmoid):
     check_route(dgm, logits, bias, min(8, E // groups), groups, max(1, groups // 2), gtop, sigmoid)
 
 
+# (E, groups): groups that end inside a lane's equal share, one or several lanes to a group; 930, 990
+# and 1020 experts would give a lane more than 32
+GROUP_EDGES = [(12, 3), (60, 4), (62, 31), (96, 3), (150, 30), (231, 7), (408, 8), (510, 17), (930, 6), (992, 31),
+               (990, 30), (1020, 20)]
+
+
+@pytest.mark.parametrize("E,groups", GROUP_EDGES)
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("gtop", [1, 2])
+def test_groups_that_are_not_equal_shares_of_the_lanes(dgm, E, groups, sigmoid, with_bias, gtop):
+    g = torch.Generator().manual_seed(E + groups)
+    keep = max(1, groups // 3)
+    k = min(8, keep * (E // groups))
+    for dt in (torch.float32, torch.bfloat16):
+        logits = torch.randn(37, E, generator=g).to(dt)
+        logits[3].view(groups, -1)[::2] = -math.inf  # whole groups without an expert
+        logits[4].view(groups, -1)[:, 1:] = -math.inf  # one expert left in each
+        logits[5] = -math.inf
+        logits[6] = 0.25
+        bias = 0.1 * torch.randn(E, generator=g) if with_bias else None
+        check_route(dgm, logits, bias, k, groups, keep, gtop, sigmoid, renorm=True, scale=1.5)
+
+
+@pytest.mark.parametrize("E,groups", GROUP_EDGES)
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_groups_next_to_one_another(dgm, E, groups, sigmoid):
+    # All values equal up to the bias's rounding, and groups whose best two
+    # stand out by as much: no FP32 arithmetic orders the groups.
+    g = torch.Generator().manual_seed(E * 7 + groups)
+    logits = torch.randn(1, E, generator=g)
+    bias = (0.5 - scores64(logits, sigmoid)[0]).float()
+    ahead = bias.clone().view(groups, -1)
+    ahead[:, -2:] += 0.125
+    for b in (bias, ahead.reshape(-1)):
+        check_route(dgm, logits, b, min(2, E // groups), groups, max(1, groups // 2), 2, sigmoid)
+
+
 @pytest.mark.parametrize("groups,keep", [(1, 1), (8, 3)])
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("bias_of", ["none", "zero", "steps"])
