@@ -961,20 +961,21 @@ dg_status launch_route(const dg::RouteParams& p, int64_t grid, int smem, void* s
 }
 
 template <typename L, int EPL>
-dg_status launch_route_bwd_one(const dg::RouteBwdParams& p, int64_t grid, void* st) {
-    return launch_plain(dg::route_topk_bwd_kernel<EPL, L>, p, grid, dg::kRouteWarps * 32,
+dg_status launch_route_bwd_one(const dg::RouteBwdParams& p, bool wide, int64_t grid, void* st) {
+    return launch_plain(wide ? dg::route_topk_bwd_kernel<EPL, true, L> : dg::route_topk_bwd_kernel<EPL, false, L>, p, grid,
+                        dg::kRouteWarps * 32,
                         dg::kRouteWarps * (32 * EPL + 4 * dg::kRouteMaxK) * static_cast<int>(sizeof(float)), 1, st);
 }
 
 template <typename L>
-dg_status launch_route_bwd(const dg::RouteBwdParams& p, int64_t grid, void* st) {
-    const int per = p.per;
-    if (per <= 1) return launch_route_bwd_one<L, 1>(p, grid, st);
-    if (per <= 2) return launch_route_bwd_one<L, 2>(p, grid, st);
-    if (per <= 4) return launch_route_bwd_one<L, 4>(p, grid, st);
-    if (per <= 8) return launch_route_bwd_one<L, 8>(p, grid, st);
-    if (per <= 16) return launch_route_bwd_one<L, 16>(p, grid, st);
-    return launch_route_bwd_one<L, 32>(p, grid, st);
+dg_status launch_route_bwd(const dg::RouteBwdParams& p, bool wide, int64_t grid, void* st) {
+    const int per = cdiv(p.E, 32);
+    if (per <= 1) return launch_route_bwd_one<L, 1>(p, wide, grid, st);
+    if (per <= 2) return launch_route_bwd_one<L, 2>(p, wide, grid, st);
+    if (per <= 4) return launch_route_bwd_one<L, 4>(p, wide, grid, st);
+    if (per <= 8) return launch_route_bwd_one<L, 8>(p, wide, grid, st);
+    if (per <= 16) return launch_route_bwd_one<L, 16>(p, wide, grid, st);
+    return launch_route_bwd_one<L, 32>(p, wide, grid, st);
 }
 
 }  // namespace
@@ -1366,13 +1367,12 @@ dg_status dg_route_topk_bwd(void* dlogits, const float* dw, const void* logits, 
     if (!aligned(topk_idx, 4) || !aligned(dw, 4) || !aligned(logits, el) || !aligned(dlogits, el))
         return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements");
     const int per = cdiv(E, 32);
-    dg::RouteBwdParams p{dlogits, dw, logits, topk_idx, T, E, k, per,
-                         full_lanes(E, per) && aligned16(logits) && aligned16(dlogits), score == DG_SCORE_SOFTMAX,
-                         renorm != 0, scale};
+    const bool whole = full_lanes(E, per), wide = whole && aligned16(logits) && aligned16(dlogits);
+    dg::RouteBwdParams p{dlogits, dw, logits, topk_idx, T, E, k, whole, score == DG_SCORE_SOFTMAX, renorm != 0, scale};
     const int64_t grid = route_grid(T, per);
     if (grid == 0) return fail(DG_ERR_CUDA, "no CUDA device");
-    return logits_dtype == DG_DTYPE_BF16 ? launch_route_bwd<uint16_t>(p, grid, stream)
-                                         : launch_route_bwd<float>(p, grid, stream);
+    return logits_dtype == DG_DTYPE_BF16 ? launch_route_bwd<uint16_t>(p, wide, grid, stream)
+                                         : launch_route_bwd<float>(p, wide, grid, stream);
 }
 
 int dg_get_layout_rows(int T, int k, int E) {

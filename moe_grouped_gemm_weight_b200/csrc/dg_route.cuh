@@ -54,10 +54,10 @@ struct RouteParams {
 __device__ __forceinline__ float logit_at(const float* p) { return *p; }
 __device__ __forceinline__ float logit_at(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
 
-// N consecutive logits with the widest loads (the address is a multiple of
-// the load's width).
+// N consecutive floats with the widest loads (the address is a multiple of the
+// load's width).
 template <int N>
-__device__ __forceinline__ void load_logits(const float* p, float (&f)[N]) {
+__device__ __forceinline__ void load_floats(const float* p, float (&f)[N]) {
     if constexpr (N >= 4) {
 #pragma unroll
         for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(f + i) = *reinterpret_cast<const float4*>(p + i);
@@ -67,27 +67,58 @@ __device__ __forceinline__ void load_logits(const float* p, float (&f)[N]) {
         f[0] = *p;
     }
 }
-template <int N>
-__device__ __forceinline__ void load_logits(const uint16_t* p, float (&f)[N]) {
-    if constexpr (N >= 2) {
-        uint32_t w[N / 2];
-        if constexpr (N >= 8) {
+// The N logits of a row that a lane holds, as they are in memory: turning bf16
+// into floats waits for the load, so it is left to the next token's turn.
+template <int N, typename L>
+struct RawRow {
+    static constexpr bool kPairs = sizeof(L) == 2 && N >= 2;        // wide loads: two to a word
+    static constexpr int kChunk = N < 16 / static_cast<int>(sizeof(L)) ? N : 16 / static_cast<int>(sizeof(L));
+    uint32_t w[N];
+
+    // Chunks of a wide load's kChunk logits, `step` logits apart.
+    __device__ __forceinline__ void load_wide(const L* p, int step) {
+        constexpr int kWords = kPairs ? kChunk / 2 : kChunk;
 #pragma unroll
-            for (int i = 0; i < N / 2; i += 4) *reinterpret_cast<uint4*>(w + i) = *reinterpret_cast<const uint4*>(p + 2 * i);
-        } else if constexpr (N == 4) {
-            *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
-        } else {
-            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        for (int c = 0; c < N / kChunk; ++c) {
+            uint32_t* to = w + c * kWords;
+            const L* at = p + c * step;
+            if constexpr (kWords == 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(at);
+                to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+            } else if constexpr (kWords == 2) {
+                const uint2 v = *reinterpret_cast<const uint2*>(at);
+                to[0] = v.x, to[1] = v.y;
+            } else if constexpr (kPairs) {
+                to[0] = *reinterpret_cast<const uint32_t*>(at);
+            } else {
+                to[0] = bits(at);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-        f[0] = logit_at(p);
     }
-}
+    // One by one, -inf where there is none.
+    __device__ __forceinline__ void load_one(int i, bool there, const L* p) {
+        w[i] = there ? bits(p) : sizeof(L) == 2 ? 0xFF80u : 0xFF800000u;
+    }
+    __device__ __forceinline__ void get(bool wide, float (&f)[N]) const {
+        if constexpr (sizeof(L) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = __uint_as_float(w[i]);
+        } else if (kPairs && wide) {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = __uint_as_float(w[i] << 16);
+        }
+    }
+
+   private:
+    static __device__ __forceinline__ uint32_t bits(const float* p) { return __float_as_uint(*p); }
+    static __device__ __forceinline__ uint32_t bits(const uint16_t* p) { return *p; }
+};
 
 // Order-preserving integer key of a double: a < b <=> key(a) < key(b); both
 // zeros share a key, NaN is above everything, and 0 is left for "none".
@@ -392,21 +423,22 @@ route_topk_kernel(const RouteParams p) {
     int t = blockIdx.x * kRouteWarps + warp;
     if (t >= p.T) return;
 
-    auto load = [&](int token, float (&v)[EPL]) {
+    auto load = [&](int token, RawRow<EPL, L>& v) {
         const L* row = static_cast<const L*>(p.logits) + static_cast<int64_t>(token) * p.E;
         if (p.vec) {
-            load_logits<EPL>(row + lane * EPL, v);
+            v.load_wide(row + lane * EPL, RawRow<EPL, L>::kChunk);
         } else {
             const int e0 = p.first_of<kSpans>(lane), held = p.count_of<kSpans>(lane);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) v[i] = i < held ? logit_at(row + e0 + i) : -INFINITY;
+            for (int i = 0; i < EPL; ++i) v.load_one(i, i < held, row + e0 + i);
         }
     };
-    float bias[EPL], fetched[EPL];
+    float bias[EPL];
+    RawRow<EPL, L> fetched;
     load(t, fetched);
     if (biased) {
         if (p.vec) {
-            load_logits<EPL>(p.bias + lane * EPL, bias);
+            load_floats<EPL>(p.bias + lane * EPL, bias);
         } else {
             const int e0 = p.first_of<kSpans>(lane), held = p.count_of<kSpans>(lane);
 #pragma unroll
@@ -417,8 +449,7 @@ route_topk_kernel(const RouteParams p) {
     for (; t < p.T; t += stride) {
         const L* row = static_cast<const L*>(p.logits) + static_cast<int64_t>(t) * p.E;
         float v[EPL];  // logits, then (with a bias) choice values; -inf: not eligible
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) v[i] = fetched[i];
+        fetched.get(p.vec, v);
         if (p.T - t > stride) load(t + stride, fetched);
 
         float mx = 0.f, rz = 1.f;
@@ -664,8 +695,7 @@ struct RouteBwdParams {
     const void* logits;   // [T][E]
     const int32_t* idx;   // [T][k]
     int T, E, k;
-    int per;              // experts per lane, as in RouteParams
-    int vec;
+    int whole;            // every lane has EPL experts
     int softmax, renorm;
     float scale;
 };
@@ -674,11 +704,14 @@ __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, float v) {
     *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
+// N <= 4 floats or N <= 8 values of bf16 in one store.
 template <int N>
-__device__ __forceinline__ void store_logits(float* p, const float (&f)[N]) {
-    if constexpr (N >= 4) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+__device__ __forceinline__ void store_chunk(float* p, const float* f) {
+    if constexpr (N == 8) {
+        store_chunk<4>(p, f);
+        store_chunk<4>(p + 4, f + 4);
+    } else if constexpr (N == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
     } else if constexpr (N == 2) {
         *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
     } else {
@@ -686,15 +719,14 @@ __device__ __forceinline__ void store_logits(float* p, const float (&f)[N]) {
     }
 }
 template <int N>
-__device__ __forceinline__ void store_logits(uint16_t* p, const float (&f)[N]) {
+__device__ __forceinline__ void store_chunk(uint16_t* p, const float* f) {
     if constexpr (N >= 2) {
         uint32_t w[N / 2];
 #pragma unroll
         for (int i = 0; i < N / 2; ++i)
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-        if constexpr (N >= 8) {
-#pragma unroll
-            for (int i = 0; i < N / 2; i += 4) *reinterpret_cast<uint4*>(p + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        if constexpr (N == 8) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
         } else if constexpr (N == 4) {
             *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
         } else {
@@ -712,16 +744,24 @@ __device__ __forceinline__ void store_logits(uint16_t* p, const float (&f)[N]) {
 // experts' scores come from the row's in shared memory; the row is stored as it
 // is without a choice, then the k elements (a row put together in shared memory
 // first took 11.7 us below).  What the next token needs is on its way meanwhile.
-// 16384 tokens of 256 float32 logits, softmax: 9.5 us, 3.7 TB/s, bound by
-// instructions (328 a token, 67 % of the issue slots; HBM alone 5.4 us).
-template <int EPL, typename L>
+// kWide: rows are 16-byte aligned and every lane has EPL experts.
+// 16384 tokens of 256 float32 logits, softmax: 8.6 us, 4.0 TB/s, bound by
+// instructions (HBM alone 5.4 us); 65536 of 1024: 90 us, 6.0 TB/s.  A lane's wide
+// chunks lie 32 chunks apart, so that a load takes whole lines: 203 us there with
+// 32 logits in a row to a lane, and 568 against 97 us for 1000.
+template <int EPL, bool kWide, typename L>
 __global__ void __launch_bounds__(kRouteWarps * 32, route_ctas(EPL))
 route_topk_bwd_kernel(const RouteBwdParams p) {
     extern __shared__ __align__(16) float route_smem[];  // per warp a row of 32 * EPL; then per warp 16 slots
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e0 = lane * p.per;
+    // Experts of a lane: a wide load's chunk, the next one 32 chunks on; where not
+    // all lanes have EPL, every 32nd.
+    constexpr int kChunk = RawRow<EPL, L>::kChunk;
+    const bool whole = kWide || p.whole;
+    const int e0 = whole ? lane * kChunk : lane;
+    auto expert = [&](int i) { return e0 + (whole ? i / kChunk * 32 * kChunk + i % kChunk : 32 * i); };
     float* line = route_smem + warp * 32 * EPL;
     float4* slots = reinterpret_cast<float4*>(route_smem + kRouteWarps * 32 * EPL) + warp * kRouteMaxK;
     const int stride = gridDim.x * kRouteWarps;
@@ -729,7 +769,8 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
     if (t >= p.T) return;
 
     int next_e = -1;
-    float next_g = 0.f, next_d[EPL];
+    float next_g = 0.f;
+    RawRow<EPL, L> next_d;
     auto load = [&](int token) {
         if (lane < p.k) {
             next_e = p.idx[static_cast<int64_t>(token) * p.k + lane];
@@ -737,11 +778,11 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         }
         if (p.softmax) {
             const L* row = static_cast<const L*>(p.logits) + static_cast<int64_t>(token) * p.E;
-            if (p.vec) {
-                load_logits<EPL>(row + lane * EPL, next_d);
+            if (kWide) {
+                next_d.load_wide(row + e0, 32 * kChunk);
             } else {
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) next_d[i] = i < p.per && e0 + i < p.E ? logit_at(row + e0 + i) : -INFINITY;
+                for (int i = 0; i < EPL; ++i) next_d.load_one(i, expert(i) < p.E, row + expert(i));
             }
         }
     };
@@ -753,10 +794,7 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             e = -1;
             g = 0.f;
         }
-        if (p.softmax) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) d[i] = next_d[i];
-        }
+        if (p.softmax) next_d.get(kWide, d);
         if (p.T - t > stride) load(t + stride);
 
         float s = 0.f, rz = 1.f;
@@ -772,12 +810,12 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
                 d[i] = exp_fast(d[i] - m);
                 z += d[i];
             }
-            if (p.per == EPL) {
-                store_logits<EPL>(line + e0, d);
+            if (kWide) {
+#pragma unroll
+                for (int i = 0; i < EPL; i += kChunk) store_chunk<kChunk>(line + e0 + 32 * i, d + i);
             } else {
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (i < p.per) line[e0 + i] = d[i];
+                for (int i = 0; i < EPL; ++i) line[expert(i)] = d[i];
             }
             z = warp_sum(z);
             __syncwarp();
@@ -828,12 +866,13 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         float r[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) r[i] = p.softmax ? rest * d[i] : 0.f;
-        if (p.vec) {
-            store_logits<EPL>(out + lane * EPL, r);
+        if (kWide) {
+#pragma unroll
+            for (int i = 0; i < EPL; i += kChunk) store_chunk<kChunk>(out + e0 + 32 * i, r + i);
         } else {
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (i < p.per && e0 + i < p.E) store_logit(out + e0 + i, r[i]);
+                if (expert(i) < p.E) store_logit(out + expert(i), r[i]);
         }
         __syncwarp();  // orders the two stores of an element; `line` and `slots` have been read
         if (first) store_logit(out + e, p.softmax ? s * (g - dot) : g * (s * (1.f - s)));
