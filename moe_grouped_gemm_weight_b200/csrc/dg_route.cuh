@@ -403,7 +403,7 @@ struct Top4 {
 // without a bias fit a key whole.
 //
 // 16384 tokens of 256 float32 logits, 8 groups, bias: 18.5 us on one B200 in
-// graph replays (HBM alone 2.6 us), 686 instructions a token at 59 % of the
+// graph replays (HBM alone 2.6 us), 659 instructions a token at 56 % of the
 // issue slots; 17.0 us without any FP64.
 template <int EPL, bool kSpans, typename L>
 __global__ void __launch_bounds__(kRouteWarps * 32, route_ctas(EPL))
