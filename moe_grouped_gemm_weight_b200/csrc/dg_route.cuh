@@ -8,6 +8,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <float.h>
 #include <stdint.h>
 
 #include "dg_ptx.cuh"
@@ -538,8 +539,10 @@ route_topk_kernel(const RouteParams p) {
                 b = fmaxf(fmaxf(b, xb), fminf(a, xa));
                 a = fmaxf(a, xa);
             }
-            float sum = a + (p.gtop == 2 && b != -INFINITY ? b : 0.f);
-            if (g >= p.groups) sum = -INFINITY;
+            // -inf marks a group without an expert, so a sum below every float (two soft
+            // masks of the lowest one) stays at the lowest, level with all such sums.
+            float sum = fmaxf(a + (p.gtop == 2 && b != -INFINITY ? b : 0.f), -FLT_MAX);
+            if (a == -INFINITY || g >= p.groups) sum = -INFINITY;
             // The best groups, one value (mostly one group) a round.
             bool kept = false;
             float lo = -INFINITY, hi = warp_max(sum);
