@@ -941,8 +941,8 @@ route_layout_kernel(const LayoutParams p) {
     int* total = run + p.warps * p.E;  // read by the other CTAs
     int* start = total + p.E;
     int* held = start + p.E + 1;
-    int* base = held + p.E;
-    int* local_start = base + p.E;
+    uint32_t* base = reinterpret_cast<uint32_t*>(held + p.E);
+    int* local_start = held + 2 * p.E;
     unsigned long long* wsum = reinterpret_cast<unsigned long long*>(layout_smem + (((p.warps + 5) * p.E + 2) & ~1));
     uint32_t* staged = reinterpret_cast<uint32_t*>(wsum + kLayoutWarps);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1057,7 +1057,7 @@ route_layout_kernel(const LayoutParams p) {
     if (e < p.E) {
         start[e] = first;
         if (e == p.E - 1) start[p.E] = first + len;
-        base[e] = first + before;
+        base[e] = static_cast<uint32_t>(first) + static_cast<uint32_t>(before);
         local_start[e] = static_cast<int>(incl >> 32) - static_cast<int>(own);
         held[e] = kept;
         if (rank == 0) {
@@ -1068,9 +1068,10 @@ route_layout_kernel(const LayoutParams p) {
     }
     __syncthreads();
 
+    // Places past a masked group's end may pass 31 bits (rows and slots are below that each), 32 never.
     auto row_at = [&](int x, int r) {
-        const int row = base[x] + r;
-        return p.max_rows > 0 && row >= start[x] + p.max_rows ? -1 : row;
+        const uint32_t row = base[x] + static_cast<uint32_t>(r);
+        return p.max_rows > 0 && row >= static_cast<uint32_t>(start[x] + p.max_rows) ? -1 : static_cast<int>(row);
     };
     auto place = [&](int64_t at, int x, int r) {  // r: rank among the CTA's slots of x
         const int row = x >= 0 ? row_at(x, r) : -1;

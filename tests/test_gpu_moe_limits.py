@@ -38,3 +38,21 @@ def test_a_group_whose_sum_leaves_fp32_is_no_masked_group(dgm, E, groups, sigmoi
     bias[2 * n + 3:3 * n] = -math.inf
     check_route(dgm, logits, bias, k=8, groups=groups, keep=3, gtop=2, sigmoid=sigmoid, renorm=True, scale=1.0)
     check_route(dgm, logits, bias, k=8, groups=groups, keep=groups - 1, gtop=2, sigmoid=sigmoid)
+
+
+def test_masked_layout_whose_ranks_pass_31_bits(dgm):
+    # The last group starts three million rows below 2^31, and more slots ask for it than there are numbers left.
+    E, k = 1024, 1
+    M = 0x7FF00000 // E
+    T = (1 << 31) - (E - 1) * M + 70000
+    i = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    idx = torch.full((T, k), E - 1, dtype=torch.int32, device="cuda")
+    row_of, m_indices, slot_of, off, cnt = i(T, k), i(E * M), i(E * M), i(E + 1), i(E)
+    dgm.dg_route_layout(row_of, m_indices, slot_of, off, cnt, idx, max_rows=M)
+    want = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    want[:M] = torch.arange(M, dtype=torch.int32, device="cuda") + (E - 1) * M
+    assert torch.equal(row_of.view(-1), want)
+    assert int(cnt[-1]) == M and int(cnt[:-1].sum()) == 0 and int(off[-1]) == E * M
+    assert bool((m_indices[:(E - 1) * M] == -1).all() and (m_indices[(E - 1) * M:] == E - 1).all())
+    assert torch.equal(slot_of[(E - 1) * M:], torch.arange(M, dtype=torch.int32, device="cuda"))
+    assert dgm.dg_get_device_error() == 0
