@@ -166,7 +166,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.f + exp_fast(-x)); }
 // For results: relative error a few 2^-24.
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+__device__ __forceinline__ float sigmoid_f(float x) { return __frcp_rn(1.f + expf(-x)); }
 
 // Signed integers in the order of finite or infinite floats, and back.
 __device__ __forceinline__ int ordered_int(float f) {
@@ -800,7 +800,7 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         if (p.softmax) next_d.get(kWide, d);
         if (p.T - t > stride) load(t + stride);
 
-        float s = 0.f, rz = 1.f;
+        float s = 0.f, not_s = 0.f, rz = 1.f;  // not_s: 1 - s, for sigmoid
         if (p.softmax) {
             float m = d[0];
 #pragma unroll
@@ -825,7 +825,11 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             rz = z > 0.f || z != z ? 1.f / z : 0.f;
             if (e >= 0) s = line[e] * rz;
         } else if (e >= 0) {
-            s = sigmoid_f(logit_at(static_cast<const L*>(p.logits) + static_cast<int64_t>(t) * p.E + e));
+            const float x = logit_at(static_cast<const L*>(p.logits) + static_cast<int64_t>(t) * p.E + e);
+            // Both of 1 / (1 + e) and e / (1 + e); 1 - s itself cancels (6 % off at x = 16, zero from 17 on).
+            const float ex = expf(-fabsf(x)), more = __frcp_rn(1.f + ex), less = ex * more;
+            s = x < 0.f ? less : more;
+            not_s = x < 0.f ? more : less;
         }
         // The slots among themselves, through shared memory; past k: zeros, expert -1.
         if (lane < kRouteMaxK) slots[lane] = make_float4(g, s, __int_as_float(e), 0.f);
@@ -878,7 +882,7 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
                 if (expert(i) < p.E) store_logit(out + expert(i), r[i]);
         }
         __syncwarp();  // orders the two stores of an element; `line` and `slots` have been read
-        if (first) store_logit(out + e, p.softmax ? s * (g - dot) : g * (s * (1.f - s)));
+        if (first) store_logit(out + e, p.softmax ? s * (g - dot) : g * (s * not_s));
     }
 }
 

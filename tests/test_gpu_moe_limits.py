@@ -56,3 +56,22 @@ def test_masked_layout_whose_ranks_pass_31_bits(dgm):
     assert bool((m_indices[:(E - 1) * M] == -1).all() and (m_indices[(E - 1) * M:] == E - 1).all())
     assert torch.equal(slot_of[(E - 1) * M:], torch.arange(M, dtype=torch.int32, device="cuda"))
     assert dgm.dg_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sigmoid_gradient_where_the_score_is_nearly_one(dgm, dtype):
+    # s (1 - s) with 1 - s for itself: 1 / (1 + e) and e / (1 + e), an exponential of 2 ulp (4 U), an addition, a
+    # quotient, a product each; scale dw and two more: at most 2 (4 + 1 + 1) + 4 half steps, and the type's rounding.
+    l = torch.cat([torch.arange(-80, 80, 0.625), torch.tensor([16.0, 17.0, 18.0, 40.0, 80.0])]).to(dtype)
+    T, E = l.numel(), 5
+    logits = torch.zeros(T, E, dtype=dtype)
+    logits[:, 3] = l
+    dw = torch.linspace(0.5, 2.0, T)[:, None]
+    d = torch.empty(T, E, dtype=dtype, device="cuda")
+    dgm.dg_route_topk_bwd(d, dw.cuda(), logits.cuda(), torch.full((T, 1), 3, dtype=torch.int32, device="cuda"),
+                          score=dgm.DG_SCORE_SIGMOID, scale=1.0)
+    x = l.double()
+    want = dw[:, 0].double() * torch.sigmoid(x) * torch.sigmoid(-x)
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    got = d.cpu().double()[:, 3]
+    assert bool(((got - want).abs() <= (16 * U + half) * want).all()), float(((got - want).abs() / want).max())
