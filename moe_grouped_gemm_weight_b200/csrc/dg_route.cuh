@@ -800,7 +800,7 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         if (p.softmax) next_d.get(kWide, d);
         if (p.T - t > stride) load(t + stride);
 
-        float s = 0.f, not_s = 0.f, rz = 1.f;  // not_s: 1 - s, for sigmoid
+        float s = 0.f, not_s = 0.f, rz = 1.f;  // not_s: 1 - s
         if (p.softmax) {
             float m = d[0];
 #pragma unroll
@@ -823,7 +823,19 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             z = warp_sum(z);
             __syncwarp();
             rz = z > 0.f || z != z ? 1.f / z : 0.f;
-            if (e >= 0) s = line[e] * rz;
+            // 1 - s is the other scores' sum: z less the expert's own term cancels for one that
+            // has most of z alone, the only one at the maximum.
+            float others = 0.f;
+            if (z < 2.f) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) others += d[i] == 1.f ? 0.f : d[i];
+                others = warp_sum(others);
+            }
+            if (e >= 0) {
+                const float mine = line[e];
+                s = mine * rz;
+                not_s = (z < 2.f && mine == 1.f ? others : z - mine) * rz;
+            }
         } else if (e >= 0) {
             const float x = logit_at(static_cast<const L*>(p.logits) + static_cast<int64_t>(t) * p.E + e);
             // Both of 1 / (1 + e) and e / (1 + e); 1 - s itself cancels (6 % off at x = 16, zero from 17 on).
@@ -834,9 +846,10 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
         // The slots among themselves, through shared memory; past k: zeros, expert -1.
         if (lane < kRouteMaxK) slots[lane] = make_float4(g, s, __int_as_float(e), 0.f);
         __syncwarp();
-        // g_j - sum_i g_i s_i / S = (sum_i (g_j - g_i) s_i + g_j eps) / S: nothing cancels
-        // where one expert has nearly all the weight, or is the only one.
-        float diff = g * kRouteEps, total = kRouteEps, dot = 0.f;
+        // g_j - sum_i g_i s_i / S = (sum_i (g_j - g_i) s_i + g_j eps) / S, and
+        // g_j - sum_i g_i s_i = g_j (1 - s_j) - sum over the other experts' slots: nothing
+        // cancels where one expert has nearly all the weight, or is the only one.
+        float diff = 0.f, total = kRouteEps, dot = 0.f, other = 0.f;
         int alike = 0;  // slots with this one's expert
 #pragma unroll 1  // unrolled, its loads spill
         for (int j0 = 0; j0 < p.k; j0 += 4) {
@@ -845,27 +858,32 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             for (int j = 0; j < 4; ++j) o[j] = slots[j0 + j];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                const bool same = __float_as_int(o[j].z) == e;
                 total += o[j].y;
                 dot = fmaf(o[j].x, o[j].y, dot);
+                other = fmaf(same ? 0.f : o[j].x, o[j].y, other);
                 diff = fmaf(g - o[j].x, o[j].y, diff);
-                alike += __float_as_int(o[j].z) == e ? 1 : 0;
+                alike += same ? 1 : 0;
             }
-        }
-        if (p.renorm) {
-            const float rs = 1.f / total;
-            g = e < 0 ? 0.f : diff * rs * rs;
-            dot = dot * rs * (kRouteEps * rs);  // sum of the new g s: the differences cancel in pairs
         }
         bool first = e >= 0;
-        if (__any_sync(0xffffffffu, first && alike > 1)) {  // an expert's first slot takes the sum, in slot order
-            float sum = 0.f;
+        if (__any_sync(0xffffffffu, first && alike > 1)) {  // an expert's first slot takes the sums, in slot order
+            float sum_g = 0.f, sum_d = 0.f;
             for (int j = 0; j < p.k; ++j) {
                 const int ej = __shfl_sync(0xffffffffu, e, j);
-                const float gj = __shfl_sync(0xffffffffu, g, j);
-                sum += ej == e ? gj : 0.f;
+                const float gj = __shfl_sync(0xffffffffu, g, j), dj = __shfl_sync(0xffffffffu, diff, j);
+                sum_g += ej == e ? gj : 0.f;
+                sum_d += ej == e ? dj : 0.f;
                 first = first && !(ej == e && j < lane);
             }
-            g = sum;
+            g = sum_g;
+            diff = sum_d;
+        }
+        if (p.softmax) g = fmaf(g, not_s, -other);
+        if (p.renorm) {
+            const float rs = 1.f / total;
+            g = fmaf(g, kRouteEps, diff) * rs * rs;
+            dot = dot * rs * (kRouteEps * rs);  // sum of the new g s: the differences cancel in pairs
         }
         // The row as it is without a choice, then the chosen experts' values over it.
         L* out = static_cast<L*>(p.dlogits) + static_cast<int64_t>(t) * p.E;
@@ -882,7 +900,7 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
                 if (expert(i) < p.E) store_logit(out + expert(i), r[i]);
         }
         __syncwarp();  // orders the two stores of an element; `line` and `slots` have been read
-        if (first) store_logit(out + e, p.softmax ? s * (g - dot) : g * (s * not_s));
+        if (first) store_logit(out + e, g * (p.softmax ? s : s * not_s));
     }
 }
 

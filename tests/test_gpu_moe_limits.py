@@ -75,3 +75,41 @@ def test_sigmoid_gradient_where_the_score_is_nearly_one(dgm, dtype):
     half = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
     got = d.cpu().double()[:, 3]
     assert bool(((got - want).abs() <= (16 * U + half) * want).all()), float(((got - want).abs() / want).max())
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E", [8, 60, 256, 1024])
+def test_softmax_gradient_of_a_dominant_expert(dgm, E, renorm):
+    # ds_e - sum_j ds_j s_j is (1 - s_e) ds_e - sum over the other experts' slots, and 1 - s_e a sum of other
+    # scores.  k = 1: dl_e = s_e dw (1 - s_e), dl_i = -s_i s_e dw.  Logits are multiples of 1/8, so their
+    # differences are exact: a score is an exponential (5 U), a sum of E of them (5 U + at most 37 U), quotient and
+    # product; dl has two scores and a few products: 2 (5 + 42 + 2) + 6 half steps.
+    g = torch.Generator().manual_seed(E)
+    logits = (-10 - torch.randint(0, 400, (40, E), generator=g).float() / 8)
+    top = torch.randint(0, E, (40,), generator=g)
+    logits[torch.arange(40), top] = torch.arange(40).float() / 4
+    k = 2 if renorm else 1
+    idx = torch.stack([top, (top + 1) % E], dim=1)[:, :k].int().contiguous()
+    dw = torch.randn(40, k, generator=g)
+    d = torch.empty(40, E, device="cuda")
+    dgm.dg_route_topk_bwd(d, dw.cuda(), logits.cuda(), idx.cuda(), renorm=renorm)
+    s = scores64(logits, False)
+    w = dw.double()
+    if not renorm:
+        rest = torch.where(torch.arange(E) == top[:, None], 0.0, s).sum(1)  # 1 - s_e without cancellation
+        se = s.gather(1, top[:, None])[:, 0]
+        want = -s * (se * w[:, 0])[:, None]
+        want[torch.arange(40), top] = se * w[:, 0] * rest
+        tol = 105 * U * want.abs() + 1e-37
+    else:
+        s1, s2 = s.gather(1, idx.long()).unbind(1)
+        S = s1 + s2 + 1e-20
+        want = torch.zeros_like(s)
+        # w1 = s1 / S: dL = (dw1 - dw2) s1 s2 / S^2 (dl1 - dl2), up to 1e-20
+        x = (w[:, 0] - w[:, 1]) * s1 * s2 / S ** 2
+        want[torch.arange(40), idx[:, 0].long()] = x
+        want[torch.arange(40), idx[:, 1].long()] = -x
+        mag = (w.abs().sum(1) * 1e-20 / S)[:, None] * s
+        tol = 250 * U * want.abs() + 4 * mag + 1e-37  # four scores of 49, and products
+    far = (d.cpu().double() - want).abs() - tol
+    assert not bool((far > 0).any()), float(((d.cpu().double() - want).abs() / want.abs().clamp_min(1e-300)).max())
