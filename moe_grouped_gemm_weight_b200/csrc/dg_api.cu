@@ -836,13 +836,16 @@ bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p)
 
 // Launch of a kernel without a register split: programmatic dependent launch
 // as everywhere, `cluster` CTAs per cluster, `smem` bytes of dynamic shared
-// memory (raised once per device where it is above the 48 KiB default).
+// memory; `smem_max`: the most that any call of the kernel takes (0: always
+// `smem`).
 template <typename P>
-dg_status launch_plain(void (*kern)(P), const P& p, int64_t grid, int threads, int smem, int cluster, void* stream) {
+dg_status launch_plain(void (*kern)(P), const P& p, int64_t grid, int threads, int smem, int cluster, void* stream,
+                       int smem_max = 0) {
     if (grid > 0x7FFFFFFF) return fail(DG_ERR_UNSUPPORTED, "problem too large");
     if (smem > 48 * 1024) {
-        // Not remembered: the attribute belongs to (kernel, device), the call costs under a microsecond.
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        // The attribute belongs to (kernel, device): every call of a kernel asks for the same, or one host thread
+        // would take back what another is about to launch with.  Not remembered: it costs under a microsecond.
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max ? smem_max : smem) != cudaSuccess)
             return fail(DG_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(cudaGetLastError()));
     }
     cudaLaunchConfig_t cfg = {};
@@ -1375,6 +1378,10 @@ dg_status dg_route_topk_bwd(void* dlogits, const float* dw, const void* logits, 
                                          : launch_route_bwd<float>(p, wide, grid, stream);
 }
 
+// Shared memory of a layout call: without staged slots every size that the call takes fits.
+constexpr int kLayoutMaxSmem = 220 * 1024;
+static_assert(4 * dg::layout_smem_ints(dg::kRouteMaxExperts, dg::kLayoutWarps, 0) <= kLayoutMaxSmem);
+
 int dg_get_layout_rows(int T, int k, int E) {
     if (T < 0 || k <= 0 || k > kMaxSlots || E <= 0 || E > dg::kRouteMaxExperts) return -1;
     const int64_t S = static_cast<int64_t>(T) * k;
@@ -1415,12 +1422,12 @@ dg_status dg_route_layout(int32_t* row_of, int32_t* m_indices, int32_t* slot_of,
     const int64_t cta_slots = p.warps * p.warp_slots;
     const int64_t staged = cta_slots <= dg::kLayoutMaxStaged ? cta_slots : 0;
     int64_t smem = 4ll * dg::layout_smem_ints(E, p.warps, static_cast<int>(staged));
-    const bool fits = staged > 0 && smem <= 220 * 1024;
+    const bool fits = staged > 0 && smem <= kLayoutMaxSmem;
     if (!fits) smem = 4ll * dg::layout_smem_ints(E, p.warps, 0);
     return launch_plain(!fits                                       ? dg::route_layout_kernel<dg::kLayoutDirect>
                         : p.warp_slots <= 32 * dg::kLayoutHeld ? dg::route_layout_kernel<dg::kLayoutHeldRun>
                                                                     : dg::route_layout_kernel<dg::kLayoutStaged>,
-                        p, ctas, dg::kLayoutThreads, static_cast<int>(smem), ctas, stream);
+                        p, ctas, dg::kLayoutThreads, static_cast<int>(smem), ctas, stream, kLayoutMaxSmem);
 }
 
 dg_status dg_dispatch_fp8_1x128(uint8_t* Q, float* sa, int sa_stride, const uint16_t* X, const int32_t* row_of, int T,

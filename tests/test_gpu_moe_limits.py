@@ -1,5 +1,7 @@
 """GPU: the calls around the grouped GEMMs where FP32, 31 bits, a cap or a second host thread can go wrong."""
+import ctypes
 import math
+import subprocess
 import threading
 
 import pytest
@@ -21,6 +23,56 @@ def dgm():
     dg.dg_set_num_sms(0)
     assert dg.dg_get_device_error() == 0
     return dg
+
+
+HAMMER = """
+typedef int (*layout_fn)(void *, void *, void *, void *, void *, const void *, int, int, int, int, int, void *);
+int hammer(layout_fn f, void **p, int T, int k, int E, int rows, void *stream, int n) {
+    int failed = 0;
+    for (int i = 0; i < n; ++i) failed += f(p[0], p[1], p[2], p[3], p[4], p[5], T, k, E, rows, 0, stream) != 0;
+    return failed;
+}
+"""
+
+
+def test_layouts_of_different_sizes_from_two_host_threads(dgm, tmp_path):
+    # 8192 slots over 512 and over 600 experts take 80 and 94 KiB of shared memory, above what a kernel may have
+    # without asking: a call must not lower what another thread has just asked for.
+    (tmp_path / "hammer.c").write_text(HAMMER)
+    subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-o", str(tmp_path / "hammer.so"), str(tmp_path / "hammer.c")],
+                   check=True)
+    hammer = ctypes.CDLL(str(tmp_path / "hammer.so")).hammer  # without the interpreter lock
+    fn = ctypes.cast(dgm.lib().dg_route_layout, ctypes.c_void_p)
+    T, k = 1024, 8
+    i = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    failed, outs = {}, {}
+
+    def make(E):
+        rows = dgm.dg_get_layout_rows(T, k, E)
+        idx = torch.randint(0, E, (T, k), generator=torch.Generator().manual_seed(E)).int().cuda()
+        return i(T, k), i(rows), i(rows), i(E + 1), i(E), idx
+
+    def work(E):
+        args = outs[E]
+        ptrs = (ctypes.c_void_p * 6)(*(t.data_ptr() for t in args))
+        stream = torch.cuda.Stream()
+        failed[E] = hammer(fn, ptrs, T, k, E, args[1].numel(), ctypes.c_void_p(stream.cuda_stream), 5000)
+        stream.synchronize()
+
+    for E in (512, 600):
+        outs[E] = make(E)
+        dgm.dg_route_layout(*outs[E])
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(E,)) for E in outs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert failed == {512: 0, 600: 0}
+    for E, args in outs.items():
+        again = make(E)
+        dgm.dg_route_layout(*again)
+        assert all(torch.equal(a, b) for a, b in zip(args, again)), E
 
 
 @pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (60, 5), (1020, 20)])
