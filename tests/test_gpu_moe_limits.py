@@ -165,3 +165,54 @@ def test_softmax_gradient_of_a_dominant_expert(dgm, E, renorm):
         tol = 250 * U * want.abs() + 4 * mag + 1e-37  # four scores of 49, and products
     far = (d.cpu().double() - want).abs() - tol
     assert not bool((far > 0).any()), float(((d.cpu().double() - want).abs() / want.abs().clamp_min(1e-300)).max())
+
+
+@pytest.mark.parametrize("g_range", [(-80.0, -20.0), (-20.0, 0.0), (0.0, 80.0)])
+def test_gated_activation_is_good_to_fp32(dgm, g_range):
+    # One value to a tile, whose scale shows it in FP32: a = 448 sa.  Exponential 2^-22.5 and two roundings (5 U),
+    # 1 + e, quotient (1 ulp: 2 U), product with the gate, up a power of two (exact), / 448: 10 half steps.
+    F, rows = 128 * 16, 64
+    lo, hi = g_range
+    gate = (lo + (hi - lo) * torch.rand(rows, F // 128, generator=torch.Generator().manual_seed(1))).bfloat16()
+    gate[0, 0], gate[0, 1] = lo or 0.5, hi or -0.5
+    x = gate.double()
+    silu = x / (1 + torch.exp(-x))
+    up = torch.exp2(torch.round(-torch.log2(silu.abs().clamp_min(1e-300))))  # a about 1
+    H = torch.zeros(rows, 2 * F)
+    H[:, ::128][:, :F // 128], H[:, ::128][:, F // 128:] = gate.float(), up.float()
+    Q, sa = codes(rows, F), scales(F // 128, rows)
+    dgm.dg_swiglu_fp8(Q, sa, rows, H.bfloat16().cuda())
+    want = (silu * up).abs() / 448
+    off = (sa.cpu().t().double() - want).abs() / want
+    assert bool((off <= 11 * U).all()), float(off.max() / U)
+
+
+@pytest.mark.parametrize("g_range", [(-80.0, -20.0), (-20.0, -3.0), (0.0, 80.0)])
+def test_gradient_of_the_gated_activation_is_good_to_fp32(dgm, g_range):
+    # As above: code 1 times the scale is the gate itself, one value to a tile, the gradient's scales show it.
+    # s as above without the product (8 U); d up = dA silu: 9 + 1 + 1.  d gate = dA up (s + silu (1 - s)): silu 9 U;
+    # 1 - s loses U and 8 U s; their product U; the sum U; two products and / 448.
+    F, rows = 128 * 16, 128
+    lo, hi = g_range
+    gate = lo + (hi - lo) * torch.rand(rows, F // 128, generator=torch.Generator().manual_seed(2))
+    x = gate.double()
+    s = 1 / (1 + torch.exp(-x))
+    silu, one = x * s, 1 / (1 + torch.exp(x))
+    t = s + silu * one
+    big = torch.exp2(torch.round(-torch.log2(torch.minimum(silu.abs(), t.abs()))))
+    C = torch.zeros(rows, 2 * F, dtype=torch.uint8)
+    C[:, ::128] = 0x38                                         # 1.0
+    cs = torch.cat([gate, torch.ones_like(gate)], dim=1).t().contiguous()
+    dA = torch.zeros(rows, F)
+    dA[:, ::128] = big.float()
+    out = (codes(rows, 2 * F), scales(2 * F // 128, rows), codes(rows, 2 * F), scales(1, 2 * F), codes(rows, F),
+           scales(F // 128, 1))
+    dgm.dg_swiglu_fp8_bwd(out[0], out[1], rows, out[2], out[3], 2 * F, out[4], out[5], dA.bfloat16().cuda(), C.cuda(),
+                          cs.cuda(), rows)
+    sr = out[1].cpu().t().double()
+    dgate, dup = (t * big).abs() / 448, (silu * big).abs() / 448
+    bound_t = (8 * s + (9 + 1) * (silu * one).abs() + silu.abs() * (1 + 8 * s) + t.abs()) / t.abs() + 3
+    off_u = (sr[:, F // 128:] - dup).abs() / dup
+    off_g = (sr[:, :F // 128] - dgate).abs() / dgate
+    assert bool((off_u <= 12 * U).all()), float(off_u.max() / U)
+    assert bool((off_g <= (bound_t + 1) * U).all()), float((off_g / bound_t).max() / U)
