@@ -151,9 +151,10 @@ __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v)
     return static_cast<unsigned long long>(hi) << 32 | lo;
 }
 
-// exp and the sigmoid by the special-function unit alone, without the care for
-// subnormal numbers: relative error 2^-22 and |x| 2^-24 for the argument's
-// rounding; absolute error of the sigmoid below 2^-22.
+// For choices, which look again where FP32 cannot tell: exp and the sigmoid by
+// the special-function unit alone, without the care for subnormal numbers:
+// relative error 2^-22 and |x| 2^-24 for the argument's rounding; absolute error
+// of the sigmoid below 2^-22.
 __device__ __forceinline__ float exp_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
@@ -165,7 +166,29 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return r;
 }
 __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.f + exp_fast(-x)); }
-// For results: relative error a few 2^-24.
+// For results.  Exponentials of N numbers up to zero: 2^t (1 + lo ln 2) with t the
+// rounded x log2(e) and lo what the product and the constant's rounding leave of
+// it, so the relative error is 5 2^-24 however low x is.  Results below 2^-126 are
+// zero (-126 stands for all lower x); a NaN stays one.
+template <int N>
+__device__ __forceinline__ void exp_results(float (&x)[N]) {
+    constexpr float kLog2e = 1.4426950408889634f, kRest = static_cast<float>(1.4426950408889634074 - kLog2e);
+    auto pair = [](float v) { return make_float2(v, v); };
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        float2 v = make_float2(x[i], i + 1 < N ? x[i + 1] : 0.f);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(v.x) : "f"(-126.f));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(v.y) : "f"(-126.f));
+        float2 e = __fmul2_rn(v, pair(kLog2e));
+        const float2 lo = __ffma2_rn(v, pair(kRest), __ffma2_rn(v, pair(kLog2e), make_float2(-e.x, -e.y)));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+        e = __fmul2_rn(e, __ffma2_rn(lo, pair(0.6931471805599453f), pair(1.f)));
+        x[i] = e.x;
+        if (i + 1 < N) x[i + 1] = e.y;
+    }
+}
+// Relative error a few 2^-24.
 __device__ __forceinline__ float sigmoid_f(float x) { return __frcp_rn(1.f + expf(-x)); }
 
 // Signed integers in the order of finite or infinite floats, and back.
@@ -809,10 +832,10 @@ route_topk_bwd_kernel(const RouteBwdParams p) {
             if (m == -INFINITY) m = 0.f;  // every expert masked: no score, no gradient
             float z = 0.f;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                d[i] = exp_fast(d[i] - m);
-                z += d[i];
-            }
+            for (int i = 0; i < EPL; ++i) d[i] -= m;
+            exp_results<EPL>(d);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) z += d[i];
             if (kWide) {
 #pragma unroll
                 for (int i = 0; i < EPL; i += kChunk) store_chunk<kChunk>(line + e0 + 32 * i, d + i);

@@ -216,3 +216,21 @@ def test_gradient_of_the_gated_activation_is_good_to_fp32(dgm, g_range):
     off_g = (sr[:, :F // 128] - dgate).abs() / dgate
     assert bool((off_u <= 12 * U).all()), float(off_u.max() / U)
     assert bool((off_g <= (bound_t + 1) * U).all()), float((off_g / bound_t).max() / U)
+
+
+@pytest.mark.parametrize("E", [8, 60, 256])
+def test_softmax_scores_far_below_the_largest(dgm, E):
+    # In the gradient too a score is an exponential good to 5 U however far its logit lies below the largest
+    # (multiples of 1/8: the difference is exact): dl_i = -s_i s_e dw, counted as above.
+    g = torch.Generator().manual_seed(3)
+    logits = -torch.randint(0, 640, (64, E), generator=g).float() / 8
+    logits[:, 2] = 0.0
+    dw = torch.ones(64, 1)
+    d = torch.empty(64, E, device="cuda")
+    dgm.dg_route_topk_bwd(d, dw.cuda(), logits.cuda(), torch.full((64, 1), 2, dtype=torch.int32, device="cuda"))
+    s = scores64(logits, False)
+    want = s * s[:, 2:3]
+    off = (d.cpu().double().neg() - want).abs() / want
+    off[:, 2] = 0
+    n = 2 * (5 + 5 + 5 + (E + 31) // 32 + 2) + 3
+    assert bool((off <= n * U).all()), (float(off.max() / U), n)
