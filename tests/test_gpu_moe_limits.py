@@ -234,3 +234,13 @@ def test_softmax_scores_far_below_the_largest(dgm, E):
     off[:, 2] = 0
     n = 2 * (5 + 5 + 5 + (E + 31) // 32 + 2) + 3
     assert bool((off <= n * U).all()), (float(off.max() / U), n)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_the_renormalised_weight_of_one_expert_is_one(dgm, sigmoid):
+    # s / (s + 1e-20), the sum s itself in FP32 (s > 1e-12): a quotient rounded to nearest is 1.
+    g = torch.Generator().manual_seed(8)
+    logits = (20 * torch.rand(5000, 24, generator=g) - 20).cuda()
+    idx, w = torch.empty(5000, 1, dtype=torch.int32, device="cuda"), torch.empty(5000, 1, device="cuda")
+    dgm.dg_route_topk(idx, w, logits, score=int(sigmoid), renorm=True)
+    assert bool((w == 1.0).all()), int((w != 1.0).sum())
