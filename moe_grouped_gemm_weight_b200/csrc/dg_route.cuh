@@ -489,11 +489,13 @@ route_topk_kernel(const RouteParams p) {
             for (int i = 0; i < EPL; ++i) z += exp_fast(v[i] - mx);
             rz = 1.f / warp_sum(z);
         }
-        // FP32 moves a choice value by less than `slack`: a sigmoid by 2^-22 (see
-        // sigmoid_fast); a softmax score by 2^-21 of the largest (exponential,
-        // product) and, all of a token alike, by the sum's error (at most 37
-        // roundings) and the reciprocal's, together below 2^-19.  Adding the bias
-        // adds 2^-24 of the value.
+        // FP32 moves the difference of two choice values by less than 2 slack and 2^-24
+        // of each value (adding the bias), that of two sums of two by 4 slack and the
+        // like.  A sigmoid moves by 2^-22 (see sigmoid_fast).  A softmax score by
+        // 5 2^-24 of the largest, rz, for itself (exponential, product).  The sum's
+        // error (at most 36 additions and the exponentials' 2^-22) and the reciprocal's
+        // are a factor that all scores of a token share, 41 2^-24 of the difference:
+        // 51 2^-24 rz in all, and 102 for the sums, where slack allows 64 and 128.
         const float slack = p.softmax ? rz * 0x1p-19f : 0x1p-22f;
         auto apart_by = [&](float x, float y) {  // more than FP32 can have moved x - y
             return biased ? 2.f * slack + 0x1p-22f * (fabsf(x) + fabsf(y)) : 0.f;
