@@ -491,11 +491,12 @@ route_topk_kernel(const RouteParams p) {
         }
         // FP32 moves the difference of two choice values by less than 2 slack and 2^-24
         // of each value (adding the bias), that of two sums of two by 4 slack and the
-        // like.  A sigmoid moves by 2^-22 (see sigmoid_fast).  A softmax score by
-        // 5 2^-24 of the largest, rz, for itself (exponential, product).  The sum's
-        // error (at most 36 additions and the exponentials' 2^-22) and the reciprocal's
-        // are a factor that all scores of a token share, 41 2^-24 of the difference:
-        // 51 2^-24 rz in all, and 102 for the sums, where slack allows 64 and 128.
+        // like.  A sigmoid moves by 2^-22 (see sigmoid_fast).  A softmax score moves by
+        // 6 2^-24 of the largest, rz, for itself (exponential, argument, product).  The
+        // sum's error (at most 36 additions, the exponentials' 2^-22, their arguments'
+        // 6 2^-24) and the reciprocal's are a factor that all scores of a token share,
+        // 47 2^-24 of the difference: 59 2^-24 rz in all, and 118 for the sums, where
+        // slack allows 64 and 128.
         const float slack = p.softmax ? rz * 0x1p-19f : 0x1p-22f;
         auto apart_by = [&](float x, float y) {  // more than FP32 can have moved x - y
             return biased ? 2.f * slack + 0x1p-22f * (fabsf(x) + fabsf(y)) : 0.f;
