@@ -335,13 +335,16 @@ def dg_grouped_masked_nt(D, A, sa, sa_stride: int, B, sb, masked_m, expected_m: 
                                       _ptr(masked_m), G, Mmax, N, K, int(expected_m), _stream(stream)))
 
 
-def _rank_error(func: str, **tensors) -> DGError:
-    names = [n for n, t in tensors.items() if not hasattr(t, "dim") or t.dim() != 2]
-    return DGError(func, DG_ERR_INVALID_ARG, f"{names[0]} must be a tensor of rank 2")
+def _rank_error(func: str, of_rows=(), **tensors) -> DGError:
+    """What is wrong with the tensors that a call's sizes come from: rank 2, or (`of_rows`) any but 0."""
+    for n, t in tensors.items():
+        if not isinstance(t, torch.Tensor) or t.dim() != (2 if n not in of_rows else max(t.dim(), 1)):
+            return DGError(func, DG_ERR_INVALID_ARG, f"{n} must be a tensor of " + ("rows" if n in of_rows else "rank 2"))
+    return DGError(func, DG_ERR_INVALID_ARG, f"bad sizes of {', '.join(tensors)}")
 
 
 def _shape1(func: str, name: str, t) -> int:
-    if t is None or t.dim() != 1:
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
         raise DGError(func, DG_ERR_INVALID_ARG, f"{name} must be a tensor of rank 1")
     return t.shape[0]
 
@@ -363,6 +366,8 @@ def _check_tensors(func: str, names: str, *triples) -> int:
         return cur
     given = [(name, *triples[3 * i:3 * i + 3]) for i, name in enumerate(names.split()) if triples[3 * i] is not None]
     for name, t, kind, need in given:
+        if not isinstance(t, torch.Tensor) or t.layout != torch.strided:
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} must be a dense tensor")
         if t.element_size() != 1 if kind == _U8 else t.dtype != _KINDS[kind]:
             raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call takes "
                           + ("1-byte elements" if kind == _U8 else str(_KINDS[kind])))
@@ -434,7 +439,7 @@ def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTM
     _check_dim(func, "token count of topk_idx", Ti, T)
     dt = _logits_dtype(func, logits)
     kind = _BF16 if dt == DG_DTYPE_BF16 else _F32
-    if dlogits is not None and dlogits.dtype != logits.dtype:
+    if isinstance(dlogits, torch.Tensor) and dlogits.dtype != logits.dtype:
         raise DGError(func, DG_ERR_INVALID_ARG, f"dlogits are {dlogits.dtype}, logits {logits.dtype}")
     dev = _check_tensors(func, "dlogits dw logits topk_idx",
                          dlogits, kind, T * E, dw, _F32, T * k, logits, kind, T * E, topk_idx, _I32, T * k)
@@ -476,11 +481,12 @@ def dg_dispatch_fp8_1x128(Q, sa, sa_stride: int, X, row_of, group_rows: int = 0,
     try:
         T, K = X.shape
         Ti, k = row_of.shape
-    except (AttributeError, ValueError):
-        raise _rank_error(func, X=X, row_of=row_of) from None
+        n, Kq = Q.numel(), Q.shape[-1]
+    except (AttributeError, ValueError, TypeError, IndexError):
+        raise _rank_error(func, ("Q",), X=X, row_of=row_of, Q=Q) from None
     _check_dim(func, "token count of row_of", Ti, T)
-    _check_dim(func, "K of Q", Q.shape[-1], K)
-    rows = Q.numel() // K if K else 0
+    _check_dim(func, "K of Q", Kq, K)
+    rows = n // K if K else 0
     dev = _check_tensors(func, "Q sa X row_of",
                          Q, _U8, rows * K, sa, _F32, _scales_need(_cdiv(K, 128), sa_stride, rows, group_rows),
                          X, _BF16, T * K, row_of, _I32, T * k)
@@ -497,11 +503,12 @@ def dg_combine(out, Y, row_of, w=None, stream=None) -> None:
     try:
         T, N = out.shape
         Ti, k = row_of.shape
-    except (AttributeError, ValueError):
-        raise _rank_error(func, out=out, row_of=row_of) from None
+        n, Ny = Y.numel(), Y.shape[-1]
+    except (AttributeError, ValueError, TypeError, IndexError):
+        raise _rank_error(func, ("Y",), out=out, row_of=row_of, Y=Y) from None
     _check_dim(func, "token count of row_of", Ti, T)
-    _check_dim(func, "N of Y", Y.shape[-1], N)
-    rows = Y.numel() // N if N else 0
+    _check_dim(func, "N of Y", Ny, N)
+    rows = n // N if N else 0
     dev = _check_tensors(func, "out Y row_of w",
                          out, _BF16, T * N, Y, _BF16, rows * N, row_of, _I32, T * k, w, _F32, T * k)
     status = _calls.dg_combine(out, Y, row_of, w, T, k, N, rows, _raw_stream(stream, dev))
@@ -537,10 +544,14 @@ def dg_swiglu_fp8(Q, sa, sa_stride: int, H, C=None, cs=None, cs_stride: int = 0,
     """silu(gate) * up of bf16 H [rows,2F] (or [G,M_max,2F]) -> e4m3 Q [rows,F]
     and sa; with C and cs also the e4m3 checkpoint of gate and up [rows,2F]."""
     func = "dg_swiglu_fp8"
-    F = H.shape[-1] // 2
-    _check_dim(func, "last extent of H", H.shape[-1], 2 * F)
-    _check_dim(func, "F of Q", Q.shape[-1], F)
-    rows = H.numel() // (2 * F) if F else 0
+    try:
+        n, width, Fq = H.numel(), H.shape[-1], Q.shape[-1]
+    except (AttributeError, TypeError, IndexError):
+        raise _rank_error(func, ("H", "Q"), H=H, Q=Q) from None
+    F = width // 2
+    _check_dim(func, "last extent of H", width, 2 * F)
+    _check_dim(func, "F of Q", Fq, F)
+    rows = n // (2 * F) if F else 0
     dev = _check_tensors(func, "Q sa H C cs m_indices",
                          Q, _U8, rows * F, sa, _F32, _scales_need(_cdiv(F, 128), sa_stride, rows, group_rows),
                          H, _BF16, rows * 2 * F, C, _U8, rows * 2 * F,
@@ -560,9 +571,10 @@ def dg_swiglu_fp8_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, Qa, sb, dA
     func = "dg_swiglu_fp8_bwd"
     try:
         rows, F = dA.shape
-    except (AttributeError, ValueError):
-        raise _rank_error(func, dA=dA) from None
-    _check_dim(func, "last extent of C", C.shape[-1], 2 * F)
+        width = C.shape[-1]
+    except (AttributeError, ValueError, TypeError, IndexError):
+        raise _rank_error(func, ("C",), dA=dA, C=C) from None
+    _check_dim(func, "last extent of C", width, 2 * F)
     dev = _check_tensors(func, "Qr sr Qc sc Qa sb dA C cs m_indices",
                          Qr, _U8, rows * 2 * F, sr, _F32, _sa_need(2 * _cdiv(F, 128), sr_stride, rows),
                          Qc, _U8, rows * 2 * F, sc, _F32, _sa_need(_cdiv(rows, 128), sc_stride, 2 * F),

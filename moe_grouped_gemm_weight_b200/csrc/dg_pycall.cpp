@@ -153,9 +153,9 @@ static const char *const kNames[9] = {"dg_route_topk", "dg_route_topk_bwd", "dg_
 
 /*
  * fits(tensor, kind, need, ...): the current CUDA device's index if every
- * tensor (None: absent) has the kind's elements, is contiguous, holds `need` of
- * them and lies on that device, else -1.  Kinds: 1 any one-byte elements, 2
- * bfloat16, 4 float32, 5 int32.
+ * tensor (None: absent) has the kind's elements, is dense and contiguous, holds
+ * `need` of them and lies on that device, else -1.  Kinds: 1 any one-byte
+ * elements, 2 bfloat16, 4 float32, 5 int32.
  */
 static PyObject *fits(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
@@ -169,6 +169,7 @@ static PyObject *fits(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         const long kind = PyLong_AsLong(a[i + 1]);
         const long long need = PyErr_Occurred() ? 0 : PyLong_AsLongLong(a[i + 2]);
         if (PyErr_Occurred()) return NULL;
+        if (t.layout() != at::kStrided) return PyLong_FromLong(-1);
         const at::ScalarType type = t.scalar_type();
         const bool right = kind == 1   ? t.element_size() == 1
                            : kind == 2 ? type == at::kBFloat16

@@ -1,0 +1,34 @@
+"""The calls around the grouped GEMMs refuse missing and foreign arguments as they refuse bad
+sizes, before anything is launched (no GPU needed)."""
+import numpy as np
+import pytest
+import torch
+
+import moe_grouped_gemm_weight_b200 as dg
+from moe_grouped_gemm_weight_b200 import build as dgbuild
+from tests.test_moe_checks import BINDING, TENSORS
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    dgbuild.build()
+    yield
+
+
+# Arguments that a call may do without.
+OPTIONAL = {("dg_route_topk", "bias"), ("dg_combine", "w"), ("dg_swiglu_fp8", "C"), ("dg_swiglu_fp8", "cs"),
+            ("dg_swiglu_fp8", "m_indices"), ("dg_swiglu_fp8_bwd", "m_indices"),
+            ("dg_fp8_1x128_to_128x128", "m_indices")}
+
+
+@pytest.mark.parametrize("name,arg", TENSORS)
+def test_arguments_that_are_no_tensors_are_refused(name, arg):
+    kw = BINDING[name]
+    foreign = [[1, 2], 3, "x", np.zeros(tuple(kw[arg].shape), np.float32), kw[arg].to_sparse(), kw[arg].reshape(-1)[0]]
+    for value in foreign + ([] if (name, arg) in OPTIONAL else [None]):
+        with pytest.raises(dg.DGError) as ei:
+            getattr(dg, name)(**{**kw, arg: value})
+        # a missing output that no size comes from is left to the library, behind the device check
+        assert ei.value.status == dg.DG_ERR_INVALID_ARG
+        if value is not None:
+            assert arg in str(ei.value), (type(value), str(ei.value))
