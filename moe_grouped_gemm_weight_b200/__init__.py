@@ -450,8 +450,11 @@ def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTM
 
 
 def dg_get_layout_rows(T: int, k: int, E: int) -> int:
-    """Rows that dg_route_layout's contiguous form needs for any choice of experts."""
-    return int(lib().dg_get_layout_rows(int(T), int(k), int(E)))
+    """Rows that dg_route_layout's contiguous form needs for any choice of experts; -1 for sizes it does not take."""
+    sizes = [int(x) for x in (T, k, E)]
+    if any(abs(x) > 0x7FFFFFFF for x in sizes):  # ctypes would keep the low 32 bits
+        return -1
+    return int(lib().dg_get_layout_rows(*sizes))
 
 
 def dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx, max_rows: int = 0,

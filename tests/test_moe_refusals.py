@@ -32,3 +32,9 @@ def test_arguments_that_are_no_tensors_are_refused(name, arg):
         assert ei.value.status == dg.DG_ERR_INVALID_ARG
         if value is not None:
             assert arg in str(ei.value), (type(value), str(ei.value))
+
+
+def test_layout_rows_of_sizes_past_32_bits():
+    for bad in [(1 << 32, 8, 256), ((1 << 32) + 5, 2, 4), (5, (1 << 32) + 2, 4), (5, 2, (1 << 32) + 4), (-(1 << 32) + 5, 2, 4),
+                (1 << 70, 2, 4)]:
+        assert dg.dg_get_layout_rows(*bad) == -1, bad
