@@ -20,8 +20,6 @@ import ctypes
 import os
 import threading
 
-import torch
-
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdg.so")
 
@@ -34,6 +32,7 @@ DG_SCORE_SOFTMAX, DG_SCORE_SIGMOID = 0, 1
 
 _lock = threading.Lock()
 _lib = None
+torch = None  # imported by the first call that takes tensors: plans, sizes and switches work without it
 
 
 class DGError(RuntimeError):
@@ -128,10 +127,17 @@ _CALLS = ("dg_route_topk", "dg_route_topk_bwd", "dg_route_layout", "dg_dispatch_
 _calls = None
 
 
+def _need_torch() -> None:
+    global torch
+    if torch is None:
+        import torch
+
+
 def _marshal():
-    """The calls around the grouped GEMMs as vector calls (csrc/dg_pycall.c), bound to the loaded library."""
+    """The calls around the grouped GEMMs as vector calls (csrc/dg_pycall.cpp), bound to the loaded library."""
     global _calls
     L = lib()
+    _need_torch()
     try:
         from . import _dgcall
     except ImportError as e:
@@ -190,6 +196,7 @@ def _check_args(func: str, *specs) -> None:
         if t.device.type != "cuda":
             raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is not on a CUDA device ({t.device})")
     if given:
+        _need_torch()
         cur = torch.cuda.current_device()
         for name, t, _, _ in given:
             if t.device.index != cur:
@@ -208,6 +215,7 @@ def _check_dense(func: str, D, A, sa, sa_stride, B, sb, M: int, N: int, K: int, 
 
 def _stream(stream) -> int:
     if stream is None:
+        _need_torch()
         return int(torch.cuda.current_stream().cuda_stream)
     return int(stream if isinstance(stream, int) else stream.cuda_stream)
 
@@ -351,7 +359,6 @@ def _shape1(func: str, name: str, t) -> int:
 
 # Kinds of elements, as the extension's check of a call's tensors numbers them.
 _U8, _BF16, _F32, _I32 = 1, 2, 4, 5
-_KINDS = {_BF16: torch.bfloat16, _F32: torch.float32, _I32: torch.int32}
 
 
 def _check_tensors(func: str, names: str, *triples) -> int:
@@ -361,16 +368,17 @@ def _check_tensors(func: str, names: str, *triples) -> int:
     `names` their names.  The extension checks them in one go (a decoding step
     makes these calls every few microseconds); what is wrong is looked up only
     for the message."""
-    cur = (_calls or _marshal()).fits(*triples)
+    cur = _calls.fits(*triples)
     if cur >= 0:
         return cur
+    kinds = {_BF16: torch.bfloat16, _F32: torch.float32, _I32: torch.int32}
     given = [(name, *triples[3 * i:3 * i + 3]) for i, name in enumerate(names.split()) if triples[3 * i] is not None]
     for name, t, kind, need in given:
         if not isinstance(t, torch.Tensor) or t.layout != torch.strided:
             raise DGError(func, DG_ERR_INVALID_ARG, f"{name} must be a dense tensor")
-        if t.element_size() != 1 if kind == _U8 else t.dtype != _KINDS[kind]:
+        if t.element_size() != 1 if kind == _U8 else t.dtype != kinds[kind]:
             raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is {t.dtype}, the call takes "
-                          + ("1-byte elements" if kind == _U8 else str(_KINDS[kind])))
+                          + ("1-byte elements" if kind == _U8 else str(kinds[kind])))
         if not t.is_contiguous():
             raise DGError(func, DG_ERR_INVALID_ARG, f"{name} is not contiguous")
         if t.numel() < need:
@@ -411,6 +419,7 @@ def dg_route_topk(topk_idx, topk_w, logits, bias=None, n_groups: int = 1, topk_g
     """The k experts of each token: logits [T,E] (bfloat16 or float32), optional
     float32 bias [E] -> int32 topk_idx [T,k] and float32 topk_w [T,k]."""
     func = "dg_route_topk"
+    calls = _calls or _marshal()
     try:
         T, E = logits.shape
         Ti, k = topk_idx.shape
@@ -421,8 +430,8 @@ def dg_route_topk(topk_idx, topk_w, logits, bias=None, n_groups: int = 1, topk_g
     kind = _BF16 if dt == DG_DTYPE_BF16 else _F32
     dev = _check_tensors(func, "topk_idx topk_w logits bias",
                          topk_idx, _I32, T * k, topk_w, _F32, T * k, logits, kind, T * E, bias, _F32, E)
-    status = _calls.dg_route_topk(topk_idx, topk_w, logits, dt, bias, T, E, k, n_groups, topk_groups, group_top,
-                                  score, 1 if renorm else 0, scale, _raw_stream(stream, dev))
+    status = calls.dg_route_topk(topk_idx, topk_w, logits, dt, bias, T, E, k, n_groups, topk_groups, group_top,
+                                 score, 1 if renorm else 0, scale, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -431,6 +440,7 @@ def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTM
                       scale: float = 1.0, stream=None) -> None:
     """Gradient of dg_route_topk: float32 dw [T,k] -> dlogits [T,E] (the logits' type)."""
     func = "dg_route_topk_bwd"
+    calls = _calls or _marshal()
     try:
         T, E = logits.shape
         Ti, k = topk_idx.shape
@@ -443,8 +453,8 @@ def dg_route_topk_bwd(dlogits, dw, logits, topk_idx, score: int = DG_SCORE_SOFTM
         raise DGError(func, DG_ERR_INVALID_ARG, f"dlogits are {dlogits.dtype}, logits {logits.dtype}")
     dev = _check_tensors(func, "dlogits dw logits topk_idx",
                          dlogits, kind, T * E, dw, _F32, T * k, logits, kind, T * E, topk_idx, _I32, T * k)
-    status = _calls.dg_route_topk_bwd(dlogits, dw, logits, dt, topk_idx, T, E, k, score, 1 if renorm else 0, scale,
-                                      _raw_stream(stream, dev))
+    status = calls.dg_route_topk_bwd(dlogits, dw, logits, dt, topk_idx, T, E, k, score, 1 if renorm else 0, scale,
+                                     _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -463,6 +473,7 @@ def dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx,
     m_indices and slot_of [rows], group_offsets [E+1], counts [E]; contiguous,
     or masked with max_rows rows per group."""
     func = "dg_route_layout"
+    calls = _calls or _marshal()
     try:
         T, k = topk_idx.shape
     except (AttributeError, ValueError):
@@ -471,8 +482,8 @@ def dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx,
     dev = _check_tensors(func, "row_of m_indices slot_of group_offsets counts topk_idx",
                          row_of, _I32, T * k, m_indices, _I32, rows, slot_of, _I32, rows, group_offsets, _I32, E + 1,
                          counts, _I32, E, topk_idx, _I32, T * k)
-    status = _calls.dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx, T, k, E, rows,
-                                    max_rows, _raw_stream(stream, dev))
+    status = calls.dg_route_layout(row_of, m_indices, slot_of, group_offsets, counts, topk_idx, T, k, E, rows,
+                                   max_rows, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -481,6 +492,7 @@ def dg_dispatch_fp8_1x128(Q, sa, sa_stride: int, X, row_of, group_rows: int = 0,
     """Cast bf16 X [T,K] into the rows of the layout: e4m3 Q [rows,K] (or
     [G,M_max,K]) and its transposed scales; group_rows = M_max when masked."""
     func = "dg_dispatch_fp8_1x128"
+    calls = _calls or _marshal()
     try:
         T, K = X.shape
         Ti, k = row_of.shape
@@ -493,8 +505,8 @@ def dg_dispatch_fp8_1x128(Q, sa, sa_stride: int, X, row_of, group_rows: int = 0,
     dev = _check_tensors(func, "Q sa X row_of",
                          Q, _U8, rows * K, sa, _F32, _scales_need(_cdiv(K, 128), sa_stride, rows, group_rows),
                          X, _BF16, T * K, row_of, _I32, T * k)
-    status = _calls.dg_dispatch_fp8_1x128(Q, sa, sa_stride, X, row_of, T, k, K, rows, group_rows,
-                                          _raw_stream(stream, dev))
+    status = calls.dg_dispatch_fp8_1x128(Q, sa, sa_stride, X, row_of, T, k, K, rows, group_rows,
+                                         _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -503,6 +515,7 @@ def dg_combine(out, Y, row_of, w=None, stream=None) -> None:
     """out [T,N] = sum over slots of w [T,k] (None: ones) times the rows of Y
     ([rows,N] or [G,M_max,N]), bf16; without w the backward pass of the dispatch."""
     func = "dg_combine"
+    calls = _calls or _marshal()
     try:
         T, N = out.shape
         Ti, k = row_of.shape
@@ -514,7 +527,7 @@ def dg_combine(out, Y, row_of, w=None, stream=None) -> None:
     rows = n // N if N else 0
     dev = _check_tensors(func, "out Y row_of w",
                          out, _BF16, T * N, Y, _BF16, rows * N, row_of, _I32, T * k, w, _F32, T * k)
-    status = _calls.dg_combine(out, Y, row_of, w, T, k, N, rows, _raw_stream(stream, dev))
+    status = calls.dg_combine(out, Y, row_of, w, T, k, N, rows, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -524,6 +537,7 @@ def dg_combine_bwd(dw, Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, dout, Y, 
     """Gradient of dg_combine (contiguous layout): dout [T,N] -> dY [rows,N]
     cast per 1x128 (Qr, sr) and per 128x1 (Qc, sc), and float32 dw [T,k]."""
     func = "dg_combine_bwd"
+    calls = _calls or _marshal()
     try:
         T, N = dout.shape
         Ti, k = row_of.shape
@@ -536,8 +550,8 @@ def dg_combine_bwd(dw, Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, dout, Y, 
                          dw, _F32, T * k, Qr, _U8, rows * N, sr, _F32, _sa_need(_cdiv(N, 128), sr_stride, rows),
                          Qc, _U8, rows * N, sc, _F32, _sa_need(_cdiv(rows, 128), sc_stride, N), dout, _BF16, T * N,
                          Y, _BF16, rows * N, row_of, _I32, T * k, slot_of, _I32, rows, w, _F32, T * k)
-    status = _calls.dg_combine_bwd(dw, Qr, sr, sr_stride, Qc, sc, sc_stride, dout, Y, row_of, slot_of, w, T, k, N,
-                                   rows, _raw_stream(stream, dev))
+    status = calls.dg_combine_bwd(dw, Qr, sr, sr_stride, Qc, sc, sc_stride, dout, Y, row_of, slot_of, w, T, k, N,
+                                  rows, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -547,6 +561,7 @@ def dg_swiglu_fp8(Q, sa, sa_stride: int, H, C=None, cs=None, cs_stride: int = 0,
     """silu(gate) * up of bf16 H [rows,2F] (or [G,M_max,2F]) -> e4m3 Q [rows,F]
     and sa; with C and cs also the e4m3 checkpoint of gate and up [rows,2F]."""
     func = "dg_swiglu_fp8"
+    calls = _calls or _marshal()
     try:
         n, width, Fq = H.numel(), H.shape[-1], Q.shape[-1]
     except (AttributeError, TypeError, IndexError):
@@ -560,8 +575,8 @@ def dg_swiglu_fp8(Q, sa, sa_stride: int, H, C=None, cs=None, cs_stride: int = 0,
                          H, _BF16, rows * 2 * F, C, _U8, rows * 2 * F,
                          cs if C is not None else None, _F32, _scales_need(2 * _cdiv(F, 128), cs_stride, rows, group_rows),
                          m_indices, _I32, rows)
-    status = _calls.dg_swiglu_fp8(Q, sa, sa_stride, C, cs, cs_stride, H, m_indices, rows, F, group_rows,
-                                  _raw_stream(stream, dev))
+    status = calls.dg_swiglu_fp8(Q, sa, sa_stride, C, cs, cs_stride, H, m_indices, rows, F, group_rows,
+                                 _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -572,6 +587,7 @@ def dg_swiglu_fp8_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, Qa, sb, dA
     dA [rows,F] -> dH [rows,2F] cast per 1x128 (Qr, sr) and per 128x1 (Qc, sc),
     and the activation again per 128x128 (Qa [rows,F], sb [F/128, rows/128])."""
     func = "dg_swiglu_fp8_bwd"
+    calls = _calls or _marshal()
     try:
         rows, F = dA.shape
         width = C.shape[-1]
@@ -584,8 +600,8 @@ def dg_swiglu_fp8_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, Qa, sb, dA
                          Qa, _U8, rows * F, sb, _F32, _cdiv(F, 128) * _cdiv(rows, 128), dA, _BF16, rows * F,
                          C, _U8, rows * 2 * F, cs, _F32, _sa_need(2 * _cdiv(F, 128), cs_stride, rows),
                          m_indices, _I32, rows)
-    status = _calls.dg_swiglu_fp8_bwd(Qr, sr, sr_stride, Qc, sc, sc_stride, Qa, sb, dA, C, cs, cs_stride, m_indices,
-                                      rows, F, _raw_stream(stream, dev))
+    status = calls.dg_swiglu_fp8_bwd(Qr, sr, sr_stride, Qc, sc, sc_stride, Qa, sb, dA, C, cs, cs_stride, m_indices,
+                                     rows, F, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -594,6 +610,7 @@ def dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride: int, m_indices=None, strea
     """e4m3 Q [rows,K] with scales per 1x128 -> Qb [rows,K] with scales per
     128x128, sb [K/128, rows/128] (contiguous layout)."""
     func = "dg_fp8_1x128_to_128x128"
+    calls = _calls or _marshal()
     try:
         rows, K = Q.shape
     except (AttributeError, ValueError):
@@ -601,7 +618,7 @@ def dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride: int, m_indices=None, strea
     dev = _check_tensors(func, "Qb sb Q sa m_indices",
                          Qb, _U8, rows * K, sb, _F32, _cdiv(K, 128) * _cdiv(rows, 128), Q, _U8, rows * K,
                          sa, _F32, _sa_need(_cdiv(K, 128), sa_stride, rows), m_indices, _I32, rows)
-    status = _calls.dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride, m_indices, rows, K, _raw_stream(stream, dev))
+    status = calls.dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride, m_indices, rows, K, _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 
@@ -668,6 +685,7 @@ def dg_get_col_major_tma_aligned_tensor(s):
 
     Layout helper for callers (the pages' get_col_major_tma_aligned_tensor);
     runs as torch tensor ops outside the timed path."""
+    _need_torch()
     grouped = s.dim() == 3
     s3 = s if grouped else s.unsqueeze(0)
     G, M, nkb = s3.shape
