@@ -1,5 +1,6 @@
 """Build libdg.so (the sm_100a CUDA library behind include/dg.h) in-tree with nvcc, and
-_dgcall.so (argument marshalling of the binding's frequent calls) with g++."""
+_dgcall.so (argument marshalling of the binding's frequent calls) with g++, where g++ and torch's
+C++ headers are at hand: libdg.so and the calls that start from m_indices or masked_m work without it."""
 from __future__ import annotations
 
 import os
@@ -44,6 +45,20 @@ def call_command(out: str = CALL_LIB) -> list:
             "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", f"-Wl,-rpath,{lib}"]
 
 
+def call_unavailable() -> str:
+    """Why the extension cannot be built here ("": it can)."""
+    if not shutil.which("g++"):
+        return "no g++"
+    try:
+        from torch.utils import cpp_extension
+    except ImportError:
+        return "no torch"
+    header = os.path.join("torch", "csrc", "autograd", "python_variable.h")
+    if not any(os.path.exists(os.path.join(d, header)) for d in cpp_extension.include_paths()):
+        return "no C++ headers of torch"
+    return ""
+
+
 def _newer(out: str, deps: list) -> bool:
     if not os.path.exists(out):
         return False
@@ -59,7 +74,12 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if force or not up_to_date():
         subprocess.run(command(verbose_ptxas=verbose_ptxas), check=True)
     if force or not _newer(CALL_LIB, [CALL_SOURCE, HEADER]):
-        subprocess.run(call_command(), check=True)
+        why = call_unavailable()
+        if why:
+            print(f"{CALL_LIB} is not built ({why}): routing, dispatch, combine and checkpoint calls need it",
+                  file=sys.stderr)
+        else:
+            subprocess.run(call_command(CALL_LIB), check=True)
     return LIB
 
 
