@@ -141,7 +141,9 @@ def _marshal():
     try:
         from . import _dgcall
     except ImportError as e:
-        raise RuntimeError(f"the extension _dgcall.so is missing in {_HERE}: run __graft_entry__.build() first") from e
+        path = os.path.join(_HERE, "_dgcall.so")
+        why = f"does not load ({e})" if os.path.exists(path) else "is missing"
+        raise RuntimeError(f"the extension {path} {why}: run __graft_entry__.build() first") from e
     for name in _CALLS:
         _dgcall.bind(name, ctypes.cast(getattr(L, name), ctypes.c_void_p).value)
     _calls = _dgcall

@@ -3,6 +3,7 @@ _dgcall.so (argument marshalling of the binding's frequent calls) with g++, wher
 C++ headers are at hand: libdg.so and the calls that start from m_indices or masked_m work without it."""
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -59,6 +60,25 @@ def call_unavailable() -> str:
     return ""
 
 
+def call_tag() -> str:
+    """What the extension's binary interface depends on, kept beside it: the Python and the torch it is built for."""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "none"
+    return f"{sysconfig.get_config_var('SOABI')} torch {torch}\n"
+
+
+def call_up_to_date() -> bool:
+    if not _newer(CALL_LIB, [CALL_SOURCE, HEADER]):
+        return False
+    try:
+        with open(CALL_LIB + ".tag") as f:
+            return f.read() == call_tag()
+    except OSError:
+        return False
+
+
 def _newer(out: str, deps: list) -> bool:
     if not os.path.exists(out):
         return False
@@ -73,13 +93,15 @@ def up_to_date() -> bool:
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if force or not up_to_date():
         subprocess.run(command(verbose_ptxas=verbose_ptxas), check=True)
-    if force or not _newer(CALL_LIB, [CALL_SOURCE, HEADER]):
+    if force or not call_up_to_date():
         why = call_unavailable()
         if why:
             print(f"{CALL_LIB} is not built ({why}): routing, dispatch, combine and checkpoint calls need it",
                   file=sys.stderr)
         else:
             subprocess.run(call_command(CALL_LIB), check=True)
+            with open(CALL_LIB + ".tag", "w") as f:
+                f.write(call_tag())
     return LIB
 
 

@@ -1,8 +1,10 @@
 """Building the marshalling extension: a user of libdg.so alone needs neither g++ nor torch's headers (no GPU needed)."""
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 import pytest
 
@@ -60,3 +62,28 @@ def test_a_current_extension_is_left_alone(runs):
     assert len(runs) == 1 and "g++" in runs[0][0]
     dgbuild.build()
     assert len(runs) == 1
+
+
+def test_an_extension_of_another_torch_or_python_is_built_again(runs, monkeypatch):
+    dgbuild.build()
+    assert len(runs) == 1
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.0.0+other")
+    dgbuild.build()
+    assert len(runs) == 2
+    dgbuild.build()
+    assert len(runs) == 2
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399")
+    dgbuild.build()
+    assert len(runs) == 3
+
+
+def test_an_extension_that_does_not_load_is_not_called_missing(monkeypatch):
+    import moe_grouped_gemm_weight_b200 as dg
+    dgbuild.build()
+    assert os.path.exists(dgbuild.CALL_LIB)
+    monkeypatch.setattr(dg, "_calls", None)
+    monkeypatch.setitem(sys.modules, dg.__name__ + "._dgcall", None)
+    monkeypatch.delattr(dg, "_dgcall", raising=False)
+    with pytest.raises(RuntimeError, match="_dgcall.so.*does not load") as ei:
+        dg._marshal()
+    assert "missing" not in str(ei.value) and isinstance(ei.value.__cause__, ImportError)
