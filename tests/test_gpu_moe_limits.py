@@ -110,6 +110,51 @@ def test_masked_layout_whose_ranks_pass_31_bits(dgm):
     assert dgm.dg_get_device_error() == 0
 
 
+@pytest.mark.parametrize("sms", [1, 3, 7])
+def test_nothing_is_left_out_under_an_sm_cap(dgm, sms):
+    # Every output starts from the same bytes with and without the cap; what a call leaves, it leaves in both.  The
+    # GEMMs' results stay.  dw's partial sums may be joined in another order: one rounding for each of the 1152 / 16
+    # products of a lane and the joins, of the terms' magnitudes, in both runs.
+    L = Layer(dgm, 300, 4, 9, 1152, 384, seed=3)
+    for t in (L.Hid, L.Y, L.dA, L.dXr):
+        t.zero_()
+    L.forward()
+    L.backward()
+    made = [n for n, t in vars(L).items() if torch.is_tensor(t) and n not in
+            ("X", "logits", "bias", "dout", "W1", "W2", "Hid", "Y", "dA", "dXr", "dW1", "dW2")]
+    given = L.dw.clone()
+
+    def step():
+        for n in made:
+            getattr(L, n).view(torch.uint8).fill_(0x11)
+        dgm.dg_route_topk(L.idx, L.wt, L.logits, L.bias, score=dgm.DG_SCORE_SIGMOID, renorm=True, scale=2.0)
+        dgm.dg_route_layout(L.row_of, L.mi, L.slot_of, L.off, L.cnt, L.idx)
+        dgm.dg_dispatch_fp8_1x128(L.Q, L.sa, L.R, L.X, L.row_of)
+        dgm.dg_swiglu_fp8(L.Q2, L.sa2, L.R, L.Hid, L.C, L.cs, L.R, m_indices=L.mi)
+        dgm.dg_combine(L.out, L.Y, L.row_of, L.wt)
+        dgm.dg_combine_bwd(L.dw, L.dYr, L.sr, L.R, L.dYc, L.sc, L.H, L.dout, L.Y, L.row_of, L.slot_of, L.wt)
+        dgm.dg_swiglu_fp8_bwd(L.dHr, L.shr, L.R, L.dHc, L.shc, 2 * L.F, L.Qa, L.sb, L.dA, L.C, L.cs, L.R, m_indices=L.mi)
+        dgm.dg_fp8_1x128_to_128x128(L.Xb, L.sx, L.Q, L.sa, L.R, m_indices=L.mi)
+        dgm.dg_combine(L.dX, L.dXr, L.row_of)
+        dgm.dg_route_topk_bwd(L.dlogits, given, L.logits, L.idx, score=dgm.DG_SCORE_SIGMOID, renorm=True, scale=2.0)
+        torch.cuda.synchronize()
+        return {n: getattr(L, n).clone() for n in made}
+
+    want = step()
+    assert all(bool((want[n].view(torch.uint8) != 0x11).any()) for n in made)
+    dgm.dg_set_num_sms(sms)
+    try:
+        got = step()
+    finally:
+        dgm.dg_set_num_sms(0)
+    for n in made:
+        if n != "dw":
+            assert torch.equal(got[n].view(torch.uint8), want[n].view(torch.uint8)), n
+    row = L.row_of.long()
+    mag = (L.dout.float()[:, None] * L.Y[row.clamp_min(0)].float()).abs().sum(2) * (row >= 0)
+    assert bool(((got["dw"] - want["dw"]).abs() <= 2 * (1152 / 16 + 32) * U * mag).all())
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_sigmoid_gradient_where_the_score_is_nearly_one(dgm, dtype):
     # s (1 - s) with 1 - s for itself: 1 / (1 + e) and e / (1 + e), an exponential of 2 ulp (4 U), an addition, a
