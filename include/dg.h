@@ -283,8 +283,12 @@ DG_API dg_status dg_grouped_masked_nt(uint16_t* D, const uint8_t* A, const float
  *
  * Words: a token t < T has k slots, slot t*k + j; `rows` is the number of rows
  * of the grouped layout (M_total, or G*M_max).  Sums, softmax statistics and
- * products are FP32; e4m3 casts are dg_to_fp8_1x128's steps (amax floored at
- * 1e-4, s = amax/448, x * (448/amax) rounded to nearest even, NaN stays NaN).
+ * products are FP32.  Sigmoids, exponentials and renormalised quotients are good
+ * to 8 * 2^-24 of their value (zero below 2^-126), but for the terms of the sum
+ * that dg_route_topk's softmax scores are divided by, (4 + |x|) * 2^-24 for a
+ * logit x below the largest.  e4m3 casts are dg_to_fp8_1x128's steps (amax
+ * floored at 1e-4, s = amax/448, x * (448/amax) rounded to nearest even, NaN
+ * stays NaN).
  * The general conventions at the top hold: nothing is allocated, synchronised
  * or read by the host, every call may be captured, results are deterministic.
  */
@@ -471,7 +475,13 @@ DG_API dg_status dg_fp8_1x128_to_128x128(uint8_t* Qb, float* sb, const uint8_t* 
 DG_API void dg_set_pdl(int enable);
 DG_API int dg_get_pdl(void);
 
-/* Cap the number of SMs the persistent kernels use (n <= 0: all SMs). */
+/*
+ * Cap the number of SMs the persistent kernels use (n <= 0: all SMs): those of
+ * the GEMMs, dg_to_fp8_1x128, dg_route_topk and its gradient,
+ * dg_dispatch_fp8_1x128, dg_swiglu_fp8 and its gradient.  dg_route_layout is one
+ * cluster of at most 8 CTAs; dg_to_fp8_128x128, dg_combine, dg_combine_bwd and
+ * dg_fp8_1x128_to_128x128 launch a CTA for each piece of work and are not capped.
+ */
 DG_API void dg_set_num_sms(int n);
 /* Current cap; the device's SM count when no cap is set (0 without a GPU). */
 DG_API int dg_get_num_sms(void);

@@ -68,8 +68,9 @@ constexpr int kSwigluCtas = 4;  // resident per SM
 
 // Half-warp h of a CTA takes a row, two pairs of gate and up blocks at a time:
 // six tiles whose scales are found together (places 3 and 7 of 8 are spare).
-// 32768 rows of F = 2048 with the checkpoint: 91 us, 5.2 TB/s, bound by HBM and,
-// at 59 % of the issue slots, nearly by instructions.
+// 32768 rows of F = 2048 with the checkpoint: 94 us, 5.1 TB/s, bound by HBM and,
+// at 62 % of the issue slots, nearly by instructions; without it 68 us.  512 slots
+// in a masked layout of 32 groups of 64 rows, no checkpoint: 4.1 us.
 __global__ void __launch_bounds__(kCastThreads, kSwigluCtas)
 swiglu_fp8_kernel(const SwigluParams p) {
     griddep_wait();
@@ -163,7 +164,7 @@ constexpr int kSwigluBwdFlags = kSwigluBwdThreads / 32 * 128 * 4;  // behind the
 // itself use, no barrier guards them; the row flags come a tile ahead of the
 // rows they decide on.
 //
-// 32768 rows of F = 2048: 152 us, 4.1 TB/s, bound by instructions (63 % of the
+// 32768 rows of F = 2048: 156 us, 4.0 TB/s, bound by instructions (64 % of the
 // issue slots with the 16 warps that the registers allow).
 __global__ void __launch_bounds__(kSwigluBwdThreads)
 swiglu_fp8_bwd_kernel(const SwigluBwdParams p) {

@@ -428,9 +428,9 @@ struct Top4 {
 // values, and by FP64 values where those are not clearly apart.  bf16 logits
 // without a bias fit a key whole.
 //
-// 16384 tokens of 256 float32 logits, 8 groups, bias: 18.5 us on one B200 in
-// graph replays (HBM alone 2.6 us), 659 instructions a token at 56 % of the
-// issue slots; 17.0 us without any FP64.
+// 16384 tokens of 256 float32 logits, 8 groups, bias: 18.7 us on one B200 in
+// graph replays (HBM alone 2.6 us), 668 instructions a token at 56 % of the
+// issue slots, 20 of them spills (14 loads, 6 stores); 17.0 us without any FP64.
 template <int EPL, bool kSpans, typename L>
 __global__ void __launch_bounds__(kRouteWarps * 32, route_ctas(EPL))
 route_topk_kernel(const RouteParams p) {
@@ -783,7 +783,7 @@ __device__ __forceinline__ void store_chunk(uint16_t* p, const float* f) {
 // is without a choice, then the k elements (a row put together in shared memory
 // first took 11.7 us below).  What the next token needs is on its way meanwhile.
 // kWide: rows are 16-byte aligned and every lane has EPL experts.
-// 16384 tokens of 256 float32 logits, softmax: 8.6 us, 4.0 TB/s, bound by
+// 16384 tokens of 256 float32 logits, softmax: 8.9 us, 3.9 TB/s, bound by
 // instructions (HBM alone 5.4 us); 65536 of 1024: 90 us, 6.0 TB/s.  A lane's wide
 // chunks lie 32 chunks apart, so that a load takes whole lines: 203 us there with
 // 32 logits in a row to a lane, and 568 against 97 us for 1000.
