@@ -7,7 +7,7 @@ import threading
 import pytest
 import torch
 
-from tests.test_gpu_moe import Layer, Layout, codes, scales
+from tests.test_gpu_moe import Layer, codes, scales
 from tests.test_gpu_route import check_route, scores64
 
 pytestmark = pytest.mark.gpu
