@@ -95,6 +95,8 @@ typedef enum dg_status {
 #define DG_DEVERR_BAD_K_OFFSET 16u  /* K-grouped: k_offsets not increasing       */
                                     /* multiples of 128 within [0, K]            */
 #define DG_DEVERR_BAD_EXPERT 32u    /* layout: a chosen expert not in [-1,E)     */
+#define DG_DEVERR_BAD_SEQ_OFFSET 64u  /* balance: seq_offsets falling or outside   */
+                                    /* [0, T]                                    */
 
 /*
  * Dense GEMM: D[M,N] = scaled A[M,K] . B[N,K]^T (section "常规密集型 GEMM（非分组）",
@@ -459,6 +461,160 @@ DG_API dg_status dg_swiglu_fp8_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_
 DG_API dg_status dg_fp8_1x128_to_128x128(uint8_t* Qb, float* sb, const uint8_t* Q, const float* sa, int sa_stride,
                                          const int32_t* m_indices, int rows, int K, void* stream);
 
+/*
+ * Between a block's GEMMs and the rest of a transformer: a dense GEMM with bias,
+ * activation and residual in its epilogue, the norms before and after a block
+ * fused with its gate and residual scale, and a router's balance loss (no
+ * counterpart on the pages).  One step of a pre- and post-normed block is
+ *   dg_norm_residual (the block's input, as bf16 for the router or e4m3 for a
+ *   GEMM), the block, dg_norm_residual (its output into the stream, and the next
+ *   block's input),
+ * the block being the MoE calls above, with dg_balance_loss behind dg_route_topk,
+ * or two dense products,
+ *   dg_fp8_gemm_nt_epilogue (bias, activation, Q for the second, Z kept),
+ *   dg_fp8_gemm_nt_epilogue (bias, residual),
+ * whose gradients are dg_epilogue_bwd, dg_fp8_gemm_nn (input) and dg_fp8_gemm_tn
+ * (weight), dg_norm_residual_bwd and dg_balance_loss_bwd.
+ * The general conventions at the top hold.  Workspaces (`ws`) are the caller's,
+ * written before they are read; what they hold between calls does not matter.
+ * Calls that may overlap on the GPU (streams, graphs) need one each.  All sums are
+ * FP32 or more, in an order that depends on the sizes only (dg_norm_residual_bwd's
+ * sums over tokens also on the SM cap), so results repeat bit for bit.
+ */
+
+/* Activations of dg_fp8_gemm_nt_epilogue: z, max(z, 0), z Phi(z), its form with tanh
+ * (z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))), z / (1 + exp(-z)). */
+#define DG_ACT_NONE 0
+#define DG_ACT_RELU 1
+#define DG_ACT_GELU 2
+#define DG_ACT_GELU_TANH 3
+#define DG_ACT_SILU 4
+
+/*
+ * Dense GEMM with an epilogue: z = scaled A . B^T + bias, v = act(z) + residual.
+ * All steps are FP32 on the accumulators; each output is rounded once.
+ *   D          bf16 [M][N]: v; may be the residual itself
+ *   Z          bf16 [M][N]: z, which dg_epilogue_bwd needs
+ *   Q, sq      v cast per 1x128 (dg_to_fp8_1x128's steps, from FP32): e4m3 [M][N],
+ *              sq[(n/128)*sq_stride + m], sq_stride >= M; N % 128 == 0
+ *   bias       float32 [N], residual bf16 [M][N]
+ * D, Z, Q, bias and residual may be null, but one of D, Z and Q is given.  All else
+ * as in dg_fp8_gemm_nt, its K-split workspace too.
+ */
+DG_API dg_status dg_fp8_gemm_nt_epilogue(uint16_t* D, uint16_t* Z, uint8_t* Q, float* sq, int sq_stride,
+                                         const uint8_t* A, const float* sa, int sa_stride, const uint8_t* B,
+                                         const float* sb, const float* bias, int act, const uint16_t* residual, int M,
+                                         int N, int K, void* stream);
+
+/* Floats of dg_epilogue_bwd's workspace; -1 for sizes it does not take. */
+DG_API int dg_get_bias_workspace(int M, int N);
+
+/*
+ * Gradient of that epilogue: dz = dD * act'(Z), in both casts that the backward
+ * GEMMs read, and the bias's gradient.  (The residual's gradient is dD.)
+ *   Qr, sr     dz per 1x128: e4m3 [M][N], sr[(n/128)*sr_stride + m], sr_stride >= M
+ *              (A of dg_fp8_gemm_nn with the weights as B: the input's gradient)
+ *   Qc, sc     dz per 128x1: e4m3 [R][N], R = M rounded up to whole 128 rows,
+ *              sc[(m/128)*sc_stride + n], sc_stride >= N (A of dg_fp8_gemm_tn, whose
+ *              K is the rows: the weights' gradient).  Rows past M are zeros.
+ *   dbias      float32 [N] or null: sum over the rows of dz, before the casts
+ *   ws         dg_get_bias_workspace(M, N) floats; null without dbias
+ *   dD, Z      bf16 [M][N]; Z may be null for DG_ACT_NONE
+ * N % 128 == 0.  M == 0 writes zeros to dbias and nothing else.
+ */
+DG_API dg_status dg_epilogue_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, float* sc, int sc_stride,
+                                 float* dbias, float* ws, const uint16_t* dD, const uint16_t* Z, int act, int M, int N,
+                                 void* stream);
+
+/*
+ * The norms between two blocks, with the residual stream between them:
+ *   r_y = post_norm != 0 ? 1 / sqrt(mean_n y^2 + eps) : 1
+ *   u   = x + scale * gate[t] * w_post[n] * r_y * y
+ *   r_u = 1 / sqrt(mean_n u^2 + eps)
+ *   h   = u * r_u * w_pre[n]
+ *   U          [T][N], the stream's type: u rounded (h is formed from u itself)
+ *   H          bf16 [T][N]: h
+ *   Q, sq      h cast per 1x128: e4m3 [T][N], sq[(n/128)*sq_stride + t], sq_stride >=
+ *              T; N % 128 == 0
+ *   rstd       float32 [T][2]: r_y, r_u, for dg_norm_residual_bwd
+ *   X          [T][N], the stream: bf16 or float32 (x_dtype, DG_DTYPE_*)
+ *   Y          bf16 [T][N], the block's output
+ *   w_post, w_pre float32 [N], gate float32 [T]
+ * U, H, Q and rstd may be null, but not all.  U may be X.  Null X: zeros; null Y: u =
+ * x (the first block's norm alone); null weights and gate: ones.  eps > 0.
+ * N % 8 == 0, N <= 16384.  Sums of squares are FP32: a row whose sum leaves it has
+ * h = 0.  T == 0 launches nothing.
+ */
+DG_API dg_status dg_norm_residual(void* U, uint16_t* H, uint8_t* Q, float* sq, int sq_stride, float* rstd,
+                                  const void* X, int x_dtype, const uint16_t* Y, const float* w_post,
+                                  const float* gate, const float* w_pre, int T, int N, int post_norm, float scale,
+                                  float eps, void* stream);
+
+/* Floats of dg_norm_residual_bwd's workspace; -1 for sizes it does not take. */
+DG_API int dg_get_norm_workspace(int T, int N);
+
+/*
+ * Gradient of dg_norm_residual, with a = u r_u and b = y r_y:
+ *   du = dU + r_u (w_pre dH - a mean(a w_pre dH)),  dX = du,  d = scale gate[t] du
+ *   dw_pre = sum_t dH a,  dw_post = sum_t d b,  dgate = scale sum_n du w_post b
+ *   dY = post_norm != 0 ? r_y (w_post d - b mean(b w_post d)) : w_post d
+ *   dX         [T][N], the stream's type; may be dU
+ *   dY bf16 [T][N], dgate float32 [T], dw_post and dw_pre float32 [N]
+ *   ws         dg_get_norm_workspace(T, N) floats, 16-byte aligned; null without dw_post and dw_pre
+ *   dU         [T][N], the stream's type: gradient of U; null: zeros
+ *   dH         bf16 [T][N]: gradient of H; null: zeros
+ *   U, rstd    as dg_norm_residual wrote them; Y, w_post, gate, w_pre, post_norm and
+ *              scale as given to it
+ * Outputs may be null, but not all; dY, dgate and dw_post need Y; one of dU and dH is
+ * given.  T == 0 writes zeros to dw_post and dw_pre and nothing else.
+ */
+DG_API dg_status dg_norm_residual_bwd(void* dX, uint16_t* dY, float* dgate, float* dw_post, float* dw_pre, float* ws,
+                                      const void* dU, const uint16_t* dH, const void* U, int x_dtype,
+                                      const uint16_t* Y, const float* rstd, const float* w_post, const float* gate,
+                                      const float* w_pre, int T, int N, int post_norm, float scale, void* stream);
+
+/* Floats of dg_balance_loss's workspace; -1 for sizes it does not take. */
+DG_API int dg_get_balance_workspace(int T, int E, int S);
+
+/*
+ * Balance loss of a router and the slots of each expert, per sequence: sequence s
+ * holds the tokens [seq_offsets[s], seq_offsets[s+1]), L_s of them; L in all.
+ *   n[s][e] = slots of the sequence with topk_idx == e (values outside [0,E): none)
+ *   p_t     = softmax(l_t), or sigmoid(l_t) over its sum
+ *   P[s][e] = mean over the sequence of p_te
+ *   loss    = coef * sum_s L_s / L * sum_e E n[s][e] / (k L_s) * P[s][e]
+ * so a token counts the same in whichever sequence; perfectly even loads give coef.
+ * Sequences without tokens have zeros; tokens in no sequence (padding before the
+ * first or behind the last) count nowhere; L == 0 gives 0.  A logit of -inf has p = 0,
+ * and so has a token with no other; a NaN makes its token's p NaN.
+ *   loss       float32 [1]
+ *   counts     int32 [S][E]: n (the balance of a bias that dg_route_topk takes, too)
+ *   probs      float32 [S][E] or null: P
+ *   ws         dg_get_balance_workspace(T, E, S) floats
+ *   logits     [T][E], bf16 or float32 (logits_dtype); topk_idx int32 [T][k]
+ *   seq_offsets int32 [S+1] on the device, not falling, within [0, T] (other values
+ *              set DG_DEVERR_BAD_SEQ_OFFSET, and the sums are then undefined); null,
+ *              with S == 1: all tokens
+ * E <= 1024, k <= E.
+ */
+DG_API dg_status dg_balance_loss(float* loss, int32_t* counts, float* probs, float* ws, const void* logits,
+                                 int logits_dtype, const int32_t* topk_idx, const int32_t* seq_offsets, int T, int E,
+                                 int k, int S, int score, float coef, void* stream);
+
+/*
+ * Gradient of that loss with respect to the logits (the choice has none):
+ *   dlogits = add + dloss * coef / L * p_j * (f_j - sum_e f_e p_e),  f_e = E n[s][e] / (k L_s),
+ * for sigmoid scores times 1 - sigmoid(l_j); `add` alone for tokens in no sequence.
+ *   dlogits    [T][E], the logits' type
+ *   add        [T][E], the logits' type, or null (zeros): dg_route_topk_bwd's gradient,
+ *              say; may be dlogits
+ *   dloss      float32 [1] on the device, or null: 1
+ *   counts     as dg_balance_loss wrote them
+ */
+DG_API dg_status dg_balance_loss_bwd(void* dlogits, const void* add, const float* dloss, const void* logits,
+                                     int logits_dtype, const int32_t* counts, const int32_t* seq_offsets, int T, int E,
+                                     int k, int S, int score, float coef, void* stream);
+
 /* Utility functions (section "工具函数" (utility functions) of the same page). */
 
 /*
@@ -478,9 +634,11 @@ DG_API int dg_get_pdl(void);
 /*
  * Cap the number of SMs the persistent kernels use (n <= 0: all SMs): those of
  * the GEMMs, dg_to_fp8_1x128, dg_route_topk and its gradient,
- * dg_dispatch_fp8_1x128, dg_swiglu_fp8 and its gradient.  dg_route_layout is one
- * cluster of at most 8 CTAs; dg_to_fp8_128x128, dg_combine, dg_combine_bwd and
- * dg_fp8_1x128_to_128x128 launch a CTA for each piece of work and are not capped.
+ * dg_dispatch_fp8_1x128, dg_swiglu_fp8 and its gradient, dg_norm_residual and its
+ * gradient, dg_balance_loss_bwd.  dg_route_layout is one cluster of at most 8 CTAs;
+ * dg_to_fp8_128x128, dg_combine, dg_combine_bwd, dg_fp8_1x128_to_128x128,
+ * dg_epilogue_bwd and dg_balance_loss launch a CTA for each piece of work and are not
+ * capped.
  */
 DG_API void dg_set_num_sms(int n);
 /* Current cap; the device's SM count when no cap is set (0 without a GPU). */

@@ -27,8 +27,10 @@ DG_OK, DG_ERR_INVALID_ARG, DG_ERR_UNSUPPORTED, DG_ERR_MISALIGNED, DG_ERR_CUDA = 
 DG_DEVERR_TIMEOUT, DG_DEVERR_BAD_M_INDEX, DG_DEVERR_BAD_MASKED_M, DG_DEVERR_NOT_POW2 = 1, 2, 4, 8
 DG_DEVERR_BAD_K_OFFSET = 16
 DG_DEVERR_BAD_EXPERT = 32
+DG_DEVERR_BAD_SEQ_OFFSET = 64
 DG_DTYPE_BF16, DG_DTYPE_FP32 = 0, 1
 DG_SCORE_SOFTMAX, DG_SCORE_SIGMOID = 0, 1
+DG_ACT_NONE, DG_ACT_RELU, DG_ACT_GELU, DG_ACT_GELU_TANH, DG_ACT_SILU = range(5)
 
 _lock = threading.Lock()
 _lib = None
@@ -89,7 +91,16 @@ def lib() -> ctypes.CDLL:
                     ("dg_combine_bwd", [P, P, P, I, P, P, I, P, P, P, P, P, I, I, I, I, P]),
                     ("dg_swiglu_fp8", [P, P, I, P, P, I, P, P, I, I, I, P]),
                     ("dg_swiglu_fp8_bwd", [P, P, I, P, P, I, P, P, P, P, P, I, P, I, I, P]),
-                    ("dg_fp8_1x128_to_128x128", [P, P, P, P, I, P, I, I, P])):
+                    ("dg_fp8_1x128_to_128x128", [P, P, P, P, I, P, I, I, P]),
+                    ("dg_fp8_gemm_nt_epilogue", [P, P, P, P, I, P, P, I, P, P, P, I, P, I, I, I, P]),
+                    ("dg_get_bias_workspace", [I, I]),
+                    ("dg_epilogue_bwd", [P, P, I, P, P, I, P, P, P, P, I, I, I, P]),
+                    ("dg_norm_residual", [P, P, P, P, I, P, P, I, P, P, P, P, I, I, I, F, F, P]),
+                    ("dg_get_norm_workspace", [I, I]),
+                    ("dg_norm_residual_bwd", [P, P, P, P, P, P, P, P, P, I, P, P, P, P, P, I, I, I, F, P]),
+                    ("dg_get_balance_workspace", [I, I, I]),
+                    ("dg_balance_loss", [P, P, P, P, P, I, P, P, I, I, I, I, I, F, P]),
+                    ("dg_balance_loss_bwd", [P, P, P, P, I, P, P, I, I, I, I, I, F, P])):
                 getattr(L, nm).restype = I
                 getattr(L, nm).argtypes = at
             L.dg_set_pdl.restype = None
@@ -123,7 +134,9 @@ def lib() -> ctypes.CDLL:
 
 
 _CALLS = ("dg_route_topk", "dg_route_topk_bwd", "dg_route_layout", "dg_dispatch_fp8_1x128", "dg_combine",
-          "dg_combine_bwd", "dg_swiglu_fp8", "dg_swiglu_fp8_bwd", "dg_fp8_1x128_to_128x128")
+          "dg_combine_bwd", "dg_swiglu_fp8", "dg_swiglu_fp8_bwd", "dg_fp8_1x128_to_128x128",
+          "dg_fp8_gemm_nt_epilogue", "dg_epilogue_bwd",
+          "dg_norm_residual", "dg_norm_residual_bwd", "dg_balance_loss", "dg_balance_loss_bwd")
 _calls = None
 
 
@@ -134,7 +147,7 @@ def _need_torch() -> None:
 
 
 def _marshal():
-    """The calls around the grouped GEMMs as vector calls (csrc/dg_pycall.cpp), bound to the loaded library."""
+    """The calls around the GEMMs as vector calls (csrc/dg_pycall.cpp), bound to the loaded library."""
     global _calls
     L = lib()
     _need_torch()
@@ -621,6 +634,187 @@ def dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride: int, m_indices=None, strea
                          Qb, _U8, rows * K, sb, _F32, _cdiv(K, 128) * _cdiv(rows, 128), Q, _U8, rows * K,
                          sa, _F32, _sa_need(_cdiv(K, 128), sa_stride, rows), m_indices, _I32, rows)
     status = calls.dg_fp8_1x128_to_128x128(Qb, sb, Q, sa, sa_stride, m_indices, rows, K, _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
+
+
+def _int32_sizes(*sizes) -> bool:
+    return all(abs(int(x)) <= 0x7FFFFFFF for x in sizes)  # ctypes would keep the low 32 bits
+
+
+def dg_fp8_gemm_nt_epilogue(D, A, sa, sa_stride: int, B, sb, bias=None, act: int = DG_ACT_NONE, residual=None, Z=None,
+                            Q=None, sq=None, sq_stride: int = 0, stream=None) -> None:
+    """z = scaled A[M,K] . B[N,K]^T + bias [N], v = act(z) + residual [M,N]: bf16 D
+    (v) and Z (z), and v as e4m3 Q [M,N] with its transposed scales sq (any of
+    D, Z, Q may be None, but not all; D may be the residual)."""
+    func = "dg_fp8_gemm_nt_epilogue"
+    calls = _calls or _marshal()
+    try:
+        M, K = A.shape
+        N, Kb = B.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, A=A, B=B) from None
+    _check_dim(func, "K of B", Kb, K)
+    nkb, nnb = _cdiv(K, 128), _cdiv(N, 128)
+    dev = _check_tensors(func, "D A sa B sb bias residual Z Q sq",
+                         D, _BF16, M * N, A, _U8, M * K, sa, _F32, _sa_need(nkb, sa_stride, M), B, _U8, N * K,
+                         sb, _F32, nnb * nkb, bias, _F32, N, residual, _BF16, M * N, Z, _BF16, M * N, Q, _U8, M * N,
+                         sq if Q is not None else None, _F32, _sa_need(nnb, sq_stride, M))
+    status = calls.dg_fp8_gemm_nt_epilogue(D, Z, Q, sq, sq_stride, A, sa, sa_stride, B, sb, bias, act, residual, M, N,
+                                           K, _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
+
+
+def dg_get_bias_workspace(M: int, N: int) -> int:
+    """Floats of dg_epilogue_bwd's workspace; -1 for sizes it does not take."""
+    return int(lib().dg_get_bias_workspace(int(M), int(N))) if _int32_sizes(M, N) else -1
+
+
+def dg_epilogue_bwd(Qr, sr, sr_stride: int, Qc, sc, sc_stride: int, dD, Z=None, act: int = DG_ACT_NONE, dbias=None,
+                    ws=None, stream=None) -> None:
+    """Gradient of dg_fp8_gemm_nt_epilogue: bf16 dD and Z [M,N] -> dz cast per
+    1x128 (Qr [M,N], sr) and per 128x1 (Qc [M rounded up to 128, N], sc), and the
+    float32 bias gradient dbias [N]."""
+    func = "dg_epilogue_bwd"
+    calls = _calls or _marshal()
+    try:
+        M, N = dD.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, dD=dD) from None
+    mb, nb = _cdiv(M, 128), _cdiv(N, 128)
+    dev = _check_tensors(func, "Qr sr Qc sc dD Z dbias ws",
+                         Qr, _U8, M * N, sr, _F32, _sa_need(nb, sr_stride, M), Qc, _U8, 128 * mb * N,
+                         sc, _F32, _sa_need(mb, sc_stride, N), dD, _BF16, M * N,
+                         Z if act != DG_ACT_NONE else None, _BF16, M * N, dbias, _F32, N,
+                         ws if dbias is not None else None, _F32, mb * N)
+    status = calls.dg_epilogue_bwd(Qr, sr, sr_stride, Qc, sc, sc_stride, dbias, ws, dD, Z, act, M, N,
+                                   _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
+
+
+def _stream_dtype(func: str, *tensors) -> int:
+    """Element type of the residual stream: that of the first tensor given."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            if t.dtype == torch.bfloat16:
+                return DG_DTYPE_BF16
+            if t.dtype == torch.float32:
+                return DG_DTYPE_FP32
+            raise DGError(func, DG_ERR_INVALID_ARG, f"the stream is {t.dtype}, the call takes bfloat16 or float32")
+    return DG_DTYPE_BF16
+
+
+def dg_norm_residual(U, X, Y=None, H=None, Q=None, sq=None, sq_stride: int = 0, rstd=None, w_post=None, gate=None,
+                     w_pre=None, post_norm: bool = False, scale: float = 1.0, eps: float = 1e-6, stream=None) -> None:
+    """u = x + scale * gate[t] * w_post * (norm of) y into U [T,N] (X's type,
+    bfloat16 or float32), and h = w_pre * norm of u as bf16 H [T,N] and as e4m3 Q
+    [T,N] with its transposed scales sq; float32 rstd [T,2] for the gradient.
+    Outputs that are None are left out; X or Y may be None."""
+    func = "dg_norm_residual"
+    calls = _calls or _marshal()
+    try:
+        T, N = (X if X is not None else Y).shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, **({"X": X} if X is not None else {"Y": Y})) from None
+    dt = _stream_dtype(func, X, U)
+    kind = _BF16 if dt == DG_DTYPE_BF16 else _F32
+    dev = _check_tensors(func, "U X Y H Q sq rstd w_post gate w_pre",
+                         U, kind, T * N, X, kind, T * N, Y, _BF16, T * N, H, _BF16, T * N, Q, _U8, T * N,
+                         sq if Q is not None else None, _F32, _sa_need(_cdiv(N, 128), sq_stride, T),
+                         rstd, _F32, 2 * T, w_post, _F32, N, gate, _F32, T, w_pre, _F32, N)
+    status = calls.dg_norm_residual(U, H, Q, sq, sq_stride, rstd, X, dt, Y, w_post, gate, w_pre, T, N,
+                                    1 if post_norm else 0, scale, eps, _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
+
+
+def dg_get_norm_workspace(T: int, N: int) -> int:
+    """Floats of dg_norm_residual_bwd's workspace; -1 for sizes it does not take."""
+    return int(lib().dg_get_norm_workspace(int(T), int(N))) if _int32_sizes(T, N) else -1
+
+
+def dg_norm_residual_bwd(dX, dU, dH, U, Y, rstd, dY=None, dgate=None, dw_post=None, dw_pre=None, ws=None, w_post=None,
+                         gate=None, w_pre=None, post_norm: bool = False, scale: float = 1.0, stream=None) -> None:
+    """Gradient of dg_norm_residual: dU [T,N] (U's type) and bf16 dH [T,N] (either
+    may be None: zeros) -> dX [T,N] (U's type), bf16 dY [T,N], float32 dgate [T],
+    dw_post and dw_pre [N] (with ws); outputs that are None are left out."""
+    func = "dg_norm_residual_bwd"
+    calls = _calls or _marshal()
+    try:
+        T, N = U.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, U=U) from None
+    dt = _stream_dtype(func, U)
+    kind = _BF16 if dt == DG_DTYPE_BF16 else _F32
+    sums = dw_post is not None or dw_pre is not None
+    dev = _check_tensors(func, "dX dU dH U Y rstd dY dgate dw_post dw_pre ws w_post gate w_pre",
+                         dX, kind, T * N, dU, kind, T * N, dH, _BF16, T * N, U, kind, T * N, Y, _BF16, T * N,
+                         rstd, _F32, 2 * T, dY, _BF16, T * N, dgate, _F32, T, dw_post, _F32, N, dw_pre, _F32, N,
+                         ws if sums else None, _F32, max(dg_get_norm_workspace(T, N), 0) if sums else 0,
+                         w_post, _F32, N, gate, _F32, T, w_pre, _F32, N)
+    status = calls.dg_norm_residual_bwd(dX, dY, dgate, dw_post, dw_pre, ws, dU, dH, U, dt, Y, rstd, w_post, gate, w_pre,
+                                        T, N, 1 if post_norm else 0, scale, _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
+
+
+def dg_get_balance_workspace(T: int, E: int, S: int = 1) -> int:
+    """Floats of dg_balance_loss's workspace; -1 for sizes it does not take."""
+    return int(lib().dg_get_balance_workspace(int(T), int(E), int(S))) if _int32_sizes(T, E, S) else -1
+
+
+def dg_balance_loss(loss, counts, probs, logits, topk_idx, ws, seq_offsets=None, score: int = DG_SCORE_SOFTMAX,
+                    coef: float = 1.0, stream=None) -> None:
+    """Balance loss of a router: logits [T,E] and int32 topk_idx [T,k] -> float32
+    loss [1], int32 counts [S,E] and float32 mean probabilities probs [S,E] (or
+    None) of the sequences between int32 seq_offsets [S+1] (None: one of all tokens)."""
+    func = "dg_balance_loss"
+    calls = _calls or _marshal()
+    try:
+        T, E = logits.shape
+        Ti, k = topk_idx.shape
+        S, Ec = counts.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, logits=logits, topk_idx=topk_idx, counts=counts) from None
+    _check_dim(func, "token count of topk_idx", Ti, T)
+    _check_dim(func, "E of counts", Ec, E)
+    dt = _logits_dtype(func, logits)
+    kind = _BF16 if dt == DG_DTYPE_BF16 else _F32
+    dev = _check_tensors(func, "loss counts probs logits topk_idx ws seq_offsets",
+                         loss, _F32, 1, counts, _I32, S * E, probs, _F32, S * E, logits, kind, T * E,
+                         topk_idx, _I32, T * k, ws, _F32, max(dg_get_balance_workspace(T, E, S), 0),
+                         seq_offsets, _I32, S + 1)
+    status = calls.dg_balance_loss(loss, counts, probs, ws, logits, dt, topk_idx, seq_offsets, T, E, k, S, score, coef,
+                                   _raw_stream(stream, dev))
+    if status != DG_OK:
+        _check(func, status)
+
+
+def dg_balance_loss_bwd(dlogits, logits, counts, k: int, dloss=None, add=None, seq_offsets=None,
+                        score: int = DG_SCORE_SOFTMAX, coef: float = 1.0, stream=None) -> None:
+    """Gradient of dg_balance_loss with k choices per token: dlogits [T,E] (the
+    logits' type) = add [T,E] (or zeros) + float32 dloss [1] (or 1) times the
+    loss's gradient; counts [S,E] as the forward call wrote them."""
+    func = "dg_balance_loss_bwd"
+    calls = _calls or _marshal()
+    try:
+        T, E = logits.shape
+        S, Ec = counts.shape
+    except (AttributeError, ValueError):
+        raise _rank_error(func, logits=logits, counts=counts) from None
+    _check_dim(func, "E of counts", Ec, E)
+    dt = _logits_dtype(func, logits)
+    kind = _BF16 if dt == DG_DTYPE_BF16 else _F32
+    for name, t in (("dlogits", dlogits), ("add", add)):
+        if isinstance(t, torch.Tensor) and t.dtype != logits.dtype:
+            raise DGError(func, DG_ERR_INVALID_ARG, f"{name} are {t.dtype}, logits {logits.dtype}")
+    dev = _check_tensors(func, "dlogits logits counts dloss add seq_offsets",
+                         dlogits, kind, T * E, logits, kind, T * E, counts, _I32, S * E, dloss, _F32, 1,
+                         add, kind, T * E, seq_offsets, _I32, S + 1)
+    status = calls.dg_balance_loss_bwd(dlogits, add, dloss, logits, dt, counts, seq_offsets, T, E, k, S, score, coef,
+                                       _raw_stream(stream, dev))
     if status != DG_OK:
         _check(func, status)
 

@@ -1,0 +1,153 @@
+// dg_act.cuh -- activations of the GEMM's epilogue, their slopes, and the
+// sigmoid they share, on pairs of FP32 values.
+//
+//   relu       max(z, 0)
+//   gelu       z Phi(z), Phi the normal distribution function
+//   gelu_tanh  z sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)), the form with tanh:
+//              (1 + tanh(x)) / 2 = sigmoid(2 x)
+//   silu       z sigmoid(z)
+//
+// A NaN stays one.  The tails keep their relative error: none is formed as a
+// difference from 1.
+#pragma once
+
+#include <stdint.h>
+
+namespace dg {
+
+enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4, kActCount = 5 };
+
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+
+// exp(-g) of a pair, g <= 88: 2^t 2^lo, t is -g log2(e) as rounded, lo what the
+// product and the constant's rounding leave of it (a first-order factor is good
+// to 2^-40), so the relative error does not grow with |g| (it was 64 times 2^-24 at
+// -80): the unit's 2^power and two roundings.
+__device__ __forceinline__ float2 exp_minus2(float2 g) {
+    constexpr float kLog2e = 1.4426950408889634f, kRest = static_cast<float>(1.4426950408889634074 - kLog2e);
+    float2 e = __fmul2_rn(g, pair(-kLog2e));
+    float2 lo = __ffma2_rn(g, pair(-kRest), __ffma2_rn(g, pair(-kLog2e), make_float2(-e.x, -e.y)));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    return __fmul2_rn(e, __ffma2_rn(lo, pair(0.6931471805599453f), pair(1.f)));
+}
+__device__ __forceinline__ float2 rcp2(float2 v) {
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(v.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(v.y));
+    return v;
+}
+
+// s = 1 / (1 + exp(-g)) of a pair, to 8 2^-24 of its value.  88 keeps an infinite
+// gate's product finite.
+__device__ __forceinline__ float2 sigmoid2(float2 g) {
+    return rcp2(__fadd2_rn(exp_minus2(make_float2(fminf(g.x, 88.f), fminf(g.y, 88.f))), pair(1.f)));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 clamp2(float2 v, float lo, float hi) {
+    return make_float2(min_nan(max_nan(v.x, lo), hi), min_nan(max_nan(v.y, lo), hi));
+}
+
+// sigmoid2 for any argument: below -126 the result is zero as at -126, which
+// keeps sigmoid2's exponent and what is left of it finite.
+__device__ __forceinline__ float2 sigmoid2_any(float2 g) { return sigmoid2(clamp2(g, -126.f, 88.f)); }
+
+// s = sigmoid(g) and c = 1 - s, each to a few 2^-24 of its own value; -87 <= g <= 88.
+__device__ __forceinline__ void sigmoid_parts2(float2 g, float2& s, float2& c) {
+    const float2 e = exp_minus2(g);
+    s = rcp2(__fadd2_rn(e, pair(1.f)));
+    c = __fmul2_rn(e, s);
+}
+
+// The two factors of the normal distribution's tail at |z|: q = exp(-z^2/2) R(|z|) =
+// Phi(-|z|), and the exponential itself.  R(x) = erfcx(x / sqrt 2) / 2 falls
+// smoothly from 1/2 as 1 / (x sqrt(2 pi)); it is a polynomial of degree 8 in
+// t = 1 / (1 + 0.3 x), fitted for the least relative error over 0 <= x <= 14.5 (5.8e-8;
+// with FP32 arithmetic 4.3e-7).  The exponent's roundings are carried along as in
+// sigmoid2.  Past |z| = 13.2 the exponential is below 2^-126 and the tail zero.
+__device__ __forceinline__ void normal_tail2(float2 z, float2& q, float2& ez) {
+    constexpr float kC = -0.72134752044448170f;  // -log2(e) / 2
+    constexpr float kCRest = static_cast<float>(-0.72134752044448170368 - kC);
+    const float2 x = make_float2(min_nan(fabsf(z.x), 14.5f), min_nan(fabsf(z.y), 14.5f));
+    const float2 a = __fmul2_rn(x, x), ra = __ffma2_rn(x, x, make_float2(-a.x, -a.y));
+    ez = __fmul2_rn(a, pair(kC));
+    float2 lo = __ffma2_rn(a, pair(kC), make_float2(-ez.x, -ez.y));
+    lo = __ffma2_rn(a, pair(kCRest), __ffma2_rn(ra, pair(kC), lo));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(ez.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(ez.y));
+    ez = __fmul2_rn(ez, __ffma2_rn(lo, pair(0.6931471805599453f), pair(1.f)));
+    float2 t = __ffma2_rn(x, pair(0.3f), pair(1.f));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t.y));
+    float2 r = pair(0.03840739652514458f);
+    r = __ffma2_rn(r, t, pair(-0.16930747032165527f));
+    r = __ffma2_rn(r, t, pair(0.22895179688930511f));
+    r = __ffma2_rn(r, t, pair(-0.07683967798948288f));
+    r = __ffma2_rn(r, t, pair(0.14276528358459473f));
+    r = __ffma2_rn(r, t, pair(0.0945858582854271f));
+    r = __ffma2_rn(r, t, pair(0.12194526195526123f));
+    r = __ffma2_rn(r, t, pair(0.11948420852422714f));
+    r = __ffma2_rn(r, t, pair(7.372390427917708e-06f));
+    q = __fmul2_rn(r, ez);
+}
+
+constexpr float kGeluTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+
+template <int ACT>
+__device__ __forceinline__ float2 act2(float2 z) {
+    if constexpr (ACT == kActRelu) return make_float2(max_nan(z.x, 0.f), max_nan(z.y, 0.f));
+    if constexpr (ACT == kActSilu) return __fmul2_rn(z, sigmoid2_any(z));
+    if constexpr (ACT == kActGeluTanh) {
+        const float2 z2 = __fmul2_rn(z, z);
+        const float2 c = __ffma2_rn(z2, pair(kGeluTanhC * 0.044715f), pair(kGeluTanhC));
+        return __fmul2_rn(z, sigmoid2_any(__fmul2_rn(z, c)));
+    }
+    if constexpr (ACT == kActGelu) {
+        float2 q, e;
+        normal_tail2(z, q, e);
+        return __fmul2_rn(z, make_float2(z.x > 0.f ? 1.f - q.x : q.x, z.y > 0.f ? 1.f - q.y : q.y));
+    }
+    return z;
+}
+
+// The activation's derivative.  Past |z| = 30 those of gelu_tanh and silu are 0 or 1
+// but for less than 2^-35; there the argument stays at 30 (silu: -87), which keeps
+// z^2 and z (1 - s) finite.
+template <int ACT>
+__device__ __forceinline__ float2 act_slope2(float2 z) {
+    if constexpr (ACT == kActRelu) return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
+    if constexpr (ACT == kActSilu) {
+        float2 s, c;
+        z = clamp2(z, -87.f, 88.f);
+        sigmoid_parts2(z, s, c);
+        return __fmul2_rn(s, __ffma2_rn(z, c, pair(1.f)));
+    }
+    if constexpr (ACT == kActGeluTanh) {
+        float2 s, c;
+        z = clamp2(z, -30.f, 30.f);
+        const float2 z2 = __fmul2_rn(z, z);
+        const float2 g = __fmul2_rn(z, __ffma2_rn(z2, pair(kGeluTanhC * 0.044715f), pair(kGeluTanhC)));
+        sigmoid_parts2(clamp2(g, -87.f, 88.f), s, c);
+        const float2 up = __ffma2_rn(z2, pair(kGeluTanhC * 3.f * 0.044715f), pair(kGeluTanhC));  // of the sigmoid's argument
+        return __fmul2_rn(s, __ffma2_rn(__fmul2_rn(z, up), c, pair(1.f)));
+    }
+    if constexpr (ACT == kActGelu) {
+        float2 q, e;
+        normal_tail2(z, q, e);
+        z = clamp2(z, -14.5f, 14.5f);  // the exponential is zero before
+        const float2 phi = make_float2(z.x > 0.f ? 1.f - q.x : q.x, z.y > 0.f ? 1.f - q.y : q.y);
+        return __ffma2_rn(z, __fmul2_rn(e, pair(0.3989422804014327f)), phi);
+    }
+    return pair(1.f);
+}
+
+}  // namespace dg

@@ -24,6 +24,9 @@
 #include "dg_ckpt.cuh"
 #include "dg_moe.cuh"
 #include "dg_route.cuh"
+#include "dg_act_bwd.cuh"
+#include "dg_balance.cuh"
+#include "dg_norm.cuh"
 #include "dg_kernel_ue8m0.cuh"
 
 namespace dg {
@@ -191,13 +194,13 @@ constexpr int smem_for() {
 // the DeepGEMM README page (section "非对齐的块大小"); here BN stays a
 // multiple of 64 so that the two promotion warpgroups split it into 32-column
 // TMEM loads.
-Choice choose(int m_blocks, int N, int num_sms, bool mn_major = false) {
+Choice choose(int m_blocks, int N, int num_sms, bool mn_major = false, int least_bn = 64) {
     // An MN-major B is loaded in 128-wide atoms: tiles of 128 or 256 only.
     const int cands[3] = {256, 128, 64};
     Choice best{128, max_stages<128>()};
     double best_cost = -1.0;
     for (int bn : cands) {
-        if (mn_major && bn % 128 != 0) continue;
+        if ((mn_major && bn % 128 != 0) || bn < least_bn) continue;
         const int tiles = m_blocks * cdiv(N, bn);
         const double t_kb = bn > 0.75 * (128 + bn) ? bn : 0.75 * (128 + bn);
         const double cost = static_cast<double>(waves_cost(tiles, num_sms)) * t_kb;
@@ -338,7 +341,7 @@ int small_stages(int tn) {
 }
 
 dg_status plan(int mode, int rows, int N, int K, int G, int num_sms, dg_plan* out, int expected_m = 0,
-               int layout = 0) {
+               int layout = 0, int least_bn = 64) {
     dg_status s = check_sizes(mode, rows, N, K, G);
     if (s != DG_OK) return s;
     if (num_sms <= 0) return fail(DG_ERR_INVALID_ARG, "num_sms must be positive");
@@ -370,7 +373,7 @@ dg_status plan(int mode, int rows, int N, int K, int G, int num_sms, dg_plan* ou
         return DG_OK;
     }
     const int m_blocks = (mode == 2) ? G * cdiv(rows, dg::kBM) : cdiv(rows, dg::kBM);
-    const Choice c = choose(m_blocks, N, num_sms, layout != 0);
+    const Choice c = choose(m_blocks, N, num_sms, layout != 0, least_bn);
     out->block_m = dg::kBM;
     out->block_n = c.bn;
     out->stages = c.stages;
@@ -432,12 +435,12 @@ void set_pdl(cudaLaunchAttribute& a) {
     a.val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
 }
 
-template <int BN, int STAGES, int MODE, int LAYOUT = 0, int SP = 1>
-dg_status launch_one(const dg::Params& p, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td,
+template <int BN, int STAGES, int MODE, int LAYOUT = 0, int SP = 1, typename PT = dg::Params>
+dg_status launch_one(const PT& p, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td,
                      int grid, cudaStream_t stream) {
     constexpr int smem = dg::smem_bytes<BN, STAGES, SP>();
     static_assert(smem <= 227 * 1024, "shared memory budget exceeded");
-    auto kern = dg::fp8_gemm_kernel<BN, STAGES, MODE, LAYOUT, SP>;
+    auto kern = dg::fp8_gemm_kernel<BN, STAGES, MODE, LAYOUT, SP, PT>;
     static std::atomic<int> attr_set[kMaxDevices];
     int dev = 0;
     cudaGetDevice(&dev);
@@ -475,11 +478,11 @@ dg_status launch_one(const dg::Params& p, const CUtensorMap& ta, const CUtensorM
     return ok();
 }
 
-template <int TN, int MODE>
-dg_status launch_small(const dg::Params& p, const CUtensorMap& ta, const CUtensorMap& tb, const dg_plan& pl,
+template <int TN, int MODE, typename PT>
+dg_status launch_small(const PT& p, const CUtensorMap& ta, const CUtensorMap& tb, const dg_plan& pl,
                        cudaStream_t stream) {
-    constexpr int smem = dg::small_smem_bytes<TN>();
-    auto kern = dg::fp8_gemm_swapab_kernel<TN, MODE>;
+    constexpr int smem = dg::small_smem_bytes<TN, !std::is_same<PT, dg::Params>::value>();
+    auto kern = dg::fp8_gemm_swapab_kernel<TN, MODE, PT>;
     static std::atomic<int> attr_set[kMaxDevices];
     int dev = 0;
     cudaGetDevice(&dev);
@@ -507,27 +510,27 @@ dg_status launch_small(const dg::Params& p, const CUtensorMap& ta, const CUtenso
     return ok();
 }
 
-template <int MODE>
-dg_status dispatch_small(const dg_plan& pl, const dg::Params& p, const CUtensorMap& ta, const CUtensorMap& tb,
+template <int MODE, typename PT>
+dg_status dispatch_small(const dg_plan& pl, const PT& p, const CUtensorMap& ta, const CUtensorMap& tb,
                          cudaStream_t stream) {
     switch (pl.block_m) {
-        case 32: return launch_small<32, MODE>(p, ta, tb, pl, stream);
-        case 64: return launch_small<64, MODE>(p, ta, tb, pl, stream);
-        case 128: return launch_small<128, MODE>(p, ta, tb, pl, stream);
+        case 32: return launch_small<32, MODE, PT>(p, ta, tb, pl, stream);
+        case 64: return launch_small<64, MODE, PT>(p, ta, tb, pl, stream);
+        case 128: return launch_small<128, MODE, PT>(p, ta, tb, pl, stream);
         default: return fail(DG_ERR_UNSUPPORTED, "no few-row kernel for block_m=%d", pl.block_m);
     }
 }
 
-template <int MODE>
-dg_status dispatch(const dg_plan& pl, const dg::Params& p, const CUtensorMap& ta, const CUtensorMap& tb,
+template <int MODE, typename PT>
+dg_status dispatch(const dg_plan& pl, const PT& p, const CUtensorMap& ta, const CUtensorMap& tb,
                    const CUtensorMap& td, cudaStream_t stream) {
     switch (pl.block_n) {
         case 256:
             if (MODE == dg::kDense && pl.stages == kShortKStages)
-                return launch_one<256, kShortKStages, MODE, 0, 4>(p, ta, tb, td, pl.grid, stream);
-            return launch_one<256, max_stages<256>(), MODE>(p, ta, tb, td, pl.grid, stream);
-        case 128: return launch_one<128, max_stages<128>(), MODE>(p, ta, tb, td, pl.grid, stream);
-        case 64: return launch_one<64, max_stages<64>(), MODE>(p, ta, tb, td, pl.grid, stream);
+                return launch_one<256, kShortKStages, MODE, 0, 4, PT>(p, ta, tb, td, pl.grid, stream);
+            return launch_one<256, max_stages<256>(), MODE, 0, 1, PT>(p, ta, tb, td, pl.grid, stream);
+        case 128: return launch_one<128, max_stages<128>(), MODE, 0, 1, PT>(p, ta, tb, td, pl.grid, stream);
+        case 64: return launch_one<64, max_stages<64>(), MODE, 0, 1, PT>(p, ta, tb, td, pl.grid, stream);
         default: return fail(DG_ERR_UNSUPPORTED, "no kernel for block_n=%d", pl.block_n);
     }
 }
@@ -980,6 +983,99 @@ dg_status launch_route_bwd(const dg::RouteBwdParams& p, bool wide, int64_t grid,
     if (per <= 16) return launch_route_bwd_one<L, 16>(p, wide, grid, st);
     return launch_route_bwd_one<L, 32>(p, wide, grid, st);
 }
+
+// Threads of a norm kernel: a row's runs of 8 columns, `ch` to a thread.
+int norm_threads(int N, int ch) { return cdiv(cdiv(N / 8, ch), 32) * 32; }
+
+dg_status check_norm(int T, int N, int dtype, float scale) {
+    if (T < 0 || N <= 0) return fail(DG_ERR_INVALID_ARG, "bad sizes T=%d N=%d", T, N);
+    if (N % 8 != 0) return fail(DG_ERR_UNSUPPORTED, "N=%d must be a multiple of 8", N);
+    if (N > dg::kNormMaxColumns) return fail(DG_ERR_UNSUPPORTED, "N=%d is more than %d", N, dg::kNormMaxColumns);
+    if (T > kMaxSlotCount) return fail(DG_ERR_UNSUPPORTED, "T=%d is too large", T);
+    if (dtype != DG_DTYPE_BF16 && dtype != DG_DTYPE_FP32) return fail(DG_ERR_INVALID_ARG, "bad x_dtype %d", dtype);
+    if (!std::isfinite(scale)) return fail(DG_ERR_INVALID_ARG, "scale must be finite");
+    return DG_OK;
+}
+
+dg_status launch_column_sum(float* out0, const float* in0, float* out1, const float* in1, int parts, int N, void* stream) {
+    dg::ColumnSumParams p{{out0, out1}, {in0, in1}, parts, N};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, 32)), out1 ? 2u : 1u, 1);
+    cfg.blockDim = dim3(dg::kColumnSumThreads, 1, 1);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    set_pdl(attr[0]);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, dg::column_sum_kernel, p);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(DG_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+// Sizes that the balance calls share.
+dg_status check_balance(int T, int E, int k, int S, int dtype, int score, float coef, const void* offsets) {
+    if (T < 0 || E <= 0 || k <= 0 || S <= 0) return fail(DG_ERR_INVALID_ARG, "bad sizes T=%d E=%d k=%d S=%d", T, E, k, S);
+    if (k > E) return fail(DG_ERR_INVALID_ARG, "k=%d is more than E=%d", k, E);
+    if (dtype != DG_DTYPE_BF16 && dtype != DG_DTYPE_FP32) return fail(DG_ERR_INVALID_ARG, "bad logits_dtype %d", dtype);
+    if (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID) return fail(DG_ERR_INVALID_ARG, "bad score %d", score);
+    if (!std::isfinite(coef)) return fail(DG_ERR_INVALID_ARG, "coef must be finite");
+    if (!offsets && S != 1) return fail(DG_ERR_INVALID_ARG, "S=%d sequences need seq_offsets", S);
+    if (E > dg::kRouteMaxExperts) return fail(DG_ERR_UNSUPPORTED, "E=%d is more than %d", E, dg::kRouteMaxExperts);
+    if (static_cast<int64_t>(T) * k > kMaxSlotCount) return fail(DG_ERR_UNSUPPORTED, "T*k=%lld is too large", static_cast<long long>(T) * k);
+    if (static_cast<int64_t>(S) * E > kMaxSlotCount) return fail(DG_ERR_UNSUPPORTED, "S*E=%lld is too large", static_cast<long long>(S) * E);
+    if (!aligned(offsets, 4)) return fail(DG_ERR_MISALIGNED, "seq_offsets must be aligned to its elements");
+    return DG_OK;
+}
+
+// Tokens of a balance chunk: at least one a warp, and few enough chunks that their
+// partial sums are a small part of the logits.  (Of the sizes alone: results do
+// not depend on the SM cap.)
+int balance_chunk(int T) {
+    const int c = cdiv(T, dg::kBalanceMaxChunks);
+    return c < dg::kBalanceWarps ? dg::kBalanceWarps : c;
+}
+int64_t balance_rows(int T, int S) { return cdiv64(T, balance_chunk(T)) + S; }
+
+template <typename L>
+dg_status launch_balance_sum(const dg::BalanceParams& p, void* st) {
+    const int per = cdiv(p.E, 32), threads = dg::kBalanceWarps * 32;
+    const int smem = (dg::kBalanceWarps + 1) * p.E * 4;
+    if (per <= 1) return launch_plain(dg::balance_sum_kernel<1, L>, p, p.chunks, threads, smem, 1, st);
+    if (per <= 2) return launch_plain(dg::balance_sum_kernel<2, L>, p, p.chunks, threads, smem, 1, st);
+    if (per <= 4) return launch_plain(dg::balance_sum_kernel<4, L>, p, p.chunks, threads, smem, 1, st);
+    if (per <= 8) return launch_plain(dg::balance_sum_kernel<8, L>, p, p.chunks, threads, smem, 1, st);
+    if (per <= 16) return launch_plain(dg::balance_sum_kernel<16, L>, p, p.chunks, threads, smem, 1, st);
+    return launch_plain(dg::balance_sum_kernel<32, L>, p, p.chunks, threads, smem, 1, st);
+}
+
+template <typename L>
+dg_status launch_balance_bwd(const dg::BalanceBwdParams& p, int64_t grid, void* st) {
+    const int per = cdiv(p.E, 32), threads = dg::kBalanceWarps * 32;
+    if (per <= 1) return launch_plain(dg::balance_bwd_kernel<1, L>, p, grid, threads, 0, 1, st);
+    if (per <= 2) return launch_plain(dg::balance_bwd_kernel<2, L>, p, grid, threads, 0, 1, st);
+    if (per <= 4) return launch_plain(dg::balance_bwd_kernel<4, L>, p, grid, threads, 0, 1, st);
+    if (per <= 8) return launch_plain(dg::balance_bwd_kernel<8, L>, p, grid, threads, 0, 1, st);
+    if (per <= 16) return launch_plain(dg::balance_bwd_kernel<16, L>, p, grid, threads, 0, 1, st);
+    return launch_plain(dg::balance_bwd_kernel<32, L>, p, grid, threads, 0, 1, st);
+}
+
+template <typename XT>
+dg_status launch_norm(const dg::NormParams& p, int64_t grid, void* st) {
+    const int ch = p.N / 8 <= dg::kNormMaxThreads ? 1 : 2;
+    const int threads = norm_threads(p.N, ch);
+    if (ch == 1) return launch_plain(dg::norm_residual_kernel<XT, 1>, p, grid, threads, 0, 1, st);
+    return launch_plain(dg::norm_residual_kernel<XT, 2>, p, grid, threads, 0, 1, st);
+}
+template <typename XT>
+dg_status launch_norm_bwd(const dg::NormBwdParams& p, int64_t grid, void* st) {
+    const int ch = p.N / 8 <= dg::kNormMaxThreads ? 1 : 2;
+    const int threads = norm_threads(p.N, ch);
+    if (ch == 1) return launch_plain(dg::norm_residual_bwd_kernel<XT, 1>, p, grid, threads, 0, 1, st);
+    return launch_plain(dg::norm_residual_bwd_kernel<XT, 2>, p, grid, threads, 0, 1, st);
+}
+
+bool bad_act(int act) { return act < 0 || act >= dg::kActCount; }
 
 }  // namespace
 
@@ -1558,6 +1654,206 @@ dg_status dg_fp8_1x128_to_128x128(uint8_t* Qb, float* sb, const uint8_t* Q, cons
     dg::RecastParams p{Qb, sb, Q, sa, m_indices, sa_stride, K, K / dg::kBK, rows};
     return launch_plain(dg::recast_128x128_kernel, p, static_cast<int64_t>(rows / 128) * p.nkb, dg::kRecastThreads, 0, 1,
                         stream);
+}
+
+dg_status dg_fp8_gemm_nt_epilogue(uint16_t* D, uint16_t* Z, uint8_t* Q, float* sq, int sq_stride, const uint8_t* A,
+                                  const float* sa, int sa_stride, const uint8_t* B, const float* sb, const float* bias,
+                                  int act, const uint16_t* residual, int M, int N, int K, void* stream) {
+    dg_status s = check_sizes(0, M, N, K, 1);
+    if (s != DG_OK) return s;
+    if (bad_act(act)) return fail(DG_ERR_INVALID_ARG, "bad act %d", act);
+    if (M == 0) return ok();
+    if (!D && !Z && !Q) return fail(DG_ERR_INVALID_ARG, "D, Z and Q are all null");
+    if ((s = common_checks(D ? D : Z ? Z : static_cast<const void*>(Q), A, sa, sa_stride, B, sb, M)) != DG_OK) return s;
+    if (!aligned16(Z) || !aligned16(Q) || !aligned16(bias) || !aligned16(residual))
+        return fail(DG_ERR_MISALIGNED, "Z, Q, bias and residual must be 16-byte aligned");
+    if (Z && (Z == D || Z == residual)) return fail(DG_ERR_INVALID_ARG, "Z is another tensor than D and the residual");
+    if (Q) {
+        if (N % 128 != 0) return fail(DG_ERR_UNSUPPORTED, "Q needs N=%d to be a multiple of 128", N);
+        if (!sq) return fail(DG_ERR_INVALID_ARG, "Q without sq");
+        if (!aligned(sq, 4)) return fail(DG_ERR_MISALIGNED, "sq must be 4-byte aligned");
+        if (sq_stride < M) return fail(DG_ERR_INVALID_ARG, "sq_stride=%d must be >= M=%d", sq_stride, M);
+    }
+    const int sms = effective_sms();
+    if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
+    dg_plan pl;
+    if ((s = plan(0, M, N, K, 1, sms, &pl, 0, 0, Q ? 256 : 64)) != DG_OK) return s;
+    dg::EpiParams p{};
+    static_cast<dg::Params&>(p) = make_params(D, sa, sa_stride, sb, M, N, K, 1, pl);
+    p.Z = Z;
+    p.Q = Q;
+    p.sq = sq;
+    p.bias = bias;
+    p.residual = residual;
+    p.sq_stride = sq_stride;
+    p.act = act;
+    p.b_stream = pl.m_blocks == 1;
+    CUtensorMap ta, tb, td{};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pl.swap_ab) {
+        if ((s = make_operand_map(&ta, A, K, M, 1, pl.block_m, false)) != DG_OK) return s;
+        if ((s = make_operand_map(&tb, B, K, N, 1, 128, true)) != DG_OK) return s;
+        return dispatch_small<dg::kDense>(pl, p, ta, tb, st);
+    }
+    if ((s = make_operand_map(&ta, A, K, M, 1, dg::kBM, false)) != DG_OK) return s;
+    if ((s = make_operand_map(&tb, B, K, N, 1, pl.block_n, true)) != DG_OK) return s;
+    if (D && (s = make_output_map(&td, D, N, M, 1, false)) != DG_OK) return s;
+    if (Z && (s = make_output_map(&p.tmZ, Z, N, M, 1, false)) != DG_OK) return s;
+    TailWorkspace ws;
+    if (pl.tail_split > 1 && tail_workspace(st, &ws)) {
+        p.tail_split = pl.tail_split;
+        p.full_tiles = (pl.tiles / pl.grid) * pl.grid;
+        p.ws = ws.partials;
+        p.ws_flags = ws.flags;
+    }
+    return dispatch<dg::kDense>(pl, p, ta, tb, td, st);
+}
+
+int dg_get_bias_workspace(int M, int N) {
+    if (M < 0 || N <= 0) return -1;
+    const int64_t n = cdiv64(M, 128) * N;
+    return n <= 0x7FFFFFFF ? static_cast<int>(n) : -1;
+}
+
+dg_status dg_epilogue_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, float* sc, int sc_stride, float* dbias,
+                          float* ws, const uint16_t* dD, const uint16_t* Z, int act, int M, int N, void* stream) {
+    if (M < 0 || N <= 0) return fail(DG_ERR_INVALID_ARG, "bad sizes M=%d N=%d", M, N);
+    if (bad_act(act)) return fail(DG_ERR_INVALID_ARG, "bad act %d", act);
+    if (N % 128 != 0) return fail(DG_ERR_UNSUPPORTED, "N=%d must be a multiple of 128", N);
+    if (N > kMaxColumns) return fail(DG_ERR_UNSUPPORTED, "N=%d is too large", N);
+    if (M > kMaxSlotCount) return fail(DG_ERR_UNSUPPORTED, "M=%d is too large", M);
+    if (sr_stride < M) return fail(DG_ERR_INVALID_ARG, "sr_stride=%d must be >= M=%d", sr_stride, M);
+    if (sc_stride < N) return fail(DG_ERR_INVALID_ARG, "sc_stride=%d must be >= N=%d", sc_stride, N);
+    if (M > 0 && dbias && !ws) return fail(DG_ERR_INVALID_ARG, "dbias needs ws");
+    if (!aligned(dbias, 4) || !aligned(ws, 4)) return fail(DG_ERR_MISALIGNED, "dbias and ws must be 4-byte aligned");
+    if (dbias && dg_get_bias_workspace(M, N) < 0) return fail(DG_ERR_UNSUPPORTED, "M=%d N=%d: the workspace is too large", M, N);
+    if (M == 0) {
+        if (!dbias) return ok();
+        return launch_column_sum(dbias, ws, nullptr, nullptr, 0, N, stream);  // zeros
+    }
+    if (!Qr || !sr || !Qc || !sc || !dD || (act != DG_ACT_NONE && !Z)) return fail(DG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(Qr) || !aligned16(Qc) || !aligned16(dD) || !aligned16(Z) || !aligned(sr, 4) || !aligned(sc, 4))
+        return fail(DG_ERR_MISALIGNED, "Qr, Qc, dD and Z must be 16-byte aligned, the others 4-byte aligned");
+    const int64_t rb = cdiv64(M, 128);
+    dg::ActBwdParams p{{Qr, sr, Qc, sc, sr_stride, sc_stride}, dbias ? ws : nullptr, dD, Z, M, N, N / 128};
+    const int64_t grid = rb * p.nb;
+    void (*kern)(dg::ActBwdParams) = act == DG_ACT_RELU        ? dg::act_bwd_kernel<dg::kActRelu>
+                                     : act == DG_ACT_GELU      ? dg::act_bwd_kernel<dg::kActGelu>
+                                     : act == DG_ACT_GELU_TANH ? dg::act_bwd_kernel<dg::kActGeluTanh>
+                                     : act == DG_ACT_SILU      ? dg::act_bwd_kernel<dg::kActSilu>
+                                                               : dg::act_bwd_kernel<dg::kActNone>;
+    dg_status s = launch_plain(kern, p, grid, dg::kActBwdThreads, 0, 1, stream);
+    if (s != DG_OK || !dbias) return s;
+    return launch_column_sum(dbias, ws, nullptr, nullptr, static_cast<int>(rb), N, stream);
+}
+
+dg_status dg_norm_residual(void* U, uint16_t* H, uint8_t* Q, float* sq, int sq_stride, float* rstd, const void* X,
+                           int x_dtype, const uint16_t* Y, const float* w_post, const float* gate, const float* w_pre,
+                           int T, int N, int post_norm, float scale, float eps, void* stream) {
+    dg_status s = check_norm(T, N, x_dtype, scale);
+    if (s != DG_OK) return s;
+    if (!(eps > 0.f) || !std::isfinite(eps)) return fail(DG_ERR_INVALID_ARG, "eps must be positive and finite");
+    if (T == 0) return ok();
+    if (!U && !H && !Q && !rstd) return fail(DG_ERR_INVALID_ARG, "U, H, Q and rstd are all null");
+    if (Q) {
+        if (N % 128 != 0) return fail(DG_ERR_UNSUPPORTED, "Q needs N=%d to be a multiple of 128", N);
+        if (!sq) return fail(DG_ERR_INVALID_ARG, "Q without sq");
+        if (sq_stride < T) return fail(DG_ERR_INVALID_ARG, "sq_stride=%d must be >= T=%d", sq_stride, T);
+    }
+    if (!X && !Y) return fail(DG_ERR_INVALID_ARG, "X and Y are both null");
+    if (!aligned16(U) || !aligned16(H) || !aligned16(Q) || !aligned16(X) || !aligned16(Y) || !aligned16(w_post) ||
+        !aligned16(w_pre) || !aligned(rstd, 8) || !aligned(sq, 4) || !aligned(gate, 4))
+        return fail(DG_ERR_MISALIGNED, "tensors must be 16-byte aligned (rstd 8, sq and gate 4)");
+    const int sms = effective_sms();
+    if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
+    dg::NormParams p{U, H, Q, sq, rstd, X, Y, w_post, gate, w_pre, sq_stride, T, N, post_norm != 0, scale, eps};
+    const int64_t cap = static_cast<int64_t>(sms) * 4, grid = T < cap ? T : cap;
+    return x_dtype == DG_DTYPE_BF16 ? launch_norm<uint16_t>(p, grid, stream) : launch_norm<float>(p, grid, stream);
+}
+
+int dg_get_norm_workspace(int T, int N) {
+    if (T < 0 || N <= 0 || N > dg::kNormMaxColumns) return -1;
+    return 2 * N * (T < dg::kNormMaxParts ? T : dg::kNormMaxParts);
+}
+
+dg_status dg_norm_residual_bwd(void* dX, uint16_t* dY, float* dgate, float* dw_post, float* dw_pre, float* ws,
+                               const void* dU, const uint16_t* dH, const void* U, int x_dtype, const uint16_t* Y,
+                               const float* rstd, const float* w_post, const float* gate, const float* w_pre, int T, int N,
+                               int post_norm, float scale, void* stream) {
+    dg_status s = check_norm(T, N, x_dtype, scale);
+    if (s != DG_OK) return s;
+    if (T > 0 && !dX && !dY && !dgate && !dw_post && !dw_pre) return fail(DG_ERR_INVALID_ARG, "every output is null");
+    if (T > 0 && !Y && (dY || dgate || dw_post)) return fail(DG_ERR_INVALID_ARG, "dY, dgate and dw_post need Y");
+    if (T > 0 && (dw_post || dw_pre) && !ws) return fail(DG_ERR_INVALID_ARG, "dw_post and dw_pre need ws");
+    if (!aligned16(dX) || !aligned16(dY) || !aligned16(ws) || !aligned16(dU) || !aligned16(dH) || !aligned16(U) ||
+        !aligned16(Y) || !aligned16(w_post) || !aligned16(w_pre) || !aligned(rstd, 8) || !aligned(gate, 4) ||
+        !aligned(dgate, 4) || !aligned(dw_post, 4) || !aligned(dw_pre, 4))
+        return fail(DG_ERR_MISALIGNED, "tensors must be 16-byte aligned (rstd 8; dgate, dw_post, dw_pre and gate 4)");
+    const int sms = effective_sms();
+    int64_t grid = 0;
+    if (T > 0) {
+        if (!dU && !dH) return fail(DG_ERR_INVALID_ARG, "dU and dH are both null");
+        if (!U || !rstd) return fail(DG_ERR_INVALID_ARG, "null pointer");
+        if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
+        grid = sms < dg::kNormMaxParts ? sms : dg::kNormMaxParts;
+        if (grid > T) grid = T;
+        float* pre = ws && dw_post ? ws + grid * N : ws;
+        dg::NormBwdParams p{dX, dY, dgate, dw_post ? ws : nullptr, dw_pre ? pre : nullptr, dU, dH, U, Y, rstd, w_post, gate,
+                            w_pre, T, N, post_norm != 0, scale};
+        s = x_dtype == DG_DTYPE_BF16 ? launch_norm_bwd<uint16_t>(p, grid, stream) : launch_norm_bwd<float>(p, grid, stream);
+        if (s != DG_OK) return s;
+    }
+    if (!dw_post && !dw_pre) return ok();
+    if (!dw_post) return launch_column_sum(dw_pre, ws, nullptr, nullptr, static_cast<int>(grid), N, stream);
+    return launch_column_sum(dw_post, ws, dw_pre, ws + grid * N, static_cast<int>(grid), N, stream);
+}
+
+int dg_get_balance_workspace(int T, int E, int S) {
+    if (T < 0 || E <= 0 || E > dg::kRouteMaxExperts || S <= 0) return -1;
+    const int64_t n = 2 * balance_rows(T, S) * E;
+    return n <= 0x7FFFFFFF ? static_cast<int>(n) : -1;
+}
+
+dg_status dg_balance_loss(float* loss, int32_t* counts, float* probs, float* ws, const void* logits, int logits_dtype,
+                          const int32_t* topk_idx, const int32_t* seq_offsets, int T, int E, int k, int S, int score,
+                          float coef, void* stream) {
+    dg_status s = check_balance(T, E, k, S, logits_dtype, score, coef, seq_offsets);
+    if (s != DG_OK) return s;
+    if (dg_get_balance_workspace(T, E, S) < 0) return fail(DG_ERR_UNSUPPORTED, "T=%d E=%d S=%d: the workspace is too large", T, E, S);
+    if (!loss || !counts || (T > 0 && (!logits || !topk_idx || !ws))) return fail(DG_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(probs, 4) || !aligned(ws, 4) || !aligned(topk_idx, 4) ||
+        !aligned(logits, logits_dtype == DG_DTYPE_BF16 ? 2 : 4))
+        return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements");
+    const int chunk = balance_chunk(T), chunks = static_cast<int>(cdiv64(T, chunk));
+    int32_t* part_n = reinterpret_cast<int32_t*>(ws + balance_rows(T, S) * E);
+    dg::BalanceParams p{loss, counts, probs, ws, part_n, logits, topk_idx, seq_offsets, T, E, k, S, chunk, chunks,
+                        score == DG_SCORE_SOFTMAX, coef};
+    if (T > 0) {
+        s = logits_dtype == DG_DTYPE_BF16 ? launch_balance_sum<uint16_t>(p, stream) : launch_balance_sum<float>(p, stream);
+        if (s != DG_OK) return s;
+    }
+    return launch_plain(dg::balance_finish_kernel, p, dg::kBalanceFinishCtas, dg::kBalanceFinishThreads, 0,
+                        dg::kBalanceFinishCtas, stream);
+}
+
+dg_status dg_balance_loss_bwd(void* dlogits, const void* add, const float* dloss, const void* logits, int logits_dtype,
+                              const int32_t* counts, const int32_t* seq_offsets, int T, int E, int k, int S, int score,
+                              float coef, void* stream) {
+    dg_status s = check_balance(T, E, k, S, logits_dtype, score, coef, seq_offsets);
+    if (s != DG_OK) return s;
+    if (T == 0) return ok();
+    if (!dlogits || !logits || !counts) return fail(DG_ERR_INVALID_ARG, "null pointer");
+    const unsigned el = logits_dtype == DG_DTYPE_BF16 ? 2 : 4;
+    if (!aligned(dlogits, el) || !aligned(add, el) || !aligned(logits, el) || !aligned(counts, 4) || !aligned(dloss, 4))
+        return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements");
+    const int sms = effective_sms();
+    if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
+    dg::BalanceBwdParams p{dlogits, add, dloss, logits, counts, seq_offsets, T, E, S, score == DG_SCORE_SOFTMAX,
+                           static_cast<float>(static_cast<double>(coef) * E / k)};
+    const int64_t all = cdiv64(T, dg::kBalanceWarps), cap = static_cast<int64_t>(sms) * 4;
+    const int64_t grid = all < cap ? all : cap;
+    return logits_dtype == DG_DTYPE_BF16 ? launch_balance_bwd<uint16_t>(p, grid, stream)
+                                         : launch_balance_bwd<float>(p, grid, stream);
 }
 
 void dg_set_pdl(int enable) { g_pdl.store(enable < 0 ? -1 : (enable ? 1 : 0)); }

@@ -1,0 +1,329 @@
+// dg_balance.cuh -- sm_100a kernels of a router's balance loss, per-expert counts
+// and the loss's gradient.  Times are of one B200 in graph replays over inputs
+// larger than L2.
+//
+// For each sequence s of L_s tokens, L in all of them:
+//   n_e = slots that chose expert e        p_t = softmax(l_t), or sigmoids over their sum
+//   loss = coef sum_s L_s / L sum_e f_e P_e,  f_e = E n_e / (k L_s),  P_e = mean_t p_te
+//   dl_tj = coef / L p_tj (f_j - sum_e f_e p_te)     (sigmoid: times 1 - s_tj)
+#pragma once
+
+#include <stdint.h>
+
+#include "dg_ptx.cuh"
+#include "dg_route.cuh"
+
+namespace dg {
+
+constexpr int kBalanceWarps = 8;
+constexpr int kBalanceMaxChunks = 296;
+
+// Tokens [0, T) in chunks, one a CTA.  The part of sequence s inside chunk c has
+// row c + s of the partial sums: going along the tokens c and s never fall and one
+// of them rises from part to part, so no two parts share a row.
+struct BalanceParams {
+    float* loss;             // [1]
+    int32_t* counts;         // [S][E]
+    float* probs;            // [S][E] or null
+    float* part_p;           // [chunks + S][E]
+    int32_t* part_n;         // [chunks + S][E]
+    const void* logits;      // [T][E]
+    const int32_t* topk_idx; // [T][k]
+    const int32_t* offsets;  // [S + 1] or null: one sequence of all tokens
+    int T, E, k, S;
+    int chunk, chunks;
+    int softmax;
+    float coef;
+};
+
+// Offsets count as if kept within [0, T]; whether they were is checked once, by
+// balance_finish_kernel.
+__device__ __forceinline__ int seq_offset(const int32_t* offsets, int s, int T) {
+    if (offsets == nullptr) return s == 0 ? 0 : T;
+    return min(max(offsets[s], 0), T);
+}
+// The sequence that holds token t: the last with offset <= t (S: behind the last; -1: before the first).
+__device__ __forceinline__ int seq_of(const int32_t* offsets, int S, int T, int t) {
+    if (offsets == nullptr) return 0;
+    int lo = -1, hi = S;  // offset[lo] <= t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (seq_offset(offsets, mid, T) <= t) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// p of one token's E logits, lane's experts lane + 32 i; `slope`: 1 - s of a sigmoid,
+// 1 of the softmax.  A token without a finite logit has p = 0.
+template <int EPL>
+__device__ __forceinline__ void balance_probs(float (&l)[EPL], int softmax, float (&p)[EPL], float (&slope)[EPL]) {
+    float sum = 0.f;
+    if (softmax) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) m = fmaxf(m, l[i]);
+        m = warp_max(m);
+        const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            p[i] = l[i] - from;
+            slope[i] = 1.f;
+        }
+        exp_results<EPL>(p);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) sum += p[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            // s = 1 / (1 + e), 1 - s = e / (1 + e), e = exp(-l); in terms of exp(-|l|) both are sums of positives
+            float e[1] = {-fabsf(l[i])};
+            exp_results<1>(e);
+            const float r = __frcp_rn(1.f + e[0]);
+            const float big = r, small = e[0] * r;
+            const bool up = l[i] > 0.f;
+            p[i] = up ? big : small;
+            slope[i] = up ? small : big;
+            sum += p[i];
+        }
+    }
+    sum = warp_sum(sum);
+    const float inv = sum > 0.f || sum != sum ? __frcp_rn(sum) : 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) p[i] *= inv;
+}
+
+template <int EPL, typename L>
+__global__ void __launch_bounds__(kBalanceWarps * 32)
+balance_sum_kernel(const BalanceParams p) {
+    extern __shared__ float balance_smem[];  // [warps][E] sums, then [E] counts
+    int32_t* hist = reinterpret_cast<int32_t*>(balance_smem + kBalanceWarps * p.E);
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c = blockIdx.x, t0 = c * p.chunk, t1 = min(t0 + p.chunk, p.T);
+    const L* logits = static_cast<const L*>(p.logits);
+    for (int s = max(seq_of(p.offsets, p.S, p.T, t0), 0); s < p.S; ++s) {
+        const int first = seq_offset(p.offsets, s, p.T);
+        if (first >= t1) break;
+        const int a = max(first, t0), b = min(seq_offset(p.offsets, s + 1, p.T), t1);
+        if (a >= b) continue;
+        for (int e = tid; e < p.E; e += kBalanceWarps * 32) hist[e] = 0;
+        __syncthreads();
+        const int64_t s1 = static_cast<int64_t>(b) * p.k;
+        for (int64_t i = static_cast<int64_t>(a) * p.k + tid; i < s1; i += kBalanceWarps * 32) {
+            const int e = p.topk_idx[i];
+            if (e >= 0 && e < p.E) atomicAdd(hist + e, 1);
+        }
+        float acc[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
+        for (int t = a + warp; t < b; t += kBalanceWarps) {
+            const L* row = logits + static_cast<int64_t>(t) * p.E;
+            float l[EPL], q[EPL], slope[EPL];
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int e = lane + 32 * i;
+                l[i] = e < p.E ? logit_at(row + e) : -INFINITY;
+            }
+            balance_probs<EPL>(l, p.softmax, q, slope);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) acc[i] += q[i];
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (lane + 32 * i < p.E) balance_smem[warp * p.E + lane + 32 * i] = acc[i];
+        __syncthreads();
+        const int64_t at = static_cast<int64_t>(c + s) * p.E;
+        for (int e = tid; e < p.E; e += kBalanceWarps * 32) {
+            float v = balance_smem[e];
+#pragma unroll
+            for (int w = 1; w < kBalanceWarps; ++w) v += balance_smem[w * p.E + e];
+            p.part_p[at + e] = v;
+            p.part_n[at + e] = hist[e];
+        }
+        __syncthreads();
+    }
+}
+
+constexpr int kBalanceFinishThreads = 1024;
+constexpr int kBalanceFinishCtas = 8;
+
+// One cluster joins the parts of each (sequence, expert), in chunk order, and the
+// loss.  CTA r takes a run of the S E sums; if those are fewer than its threads, as
+// many threads share a sum, each with a run of its parts.
+__global__ void __launch_bounds__(kBalanceFinishThreads)
+balance_finish_kernel(const BalanceParams p) {
+    __shared__ float sp[kBalanceFinishThreads];
+    __shared__ int32_t sn[kBalanceFinishThreads];
+    __shared__ double share[kBalanceFinishThreads / 32];
+    __shared__ double mine;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x;
+    const uint32_t rank = cluster_ctarank(), nctas = cluster_nctarank();
+    if (p.offsets != nullptr) {
+        bool bad = false;
+        for (int s = rank * kBalanceFinishThreads + tid; s <= p.S; s += nctas * kBalanceFinishThreads) {
+            const int o = p.offsets[s];
+            bad |= o < 0 || o > p.T || (s < p.S && p.offsets[s + 1] < o);
+        }
+        if (bad) atomicOr(&g_dg_error, 64u);
+    }
+    const int64_t sums = static_cast<int64_t>(p.S) * p.E;
+    const int64_t i0 = sums * rank / nctas, i1 = sums * (rank + 1) / nctas;
+    const int n = static_cast<int>(min(i1 - i0, static_cast<int64_t>(kBalanceFinishThreads)));
+    const int split = n > 0 ? kBalanceFinishThreads / n : 1;  // threads to a sum
+    const int width = n > 0 ? n : 1, part = tid / width;
+    const double len = static_cast<double>(seq_offset(p.offsets, p.S, p.T)) - seq_offset(p.offsets, 0, p.T);
+    double loss = 0.0;
+    for (int64_t base = i0; base < i1; base += width) {
+        const int64_t i = base + tid % width;
+        const bool there = i < i1 && part < split;
+        float sum = 0.f;
+        int32_t count = 0;
+        int s = 0, e = 0, a = 0, b = 0;
+        if (there) {
+            s = static_cast<int>(i / p.E);
+            e = static_cast<int>(i - static_cast<int64_t>(s) * p.E);
+            a = seq_offset(p.offsets, s, p.T);
+            b = seq_offset(p.offsets, s + 1, p.T);
+            if (a < b) {
+                const int c0 = a / p.chunk, c1 = (b - 1) / p.chunk + 1, cs = c1 - c0;
+                const int from = c0 + static_cast<int>(static_cast<int64_t>(cs) * part / split);
+                const int to = c0 + static_cast<int>(static_cast<int64_t>(cs) * (part + 1) / split);
+#pragma unroll 4
+                for (int c = from; c < to; ++c) {
+                    const int64_t at = static_cast<int64_t>(c + s) * p.E + e;
+                    sum += p.part_p[at];
+                    count += p.part_n[at];
+                }
+            }
+        }
+        if (split > 1) {
+            sp[tid] = sum;
+            sn[tid] = count;
+            __syncthreads();
+            if (there && part == 0)
+                for (int j = 1; j < split; ++j) {
+                    sum += sp[tid + j * width];
+                    count += sn[tid + j * width];
+                }
+            __syncthreads();
+        }
+        if (there && part == 0) {
+            const int l = b > a ? b - a : 1;
+            p.counts[i] = count;
+            if (p.probs != nullptr) p.probs[i] = sum / static_cast<float>(l);
+            loss += static_cast<double>(sum) * count / l;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+    if ((tid & 31) == 0) share[tid >> 5] = loss;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < kBalanceFinishThreads / 32; ++w) loss += share[w];
+        mine = loss;
+    }
+    __syncwarp();
+    cluster_sync();
+    if (rank == 0 && tid == 0) {
+        double all = 0.0;
+        for (uint32_t r = 0; r < nctas; ++r) {
+            double x;
+            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(x) : "r"(dsmem_addr(smem_u32(&mine), r)) : "memory");
+            all += x;
+        }
+        *p.loss = len > 0.0 ? static_cast<float>(all * p.coef * p.E / (static_cast<double>(p.k) * len)) : 0.f;
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while its sum is being read
+}
+
+struct BalanceBwdParams {
+    void* dlogits;           // [T][E]
+    const void* add;         // [T][E] or null
+    const float* dloss;      // [1] or null: 1
+    const void* logits;      // [T][E]
+    const int32_t* counts;   // [S][E]
+    const int32_t* offsets;
+    int T, E, S;
+    int softmax;
+    float scale;             // coef E / k
+};
+
+// A warp takes runs of neighbouring tokens.  f_j - sum f_e p_e is formed from the
+// counts' distances to that of the token's likeliest expert c, whole numbers:
+// (n_j - n_c) - sum_e p_e (n_e - n_c) has no large terms that cancel where one expert has
+// nearly all the weight, or where all loads are nearly alike.
+template <int EPL, typename L>
+__global__ void __launch_bounds__(kBalanceWarps * 32)
+balance_bwd_kernel(const BalanceBwdParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kBalanceWarps;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kBalanceWarps + (threadIdx.x >> 5);
+    const int t0 = static_cast<int>(p.T * w / warps), t1 = static_cast<int>(p.T * (w + 1) / warps);
+    const int len = seq_offset(p.offsets, p.S, p.T) - seq_offset(p.offsets, 0, p.T);
+    const float up = p.dloss != nullptr ? *p.dloss : 1.f;
+    const L* logits = static_cast<const L*>(p.logits);
+    int32_t n[EPL];
+    int end = t0, s = 0;  // the sequence s holds tokens up to `end`
+    float k = 0.f;
+    for (int t = t0; t < t1; ++t) {
+        if (t >= end) {
+            s = seq_of(p.offsets, p.S, p.T, t);
+            const bool in = s >= 0 && s < p.S;
+            const int first = in ? seq_offset(p.offsets, s, p.T) : 0;
+            end = in ? seq_offset(p.offsets, s + 1, p.T) : s < 0 ? seq_offset(p.offsets, 0, p.T) : p.T;
+            if (end <= t) end = t + 1;  // offsets that fall
+            k = in && len > 0 && end > first ? p.scale * up / (static_cast<float>(len) * static_cast<float>(end - first)) : 0.f;
+            if (!in) s = -1;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int e = lane + 32 * i;
+                n[i] = s >= 0 && e < p.E ? p.counts[static_cast<int64_t>(s) * p.E + e] : 0;
+            }
+        }
+        const int64_t at = static_cast<int64_t>(t) * p.E;
+        float l[EPL], d[EPL], q[EPL], slope[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = lane + 32 * i;
+            d[i] = p.add != nullptr && e < p.E ? logit_at(static_cast<const L*>(p.add) + at + e) : 0.f;
+        }
+        if (s >= 0) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int e = lane + 32 * i;
+                l[i] = e < p.E ? logit_at(logits + at + e) : -INFINITY;
+            }
+            balance_probs<EPL>(l, p.softmax, q, slope);
+            float best = -1.f;
+            int nc = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (q[i] > best) {
+                    best = q[i];
+                    nc = n[i];
+                }
+            const float top = warp_max(best);
+            const uint32_t who = __ballot_sync(0xffffffffu, best == top);
+            nc = __shfl_sync(0xffffffffu, nc, who ? __ffs(who) - 1 : 0);
+            float mean = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) mean = fmaf(q[i], static_cast<float>(n[i] - nc), mean);
+            mean = warp_sum(mean);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                d[i] = fmaf(k * q[i] * slope[i], static_cast<float>(n[i] - nc) - mean, d[i]);
+        }
+        L* out = static_cast<L*>(p.dlogits) + at;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (lane + 32 * i < p.E) store_logit(out + lane + 32 * i, d[i]);
+    }
+}
+
+}  // namespace dg

@@ -11,6 +11,7 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include "dg_act.cuh"
 #include "dg_cast.cuh"
 #include "dg_moe.cuh"
 #include "dg_ptx.cuh"
@@ -26,27 +27,6 @@ __device__ __forceinline__ void e4m3x8_to_f8(const uint2& c, F8& f) {
     f[1] = __half22float2(e4m3x2_to_half2(c.x >> 16));
     f[2] = __half22float2(e4m3x2_to_half2(c.y));
     f[3] = __half22float2(e4m3x2_to_half2(c.y >> 16));
-}
-__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
-
-// s = 1 / (1 + exp(-g)) of a pair.  exp(-g) = 2^t 2^lo: t is -g log2(e) as rounded,
-// lo what the product and the constant's rounding leave of it (a first-order
-// factor is good to 2^-40), so the error does not grow with |g| (it was 64 times
-// 2^-24 at -80, and now is at most 8: the unit's 2^power, two roundings, 1 + e,
-// the unit's reciprocal).  88 keeps an infinite gate's product finite.
-__device__ __forceinline__ float2 sigmoid2(float2 g) {
-    constexpr float kLog2e = 1.4426950408889634f, kRest = static_cast<float>(1.4426950408889634074 - kLog2e);
-    g.x = fminf(g.x, 88.f);
-    g.y = fminf(g.y, 88.f);
-    float2 e = __fmul2_rn(g, pair(-kLog2e));
-    float2 lo = __ffma2_rn(g, pair(-kRest), __ffma2_rn(g, pair(-kLog2e), make_float2(-e.x, -e.y)));
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-    e = __fmul2_rn(e, __ffma2_rn(lo, pair(0.6931471805599453f), pair(1.f)));
-    e = __fadd2_rn(e, pair(1.f));
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-    return e;
 }
 
 // -------------------------------------------------------------- forward ----

@@ -30,6 +30,10 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "dg_act.cuh"
+#include "dg_moe.cuh"
 #include "dg_ptx.cuh"
 
 namespace dg {
@@ -75,6 +79,19 @@ struct Params {
     int tail_split;
     float* ws;            // FP32 partials of slices 1..tail_split-1
     unsigned int* ws_flags;  // one ready flag per partial
+};
+
+// Epilogue of dense calls with bias, activation and residual: z = acc + bias, v =
+// act(z) + residual; z and v are stored as bf16, v as e4m3 with a scale per 1x128.
+struct EpiParams : Params {
+    CUtensorMap tmZ;           // of Z, like tmD
+    uint16_t* Z;               // [M][N] or null; D may be null too
+    uint8_t* Q;                // [M][N] or null
+    float* sq;                 // sq[(n/128)*sq_stride + m]
+    const float* bias;         // [N] or null
+    const uint16_t* residual;  // [M][N] or null
+    int64_t sq_stride;
+    int act;
 };
 
 // One unit of work of this CTA: a tile (index t) over K blocks [kb0, kb1);
@@ -219,6 +236,99 @@ __device__ __forceinline__ void group_k_range(const Params& p, const Tile& tl, W
     w.kb1 = k1 / kBK;
 }
 
+// One promotion warp's share of a tile, staged 32 x 32 values at a time in `piece`
+// as bf16 (64-byte swizzle, as in the kernel's own epilogue) and stored by TMA.
+__device__ __forceinline__ void stage_piece(const CUtensorMap* tm, uint8_t* piece, const float2* v, int x, int y, int N, int lane) {
+    if (lane == 0) bulk_wait_read<0>();  // the previous store has read the buffer
+    __syncwarp();
+    const uint32_t stg = smem_u32(piece);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        st_shared_v4(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), pack_bf16x2(v[4 * q].x, v[4 * q].y),
+                     pack_bf16x2(v[4 * q + 1].x, v[4 * q + 1].y), pack_bf16x2(v[4 * q + 2].x, v[4 * q + 2].y),
+                     pack_bf16x2(v[4 * q + 3].x, v[4 * q + 3].y));
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && x < N) {
+        tma_store_2d(tm, piece, x, y);
+        bulk_commit();
+    }
+}
+
+template <int BN, int SP, int ACT>
+__device__ __forceinline__ void epilogue_store_act(const EpiParams& p, const CUtensorMap& tmD, float2* acc, const Tile& tl, int ew,
+                                                   int quarter, int lane, uint8_t* piece) {
+    using C = Cfg<BN>;
+    const int col0 = tl.n0 + (ew >> 2) * C::kColsPerWarp;
+    const int row0 = tl.m0 + quarter * 32;
+    const int64_t row = row0 + lane;
+    const bool there = row < p.M;
+    float amax = 0.f;
+#pragma unroll
+    for (int pc = 0; pc < C::kColsPerWarp / 32; ++pc) {
+        const int x = col0 + pc * 32;
+        float2* v = acc + pc * 16;
+        if (p.bias != nullptr) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (x + (q & ~1) * 4 < p.N) {  // 8 columns exist or none of them
+                    const float4 b = *reinterpret_cast<const float4*>(p.bias + x + q * 4);
+                    v[2 * q] = __fadd2_rn(v[2 * q], make_float2(b.x, b.y));
+                    v[2 * q + 1] = __fadd2_rn(v[2 * q + 1], make_float2(b.z, b.w));
+                }
+        }
+        if (p.Z != nullptr) stage_piece(&p.tmZ, piece, v, x, row0, p.N, lane);
+        if (ACT != kActNone)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = act2<ACT>(v[j]);
+        if (p.residual != nullptr && there) {
+            uint4 r[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                r[q] = x + q * 8 < p.N ? ld_once_16(p.residual + row * p.N + x + q * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                F8 f;
+                bf16x8_to_f8(r[q], f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[q * 4 + j] = __fadd2_rn(v[q * 4 + j], f[j]);
+            }
+        }
+        if (p.D != nullptr) stage_piece(&tmD, piece, v, x, row0, p.N, lane);
+        if (p.Q != nullptr)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) amax = amax3(amax, v[j].x, v[j].y);
+    }
+    if constexpr (C::kColsPerWarp == 128) {
+        // A thread holds a whole 1x128 tile: its row's 128 columns.
+        if (p.Q != nullptr && there && col0 < p.N) {
+            amax = fmaxf(amax, 1e-4f);
+            const float r = __fdiv_rn(448.f, amax);
+            p.sq[(col0 >> 7) * p.sq_stride + row] = __fdiv_rn(amax, 448.f);
+            uint8_t* q = p.Q + row * p.N + col0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2* v = acc + j * 8;
+                const F8 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+                const uint2 a = e4m3x8(lo, r), b = e4m3x8(hi, r);
+                *reinterpret_cast<uint4*>(q + j * 16) = make_uint4(a.x, a.y, b.x, b.y);
+            }
+        }
+    }
+}
+
+template <int BN, int SP>
+__device__ __forceinline__ void epilogue_store(const EpiParams& p, const CUtensorMap& tmD, float2* acc, const Tile& tl, int ew,
+                                               int quarter, int lane, uint8_t* piece) {
+    switch (p.act) {
+        case kActRelu: return epilogue_store_act<BN, SP, kActRelu>(p, tmD, acc, tl, ew, quarter, lane, piece);
+        case kActGelu: return epilogue_store_act<BN, SP, kActGelu>(p, tmD, acc, tl, ew, quarter, lane, piece);
+        case kActGeluTanh: return epilogue_store_act<BN, SP, kActGeluTanh>(p, tmD, acc, tl, ew, quarter, lane, piece);
+        case kActSilu: return epilogue_store_act<BN, SP, kActSilu>(p, tmD, acc, tl, ew, quarter, lane, piece);
+        default: return epilogue_store_act<BN, SP, kActNone>(p, tmD, acc, tl, ew, quarter, lane, piece);
+    }
+}
+
 // LAYOUT (dense only) gives the operands' storage: bit 0 set = A stored
 // [K][M] (M-major, the "T" of TN / TT), bit 1 set = B stored [K][N] (N-major,
 // the "N" of NN / TN); clear = K-major as in NT.  An MN-major operand is loaded
@@ -228,14 +338,17 @@ __device__ __forceinline__ void group_k_range(const Params& p, const Tile& tl, W
 // buffer; with one per piece of the warp's columns, a tile's whole epilogue
 // is staged and stored without waiting (the next tile's epilogue waits once),
 // which pays on short K where the epilogue is a large share of a tile.
-template <int BN, int STAGES, int MODE, int LAYOUT = 0, int SP = 1>
+// PT: Params, or EpiParams for calls with an epilogue of their own.
+template <int BN, int STAGES, int MODE, int LAYOUT = 0, int SP = 1, typename PT = Params>
 __global__ void __launch_bounds__(Cfg<BN>::kThreadsC, 1)
-fp8_gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmA,
+fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMap tmA,
                 const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmD) {
     using C = Cfg<BN>;
     constexpr int kNBuf = C::kNBuf;
     constexpr bool kAmn = (LAYOUT & 1) != 0;
     constexpr bool kBmn = (LAYOUT & 2) != 0;
+    constexpr bool kEpi = !std::is_same<PT, Params>::value;
+    static_assert(!kEpi || (MODE == kDense && LAYOUT == 0), "epilogue: dense NT calls");
     static_assert(LAYOUT == 0 || ((MODE == kDense || MODE == kKGrouped) && BN % 128 == 0),
                   "MN-major operands: dense or K-grouped, BN 128 or 256");
     static_assert(MODE != kKGrouped || LAYOUT == 3, "K-grouped: A stored [K][M], B stored [K][N]");
@@ -281,7 +394,7 @@ fp8_gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
-        prefetch_tmap(&tmD);
+        if (!kEpi || p.D != nullptr) prefetch_tmap(&tmD);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, C::kTmemCols);
@@ -612,6 +725,11 @@ fp8_gemm_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtens
                         acc[2 * j + 1].y += v.w;
                     }
                 }
+            }
+
+            if constexpr (kEpi) {
+                epilogue_store<BN, SP>(p, tmD, acc, tl, ew, quarter, lane, sOut + ew * SP * kStageOutBytes);
+                continue;
             }
 
             // Epilogue: bf16 round-to-nearest-even.  When every row of this

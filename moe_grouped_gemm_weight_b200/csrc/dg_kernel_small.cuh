@@ -67,7 +67,8 @@ constexpr int small_recv_bytes(int tn, int max_split) {
     return best;
 }
 
-template <int TN>
+// EPI: calls with bias, activation and residual stage their tile in FP32.
+template <int TN, bool EPI = false>
 struct SmallCfg {
     static_assert(TN == 32 || TN == 64 || TN == 128, "TN must be 32, 64 or 128");
     static constexpr int kMaxSplit = TN == 128 ? 4 : 8;  // cluster size (K slices per tile)
@@ -76,7 +77,7 @@ struct SmallCfg {
     static constexpr int kStageBytes = kTileBBytes + kTileABytes;
     static constexpr int kTileF32Bytes = TN * 128 * 4;   // FP32 partial tile
     static constexpr int kRecvBytes = small_recv_bytes(TN, kMaxSplit);
-    static constexpr int kStageOutBytes = TN * 128 * 2;  // bf16 tile staged for the store
+    static constexpr int kStageOutBytes = TN * 128 * (EPI ? 4 : 2);  // tile staged for the store
     static constexpr int kAuxBytes = kRecvBytes > kStageOutBytes ? kRecvBytes : kStageOutBytes;
     static constexpr int kScaleBytes = kSmallScaleSlots * (TN + 4) * 4;
     static constexpr int kFixedBytes = 1024 + kAuxBytes + kScaleBytes + kSmallBarrierBytes + kSmallGroupTableBytes;
@@ -92,9 +93,10 @@ struct SmallCfg {
     static_assert(kStages * kStageBytes + kFixedBytes <= kSmallSmemLimit, "shared memory overflow");
 };
 
-template <int TN>
+template <int TN, bool EPI = false>
 constexpr int small_smem_bytes() {
-    return SmallCfg<TN>::kStages * SmallCfg<TN>::kStageBytes + SmallCfg<TN>::kFixedBytes;
+    using C = SmallCfg<TN, EPI>;
+    return C::kStages * C::kStageBytes + C::kFixedBytes;
 }
 
 // One tile of the few-row kernel.
@@ -131,13 +133,67 @@ __device__ __forceinline__ SmallTile small_tile(const Params& p, int t, const in
     return tl;
 }
 
+// Eight columns of one row of a call with an epilogue of its own; the half-warp
+// holds the row's 128 columns, lane hl columns 8 hl .. 8 hl + 7.
+template <int ACT>
+__device__ __forceinline__ void small_epilogue_act(const EpiParams& p, F8& v, int64_t at) {
+    if (p.Z != nullptr)
+        *reinterpret_cast<uint4*>(p.Z + at) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                         pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+    if (ACT != kActNone)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = act2<ACT>(v[j]);
+}
+__device__ __forceinline__ void small_epilogue(const EpiParams& p, F8& v, int row, int col, int lane) {
+    if (row >= p.M) return;  // the whole half-warp
+    const uint32_t half = 0xffffu << (lane & 16);
+    const int64_t at = static_cast<int64_t>(row) * p.N + col;
+    if (col < p.N) {
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (p.residual != nullptr) r = ld_once_16(p.residual + at);
+        if (p.bias != nullptr) {
+            const float4 b0 = *reinterpret_cast<const float4*>(p.bias + col), b1 = *reinterpret_cast<const float4*>(p.bias + col + 4);
+            v[0] = __fadd2_rn(v[0], make_float2(b0.x, b0.y));
+            v[1] = __fadd2_rn(v[1], make_float2(b0.z, b0.w));
+            v[2] = __fadd2_rn(v[2], make_float2(b1.x, b1.y));
+            v[3] = __fadd2_rn(v[3], make_float2(b1.z, b1.w));
+        }
+        switch (p.act) {
+            case kActRelu: small_epilogue_act<kActRelu>(p, v, at); break;
+            case kActGelu: small_epilogue_act<kActGelu>(p, v, at); break;
+            case kActGeluTanh: small_epilogue_act<kActGeluTanh>(p, v, at); break;
+            case kActSilu: small_epilogue_act<kActSilu>(p, v, at); break;
+            default: small_epilogue_act<kActNone>(p, v, at); break;
+        }
+        if (p.residual != nullptr) {
+            F8 f;
+            bf16x8_to_f8(r, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = __fadd2_rn(v[j], f[j]);
+        }
+        if (p.D != nullptr)
+            *reinterpret_cast<uint4*>(p.D + at) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                             pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+    }
+    if (p.Q != nullptr) {  // N is a multiple of 128: every lane has columns
+        float a = amax8(v);
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(half, a, o));
+        a = fmaxf(a, 1e-4f);
+        *reinterpret_cast<uint2*>(p.Q + at) = e4m3x8(v, __fdiv_rn(448.f, a));
+        if ((lane & 15) == 0) p.sq[(col >> 7) * p.sq_stride + row] = __fdiv_rn(a, 448.f);
+    }
+}
+
 // Grid: 1-D, clusters of S CTAs along x (S = cluster size).  Params::m_blocks
 // holds the TN-row blocks per group; Params::n_blocks the 128-wide blocks of N.
-template <int TN, int MODE>
+template <int TN, int MODE, typename PT = Params>
 __global__ void __launch_bounds__(kSmallThreads, 1)
-fp8_gemm_swapab_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmA,
+fp8_gemm_swapab_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB) {
-    using C = SmallCfg<TN>;
+    constexpr bool kEpi = !std::is_same<PT, Params>::value;
+    static_assert(!kEpi || MODE == kDense, "epilogue: dense calls");
+    using C = SmallCfg<TN, kEpi>;
     constexpr int STAGES = C::kStages;
     constexpr int kNBuf = C::kNBuf;
     // The tensor maps live in parameter space: start fetching them first.
@@ -455,21 +511,39 @@ fp8_gemm_swapab_kernel(const __grid_constant__ Params p, const __grid_constant__
                 // write each row's 128 columns with 16-byte stores.  The first
                 // barrier keeps this tile's staging off the previous tile's
                 // reads.
-                uint16_t* stg = reinterpret_cast<uint16_t*>(aux);
-                named_barrier_sync(1, kSmallEpiThreads);
+                if constexpr (kEpi) {
+                    float* stg = reinterpret_cast<float*>(aux);
+                    named_barrier_sync(1, kSmallEpiThreads);
 #pragma unroll
-                for (int q = 0; q < C::kCols / 2; ++q) {
-                    const __nv_bfloat162 h = __float22bfloat162_rn(acc[q]);
-                    stg[(j_base + 2 * q) * 128 + n] = *reinterpret_cast<const uint16_t*>(&h.x);
-                    stg[(j_base + 2 * q + 1) * 128 + n] = *reinterpret_cast<const uint16_t*>(&h.y);
-                }
-                named_barrier_sync(1, kSmallEpiThreads);
-                for (int c = ptid; c < TN * 16; c += kSmallEpiThreads) {
-                    const int j = c >> 4, col = tl.n0 + (c & 15) * 8;
-                    const int row = tl.m0 + j;
-                    if (row < tl.rows && col < p.N)
-                        *reinterpret_cast<uint4*>(p.D + (d_base + row) * p.N + col) =
-                            *reinterpret_cast<const uint4*>(stg + j * 128 + (c & 15) * 8);
+                    for (int q = 0; q < C::kCols / 2; ++q) {
+                        stg[(j_base + 2 * q) * 128 + n] = acc[q].x;
+                        stg[(j_base + 2 * q + 1) * 128 + n] = acc[q].y;
+                    }
+                    named_barrier_sync(1, kSmallEpiThreads);
+                    for (int c = ptid; c < TN * 16; c += kSmallEpiThreads) {
+                        const float4* src = reinterpret_cast<const float4*>(stg + (c >> 4) * 128 + (c & 15) * 8);
+                        const float4 a4 = src[0], b4 = src[1];
+                        F8 v = {make_float2(a4.x, a4.y), make_float2(a4.z, a4.w), make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+                        small_epilogue(p, v, tl.m0 + (c >> 4), tl.n0 + (c & 15) * 8, lane);
+                        __syncwarp();
+                    }
+                } else {
+                    uint16_t* stg = reinterpret_cast<uint16_t*>(aux);
+                    named_barrier_sync(1, kSmallEpiThreads);
+#pragma unroll
+                    for (int q = 0; q < C::kCols / 2; ++q) {
+                        const __nv_bfloat162 h = __float22bfloat162_rn(acc[q]);
+                        stg[(j_base + 2 * q) * 128 + n] = *reinterpret_cast<const uint16_t*>(&h.x);
+                        stg[(j_base + 2 * q + 1) * 128 + n] = *reinterpret_cast<const uint16_t*>(&h.y);
+                    }
+                    named_barrier_sync(1, kSmallEpiThreads);
+                    for (int c = ptid; c < TN * 16; c += kSmallEpiThreads) {
+                        const int j = c >> 4, col = tl.n0 + (c & 15) * 8;
+                        const int row = tl.m0 + j;
+                        if (row < tl.rows && col < p.N)
+                            *reinterpret_cast<uint4*>(p.D + (d_base + row) * p.N + col) =
+                                *reinterpret_cast<const uint4*>(stg + j * 128 + (c & 15) * 8);
+                    }
                 }
             } else {
                 // ------------------------------ split tile: reduction ----
@@ -533,7 +607,10 @@ fp8_gemm_swapab_kernel(const __grid_constant__ Params p, const __grid_constant__
                             }
                         }
                     const int row = tl.m0 + my_j0 + jj, col = tl.n0 + c8;
-                    if (row < tl.rows && col < p.N) {
+                    if constexpr (kEpi) {
+                        F8 v = {make_float2(sa4.x, sa4.y), make_float2(sa4.z, sa4.w), make_float2(sb4.x, sb4.y), make_float2(sb4.z, sb4.w)};
+                        small_epilogue(p, v, row, col, lane);
+                    } else if (row < tl.rows && col < p.N) {
                         __nv_bfloat162 h0 = __floats2bfloat162_rn(sa4.x, sa4.y);
                         __nv_bfloat162 h1 = __floats2bfloat162_rn(sa4.z, sa4.w);
                         __nv_bfloat162 h2 = __floats2bfloat162_rn(sb4.x, sb4.y);

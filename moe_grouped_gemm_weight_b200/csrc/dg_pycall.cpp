@@ -17,9 +17,10 @@
 
 #include "dg.h"
 
-static void *g_entry[9];
+static void *g_entry[15];
 
-enum { ROUTE, ROUTE_BWD, LAYOUT, DISPATCH, COMBINE, COMBINE_BWD, SWIGLU, SWIGLU_BWD, RECAST };
+enum { ROUTE, ROUTE_BWD, LAYOUT, DISPATCH, COMBINE, COMBINE_BWD, SWIGLU, SWIGLU_BWD, RECAST,
+       EPILOGUE, EPILOGUE_BWD, NORM, NORM_BWD, BALANCE, BALANCE_BWD };
 
 /*
  * Argument i as a pointer (a tensor's data, None as null, or a number) or an
@@ -147,9 +148,56 @@ ENTRY(dg_fp8_1x128_to_128x128, RECAST, 9, {
     RUN(dg_fp8_1x128_to_128x128, RECAST, p0, p1, p2, p3, sa, p5, rows, K, st);
 })
 
-static const char *const kNames[9] = {"dg_route_topk", "dg_route_topk_bwd", "dg_route_layout", "dg_dispatch_fp8_1x128",
+ENTRY(dg_fp8_gemm_nt_epilogue, EPILOGUE, 17, {
+    Ptr p0{P(0)}; Ptr p1{P(1)}; Ptr p2{P(2)}; Ptr p3{P(3)}; Ptr p5{P(5)}; Ptr p6{P(6)};
+    Ptr p8{P(8)}; Ptr p9{P(9)}; Ptr p10{P(10)}; Ptr p12{P(12)}; Ptr st{P(16)};
+    int qs = I(4); int as = I(7); int act = I(11); int M = I(13); int N = I(14); int K = I(15);
+    RUN(dg_fp8_gemm_nt_epilogue, EPILOGUE, p0, p1, p2, p3, qs, p5, p6, as, p8, p9, p10, act, p12, M, N, K, st);
+})
+ENTRY(dg_epilogue_bwd, EPILOGUE_BWD, 14, {
+    Ptr p0{P(0)}; Ptr p1{P(1)}; Ptr p3{P(3)}; Ptr p4{P(4)}; Ptr p6{P(6)}; Ptr p7{P(7)};
+    Ptr p8{P(8)}; Ptr p9{P(9)}; Ptr st{P(13)};
+    int rs = I(2); int cs = I(5); int act = I(10); int M = I(11); int N = I(12);
+    RUN(dg_epilogue_bwd, EPILOGUE_BWD, p0, p1, rs, p3, p4, cs, p6, p7, p8, p9, act, M, N, st);
+})
+ENTRY(dg_norm_residual, NORM, 18, {
+    Ptr p0{P(0)}; Ptr p1{P(1)}; Ptr p2{P(2)}; Ptr p3{P(3)}; Ptr p5{P(5)}; Ptr p6{P(6)};
+    Ptr p8{P(8)}; Ptr p9{P(9)}; Ptr p10{P(10)}; Ptr p11{P(11)}; Ptr st{P(17)};
+    int qs = I(4); int dt = I(7); int T = I(12); int N = I(13); int pn = I(14);
+    float scale = PyErr_Occurred() ? 0.f : (float)PyFloat_AsDouble(a[15]);
+    float eps = PyErr_Occurred() ? 0.f : (float)PyFloat_AsDouble(a[16]);
+    RUN(dg_norm_residual, NORM, p0, p1, p2, p3, qs, p5, p6, dt, p8, p9, p10, p11, T, N, pn, scale, eps, st);
+})
+ENTRY(dg_norm_residual_bwd, NORM_BWD, 20, {
+    Ptr p0{P(0)}; Ptr p1{P(1)}; Ptr p2{P(2)}; Ptr p3{P(3)}; Ptr p4{P(4)}; Ptr p5{P(5)};
+    Ptr p6{P(6)}; Ptr p7{P(7)}; Ptr p8{P(8)}; Ptr p10{P(10)}; Ptr p11{P(11)}; Ptr p12{P(12)};
+    Ptr p13{P(13)}; Ptr p14{P(14)};
+    int dt = I(9); int T = I(15); int N = I(16); int pn = I(17);
+    float scale = PyErr_Occurred() ? 0.f : (float)PyFloat_AsDouble(a[18]);
+    Ptr st{P(19)};
+    RUN(dg_norm_residual_bwd, NORM_BWD, p0, p1, p2, p3, p4, p5, p6, p7, p8, dt, p10, p11, p12, p13, p14, T, N, pn,
+        scale, st);
+})
+ENTRY(dg_balance_loss, BALANCE, 15, {
+    Ptr p0{P(0)}; Ptr p1{P(1)}; Ptr p2{P(2)}; Ptr p3{P(3)}; Ptr p4{P(4)}; Ptr p6{P(6)};
+    Ptr p7{P(7)}; Ptr st{P(14)};
+    int dt = I(5); int T = I(8); int E = I(9); int k = I(10); int S = I(11); int sc = I(12);
+    float coef = PyErr_Occurred() ? 0.f : (float)PyFloat_AsDouble(a[13]);
+    RUN(dg_balance_loss, BALANCE, p0, p1, p2, p3, p4, dt, p6, p7, T, E, k, S, sc, coef, st);
+})
+ENTRY(dg_balance_loss_bwd, BALANCE_BWD, 14, {
+    Ptr p0{P(0)}; Ptr p1{P(1)}; Ptr p2{P(2)}; Ptr p3{P(3)}; Ptr p5{P(5)}; Ptr p6{P(6)};
+    Ptr st{P(13)};
+    int dt = I(4); int T = I(7); int E = I(8); int k = I(9); int S = I(10); int sc = I(11);
+    float coef = PyErr_Occurred() ? 0.f : (float)PyFloat_AsDouble(a[12]);
+    RUN(dg_balance_loss_bwd, BALANCE_BWD, p0, p1, p2, p3, dt, p5, p6, T, E, k, S, sc, coef, st);
+})
+
+static const char *const kNames[15] = {"dg_route_topk", "dg_route_topk_bwd", "dg_route_layout", "dg_dispatch_fp8_1x128",
                                       "dg_combine", "dg_combine_bwd", "dg_swiglu_fp8", "dg_swiglu_fp8_bwd",
-                                      "dg_fp8_1x128_to_128x128"};
+                                      "dg_fp8_1x128_to_128x128", "dg_fp8_gemm_nt_epilogue", "dg_epilogue_bwd",
+                                      "dg_norm_residual",
+                                      "dg_norm_residual_bwd", "dg_balance_loss", "dg_balance_loss_bwd"};
 
 /*
  * fits(tensor, kind, need, ...): the current CUDA device's index if every
@@ -190,7 +238,7 @@ static PyObject *bind(PyObject *self, PyObject *args) {
     int i;
     (void)self;
     if (!PyArg_ParseTuple(args, "sO", &name, &address)) return NULL;
-    for (i = 0; i < 9; ++i)
+    for (i = 0; i < 15; ++i)
         if (strcmp(name, kNames[i]) == 0) {
             g_entry[i] = PyLong_AsVoidPtr(address);
             if (PyErr_Occurred()) return NULL;
@@ -203,7 +251,9 @@ static PyObject *bind(PyObject *self, PyObject *args) {
 static PyMethodDef kMethods[] = {
     FAST(dg_route_topk), FAST(dg_route_topk_bwd), FAST(dg_route_layout), FAST(dg_dispatch_fp8_1x128),
     FAST(dg_combine), FAST(dg_combine_bwd), FAST(dg_swiglu_fp8), FAST(dg_swiglu_fp8_bwd),
-    FAST(dg_fp8_1x128_to_128x128), {"fits", (PyCFunction)(void (*)(void))fits, METH_FASTCALL, NULL}, {"bind", bind, METH_VARARGS, NULL}, {NULL, NULL, 0, NULL}};
+    FAST(dg_fp8_1x128_to_128x128), FAST(dg_fp8_gemm_nt_epilogue), FAST(dg_epilogue_bwd), FAST(dg_norm_residual), FAST(dg_norm_residual_bwd),
+    FAST(dg_balance_loss), FAST(dg_balance_loss_bwd),
+    {"fits", (PyCFunction)(void (*)(void))fits, METH_FASTCALL, NULL}, {"bind", bind, METH_VARARGS, NULL}, {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_dgcall", "Argument marshalling for libdg.so", -1,
                                      kMethods, NULL, NULL, NULL, NULL};
