@@ -84,12 +84,13 @@ struct Params {
 // Epilogue of dense calls with bias, activation and residual: z = acc + bias, v =
 // act(z) + residual; z and v are stored as bf16, v as e4m3 with a scale per 1x128.
 struct EpiParams : Params {
-    CUtensorMap tmZ;           // of Z, like tmD
+    CUtensorMap tmZ, tmR;      // of Z and the residual, like tmD
+    CUtensorMap tmQ;           // of Q: boxes of a promotion warp's 32 rows and all of its columns
     uint16_t* Z;               // [M][N] or null; D may be null too
     uint8_t* Q;                // [M][N] or null
     float* sq;                 // sq[(n/128)*sq_stride + m]
     const float* bias;         // [N] or null
-    const uint16_t* residual;  // [M][N] or null
+    const uint16_t* residual;  // [M][N] or null, perhaps D
     int64_t sq_stride;
     int act;
 };
@@ -149,13 +150,15 @@ struct Cfg {
     static_assert(kChunks % kBatch == 0, "chunk batching");
 };
 
-template <int BN, int STAGES, int SP = 1>
+constexpr int kEpiTableBytes = 1536;  // EpiParams calls: their table (EpiTable) may be this much larger
+
+template <int BN, int STAGES, int SP = 1, bool EPI = false>
 constexpr int smem_bytes() {
     // 1 KiB alignment slack + operand ring + output staging (SP pieces of
     // 32 x 32 bf16 per promotion warp) + barriers and bookkeeping (512 B) +
     // scale ring + masked prefix table.
     return 1024 + STAGES * (kTileABytes + Cfg<BN>::kTileBBytes) + Cfg<BN>::kEpiWarpsC * SP * kStageOutBytes + 512 +
-           kScaleSlots * kScaleSlotFloats * 4 + 4 * (kMaxMaskedGroups + 1);
+           kScaleSlots * kScaleSlotFloats * 4 + 4 * (kMaxMaskedGroups + 1) + (EPI ? kEpiTableBytes : 0);
 }
 
 struct Tile {
@@ -236,98 +239,255 @@ __device__ __forceinline__ void group_k_range(const Params& p, const Tile& tl, W
     w.kb1 = k1 / kBK;
 }
 
-// One promotion warp's share of a tile, staged 32 x 32 values at a time in `piece`
-// as bf16 (64-byte swizzle, as in the kernel's own epilogue) and stored by TMA.
-__device__ __forceinline__ void stage_piece(const CUtensorMap* tm, uint8_t* piece, const float2* v, int x, int y, int N, int lane) {
-    if (lane == 0) bulk_wait_read<0>();  // the previous store has read the buffer
-    __syncwarp();
-    const uint32_t stg = smem_u32(piece);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        st_shared_v4(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), pack_bf16x2(v[4 * q].x, v[4 * q].y),
-                     pack_bf16x2(v[4 * q + 1].x, v[4 * q + 1].y), pack_bf16x2(v[4 * q + 2].x, v[4 * q + 2].y),
-                     pack_bf16x2(v[4 * q + 3].x, v[4 * q + 3].y));
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0 && x < N) {
-        tma_store_2d(tm, piece, x, y);
-        bulk_commit();
-    }
-}
+// Shared memory of EpiParams calls in place of the masked mode's prefix table, which
+// they do not have.
+template <int BN>
+struct EpiTable {
+    // The scale producer writes a tile's bias when it has a free ring slot for its first
+    // scales: at most kScaleGroups tiles ahead of the epilogue.
+    static constexpr int kBiasSlots = kScaleGroups + 1;
+    float bias[kBiasSlots][BN];
+    float pair_max[4][2][2][BN == 128 ? 32 : 1];  // [quarter][turn][half][row]: see EpiWarp::cast
+    uint64_t res_full;                            // the tile's residual has arrived in the staging buffers
+    uint64_t warp_full[Cfg<BN>::kEpiWarpsC];      // ... a warp's share of it, where the warp itself asked for it
+    uint64_t pair_bar[4];
 
-template <int BN, int SP, int ACT>
-__device__ __forceinline__ void epilogue_store_act(const EpiParams& p, const CUtensorMap& tmD, float2* acc, const Tile& tl, int ew,
-                                                   int quarter, int lane, uint8_t* piece) {
+    __device__ void init() {  // one thread, before the roles part
+        mbar_init(&res_full, 1);
+        for (int w = 0; w < Cfg<BN>::kEpiWarpsC; ++w) mbar_init(warp_full + w, 1);
+        for (int w = 0; w < 4; ++w) mbar_init(pair_bar + w, 2);
+    }
+};
+
+// The epilogue of EpiParams calls, for one promotion warp's 32 rows and kColsPerWarp
+// columns of a tile.  Each 32 x 32 piece has a staging buffer of its own (bf16 with the
+// 64-byte swizzle of the kernel's own epilogue), so the stores drain while the warp goes
+// on, and the residual arrives in the same buffers by TMA during the tile's K loop (with
+// Z: once Z's stores have read them).
+//
+// The promotion warps are the whole kernel's bottleneck, their K loop has every register
+// in use, and their epilogue adds to each tile's time.  So the scale producer fetches bias
+// and residual, and nothing of the epilogue stays in registers over the K loop: addresses
+// are formed from the thread's index, read anew, and phases from the CTA's count of
+// tiles.  (With a handful of registers more each K block took 36 ns longer: 4096 x 4096 x
+// 7168 115 -> 122 us; asking for the residual from within the K loop spilled: 148 us.)
+template <int BN>
+struct EpiWarp {
     using C = Cfg<BN>;
-    const int col0 = tl.n0 + (ew >> 2) * C::kColsPerWarp;
-    const int row0 = tl.m0 + quarter * 32;
-    const int64_t row = row0 + lane;
-    const bool there = row < p.M;
-    float amax = 0.f;
+    static constexpr int kPieces = C::kColsPerWarp / 32;
+
+    uint32_t lane, ew;
+    uint32_t stage;  // kPieces x kStageOutBytes
+    int x, row0;     // the warp's first column and row
+    EpiTable<BN>* tb;
+
+    __device__ __forceinline__ EpiWarp(uint8_t* out, EpiTable<BN>* table, const Tile& tl) {
+        uint32_t tid;
+        asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));  // volatile: not kept over the K loop
+        lane = tid & 31;
+        ew = (tid >> 5) - kFirstEpiWarp;
+        stage = smem_u32(out) + ew * (kPieces * kStageOutBytes);
+        x = tl.n0 + static_cast<int>(ew >> 2) * C::kColsPerWarp;
+        row0 = tl.m0 + static_cast<int>(ew & 3) * 32;
+        tb = table;
+    }
+
+    __device__ __forceinline__ void wait_stores() const {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+    }
+    __device__ __forceinline__ uint32_t piece_at(int pc, int q) const {
+        return stage + pc * kStageOutBytes + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
+    }
+    __device__ __forceinline__ void store_piece(const EpiParams& p, const CUtensorMap* tm, int pc, const float2* v) const {
 #pragma unroll
-    for (int pc = 0; pc < C::kColsPerWarp / 32; ++pc) {
-        const int x = col0 + pc * 32;
-        float2* v = acc + pc * 16;
-        if (p.bias != nullptr) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (x + (q & ~1) * 4 < p.N) {  // 8 columns exist or none of them
-                    const float4 b = *reinterpret_cast<const float4*>(p.bias + x + q * 4);
-                    v[2 * q] = __fadd2_rn(v[2 * q], make_float2(b.x, b.y));
-                    v[2 * q + 1] = __fadd2_rn(v[2 * q + 1], make_float2(b.z, b.w));
-                }
+        for (int q = 0; q < 4; ++q)
+            st_shared_v4(piece_at(pc, q), pack_bf16x2(v[4 * q].x, v[4 * q].y), pack_bf16x2(v[4 * q + 1].x, v[4 * q + 1].y),
+                         pack_bf16x2(v[4 * q + 2].x, v[4 * q + 2].y), pack_bf16x2(v[4 * q + 3].x, v[4 * q + 3].y));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && x + pc * 32 < p.N) {
+            tma_store_2d(tm, stage + pc * kStageOutBytes, x + pc * 32, row0);
+            bulk_commit();
         }
-        if (p.Z != nullptr) stage_piece(&p.tmZ, piece, v, x, row0, p.N, lane);
+    }
+
+    // acc of the CTA's it-th tile; false: a wait ran out.
+    template <int ACT>
+    __device__ __forceinline__ bool run(const EpiParams& p, const CUtensorMap& tmD, float2* acc, int it, volatile int* abort_flag) const {
+        if (p.bias != nullptr) {  // landed before the tile's first scales
+            const uint32_t b0 = smem_u32(tb->bias[it % EpiTable<BN>::kBiasSlots]) + (ew >> 2) * (C::kColsPerWarp * 4);
+#pragma unroll
+            for (int j = 0; j < C::kColsPerWarp / 4; ++j) {
+                const uint4 b = ld_shared_16(b0 + j * 16);
+                acc[2 * j] = __fadd2_rn(acc[2 * j], make_float2(__uint_as_float(b.x), __uint_as_float(b.y)));
+                acc[2 * j + 1] = __fadd2_rn(acc[2 * j + 1], make_float2(__uint_as_float(b.z), __uint_as_float(b.w)));
+            }
+        }
+        const bool res = p.residual != nullptr && x < p.N;
+        if (p.Z != nullptr) {
+            wait_stores();
+#pragma unroll
+            for (int pc = 0; pc < kPieces; ++pc) store_piece(p, &p.tmZ, pc, acc + pc * 16);
+            uint64_t* bar = tb->warp_full + ew;
+            if (p.residual != nullptr && !res && lane == 0) mbar_arrive(bar);  // a phase a tile, also without columns
+            if (res && lane == 0) {
+                bulk_wait_read<0>();
+                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(min(kPieces, (p.N - x + 31) / 32) * kStageOutBytes));
+                const uint64_t policy = l2_policy_evict_first();
+#pragma unroll
+                for (int pc = 0; pc < kPieces; ++pc)
+                    if (x + pc * 32 < p.N) tma_load_2d(stage + pc * kStageOutBytes, &p.tmR, bar, x + pc * 32, row0, policy);
+            }
+        }
         if (ACT != kActNone)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = act2<ACT>(v[j]);
-        if (p.residual != nullptr && there) {
-            uint4 r[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                r[q] = x + q * 8 < p.N ? ld_once_16(p.residual + row * p.N + x + q * 8) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                F8 f;
-                bf16x8_to_f8(r[q], f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[q * 4 + j] = __fadd2_rn(v[q * 4 + j], f[j]);
+            for (int j = 0; j < C::kColsPerWarp / 2; ++j) acc[j] = act2<ACT>(acc[j]);
+        if (res) {
+            uint64_t* bar = p.Z != nullptr ? tb->warp_full + ew : &tb->res_full;
+            if (!mbar_wait(bar, it & 1, abort_flag)) {
+                if (p.Z != nullptr) mbar_wait_drain(bar, it & 1);  // no copy may land after the CTA's end
+                return false;
             }
-        }
-        if (p.D != nullptr) stage_piece(&tmD, piece, v, x, row0, p.N, lane);
-        if (p.Q != nullptr)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) amax = amax3(amax, v[j].x, v[j].y);
-    }
-    if constexpr (C::kColsPerWarp == 128) {
-        // A thread holds a whole 1x128 tile: its row's 128 columns.
-        if (p.Q != nullptr && there && col0 < p.N) {
-            amax = fmaxf(amax, 1e-4f);
-            const float r = __fdiv_rn(448.f, amax);
-            p.sq[(col0 >> 7) * p.sq_stride + row] = __fdiv_rn(amax, 448.f);
-            uint8_t* q = p.Q + row * p.N + col0;
+            for (int pc = 0; pc < kPieces; ++pc)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2* v = acc + j * 8;
-                const F8 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
-                const uint2 a = e4m3x8(lo, r), b = e4m3x8(hi, r);
-                *reinterpret_cast<uint4*>(q + j * 16) = make_uint4(a.x, a.y, b.x, b.y);
-            }
+                for (int q = 0; q < 4; ++q) {
+                    F8 f;
+                    bf16x8_to_f8(ld_shared_16(piece_at(pc, q)), f);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[pc * 16 + q * 4 + j] = __fadd2_rn(acc[pc * 16 + q * 4 + j], f[j]);
+                }
+            __syncwarp();
+        } else {
+            wait_stores();
         }
+        if (p.D != nullptr) {
+#pragma unroll
+            for (int pc = 0; pc < kPieces; ++pc) store_piece(p, &tmD, pc, acc + pc * 16);
+        }
+        if constexpr (kPieces >= 2) {
+            if (p.Q != nullptr) return cast(p, acc, it, abort_flag);
+        }
+        return true;
     }
-}
 
-template <int BN, int SP>
-__device__ __forceinline__ void epilogue_store(const EpiParams& p, const CUtensorMap& tmD, float2* acc, const Tile& tl, int ew,
-                                               int quarter, int lane, uint8_t* piece) {
-    switch (p.act) {
-        case kActRelu: return epilogue_store_act<BN, SP, kActRelu>(p, tmD, acc, tl, ew, quarter, lane, piece);
-        case kActGelu: return epilogue_store_act<BN, SP, kActGelu>(p, tmD, acc, tl, ew, quarter, lane, piece);
-        case kActGeluTanh: return epilogue_store_act<BN, SP, kActGeluTanh>(p, tmD, acc, tl, ew, quarter, lane, piece);
-        case kActSilu: return epilogue_store_act<BN, SP, kActSilu>(p, tmD, acc, tl, ew, quarter, lane, piece);
-        default: return epilogue_store_act<BN, SP, kActNone>(p, tmD, acc, tl, ew, quarter, lane, piece);
+    // A thread holds a row's whole 1x128 tile, or half of it and the warp four warps on
+    // (or back) the other.
+    __device__ __forceinline__ bool cast(const EpiParams& p, float2* acc, int it, volatile int* abort_flag) const {
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < C::kColsPerWarp / 2; ++j) amax = amax3(amax, acc[j].x, acc[j].y);
+        if constexpr (C::kColsPerWarp == 64) {
+            // Two turns: what a warp reads of one is written again only after both have met in the next.
+            auto& both = tb->pair_max[ew & 3][it & 1];
+            both[ew >> 2][lane] = amax;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tb->pair_bar + (ew & 3));
+            if (!mbar_wait(tb->pair_bar + (ew & 3), it & 1, abort_flag)) return false;
+            amax = fmaxf(amax, both[(ew >> 2) ^ 1][lane]);
+        }
+        if (p.D != nullptr) wait_stores();
+        amax = fmaxf(amax, 1e-4f);
+        const float r = __fdiv_rn(448.f, amax);
+        const int64_t row = row0 + static_cast<int>(lane);
+        if (row < p.M && x < p.N && (C::kColsPerWarp == 128 || ew < 4)) p.sq[(x >> 7) * p.sq_stride + row] = __fdiv_rn(amax, 448.f);
+#pragma unroll
+        for (int j = 0; j < C::kColsPerWarp / 16; ++j) {
+            const float2* v = acc + j * 8;
+            const F8 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+            const uint2 a = e4m3x8(lo, r), b = e4m3x8(hi, r);
+            // rows of kColsPerWarp bytes under the swizzle of that span
+            const uint32_t at = C::kColsPerWarp == 128 ? lane * 128 + ((j ^ (lane & 7)) << 4) : lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
+            st_shared_v4(stage + at, a.x, a.y, b.x, b.y);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && x < p.N) {
+            tma_store_2d(&p.tmQ, stage, x, row0);
+            bulk_commit();
+        }
+        return true;
     }
-}
+
+    __device__ __forceinline__ bool finish(const EpiParams& p, const CUtensorMap& tmD, float2* acc, int it, volatile int* abort_flag) const {
+        switch (p.act) {
+            case kActRelu: return run<kActRelu>(p, tmD, acc, it, abort_flag);
+            case kActGelu: return run<kActGelu>(p, tmD, acc, it, abort_flag);
+            case kActGeluTanh: return run<kActGeluTanh>(p, tmD, acc, it, abort_flag);
+            case kActSilu: return run<kActSilu>(p, tmD, acc, it, abort_flag);
+            default: return run<kActNone>(p, tmD, acc, it, abort_flag);
+        }
+    }
+};
+
+// What the scale producer (a whole warp) does for that epilogue.
+template <int BN>
+struct EpiFetch {
+    using C = Cfg<BN>;
+    static constexpr int kPieces = C::kColsPerWarp / 32;
+    const EpiParams& p;
+    EpiTable<BN>* tb;
+    uint8_t* out;        // the staging buffers
+    bool pending, sent;  // a tile's residual is still to be asked for; one is on its way
+    int it, m0, n0;      // of that tile
+    int slot;            // ... the ring slot of its first scales, whose release says that the
+    uint32_t phase;      // previous tile's stores have left the buffers, and that release's parity
+
+    // With a ring slot for the tile's first scales: its bias, which lands with them.
+    __device__ __forceinline__ void begin(const Tile& tl, int tile, int lane) {
+        if (p.bias == nullptr) return;
+        const uint32_t to = smem_u32(tb->bias[tile % EpiTable<BN>::kBiasSlots]);
+#pragma unroll
+        for (int c = 0; c < BN; c += 128) {
+            const int j = c + lane * 4;
+            const bool there = tl.n0 + j < p.N;
+            if (j < BN) cp_async_16(to + j * 4, p.bias + (there ? tl.n0 + j : 0), there ? 16 : 0);
+        }
+    }
+    // Behind the tile's first scales, copied to `ring` slot in a pass of parity `ring_phase`.
+    __device__ __forceinline__ void want(const Tile& tl, int tile, int ring_slot, uint32_t ring_phase, int lane) {
+        if (p.residual == nullptr) return;
+        if (p.Z != nullptr) {
+            // The promotion warps ask for it themselves, between Z's stores and D's.
+            const int px = tl.n0 + (lane & 7) * 32;
+            if (px < p.N && (lane & 7) * 32 < BN) tma_prefetch_2d(&p.tmR, px, tl.m0 + (lane >> 3) * 32);
+            return;
+        }
+        pending = true;
+        it = tile;
+        m0 = tl.m0;
+        n0 = tl.n0;
+        slot = ring_slot;
+        phase = ring_phase;
+    }
+    // Once the slot's release has been waited for.
+    __device__ __forceinline__ void send(int lane) {
+        pending = false;
+        sent = true;
+        const int n = min(BN / 32, (p.N - n0 + 31) / 32);  // pieces across, of four rows of them
+        if (lane == 0) mbar_arrive_expect_tx(&tb->res_full, static_cast<uint32_t>(4 * n * kStageOutBytes));
+        __syncwarp();
+        const uint64_t policy = l2_policy_evict_first();
+        const int quarter = lane & 3, pc = lane >> 2;  // up to 8 pieces across
+        const int half = pc / kPieces;
+        if (pc < n)
+            tma_load_2d(smem_u32(out) + ((half * 4 + quarter) * kPieces + pc % kPieces) * kStageOutBytes, &p.tmR, &tb->res_full,
+                        n0 + pc * 32, m0 + quarter * 32, policy);
+        __syncwarp();
+    }
+    // `sempty`: the scale ring's release barriers.  false: a wait ran out.
+    __device__ __forceinline__ bool flush(uint64_t* sempty, int lane, volatile int* abort_flag) {
+        if (!pending) return true;
+        if (!mbar_wait(sempty + slot, phase, abort_flag)) return false;
+        send(lane);
+        return true;
+    }
+    // No copy into shared memory may still be on its way when the CTA exits.
+    __device__ __forceinline__ void end() {
+        if (sent) mbar_wait_drain(&tb->res_full, it & 1);
+    }
+};
 
 // LAYOUT (dense only) gives the operands' storage: bit 0 set = A stored
 // [K][M] (M-major, the "T" of TN / TT), bit 1 set = B stored [K][N] (N-major,
@@ -348,7 +508,9 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
     constexpr bool kAmn = (LAYOUT & 1) != 0;
     constexpr bool kBmn = (LAYOUT & 2) != 0;
     constexpr bool kEpi = !std::is_same<PT, Params>::value;
-    static_assert(!kEpi || (MODE == kDense && LAYOUT == 0), "epilogue: dense NT calls");
+    static_assert(!kEpi || (MODE == kDense && LAYOUT == 0 && SP == C::kColsPerWarp / 32),
+                  "epilogue: dense NT calls, a staging buffer per piece");
+    static_assert(!kEpi || sizeof(EpiTable<BN>) <= 4 * (kMaxMaskedGroups + 1) + kEpiTableBytes, "the table does not fit");
     static_assert(LAYOUT == 0 || ((MODE == kDense || MODE == kKGrouped) && BN % 128 == 0),
                   "MN-major operands: dense or K-grouped, BN 128 or 256");
     static_assert(MODE != kKGrouped || LAYOUT == 3, "K-grouped: A stored [K][M], B stored [K][N]");
@@ -369,6 +531,7 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float* sring = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 512);
     int* mb_prefix = reinterpret_cast<int*>(sring + kScaleSlots * kScaleSlotFloats);
+    EpiTable<BN>* epi_table = reinterpret_cast<EpiTable<BN>*>(mb_prefix);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -388,6 +551,7 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
         }
         mbar_init(done, 1);
         mbar_init(done + 1, 1);
+        if (kEpi) epi_table->init();
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -395,6 +559,11 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
         if (!kEpi || p.D != nullptr) prefetch_tmap(&tmD);
+        if constexpr (kEpi) {
+            if (p.Z != nullptr) prefetch_tmap(&p.tmZ);
+            if (p.Q != nullptr) prefetch_tmap(&p.tmQ);
+            if (p.residual != nullptr) prefetch_tmap(&p.tmR);
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, C::kTmemCols);
@@ -553,11 +722,20 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
         int slot = 0;
         uint32_t sphase = 0;
         const int row_limit = p.M;  // rows of sa that exist (dense M, M_total or M_max)
+        auto epi = [&] {
+            if constexpr (kEpi)
+                return EpiFetch<BN>{p, epi_table, sOut, false, false, 0, 0, 0, 0, 0u};
+            else
+                return 0;
+        }();
         Work w;
         for (int it = 0; next_work(p, tiles, it, w); ++it) {
             const Tile tl = decode_tile<BN, MODE>(p, w.t, m_blocks, mb_prefix);
             if (!tl.valid) continue;
             group_k_range<MODE>(p, tl, w);
+            if constexpr (kEpi) {
+                if (!epi.flush(sempty, lane, abort_flag)) break;
+            }
             const float* sa_base = p.sa + (MODE == kMasked ? static_cast<int64_t>(tl.g) * nkb * p.sa_stride : 0);
             const float* sb_g = p.sb + (MODE == kKGrouped ? 0 : static_cast<int64_t>(tl.g) * p.nbn * nkb);
             const int nb = tl.n0 / 128 + (lane & 3);
@@ -568,6 +746,10 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
             bool ok = true;
             for (int kg = w.kb0; kg < w.kb1; kg += kScaleGroup) {
                 if (!mbar_wait(sempty + slot, sphase ^ 1u, abort_flag)) { ok = false; break; }
+                if constexpr (kEpi) {
+                    if (epi.pending && slot == epi.slot) epi.send(lane);
+                    if (kg == w.kb0 && w.slice <= 0) epi.begin(tl, it, lane);
+                }
                 const int n = min(kScaleGroup, w.kb1 - kg);
                 for (int j = 0; j < n; ++j) {
                     const int kb = kg + j;
@@ -579,9 +761,16 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
                                    nb_ok ? 4u : 0u);
                 }
                 cp_async_arrive(sfull + slot);
+                if constexpr (kEpi) {
+                    if (kg == w.kb0 && w.slice <= 0) epi.want(tl, it, slot, sphase, lane);
+                }
                 if (++slot == kScaleGroups) { slot = 0; sphase ^= 1u; }
             }
             if (!ok) break;
+        }
+        if constexpr (kEpi) {
+            epi.flush(sempty, lane, abort_flag);
+            epi.end();
         }
         // Let every copy land before the CTA can exit.
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -646,7 +835,10 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
                 }
                 if (jg == kScaleGroup - 1 || kb == w.kb1 - 1) {
                     // The group's last K block has read its scales: release the slot.
+                    // (EpiParams calls: and the staging buffers, which the previous
+                    // tile's stores have long read.)
                     __syncwarp();
+                    if (kEpi && lane == 0) bulk_wait_read<0>();
                     if (lane == 0) mbar_arrive(sempty + slot);
                     if (++slot == kScaleGroups) { slot = 0; sphase ^= 1u; }
                 }
@@ -728,7 +920,7 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
             }
 
             if constexpr (kEpi) {
-                epilogue_store<BN, SP>(p, tmD, acc, tl, ew, quarter, lane, sOut + ew * SP * kStageOutBytes);
+                if (!EpiWarp<BN>(sOut, epi_table, tl).finish(p, tmD, acc, it, abort_flag)) { ok = false; break; }
                 continue;
             }
 
