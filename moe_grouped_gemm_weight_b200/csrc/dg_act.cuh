@@ -57,15 +57,34 @@ __device__ __forceinline__ float2 clamp2(float2 v, float lo, float hi) {
     return make_float2(min_nan(max_nan(v.x, lo), hi), min_nan(max_nan(v.y, lo), hi));
 }
 
-// sigmoid2 for any argument: below -126 the result is zero as at -126, which
-// keeps sigmoid2's exponent and what is left of it finite.
-__device__ __forceinline__ float2 sigmoid2_any(float2 g) { return sigmoid2(clamp2(g, -126.f, 88.f)); }
+// -min(|g|, 126) of a pair, -126 for a NaN.
+__device__ __forceinline__ float2 minus_abs2(float2 g) { return make_float2(fmaxf(-fabsf(g.x), -126.f), fmaxf(-fabsf(g.y), -126.f)); }
+// 1 / v of a pair by one reciprocal, where the product of the two stays within FP32.  Not
+// for a NaN, which would be its neighbour's too: callers bring it back with a factor.
+__device__ __forceinline__ float2 rcp_pair(float2 v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v.x * v.y));
+    return __fmul2_rn(pair(r), make_float2(v.y, v.x));
+}
 
-// s = sigmoid(g) and c = 1 - s, each to a few 2^-24 of its own value; -87 <= g <= 88.
-__device__ __forceinline__ void sigmoid_parts2(float2 g, float2& s, float2& c) {
-    const float2 e = exp_minus2(g);
-    s = rcp2(__fadd2_rn(e, pair(1.f)));
-    c = __fmul2_rn(e, s);
+// t = exp(-|g|) and r = 1 / (1 + t): sigmoid(g) is r for g >= 0, else t r, and 1 - sigmoid(g)
+// the other, each to a few 2^-24 of its own value (EXACT) or with |g| 2^-24 more, the
+// rounding of the exponent.  t is zero below 2^-126.  1 + t is at most 2, so one reciprocal
+// serves both of the pair: the special-function unit bounds the GEMM's epilogue.
+template <bool EXACT>
+__device__ __forceinline__ void sigmoid_parts2(float2 g, float2& t, float2& r) {
+    const float2 m = minus_abs2(g);
+    if (EXACT) {
+        t = exp_minus2(make_float2(-m.x, -m.y));
+    } else {
+        t = __fmul2_rn(m, pair(1.4426950408889634f));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.x));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.y));
+    }
+    r = rcp_pair(__fadd2_rn(t, pair(1.f)));
+}
+__device__ __forceinline__ float2 sigmoid_of_parts2(float2 g, float2 t, float2 r) {
+    return __fmul2_rn(r, make_float2(g.x < 0.f ? t.x : 1.f, g.y < 0.f ? t.y : 1.f));
 }
 
 // The two factors of the normal distribution's tail at |z|: q = exp(-z^2/2) R(|z|) =
@@ -77,7 +96,7 @@ __device__ __forceinline__ void sigmoid_parts2(float2 g, float2& s, float2& c) {
 __device__ __forceinline__ void normal_tail2(float2 z, float2& q, float2& ez) {
     constexpr float kC = -0.72134752044448170f;  // -log2(e) / 2
     constexpr float kCRest = static_cast<float>(-0.72134752044448170368 - kC);
-    const float2 x = make_float2(min_nan(fabsf(z.x), 14.5f), min_nan(fabsf(z.y), 14.5f));
+    const float2 x = make_float2(fminf(fabsf(z.x), 14.5f), fminf(fabsf(z.y), 14.5f));  // a NaN: 14.5
     const float2 a = __fmul2_rn(x, x), ra = __ffma2_rn(x, x, make_float2(-a.x, -a.y));
     ez = __fmul2_rn(a, pair(kC));
     float2 lo = __ffma2_rn(a, pair(kC), make_float2(-ez.x, -ez.y));
@@ -85,9 +104,7 @@ __device__ __forceinline__ void normal_tail2(float2 z, float2& q, float2& ez) {
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(ez.x));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(ez.y));
     ez = __fmul2_rn(ez, __ffma2_rn(lo, pair(0.6931471805599453f), pair(1.f)));
-    float2 t = __ffma2_rn(x, pair(0.3f), pair(1.f));
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t.x));
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t.y));
+    const float2 t = rcp_pair(__ffma2_rn(x, pair(0.3f), pair(1.f)));
     float2 r = pair(0.03840739652514458f);
     r = __ffma2_rn(r, t, pair(-0.16930747032165527f));
     r = __ffma2_rn(r, t, pair(0.22895179688930511f));
@@ -105,11 +122,11 @@ constexpr float kGeluTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 template <int ACT>
 __device__ __forceinline__ float2 act2(float2 z) {
     if constexpr (ACT == kActRelu) return make_float2(max_nan(z.x, 0.f), max_nan(z.y, 0.f));
-    if constexpr (ACT == kActSilu) return __fmul2_rn(z, sigmoid2_any(z));
-    if constexpr (ACT == kActGeluTanh) {
-        const float2 z2 = __fmul2_rn(z, z);
-        const float2 c = __ffma2_rn(z2, pair(kGeluTanhC * 0.044715f), pair(kGeluTanhC));
-        return __fmul2_rn(z, sigmoid2_any(__fmul2_rn(z, c)));
+    if constexpr (ACT == kActSilu || ACT == kActGeluTanh) {
+        float2 g = z, t, r;
+        if (ACT == kActGeluTanh) g = __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), pair(kGeluTanhC * 0.044715f), pair(kGeluTanhC)));
+        sigmoid_parts2<false>(g, t, r);
+        return __fmul2_rn(z, sigmoid_of_parts2(g, t, r));
     }
     if constexpr (ACT == kActGelu) {
         float2 q, e;
@@ -119,26 +136,23 @@ __device__ __forceinline__ float2 act2(float2 z) {
     return z;
 }
 
-// The activation's derivative.  Past |z| = 30 those of gelu_tanh and silu are 0 or 1
-// but for less than 2^-35; there the argument stays at 30 (silu: -87), which keeps
-// z^2 and z (1 - s) finite.
+// The activation's derivative, s (1 + z g'(z) (1 - s)) with s = sigmoid(g).  Past |z| = 126
+// (gelu_tanh: 30) those of gelu_tanh and silu are 0 or 1 but for less than 2^-100; there
+// the argument stays, which keeps z^2 and z (1 - s) finite.
 template <int ACT>
 __device__ __forceinline__ float2 act_slope2(float2 z) {
     if constexpr (ACT == kActRelu) return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
-    if constexpr (ACT == kActSilu) {
-        float2 s, c;
-        z = clamp2(z, -87.f, 88.f);
-        sigmoid_parts2(z, s, c);
-        return __fmul2_rn(s, __ffma2_rn(z, c, pair(1.f)));
-    }
-    if constexpr (ACT == kActGeluTanh) {
-        float2 s, c;
-        z = clamp2(z, -30.f, 30.f);
-        const float2 z2 = __fmul2_rn(z, z);
-        const float2 g = __fmul2_rn(z, __ffma2_rn(z2, pair(kGeluTanhC * 0.044715f), pair(kGeluTanhC)));
-        sigmoid_parts2(clamp2(g, -87.f, 88.f), s, c);
-        const float2 up = __ffma2_rn(z2, pair(kGeluTanhC * 3.f * 0.044715f), pair(kGeluTanhC));  // of the sigmoid's argument
-        return __fmul2_rn(s, __ffma2_rn(__fmul2_rn(z, up), c, pair(1.f)));
+    if constexpr (ACT == kActSilu || ACT == kActGeluTanh) {
+        z = ACT == kActSilu ? clamp2(z, -126.f, 126.f) : clamp2(z, -30.f, 30.f);
+        float2 g = z, up = z, t, r;  // up = z g'(z)
+        if (ACT == kActGeluTanh) {
+            const float2 z2 = __fmul2_rn(z, z);
+            g = __fmul2_rn(z, __ffma2_rn(z2, pair(kGeluTanhC * 0.044715f), pair(kGeluTanhC)));
+            up = __fmul2_rn(z, __ffma2_rn(z2, pair(kGeluTanhC * 3.f * 0.044715f), pair(kGeluTanhC)));
+        }
+        sigmoid_parts2<true>(g, t, r);
+        const float2 c = __fmul2_rn(r, make_float2(g.x < 0.f ? 1.f : t.x, g.y < 0.f ? 1.f : t.y));
+        return __fmul2_rn(sigmoid_of_parts2(g, t, r), __ffma2_rn(up, c, pair(1.f)));
     }
     if constexpr (ACT == kActGelu) {
         float2 q, e;

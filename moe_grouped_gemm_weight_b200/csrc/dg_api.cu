@@ -554,11 +554,30 @@ dg_status dispatch(const dg_plan& pl, const dg::Params& p, const CUtensorMap& ta
 // Calls with an epilogue of their own stage each promotion warp's whole share of a
 // tile, and give up ring stages for it: three for 128 x 256 tiles, which measured no
 // slower than four (4096 x 7168 x 16384 without an epilogue: 467 against 473 us).
+template <int BN, int ACT, bool RES>
+dg_status launch_epilogue_one(const dg_plan& pl, const dg::EpiParams& p, const CUtensorMap& ta, const CUtensorMap& tb,
+                              const CUtensorMap& td, cudaStream_t stream) {
+    constexpr int pieces = dg::Cfg<BN>::kColsPerWarp / 32, stages = BN == 256 ? kShortKStages : BN == 128 ? 5 : 8;
+    dg::EpiCall<ACT, RES> call;
+    static_cast<dg::EpiParams&>(call) = p;
+    return launch_one<BN, stages, dg::kDense, 0, pieces, dg::EpiCall<ACT, RES>>(call, ta, tb, td, pl.grid, stream);
+}
+template <int BN, int ACT>
+dg_status launch_epilogue_act(const dg_plan& pl, const dg::EpiParams& p, const CUtensorMap& ta, const CUtensorMap& tb,
+                              const CUtensorMap& td, cudaStream_t stream) {
+    return p.residual ? launch_epilogue_one<BN, ACT, true>(pl, p, ta, tb, td, stream)
+                      : launch_epilogue_one<BN, ACT, false>(pl, p, ta, tb, td, stream);
+}
 template <int BN>
 dg_status launch_epilogue(const dg_plan& pl, const dg::EpiParams& p, const CUtensorMap& ta, const CUtensorMap& tb,
                           const CUtensorMap& td, cudaStream_t stream) {
-    constexpr int pieces = dg::Cfg<BN>::kColsPerWarp / 32, stages = BN == 256 ? kShortKStages : BN == 128 ? 5 : 8;
-    return launch_one<BN, stages, dg::kDense, 0, pieces, dg::EpiParams>(p, ta, tb, td, pl.grid, stream);
+    switch (p.act) {
+        case dg::kActRelu: return launch_epilogue_act<BN, dg::kActRelu>(pl, p, ta, tb, td, stream);
+        case dg::kActGelu: return launch_epilogue_act<BN, dg::kActGelu>(pl, p, ta, tb, td, stream);
+        case dg::kActGeluTanh: return launch_epilogue_act<BN, dg::kActGeluTanh>(pl, p, ta, tb, td, stream);
+        case dg::kActSilu: return launch_epilogue_act<BN, dg::kActSilu>(pl, p, ta, tb, td, stream);
+        default: return launch_epilogue_act<BN, dg::kActNone>(pl, p, ta, tb, td, stream);
+    }
 }
 
 template <int LAYOUT>

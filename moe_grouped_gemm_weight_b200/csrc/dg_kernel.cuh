@@ -94,6 +94,13 @@ struct EpiParams : Params {
     int64_t sq_stride;
     int act;
 };
+// ... as a 128-row kernel's instance knows it: without the other activations and the
+// residual's code the K loop is compiled better (see EpiWarp).
+template <int ACT, bool RES>
+struct EpiCall : EpiParams {
+    static constexpr int kAct = ACT;
+    static constexpr bool kRes = RES;
+};
 
 // One unit of work of this CTA: a tile (index t) over K blocks [kb0, kb1);
 // slice = -1 for a whole tile, else the K slice of a split tail tile.
@@ -271,9 +278,10 @@ struct EpiTable {
 // are formed from the thread's index, read anew, and phases from the CTA's count of
 // tiles.  (With a handful of registers more each K block took 36 ns longer: 4096 x 4096 x
 // 7168 115 -> 122 us; asking for the residual from within the K loop spilled: 148 us.)
-template <int BN>
+template <int BN, typename PT>
 struct EpiWarp {
     using C = Cfg<BN>;
+    static constexpr int kAct = PT::kAct;
     static constexpr int kPieces = C::kColsPerWarp / 32;
 
     uint32_t lane, ew;
@@ -313,8 +321,7 @@ struct EpiWarp {
     }
 
     // acc of the CTA's it-th tile; false: a wait ran out.
-    template <int ACT>
-    __device__ __forceinline__ bool run(const EpiParams& p, const CUtensorMap& tmD, float2* acc, int it, volatile int* abort_flag) const {
+    __device__ __forceinline__ bool finish(const EpiParams& p, const CUtensorMap& tmD, float2* acc, int it, volatile int* abort_flag) const {
         if (p.bias != nullptr) {  // landed before the tile's first scales
             const uint32_t b0 = smem_u32(tb->bias[it % EpiTable<BN>::kBiasSlots]) + (ew >> 2) * (C::kColsPerWarp * 4);
 #pragma unroll
@@ -324,13 +331,13 @@ struct EpiWarp {
                 acc[2 * j + 1] = __fadd2_rn(acc[2 * j + 1], make_float2(__uint_as_float(b.z), __uint_as_float(b.w)));
             }
         }
-        const bool res = p.residual != nullptr && x < p.N;
+        const bool res = PT::kRes && x < p.N;
         if (p.Z != nullptr) {
             wait_stores();
 #pragma unroll
             for (int pc = 0; pc < kPieces; ++pc) store_piece(p, &p.tmZ, pc, acc + pc * 16);
             uint64_t* bar = tb->warp_full + ew;
-            if (p.residual != nullptr && !res && lane == 0) mbar_arrive(bar);  // a phase a tile, also without columns
+            if (PT::kRes && !res && lane == 0) mbar_arrive(bar);  // a phase a tile, also without columns
             if (res && lane == 0) {
                 bulk_wait_read<0>();
                 mbar_arrive_expect_tx(bar, static_cast<uint32_t>(min(kPieces, (p.N - x + 31) / 32) * kStageOutBytes));
@@ -340,9 +347,9 @@ struct EpiWarp {
                     if (x + pc * 32 < p.N) tma_load_2d(stage + pc * kStageOutBytes, &p.tmR, bar, x + pc * 32, row0, policy);
             }
         }
-        if (ACT != kActNone)
+        if (kAct != kActNone)
 #pragma unroll
-            for (int j = 0; j < C::kColsPerWarp / 2; ++j) acc[j] = act2<ACT>(acc[j]);
+            for (int j = 0; j < C::kColsPerWarp / 2; ++j) acc[j] = act2<kAct>(acc[j]);
         if (res) {
             uint64_t* bar = p.Z != nullptr ? tb->warp_full + ew : &tb->res_full;
             if (!mbar_wait(bar, it & 1, abort_flag)) {
@@ -408,16 +415,6 @@ struct EpiWarp {
             bulk_commit();
         }
         return true;
-    }
-
-    __device__ __forceinline__ bool finish(const EpiParams& p, const CUtensorMap& tmD, float2* acc, int it, volatile int* abort_flag) const {
-        switch (p.act) {
-            case kActRelu: return run<kActRelu>(p, tmD, acc, it, abort_flag);
-            case kActGelu: return run<kActGelu>(p, tmD, acc, it, abort_flag);
-            case kActGeluTanh: return run<kActGeluTanh>(p, tmD, acc, it, abort_flag);
-            case kActSilu: return run<kActSilu>(p, tmD, acc, it, abort_flag);
-            default: return run<kActNone>(p, tmD, acc, it, abort_flag);
-        }
     }
 };
 
@@ -838,7 +835,9 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
                     // (EpiParams calls: and the staging buffers, which the previous
                     // tile's stores have long read.)
                     __syncwarp();
-                    if (kEpi && lane == 0) bulk_wait_read<0>();
+                    if constexpr (kEpi) {
+                        if (PT::kRes && lane == 0) bulk_wait_read<0>();
+                    }
                     if (lane == 0) mbar_arrive(sempty + slot);
                     if (++slot == kScaleGroups) { slot = 0; sphase ^= 1u; }
                 }
@@ -920,7 +919,7 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
             }
 
             if constexpr (kEpi) {
-                if (!EpiWarp<BN>(sOut, epi_table, tl).finish(p, tmD, acc, it, abort_flag)) { ok = false; break; }
+                if (!EpiWarp<BN, PT>(sOut, epi_table, tl).finish(p, tmD, acc, it, abort_flag)) { ok = false; break; }
                 continue;
             }
 

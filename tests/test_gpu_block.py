@@ -103,11 +103,13 @@ def act64(z, act):
     g = C2 * (z + 0.044715 * z ** 3) if act == "gelu_tanh" else z
     up = C2 * (1 + 3 * 0.044715 * z * z) if act == "gelu_tanh" else torch.ones_like(z)
     s, c = torch.sigmoid(g), torch.sigmoid(-g)
-    # the sigmoid 8 units, and 4 roundings of its argument (gelu_tanh) times its slope
+    # the sigmoid 8 units, and 4 roundings of its argument (gelu_tanh) times its slope.  The value's exponent is one more
+    # product, rounded, with a constant: 1.3 |g| units of exp(-|g|), by which the sigmoid moves 1 - s as much
     rel = 8 + (4 * g.abs() * c if act == "gelu_tanh" else 0)
+    rel_v = rel + 1.3 * g.abs() * c
     rel_c = 8 + (4 * g.abs() * s if act == "gelu_tanh" else 0)
     value, slope = z * s, s + z * up * s * c
-    return value, slope, value.abs() * (rel + 2), (s * (rel + 2) + (z * up * s * c).abs() * (rel + rel_c + 6))
+    return value, slope, value.abs() * (rel_v + 2), (s * (rel + 2) + (z * up * s * c).abs() * (rel + rel_c + 6))
 
 
 # ------------------------------------------------------------------------------------ GEMM with an epilogue
@@ -206,7 +208,7 @@ def test_gemm_epilogue_adds_to_the_residual_in_place(dgm, M, N, K):
 @pytest.mark.parametrize("act", ACTS)
 def test_gemm_epilogue_extreme_values(dgm, M, act):
     G = Gemm(dgm, M, 256, 128, seed=3, residual=False)
-    special = [0.0, -0.0, 1e30, -1e30, 3e38, -3e38, 50.0, -50.0, 88.0, -88.0, -12.9, -13.4, -100.0, -127.0, NAN, INF, 1e-30, -5.0]
+    special = [0.0, -0.0, 1e30, -1e30, 3e38, -3e38, 50.0, -50.0, 88.0, -88.0, -12.9, -13.4, -100.0, -127.0, NAN, INF, 1e-30, -5.0, 1.5, NAN]
     G.B.view(torch.uint8).zero_()  # z is the bias
     G.bias = torch.zeros(256, device="cuda")
     G.bias[:len(special)] = torch.tensor(special, device="cuda")
@@ -245,6 +247,15 @@ def test_epilogue_gradient(dgm, M, N, act):
     dD = (0.02 * randn(g, M, N)).bfloat16()
     Z = (1.5 * randn(g, M, N)).bfloat16()
     Z[0, :10] = torch.tensor([0.0, -0.0, 40.0, -40.0, 88.0, -100.0, 1e30, -1e30, 13.5, -13.5], device="cuda").bfloat16()
+    if act not in ("none", "relu") and M > 1:  # a NaN is its own element's alone
+        one = Z.clone()
+        one[1, 4] = NAN
+        outs = [torch.zeros(M, N, dtype=torch.uint8, device="cuda"), torch.zeros(-(-M // 128) * 128, N, dtype=torch.uint8, device="cuda")]
+        dgm.dg_epilogue_bwd(outs[0], torch.zeros(N // BLOCK, M, device="cuda"), M, outs[1], torch.zeros(-(-M // 128), N, device="cuda"), N,
+                            dD, Z=one, act=number(dgm, act))
+        for q in outs:
+            nan = torch.nonzero((q & 0x7F) == 0x7F).tolist()
+            assert nan == [[1, 4]]
     R = -(-M // BLOCK) * BLOCK
     Qr, qr_ok = framed(M, N, dtype=torch.uint8)
     Qc, qc_ok = framed(R, N, dtype=torch.uint8)
