@@ -1029,8 +1029,24 @@ dg_status launch_route_bwd(const dg::RouteBwdParams& p, bool wide, int64_t grid,
     return launch_route_bwd_one<L, 32>(p, wide, grid, st);
 }
 
-// Threads of a norm kernel: a row's runs of 8 columns, `ch` to a thread.
-int norm_threads(int N, int ch) { return cdiv(cdiv(N / 8, ch), 32) * 32; }
+// Division of a norm kernel's CTA: rows of N columns, `slot` bytes of each in shared
+// memory, `rows` of them for each CTA of the grid, if there is one an SM.
+dg::NormPlan norm_plan(int N, uint32_t slot, int64_t rows) {
+    dg::NormPlan pl;
+    pl.threads = cdiv(cdiv(N / 8, dg::kNormRuns), 32) * 32;
+    pl.slot = (slot + 127) / 128 * 128;
+    int64_t groups = (N <= dg::kNormHeldColumns ? dg::kNormHeldThreads : dg::kNormMaxThreads) / pl.threads;
+    if (groups > dg::kNormMaxGroups) groups = dg::kNormMaxGroups;
+    if (groups > dg::kNormSmem / pl.slot) groups = dg::kNormSmem / pl.slot;
+    if (groups > rows) groups = rows;
+    pl.groups = groups < 1 ? 1 : static_cast<int>(groups);
+    int64_t depth = dg::kNormSmem / (static_cast<int64_t>(pl.slot) * pl.groups);
+    if (depth > dg::kNormMaxDepth) depth = dg::kNormMaxDepth;
+    const int64_t turns = cdiv64(rows, pl.groups);
+    if (depth > turns) depth = turns;
+    pl.depth = depth < 1 ? 1 : static_cast<int>(depth);
+    return pl;
+}
 
 dg_status check_norm(int T, int N, int dtype, float scale) {
     if (T < 0 || N <= 0) return fail(DG_ERR_INVALID_ARG, "bad sizes T=%d N=%d", T, N);
@@ -1107,17 +1123,18 @@ dg_status launch_balance_bwd(const dg::BalanceBwdParams& p, int64_t grid, void* 
 
 template <typename XT>
 dg_status launch_norm(const dg::NormParams& p, int64_t grid, void* st) {
-    const int ch = p.N / 8 <= dg::kNormMaxThreads ? 1 : 2;
-    const int threads = norm_threads(p.N, ch);
-    if (ch == 1) return launch_plain(dg::norm_residual_kernel<XT, 1>, p, grid, threads, 0, 1, st);
-    return launch_plain(dg::norm_residual_kernel<XT, 2>, p, grid, threads, 0, 1, st);
+    const int threads = p.plan.threads * p.plan.groups, smem = static_cast<int>(p.plan.slot) * p.plan.groups * p.plan.depth;
+    return launch_plain(p.N <= dg::kNormHeldColumns ? dg::norm_residual_kernel<XT, true> : dg::norm_residual_kernel<XT, false>, p,
+                        grid, threads, dg::kNormSharedBytes + smem, 1, st, dg::kNormSharedBytes + dg::kNormSmem);
 }
 template <typename XT>
 dg_status launch_norm_bwd(const dg::NormBwdParams& p, int64_t grid, void* st) {
-    const int ch = p.N / 8 <= dg::kNormMaxThreads ? 1 : 2;
-    const int threads = norm_threads(p.N, ch);
-    if (ch == 1) return launch_plain(dg::norm_residual_bwd_kernel<XT, 1>, p, grid, threads, 0, 1, st);
-    return launch_plain(dg::norm_residual_bwd_kernel<XT, 2>, p, grid, threads, 0, 1, st);
+    const int threads = p.plan.threads * p.plan.groups;
+    int smem = static_cast<int>(p.plan.slot) * p.plan.groups * p.plan.depth;
+    const int join = p.plan.groups > 1 ? p.plan.groups * 2 * p.N * 4 : 0;  // at most 8 KiB a 128 columns of 1024 threads
+    if (smem < join) smem = join;
+    return launch_plain(p.N <= dg::kNormHeldColumns ? dg::norm_residual_bwd_kernel<XT, true> : dg::norm_residual_bwd_kernel<XT, false>,
+                        p, grid, threads, dg::kNormSharedBytes + smem, 1, st, dg::kNormSharedBytes + dg::kNormSmem);
 }
 
 bool bad_act(int act) { return act < 0 || act >= dg::kActCount; }
@@ -1819,8 +1836,9 @@ dg_status dg_norm_residual(void* U, uint16_t* H, uint8_t* Q, float* sq, int sq_s
         return fail(DG_ERR_MISALIGNED, "tensors must be 16-byte aligned (rstd 8, sq and gate 4)");
     const int sms = effective_sms();
     if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
-    dg::NormParams p{U, H, Q, sq, rstd, X, Y, w_post, gate, w_pre, sq_stride, T, N, post_norm != 0, scale, eps};
-    const int64_t cap = static_cast<int64_t>(sms) * 4, grid = T < cap ? T : cap;
+    const int64_t grid = T < sms ? T : sms;
+    const dg::NormPlan pl = norm_plan(N, static_cast<uint32_t>(N) * (x_dtype == DG_DTYPE_BF16 ? 4 : 6), cdiv64(T, grid));
+    dg::NormParams p{pl, U, H, Q, sq, rstd, X, Y, w_post, gate, w_pre, sq_stride, T, N, post_norm != 0, scale, eps};
     return x_dtype == DG_DTYPE_BF16 ? launch_norm<uint16_t>(p, grid, stream) : launch_norm<float>(p, grid, stream);
 }
 
@@ -1851,7 +1869,8 @@ dg_status dg_norm_residual_bwd(void* dX, uint16_t* dY, float* dgate, float* dw_p
         grid = sms < dg::kNormMaxParts ? sms : dg::kNormMaxParts;
         if (grid > T) grid = T;
         float* pre = ws && dw_post ? ws + grid * N : ws;
-        dg::NormBwdParams p{dX, dY, dgate, dw_post ? ws : nullptr, dw_pre ? pre : nullptr, dU, dH, U, Y, rstd, w_post, gate,
+        const dg::NormPlan pl = norm_plan(N, static_cast<uint32_t>(N) * (x_dtype == DG_DTYPE_BF16 ? 8 : 12), cdiv64(T, grid));
+        dg::NormBwdParams p{pl, dX, dY, dgate, dw_post ? ws : nullptr, dw_pre ? pre : nullptr, dU, dH, U, Y, rstd, w_post, gate,
                             w_pre, T, N, post_norm != 0, scale};
         s = x_dtype == DG_DTYPE_BF16 ? launch_norm_bwd<uint16_t>(p, grid, stream) : launch_norm_bwd<float>(p, grid, stream);
         if (s != DG_OK) return s;

@@ -19,17 +19,36 @@
 namespace dg {
 
 constexpr int kNormMaxColumns = 16384;
+constexpr int kNormRuns = 2;         // runs of 8 columns a thread
+// Up to 8192 columns a CTA has 512 threads, which hold the weights of their columns in
+// registers; above, 1024, which load them for each row.  (The rows in flight leave L1 no
+// room for weights: with those loaded for each row, from L2, 8192 x 7168 FP32 rows took 194
+// us, the gradient 289.)
+constexpr int kNormHeldColumns = 8192;
+constexpr int kNormHeldThreads = 512;
 constexpr int kNormMaxThreads = 1024;
-constexpr int kNormMaxParts = 148;  // rows of partial weight gradients, at most
+constexpr int kNormMaxParts = 148;   // rows of partial weight gradients, at most
+constexpr int kNormMaxGroups = 15;   // rows at once in a CTA: each a named barrier
+constexpr int kNormMaxDepth = 4;     // rows in shared memory per group
+constexpr int kNormSmem = 212 * 1024;  // for them, at most: 16384 FP32 columns of the gradient take 192 KiB
 
-// Eight consecutive values of the residual stream, bf16 or FP32.
-__device__ __forceinline__ void load_f8(const uint16_t* p, F8& f) { bf16x8_to_f8(ld_once_16(p), f); }
-__device__ __forceinline__ void load_f8(const float* p, F8& f) {
-    const uint4 a = ld_once_16(p), b = ld_once_16(p + 4);
-    f[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
-    f[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
-    f[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
-    f[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+// Eight consecutive values in shared memory, bf16 or FP32.
+template <typename XT>
+__device__ __forceinline__ void shared_f8(uint32_t at, F8& f) {
+    const uint4 a = ld_shared_16(at);
+    if constexpr (sizeof(XT) == 2) {
+        bf16x8_to_f8(a, f);
+    } else {
+        const uint4 b = ld_shared_16(at + 16);
+        f[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+        f[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+        f[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+        f[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+}
+__device__ __forceinline__ void zero_f8(F8& f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(0.f, 0.f);
 }
 __device__ __forceinline__ void store_f8(uint16_t* p, const F8& f) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
@@ -52,6 +71,24 @@ __device__ __forceinline__ void load_weights(const float* w, int c, F8& f) {
     f[2] = make_float2(b.x, b.y);
     f[3] = make_float2(b.z, b.w);
 }
+// Weights of a thread's runs, held over all its rows or loaded for each.
+template <bool HELD>
+struct HeldWeights {
+    F8 w[HELD ? kNormRuns : 1];
+    __device__ __forceinline__ void load(const float* p, int tid, int threads, int runs) {
+        if constexpr (HELD)
+#pragma unroll
+            for (int j = 0; j < kNormRuns; ++j) load_weights(tid + j * threads < runs ? p : nullptr, (tid + j * threads) * 8, w[j]);
+    }
+    __device__ __forceinline__ void get(const float* p, int j, int run, F8& f) const {
+        if constexpr (HELD) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) f[x] = w[j][x];
+        } else {
+            load_weights(p, run * 8, f);
+        }
+    }
+};
 __device__ __forceinline__ float dot_f8(const F8& a, const F8& b, float s) {
     float2 d = make_float2(s, 0.f);
 #pragma unroll
@@ -59,29 +96,76 @@ __device__ __forceinline__ float dot_f8(const F8& a, const F8& b, float s) {
     return d.x + d.y;
 }
 
-// Sums of K values over the CTA, the same in every thread: warps first, then the
-// warps' sums in warp order.  `part` holds 32 K floats and is not written again
-// before the next but one call's barrier (callers alternate two of them).
-template <int K>
-__device__ __forceinline__ void cta_sum(float (&v)[K], float* part) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = (blockDim.x + 31) >> 5;
+// How a norm kernel's CTA is divided: `groups` of `threads` threads each, a row at a
+// time per group, `depth` rows of each group in shared memory.
+struct NormPlan {
+    int threads, groups, depth;
+    uint32_t slot;  // bytes of a row
+};
+
+// A group of threads that shares a row: its rows are those of worker blockIdx.x +
+// gridDim.x * group, of gridDim.x * groups workers.  Rows come by bulk copies, `depth`
+// rows ahead, which the group's first thread asks for.
+struct NormGroup {
+    const NormPlan& plan;
+    int group, tid, lane, warp, warps;
+    uint32_t ring;   // the group's slots
+    uint64_t* full;  // [depth]
+    int* abort_flag;
+
+    // Sums of K values over the group, the same in every thread: warps first, then the
+    // warps' sums in warp order.  `part` holds 32 K floats; it is written again only after
+    // another call's barrier.  Behind the call every thread has passed its start.
+    template <int K>
+    __device__ __forceinline__ void sum(float (&v)[K], float* part) const {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (lane == 0)
+            for (int o = 16; o >= 1; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        if (warps == 1) return;
+        if (lane == 0)
 #pragma unroll
-        for (int k = 0; k < K; ++k) part[k * 32 + warp] = v[k];
-    __syncthreads();
+            for (int k = 0; k < K; ++k) part[k * 32 + warp] = v[k];
+        barrier();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        v[k] = lane < warps ? part[k * 32 + lane] : 0.f;
+        for (int k = 0; k < K; ++k) {
+            v[k] = lane < warps ? part[k * 32 + lane] : 0.f;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            for (int o = 16; o >= 1; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        }
     }
+    __device__ __forceinline__ void barrier() const {
+        if (warps == 1) __syncwarp(); else named_barrier_sync(1 + group, plan.threads);
+    }
+    __device__ __forceinline__ uint32_t slot_at(int i) const { return ring + static_cast<uint32_t>(i % plan.depth) * plan.slot; }
+    // The group's i-th row has arrived.
+    __device__ __forceinline__ void wait(int i) const { mbar_wait(full + i % plan.depth, (i / plan.depth) & 1, abort_flag); }
+};
+
+struct NormShared {  // ahead of the rows
+    float part[kNormMaxGroups][2][3 * 32];
+    uint64_t full[kNormMaxGroups][kNormMaxDepth];
+    int abort_flag;
+};
+constexpr int kNormSharedBytes = (sizeof(NormShared) + 127) / 128 * 128;
+static_assert(kNormSharedBytes + kNormSmem <= 227 * 1024, "shared memory overflow");
+
+__device__ __forceinline__ NormGroup norm_group(const NormPlan& plan, NormShared& sh, uint8_t* smem) {
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        for (int g = 0; g < plan.groups; ++g)
+            for (int d = 0; d < plan.depth; ++d) mbar_init(&sh.full[g][d], 1);
+        sh.abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const int group = tid / plan.threads, mine = tid - group * plan.threads;
+    return {plan, group, mine, mine & 31, mine >> 5, plan.threads >> 5,
+            smem_u32(smem) + static_cast<uint32_t>(group * plan.depth) * plan.slot, sh.full[group], &sh.abort_flag};
 }
 
 struct NormParams {
+    NormPlan plan;
     void* U;               // [T][N] or null
     uint16_t* H;           // [T][N] or null
     uint8_t* Q;            // [T][N] or null, scales like dg_to_fp8_1x128's
@@ -98,28 +182,50 @@ struct NormParams {
     float scale, eps;
 };
 
-// One CTA a row at a time; thread i holds the runs of 8 columns i, i + threads,
-// ... of it, so a half-warp holds whole 1x128 tiles.
-template <typename XT, int CH>
-__global__ void __launch_bounds__(kNormMaxThreads)
-norm_residual_kernel(const NormParams p) {
-    __shared__ float part[4][32];
+// Thread i of a group holds the runs of 8 columns i, i + threads, ... of its row, so a
+// half-warp holds whole 1x128 tiles.
+template <typename XT, bool HELD>
+__global__ void __launch_bounds__(HELD ? kNormHeldThreads : kNormMaxThreads)
+norm_residual_kernel(const __grid_constant__ NormParams p) {
+    constexpr int CH = kNormRuns;
+    extern __shared__ __align__(128) uint8_t norm_smem[];
+    NormShared& sh = *reinterpret_cast<NormShared*>(norm_smem);
+    const NormGroup g = norm_group(p.plan, sh, norm_smem + kNormSharedBytes);
     griddep_wait();
     griddep_launch_dependents();
-    const int tid = threadIdx.x, runs = p.N / 8;
+    const int runs = p.N / 8, workers = gridDim.x * p.plan.groups;
+    const uint32_t y_at = p.N * static_cast<uint32_t>(sizeof(XT));  // in a slot, behind X's row
     const float inv_n = 1.f / static_cast<float>(p.N);
-    int turn = 0;
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
-        const int64_t row = static_cast<int64_t>(t) * p.N;
+    auto fetch = [&](int64_t t, int i) {
+        uint64_t* bar = g.full + i % p.plan.depth;
+        const uint32_t xb = p.X != nullptr ? y_at : 0, yb = p.Y != nullptr ? p.N * 2u : 0;
+        mbar_arrive_expect_tx(bar, xb + yb);
+        if (xb) bulk_load(g.slot_at(i), static_cast<const XT*>(p.X) + t * p.N, xb, bar);
+        if (yb) bulk_load(g.slot_at(i) + y_at, p.Y + t * p.N, yb, bar);
+    };
+    const int first = blockIdx.x + gridDim.x * g.group;
+    if (g.tid == 0)
+        for (int i = 0; i < p.plan.depth && first + static_cast<int64_t>(i) * workers < p.T; ++i)
+            fetch(first + static_cast<int64_t>(i) * workers, i);
+    HeldWeights<HELD> post, pre;
+    post.load(p.w_post, g.tid, p.plan.threads, runs);
+    pre.load(p.w_pre, g.tid, p.plan.threads, runs);
+    int i = 0;
+    for (int64_t t = first; t < p.T; t += workers, ++i) {
+        const int64_t row = t * p.N;
+        float* part = sh.part[g.group][i & 1];
+        const float gate = p.gate != nullptr ? p.gate[t] : 1.f;
+        g.wait(i);
+        const uint32_t at = g.slot_at(i);
         F8 u[CH], y[CH];
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int c = tid + i * blockDim.x;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) u[i][x] = y[i][x] = make_float2(0.f, 0.f);
+        for (int j = 0; j < CH; ++j) {
+            const int c = g.tid + j * p.plan.threads;
+            zero_f8(u[j]);
+            zero_f8(y[j]);
             if (c < runs) {
-                if (p.X != nullptr) load_f8(static_cast<const XT*>(p.X) + row + c * 8, u[i]);
-                if (p.Y != nullptr) load_f8(p.Y + row + c * 8, y[i]);
+                if (p.X != nullptr) shared_f8<XT>(at + c * 8 * sizeof(XT), u[j]);
+                if (p.Y != nullptr) shared_f8<uint16_t>(at + y_at + c * 16, y[j]);
             }
         }
         float ry = 1.f;
@@ -127,58 +233,64 @@ norm_residual_kernel(const NormParams p) {
             if (p.post_norm) {
                 float s[1] = {0.f};
 #pragma unroll
-                for (int i = 0; i < CH; ++i) s[0] = dot_f8(y[i], y[i], s[0]);
-                cta_sum<1>(s, part[2 * turn]);
+                for (int j = 0; j < CH; ++j) s[0] = dot_f8(y[j], y[j], s[0]);
+                g.sum<1>(s, part);
                 ry = __frsqrt_rn(fmaf(s[0], inv_n, p.eps));
             }
-            float k = p.scale * ry;
-            if (p.gate != nullptr) k *= p.gate[t];
+            const float k = p.scale * ry * gate;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = tid + i * blockDim.x;
+            for (int j = 0; j < CH; ++j) {
+                const int c = g.tid + j * p.plan.threads;
                 if (c >= runs) continue;
                 F8 w;
-                load_weights(p.w_post, c * 8, w);
+                post.get(p.w_post, j, c, w);
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    u[i][x] = __ffma2_rn(__fmul2_rn(y[i][x], make_float2(k, k)), w[x], u[i][x]);
+                    u[j][x] = __ffma2_rn(__fmul2_rn(y[j][x], make_float2(k, k)), w[x], u[j][x]);
             }
         }
         float s[1] = {0.f};
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            s[0] = dot_f8(u[i], u[i], s[0]);
-            const int c = tid + i * blockDim.x;
-            if (p.U != nullptr && c < runs) store_f8(static_cast<XT*>(p.U) + row + c * 8, u[i]);
-        }
-        cta_sum<1>(s, part[2 * turn + 1]);
+        for (int j = 0; j < CH; ++j) s[0] = dot_f8(u[j], u[j], s[0]);
+        g.sum<1>(s, part + 32);
+        // Every thread of the group has its values in registers: the slot is free.
+        if (g.tid == 0 && t + static_cast<int64_t>(p.plan.depth) * workers < p.T)
+            fetch(t + static_cast<int64_t>(p.plan.depth) * workers, i + p.plan.depth);
         const float ru = __frsqrt_rn(fmaf(s[0], inv_n, p.eps));
-        if (p.rstd != nullptr && tid == 0) *reinterpret_cast<float2*>(p.rstd + 2ll * t) = make_float2(ry, ru);
+        if (p.rstd != nullptr && g.tid == 0) *reinterpret_cast<float2*>(p.rstd + 2 * t) = make_float2(ry, ru);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int c = tid + i * blockDim.x;
-            F8 h, w;
-            if (c < runs) load_weights(p.w_pre, c * 8, w);
+        for (int j = 0; j < CH; ++j) {
+            const int c = g.tid + j * p.plan.threads;
+            F8 h;
+            zero_f8(h);
+            if (c < runs) {
+                F8 w;
+                if (p.U != nullptr) store_f8(static_cast<XT*>(p.U) + row + c * 8, u[j]);
+                pre.get(p.w_pre, j, c, w);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) h[x] = c < runs ? __fmul2_rn(__fmul2_rn(u[i][x], make_float2(ru, ru)), w[x]) : make_float2(0.f, 0.f);
-            if (p.H != nullptr && c < runs) store_f8(p.H + row + c * 8, h);
+                for (int x = 0; x < 4; ++x) h[x] = __fmul2_rn(__fmul2_rn(u[j][x], make_float2(ru, ru)), w[x]);
+                if (p.H != nullptr) store_f8(p.H + row + c * 8, h);
+            }
             if (p.Q != nullptr) {
+                __syncwarp();
                 float a = amax8(h);
 #pragma unroll
                 for (int o = 8; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
                 a = fmaxf(a, 1e-4f);
                 if (c < runs) {
                     *reinterpret_cast<uint2*>(p.Q + row + c * 8) = e4m3x8(h, __fdiv_rn(448.f, a));
-                    if ((tid & 15) == 0) p.sq[(c >> 4) * p.sq_stride + t] = __fdiv_rn(a, 448.f);
+                    if ((g.tid & 15) == 0) p.sq[(c >> 4) * p.sq_stride + t] = __fdiv_rn(a, 448.f);
                 }
             }
         }
+        __syncwarp();
     }
 }
 
 // ------------------------------------------------------------- backward ----
 
 struct NormBwdParams {
+    NormPlan plan;
     void* dX;              // [T][N] or null
     uint16_t* dY;          // [T][N] or null
     float* dgate;          // [T] or null
@@ -197,100 +309,155 @@ struct NormBwdParams {
     float scale;
 };
 
-// With a = u r_u and b = y r_y, both normalised rows:
-//   du = dU + r_u (w_pre dH - a mean(a w_pre dH)),  dX = du
+// With a = u r_u and b = y r_y, both normalised rows, and m = mean(a w_pre dH):
+//   e  = dU + r_u w_pre dH,  du = e - r_u m a,  dX = du
 //   d  = c gate du:  dw_post += d b,  dw_pre += dH a,  dgate = c sum(du w_post b)
 //   dY = r_y (w_post d - b mean(b w_post d)), or w_post d without the norm
-// One CTA a row at a time, thread layout as in the forward kernel; the weights'
-// gradients of a thread's columns stay in its registers until the last row.
-template <typename XT, int CH>
-__global__ void __launch_bounds__(kNormMaxThreads)
-norm_residual_bwd_kernel(const NormBwdParams p) {
-    __shared__ float part[4][32];
+// and sum(du w_post b) = sum(e w_post b) - r_u m sum(a w_post b), so that one pass over the
+// row gives all three sums and a second one, from shared memory, the results.  The weights'
+// gradients of a thread's columns stay in its registers until the last row; the groups'
+// are joined in order.
+template <typename XT, bool HELD>
+__global__ void __launch_bounds__(HELD ? kNormHeldThreads : kNormMaxThreads)
+norm_residual_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+    constexpr int CH = kNormRuns;
+    extern __shared__ __align__(128) uint8_t norm_smem[];
+    NormShared& sh = *reinterpret_cast<NormShared*>(norm_smem);
+    const NormGroup g = norm_group(p.plan, sh, norm_smem + kNormSharedBytes);
     griddep_wait();
     griddep_launch_dependents();
-    const int tid = threadIdx.x, runs = p.N / 8;
+    const int runs = p.N / 8, workers = gridDim.x * p.plan.groups;
+    const uint32_t xs = p.N * static_cast<uint32_t>(sizeof(XT)), ys = p.N * 2u;  // in a slot: dU, U, dH, Y
     const float inv_n = 1.f / static_cast<float>(p.N);
+    auto fetch = [&](int64_t t, int i) {
+        uint64_t* bar = g.full + i % p.plan.depth;
+        const uint32_t at = g.slot_at(i);
+        mbar_arrive_expect_tx(bar, (p.dU != nullptr ? xs : 0) + xs + (p.dH != nullptr ? ys : 0) + (p.Y != nullptr ? ys : 0));
+        if (p.dU != nullptr) bulk_load(at, static_cast<const XT*>(p.dU) + t * p.N, xs, bar);
+        bulk_load(at + xs, static_cast<const XT*>(p.U) + t * p.N, xs, bar);
+        if (p.dH != nullptr) bulk_load(at + 2 * xs, p.dH + t * p.N, ys, bar);
+        if (p.Y != nullptr) bulk_load(at + 2 * xs + ys, p.Y + t * p.N, ys, bar);
+    };
+    // Values of the thread's j-th run of the row in the slot: e, a, b, dH.
+    auto get = [&](uint32_t at, int c, float2 ru, float2 ry, F8& e, F8& a, F8& b, F8& h) {
+        zero_f8(e);
+        zero_f8(h);
+        zero_f8(b);
+        if (p.dU != nullptr) shared_f8<XT>(at + c * 8 * sizeof(XT), e);
+        shared_f8<XT>(at + xs + c * 8 * sizeof(XT), a);
+        if (p.dH != nullptr) shared_f8<uint16_t>(at + 2 * xs + c * 16, h);
+        if (p.Y != nullptr) shared_f8<uint16_t>(at + 2 * xs + ys + c * 16, b);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            a[x] = __fmul2_rn(a[x], ru);
+            b[x] = __fmul2_rn(b[x], ry);
+        }
+    };
+    HeldWeights<HELD> post, pre;
+    post.load(p.w_post, g.tid, p.plan.threads, runs);
+    pre.load(p.w_pre, g.tid, p.plan.threads, runs);
     F8 dpost[CH], dpre[CH];
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) dpost[i][x] = dpre[i][x] = make_float2(0.f, 0.f);
-    int turn = 0;
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
-        const int64_t row = static_cast<int64_t>(t) * p.N;
-        const float2 r = *reinterpret_cast<const float2*>(p.rstd + 2ll * t);
+    for (int j = 0; j < CH; ++j) {
+        zero_f8(dpost[j]);
+        zero_f8(dpre[j]);
+    }
+    const int first = blockIdx.x + gridDim.x * g.group;
+    if (g.tid == 0)
+        for (int i = 0; i < p.plan.depth && first + static_cast<int64_t>(i) * workers < p.T; ++i)
+            fetch(first + static_cast<int64_t>(i) * workers, i);
+    int i = 0;
+    for (int64_t t = first; t < p.T; t += workers, ++i) {
+        const int64_t row = t * p.N;
+        const float2 r = *reinterpret_cast<const float2*>(p.rstd + 2 * t);
         const float2 ry = make_float2(r.x, r.x), ru = make_float2(r.y, r.y);
         const float k = p.gate != nullptr ? p.scale * p.gate[t] : p.scale;
-        F8 d[CH], a[CH], b[CH], g[CH];
-        float s[1] = {0.f};
+        g.wait(i);
+        const uint32_t at = g.slot_at(i);
+        float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int c = tid + i * blockDim.x;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) d[i][x] = a[i][x] = b[i][x] = g[i][x] = make_float2(0.f, 0.f);
-            if (c < runs) {
-                if (p.dU != nullptr) load_f8(static_cast<const XT*>(p.dU) + row + c * 8, d[i]);
-                if (p.dH != nullptr) load_f8(p.dH + row + c * 8, g[i]);
-                load_f8(static_cast<const XT*>(p.U) + row + c * 8, a[i]);
-                if (p.Y != nullptr) load_f8(p.Y + row + c * 8, b[i]);
-                F8 w;
-                load_weights(p.w_pre, c * 8, w);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    a[i][x] = __fmul2_rn(a[i][x], ru);
-                    b[i][x] = __fmul2_rn(b[i][x], ry);
-                    dpre[i][x] = __ffma2_rn(g[i][x], a[i][x], dpre[i][x]);
-                    g[i][x] = __fmul2_rn(g[i][x], w[x]);
-                }
-                s[0] = dot_f8(a[i], g[i], s[0]);
-            }
-        }
-        cta_sum<1>(s, part[2 * turn]);
-        const float mean = s[0] * inv_n;
-        s[0] = 0.f;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int c = tid + i * blockDim.x;
+        for (int j = 0; j < CH; ++j) {
+            const int c = g.tid + j * p.plan.threads;
             if (c >= runs) continue;
-            F8 w;
-            load_weights(p.w_post, c * 8, w);
+            F8 e, a, b, h, w;
+            get(at, c, ru, ry, e, a, b, h);
+            pre.get(p.w_pre, j, c, w);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float2 in = __ffma2_rn(a[i][x], make_float2(-mean, -mean), g[i][x]);
-                d[i][x] = __ffma2_rn(ru, in, d[i][x]);
+                dpre[j][x] = __ffma2_rn(h[x], a[x], dpre[j][x]);
+                w[x] = __fmul2_rn(h[x], w[x]);
+                e[x] = __ffma2_rn(ru, w[x], e[x]);
             }
-            if (p.dX != nullptr) store_f8(static_cast<XT*>(p.dX) + row + c * 8, d[i]);
+            s[0] = dot_f8(a, w, s[0]);
+            if (p.Y == nullptr) continue;
+            post.get(p.w_post, j, c, w);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                dpost[i][x] = __ffma2_rn(__fmul2_rn(d[i][x], make_float2(k, k)), b[i][x], dpost[i][x]);
-                d[i][x] = __fmul2_rn(d[i][x], w[x]);
-            }
-            s[0] = dot_f8(d[i], b[i], s[0]);
+            for (int x = 0; x < 4; ++x) w[x] = __fmul2_rn(w[x], b[x]);
+            s[1] = dot_f8(e, w, s[1]);
+            s[2] = dot_f8(a, w, s[2]);
         }
-        if (p.Y == nullptr) continue;
-        cta_sum<1>(s, part[2 * turn + 1]);
-        if (p.dgate != nullptr && tid == 0) p.dgate[t] = p.scale * s[0];
-        if (p.dY == nullptr) continue;
-        const float sub = p.post_norm ? -s[0] * inv_n : 0.f;
+        g.sum<3>(s, sh.part[g.group][i & 1]);
+        const float rm = r.y * (s[0] * inv_n);
+        const float dot = fmaf(-rm, s[2], s[1]);
+        if (p.dgate != nullptr && g.tid == 0) p.dgate[t] = p.scale * dot;
+        const float sub = p.post_norm ? -dot * inv_n : 0.f;
         const float kr = k * r.x;  // r_y is 1 without the norm
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int c = tid + i * blockDim.x;
+        for (int j = 0; j < CH; ++j) {
+            const int c = g.tid + j * p.plan.threads;
             if (c >= runs) continue;
+            F8 e, a, b, h, w;
+            get(at, c, ru, ry, e, a, b, h);
+            pre.get(p.w_pre, j, c, w);
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                d[i][x] = __fmul2_rn(__ffma2_rn(b[i][x], make_float2(sub, sub), d[i][x]), make_float2(kr, kr));
-            store_f8(p.dY + row + c * 8, d[i]);
-        }
-    }
+                e[x] = __ffma2_rn(a[x], make_float2(-rm, -rm), __ffma2_rn(ru, __fmul2_rn(h[x], w[x]), e[x]));
+            if (p.dX != nullptr) store_f8(static_cast<XT*>(p.dX) + row + c * 8, e);
+            if (p.Y == nullptr) continue;
+            post.get(p.w_post, j, c, w);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = tid + i * blockDim.x;
+            for (int x = 0; x < 4; ++x) {
+                dpost[j][x] = __ffma2_rn(__fmul2_rn(e[x], make_float2(k, k)), b[x], dpost[j][x]);
+                e[x] = __fmul2_rn(__ffma2_rn(b[x], make_float2(sub, sub), __fmul2_rn(e[x], w[x])), make_float2(kr, kr));
+            }
+            if (p.dY != nullptr) store_f8(p.dY + row + c * 8, e);
+        }
+        g.barrier();  // the slot is free
+        if (g.tid == 0 && t + static_cast<int64_t>(p.plan.depth) * workers < p.T)
+            fetch(t + static_cast<int64_t>(p.plan.depth) * workers, i + p.plan.depth);
+    }
+    if (p.part_post == nullptr && p.part_pre == nullptr) return;
+    // The groups' sums, in group order.
+    float* joined = reinterpret_cast<float*>(norm_smem + kNormSharedBytes);  // [groups][2][N]
+    if (p.plan.groups > 1) {
+        __syncthreads();  // no group still reads its rows
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = g.tid + j * p.plan.threads;
+            if (c >= runs || g.group == 0) continue;
+            store_f8(joined + (2 * g.group) * p.N + c * 8, dpost[j]);
+            store_f8(joined + (2 * g.group + 1) * p.N + c * 8, dpre[j]);
+        }
+        __syncthreads();
+    }
+    if (g.group != 0) return;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        const int c = g.tid + j * p.plan.threads;
         if (c >= runs) continue;
+        for (int o = 1; o < p.plan.groups; ++o) {
+            F8 a, b;
+            shared_f8<float>(smem_u32(joined) + ((2 * o) * p.N + c * 8) * 4, a);
+            shared_f8<float>(smem_u32(joined) + ((2 * o + 1) * p.N + c * 8) * 4, b);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                dpost[j][x] = __fadd2_rn(dpost[j][x], a[x]);
+                dpre[j][x] = __fadd2_rn(dpre[j][x], b[x]);
+            }
+        }
         const int64_t at = static_cast<int64_t>(blockIdx.x) * p.N + c * 8;
-        if (p.part_post != nullptr) store_f8(p.part_post + at, dpost[i]);
-        if (p.part_pre != nullptr) store_f8(p.part_pre + at, dpre[i]);
+        if (p.part_post != nullptr) store_f8(p.part_post + at, dpost[j]);
+        if (p.part_pre != nullptr) store_f8(p.part_pre + at, dpre[j]);
     }
 }
 

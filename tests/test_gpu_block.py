@@ -449,8 +449,13 @@ class NormGrad:
         self.npre = (steps + 2) * U * (dH * a).abs().sum(dim=0)
         self.dw_post = (d * b).sum(dim=0)
         self.npost = (k * b).abs().mul(ndu).sum(dim=0) + (steps + 4) * U * (d * b).abs().sum(dim=0)
-        dot, dsize = (self.du * wp * b).sum(dim=1), (self.du * wp * b).abs().sum(dim=1)
-        ndot = ((wp * b).abs() * ndu).sum(dim=1) + (ROW + 4) * U * dsize
+        # sum(du w b) as sum(e w b) - r m sum(a w b), e = dU + r w_pre dH: each a row's sum of terms with 5 roundings, then r m
+        # with the mean's error and two roundings, and their difference
+        e, rm, wb = dU + ru * g, ru * mean, wp * b
+        dot = (self.du * wb).sum(dim=1)
+        left, right = (e * wb).abs().sum(dim=1), (a * wb).abs().sum(dim=1)
+        ndot = (ROW + 5) * U * (left + rm[:, 0].abs() * right) + ((ROW + 4) * ru * size)[:, 0] * U * right + 3 * U * (left + rm[:, 0].abs() * right)
+        del e, wb
         self.dgate, self.ngate = n.scale * dot, n.scale * ndot + U * (n.scale * dot).abs()
         self.dY = wp * d
         self.ny = wp.abs() * k.abs() * ndu + 3 * U * self.dY.abs()
