@@ -1033,7 +1033,7 @@ dg_status launch_route_bwd(const dg::RouteBwdParams& p, bool wide, int64_t grid,
 // memory, `rows` of them for each CTA of the grid, if there is one an SM.
 dg::NormPlan norm_plan(int N, uint32_t slot, int64_t rows) {
     dg::NormPlan pl;
-    pl.threads = cdiv(cdiv(N / 8, dg::kNormRuns), 32) * 32;
+    pl.threads = cdiv(cdiv(N / 4, dg::kNormRuns), 32) * 32;
     pl.slot = (slot + 127) / 128 * 128;
     int64_t groups = (N <= dg::kNormHeldColumns ? dg::kNormHeldThreads : dg::kNormMaxThreads) / pl.threads;
     if (groups > dg::kNormMaxGroups) groups = dg::kNormMaxGroups;

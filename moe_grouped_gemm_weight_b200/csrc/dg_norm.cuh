@@ -15,11 +15,12 @@
 #include "dg_cast.cuh"
 #include "dg_moe.cuh"
 #include "dg_ptx.cuh"
+#include "dg_route.cuh"
 
 namespace dg {
 
 constexpr int kNormMaxColumns = 16384;
-constexpr int kNormRuns = 2;         // runs of 8 columns a thread
+constexpr int kNormRuns = 4;         // runs of 4 columns a thread
 // Up to 8192 columns a CTA has 512 threads, which hold the weights of their columns in
 // registers; above, 1024, which load them for each row.  (The rows in flight leave L1 no
 // room for weights: with those loaded for each row, from L2, 8192 x 7168 FP32 rows took 194
@@ -32,114 +33,64 @@ constexpr int kNormMaxGroups = 15;   // rows at once in a CTA: each a named barr
 constexpr int kNormMaxDepth = 4;     // rows in shared memory per group
 constexpr int kNormSmem = 212 * 1024;  // for them, at most: 16384 FP32 columns of the gradient take 192 KiB
 
-// Eight consecutive values in shared memory, bf16 or FP32.
+// Four consecutive values as two pairs.
+using F4 = float2[2];
+
+__device__ __forceinline__ void zero_f4(F4& f) { f[0] = f[1] = make_float2(0.f, 0.f); }
+// From shared memory, bf16 or FP32.
 template <typename XT>
-__device__ __forceinline__ void shared_f8(uint32_t at, F8& f) {
-    const uint4 a = ld_shared_16(at);
+__device__ __forceinline__ void shared_f4(uint32_t at, F4& f) {
     if constexpr (sizeof(XT) == 2) {
-        bf16x8_to_f8(a, f);
+        uint2 v;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+        f[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+        f[1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
     } else {
-        const uint4 b = ld_shared_16(at + 16);
-        f[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
-        f[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
-        f[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
-        f[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+        const uint4 v = ld_shared_16(at);
+        f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
     }
 }
-__device__ __forceinline__ void zero_f8(F8& f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = make_float2(0.f, 0.f);
+__device__ __forceinline__ void store_f4(uint16_t* p, const F4& f) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y));
 }
-__device__ __forceinline__ void store_f8(uint16_t* p, const F8& f) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
-                                              pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
-}
-__device__ __forceinline__ void store_f8(float* p, const F8& f) {
+__device__ __forceinline__ void store_f4(float* p, const F4& f) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
 }
-// Eight weights of a column run, ones without any.
-__device__ __forceinline__ void load_weights(const float* w, int c, F8& f) {
-    if (w == nullptr) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = make_float2(1.f, 1.f);
-        return;
-    }
-    const float4 a = *reinterpret_cast<const float4*>(w + c), b = *reinterpret_cast<const float4*>(w + c + 4);
-    f[0] = make_float2(a.x, a.y);
-    f[1] = make_float2(a.z, a.w);
-    f[2] = make_float2(b.x, b.y);
-    f[3] = make_float2(b.z, b.w);
+__device__ __forceinline__ float dot_f4(const F4& a, const F4& b, float s) {
+    const float2 d = __ffma2_rn(a[1], b[1], __ffma2_rn(a[0], b[0], make_float2(s, 0.f)));
+    return d.x + d.y;
+}
+// Four weights, ones without any.
+__device__ __forceinline__ void load_weights(const float* w, int run, F4& f) {
+    const float4 v = w != nullptr ? *reinterpret_cast<const float4*>(w + run * 4) : make_float4(1.f, 1.f, 1.f, 1.f);
+    f[0] = make_float2(v.x, v.y);
+    f[1] = make_float2(v.z, v.w);
 }
 // Weights of a thread's runs, held over all its rows or loaded for each.
 template <bool HELD>
-struct HeldWeights {
-    F8 w[HELD ? kNormRuns : 1];
+struct NormWeights {
+    F4 w[HELD ? kNormRuns : 1];
     __device__ __forceinline__ void load(const float* p, int tid, int threads, int runs) {
         if constexpr (HELD)
 #pragma unroll
-            for (int j = 0; j < kNormRuns; ++j) load_weights(tid + j * threads < runs ? p : nullptr, (tid + j * threads) * 8, w[j]);
+            for (int j = 0; j < kNormRuns; ++j) load_weights(tid + j * threads < runs ? p : nullptr, tid + j * threads, w[j]);
     }
-    __device__ __forceinline__ void get(const float* p, int j, int run, F8& f) const {
+    __device__ __forceinline__ void get(const float* p, int j, int run, F4& f) const {
         if constexpr (HELD) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) f[x] = w[j][x];
+            f[0] = w[j][0];
+            f[1] = w[j][1];
         } else {
-            load_weights(p, run * 8, f);
+            load_weights(p, run, f);
         }
     }
 };
-__device__ __forceinline__ float dot_f8(const F8& a, const F8& b, float s) {
-    float2 d = make_float2(s, 0.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d = __ffma2_rn(a[i], b[i], d);
-    return d.x + d.y;
-}
 
 // How a norm kernel's CTA is divided: `groups` of `threads` threads each, a row at a
 // time per group, `depth` rows of each group in shared memory.
 struct NormPlan {
     int threads, groups, depth;
     uint32_t slot;  // bytes of a row
-};
-
-// A group of threads that shares a row: its rows are those of worker blockIdx.x +
-// gridDim.x * group, of gridDim.x * groups workers.  Rows come by bulk copies, `depth`
-// rows ahead, which the group's first thread asks for.
-struct NormGroup {
-    const NormPlan& plan;
-    int group, tid, lane, warp, warps;
-    uint32_t ring;   // the group's slots
-    uint64_t* full;  // [depth]
-    int* abort_flag;
-
-    // Sums of K values over the group, the same in every thread: warps first, then the
-    // warps' sums in warp order.  `part` holds 32 K floats; it is written again only after
-    // another call's barrier.  Behind the call every thread has passed its start.
-    template <int K>
-    __device__ __forceinline__ void sum(float (&v)[K], float* part) const {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-        if (warps == 1) return;
-        if (lane == 0)
-#pragma unroll
-            for (int k = 0; k < K; ++k) part[k * 32 + warp] = v[k];
-        barrier();
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            v[k] = lane < warps ? part[k * 32 + lane] : 0.f;
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-        }
-    }
-    __device__ __forceinline__ void barrier() const {
-        if (warps == 1) __syncwarp(); else named_barrier_sync(1 + group, plan.threads);
-    }
-    __device__ __forceinline__ uint32_t slot_at(int i) const { return ring + static_cast<uint32_t>(i % plan.depth) * plan.slot; }
-    // The group's i-th row has arrived.
-    __device__ __forceinline__ void wait(int i) const { mbar_wait(full + i % plan.depth, (i / plan.depth) & 1, abort_flag); }
 };
 
 struct NormShared {  // ahead of the rows
@@ -150,19 +101,73 @@ struct NormShared {  // ahead of the rows
 constexpr int kNormSharedBytes = (sizeof(NormShared) + 127) / 128 * 128;
 static_assert(kNormSharedBytes + kNormSmem <= 227 * 1024, "shared memory overflow");
 
-__device__ __forceinline__ NormGroup norm_group(const NormPlan& plan, NormShared& sh, uint8_t* smem) {
-    const int tid = threadIdx.x;
-    if (tid == 0) {
-        for (int g = 0; g < plan.groups; ++g)
-            for (int d = 0; d < plan.depth; ++d) mbar_init(&sh.full[g][d], 1);
-        sh.abort_flag = 0;
-        fence_mbar_init();
+// A group of threads that shares a row: its rows are those of worker blockIdx.x +
+// gridDim.x * group, of gridDim.x * groups workers.  Rows come by bulk copies, `depth`
+// rows ahead, which the group's first thread asks for.
+struct NormGroup {
+    int tid, lane, warp, warps, group, threads, depth;
+    uint32_t ring, slot_bytes;  // the group's slots
+    uint64_t* full;             // [depth]
+    int* abort_flag;
+    int slot;                   // of the row at hand
+    uint32_t phase, turn;
+
+    __device__ __forceinline__ NormGroup(const NormPlan& plan, NormShared& sh, uint8_t* rows) {
+        if (threadIdx.x == 0) {
+            for (int g = 0; g < plan.groups; ++g)
+                for (int d = 0; d < plan.depth; ++d) mbar_init(&sh.full[g][d], 1);
+            sh.abort_flag = 0;
+            fence_mbar_init();
+        }
+        __syncthreads();
+        group = threadIdx.x / plan.threads;
+        tid = threadIdx.x - group * plan.threads;
+        lane = tid & 31;
+        warp = tid >> 5;
+        warps = plan.threads >> 5;
+        threads = plan.threads;
+        depth = plan.depth;
+        slot_bytes = plan.slot;
+        ring = smem_u32(rows) + static_cast<uint32_t>(group * plan.depth) * plan.slot;
+        full = sh.full[group];
+        abort_flag = &sh.abort_flag;
+        slot = 0;
+        phase = turn = 0;
     }
-    __syncthreads();
-    const int group = tid / plan.threads, mine = tid - group * plan.threads;
-    return {plan, group, mine, mine & 31, mine >> 5, plan.threads >> 5,
-            smem_u32(smem) + static_cast<uint32_t>(group * plan.depth) * plan.slot, sh.full[group], &sh.abort_flag};
-}
+    // Sums of K values over the group, the same in every thread: warps first, then the
+    // warps' sums in warp order.  `part` holds 32 K floats; it is written again only after
+    // another call's barrier.  Behind the call every thread has passed its start.
+    template <int K>
+    __device__ __forceinline__ void sum(float (&v)[K], float* part) const {
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        if (warps == 1) return;
+        if (lane == 0)
+#pragma unroll
+            for (int k = 0; k < K; ++k) part[k * 32 + warp] = v[k];
+        barrier();
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = lane < warps ? part[k * 32 + lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
+    __device__ __forceinline__ void barrier() const {
+        if (warps == 1) __syncwarp(); else named_barrier_sync(1 + group, threads);
+    }
+    __device__ __forceinline__ uint32_t at() const { return ring + static_cast<uint32_t>(slot) * slot_bytes; }
+    __device__ __forceinline__ void wait() const { mbar_wait(full + slot, phase, abort_flag); }  // the row has arrived
+    __device__ __forceinline__ void next() {
+        if (++slot == depth) {
+            slot = 0;
+            phase ^= 1;
+        }
+        turn ^= 1;
+    }
+};
 
 struct NormParams {
     NormPlan plan;
@@ -182,50 +187,53 @@ struct NormParams {
     float scale, eps;
 };
 
-// Thread i of a group holds the runs of 8 columns i, i + threads, ... of its row, so a
-// half-warp holds whole 1x128 tiles.
+// Thread i of a group holds the runs of 4 columns i, i + threads, ... of its row: a warp
+// holds whole 1x128 tiles, and reads and writes whole lines.  Bound by HBM.
 template <typename XT, bool HELD>
 __global__ void __launch_bounds__(HELD ? kNormHeldThreads : kNormMaxThreads)
 norm_residual_kernel(const __grid_constant__ NormParams p) {
     constexpr int CH = kNormRuns;
     extern __shared__ __align__(128) uint8_t norm_smem[];
     NormShared& sh = *reinterpret_cast<NormShared*>(norm_smem);
-    const NormGroup g = norm_group(p.plan, sh, norm_smem + kNormSharedBytes);
+    NormGroup g(p.plan, sh, norm_smem + kNormSharedBytes);
     griddep_wait();
     griddep_launch_dependents();
-    const int runs = p.N / 8, workers = gridDim.x * p.plan.groups;
+    const int runs = p.N / 4, workers = gridDim.x * p.plan.groups;
     const uint32_t y_at = p.N * static_cast<uint32_t>(sizeof(XT));  // in a slot, behind X's row
     const float inv_n = 1.f / static_cast<float>(p.N);
-    auto fetch = [&](int64_t t, int i) {
-        uint64_t* bar = g.full + i % p.plan.depth;
+    auto fetch = [&](int64_t t, int slot) {
+        uint64_t* bar = g.full + slot;
         const uint32_t xb = p.X != nullptr ? y_at : 0, yb = p.Y != nullptr ? p.N * 2u : 0;
+        const uint32_t to = g.ring + static_cast<uint32_t>(slot) * g.slot_bytes;
         mbar_arrive_expect_tx(bar, xb + yb);
-        if (xb) bulk_load(g.slot_at(i), static_cast<const XT*>(p.X) + t * p.N, xb, bar);
-        if (yb) bulk_load(g.slot_at(i) + y_at, p.Y + t * p.N, yb, bar);
+        if (xb) bulk_load(to, static_cast<const XT*>(p.X) + t * p.N, xb, bar);
+        if (yb) bulk_load(to + y_at, p.Y + t * p.N, yb, bar);
     };
-    const int first = blockIdx.x + gridDim.x * g.group;
+    int64_t t = blockIdx.x + static_cast<int64_t>(gridDim.x) * g.group;
+    const int64_t ahead = static_cast<int64_t>(p.plan.depth) * workers;
     if (g.tid == 0)
-        for (int i = 0; i < p.plan.depth && first + static_cast<int64_t>(i) * workers < p.T; ++i)
-            fetch(first + static_cast<int64_t>(i) * workers, i);
-    HeldWeights<HELD> post, pre;
-    post.load(p.w_post, g.tid, p.plan.threads, runs);
-    pre.load(p.w_pre, g.tid, p.plan.threads, runs);
-    int i = 0;
-    for (int64_t t = first; t < p.T; t += workers, ++i) {
+        for (int i = 0; i < p.plan.depth && t + static_cast<int64_t>(i) * workers < p.T; ++i)
+            fetch(t + static_cast<int64_t>(i) * workers, i);
+    NormWeights<HELD> post, pre;
+    post.load(p.w_post, g.tid, g.threads, runs);
+    pre.load(p.w_pre, g.tid, g.threads, runs);
+    float gate = p.gate != nullptr && t < p.T ? p.gate[t] : 1.f;
+    for (; t < p.T; t += workers) {
         const int64_t row = t * p.N;
-        float* part = sh.part[g.group][i & 1];
-        const float gate = p.gate != nullptr ? p.gate[t] : 1.f;
-        g.wait(i);
-        const uint32_t at = g.slot_at(i);
-        F8 u[CH], y[CH];
+        float* part = sh.part[g.group][g.turn];
+        const float k0 = p.scale * gate;
+        if (p.gate != nullptr && t + workers < p.T) gate = p.gate[t + workers];  // the next row's, on its way meanwhile
+        g.wait();
+        const uint32_t at = g.at();
+        F4 u[CH], y[CH];
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = g.tid + j * p.plan.threads;
-            zero_f8(u[j]);
-            zero_f8(y[j]);
+            const int c = g.tid + j * g.threads;
+            zero_f4(u[j]);
+            zero_f4(y[j]);
             if (c < runs) {
-                if (p.X != nullptr) shared_f8<XT>(at + c * 8 * sizeof(XT), u[j]);
-                if (p.Y != nullptr) shared_f8<uint16_t>(at + y_at + c * 16, y[j]);
+                if (p.X != nullptr) shared_f4<XT>(at + c * 4 * sizeof(XT), u[j]);
+                if (p.Y != nullptr) shared_f4<uint16_t>(at + y_at + c * 8, y[j]);
             }
         }
         float ry = 1.f;
@@ -233,57 +241,70 @@ norm_residual_kernel(const __grid_constant__ NormParams p) {
             if (p.post_norm) {
                 float s[1] = {0.f};
 #pragma unroll
-                for (int j = 0; j < CH; ++j) s[0] = dot_f8(y[j], y[j], s[0]);
+                for (int j = 0; j < CH; ++j) s[0] = dot_f4(y[j], y[j], s[0]);
                 g.sum<1>(s, part);
                 ry = __frsqrt_rn(fmaf(s[0], inv_n, p.eps));
             }
-            const float k = p.scale * ry * gate;
+            const float k = k0 * ry;
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const int c = g.tid + j * p.plan.threads;
-                if (c >= runs) continue;
-                F8 w;
+                const int c = g.tid + j * g.threads;
+                if (!HELD && c >= runs) continue;
+                F4 w;
                 post.get(p.w_post, j, c, w);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+                for (int x = 0; x < 2; ++x)
                     u[j][x] = __ffma2_rn(__fmul2_rn(y[j][x], make_float2(k, k)), w[x], u[j][x]);
             }
         }
         float s[1] = {0.f};
 #pragma unroll
-        for (int j = 0; j < CH; ++j) s[0] = dot_f8(u[j], u[j], s[0]);
+        for (int j = 0; j < CH; ++j) s[0] = dot_f4(u[j], u[j], s[0]);
         g.sum<1>(s, part + 32);
         // Every thread of the group has its values in registers: the slot is free.
-        if (g.tid == 0 && t + static_cast<int64_t>(p.plan.depth) * workers < p.T)
-            fetch(t + static_cast<int64_t>(p.plan.depth) * workers, i + p.plan.depth);
+        if (g.tid == 0 && t + ahead < p.T) fetch(t + ahead, g.slot);
         const float ru = __frsqrt_rn(fmaf(s[0], inv_n, p.eps));
         if (p.rstd != nullptr && g.tid == 0) *reinterpret_cast<float2*>(p.rstd + 2 * t) = make_float2(ry, ru);
+        if (p.U != nullptr) {
+            XT* to = static_cast<XT*>(p.U) + row;
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                if (g.tid + j * g.threads < runs) store_f4(to + (g.tid + j * g.threads) * 4, u[j]);
+        }
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = g.tid + j * p.plan.threads;
-            F8 h;
-            zero_f8(h);
-            if (c < runs) {
-                F8 w;
-                if (p.U != nullptr) store_f8(static_cast<XT*>(p.U) + row + c * 8, u[j]);
+            const int c = g.tid + j * g.threads;
+            F4 w;
+            if (HELD || c < runs) {
                 pre.get(p.w_pre, j, c, w);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) h[x] = __fmul2_rn(__fmul2_rn(u[j][x], make_float2(ru, ru)), w[x]);
-                if (p.H != nullptr) store_f8(p.H + row + c * 8, h);
+                for (int x = 0; x < 2; ++x) u[j][x] = __fmul2_rn(__fmul2_rn(u[j][x], make_float2(ru, ru)), w[x]);
             }
-            if (p.Q != nullptr) {
-                __syncwarp();
-                float a = amax8(h);
+        }
+        if (p.H != nullptr) {
 #pragma unroll
-                for (int o = 8; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                a = fmaxf(a, 1e-4f);
-                if (c < runs) {
-                    *reinterpret_cast<uint2*>(p.Q + row + c * 8) = e4m3x8(h, __fdiv_rn(448.f, a));
-                    if ((g.tid & 15) == 0) p.sq[(c >> 4) * p.sq_stride + t] = __fdiv_rn(a, 448.f);
-                }
+            for (int j = 0; j < CH; ++j)
+                if (g.tid + j * g.threads < runs) store_f4(p.H + row + (g.tid + j * g.threads) * 4, u[j]);
+        }
+        if (p.Q != nullptr) {
+            float a[CH];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) a[j] = amax3(amax3(0.f, u[j][0].x, u[j][0].y), u[j][1].x, u[j][1].y);
+#pragma unroll
+            for (int j = 0; j < CH; ++j) a[j] = fmaxf(warp_max(a[j]), 1e-4f);
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const int c = g.tid + j * g.threads;
+                if (c >= runs) continue;  // whole warps
+                const float r = __fdiv_rn(448.f, a[j]);
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(__fmul2_rn(u[j][0], make_float2(r, r)), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(__fmul2_rn(u[j][1], make_float2(r, r)), __NV_SATFINITE, __NV_E4M3);
+                *reinterpret_cast<uint32_t*>(p.Q + row + c * 4) = __byte_perm(lo, hi, 0x5410);
+                if (g.lane == 0) p.sq[(c >> 5) * p.sq_stride + t] = __fdiv_rn(a[j], 448.f);
             }
         }
         __syncwarp();
+        g.next();
     }
 }
 
@@ -323,80 +344,80 @@ norm_residual_bwd_kernel(const __grid_constant__ NormBwdParams p) {
     constexpr int CH = kNormRuns;
     extern __shared__ __align__(128) uint8_t norm_smem[];
     NormShared& sh = *reinterpret_cast<NormShared*>(norm_smem);
-    const NormGroup g = norm_group(p.plan, sh, norm_smem + kNormSharedBytes);
+    NormGroup g(p.plan, sh, norm_smem + kNormSharedBytes);
     griddep_wait();
     griddep_launch_dependents();
-    const int runs = p.N / 8, workers = gridDim.x * p.plan.groups;
+    const int runs = p.N / 4, workers = gridDim.x * p.plan.groups;
     const uint32_t xs = p.N * static_cast<uint32_t>(sizeof(XT)), ys = p.N * 2u;  // in a slot: dU, U, dH, Y
     const float inv_n = 1.f / static_cast<float>(p.N);
-    auto fetch = [&](int64_t t, int i) {
-        uint64_t* bar = g.full + i % p.plan.depth;
-        const uint32_t at = g.slot_at(i);
+    auto fetch = [&](int64_t t, int slot) {
+        uint64_t* bar = g.full + slot;
+        const uint32_t to = g.ring + static_cast<uint32_t>(slot) * g.slot_bytes;
         mbar_arrive_expect_tx(bar, (p.dU != nullptr ? xs : 0) + xs + (p.dH != nullptr ? ys : 0) + (p.Y != nullptr ? ys : 0));
-        if (p.dU != nullptr) bulk_load(at, static_cast<const XT*>(p.dU) + t * p.N, xs, bar);
-        bulk_load(at + xs, static_cast<const XT*>(p.U) + t * p.N, xs, bar);
-        if (p.dH != nullptr) bulk_load(at + 2 * xs, p.dH + t * p.N, ys, bar);
-        if (p.Y != nullptr) bulk_load(at + 2 * xs + ys, p.Y + t * p.N, ys, bar);
+        if (p.dU != nullptr) bulk_load(to, static_cast<const XT*>(p.dU) + t * p.N, xs, bar);
+        bulk_load(to + xs, static_cast<const XT*>(p.U) + t * p.N, xs, bar);
+        if (p.dH != nullptr) bulk_load(to + 2 * xs, p.dH + t * p.N, ys, bar);
+        if (p.Y != nullptr) bulk_load(to + 2 * xs + ys, p.Y + t * p.N, ys, bar);
     };
-    // Values of the thread's j-th run of the row in the slot: e, a, b, dH.
-    auto get = [&](uint32_t at, int c, float2 ru, float2 ry, F8& e, F8& a, F8& b, F8& h) {
-        zero_f8(e);
-        zero_f8(h);
-        zero_f8(b);
-        if (p.dU != nullptr) shared_f8<XT>(at + c * 8 * sizeof(XT), e);
-        shared_f8<XT>(at + xs + c * 8 * sizeof(XT), a);
-        if (p.dH != nullptr) shared_f8<uint16_t>(at + 2 * xs + c * 16, h);
-        if (p.Y != nullptr) shared_f8<uint16_t>(at + 2 * xs + ys + c * 16, b);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            a[x] = __fmul2_rn(a[x], ru);
-            b[x] = __fmul2_rn(b[x], ry);
-        }
+    // Values of run c of the row in the slot: dU, u, y, dH.
+    auto get = [&](uint32_t at, int c, F4& e, F4& a, F4& b, F4& h) {
+        zero_f4(e);
+        zero_f4(h);
+        zero_f4(b);
+        if (p.dU != nullptr) shared_f4<XT>(at + c * 4 * sizeof(XT), e);
+        shared_f4<XT>(at + xs + c * 4 * sizeof(XT), a);
+        if (p.dH != nullptr) shared_f4<uint16_t>(at + 2 * xs + c * 8, h);
+        if (p.Y != nullptr) shared_f4<uint16_t>(at + 2 * xs + ys + c * 8, b);
     };
-    HeldWeights<HELD> post, pre;
-    post.load(p.w_post, g.tid, p.plan.threads, runs);
-    pre.load(p.w_pre, g.tid, p.plan.threads, runs);
-    F8 dpost[CH], dpre[CH];
+    int64_t t = blockIdx.x + static_cast<int64_t>(gridDim.x) * g.group;
+    const int64_t ahead = static_cast<int64_t>(p.plan.depth) * workers;
+    if (g.tid == 0)
+        for (int i = 0; i < p.plan.depth && t + static_cast<int64_t>(i) * workers < p.T; ++i)
+            fetch(t + static_cast<int64_t>(i) * workers, i);
+    NormWeights<HELD> post, pre;
+    post.load(p.w_post, g.tid, g.threads, runs);
+    pre.load(p.w_pre, g.tid, g.threads, runs);
+    F4 dpost[CH], dpre[CH];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        zero_f8(dpost[j]);
-        zero_f8(dpre[j]);
+        zero_f4(dpost[j]);
+        zero_f4(dpre[j]);
     }
-    const int first = blockIdx.x + gridDim.x * g.group;
-    if (g.tid == 0)
-        for (int i = 0; i < p.plan.depth && first + static_cast<int64_t>(i) * workers < p.T; ++i)
-            fetch(first + static_cast<int64_t>(i) * workers, i);
-    int i = 0;
-    for (int64_t t = first; t < p.T; t += workers, ++i) {
+    float2 r_next = t < p.T ? *reinterpret_cast<const float2*>(p.rstd + 2 * t) : make_float2(0.f, 0.f);
+    float gate = p.gate != nullptr && t < p.T ? p.gate[t] : 1.f;
+    for (; t < p.T; t += workers) {
         const int64_t row = t * p.N;
-        const float2 r = *reinterpret_cast<const float2*>(p.rstd + 2 * t);
-        const float2 ry = make_float2(r.x, r.x), ru = make_float2(r.y, r.y);
-        const float k = p.gate != nullptr ? p.scale * p.gate[t] : p.scale;
-        g.wait(i);
-        const uint32_t at = g.slot_at(i);
+        const float2 r = r_next, ru = make_float2(r.y, r.y), ry = make_float2(r.x, r.x);
+        const float k = p.scale * gate;
+        if (t + workers < p.T) {  // the next row's, on their way meanwhile
+            r_next = *reinterpret_cast<const float2*>(p.rstd + 2 * (t + workers));
+            if (p.gate != nullptr) gate = p.gate[t + workers];
+        }
+        g.wait();
+        const uint32_t at = g.at();
         float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = g.tid + j * p.plan.threads;
+            const int c = g.tid + j * g.threads;
             if (c >= runs) continue;
-            F8 e, a, b, h, w;
-            get(at, c, ru, ry, e, a, b, h);
+            F4 e, a, b, h, w;
+            get(at, c, e, a, b, h);
             pre.get(p.w_pre, j, c, w);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 2; ++x) {
+                a[x] = __fmul2_rn(a[x], ru);
                 dpre[j][x] = __ffma2_rn(h[x], a[x], dpre[j][x]);
                 w[x] = __fmul2_rn(h[x], w[x]);
                 e[x] = __ffma2_rn(ru, w[x], e[x]);
             }
-            s[0] = dot_f8(a, w, s[0]);
-            if (p.Y == nullptr) continue;
+            s[0] = dot_f4(a, w, s[0]);
             post.get(p.w_post, j, c, w);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] = __fmul2_rn(w[x], b[x]);
-            s[1] = dot_f8(e, w, s[1]);
-            s[2] = dot_f8(a, w, s[2]);
+            for (int x = 0; x < 2; ++x) w[x] = __fmul2_rn(w[x], __fmul2_rn(b[x], ry));
+            s[1] = dot_f4(e, w, s[1]);
+            s[2] = dot_f4(a, w, s[2]);
         }
-        g.sum<3>(s, sh.part[g.group][i & 1]);
+        g.sum<3>(s, sh.part[g.group][g.turn]);
         const float rm = r.y * (s[0] * inv_n);
         const float dot = fmaf(-rm, s[2], s[1]);
         if (p.dgate != nullptr && g.tid == 0) p.dgate[t] = p.scale * dot;
@@ -404,60 +425,65 @@ norm_residual_bwd_kernel(const __grid_constant__ NormBwdParams p) {
         const float kr = k * r.x;  // r_y is 1 without the norm
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = g.tid + j * p.plan.threads;
+            const int c = g.tid + j * g.threads;
             if (c >= runs) continue;
-            F8 e, a, b, h, w;
-            get(at, c, ru, ry, e, a, b, h);
+            F4 e, a, b, h, w;
+            get(at, c, e, a, b, h);
             pre.get(p.w_pre, j, c, w);
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                e[x] = __ffma2_rn(a[x], make_float2(-rm, -rm), __ffma2_rn(ru, __fmul2_rn(h[x], w[x]), e[x]));
-            if (p.dX != nullptr) store_f8(static_cast<XT*>(p.dX) + row + c * 8, e);
+            for (int x = 0; x < 2; ++x)
+                e[x] = __ffma2_rn(__fmul2_rn(a[x], ru), make_float2(-rm, -rm), __ffma2_rn(ru, __fmul2_rn(h[x], w[x]), e[x]));
+            if (p.dX != nullptr) store_f4(static_cast<XT*>(p.dX) + row + c * 4, e);
             if (p.Y == nullptr) continue;
             post.get(p.w_post, j, c, w);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 2; ++x) {
+                b[x] = __fmul2_rn(b[x], ry);
                 dpost[j][x] = __ffma2_rn(__fmul2_rn(e[x], make_float2(k, k)), b[x], dpost[j][x]);
                 e[x] = __fmul2_rn(__ffma2_rn(b[x], make_float2(sub, sub), __fmul2_rn(e[x], w[x])), make_float2(kr, kr));
             }
-            if (p.dY != nullptr) store_f8(p.dY + row + c * 8, e);
+            if (p.dY != nullptr) store_f4(p.dY + row + c * 4, e);
         }
         g.barrier();  // the slot is free
-        if (g.tid == 0 && t + static_cast<int64_t>(p.plan.depth) * workers < p.T)
-            fetch(t + static_cast<int64_t>(p.plan.depth) * workers, i + p.plan.depth);
+        if (g.tid == 0 && t + ahead < p.T) fetch(t + ahead, g.slot);
+        g.next();
     }
     if (p.part_post == nullptr && p.part_pre == nullptr) return;
     // The groups' sums, in group order.
-    float* joined = reinterpret_cast<float*>(norm_smem + kNormSharedBytes);  // [groups][2][N]
+    const uint32_t joined = smem_u32(norm_smem) + kNormSharedBytes;  // [groups][2][N]
     if (p.plan.groups > 1) {
         __syncthreads();  // no group still reads its rows
+        if (g.group > 0)
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int c = g.tid + j * p.plan.threads;
-            if (c >= runs || g.group == 0) continue;
-            store_f8(joined + (2 * g.group) * p.N + c * 8, dpost[j]);
-            store_f8(joined + (2 * g.group + 1) * p.N + c * 8, dpre[j]);
-        }
+            for (int j = 0; j < CH; ++j) {
+                const int c = g.tid + j * g.threads;
+                if (c >= runs) continue;
+                const uint32_t to = joined + (2 * g.group * p.N + c * 4) * 4;
+                st_shared_v4(to, __float_as_uint(dpost[j][0].x), __float_as_uint(dpost[j][0].y), __float_as_uint(dpost[j][1].x),
+                             __float_as_uint(dpost[j][1].y));
+                st_shared_v4(to + p.N * 4, __float_as_uint(dpre[j][0].x), __float_as_uint(dpre[j][0].y), __float_as_uint(dpre[j][1].x),
+                             __float_as_uint(dpre[j][1].y));
+            }
         __syncthreads();
     }
     if (g.group != 0) return;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const int c = g.tid + j * p.plan.threads;
+        const int c = g.tid + j * g.threads;
         if (c >= runs) continue;
         for (int o = 1; o < p.plan.groups; ++o) {
-            F8 a, b;
-            shared_f8<float>(smem_u32(joined) + ((2 * o) * p.N + c * 8) * 4, a);
-            shared_f8<float>(smem_u32(joined) + ((2 * o + 1) * p.N + c * 8) * 4, b);
+            F4 a, b;
+            shared_f4<float>(joined + (2 * o * p.N + c * 4) * 4, a);
+            shared_f4<float>(joined + ((2 * o + 1) * p.N + c * 4) * 4, b);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 2; ++x) {
                 dpost[j][x] = __fadd2_rn(dpost[j][x], a[x]);
                 dpre[j][x] = __fadd2_rn(dpre[j][x], b[x]);
             }
         }
-        const int64_t at = static_cast<int64_t>(blockIdx.x) * p.N + c * 8;
-        if (p.part_post != nullptr) store_f8(p.part_post + at, dpost[j]);
-        if (p.part_pre != nullptr) store_f8(p.part_pre + at, dpre[j]);
+        const int64_t to = static_cast<int64_t>(blockIdx.x) * p.N + c * 4;
+        if (p.part_post != nullptr) store_f4(p.part_post + to, dpost[j]);
+        if (p.part_pre != nullptr) store_f4(p.part_pre + to, dpre[j]);
     }
 }
 
