@@ -518,7 +518,7 @@ DG_API int dg_get_bias_workspace(int M, int N);
  *              sc[(m/128)*sc_stride + n], sc_stride >= N (A of dg_fp8_gemm_tn, whose
  *              K is the rows: the weights' gradient).  Rows past M are zeros.
  *   dbias      float32 [N] or null: sum over the rows of dz, before the casts
- *   ws         dg_get_bias_workspace(M, N) floats; null without dbias
+ *   ws         dg_get_bias_workspace(M, N) floats, 16-byte aligned; null without dbias
  *   dD, Z      bf16 [M][N]; Z may be null for DG_ACT_NONE
  * N % 128 == 0.  M == 0 writes zeros to dbias and nothing else.
  */

@@ -1059,9 +1059,9 @@ dg_status check_norm(int T, int N, int dtype, float scale) {
 }
 
 dg_status launch_column_sum(float* out0, const float* in0, float* out1, const float* in1, int parts, int N, void* stream) {
-    dg::ColumnSumParams p{{out0, out1}, {in0, in1}, parts, N};
+    dg::ColumnSumParams p{out0, out1, in0, in1, parts, N};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, 32)), out1 ? 2u : 1u, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, 64)), out1 ? 2u : 1u, 1);
     cfg.blockDim = dim3(dg::kColumnSumThreads, 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
@@ -1094,31 +1094,43 @@ dg_status check_balance(int T, int E, int k, int S, int dtype, int score, float 
 // not depend on the SM cap.)
 int balance_chunk(int T) {
     const int c = cdiv(T, dg::kBalanceMaxChunks);
-    return c < dg::kBalanceWarps ? dg::kBalanceWarps : c;
+    return c < 8 ? 8 : c;
 }
 int64_t balance_rows(int T, int S) { return cdiv64(T, balance_chunk(T)) + S; }
 
+template <typename L, int EPL>
+dg_status launch_balance_sum_one(const dg::BalanceParams& p, bool wide, void* st) {
+    constexpr int W = dg::balance_warps(EPL);
+    return launch_plain(wide ? dg::balance_sum_kernel<EPL, true, L> : dg::balance_sum_kernel<EPL, false, L>, p, p.chunks, W * 32,
+                        (W + 1) * p.E * 4, 1, st);
+}
 template <typename L>
 dg_status launch_balance_sum(const dg::BalanceParams& p, void* st) {
-    const int per = cdiv(p.E, 32), threads = dg::kBalanceWarps * 32;
-    const int smem = (dg::kBalanceWarps + 1) * p.E * 4;
-    if (per <= 1) return launch_plain(dg::balance_sum_kernel<1, L>, p, p.chunks, threads, smem, 1, st);
-    if (per <= 2) return launch_plain(dg::balance_sum_kernel<2, L>, p, p.chunks, threads, smem, 1, st);
-    if (per <= 4) return launch_plain(dg::balance_sum_kernel<4, L>, p, p.chunks, threads, smem, 1, st);
-    if (per <= 8) return launch_plain(dg::balance_sum_kernel<8, L>, p, p.chunks, threads, smem, 1, st);
-    if (per <= 16) return launch_plain(dg::balance_sum_kernel<16, L>, p, p.chunks, threads, smem, 1, st);
-    return launch_plain(dg::balance_sum_kernel<32, L>, p, p.chunks, threads, smem, 1, st);
+    const int per = cdiv(p.E, 32);
+    const bool wide = full_lanes(p.E, per) && aligned16(p.logits);
+    if (per <= 1) return launch_balance_sum_one<L, 1>(p, wide, st);
+    if (per <= 2) return launch_balance_sum_one<L, 2>(p, wide, st);
+    if (per <= 4) return launch_balance_sum_one<L, 4>(p, wide, st);
+    if (per <= 8) return launch_balance_sum_one<L, 8>(p, wide, st);
+    if (per <= 16) return launch_balance_sum_one<L, 16>(p, wide, st);
+    return launch_balance_sum_one<L, 32>(p, wide, st);
 }
 
+template <typename L, int EPL>
+dg_status launch_balance_bwd_one(const dg::BalanceBwdParams& p, bool wide, int64_t grid, void* st) {
+    return launch_plain(wide ? dg::balance_bwd_kernel<EPL, true, L> : dg::balance_bwd_kernel<EPL, false, L>, p, grid,
+                        dg::kBalanceBwdWarps * 32, 0, 1, st);
+}
 template <typename L>
 dg_status launch_balance_bwd(const dg::BalanceBwdParams& p, int64_t grid, void* st) {
-    const int per = cdiv(p.E, 32), threads = dg::kBalanceWarps * 32;
-    if (per <= 1) return launch_plain(dg::balance_bwd_kernel<1, L>, p, grid, threads, 0, 1, st);
-    if (per <= 2) return launch_plain(dg::balance_bwd_kernel<2, L>, p, grid, threads, 0, 1, st);
-    if (per <= 4) return launch_plain(dg::balance_bwd_kernel<4, L>, p, grid, threads, 0, 1, st);
-    if (per <= 8) return launch_plain(dg::balance_bwd_kernel<8, L>, p, grid, threads, 0, 1, st);
-    if (per <= 16) return launch_plain(dg::balance_bwd_kernel<16, L>, p, grid, threads, 0, 1, st);
-    return launch_plain(dg::balance_bwd_kernel<32, L>, p, grid, threads, 0, 1, st);
+    const int per = cdiv(p.E, 32);
+    const bool wide = full_lanes(p.E, per) && aligned16(p.logits) && aligned16(p.dlogits) && aligned16(p.add);
+    if (per <= 1) return launch_balance_bwd_one<L, 1>(p, wide, grid, st);
+    if (per <= 2) return launch_balance_bwd_one<L, 2>(p, wide, grid, st);
+    if (per <= 4) return launch_balance_bwd_one<L, 4>(p, wide, grid, st);
+    if (per <= 8) return launch_balance_bwd_one<L, 8>(p, wide, grid, st);
+    if (per <= 16) return launch_balance_bwd_one<L, 16>(p, wide, grid, st);
+    return launch_balance_bwd_one<L, 32>(p, wide, grid, st);
 }
 
 template <typename XT>
@@ -1795,7 +1807,7 @@ dg_status dg_epilogue_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, fl
     if (sr_stride < M) return fail(DG_ERR_INVALID_ARG, "sr_stride=%d must be >= M=%d", sr_stride, M);
     if (sc_stride < N) return fail(DG_ERR_INVALID_ARG, "sc_stride=%d must be >= N=%d", sc_stride, N);
     if (M > 0 && dbias && !ws) return fail(DG_ERR_INVALID_ARG, "dbias needs ws");
-    if (!aligned(dbias, 4) || !aligned(ws, 4)) return fail(DG_ERR_MISALIGNED, "dbias and ws must be 4-byte aligned");
+    if (!aligned(dbias, 4) || !aligned16(ws)) return fail(DG_ERR_MISALIGNED, "ws must be 16-byte aligned, dbias 4-byte aligned");
     if (dbias && dg_get_bias_workspace(M, N) < 0) return fail(DG_ERR_UNSUPPORTED, "M=%d N=%d: the workspace is too large", M, N);
     if (M == 0) {
         if (!dbias) return ok();
@@ -1921,8 +1933,9 @@ dg_status dg_balance_loss_bwd(void* dlogits, const void* add, const float* dloss
     const int sms = effective_sms();
     if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
     dg::BalanceBwdParams p{dlogits, add, dloss, logits, counts, seq_offsets, T, E, S, score == DG_SCORE_SOFTMAX,
+                           static_cast<int64_t>(T) * k <= 1 << 24,
                            static_cast<float>(static_cast<double>(coef) * E / k)};
-    const int64_t all = cdiv64(T, dg::kBalanceWarps), cap = static_cast<int64_t>(sms) * 4;
+    const int64_t all = cdiv64(T, dg::kBalanceBwdWarps), cap = static_cast<int64_t>(sms) * 4;
     const int64_t grid = all < cap ? all : cap;
     return logits_dtype == DG_DTYPE_BF16 ? launch_balance_bwd<uint16_t>(p, grid, stream)
                                          : launch_balance_bwd<float>(p, grid, stream);

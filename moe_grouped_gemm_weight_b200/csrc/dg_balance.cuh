@@ -15,8 +15,28 @@
 
 namespace dg {
 
-constexpr int kBalanceWarps = 8;
 constexpr int kBalanceMaxChunks = 296;
+constexpr int kBalanceBwdWarps = 8;
+// Warps of a CTA of the sums: many short runs of tokens hide the loads' latency; 32
+// logits a lane need the registers.
+__host__ __device__ constexpr int balance_warps(int epl) { return epl <= 16 ? 16 : 8; }
+
+// The expert of a lane's i-th logit: chunks of a wide load, 32 chunks apart (kWide: rows
+// are 16-byte aligned and every lane has EPL experts), or every 32nd.
+template <int EPL, bool kWide, typename L>
+__device__ __forceinline__ int balance_expert(int lane, int i) {
+    constexpr int kChunk = RawRow<EPL, L>::kChunk;
+    return kWide ? (i / kChunk) * 32 * kChunk + lane * kChunk + i % kChunk : lane + 32 * i;
+}
+template <int EPL, bool kWide, typename L>
+__device__ __forceinline__ void balance_load(RawRow<EPL, L>& r, const L* row, int E, int lane) {
+    if constexpr (kWide) {
+        r.load_wide(row + lane * RawRow<EPL, L>::kChunk, 32 * RawRow<EPL, L>::kChunk);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) r.load_one(i, lane + 32 * i < E, row + lane + 32 * i);
+    }
+}
 
 // Tokens [0, T) in chunks, one a CTA.  The part of sequence s inside chunk c has
 // row c + s of the partial sums: going along the tokens c and s never fall and one
@@ -42,47 +62,48 @@ __device__ __forceinline__ int seq_offset(const int32_t* offsets, int s, int T) 
     if (offsets == nullptr) return s == 0 ? 0 : T;
     return min(max(offsets[s], 0), T);
 }
-// The sequence that holds token t: the last with offset <= t (S: behind the last; -1: before the first).
+// The sequence that holds token t: the last with offset <= t (S: behind the last; -1:
+// before the first).  A warp's search, 32 offsets at a time.
 __device__ __forceinline__ int seq_of(const int32_t* offsets, int S, int T, int t) {
     if (offsets == nullptr) return 0;
-    int lo = -1, hi = S;  // offset[lo] <= t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (seq_offset(offsets, mid, T) <= t) lo = mid; else hi = mid - 1;
+    const int lane = threadIdx.x & 31;
+    int base = 0, n = S + 1;  // of the offsets, how many are <= t: base, and some of the next n
+    while (n > 0) {
+        const int step = (n + 31) / 32, at = (lane + 1) * step - 1;
+        const bool below = at < n && seq_offset(offsets, base + at, T) <= t;
+        const int skip = __popc(__ballot_sync(0xffffffffu, below)) * step;
+        base += skip;
+        n = n - skip >= step ? step - 1 : n - skip;  // the next one probed is not, if there is one
     }
-    return lo;
+    return base - 1;
 }
 
-// p of one token's E logits, lane's experts lane + 32 i; `slope`: 1 - s of a sigmoid,
-// 1 of the softmax.  A token without a finite logit has p = 0.
+// p of one token's E logits; `slope`: 1 - s of a sigmoid (not written for the softmax).
+// A token without a finite logit has p = 0.
 template <int EPL>
-__device__ __forceinline__ void balance_probs(float (&l)[EPL], int softmax, float (&p)[EPL], float (&slope)[EPL]) {
+__device__ __forceinline__ void balance_probs(const float (&l)[EPL], int softmax, float (&p)[EPL], float (&slope)[EPL]) {
     float sum = 0.f;
     if (softmax) {
-        float m = -INFINITY;
+        float m = l[0];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) m = fmaxf(m, l[i]);
+        for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
         m = warp_max(m);
-        const float from = m == -INFINITY ? 0.f : m;
+        m = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            p[i] = l[i] - from;
-            slope[i] = 1.f;
-        }
+        for (int i = 0; i < EPL; ++i) p[i] = l[i] - m;
         exp_results<EPL>(p);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) sum += p[i];
     } else {
+        // s = 1 / (1 + e), 1 - s = e / (1 + e), e = exp(-l); in terms of exp(-|l|) both are sums of positives
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) p[i] = -fabsf(l[i]);
+        exp_results<EPL>(p);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            // s = 1 / (1 + e), 1 - s = e / (1 + e), e = exp(-l); in terms of exp(-|l|) both are sums of positives
-            float e[1] = {-fabsf(l[i])};
-            exp_results<1>(e);
-            const float r = __frcp_rn(1.f + e[0]);
-            const float big = r, small = e[0] * r;
-            const bool up = l[i] > 0.f;
-            p[i] = up ? big : small;
-            slope[i] = up ? small : big;
+            const float r = rcp_fast(1.f + p[i]), small = p[i] * r;
+            p[i] = l[i] > 0.f ? r : small;
+            slope[i] = l[i] > 0.f ? small : r;
             sum += p[i];
         }
     }
@@ -92,11 +113,12 @@ __device__ __forceinline__ void balance_probs(float (&l)[EPL], int softmax, floa
     for (int i = 0; i < EPL; ++i) p[i] *= inv;
 }
 
-template <int EPL, typename L>
-__global__ void __launch_bounds__(kBalanceWarps * 32)
+template <int EPL, bool kWide, typename L>
+__global__ void __launch_bounds__(balance_warps(EPL) * 32)
 balance_sum_kernel(const BalanceParams p) {
-    extern __shared__ float balance_smem[];  // [warps][E] sums, then [E] counts
-    int32_t* hist = reinterpret_cast<int32_t*>(balance_smem + kBalanceWarps * p.E);
+    constexpr int W = balance_warps(EPL);
+    extern __shared__ float balance_smem[];  // [W][E] sums, then [E] counts
+    int32_t* hist = reinterpret_cast<int32_t*>(balance_smem + W * p.E);
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -107,37 +129,38 @@ balance_sum_kernel(const BalanceParams p) {
         if (first >= t1) break;
         const int a = max(first, t0), b = min(seq_offset(p.offsets, s + 1, p.T), t1);
         if (a >= b) continue;
-        for (int e = tid; e < p.E; e += kBalanceWarps * 32) hist[e] = 0;
+        int t = a + warp;
+        RawRow<EPL, L> raw;
+        if (t < b) balance_load<EPL, kWide>(raw, logits + static_cast<int64_t>(t) * p.E, p.E, lane);
+        for (int e = tid; e < p.E; e += W * 32) hist[e] = 0;
         __syncthreads();
         const int64_t s1 = static_cast<int64_t>(b) * p.k;
-        for (int64_t i = static_cast<int64_t>(a) * p.k + tid; i < s1; i += kBalanceWarps * 32) {
+        for (int64_t i = static_cast<int64_t>(a) * p.k + tid; i < s1; i += W * 32) {
             const int e = p.topk_idx[i];
             if (e >= 0 && e < p.E) atomicAdd(hist + e, 1);
         }
         float acc[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
-        for (int t = a + warp; t < b; t += kBalanceWarps) {
-            const L* row = logits + static_cast<int64_t>(t) * p.E;
+        for (; t < b; t += W) {
             float l[EPL], q[EPL], slope[EPL];
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = lane + 32 * i;
-                l[i] = e < p.E ? logit_at(row + e) : -INFINITY;
-            }
+            raw.get(kWide, l);
+            if (t + W < b) balance_load<EPL, kWide>(raw, logits + static_cast<int64_t>(t + W) * p.E, p.E, lane);
             balance_probs<EPL>(l, p.softmax, q, slope);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) acc[i] += q[i];
         }
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (lane + 32 * i < p.E) balance_smem[warp * p.E + lane + 32 * i] = acc[i];
+        for (int i = 0; i < EPL; ++i) {
+            const int e = balance_expert<EPL, kWide, L>(lane, i);
+            if (kWide || e < p.E) balance_smem[warp * p.E + e] = acc[i];
+        }
         __syncthreads();
         const int64_t at = static_cast<int64_t>(c + s) * p.E;
-        for (int e = tid; e < p.E; e += kBalanceWarps * 32) {
+        for (int e = tid; e < p.E; e += W * 32) {
             float v = balance_smem[e];
 #pragma unroll
-            for (int w = 1; w < kBalanceWarps; ++w) v += balance_smem[w * p.E + e];
+            for (int w = 1; w < W; ++w) v += balance_smem[w * p.E + e];
             p.part_p[at + e] = v;
             p.part_n[at + e] = hist[e];
         }
@@ -145,13 +168,14 @@ balance_sum_kernel(const BalanceParams p) {
     }
 }
 
-constexpr int kBalanceFinishThreads = 1024;
+constexpr int kBalanceFinishThreads = 512;
 constexpr int kBalanceFinishCtas = 8;
+constexpr int kBalanceFinishBatch = 8;
 
 // One cluster joins the parts of each (sequence, expert), in chunk order, and the
 // loss.  CTA r takes a run of the S E sums; if those are fewer than its threads, as
 // many threads share a sum, each with a run of its parts.
-__global__ void __launch_bounds__(kBalanceFinishThreads)
+__global__ void __launch_bounds__(kBalanceFinishThreads, 1)
 balance_finish_kernel(const BalanceParams p) {
     __shared__ float sp[kBalanceFinishThreads];
     __shared__ int32_t sn[kBalanceFinishThreads];
@@ -191,11 +215,22 @@ balance_finish_kernel(const BalanceParams p) {
                 const int c0 = a / p.chunk, c1 = (b - 1) / p.chunk + 1, cs = c1 - c0;
                 const int from = c0 + static_cast<int>(static_cast<int64_t>(cs) * part / split);
                 const int to = c0 + static_cast<int>(static_cast<int64_t>(cs) * (part + 1) / split);
-#pragma unroll 4
-                for (int c = from; c < to; ++c) {
-                    const int64_t at = static_cast<int64_t>(c + s) * p.E + e;
-                    sum += p.part_p[at];
-                    count += p.part_n[at];
+                const float* sums = p.part_p + static_cast<int64_t>(from + s) * p.E + e;
+                const int32_t* counts = p.part_n + static_cast<int64_t>(from + s) * p.E + e;
+                const int n = to - from;
+                for (int c = 0; c < n; c += kBalanceFinishBatch) {  // loads of a batch in flight together
+                    float x[kBalanceFinishBatch];
+                    int32_t m[kBalanceFinishBatch];
+#pragma unroll
+                    for (int j = 0; j < kBalanceFinishBatch; ++j) {
+                        x[j] = c + j < n ? sums[static_cast<int64_t>(c + j) * p.E] : 0.f;
+                        m[j] = c + j < n ? counts[static_cast<int64_t>(c + j) * p.E] : 0;
+                    }
+#pragma unroll
+                    for (int j = 0; j < kBalanceFinishBatch; ++j) {
+                        sum += x[j];
+                        count += m[j];
+                    }
                 }
             }
         }
@@ -203,12 +238,16 @@ balance_finish_kernel(const BalanceParams p) {
             sp[tid] = sum;
             sn[tid] = count;
             __syncthreads();
-            if (there && part == 0)
-                for (int j = 1; j < split; ++j) {
-                    sum += sp[tid + j * width];
-                    count += sn[tid + j * width];
+            // Halves of the parts, then quarters, ...: the first takes its partner's.
+            for (int live = split; live > 1;) {
+                const int half = (live + 1) / 2;
+                if (there && part < live - half) {
+                    sp[tid] = sum += sp[tid + half * width];
+                    sn[tid] = count += sn[tid + half * width];
                 }
-            __syncthreads();
+                live = half;
+                __syncthreads();
+            }
         }
         if (there && part == 0) {
             const int l = b > a ? b - a : 1;
@@ -221,9 +260,11 @@ balance_finish_kernel(const BalanceParams p) {
     for (int o = 16; o >= 1; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
     if ((tid & 31) == 0) share[tid >> 5] = loss;
     __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kBalanceFinishThreads / 32; ++w) loss += share[w];
-        mine = loss;
+    if (tid < 32) {
+        loss = tid < kBalanceFinishThreads / 32 ? share[tid] : 0.0;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+        if (tid == 0) mine = loss;
     }
     __syncwarp();
     cluster_sync();
@@ -249,6 +290,7 @@ struct BalanceBwdParams {
     const int32_t* offsets;
     int T, E, S;
     int softmax;
+    int exact;               // no count passes 2^24: floats hold it
     float scale;             // coef E / k
 };
 
@@ -256,22 +298,27 @@ struct BalanceBwdParams {
 // counts' distances to that of the token's likeliest expert c, whole numbers:
 // (n_j - n_c) - sum_e p_e (n_e - n_c) has no large terms that cancel where one expert has
 // nearly all the weight, or where all loads are nearly alike.
-template <int EPL, typename L>
-__global__ void __launch_bounds__(kBalanceWarps * 32)
+template <int EPL, bool kWide, typename L>
+__global__ void __launch_bounds__(kBalanceBwdWarps * 32)
 balance_bwd_kernel(const BalanceBwdParams p) {
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * kBalanceWarps;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * kBalanceWarps + (threadIdx.x >> 5);
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kBalanceBwdWarps;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kBalanceBwdWarps + (threadIdx.x >> 5);
     const int t0 = static_cast<int>(p.T * w / warps), t1 = static_cast<int>(p.T * (w + 1) / warps);
+    const L* logits = static_cast<const L*>(p.logits);
+    RawRow<EPL, L> raw;
+    if (t0 < t1) balance_load<EPL, kWide>(raw, logits + static_cast<int64_t>(t0) * p.E, p.E, lane);
     const int len = seq_offset(p.offsets, p.S, p.T) - seq_offset(p.offsets, 0, p.T);
     const float up = p.dloss != nullptr ? *p.dloss : 1.f;
-    const L* logits = static_cast<const L*>(p.logits);
-    int32_t n[EPL];
+    float n[EPL];         // whole numbers; as float where those are exact, else their bits
     int end = t0, s = 0;  // the sequence s holds tokens up to `end`
     float k = 0.f;
     for (int t = t0; t < t1; ++t) {
+        float l[EPL], d[EPL];
+        raw.get(kWide, l);
+        if (t + 1 < t1) balance_load<EPL, kWide>(raw, logits + static_cast<int64_t>(t + 1) * p.E, p.E, lane);
         if (t >= end) {
             s = seq_of(p.offsets, p.S, p.T, t);
             const bool in = s >= 0 && s < p.S;
@@ -282,47 +329,60 @@ balance_bwd_kernel(const BalanceBwdParams p) {
             if (!in) s = -1;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                const int e = lane + 32 * i;
-                n[i] = s >= 0 && e < p.E ? p.counts[static_cast<int64_t>(s) * p.E + e] : 0;
+                const int e = balance_expert<EPL, kWide, L>(lane, i);
+                const int32_t c = s >= 0 && (kWide || e < p.E) ? p.counts[static_cast<int64_t>(s) * p.E + e] : 0;
+                n[i] = p.exact ? static_cast<float>(c) : __int_as_float(c);
             }
         }
         const int64_t at = static_cast<int64_t>(t) * p.E;
-        float l[EPL], d[EPL], q[EPL], slope[EPL];
+        if (p.add != nullptr) {
+            RawRow<EPL, L> base;
+            balance_load<EPL, kWide>(base, static_cast<const L*>(p.add) + at, p.E, lane);
+            base.get(kWide, d);
+        } else {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = lane + 32 * i;
-            d[i] = p.add != nullptr && e < p.E ? logit_at(static_cast<const L*>(p.add) + at + e) : 0.f;
+            for (int i = 0; i < EPL; ++i) d[i] = 0.f;
         }
         if (s >= 0) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = lane + 32 * i;
-                l[i] = e < p.E ? logit_at(logits + at + e) : -INFINITY;
-            }
+            float q[EPL], slope[EPL];
             balance_probs<EPL>(l, p.softmax, q, slope);
-            float best = -1.f;
-            int nc = 0;
+            float best = -1.f, nc = 0.f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
                 if (q[i] > best) {
                     best = q[i];
                     nc = n[i];
                 }
-            const float top = warp_max(best);
-            const uint32_t who = __ballot_sync(0xffffffffu, best == top);
+            const uint32_t who = __ballot_sync(0xffffffffu, best == warp_max(best));
             nc = __shfl_sync(0xffffffffu, nc, who ? __ffs(who) - 1 : 0);
             float mean = 0.f;
+            if (p.exact) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) mean = fmaf(q[i], static_cast<float>(n[i] - nc), mean);
+                for (int i = 0; i < EPL; ++i) l[i] = n[i] - nc;
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) l[i] = static_cast<float>(__float_as_int(n[i]) - __float_as_int(nc));
+            }
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) mean = fmaf(q[i], l[i], mean);
             mean = warp_sum(mean);
+            if (!p.softmax) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                d[i] = fmaf(k * q[i] * slope[i], static_cast<float>(n[i] - nc) - mean, d[i]);
+                for (int i = 0; i < EPL; ++i) q[i] *= slope[i];
+            }
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) d[i] = fmaf(k * q[i], l[i] - mean, d[i]);
         }
         L* out = static_cast<L*>(p.dlogits) + at;
+        if constexpr (kWide) {
+            constexpr int kChunk = RawRow<EPL, L>::kChunk;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (lane + 32 * i < p.E) store_logit(out + lane + 32 * i, d[i]);
+            for (int c = 0; c < EPL / kChunk; ++c) store_chunk<kChunk>(out + c * 32 * kChunk + lane * kChunk, d + c * kChunk);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (lane + 32 * i < p.E) store_logit(out + lane + 32 * i, d[i]);
+        }
     }
 }
 

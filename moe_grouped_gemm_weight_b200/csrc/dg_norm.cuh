@@ -487,38 +487,46 @@ norm_residual_bwd_kernel(const __grid_constant__ NormBwdParams p) {
     }
 }
 
-// Sums over the rows of up to two [parts][N] arrays, in row order: the last step
-// of the sums over tokens.  A warp takes 32 columns of one array.
+// Sums over the rows of up to two [parts][N] arrays: the last step of the sums over
+// tokens.
 struct ColumnSumParams {
-    float* out[2];
-    const float* in[2];
+    float *out0, *out1;
+    const float *in0, *in1;
     int parts, N;
 };
 constexpr int kColumnSumThreads = 256;
+constexpr int kColumnSumBatch = 10;
 
-// A CTA takes 32 columns of an array: its 8 warps every eighth row, then the
-// warps' sums in order.
+// A CTA takes 64 columns of an array, two a lane: its 8 warps every eighth row, a batch
+// of them in flight together, then the warps' sums in order.
 __global__ void __launch_bounds__(kColumnSumThreads)
 column_sum_kernel(const ColumnSumParams p) {
-    __shared__ float part[kColumnSumThreads / 32][32];
+    constexpr int W = kColumnSumThreads / 32;
+    __shared__ float2 part[W][32];
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x * 32 + lane;
-    const float* in = p.in[blockIdx.y];
-    float* out = p.out[blockIdx.y];
-    if (out == nullptr) return;
-    float s = 0.f;
-    if (c < p.N) {
-#pragma unroll 4
-        for (int r = warp; r < p.parts; r += kColumnSumThreads / 32) s += in[static_cast<int64_t>(r) * p.N + c];
-    }
+    const int c = blockIdx.x * 64 + lane * 2;  // N is a multiple of 8
+    const float* in = blockIdx.y == 0 ? p.in0 : p.in1;
+    float* out = blockIdx.y == 0 ? p.out0 : p.out1;
+    float2 s = make_float2(0.f, 0.f);
+    if (c < p.N)
+        for (int r = warp; r < p.parts; r += W * kColumnSumBatch) {
+            float2 v[kColumnSumBatch];
+#pragma unroll
+            for (int j = 0; j < kColumnSumBatch; ++j)
+                v[j] = r + j * W < p.parts ? *reinterpret_cast<const float2*>(in + static_cast<int64_t>(r + j * W) * p.N + c)
+                                           : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < kColumnSumBatch; ++j) s = __fadd2_rn(s, v[j]);
+        }
     part[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < p.N) {
 #pragma unroll
-        for (int w = 1; w < kColumnSumThreads / 32; ++w) s += part[w][lane];
-        out[c] = s;
+        for (int w = 1; w < W; ++w) s = __fadd2_rn(s, part[w][lane]);
+        out[c] = s.x;
+        out[c + 1] = s.y;
     }
 }
 
