@@ -635,10 +635,10 @@ DG_API int dg_get_pdl(void);
  * Cap the number of SMs the persistent kernels use (n <= 0: all SMs): those of
  * the GEMMs, dg_to_fp8_1x128, dg_route_topk and its gradient,
  * dg_dispatch_fp8_1x128, dg_swiglu_fp8 and its gradient, dg_norm_residual and its
- * gradient, dg_balance_loss_bwd.  dg_route_layout is one cluster of at most 8 CTAs;
- * dg_to_fp8_128x128, dg_combine, dg_combine_bwd, dg_fp8_1x128_to_128x128,
- * dg_epilogue_bwd and dg_balance_loss launch a CTA for each piece of work and are not
- * capped.
+ * gradient, dg_epilogue_bwd, dg_balance_loss_bwd.  dg_route_layout is one cluster of
+ * at most 8 CTAs; dg_to_fp8_128x128, dg_combine, dg_combine_bwd,
+ * dg_fp8_1x128_to_128x128 and dg_balance_loss launch a CTA for each piece of work and are
+ * not capped.
  */
 DG_API void dg_set_num_sms(int n);
 /* Current cap; the device's SM count when no cap is set (0 without a GPU). */

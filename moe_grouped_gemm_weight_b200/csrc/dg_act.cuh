@@ -19,12 +19,14 @@ enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kAc
 
 __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // exp(-g) of a pair, g <= 88: 2^t 2^lo, t is -g log2(e) as rounded, lo what the
 // product and the constant's rounding leave of it (a first-order factor is good
 // to 2^-40), so the relative error does not grow with |g| (it was 64 times 2^-24 at
 // -80): the unit's 2^power and two roundings.
 __device__ __forceinline__ float2 exp_minus2(float2 g) {
-    constexpr float kLog2e = 1.4426950408889634f, kRest = static_cast<float>(1.4426950408889634074 - kLog2e);
+    constexpr float kRest = static_cast<float>(1.4426950408889634074 - kLog2e);
     float2 e = __fmul2_rn(g, pair(-kLog2e));
     float2 lo = __ffma2_rn(g, pair(-kRest), __ffma2_rn(g, pair(-kLog2e), make_float2(-e.x, -e.y)));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
@@ -48,62 +50,28 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 clamp2(float2 v, float lo, float hi) {
-    return make_float2(min_nan(max_nan(v.x, lo), hi), min_nan(max_nan(v.y, lo), hi));
-}
-
-// -min(|g|, 126) of a pair, -126 for a NaN.
-__device__ __forceinline__ float2 minus_abs2(float2 g) { return make_float2(fmaxf(-fabsf(g.x), -126.f), fmaxf(-fabsf(g.y), -126.f)); }
-// 1 / v of a pair by one reciprocal, where the product of the two stays within FP32.  Not
-// for a NaN, which would be its neighbour's too: callers bring it back with a factor.
+// 1 / v of a pair by one reciprocal, where the product of the two stays within FP32: the
+// special-function unit bounds these functions.  Not for a NaN, which would be its
+// neighbour's too: callers keep it out and bring it back with a factor.
 __device__ __forceinline__ float2 rcp_pair(float2 v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v.x * v.y));
     return __fmul2_rn(pair(r), make_float2(v.y, v.x));
 }
-
-// t = exp(-|g|) and r = 1 / (1 + t): sigmoid(g) is r for g >= 0, else t r, and 1 - sigmoid(g)
-// the other, each to a few 2^-24 of its own value (EXACT) or with |g| 2^-24 more, the
-// rounding of the exponent.  t is zero below 2^-126.  1 + t is at most 2, so one reciprocal
-// serves both of the pair: the special-function unit bounds the GEMM's epilogue.
-template <bool EXACT>
-__device__ __forceinline__ void sigmoid_parts2(float2 g, float2& t, float2& r) {
-    const float2 m = minus_abs2(g);
-    if (EXACT) {
-        t = exp_minus2(make_float2(-m.x, -m.y));
-    } else {
-        t = __fmul2_rn(m, pair(1.4426950408889634f));
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.x));
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t.y));
-    }
-    r = rcp_pair(__fadd2_rn(t, pair(1.f)));
+__device__ __forceinline__ float2 ex2_pair(float2 v) {
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v.y));
+    return v;
 }
-__device__ __forceinline__ float2 sigmoid_of_parts2(float2 g, float2 t, float2 r) {
-    return __fmul2_rn(r, make_float2(g.x < 0.f ? t.x : 1.f, g.y < 0.f ? t.y : 1.f));
-}
-
 // The two factors of the normal distribution's tail at |z|: q = exp(-z^2/2) R(|z|) =
 // Phi(-|z|), and the exponential itself.  R(x) = erfcx(x / sqrt 2) / 2 falls
 // smoothly from 1/2 as 1 / (x sqrt(2 pi)); it is a polynomial of degree 8 in
 // t = 1 / (1 + 0.3 x), fitted for the least relative error over 0 <= x <= 14.5 (5.8e-8;
-// with FP32 arithmetic 4.3e-7).  The exponent's roundings are carried along as in
-// sigmoid2.  Past |z| = 13.2 the exponential is below 2^-126 and the tail zero.
+// with FP32 arithmetic 4.3e-7).  The exponent's roundings add 1.2 z^2 2^-24.  Past |z| =
+// 13.2 the exponential is below 2^-126 and the tail zero; a NaN counts as 14.5.
 __device__ __forceinline__ void normal_tail2(float2 z, float2& q, float2& ez) {
-    constexpr float kC = -0.72134752044448170f;  // -log2(e) / 2
-    constexpr float kCRest = static_cast<float>(-0.72134752044448170368 - kC);
-    const float2 x = make_float2(fminf(fabsf(z.x), 14.5f), fminf(fabsf(z.y), 14.5f));  // a NaN: 14.5
-    const float2 a = __fmul2_rn(x, x), ra = __ffma2_rn(x, x, make_float2(-a.x, -a.y));
-    ez = __fmul2_rn(a, pair(kC));
-    float2 lo = __ffma2_rn(a, pair(kC), make_float2(-ez.x, -ez.y));
-    lo = __ffma2_rn(a, pair(kCRest), __ffma2_rn(ra, pair(kC), lo));
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(ez.x));
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(ez.y));
-    ez = __fmul2_rn(ez, __ffma2_rn(lo, pair(0.6931471805599453f), pair(1.f)));
+    const float2 x = make_float2(fminf(fabsf(z.x), 14.5f), fminf(fabsf(z.y), 14.5f));
+    ez = ex2_pair(__fmul2_rn(__fmul2_rn(x, x), pair(-0.5f * kLog2e)));
     const float2 t = rcp_pair(__ffma2_rn(x, pair(0.3f), pair(1.f)));
     float2 r = pair(0.03840739652514458f);
     r = __ffma2_rn(r, t, pair(-0.16930747032165527f));
@@ -119,14 +87,20 @@ __device__ __forceinline__ void normal_tail2(float2 z, float2& q, float2& ez) {
 
 constexpr float kGeluTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
+// The activation of a pair.  A sigmoid is 1 / (1 + t) or t / (1 + t) with t = exp(-|g|) by
+// the sign of g: neither overflows, and 1 + t is at most 2, so one reciprocal serves
+// both of the pair.  Its error is a few 2^-24 and the exponent's rounding, 1.3 |g| 2^-24
+// times 1 - sigmoid.
 template <int ACT>
 __device__ __forceinline__ float2 act2(float2 z) {
     if constexpr (ACT == kActRelu) return make_float2(max_nan(z.x, 0.f), max_nan(z.y, 0.f));
     if constexpr (ACT == kActSilu || ACT == kActGeluTanh) {
-        float2 g = z, t, r;
-        if (ACT == kActGeluTanh) g = __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), pair(kGeluTanhC * 0.044715f), pair(kGeluTanhC)));
-        sigmoid_parts2<false>(g, t, r);
-        return __fmul2_rn(z, sigmoid_of_parts2(g, t, r));
+        // g in units of ln 2
+        const float2 g = ACT == kActSilu ? __fmul2_rn(z, pair(kLog2e))
+                                         : __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), pair(kGeluTanhC * 0.044715f * kLog2e), pair(kGeluTanhC * kLog2e)));
+        const float2 t = ex2_pair(make_float2(fmaxf(-fabsf(g.x), -200.f), fmaxf(-fabsf(g.y), -200.f)));  // a NaN: 0
+        const float2 r = rcp_pair(__fadd2_rn(t, pair(1.f)));
+        return __fmul2_rn(z, __fmul2_rn(r, make_float2(z.x < 0.f ? t.x : 1.f, z.y < 0.f ? t.y : 1.f)));
     }
     if constexpr (ACT == kActGelu) {
         float2 q, e;
@@ -136,28 +110,43 @@ __device__ __forceinline__ float2 act2(float2 z) {
     return z;
 }
 
-// The activation's derivative, s (1 + z g'(z) (1 - s)) with s = sigmoid(g).  Past |z| = 126
-// (gelu_tanh: 30) those of gelu_tanh and silu are 0 or 1 but for less than 2^-100; there
-// the argument stays, which keeps z^2 and z (1 - s) finite.
+// Bounds within which act_slope2 takes its argument, for a pair of bf16: past them the
+// slope is 0 or 1 but for less than 2^-45, and z^2, and z times a tail, stay finite.  A NaN
+// stays one.
+template <int ACT>
+__device__ __forceinline__ uint32_t clamp_slope_bf16x2(uint32_t z) {
+    if constexpr (ACT == kActSilu || ACT == kActGeluTanh || ACT == kActGelu) {
+        // bf16: 43, 30, 14.5
+        constexpr uint32_t hi = ACT == kActSilu ? 0x422C422Cu : ACT == kActGeluTanh ? 0x41F041F0u : 0x41684168u, lo = hi | 0x80008000u;
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(z) : "r"(lo));
+        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(z) : "r"(hi));
+    }
+    return z;
+}
+
+// The activation's derivative within those bounds: s (1 + z g'(z) (1 - s)) with s = sigmoid(g),
+// 1 - s = e s, e = exp(-g).  g is taken no lower than -43, where (1 + e)^2 stays within FP32
+// for the pair's common reciprocal: s stays at 2^-62 below, and the slope's error
+// below 2^-49.
 template <int ACT>
 __device__ __forceinline__ float2 act_slope2(float2 z) {
     if constexpr (ACT == kActRelu) return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
     if constexpr (ACT == kActSilu || ACT == kActGeluTanh) {
-        z = ACT == kActSilu ? clamp2(z, -126.f, 126.f) : clamp2(z, -30.f, 30.f);
-        float2 g = z, up = z, t, r;  // up = z g'(z)
+        float2 g, up = z;  // g in units of -ln 2; up = z g'(z)
         if (ACT == kActGeluTanh) {
             const float2 z2 = __fmul2_rn(z, z);
-            g = __fmul2_rn(z, __ffma2_rn(z2, pair(kGeluTanhC * 0.044715f), pair(kGeluTanhC)));
+            g = __fmul2_rn(z, __ffma2_rn(z2, pair(-kGeluTanhC * 0.044715f * kLog2e), pair(-kGeluTanhC * kLog2e)));
             up = __fmul2_rn(z, __ffma2_rn(z2, pair(kGeluTanhC * 3.f * 0.044715f), pair(kGeluTanhC)));
+        } else {
+            g = __fmul2_rn(z, pair(-kLog2e));
         }
-        sigmoid_parts2<true>(g, t, r);
-        const float2 c = __fmul2_rn(r, make_float2(g.x < 0.f ? 1.f : t.x, g.y < 0.f ? 1.f : t.y));
-        return __fmul2_rn(sigmoid_of_parts2(g, t, r), __ffma2_rn(up, c, pair(1.f)));
+        const float2 e = ex2_pair(make_float2(fminf(g.x, 62.f), fminf(g.y, 62.f)));  // a NaN: 2^62; it comes back with `up`
+        const float2 s = rcp_pair(__fadd2_rn(e, pair(1.f)));
+        return __fmul2_rn(s, __ffma2_rn(up, __fmul2_rn(e, s), pair(1.f)));
     }
     if constexpr (ACT == kActGelu) {
         float2 q, e;
         normal_tail2(z, q, e);
-        z = clamp2(z, -14.5f, 14.5f);  // the exponential is zero before
         const float2 phi = make_float2(z.x > 0.f ? 1.f - q.x : q.x, z.y > 0.f ? 1.f - q.y : q.y);
         return __ffma2_rn(z, __fmul2_rn(e, pair(0.3989422804014327f)), phi);
     }

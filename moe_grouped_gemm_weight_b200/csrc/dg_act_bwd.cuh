@@ -19,9 +19,11 @@ struct ActBwdParams {
     const uint16_t* dD;  // [M][N]
     const uint16_t* Z;   // [M][N]
     int M, N, nb;        // nb = N / 128
+    uint32_t tiles;      // row blocks times column blocks
 };
 
 constexpr int kActBwdThreads = 256;
+constexpr int kActBwdStage = 2 * 128 * 128 * 2;  // bytes: a tile of dD and of Z
 
 // tile_cast_rows of one matrix whose last rows may be missing.
 template <int T>
@@ -44,68 +46,107 @@ __device__ __forceinline__ void tile_cast_rows_below(const TileOut& o, const F8 
     }
 }
 
-// A CTA takes a 128 x 128 tile, thread layout as in dg_moe.cuh's tiles.
+// A persistent CTA takes 128 x 128 tiles, thread layout as in dg_moe.cuh's tiles.  Each
+// thread copies the 16-byte pieces that it will use itself to shared memory (cp.async),
+// takes them into registers when they have landed and at once asks for the next tile's,
+// so that HBM works during the casts and no barrier guards the buffer.
 template <int ACT>
 __global__ void __launch_bounds__(kActBwdThreads, 2)
 act_bwd_kernel(const ActBwdParams p) {
     constexpr int T = kActBwdThreads, R = CastTile<T>::kRows;
+    extern __shared__ __align__(16) uint8_t stage_smem[];
     __shared__ __align__(16) float cm[CastTile<T>::kWarps * CastTile<T>::kStride];
     __shared__ __align__(16) float cs[CastTile<T>::kWarps * CastTile<T>::kStride];
     __shared__ __align__(16) float cr[128];
+    __shared__ uint64_t bars[2];
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, half = tid >> 4, hl = tid & 15;
+    if (tid == 0) {
+        mbar_init(&bars[0], CastTile<T>::kWarps);
+        mbar_init(&bars[1], CastTile<T>::kWarps);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    SplitBarrier maxima{&bars[0], &abort_flag}, joined{&bars[1], &abort_flag};
+    __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
-    const int tid = threadIdx.x, half = tid >> 4, hl = tid & 15;
-    const uint32_t rb = blockIdx.x / p.nb;
-    const int col = static_cast<int>(blockIdx.x - rb * p.nb) * 128;
-    const int64_t row0 = static_cast<int64_t>(rb) * 128;
-    const int64_t at = (row0 + half) * p.N + col + hl * 8, step = static_cast<int64_t>(CastTile<T>::kStep) * p.N;
-    uint4 d[R], z[R];
+    const uint32_t stage = smem_u32(stage_smem) + tid * 16;
+    const int64_t step = static_cast<int64_t>(CastTile<T>::kStep) * p.N;
+    // Tiles in turn: row block rb, column block cb, without a division per step.
+    uint32_t rb = blockIdx.x / p.nb, cb = blockIdx.x % p.nb;
+    const uint32_t step_rb = gridDim.x / p.nb, step_cb = gridDim.x % p.nb;
+    auto fetch = [&] {
+        const int64_t row0 = static_cast<int64_t>(rb) * 128 + half;
+        const int64_t at = row0 * p.N + cb * 128 + hl * 8;
+        const uint16_t *d = p.dD + at, *z = p.Z + at;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const bool there = row0 + half + CastTile<T>::kStep * i < p.M;
-        d[i] = there ? ld_once_16(p.dD + at + i * step) : make_uint4(0, 0, 0, 0);
-        z[i] = there && ACT != kActNone ? ld_once_16(p.Z + at + i * step) : make_uint4(0, 0, 0, 0);
-    }
-    F8 v[R];
-    float2 sum[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) sum[x] = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        F8 zz;
-        bf16x8_to_f8(d[i], v[i]);
-        bf16x8_to_f8(z[i], zz);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if (ACT != kActNone) v[i][x] = __fmul2_rn(v[i][x], act_slope2<ACT>(zz[x]));
-            sum[x] = __fadd2_rn(sum[x], v[i][x]);
+        for (int i = 0; i < R; ++i, d += step, z += step) {
+            const bool there = row0 + CastTile<T>::kStep * i < p.M;  // missing rows are zeros
+            cp_async_16(stage + 2 * i * T * 16, there ? d : p.dD, there ? 16 : 0);
+            if (ACT != kActNone) cp_async_16(stage + (2 * i + 1) * T * 16, there ? z : p.Z, there ? 16 : 0);
         }
-    }
-    tile_column_max<T>(v, cm);
-    if (p.part != nullptr) {
-        // the two half-warps exchange four columns each
-        const bool hi = tid & 16;
-        float m[8] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y, sum[2].x, sum[2].y, sum[3].x, sum[3].y};
+        cp_async_commit();
+    };
+    if (blockIdx.x < p.tiles) fetch();
+    for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+        const int64_t row0 = static_cast<int64_t>(rb) * 128, part_at = static_cast<int64_t>(rb) * p.N;
+        const int col = static_cast<int>(cb) * 128;
+        cp_async_wait<0>();
+        F8 v[R];
+        float2 sum[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float keep = hi ? m[4 + x] : m[x], send = hi ? m[x] : m[4 + x];
-            m[x] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+        for (int x = 0; x < 4; ++x) sum[x] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            bf16x8_to_f8(ld_shared_16(stage + 2 * i * T * 16), v[i]);
+            if (ACT != kActNone) {
+                uint4 raw = ld_shared_16(stage + (2 * i + 1) * T * 16);
+                raw = make_uint4(clamp_slope_bf16x2<ACT>(raw.x), clamp_slope_bf16x2<ACT>(raw.y), clamp_slope_bf16x2<ACT>(raw.z),
+                                 clamp_slope_bf16x2<ACT>(raw.w));
+                F8 z;
+                bf16x8_to_f8(raw, z);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[i][x] = __fmul2_rn(v[i][x], act_slope2<ACT>(z[x]));
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sum[x] = __fadd2_rn(sum[x], v[i][x]);
         }
-        *reinterpret_cast<float4*>(cs + (tid >> 5) * CastTile<T>::kStride + hl * 8 + (hi ? 4 : 0)) =
-            make_float4(m[0], m[1], m[2], m[3]);
-    }
-    __syncthreads();
-    const int cols[1] = {col};
-    tile_column_scale<T>(p.out, cm, cr, row0, cols);
-    if (p.part != nullptr && tid < 128) {
-        float s = cs[tid];
+        tile_column_max<T>(v, cm);
+        if (p.part != nullptr) {
+            // the two half-warps exchange four columns each
+            const bool hi = tid & 16;
+            float m[8] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y, sum[2].x, sum[2].y, sum[3].x, sum[3].y};
 #pragma unroll
-        for (int w = 1; w < CastTile<T>::kWarps; ++w) s += cs[w * CastTile<T>::kStride + tid];
-        p.part[static_cast<int64_t>(rb) * p.N + col + tid] = s;
+            for (int x = 0; x < 4; ++x) {
+                const float keep = hi ? m[4 + x] : m[x], send = hi ? m[x] : m[4 + x];
+                m[x] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+            }
+            *reinterpret_cast<float4*>(cs + (tid >> 5) * CastTile<T>::kStride + hl * 8 + (hi ? 4 : 0)) =
+                make_float4(m[0], m[1], m[2], m[3]);
+        }
+        maxima.arrive();
+        rb += step_rb;
+        cb += step_cb;
+        if (cb >= static_cast<uint32_t>(p.nb)) {
+            cb -= p.nb;
+            ++rb;
+        }
+        if (tile + gridDim.x < p.tiles) fetch();
+        maxima.wait();
+        const int cols[1] = {col};
+        tile_column_scale<T>(p.out, cm, cr, row0, cols);
+        if (p.part != nullptr && tid < 128) {
+            float s = cs[tid];
+#pragma unroll
+            for (int w = 1; w < CastTile<T>::kWarps; ++w) s += cs[w * CastTile<T>::kStride + tid];
+            p.part[part_at + col + tid] = s;
+        }
+        joined.arrive();
+        tile_cast_rows_below<T>(p.out, v, row0, p.M, p.N, col);
+        joined.wait();
+        tile_cast_columns<T>(p.out, v, cr, row0, p.N, col);
     }
-    tile_cast_rows_below<T>(p.out, v, row0, p.M, p.N, col);
-    __syncthreads();
-    tile_cast_columns<T>(p.out, v, cr, row0, p.N, col);
 }
 
 }  // namespace dg

@@ -1117,20 +1117,22 @@ dg_status launch_balance_sum(const dg::BalanceParams& p, void* st) {
 }
 
 template <typename L, int EPL>
-dg_status launch_balance_bwd_one(const dg::BalanceBwdParams& p, bool wide, int64_t grid, void* st) {
+dg_status launch_balance_bwd_one(const dg::BalanceBwdParams& p, bool wide, int sms, void* st) {
+    const int64_t all = cdiv64(p.T, dg::kBalanceBwdWarps), cap = static_cast<int64_t>(sms) * dg::balance_bwd_ctas(EPL);
+    const int64_t grid = all < cap ? all : cap;
     return launch_plain(wide ? dg::balance_bwd_kernel<EPL, true, L> : dg::balance_bwd_kernel<EPL, false, L>, p, grid,
                         dg::kBalanceBwdWarps * 32, 0, 1, st);
 }
 template <typename L>
-dg_status launch_balance_bwd(const dg::BalanceBwdParams& p, int64_t grid, void* st) {
+dg_status launch_balance_bwd(const dg::BalanceBwdParams& p, int sms, void* st) {
     const int per = cdiv(p.E, 32);
     const bool wide = full_lanes(p.E, per) && aligned16(p.logits) && aligned16(p.dlogits) && aligned16(p.add);
-    if (per <= 1) return launch_balance_bwd_one<L, 1>(p, wide, grid, st);
-    if (per <= 2) return launch_balance_bwd_one<L, 2>(p, wide, grid, st);
-    if (per <= 4) return launch_balance_bwd_one<L, 4>(p, wide, grid, st);
-    if (per <= 8) return launch_balance_bwd_one<L, 8>(p, wide, grid, st);
-    if (per <= 16) return launch_balance_bwd_one<L, 16>(p, wide, grid, st);
-    return launch_balance_bwd_one<L, 32>(p, wide, grid, st);
+    if (per <= 1) return launch_balance_bwd_one<L, 1>(p, wide, sms, st);
+    if (per <= 2) return launch_balance_bwd_one<L, 2>(p, wide, sms, st);
+    if (per <= 4) return launch_balance_bwd_one<L, 4>(p, wide, sms, st);
+    if (per <= 8) return launch_balance_bwd_one<L, 8>(p, wide, sms, st);
+    if (per <= 16) return launch_balance_bwd_one<L, 16>(p, wide, sms, st);
+    return launch_balance_bwd_one<L, 32>(p, wide, sms, st);
 }
 
 template <typename XT>
@@ -1817,14 +1819,18 @@ dg_status dg_epilogue_bwd(uint8_t* Qr, float* sr, int sr_stride, uint8_t* Qc, fl
     if (!aligned16(Qr) || !aligned16(Qc) || !aligned16(dD) || !aligned16(Z) || !aligned(sr, 4) || !aligned(sc, 4))
         return fail(DG_ERR_MISALIGNED, "Qr, Qc, dD and Z must be 16-byte aligned, the others 4-byte aligned");
     const int64_t rb = cdiv64(M, 128);
-    dg::ActBwdParams p{{Qr, sr, Qc, sc, sr_stride, sc_stride}, dbias ? ws : nullptr, dD, Z, M, N, N / 128};
-    const int64_t grid = rb * p.nb;
+    const int sms = effective_sms();
+    if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
+    const int64_t tiles = rb * (N / 128), grid = tiles < 2 * sms ? tiles : 2 * sms;
+    if (tiles > 0x7FFFFFFF - 2 * sms) return fail(DG_ERR_UNSUPPORTED, "problem too large");
+    dg::ActBwdParams p{{Qr, sr, Qc, sc, sr_stride, sc_stride}, dbias ? ws : nullptr, dD, Z, M, N, N / 128,
+                       static_cast<uint32_t>(tiles)};
     void (*kern)(dg::ActBwdParams) = act == DG_ACT_RELU        ? dg::act_bwd_kernel<dg::kActRelu>
                                      : act == DG_ACT_GELU      ? dg::act_bwd_kernel<dg::kActGelu>
                                      : act == DG_ACT_GELU_TANH ? dg::act_bwd_kernel<dg::kActGeluTanh>
                                      : act == DG_ACT_SILU      ? dg::act_bwd_kernel<dg::kActSilu>
                                                                : dg::act_bwd_kernel<dg::kActNone>;
-    dg_status s = launch_plain(kern, p, grid, dg::kActBwdThreads, 0, 1, stream);
+    dg_status s = launch_plain(kern, p, grid, dg::kActBwdThreads, dg::kActBwdStage, 1, stream);
     if (s != DG_OK || !dbias) return s;
     return launch_column_sum(dbias, ws, nullptr, nullptr, static_cast<int>(rb), N, stream);
 }
@@ -1933,12 +1939,10 @@ dg_status dg_balance_loss_bwd(void* dlogits, const void* add, const float* dloss
     const int sms = effective_sms();
     if (sms <= 0) return fail(DG_ERR_CUDA, "no CUDA device");
     dg::BalanceBwdParams p{dlogits, add, dloss, logits, counts, seq_offsets, T, E, S, score == DG_SCORE_SOFTMAX,
-                           static_cast<int64_t>(T) * k <= 1 << 24,
+                           k,
                            static_cast<float>(static_cast<double>(coef) * E / k)};
-    const int64_t all = cdiv64(T, dg::kBalanceBwdWarps), cap = static_cast<int64_t>(sms) * 4;
-    const int64_t grid = all < cap ? all : cap;
-    return logits_dtype == DG_DTYPE_BF16 ? launch_balance_bwd<uint16_t>(p, grid, stream)
-                                         : launch_balance_bwd<float>(p, grid, stream);
+    return logits_dtype == DG_DTYPE_BF16 ? launch_balance_bwd<uint16_t>(p, sms, stream)
+                                         : launch_balance_bwd<float>(p, sms, stream);
 }
 
 void dg_set_pdl(int enable) { g_pdl.store(enable < 0 ? -1 : (enable ? 1 : 0)); }

@@ -21,6 +21,9 @@ constexpr int kBalanceBwdWarps = 8;
 // logits a lane need the registers.
 __host__ __device__ constexpr int balance_warps(int epl) { return epl <= 16 ? 16 : 8; }
 
+// CTAs of the gradient resident per SM.
+__host__ __device__ constexpr int balance_bwd_ctas(int epl) { return epl <= 8 ? 4 : epl <= 16 ? 2 : 1; }
+
 // The expert of a lane's i-th logit: chunks of a wide load, 32 chunks apart (kWide: rows
 // are 16-byte aligned and every lane has EPL experts), or every 32nd.
 template <int EPL, bool kWide, typename L>
@@ -80,9 +83,10 @@ __device__ __forceinline__ int seq_of(const int32_t* offsets, int S, int T, int 
 
 // p of one token's E logits; `slope`: 1 - s of a sigmoid (not written for the softmax).
 // A token without a finite logit has p = 0.
+// Returns the largest p.
 template <int EPL>
-__device__ __forceinline__ void balance_probs(const float (&l)[EPL], int softmax, float (&p)[EPL], float (&slope)[EPL]) {
-    float sum = 0.f;
+__device__ __forceinline__ float balance_probs(const float (&l)[EPL], int softmax, float (&p)[EPL], float (&slope)[EPL]) {
+    float sum = 0.f, top = 1.f;  // the softmax's largest exponential is 1
     if (softmax) {
         float m = l[0];
 #pragma unroll
@@ -106,11 +110,16 @@ __device__ __forceinline__ void balance_probs(const float (&l)[EPL], int softmax
             slope[i] = l[i] > 0.f ? small : r;
             sum += p[i];
         }
+        top = p[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) top = fmaxf(top, p[i]);
+        top = warp_max(top);
     }
     sum = warp_sum(sum);
     const float inv = sum > 0.f || sum != sum ? __frcp_rn(sum) : 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) p[i] *= inv;
+    return top * inv;
 }
 
 template <int EPL, bool kWide, typename L>
@@ -290,16 +299,17 @@ struct BalanceBwdParams {
     const int32_t* offsets;
     int T, E, S;
     int softmax;
-    int exact;               // no count passes 2^24: floats hold it
+    int k;
     float scale;             // coef E / k
 };
 
 // A warp takes runs of neighbouring tokens.  f_j - sum f_e p_e is formed from the
-// counts' distances to that of the token's likeliest expert c, whole numbers:
-// (n_j - n_c) - sum_e p_e (n_e - n_c) has no large terms that cancel where one expert has
-// nearly all the weight, or where all loads are nearly alike.
+// counts' distances to one of them, n_j - n_o - sum_e p_e (n_e - n_o), whole numbers that are
+// rounded once: to the mean load, so that nothing large cancels where all loads are nearly
+// alike, or, for a token whose likeliest expert has more than half of p, to that expert's,
+// whose own term is then zero, so that nothing cancels where it has nearly all.
 template <int EPL, bool kWide, typename L>
-__global__ void __launch_bounds__(kBalanceBwdWarps * 32)
+__global__ void __launch_bounds__(kBalanceBwdWarps * 32, balance_bwd_ctas(EPL))
 balance_bwd_kernel(const BalanceBwdParams p) {
     griddep_wait();
     griddep_launch_dependents();
@@ -312,7 +322,7 @@ balance_bwd_kernel(const BalanceBwdParams p) {
     if (t0 < t1) balance_load<EPL, kWide>(raw, logits + static_cast<int64_t>(t0) * p.E, p.E, lane);
     const int len = seq_offset(p.offsets, p.S, p.T) - seq_offset(p.offsets, 0, p.T);
     const float up = p.dloss != nullptr ? *p.dloss : 1.f;
-    float n[EPL];         // whole numbers; as float where those are exact, else their bits
+    float n[EPL];         // counts less the mean load
     int end = t0, s = 0;  // the sequence s holds tokens up to `end`
     float k = 0.f;
     for (int t = t0; t < t1; ++t) {
@@ -327,11 +337,11 @@ balance_bwd_kernel(const BalanceBwdParams p) {
             if (end <= t) end = t + 1;  // offsets that fall
             k = in && len > 0 && end > first ? p.scale * up / (static_cast<float>(len) * static_cast<float>(end - first)) : 0.f;
             if (!in) s = -1;
+            const int mean = in ? static_cast<int>(static_cast<int64_t>(end - first) * p.k / p.E) : 0;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const int e = balance_expert<EPL, kWide, L>(lane, i);
-                const int32_t c = s >= 0 && (kWide || e < p.E) ? p.counts[static_cast<int64_t>(s) * p.E + e] : 0;
-                n[i] = p.exact ? static_cast<float>(c) : __int_as_float(c);
+                n[i] = s >= 0 && (kWide || e < p.E) ? static_cast<float>(p.counts[static_cast<int64_t>(s) * p.E + e] - mean) : 0.f;
             }
         }
         const int64_t at = static_cast<int64_t>(t) * p.E;
@@ -345,24 +355,23 @@ balance_bwd_kernel(const BalanceBwdParams p) {
         }
         if (s >= 0) {
             float q[EPL], slope[EPL];
-            balance_probs<EPL>(l, p.softmax, q, slope);
-            float best = -1.f, nc = 0.f;
+            const float top = balance_probs<EPL>(l, p.softmax, q, slope);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (q[i] > best) {
-                    best = q[i];
-                    nc = n[i];
+            for (int i = 0; i < EPL; ++i) l[i] = n[i];
+            if (top > 0.5f) {
+                const int32_t* counts = p.counts + static_cast<int64_t>(s) * p.E;
+                int best = -1;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) best = q[i] > 0.5f ? balance_expert<EPL, kWide, L>(lane, i) : best;
+                best = __reduce_max_sync(0xffffffffu, best);
+                const int32_t from = best >= 0 ? counts[best] : 0;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const int e = balance_expert<EPL, kWide, L>(lane, i);
+                    l[i] = kWide || e < p.E ? static_cast<float>(counts[e] - from) : 0.f;
                 }
-            const uint32_t who = __ballot_sync(0xffffffffu, best == warp_max(best));
-            nc = __shfl_sync(0xffffffffu, nc, who ? __ffs(who) - 1 : 0);
-            float mean = 0.f;
-            if (p.exact) {
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) l[i] = n[i] - nc;
-            } else {
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) l[i] = static_cast<float>(__float_as_int(n[i]) - __float_as_int(nc));
             }
+            float mean = 0.f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) mean = fmaf(q[i], l[i], mean);
             mean = warp_sum(mean);
