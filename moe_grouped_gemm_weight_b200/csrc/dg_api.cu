@@ -1138,7 +1138,10 @@ dg_status launch_balance_bwd(const dg::BalanceBwdParams& p, int sms, void* st) {
 template <typename XT>
 dg_status launch_norm(const dg::NormParams& p, int64_t grid, void* st) {
     const int threads = p.plan.threads * p.plan.groups, smem = static_cast<int>(p.plan.slot) * p.plan.groups * p.plan.depth;
-    return launch_plain(p.N <= dg::kNormHeldColumns ? dg::norm_residual_kernel<XT, true> : dg::norm_residual_kernel<XT, false>, p,
+    return launch_plain(p.N > dg::kNormHeldColumns                              ? dg::norm_residual_kernel<XT, false, false>
+                        : p.N == 4 * dg::kNormRuns * p.plan.threads ? dg::norm_residual_kernel<XT, true, true>
+                                                                    : dg::norm_residual_kernel<XT, true, false>,
+                        p,
                         grid, threads, dg::kNormSharedBytes + smem, 1, st, dg::kNormSharedBytes + dg::kNormSmem);
 }
 template <typename XT>
@@ -1147,7 +1150,9 @@ dg_status launch_norm_bwd(const dg::NormBwdParams& p, int64_t grid, void* st) {
     int smem = static_cast<int>(p.plan.slot) * p.plan.groups * p.plan.depth;
     const int join = p.plan.groups > 1 ? p.plan.groups * 2 * p.N * 4 : 0;  // at most 8 KiB a 128 columns of 1024 threads
     if (smem < join) smem = join;
-    return launch_plain(p.N <= dg::kNormHeldColumns ? dg::norm_residual_bwd_kernel<XT, true> : dg::norm_residual_bwd_kernel<XT, false>,
+    return launch_plain(p.N > dg::kNormHeldColumns                              ? dg::norm_residual_bwd_kernel<XT, false, false>
+                        : p.N == 4 * dg::kNormRuns * p.plan.threads ? dg::norm_residual_bwd_kernel<XT, true, true>
+                                                                    : dg::norm_residual_bwd_kernel<XT, true, false>,
                         p, grid, threads, dg::kNormSharedBytes + smem, 1, st, dg::kNormSharedBytes + dg::kNormSmem);
 }
 

@@ -57,10 +57,7 @@ __device__ __forceinline__ void store_f4(uint16_t* p, const F4& f) {
 __device__ __forceinline__ void store_f4(float* p, const F4& f) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
 }
-__device__ __forceinline__ float dot_f4(const F4& a, const F4& b, float s) {
-    const float2 d = __ffma2_rn(a[1], b[1], __ffma2_rn(a[0], b[0], make_float2(s, 0.f)));
-    return d.x + d.y;
-}
+__device__ __forceinline__ void dot_f4(const F4& a, const F4& b, float2& s) { s = __ffma2_rn(a[1], b[1], __ffma2_rn(a[0], b[0], s)); }
 // Four weights, ones without any.
 __device__ __forceinline__ void load_weights(const float* w, int run, F4& f) {
     const float4 v = w != nullptr ? *reinterpret_cast<const float4*>(w + run * 4) : make_float4(1.f, 1.f, 1.f, 1.f);
@@ -68,13 +65,13 @@ __device__ __forceinline__ void load_weights(const float* w, int run, F4& f) {
     f[1] = make_float2(v.z, v.w);
 }
 // Weights of a thread's runs, held over all its rows or loaded for each.
-template <bool HELD>
+template <bool HELD, bool FULL>
 struct NormWeights {
     F4 w[HELD ? kNormRuns : 1];
     __device__ __forceinline__ void load(const float* p, int tid, int threads, int runs) {
         if constexpr (HELD)
 #pragma unroll
-            for (int j = 0; j < kNormRuns; ++j) load_weights(tid + j * threads < runs ? p : nullptr, tid + j * threads, w[j]);
+            for (int j = 0; j < kNormRuns; ++j) load_weights(FULL || tid + j * threads < runs ? p : nullptr, tid + j * threads, w[j]);
     }
     __device__ __forceinline__ void get(const float* p, int j, int run, F4& f) const {
         if constexpr (HELD) {
@@ -158,6 +155,13 @@ struct NormGroup {
     __device__ __forceinline__ void barrier() const {
         if (warps == 1) __syncwarp(); else named_barrier_sync(1 + group, threads);
     }
+    // Zeros in `bytes` of each slot, from `from`: a missing tensor's row.
+    __device__ __forceinline__ void clear(uint32_t from, uint32_t bytes) const {
+        for (int d = 0; d < depth; ++d)
+            for (uint32_t b = tid * 8; b < bytes; b += threads * 8)
+                asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(ring + d * slot_bytes + from + b), "r"(0) : "memory");
+        barrier();
+    }
     __device__ __forceinline__ uint32_t at() const { return ring + static_cast<uint32_t>(slot) * slot_bytes; }
     __device__ __forceinline__ void wait() const { mbar_wait(full + slot, phase, abort_flag); }  // the row has arrived
     __device__ __forceinline__ void next() {
@@ -189,7 +193,8 @@ struct NormParams {
 
 // Thread i of a group holds the runs of 4 columns i, i + threads, ... of its row: a warp
 // holds whole 1x128 tiles, and reads and writes whole lines.  Bound by HBM.
-template <typename XT, bool HELD>
+// FULL: every thread has four runs.
+template <typename XT, bool HELD, bool FULL>
 __global__ void __launch_bounds__(HELD ? kNormHeldThreads : kNormMaxThreads)
 norm_residual_kernel(const __grid_constant__ NormParams p) {
     constexpr int CH = kNormRuns;
@@ -214,52 +219,55 @@ norm_residual_kernel(const __grid_constant__ NormParams p) {
     if (g.tid == 0)
         for (int i = 0; i < p.plan.depth && t + static_cast<int64_t>(i) * workers < p.T; ++i)
             fetch(t + static_cast<int64_t>(i) * workers, i);
-    NormWeights<HELD> post, pre;
-    post.load(p.w_post, g.tid, g.threads, runs);
+    if (p.X == nullptr) g.clear(0, y_at);
+    if (p.Y == nullptr) g.clear(y_at, p.N * 2);
+    NormWeights<HELD, FULL> post, pre;
+    post.load(p.Y != nullptr ? p.w_post : nullptr, g.tid, g.threads, runs);
     pre.load(p.w_pre, g.tid, g.threads, runs);
+    const uint32_t x_tid = g.tid * 4 * static_cast<uint32_t>(sizeof(XT)), x_step = g.threads * 4 * static_cast<uint32_t>(sizeof(XT));
+    const uint32_t y_tid = y_at + g.tid * 8, y_step = g.threads * 8;
     float gate = p.gate != nullptr && t < p.T ? p.gate[t] : 1.f;
     for (; t < p.T; t += workers) {
-        const int64_t row = t * p.N;
+        const int64_t row = t * p.N + g.tid * 4;
         float* part = sh.part[g.group][g.turn];
-        const float k0 = p.scale * gate;
+        const float k0 = p.Y != nullptr ? p.scale * gate : -0.f;  // without a block's output u is x to the bit
         if (p.gate != nullptr && t + workers < p.T) gate = p.gate[t + workers];  // the next row's, on its way meanwhile
         g.wait();
         const uint32_t at = g.at();
         F4 u[CH], y[CH];
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = g.tid + j * g.threads;
-            zero_f4(u[j]);
-            zero_f4(y[j]);
-            if (c < runs) {
-                if (p.X != nullptr) shared_f4<XT>(at + c * 4 * sizeof(XT), u[j]);
-                if (p.Y != nullptr) shared_f4<uint16_t>(at + y_at + c * 8, y[j]);
+            if (FULL || g.tid + j * g.threads < runs) {
+                shared_f4<XT>(at + x_tid + j * x_step, u[j]);
+                shared_f4<uint16_t>(at + y_tid + j * y_step, y[j]);
+            } else {
+                zero_f4(u[j]);
+                zero_f4(y[j]);
             }
         }
         float ry = 1.f;
-        if (p.Y != nullptr) {
-            if (p.post_norm) {
-                float s[1] = {0.f};
+        float s[1];
+        if (p.post_norm && p.Y != nullptr) {
+            float2 d = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int j = 0; j < CH; ++j) s[0] = dot_f4(y[j], y[j], s[0]);
-                g.sum<1>(s, part);
-                ry = __frsqrt_rn(fmaf(s[0], inv_n, p.eps));
-            }
-            const float k = k0 * ry;
-#pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                const int c = g.tid + j * g.threads;
-                if (!HELD && c >= runs) continue;
-                F4 w;
-                post.get(p.w_post, j, c, w);
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    u[j][x] = __ffma2_rn(__fmul2_rn(y[j][x], make_float2(k, k)), w[x], u[j][x]);
-            }
+            for (int j = 0; j < CH; ++j) dot_f4(y[j], y[j], d);
+            s[0] = d.x + d.y;
+            g.sum<1>(s, part);
+            ry = __frsqrt_rn(fmaf(s[0], inv_n, p.eps));
         }
-        float s[1] = {0.f};
+        const float k = k0 * ry;
+        float2 d = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < CH; ++j) s[0] = dot_f4(u[j], u[j], s[0]);
+        for (int j = 0; j < CH; ++j) {
+            F4 w;
+            if (HELD || g.tid + j * g.threads < runs) {
+                post.get(p.Y != nullptr ? p.w_post : nullptr, j, g.tid + j * g.threads, w);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) u[j][x] = __ffma2_rn(__fmul2_rn(y[j][x], make_float2(k, k)), w[x], u[j][x]);
+            }
+            dot_f4(u[j], u[j], d);
+        }
+        s[0] = d.x + d.y;
         g.sum<1>(s, part + 32);
         // Every thread of the group has its values in registers: the slot is free.
         if (g.tid == 0 && t + ahead < p.T) fetch(t + ahead, g.slot);
@@ -269,14 +277,13 @@ norm_residual_kernel(const __grid_constant__ NormParams p) {
             XT* to = static_cast<XT*>(p.U) + row;
 #pragma unroll
             for (int j = 0; j < CH; ++j)
-                if (g.tid + j * g.threads < runs) store_f4(to + (g.tid + j * g.threads) * 4, u[j]);
+                if (FULL || g.tid + j * g.threads < runs) store_f4(to + j * g.threads * 4, u[j]);
         }
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = g.tid + j * g.threads;
             F4 w;
-            if (HELD || c < runs) {
-                pre.get(p.w_pre, j, c, w);
+            if (HELD || g.tid + j * g.threads < runs) {
+                pre.get(p.w_pre, j, g.tid + j * g.threads, w);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) u[j][x] = __fmul2_rn(__fmul2_rn(u[j][x], make_float2(ru, ru)), w[x]);
             }
@@ -284,7 +291,7 @@ norm_residual_kernel(const __grid_constant__ NormParams p) {
         if (p.H != nullptr) {
 #pragma unroll
             for (int j = 0; j < CH; ++j)
-                if (g.tid + j * g.threads < runs) store_f4(p.H + row + (g.tid + j * g.threads) * 4, u[j]);
+                if (FULL || g.tid + j * g.threads < runs) store_f4(p.H + row + j * g.threads * 4, u[j]);
         }
         if (p.Q != nullptr) {
             float a[CH];
@@ -299,7 +306,7 @@ norm_residual_kernel(const __grid_constant__ NormParams p) {
                 const float r = __fdiv_rn(448.f, a[j]);
                 const uint32_t lo = __nv_cvt_float2_to_fp8x2(__fmul2_rn(u[j][0], make_float2(r, r)), __NV_SATFINITE, __NV_E4M3);
                 const uint32_t hi = __nv_cvt_float2_to_fp8x2(__fmul2_rn(u[j][1], make_float2(r, r)), __NV_SATFINITE, __NV_E4M3);
-                *reinterpret_cast<uint32_t*>(p.Q + row + c * 4) = __byte_perm(lo, hi, 0x5410);
+                *reinterpret_cast<uint32_t*>(p.Q + row + j * g.threads * 4) = __byte_perm(lo, hi, 0x5410);
                 if (g.lane == 0) p.sq[(c >> 5) * p.sq_stride + t] = __fdiv_rn(a[j], 448.f);
             }
         }
@@ -338,7 +345,8 @@ struct NormBwdParams {
 // row gives all three sums and a second one, from shared memory, the results.  The weights'
 // gradients of a thread's columns stay in its registers until the last row; the groups'
 // are joined in order.
-template <typename XT, bool HELD>
+// FULL: every thread has four runs.
+template <typename XT, bool HELD, bool FULL>
 __global__ void __launch_bounds__(HELD ? kNormHeldThreads : kNormMaxThreads)
 norm_residual_bwd_kernel(const __grid_constant__ NormBwdParams p) {
     constexpr int CH = kNormRuns;
@@ -359,23 +367,25 @@ norm_residual_bwd_kernel(const __grid_constant__ NormBwdParams p) {
         if (p.dH != nullptr) bulk_load(to + 2 * xs, p.dH + t * p.N, ys, bar);
         if (p.Y != nullptr) bulk_load(to + 2 * xs + ys, p.Y + t * p.N, ys, bar);
     };
-    // Values of run c of the row in the slot: dU, u, y, dH.
-    auto get = [&](uint32_t at, int c, F4& e, F4& a, F4& b, F4& h) {
-        zero_f4(e);
-        zero_f4(h);
-        zero_f4(b);
-        if (p.dU != nullptr) shared_f4<XT>(at + c * 4 * sizeof(XT), e);
-        shared_f4<XT>(at + xs + c * 4 * sizeof(XT), a);
-        if (p.dH != nullptr) shared_f4<uint16_t>(at + 2 * xs + c * 8, h);
-        if (p.Y != nullptr) shared_f4<uint16_t>(at + 2 * xs + ys + c * 8, b);
+    const uint32_t x_tid = g.tid * 4 * static_cast<uint32_t>(sizeof(XT)), x_step = g.threads * 4 * static_cast<uint32_t>(sizeof(XT));
+    const uint32_t y_tid = 2 * xs + g.tid * 8, y_step = g.threads * 8;
+    // Values of the thread's j-th run of the row in the slot: dU, u, y, dH.
+    auto get = [&](uint32_t at, int j, F4& e, F4& a, F4& b, F4& h) {
+        shared_f4<XT>(at + x_tid + j * x_step, e);
+        shared_f4<XT>(at + xs + x_tid + j * x_step, a);
+        shared_f4<uint16_t>(at + y_tid + j * y_step, h);
+        shared_f4<uint16_t>(at + ys + y_tid + j * y_step, b);
     };
     int64_t t = blockIdx.x + static_cast<int64_t>(gridDim.x) * g.group;
     const int64_t ahead = static_cast<int64_t>(p.plan.depth) * workers;
     if (g.tid == 0)
         for (int i = 0; i < p.plan.depth && t + static_cast<int64_t>(i) * workers < p.T; ++i)
             fetch(t + static_cast<int64_t>(i) * workers, i);
-    NormWeights<HELD> post, pre;
-    post.load(p.w_post, g.tid, g.threads, runs);
+    if (p.dU == nullptr) g.clear(0, xs);
+    if (p.dH == nullptr) g.clear(2 * xs, ys);
+    if (p.Y == nullptr) g.clear(2 * xs + ys, ys);
+    NormWeights<HELD, FULL> post, pre;
+    post.load(p.Y != nullptr ? p.w_post : nullptr, g.tid, g.threads, runs);
     pre.load(p.w_pre, g.tid, g.threads, runs);
     F4 dpost[CH], dpre[CH];
 #pragma unroll
@@ -386,7 +396,7 @@ norm_residual_bwd_kernel(const __grid_constant__ NormBwdParams p) {
     float2 r_next = t < p.T ? *reinterpret_cast<const float2*>(p.rstd + 2 * t) : make_float2(0.f, 0.f);
     float gate = p.gate != nullptr && t < p.T ? p.gate[t] : 1.f;
     for (; t < p.T; t += workers) {
-        const int64_t row = t * p.N;
+        const int64_t row = t * p.N + g.tid * 4;
         const float2 r = r_next, ru = make_float2(r.y, r.y), ry = make_float2(r.x, r.x);
         const float k = p.scale * gate;
         if (t + workers < p.T) {  // the next row's, on their way meanwhile
@@ -395,14 +405,15 @@ norm_residual_bwd_kernel(const __grid_constant__ NormBwdParams p) {
         }
         g.wait();
         const uint32_t at = g.at();
-        float s[3] = {0.f, 0.f, 0.f};
+        float2 d[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) d[i] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = g.tid + j * g.threads;
-            if (c >= runs) continue;
+            if (!FULL && g.tid + j * g.threads >= runs) continue;
             F4 e, a, b, h, w;
-            get(at, c, e, a, b, h);
-            pre.get(p.w_pre, j, c, w);
+            get(at, j, e, a, b, h);
+            pre.get(p.w_pre, j, g.tid + j * g.threads, w);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 a[x] = __fmul2_rn(a[x], ru);
@@ -410,39 +421,39 @@ norm_residual_bwd_kernel(const __grid_constant__ NormBwdParams p) {
                 w[x] = __fmul2_rn(h[x], w[x]);
                 e[x] = __ffma2_rn(ru, w[x], e[x]);
             }
-            s[0] = dot_f4(a, w, s[0]);
-            post.get(p.w_post, j, c, w);
+            dot_f4(a, w, d[0]);
+            post.get(p.Y != nullptr ? p.w_post : nullptr, j, g.tid + j * g.threads, w);
 #pragma unroll
             for (int x = 0; x < 2; ++x) w[x] = __fmul2_rn(w[x], __fmul2_rn(b[x], ry));
-            s[1] = dot_f4(e, w, s[1]);
-            s[2] = dot_f4(a, w, s[2]);
+            dot_f4(e, w, d[1]);
+            dot_f4(a, w, d[2]);
         }
+        float s[3] = {d[0].x + d[0].y, d[1].x + d[1].y, d[2].x + d[2].y};
         g.sum<3>(s, sh.part[g.group][g.turn]);
         const float rm = r.y * (s[0] * inv_n);
         const float dot = fmaf(-rm, s[2], s[1]);
         if (p.dgate != nullptr && g.tid == 0) p.dgate[t] = p.scale * dot;
         const float sub = p.post_norm ? -dot * inv_n : 0.f;
         const float kr = k * r.x;  // r_y is 1 without the norm
+        XT* dx = static_cast<XT*>(p.dX) + row;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int c = g.tid + j * g.threads;
-            if (c >= runs) continue;
+            if (!FULL && g.tid + j * g.threads >= runs) continue;
             F4 e, a, b, h, w;
-            get(at, c, e, a, b, h);
-            pre.get(p.w_pre, j, c, w);
+            get(at, j, e, a, b, h);
+            pre.get(p.w_pre, j, g.tid + j * g.threads, w);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 e[x] = __ffma2_rn(__fmul2_rn(a[x], ru), make_float2(-rm, -rm), __ffma2_rn(ru, __fmul2_rn(h[x], w[x]), e[x]));
-            if (p.dX != nullptr) store_f4(static_cast<XT*>(p.dX) + row + c * 4, e);
-            if (p.Y == nullptr) continue;
-            post.get(p.w_post, j, c, w);
+            if (p.dX != nullptr) store_f4(dx + j * g.threads * 4, e);
+            post.get(p.Y != nullptr ? p.w_post : nullptr, j, g.tid + j * g.threads, w);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 b[x] = __fmul2_rn(b[x], ry);
                 dpost[j][x] = __ffma2_rn(__fmul2_rn(e[x], make_float2(k, k)), b[x], dpost[j][x]);
                 e[x] = __fmul2_rn(__ffma2_rn(b[x], make_float2(sub, sub), __fmul2_rn(e[x], w[x])), make_float2(kr, kr));
             }
-            if (p.dY != nullptr) store_f4(p.dY + row + c * 4, e);
+            if (p.dY != nullptr) store_f4(p.dY + row + j * g.threads * 4, e);
         }
         g.barrier();  // the slot is free
         if (g.tid == 0 && t + ahead < p.T) fetch(t + ahead, g.slot);
