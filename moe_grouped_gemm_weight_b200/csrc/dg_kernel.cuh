@@ -102,6 +102,11 @@ struct EpiCall : EpiParams {
     static constexpr bool kRes = RES;
 };
 
+template <typename PT>
+__host__ __device__ constexpr bool has_residual() {
+    if constexpr (std::is_same<PT, Params>::value || std::is_same<PT, EpiParams>::value) return false; else return PT::kRes;
+}
+
 // One unit of work of this CTA: a tile (index t) over K blocks [kb0, kb1);
 // slice = -1 for a whole tile, else the K slice of a split tail tile.
 struct Work {
@@ -258,8 +263,11 @@ struct EpiTable {
     uint64_t res_full;                            // the tile's residual has arrived in the staging buffers
     uint64_t warp_full[Cfg<BN>::kEpiWarpsC];      // ... a warp's share of it, where the warp itself asked for it
     uint64_t pair_bar[4];
+    alignas(16) int4 wanted;                      // EpiFetch: first row and column, count and parity
+    int sent;                                     // 1 + count of the last tile whose residual was asked for
 
     __device__ void init() {  // one thread, before the roles part
+        sent = 0;
         mbar_init(&res_full, 1);
         for (int w = 0; w < Cfg<BN>::kEpiWarpsC; ++w) mbar_init(warp_full + w, 1);
         for (int w = 0; w < 4; ++w) mbar_init(pair_bar + w, 2);
@@ -418,21 +426,19 @@ struct EpiWarp {
     }
 };
 
-// What the scale producer (a whole warp) does for that epilogue.
-template <int BN>
+// What the scale producer (a whole warp) does for that epilogue.  Its loop is as tight as
+// the promotion's (with a few registers more it spilled, and each K block took 24 ns
+// longer), so the tile whose residual is still to be asked for lies in shared memory, and
+// only its ring slot in a register.
+template <int BN, typename PT>
 struct EpiFetch {
     using C = Cfg<BN>;
     static constexpr int kPieces = C::kColsPerWarp / 32;
-    const EpiParams& p;
-    EpiTable<BN>* tb;
-    uint8_t* out;        // the staging buffers
-    bool pending, sent;  // a tile's residual is still to be asked for; one is on its way
-    int it, m0, n0;      // of that tile
-    int slot;            // ... the ring slot of its first scales, whose release says that the
-    uint32_t phase;      // previous tile's stores have left the buffers, and that release's parity
+    int pending = -1;  // ring slot of that tile's first scales: their release says that the
+                       // previous tile's stores have left the staging buffers
 
     // With a ring slot for the tile's first scales: its bias, which lands with them.
-    __device__ __forceinline__ void begin(const Tile& tl, int tile, int lane) {
+    static __device__ __forceinline__ void begin(const EpiParams& p, EpiTable<BN>* tb, const Tile& tl, int tile, int lane) {
         if (p.bias == nullptr) return;
         const uint32_t to = smem_u32(tb->bias[tile % EpiTable<BN>::kBiasSlots]);
 #pragma unroll
@@ -442,47 +448,44 @@ struct EpiFetch {
             if (j < BN) cp_async_16(to + j * 4, p.bias + (there ? tl.n0 + j : 0), there ? 16 : 0);
         }
     }
-    // Behind the tile's first scales, copied to `ring` slot in a pass of parity `ring_phase`.
-    __device__ __forceinline__ void want(const Tile& tl, int tile, int ring_slot, uint32_t ring_phase, int lane) {
-        if (p.residual == nullptr) return;
+    // Behind the tile's first scales, copied to ring slot `slot` in a pass of parity `phase`.
+    __device__ __forceinline__ void want(const EpiParams& p, EpiTable<BN>* tb, const Tile& tl, int tile, int slot, uint32_t phase, int lane) {
         if (p.Z != nullptr) {
             // The promotion warps ask for it themselves, between Z's stores and D's.
             const int px = tl.n0 + (lane & 7) * 32;
             if (px < p.N && (lane & 7) * 32 < BN) tma_prefetch_2d(&p.tmR, px, tl.m0 + (lane >> 3) * 32);
             return;
         }
-        pending = true;
-        it = tile;
-        m0 = tl.m0;
-        n0 = tl.n0;
-        slot = ring_slot;
-        phase = ring_phase;
+        if (lane == 0) tb->wanted = make_int4(tl.m0, tl.n0, tile, static_cast<int>(phase));
+        pending = slot;
+        __syncwarp();
     }
     // Once the slot's release has been waited for.
-    __device__ __forceinline__ void send(int lane) {
-        pending = false;
-        sent = true;
-        const int n = min(BN / 32, (p.N - n0 + 31) / 32);  // pieces across, of four rows of them
-        if (lane == 0) mbar_arrive_expect_tx(&tb->res_full, static_cast<uint32_t>(4 * n * kStageOutBytes));
+    __device__ __forceinline__ void send(const EpiParams& p, EpiTable<BN>* tb, uint8_t* out, int lane) {
+        pending = -1;
+        const int4 t = tb->wanted;
+        const int n = min(BN / 32, (p.N - t.y + 31) / 32);  // pieces across, of four rows of them
+        if (lane == 0) {
+            tb->sent = 1 + t.z;
+            mbar_arrive_expect_tx(&tb->res_full, static_cast<uint32_t>(4 * n * kStageOutBytes));
+        }
         __syncwarp();
-        const uint64_t policy = l2_policy_evict_first();
         const int quarter = lane & 3, pc = lane >> 2;  // up to 8 pieces across
-        const int half = pc / kPieces;
         if (pc < n)
-            tma_load_2d(smem_u32(out) + ((half * 4 + quarter) * kPieces + pc % kPieces) * kStageOutBytes, &p.tmR, &tb->res_full,
-                        n0 + pc * 32, m0 + quarter * 32, policy);
+            tma_load_2d(smem_u32(out) + ((pc / kPieces * 4 + quarter) * kPieces + pc % kPieces) * kStageOutBytes, &p.tmR, &tb->res_full,
+                        t.y + pc * 32, t.x + quarter * 32, l2_policy_evict_first());
         __syncwarp();
     }
     // `sempty`: the scale ring's release barriers.  false: a wait ran out.
-    __device__ __forceinline__ bool flush(uint64_t* sempty, int lane, volatile int* abort_flag) {
-        if (!pending) return true;
-        if (!mbar_wait(sempty + slot, phase, abort_flag)) return false;
-        send(lane);
+    __device__ __forceinline__ bool flush(const EpiParams& p, EpiTable<BN>* tb, uint8_t* out, uint64_t* sempty, int lane, volatile int* abort_flag) {
+        if (pending < 0) return true;
+        if (!mbar_wait(sempty + pending, tb->wanted.w, abort_flag)) return false;
+        send(p, tb, out, lane);
         return true;
     }
     // No copy into shared memory may still be on its way when the CTA exits.
-    __device__ __forceinline__ void end() {
-        if (sent) mbar_wait_drain(&tb->res_full, it & 1);
+    static __device__ __forceinline__ void end(EpiTable<BN>* tb) {
+        if (tb->sent) mbar_wait_drain(&tb->res_full, (tb->sent - 1) & 1);
     }
 };
 
@@ -505,6 +508,7 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
     constexpr bool kAmn = (LAYOUT & 1) != 0;
     constexpr bool kBmn = (LAYOUT & 2) != 0;
     constexpr bool kEpi = !std::is_same<PT, Params>::value;
+    constexpr bool kRes = has_residual<PT>();
     static_assert(!kEpi || (MODE == kDense && LAYOUT == 0 && SP == C::kColsPerWarp / 32),
                   "epilogue: dense NT calls, a staging buffer per piece");
     static_assert(!kEpi || sizeof(EpiTable<BN>) <= 4 * (kMaxMaskedGroups + 1) + kEpiTableBytes, "the table does not fit");
@@ -721,7 +725,7 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
         const int row_limit = p.M;  // rows of sa that exist (dense M, M_total or M_max)
         auto epi = [&] {
             if constexpr (kEpi)
-                return EpiFetch<BN>{p, epi_table, sOut, false, false, 0, 0, 0, 0, 0u};
+                return EpiFetch<BN, PT>{};
             else
                 return 0;
         }();
@@ -730,8 +734,8 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
             const Tile tl = decode_tile<BN, MODE>(p, w.t, m_blocks, mb_prefix);
             if (!tl.valid) continue;
             group_k_range<MODE>(p, tl, w);
-            if constexpr (kEpi) {
-                if (!epi.flush(sempty, lane, abort_flag)) break;
+            if constexpr (kRes) {
+                if (!epi.flush(p, epi_table, sOut, sempty, lane, abort_flag)) break;
             }
             const float* sa_base = p.sa + (MODE == kMasked ? static_cast<int64_t>(tl.g) * nkb * p.sa_stride : 0);
             const float* sb_g = p.sb + (MODE == kKGrouped ? 0 : static_cast<int64_t>(tl.g) * p.nbn * nkb);
@@ -743,9 +747,11 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
             bool ok = true;
             for (int kg = w.kb0; kg < w.kb1; kg += kScaleGroup) {
                 if (!mbar_wait(sempty + slot, sphase ^ 1u, abort_flag)) { ok = false; break; }
+                if constexpr (kRes) {
+                    if (slot == epi.pending) epi.send(p, epi_table, sOut, lane);
+                }
                 if constexpr (kEpi) {
-                    if (epi.pending && slot == epi.slot) epi.send(lane);
-                    if (kg == w.kb0 && w.slice <= 0) epi.begin(tl, it, lane);
+                    if (kg == w.kb0 && w.slice <= 0) epi.begin(p, epi_table, tl, it, lane);
                 }
                 const int n = min(kScaleGroup, w.kb1 - kg);
                 for (int j = 0; j < n; ++j) {
@@ -758,16 +764,16 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
                                    nb_ok ? 4u : 0u);
                 }
                 cp_async_arrive(sfull + slot);
-                if constexpr (kEpi) {
-                    if (kg == w.kb0 && w.slice <= 0) epi.want(tl, it, slot, sphase, lane);
+                if constexpr (kRes) {
+                    if (kg == w.kb0 && w.slice <= 0) epi.want(p, epi_table, tl, it, slot, sphase, lane);
                 }
                 if (++slot == kScaleGroups) { slot = 0; sphase ^= 1u; }
             }
             if (!ok) break;
         }
-        if constexpr (kEpi) {
-            epi.flush(sempty, lane, abort_flag);
-            epi.end();
+        if constexpr (kRes) {
+            epi.flush(p, epi_table, sOut, sempty, lane, abort_flag);
+            epi.end(epi_table);
         }
         // Let every copy land before the CTA can exit.
         asm volatile("cp.async.wait_all;" ::: "memory");
