@@ -260,16 +260,13 @@ struct EpiTable {
     static constexpr int kBiasSlots = kScaleGroups + 1;
     float bias[kBiasSlots][BN];
     float pair_max[4][2][2][BN == 128 ? 32 : 1];  // [quarter][turn][half][row]: see EpiWarp::cast
-    uint64_t res_full;                            // the tile's residual has arrived in the staging buffers
-    uint64_t warp_full[Cfg<BN>::kEpiWarpsC];      // ... a warp's share of it, where the warp itself asked for it
     uint64_t pair_bar[4];
-    alignas(16) int4 wanted;                      // EpiFetch: first row and column, count and parity
-    int sent;                                     // 1 + count of the last tile whose residual was asked for
+    uint64_t free_bar;                            // tiles of one scale group: the staging buffers are free
+    int sent;                                     // epi_fetch: 1 + ring slot and 256 x parity of the last residual's arrival
 
     __device__ void init() {  // one thread, before the roles part
         sent = 0;
-        mbar_init(&res_full, 1);
-        for (int w = 0; w < Cfg<BN>::kEpiWarpsC; ++w) mbar_init(warp_full + w, 1);
+        mbar_init(&free_bar, Cfg<BN>::kEpiWarpsC);
         for (int w = 0; w < 4; ++w) mbar_init(pair_bar + w, 2);
     }
 };
@@ -277,8 +274,7 @@ struct EpiTable {
 // The epilogue of EpiParams calls, for one promotion warp's 32 rows and kColsPerWarp
 // columns of a tile.  Each 32 x 32 piece has a staging buffer of its own (bf16 with the
 // 64-byte swizzle of the kernel's own epilogue), so the stores drain while the warp goes
-// on, and the residual arrives in the same buffers by TMA during the tile's K loop (with
-// Z: once Z's stores have read them).
+// on, and the residual arrives in the same buffers by TMA during the tile's K loop.
 //
 // The promotion warps are the whole kernel's bottleneck, their K loop has every register
 // in use, and their epilogue adds to each tile's time.  So the scale producer fetches bias
@@ -339,40 +335,37 @@ struct EpiWarp {
                 acc[2 * j + 1] = __fadd2_rn(acc[2 * j + 1], make_float2(__uint_as_float(b.z), __uint_as_float(b.w)));
             }
         }
-        const bool res = PT::kRes && x < p.N;
         if (p.Z != nullptr) {
-            wait_stores();
+            if constexpr (PT::kRes) {
+                // The residual lies in the staging buffers: straight from the registers.
+                if (row0 + static_cast<int>(lane) < p.M) {
+                    uint16_t* to = p.Z + (row0 + static_cast<int64_t>(lane)) * p.N + x;
 #pragma unroll
-            for (int pc = 0; pc < kPieces; ++pc) store_piece(p, &p.tmZ, pc, acc + pc * 16);
-            uint64_t* bar = tb->warp_full + ew;
-            if (PT::kRes && !res && lane == 0) mbar_arrive(bar);  // a phase a tile, also without columns
-            if (res && lane == 0) {
-                bulk_wait_read<0>();
-                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(min(kPieces, (p.N - x + 31) / 32) * kStageOutBytes));
-                const uint64_t policy = l2_policy_evict_first();
+                    for (int q = 0; q < 4 * kPieces; ++q) {
+                        const float2* v = acc + 4 * q;
+                        if (x + q * 8 < p.N)
+                            *reinterpret_cast<uint4*>(to + q * 8) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                                               pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+                    }
+                }
+                __syncwarp();
+            } else {
+                wait_stores();
 #pragma unroll
-                for (int pc = 0; pc < kPieces; ++pc)
-                    if (x + pc * 32 < p.N) tma_load_2d(stage + pc * kStageOutBytes, &p.tmR, bar, x + pc * 32, row0, policy);
+                for (int pc = 0; pc < kPieces; ++pc) store_piece(p, &p.tmZ, pc, acc + pc * 16);
             }
         }
         if (kAct != kActNone)
 #pragma unroll
             for (int j = 0; j < C::kColsPerWarp / 2; ++j) acc[j] = act2<kAct>(acc[j]);
-        if (res) {
-            uint64_t* bar = p.Z != nullptr ? tb->warp_full + ew : &tb->res_full;
-            if (!mbar_wait(bar, it & 1, abort_flag)) {
-                if (p.Z != nullptr) mbar_wait_drain(bar, it & 1);  // no copy may land after the CTA's end
-                return false;
+        if constexpr (PT::kRes) {  // landed before the tile's last scales; outside of D zeros, or what was there
+#pragma unroll
+            for (int q = 0; q < 4 * kPieces; ++q) {
+                F8 f;
+                bf16x8_to_f8(ld_shared_16(piece_at(q >> 2, q & 3)), f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[q * 4 + j] = __fadd2_rn(acc[q * 4 + j], f[j]);
             }
-#pragma unroll
-            for (int pc = 0; pc < kPieces; ++pc)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    F8 f;
-                    bf16x8_to_f8(ld_shared_16(piece_at(pc, q)), f);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[pc * 16 + q * 4 + j] = __fadd2_rn(acc[pc * 16 + q * 4 + j], f[j]);
-                }
             __syncwarp();
         } else {
             wait_stores();
@@ -426,68 +419,54 @@ struct EpiWarp {
     }
 };
 
-// What the scale producer (a whole warp) does for that epilogue.  Its loop is as tight as
-// the promotion's (with a few registers more it spilled, and each K block took 24 ns
-// longer), so the tile whose residual is still to be asked for lies in shared memory, and
-// only its ring slot in a register.
-template <int BN, typename PT>
-struct EpiFetch {
-    using C = Cfg<BN>;
-    static constexpr int kPieces = C::kColsPerWarp / 32;
-    int pending = -1;  // ring slot of that tile's first scales: their release says that the
-                       // previous tile's stores have left the staging buffers
-
-    // With a ring slot for the tile's first scales: its bias, which lands with them.
-    static __device__ __forceinline__ void begin(const EpiParams& p, EpiTable<BN>* tb, const Tile& tl, int tile, int lane) {
-        if (p.bias == nullptr) return;
-        const uint32_t to = smem_u32(tb->bias[tile % EpiTable<BN>::kBiasSlots]);
+// What the scale producer (a whole warp) does for that epilogue.  It remembers nothing: with
+// a few registers more its loop spilled, and each K block took 24 ns longer.
+//
+// With a ring slot for a tile's first scales: the bias, which lands with them.
+template <int BN>
+__device__ __forceinline__ void epi_fetch_bias(const EpiParams& p, EpiTable<BN>* tb, const Tile& tl, int tile, int lane) {
+    if (p.bias == nullptr) return;
+    const uint32_t to = smem_u32(tb->bias[tile % EpiTable<BN>::kBiasSlots]);
 #pragma unroll
-        for (int c = 0; c < BN; c += 128) {
-            const int j = c + lane * 4;
-            const bool there = tl.n0 + j < p.N;
-            if (j < BN) cp_async_16(to + j * 4, p.bias + (there ? tl.n0 + j : 0), there ? 16 : 0);
-        }
+    for (int c = 0; c < BN; c += 128) {
+        const int j = c + lane * 4;
+        const bool there = tl.n0 + j < p.N;
+        if (j < BN) cp_async_16(to + j * 4, p.bias + (there ? tl.n0 + j : 0), there ? 16 : 0);
     }
-    // Behind the tile's first scales, copied to ring slot `slot` in a pass of parity `phase`.
-    __device__ __forceinline__ void want(const EpiParams& p, EpiTable<BN>* tb, const Tile& tl, int tile, int slot, uint32_t phase, int lane) {
-        if (p.Z != nullptr) {
-            // The promotion warps ask for it themselves, between Z's stores and D's.
-            const int px = tl.n0 + (lane & 7) * 32;
-            if (px < p.N && (lane & 7) * 32 < BN) tma_prefetch_2d(&p.tmR, px, tl.m0 + (lane >> 3) * 32);
-            return;
-        }
-        if (lane == 0) tb->wanted = make_int4(tl.m0, tl.n0, tile, static_cast<int>(phase));
-        pending = slot;
-        __syncwarp();
+}
+// The residual goes to the staging buffers and is counted on the barrier of the scales
+// that follow, so the promotion warps, for whom a wait of its own in the epilogue made each
+// K block 50 ns longer, find it there.  Those are the scales of the tile's group of K
+// blocks `behind` groups after the first, at most four (the ring's depth) and at most the last.
+// The buffers are free when the first group's are released, or, for tiles of one group, at
+// the end of the previous tile.
+__device__ __forceinline__ int epi_groups_behind(const Work& w) {
+    return min(kScaleGroups, (w.kb1 - w.kb0 - 1) / kScaleGroup);
+}
+template <int BN>
+__device__ __forceinline__ bool epi_fetch_residual(const EpiParams& p, EpiTable<BN>* tb, uint8_t* out, const Tile& tl, int tile, int behind,
+                                                   uint64_t* sfull, uint64_t* sempty, int slot, uint32_t phase, int lane,
+                                                   volatile int* abort_flag) {
+    constexpr int kPieces = Cfg<BN>::kColsPerWarp / 32;
+    if (behind == 0) {
+        if (tile > 0 && !mbar_wait(&tb->free_bar, (tile - 1) & 1, abort_flag)) return false;
+    } else if (behind < kScaleGroups) {  // else the slot's own release was that group's
+        const int first = slot - behind;
+        if (!mbar_wait(sempty + (first & (kScaleGroups - 1)), first < 0 ? phase ^ 1u : phase, abort_flag)) return false;
     }
-    // Once the slot's release has been waited for.
-    __device__ __forceinline__ void send(const EpiParams& p, EpiTable<BN>* tb, uint8_t* out, int lane) {
-        pending = -1;
-        const int4 t = tb->wanted;
-        const int n = min(BN / 32, (p.N - t.y + 31) / 32);  // pieces across, of four rows of them
-        if (lane == 0) {
-            tb->sent = 1 + t.z;
-            mbar_arrive_expect_tx(&tb->res_full, static_cast<uint32_t>(4 * n * kStageOutBytes));
-        }
-        __syncwarp();
-        const int quarter = lane & 3, pc = lane >> 2;  // up to 8 pieces across
-        if (pc < n)
-            tma_load_2d(smem_u32(out) + ((pc / kPieces * 4 + quarter) * kPieces + pc % kPieces) * kStageOutBytes, &p.tmR, &tb->res_full,
-                        t.y + pc * 32, t.x + quarter * 32, l2_policy_evict_first());
-        __syncwarp();
+    const int n = min(BN / 32, (p.N - tl.n0 + 31) / 32);  // pieces across, of four rows of them
+    if (lane == 0) {
+        tb->sent = 1 + slot + (phase << 8);
+        mbar_expect_tx(sfull + slot, static_cast<uint32_t>(4 * n * kStageOutBytes));
     }
-    // `sempty`: the scale ring's release barriers.  false: a wait ran out.
-    __device__ __forceinline__ bool flush(const EpiParams& p, EpiTable<BN>* tb, uint8_t* out, uint64_t* sempty, int lane, volatile int* abort_flag) {
-        if (pending < 0) return true;
-        if (!mbar_wait(sempty + pending, tb->wanted.w, abort_flag)) return false;
-        send(p, tb, out, lane);
-        return true;
-    }
-    // No copy into shared memory may still be on its way when the CTA exits.
-    static __device__ __forceinline__ void end(EpiTable<BN>* tb) {
-        if (tb->sent) mbar_wait_drain(&tb->res_full, (tb->sent - 1) & 1);
-    }
-};
+    __syncwarp();
+    const int quarter = lane & 3, pc = lane >> 2;  // up to 8 pieces across
+    if (pc < n)
+        tma_load_2d(smem_u32(out) + ((pc / kPieces * 4 + quarter) * kPieces + pc % kPieces) * kStageOutBytes, &p.tmR, sfull + slot,
+                    tl.n0 + pc * 32, tl.m0 + quarter * 32, l2_policy_evict_first());
+    __syncwarp();
+    return true;
+}
 
 // LAYOUT (dense only) gives the operands' storage: bit 0 set = A stored
 // [K][M] (M-major, the "T" of TN / TT), bit 1 set = B stored [K][N] (N-major,
@@ -723,20 +702,11 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
         int slot = 0;
         uint32_t sphase = 0;
         const int row_limit = p.M;  // rows of sa that exist (dense M, M_total or M_max)
-        auto epi = [&] {
-            if constexpr (kEpi)
-                return EpiFetch<BN, PT>{};
-            else
-                return 0;
-        }();
         Work w;
         for (int it = 0; next_work(p, tiles, it, w); ++it) {
             const Tile tl = decode_tile<BN, MODE>(p, w.t, m_blocks, mb_prefix);
             if (!tl.valid) continue;
             group_k_range<MODE>(p, tl, w);
-            if constexpr (kRes) {
-                if (!epi.flush(p, epi_table, sOut, sempty, lane, abort_flag)) break;
-            }
             const float* sa_base = p.sa + (MODE == kMasked ? static_cast<int64_t>(tl.g) * nkb * p.sa_stride : 0);
             const float* sb_g = p.sb + (MODE == kKGrouped ? 0 : static_cast<int64_t>(tl.g) * p.nbn * nkb);
             const int nb = tl.n0 / 128 + (lane & 3);
@@ -747,11 +717,16 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
             bool ok = true;
             for (int kg = w.kb0; kg < w.kb1; kg += kScaleGroup) {
                 if (!mbar_wait(sempty + slot, sphase ^ 1u, abort_flag)) { ok = false; break; }
-                if constexpr (kRes) {
-                    if (slot == epi.pending) epi.send(p, epi_table, sOut, lane);
-                }
                 if constexpr (kEpi) {
-                    if (kg == w.kb0 && w.slice <= 0) epi.begin(p, epi_table, tl, it, lane);
+                    if (kg == w.kb0 && w.slice <= 0) epi_fetch_bias<BN>(p, epi_table, tl, it, lane);
+                }
+                if constexpr (kRes) {
+                    const int behind = epi_groups_behind(w);
+                    if (kg == w.kb0 + behind * kScaleGroup && w.slice <= 0 &&
+                        !epi_fetch_residual<BN>(p, epi_table, sOut, tl, it, behind, sfull, sempty, slot, sphase, lane, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
                 }
                 const int n = min(kScaleGroup, w.kb1 - kg);
                 for (int j = 0; j < n; ++j) {
@@ -764,19 +739,16 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
                                    nb_ok ? 4u : 0u);
                 }
                 cp_async_arrive(sfull + slot);
-                if constexpr (kRes) {
-                    if (kg == w.kb0 && w.slice <= 0) epi.want(p, epi_table, tl, it, slot, sphase, lane);
-                }
                 if (++slot == kScaleGroups) { slot = 0; sphase ^= 1u; }
             }
             if (!ok) break;
         }
-        if constexpr (kRes) {
-            epi.flush(p, epi_table, sOut, sempty, lane, abort_flag);
-            epi.end(epi_table);
-        }
         // Let every copy land before the CTA can exit.
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (kRes) {
+            // (After an abort only: else the promotion has waited for it, and the barrier gone on.)
+            if (*abort_flag && epi_table->sent) mbar_wait_drain(sfull + ((epi_table->sent - 1) & 255), (epi_table->sent - 1) >> 8);
+        }
     }
     } else {
         // ------------------------------------------ promotion + epilogue ----
@@ -838,11 +810,11 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
                 }
                 if (jg == kScaleGroup - 1 || kb == w.kb1 - 1) {
                     // The group's last K block has read its scales: release the slot.
-                    // (EpiParams calls: and the staging buffers, which the previous
-                    // tile's stores have long read.)
+                    // (With the tile's first group also the staging buffers, which the
+                    // previous tile's stores have long read.)
                     __syncwarp();
-                    if constexpr (kEpi) {
-                        if (PT::kRes && lane == 0) bulk_wait_read<0>();
+                    if constexpr (kRes) {
+                        if (lane == 0 && kb < w.kb0 + kScaleGroup) bulk_wait_read<0>();
                     }
                     if (lane == 0) mbar_arrive(sempty + slot);
                     if (++slot == kScaleGroups) { slot = 0; sphase ^= 1u; }
@@ -926,6 +898,15 @@ fp8_gemm_kernel(const __grid_constant__ PT p, const __grid_constant__ CUtensorMa
 
             if constexpr (kEpi) {
                 if (!EpiWarp<BN, PT>(sOut, epi_table, tl).finish(p, tmD, acc, it, abort_flag)) { ok = false; break; }
+                if constexpr (kRes) {
+                    if (p.nkb <= kScaleGroup) {  // one group of K blocks a tile
+                        __syncwarp();
+                        if (lane == 0) {
+                            bulk_wait_read<0>();
+                            mbar_arrive(&epi_table->free_bar);
+                        }
+                    }
+                }
                 continue;
             }
 

@@ -205,6 +205,17 @@ def test_gemm_epilogue_adds_to_the_residual_in_place(dgm, M, N, K):
     G.check(dgm, "gelu", "DZ", in_place=True)
 
 
+@pytest.mark.parametrize("K", [128, 256, 512, 640, 1024, 1152, 1536, 2048, 2176, 2304])
+@pytest.mark.parametrize("M,N", [(2500, 2056), (4100, 520), (2500, 2048)])
+def test_gemm_epilogue_residual_over_several_tiles(dgm, M, N, K):
+    # more tiles than SMs, of one group of K blocks up to more than the scale ring holds
+    G = Gemm(dgm, M, N, K, seed=K)
+    first = [t.clone() for t in G.check(dgm, "none", "D" if N % BLOCK else "DQ")]
+    for _ in range(3):  # the same again: what comes early in shared memory does not show
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(first, G.check(dgm, "none", "D" if N % BLOCK else "DQ")))
+    G.check(dgm, "silu", "DZ", in_place=True)
+
+
 @pytest.mark.parametrize("M", [2, 200])
 @pytest.mark.parametrize("act", ACTS)
 def test_gemm_epilogue_extreme_values(dgm, M, act):
