@@ -590,7 +590,7 @@ DG_API int dg_get_balance_workspace(int T, int E, int S);
  *   loss       float32 [1]
  *   counts     int32 [S][E]: n (the balance of a bias that dg_route_topk takes, too)
  *   probs      float32 [S][E] or null: P
- *   ws         dg_get_balance_workspace(T, E, S) floats, 8-byte aligned
+ *   ws         dg_get_balance_workspace(T, E, S) floats
  *   logits     [T][E], bf16 or float32 (logits_dtype); topk_idx int32 [T][k]
  *   seq_offsets int32 [S+1] on the device, not falling, within [0, T] (other values
  *              set DG_DEVERR_BAD_SEQ_OFFSET, and the sums are then undefined); null,

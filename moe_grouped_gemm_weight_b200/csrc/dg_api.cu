@@ -1096,7 +1096,6 @@ int balance_chunk(int T) {
     const int c = cdiv(T, dg::kBalanceMaxChunks);
     return c < 8 ? 8 : c;
 }
-constexpr int kBalanceHead = 2 * dg::kBalanceFinishCtas + 4;  // floats of the workspace ahead of the parts
 int64_t balance_rows(int T, int S) { return cdiv64(T, balance_chunk(T)) + S; }
 
 template <typename L, int EPL>
@@ -1906,7 +1905,7 @@ dg_status dg_norm_residual_bwd(void* dX, uint16_t* dY, float* dgate, float* dw_p
 
 int dg_get_balance_workspace(int T, int E, int S) {
     if (T < 0 || E <= 0 || E > dg::kRouteMaxExperts || S <= 0) return -1;
-    const int64_t n = kBalanceHead + 2 * balance_rows(T, S) * E;
+    const int64_t n = 2 * balance_rows(T, S) * E;
     return n <= 0x7FFFFFFF ? static_cast<int>(n) : -1;
 }
 
@@ -1917,23 +1916,19 @@ dg_status dg_balance_loss(float* loss, int32_t* counts, float* probs, float* ws,
     if (s != DG_OK) return s;
     if (dg_get_balance_workspace(T, E, S) < 0) return fail(DG_ERR_UNSUPPORTED, "T=%d E=%d S=%d: the workspace is too large", T, E, S);
     if (!loss || !counts || (T > 0 && (!logits || !topk_idx || !ws))) return fail(DG_ERR_INVALID_ARG, "null pointer");
-    if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(probs, 4) || !aligned(ws, 8) || !aligned(topk_idx, 4) ||
+    if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(probs, 4) || !aligned(ws, 4) || !aligned(topk_idx, 4) ||
         !aligned(logits, logits_dtype == DG_DTYPE_BF16 ? 2 : 4))
-        return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements, ws to 8 bytes");
+        return fail(DG_ERR_MISALIGNED, "tensors must be aligned to their elements");
     const int chunk = balance_chunk(T), chunks = static_cast<int>(cdiv64(T, chunk));
-    float* parts = ws + kBalanceHead;
-    int32_t* part_n = reinterpret_cast<int32_t*>(parts + balance_rows(T, S) * E);
-    dg::BalanceParams p{loss, counts, probs, parts, part_n, reinterpret_cast<double*>(ws),
-                        reinterpret_cast<unsigned int*>(ws + 2 * dg::kBalanceFinishCtas), logits, topk_idx, seq_offsets, T, E, k, S,
-                        chunk, chunks, score == DG_SCORE_SOFTMAX, coef};
-    int64_t grid = 1;  // without tokens nothing sets the workspace up
+    int32_t* part_n = reinterpret_cast<int32_t*>(ws + balance_rows(T, S) * E);
+    dg::BalanceParams p{loss, counts, probs, ws, part_n, logits, topk_idx, seq_offsets, T, E, k, S, chunk, chunks,
+                        score == DG_SCORE_SOFTMAX, coef};
     if (T > 0) {
         s = logits_dtype == DG_DTYPE_BF16 ? launch_balance_sum<uint16_t>(p, stream) : launch_balance_sum<float>(p, stream);
         if (s != DG_OK) return s;
-        grid = cdiv64(static_cast<int64_t>(S) * E, dg::kBalanceFinishSums);
-        if (grid > dg::kBalanceFinishCtas) grid = dg::kBalanceFinishCtas;
     }
-    return launch_plain(dg::balance_finish_kernel, p, grid, dg::kBalanceFinishThreads, 0, 1, stream);
+    return launch_plain(dg::balance_finish_kernel, p, dg::kBalanceFinishCtas, dg::kBalanceFinishThreads, 0,
+                        dg::kBalanceFinishCtas, stream);
 }
 
 dg_status dg_balance_loss_bwd(void* dlogits, const void* add, const float* dloss, const void* logits, int logits_dtype,

@@ -50,8 +50,6 @@ struct BalanceParams {
     float* probs;            // [S][E] or null
     float* part_p;           // [chunks + S][E]
     int32_t* part_n;         // [chunks + S][E]
-    double* part_loss;       // [kBalanceFinishCtas] of the finishing CTAs
-    unsigned int* finished;  // how many of those are done
     const void* logits;      // [T][E]
     const int32_t* topk_idx; // [T][k]
     const int32_t* offsets;  // [S + 1] or null: one sequence of all tokens
@@ -134,7 +132,6 @@ balance_sum_kernel(const BalanceParams p) {
     griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c = blockIdx.x, t0 = c * p.chunk, t1 = min(t0 + p.chunk, p.T);
-    if (c == 0 && tid == 0) *p.finished = 0;
     const L* logits = static_cast<const L*>(p.logits);
     for (int s = max(seq_of(p.offsets, p.S, p.T, t0), 0); s < p.S; ++s) {
         const int first = seq_offset(p.offsets, s, p.T);
@@ -180,26 +177,23 @@ balance_sum_kernel(const BalanceParams p) {
     }
 }
 
-constexpr int kBalanceFinishThreads = 256;
-constexpr int kBalanceFinishCtas = 64;   // at most
-constexpr int kBalanceFinishSums = 8;    // of a CTA, at least: whole sectors of a row
-constexpr int kBalanceFinishBatch = 10;
+constexpr int kBalanceFinishThreads = 512;
+constexpr int kBalanceFinishCtas = 8;
+constexpr int kBalanceFinishBatch = 8;
 
-// Joins the parts of each (sequence, expert), in chunk order, and the loss.  CTA r takes a
-// run of the S E sums; if those are fewer than its threads, as many threads share a sum,
-// each with a run of its parts.  The CTA that is done last adds the CTAs' shares of the
-// loss, in CTA order.  (One cluster of 8 CTAs, which meet in distributed shared memory:
-// 16384 x 256, loss and gradient, XX -> YY us.)
-__global__ void __launch_bounds__(kBalanceFinishThreads)
+// One cluster joins the parts of each (sequence, expert), in chunk order, and the
+// loss.  CTA r takes a run of the S E sums; if those are fewer than its threads, as
+// many threads share a sum, each with a run of its parts.
+__global__ void __launch_bounds__(kBalanceFinishThreads, 1)
 balance_finish_kernel(const BalanceParams p) {
     __shared__ float sp[kBalanceFinishThreads];
     __shared__ int32_t sn[kBalanceFinishThreads];
     __shared__ double share[kBalanceFinishThreads / 32];
-    __shared__ bool last;
+    __shared__ double mine;
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x;
-    const uint32_t rank = blockIdx.x, nctas = gridDim.x;
+    const uint32_t rank = cluster_ctarank(), nctas = cluster_nctarank();
     if (p.offsets != nullptr) {
         bool bad = false;
         for (int s = rank * kBalanceFinishThreads + tid; s <= p.S; s += nctas * kBalanceFinishThreads) {
@@ -275,26 +269,25 @@ balance_finish_kernel(const BalanceParams p) {
     for (int o = 16; o >= 1; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
     if ((tid & 31) == 0) share[tid >> 5] = loss;
     __syncthreads();
-    if (tid == 0) {
-#pragma unroll
-        for (int w = 1; w < kBalanceFinishThreads / 32; ++w) loss += share[w];
-        last = true;
-        if (nctas > 1) {
-            p.part_loss[rank] = loss;
-            __threadfence();
-            last = atomicAdd(p.finished, 1u) == nctas - 1;
-            __threadfence();
-        }
-    }
-    __syncthreads();
-    if (!last || tid >= 32) return;
-    if (nctas > 1) {  // a lane's shares, then the lanes' in a fixed tree
-        loss = 0.0;
-        for (uint32_t r = tid; r < nctas; r += 32) loss += __ldcg(p.part_loss + r);
+    if (tid < 32) {
+        loss = tid < kBalanceFinishThreads / 32 ? share[tid] : 0.0;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
+        if (tid == 0) mine = loss;
     }
-    if (tid == 0) *p.loss = len > 0.0 ? static_cast<float>(loss * p.coef * p.E / (static_cast<double>(p.k) * len)) : 0.f;
+    __syncwarp();
+    cluster_sync();
+    if (rank == 0 && tid == 0) {
+        double all = 0.0;
+        for (uint32_t r = 0; r < nctas; ++r) {
+            double x;
+            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(x) : "r"(dsmem_addr(smem_u32(&mine), r)) : "memory");
+            all += x;
+        }
+        *p.loss = len > 0.0 ? static_cast<float>(all * p.coef * p.E / (static_cast<double>(p.k) * len)) : 0.f;
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while its sum is being read
 }
 
 struct BalanceBwdParams {

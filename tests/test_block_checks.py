@@ -96,12 +96,11 @@ def test_workspaces():
     assert dg.dg_get_bias_workspace(0, 256) == 0 and dg.dg_get_bias_workspace(129, 256) == 512
     assert dg.dg_get_norm_workspace(0, 64) == 0 and dg.dg_get_norm_workspace(3, 64) == 2 * 64 * 3
     assert dg.dg_get_norm_workspace(1 << 20, 16384) == dg.dg_get_norm_workspace(1 << 19, 16384) <= 1 << 23
-    head = dg.dg_get_balance_workspace(0, 1, 1) - 2  # shares of the loss, ahead of the parts
-    assert 0 < head < 1024 and dg.dg_get_balance_workspace(1, 4, 1) == head + 2 * 4 * 2
+    assert dg.dg_get_balance_workspace(1, 4, 1) == 2 * 4 * 2
     for T in (0, 1, 8, 9, 2368, 2369, 100000):
         # a part for each chunk and for each sequence that starts inside one
         assert dg.dg_get_balance_workspace(T, 4, 5) >= 2 * 4 * 5
-        assert dg.dg_get_balance_workspace(T, 4, 5) <= head + 2 * 4 * (296 + 5)
+        assert dg.dg_get_balance_workspace(T, 4, 5) <= 2 * 4 * (296 + 5)
     for f, bad in ((dg.dg_get_bias_workspace, [(-1, 8), (1, 0), (1 << 31, 8), (1 << 30, 1 << 20)]),
                    (dg.dg_get_norm_workspace, [(-1, 8), (1, 0), (1, 16385), (1 << 32, 8)]),
                    (dg.dg_get_balance_workspace, [(-1, 4, 1), (1, 0, 1), (1, 1025, 1), (1, 4, 0), (1, 1024, 1 << 21)])):
@@ -155,7 +154,7 @@ BINDING = {
                                  dY=bf16(T, N), dgate=f32(T), dw_post=f32(N), dw_pre=f32(N), ws=f32(2 * T * N),
                                  w_post=f32(N), gate=f32(T), w_pre=f32(N)),
     "dg_balance_loss": dict(loss=f32(1), counts=i32(S, E), probs=f32(S, E), logits=bf16(T, E), topk_idx=i32(T, KK),
-                            ws=f32(dg.dg_get_balance_workspace(T, E, S)), seq_offsets=i32(S + 1)),
+                            ws=f32(2 * E * (3 + S)), seq_offsets=i32(S + 1)),
     "dg_balance_loss_bwd": dict(dlogits=bf16(T, E), logits=bf16(T, E), counts=i32(S, E), k=KK, dloss=f32(1),
                                 add=bf16(T, E), seq_offsets=i32(S + 1)),
 }
