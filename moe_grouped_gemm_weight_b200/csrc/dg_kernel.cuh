@@ -283,7 +283,7 @@ struct EpiTable {
 // activation and the residual are the instance's, and the epilogue waits for nothing:
 // each of these, done otherwise, made every K block 25 to 60 ns longer.  Times back to back
 // (power-limited), 4096 x 4096 x 7168 / 4096 x 7168 x 2048: dg_fp8_gemm_nt 135 / 78 us; here
-// plain 136 / 79; bias, gelu_tanh, Z and Q 150 / 98; bias and residual 145 / 87.  The
+// plain 136 / 79; bias, gelu_tanh, Z and Q 150 / 98; bias and residual 147 / 87.  The
 // activation costs about 1.7 us a tile (special-function unit and FP32 pipe), a second output
 // 1.  (The residual loaded by the promotion warps: 169 / 135.)
 template <int BN, typename PT>
