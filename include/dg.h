@@ -479,7 +479,8 @@ DG_API dg_status dg_fp8_1x128_to_128x128(uint8_t* Qb, float* sb, const uint8_t* 
  * written before they are read; what they hold between calls does not matter.
  * Calls that may overlap on the GPU (streams, graphs) need one each.  All sums are
  * FP32 or more, in an order that depends on the sizes only (dg_norm_residual_bwd's
- * sums over tokens also on the SM cap), so results repeat bit for bit.
+ * sums over tokens also on the SM cap, dg_fp8_gemm_nt_epilogue's also on it and on
+ * whether the call splits), so results repeat bit for bit.
  */
 
 /* Activations of dg_fp8_gemm_nt_epilogue: z, max(z, 0), z Phi(z), its form with tanh
@@ -501,7 +502,9 @@ DG_API dg_status dg_fp8_1x128_to_128x128(uint8_t* Qb, float* sb, const uint8_t* 
  *              sq[(n/128)*sq_stride + m], sq_stride >= M; N % 128 == 0
  *   bias       float32 [N], residual bf16 [M][N]
  * D, Z, Q, bias and residual may be null, but one of D, Z and Q is given.  All else
- * as in dg_fp8_gemm_nt, its K-split workspace too.
+ * as in dg_fp8_gemm_nt, its K-split workspace too, but calls that are being captured
+ * into a CUDA graph never split: graphs captured on one stream may be replayed at
+ * once, on any streams (results are the same up to FP32 summation order).
  */
 DG_API dg_status dg_fp8_gemm_nt_epilogue(uint16_t* D, uint16_t* Z, uint8_t* Q, float* sq, int sq_stride,
                                          const uint8_t* A, const float* sa, int sa_stride, const uint8_t* B,

@@ -978,6 +978,56 @@ def test_gemm_epilogue_under_an_sm_cap(dgm, sms):
         dgm.dg_set_num_sms(0)
 
 
+def test_gemm_epilogue_graphs_of_one_stream_run_at_once(dgm):
+    # sizes whose last wave is split along K where the stream's workspace may be used: not in a graph, which may run
+    # beside another one of the same stream
+    side = torch.cuda.Stream()
+    gemms = [Gemm(dgm, M, N, K, seed=M) for M, N, K in [(1300, 4096, 4096), (1500, 4096, 4096)]]
+    outs = [torch.empty(G.M, G.N, dtype=torch.bfloat16, device="cuda") for G in gemms]
+
+    def call(G, D):
+        dgm.dg_fp8_gemm_nt_epilogue(D, G.A, G.sa, G.stride, G.B, G.sb, bias=G.bias, act=dgm.DG_ACT_GELU, residual=G.residual)
+
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    graphs = []
+    for G, D in zip(gemms, outs):
+        assert dgm.dg_make_plan(0, G.M, G.N, G.K, 1, sms)["tail_split"] > 1
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            call(G, D)  # the stream has its workspace
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            for _ in range(4):
+                call(G, D)
+    want = []
+    for G, D, graph in zip(gemms, outs, graphs):
+        D.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        _, v, _, nv = G.exact("gelu")
+        inside(D, v, 2.0 ** -8 * v.abs() + (1 + 2.0 ** -8) * nv, "D")
+        want.append(D.clone())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    eager = [torch.empty_like(D) for D in outs]
+    for _ in range(5):
+        for D in outs + eager:
+            D.zero_()
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        with torch.cuda.stream(side):
+            call(gemms[0], eager[0])
+            call(gemms[1], eager[1])
+        torch.cuda.synchronize()
+        for G, D, E, w in zip(gemms, outs, eager, want):
+            assert torch.equal(D, w)
+            _, v, _, nv = G.exact("gelu")
+            inside(E, v, 2.0 ** -8 * v.abs() + (1 + 2.0 ** -8) * nv, "split")
+    assert dgm.dg_get_device_error() == 0
+
+
 def test_rows_past_31_bits_of_bytes(dgm):
     """Rows whose elements lie past 2^31: the first and the last rows of a long stream."""
     N = 8192
