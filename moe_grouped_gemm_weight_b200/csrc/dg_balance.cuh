@@ -116,6 +116,23 @@ __device__ __forceinline__ float balance_probs(const float (&l)[EPL], int softma
         top = warp_max(top);
     }
     sum = warp_sum(sum);
+    // All sigmoids small: they are exp(l) to 2^-29 of their value, and divide their sum as
+    // exp(l - max), none of which is lost below 2^-126.
+    if (!softmax && sum < 0x1p-29f) {
+        float m = l[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
+        m = warp_max(m);
+        m = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) p[i] = l[i] - m;
+        exp_results<EPL>(p);
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) sum += p[i];
+        sum = warp_sum(sum);
+        top = 1.f;
+    }
     const float inv = sum > 0.f || sum != sum ? __frcp_rn(sum) : 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) p[i] *= inv;

@@ -707,6 +707,25 @@ def test_balance_masks(dgm, score):
     assert bool(d[50].isnan().all() and d.isnan().any(dim=1).sum() == 1)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E", [60, 64, 1024])
+def test_balance_of_low_sigmoids(dgm, E, dtype):
+    # tokens whose sigmoids are small, or below FP32, still divide their sum; a token's differences of logits are exact
+    # (they lie within a factor of two)
+    b = Balance(70, E, 4, 2, 3, "sigmoid", dtype)
+    for row, base in ((5, 25.0), (6, 60.0), (7, 87.0), (8, 100.0), (9, 400.0), (69, 100.0)):
+        b.logits[row] -= base
+    b.logits[10] = -100.0
+    b.logits[10, 3] = -60.0
+    b.logits[11] = -INF
+    b.logits[11, :2] = -95.0
+    b.logits[12] = -100.0
+    b.logits[12, 1] = NAN
+    b.cut = [0, 12, 67]
+    b.offsets = torch.tensor(b.cut, dtype=torch.int32, device="cuda")
+    check_balance(dgm, b)
+
+
 @pytest.mark.parametrize("offsets", [[0, 0], [5, 5], [8, 8]])
 def test_balance_without_tokens(dgm, offsets):
     b = Balance(8, 6, 2, 1, 0, "softmax", "fp32", offsets=offsets)
